@@ -260,6 +260,122 @@ int fattn_fwd_bwd_host(const void* q, const void* k, const void* v, const void* 
                        float scale, int causal, int heads_per_chunk, void* workspace,
                        size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------ 8-bit key/value cache
+ *
+ * A paged cache of keys and values in 8 bits, its writer, its reader and the
+ * attention over it, for serving: the keys and values of `fattn_decode` kept
+ * from step to step at half the bytes, with grouped heads.  The pages have no
+ * counterpart to the storage; the attention is their recurrence over it.
+ *
+ * The pool.  k and v hold num_blocks blocks of block_size tokens for each of H
+ * key/value heads, [num_blocks, H, block_size, d], one 8-bit floating code per
+ * value; k_scale and v_scale hold one fp32 scale per (block, head),
+ * [num_blocks, H].  The value that code c of a block stands for is scale * c.
+ * All four are DEVICE pointers owned by the caller, contiguous, 16-byte
+ * aligned.  block_size is 16, 32, 64 or 128, d 64 or 128.
+ * fattn_cache_append writes powers of two as scales; the reader and the
+ * attention take any positive normal fp32 (scales of one sequence and head
+ * that lie within 2^100 of each other). */
+typedef enum {
+  FATTN_CACHE_E4M3 = 0, /* 4 exponent, 3 mantissa bits, largest value 448, no infinities */
+  FATTN_CACHE_E5M2 = 1  /* 5 exponent, 2 mantissa bits, largest value 57344 */
+} fattn_cache_format;
+
+typedef struct {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int num_blocks;
+  int H; /* key/value heads */
+  int block_size;
+  int d;
+  int format; /* fattn_cache_format */
+} fattn_cache;
+
+/* Which tokens a call works on: the LAST n_b = cu_seqlens[b+1] - cu_seqlens[b]
+ * tokens of each of B sequences, packed token by token into tensors of `total`
+ * rows (sequence b at rows [cu_seqlens[b], cu_seqlens[b+1])).
+ * lens[b] is the length of sequence b including those tokens; its token p is
+ * row p % block_size of block block_table[b * table_width + p / block_size].
+ * The three arrays are DEVICE int32, 4-byte aligned: cu_seqlens B + 1
+ * non-decreasing offsets from 0, at most `total`; rows at and behind
+ * cu_seqlens[B] are neither read nor written, so a captured graph can be sized
+ * for more tokens than a replay has.  max_seqlen >= every n_b (it sizes the
+ * grids).  A block may appear in several sequences (a shared prefix) as long as
+ * no call appends to it.
+ * Entries are checked on the device.  A sequence with offsets out of range or
+ * decreasing, n_b > max_seqlen, or a length that is negative, beyond its table
+ * row or (append, read) below n_b is skipped; a block number outside
+ * [0, num_blocks) drops its tokens (they are not written; read gives zeros for
+ * them; they are not visible to the attention).  Both are reported through the
+ * device error word (0x440 and 0x441 append, 0x450 and 0x451 read, 0x460 and
+ * 0x461 attention).  Table entries behind a sequence's length are not looked
+ * at.  n_b = 0 is allowed; total = 0 launches nothing. */
+typedef struct {
+  const int* block_table;
+  const int* lens;
+  const int* cu_seqlens;
+  int B;
+  int table_width;
+  int total;
+  int max_seqlen;
+} fattn_cache_batch;
+
+/* Quantise the n_b new tokens of each sequence into its blocks.
+ * k, v: DEVICE bf16, 16-byte aligned, element (t, h, c) at t * token stride +
+ * h * head stride + c (strides in elements, non-negative multiples of 8; so a
+ * slice of a fused projection's output or a head-major tensor is taken as it
+ * is).
+ * The scale of a block and head is the smallest power of two 2^e, e >= -100,
+ * with amax <= largest code * 2^e, amax over the finite values written so far.
+ * A block that gets its first token starts anew; one that holds earlier tokens
+ * of the sequence keeps its scale unless the new tokens need a larger one, in
+ * which case the earlier codes are rewritten for it, rounded to nearest even
+ * (the ratio is a power of two, so only codes that become subnormal change
+ * their value).  New values are divided by the scale (exact) and rounded to
+ * nearest even.  NaN and infinities are stored as NaN and do not enter amax.
+ * A call that is repeated with the same arguments leaves the same cache.
+ * No two sequences of a call may append to the same block (the writes would
+ * race; nothing out of range is touched). */
+int fattn_cache_append(const fattn_cache* cache, const fattn_cache_batch* batch, const void* k,
+                       long long k_token_stride, long long k_head_stride, const void* v,
+                       long long v_token_stride, long long v_head_stride, void* stream);
+
+/* The inverse: the last n_b tokens of each sequence as bf16(scale * code), into
+ * k and v laid out as for fattn_cache_append (strides >= d here).  Exact for
+ * the scales that append writes. */
+int fattn_cache_read(const fattn_cache* cache, const fattn_cache_batch* batch, void* k,
+                     long long k_token_stride, long long k_head_stride, void* v,
+                     long long v_token_stride, long long v_head_stride, void* stream);
+
+/* Attention of the last n_b tokens of each sequence over its cache.
+ * q, o: DEVICE bf16 [total, Hq, d] by strides as above (o's strides >= d); Hq a
+ * multiple of H, query head h reads key/value head h / (Hq / H).  lse: DEVICE
+ * fp32 [Hq, total], contiguous (the layout of fattn_fwd_varlen), 16-byte
+ * aligned.  Query i of sequence b stands at position lens[b] - n_b + i; with
+ * causal it sees keys at or before its position, else every key of the
+ * sequence.  A query that sees no key gets o = 0 and lse = -inf.  n_b may
+ * exceed lens[b].  Values of keys that a query does not see never reach its
+ * row, whatever they are (NaN included).
+ * Scores, statistics and sums are fp32.
+ * workspace: DEVICE memory of fattn_cache_fwd_workspace_bytes(...) bytes,
+ * 256-byte aligned, owned by the caller, its contents on entry do not matter;
+ * calls that overlap on the GPU need one each.  Returns FATTN_OK,
+ * FATTN_ERR_INVALID_ARG, FATTN_ERR_UNSUPPORTED, FATTN_ERR_WORKSPACE or
+ * FATTN_ERR_CUDA; launches nothing on an argument error, as the two calls
+ * above. */
+int fattn_cache_fwd(const fattn_cache* cache, const fattn_cache_batch* batch, const void* q,
+                    long long q_token_stride, long long q_head_stride, void* o,
+                    long long o_token_stride, long long o_head_stride, float* lse, int Hq,
+                    float scale, int causal, void* workspace, size_t workspace_bytes,
+                    void* stream);
+
+/* Workspace bytes of fattn_cache_fwd on the current device, from the sizes in
+ * the two descriptors (their pointers are not looked at); 0 if invalid. */
+size_t fattn_cache_fwd_workspace_bytes(const fattn_cache* cache, const fattn_cache_batch* batch,
+                                       int Hq);
+
 /* Tile shape used by a pass (0 = forward, 1 = backward) for head size d:
  * rows of Q per tile and keys per K/V tile; 128 x 128, the tile of "Decoding
  * flash attention" ("The idea: never build the matrix").  block_q and block_k may be NULL.

@@ -481,6 +481,173 @@ extern "C" int fattn_softmax_rows(const float* x, float* y, float* lse, long lon
       s);
 }
 
+namespace fattn {
+namespace {
+
+// Sizes of a cache call; the pointers are checked by check_cache_pointers.
+int check_cache_sizes(const fattn_cache* c, const fattn_cache_batch* b) {
+  if (!c || !b) return FATTN_ERR_INVALID_ARG;
+  if (c->num_blocks < 1 || c->H < 1 || c->H > 65535 || b->B < 1 || b->table_width < 1 ||
+      b->total < 0 || b->max_seqlen < 0 || b->max_seqlen > b->total)
+    return FATTN_ERR_INVALID_ARG;
+  if (c->format != FATTN_CACHE_E4M3 && c->format != FATTN_CACHE_E5M2) return FATTN_ERR_UNSUPPORTED;
+  if (c->block_size != 16 && c->block_size != 32 && c->block_size != 64 && c->block_size != 128)
+    return FATTN_ERR_UNSUPPORTED;
+  if (c->d != 64 && c->d != 128) return FATTN_ERR_UNSUPPORTED;
+  if ((long long)b->table_width * c->block_size >= (1LL << 31) ||
+      (long long)c->H * b->total >= (1LL << 31) || b->B > (1 << 24))
+    return FATTN_ERR_INVALID_ARG;
+  return FATTN_OK;
+}
+
+bool aligned4(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+int check_cache_pointers(const fattn_cache* c, const fattn_cache_batch* b) {
+  if (!aligned16(c->k) || !aligned16(c->v) || !aligned16(c->k_scale) || !aligned16(c->v_scale) ||
+      !aligned4(b->block_table) || !aligned4(b->lens) || !aligned4(b->cu_seqlens))
+    return FATTN_ERR_INVALID_ARG;
+  return FATTN_OK;
+}
+
+// Strides of a packed [total, heads, d] tensor: multiples of 8 elements (16
+// bytes), not negative and bounded (so that offsets stay far inside 64 bits); the
+// stride of an axis of one element is not used.  d != 0: the tensor is written,
+// and no two of its rows of d elements may overlap.
+int check_strides(long long st, long long sh, int total, int heads, int d) {
+  if (total <= 1) st = 0;
+  if (heads <= 1) sh = 0;
+  if (st < 0 || (st & 7) || st >= (1LL << 30)) return FATTN_ERR_INVALID_ARG;
+  if (sh < 0 || (sh & 7) || sh >= (1LL << 40)) return FATTN_ERR_INVALID_ARG;
+  if (d == 0) return FATTN_OK;
+  const bool token_major = (heads == 1 || sh >= d) && (total <= 1 || st >= (heads - 1) * sh + d);
+  const bool head_major = (total <= 1 || st >= d) && (heads == 1 || sh >= (total - 1) * st + d);
+  return token_major || head_major ? FATTN_OK : FATTN_ERR_INVALID_ARG;
+}
+
+CacheParams cache_params(const fattn_cache* c, const fattn_cache_batch* b, unsigned int* err) {
+  CacheParams p{};
+  p.k = static_cast<uint8_t*>(c->k);
+  p.v = static_cast<uint8_t*>(c->v);
+  p.k_scale = c->k_scale;
+  p.v_scale = c->v_scale;
+  p.num_blocks = c->num_blocks;
+  p.H = c->H;
+  p.block_size = c->block_size;
+  p.d = c->d;
+  p.format = c->format;
+  p.block_table = b->block_table;
+  p.lens = b->lens;
+  p.cu_seqlens = b->cu_seqlens;
+  p.B = b->B;
+  p.table_width = b->table_width;
+  p.total = b->total;
+  p.max_seqlen = b->max_seqlen;
+  p.err = err;
+  return p;
+}
+
+TokenView token_view(const void* p, long long st, long long sh, int total, int heads) {
+  return TokenView{static_cast<uint16_t*>(const_cast<void*>(p)), total > 1 ? st : 0,
+                   heads > 1 ? sh : 0};
+}
+
+using CacheMove = cudaError_t (*)(const CacheParams&, const TokenView&, const TokenView&,
+                                  cudaStream_t);
+
+// fattn_cache_append and fattn_cache_read: the same arguments, one way or the other.
+int cache_move(CacheMove launch, const fattn_cache* cache, const fattn_cache_batch* batch,
+               const void* k, long long kst, long long ksh, const void* v, long long vst,
+               long long vsh, int least_stride, void* stream) {
+  int st = check_cache_sizes(cache, batch);
+  if (st != FATTN_OK) return st;
+  st = check_cache_pointers(cache, batch);
+  if (st != FATTN_OK) return st;
+  const int T = batch->total, H = cache->H;
+  if (T == 0 || batch->max_seqlen == 0) return FATTN_OK;  // no tokens: nothing to do
+  if (!aligned16(k) || !aligned16(v)) return FATTN_ERR_INVALID_ARG;
+  const int least = least_stride ? cache->d : 0;
+  st = check_strides(kst, ksh, T, H, least);
+  if (st == FATTN_OK) st = check_strides(vst, vsh, T, H, least);
+  if (st != FATTN_OK) return st;
+  DeviceInfo* dev = nullptr;
+  st = current_device(&dev);
+  if (st != FATTN_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = launch(cache_params(cache, batch, dev->err), token_view(k, kst, ksh, T, H),
+                               token_view(v, vst, vsh, T, H), s);
+  return debug_post_call(e == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA, s);
+}
+
+int check_cache_heads(const fattn_cache* c, const fattn_cache_batch* b, int Hq) {
+  if (Hq < 1 || Hq % c->H != 0 || (long long)Hq * b->total >= (1LL << 31))
+    return FATTN_ERR_INVALID_ARG;
+  return FATTN_OK;
+}
+
+}  // namespace
+}  // namespace fattn
+
+extern "C" int fattn_cache_append(const fattn_cache* cache, const fattn_cache_batch* batch,
+                                  const void* k, long long k_token_stride, long long k_head_stride,
+                                  const void* v, long long v_token_stride, long long v_head_stride,
+                                  void* stream) {
+  return cache_move(launch_cache_append, cache, batch, k, k_token_stride, k_head_stride, v,
+                    v_token_stride, v_head_stride, 0, stream);
+}
+
+extern "C" int fattn_cache_read(const fattn_cache* cache, const fattn_cache_batch* batch, void* k,
+                                long long k_token_stride, long long k_head_stride, void* v,
+                                long long v_token_stride, long long v_head_stride, void* stream) {
+  return cache_move(launch_cache_read, cache, batch, k, k_token_stride, k_head_stride, v,
+                    v_token_stride, v_head_stride, 1, stream);
+}
+
+extern "C" size_t fattn_cache_fwd_workspace_bytes(const fattn_cache* cache,
+                                                  const fattn_cache_batch* batch, int Hq) {
+  if (check_cache_sizes(cache, batch) != FATTN_OK || check_cache_heads(cache, batch, Hq) != FATTN_OK)
+    return 0;
+  DeviceInfo* dev = nullptr;
+  if (current_device(&dev) != FATTN_OK) return 0;
+  return cache_fwd_workspace(cache_params(cache, batch, nullptr), Hq, dev->n_sm);
+}
+
+extern "C" int fattn_cache_fwd(const fattn_cache* cache, const fattn_cache_batch* batch,
+                               const void* q, long long q_token_stride, long long q_head_stride,
+                               void* o, long long o_token_stride, long long o_head_stride,
+                               float* lse, int Hq, float scale, int causal, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  int st = check_cache_sizes(cache, batch);
+  if (st != FATTN_OK) return st;
+  st = check_cache_heads(cache, batch, Hq);
+  if (st != FATTN_OK) return st;
+  if (!(scale > 0.f) || !isfinite(scale)) return FATTN_ERR_INVALID_ARG;
+  st = check_cache_pointers(cache, batch);
+  if (st != FATTN_OK) return st;
+  const int T = batch->total;
+  if (T == 0 || batch->max_seqlen == 0) return FATTN_OK;  // no queries: nothing to compute
+  if (!aligned16(q) || !aligned16(o) || !aligned16(lse)) return FATTN_ERR_INVALID_ARG;
+  st = check_strides(q_token_stride, q_head_stride, T, Hq, 0);
+  if (st == FATTN_OK) st = check_strides(o_token_stride, o_head_stride, T, Hq, cache->d);
+  if (st != FATTN_OK) return st;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return FATTN_ERR_WORKSPACE;
+  DeviceInfo* dev = nullptr;
+  st = current_device(&dev);
+  if (st != FATTN_OK) return st;
+  CacheFwdParams p{};
+  p.c = cache_params(cache, batch, dev->err);
+  if (workspace_bytes < cache_fwd_workspace(p.c, Hq, dev->n_sm)) return FATTN_ERR_WORKSPACE;
+  p.q = token_view(q, q_token_stride, q_head_stride, T, Hq);
+  p.o = token_view(o, o_token_stride, o_head_stride, T, Hq);
+  p.lse = lse;
+  p.Hq = Hq;
+  p.causal = causal ? 1 : 0;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.workspace = workspace;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return debug_post_call(
+      launch_cache_fwd(p, dev->n_sm, s) == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA, s);
+}
+
 extern "C" size_t fattn_bwd_workspace_bytes(int B, int H, int N, int d) {
   if (B < 1 || H < 1 || N < 1 || (d != 64 && d != 128)) return 0;
   return workspace_bytes_for_rows((long long)B * H * N, d);

@@ -12,6 +12,9 @@ enum : uint32_t {
   ERR_SITE_FWD = 0x100,
   ERR_SITE_BWD = 0x200,
   ERR_SITE_CHECK = 0x300,  // fattn_check_wait_timeout
+  ERR_SITE_CACHE_APPEND = 0x440,  // + 0: bad sequence entry, + 1: bad block number
+  ERR_SITE_CACHE_READ = 0x450,
+  ERR_SITE_CACHE_FWD = 0x460,
 };
 
 // Variable-length batches: B sequences packed head-major, [H, T, d] with
@@ -108,6 +111,51 @@ __device__ __forceinline__ bool seq_view(const Varlen& vl, int dense_N, int seq,
   return true;
 }
 
+// The 8-bit key/value cache: the pool of blocks and the tokens a call works on
+// (fattn_cache and fattn_cache_batch, with the device's error word).
+struct CacheParams {
+  uint8_t* k;            // [num_blocks, H, block_size, d] codes
+  uint8_t* v;
+  float* k_scale;        // [num_blocks, H]
+  float* v_scale;
+  int num_blocks, H, block_size, d, format;
+  const int* block_table;
+  const int* lens;
+  const int* cu_seqlens;
+  int B, table_width, total, max_seqlen;
+  unsigned int* err;
+};
+// A packed [total, heads, d] tensor by element strides.
+struct TokenView {
+  uint16_t* p;
+  long long st, sh;  // token and head stride
+};
+struct CacheFwdParams {
+  CacheParams c;
+  TokenView q, o;
+  float* lse;        // [Hq, total]
+  int Hq;
+  int causal;
+  float scale_log2;  // scale * log2(e)
+  void* workspace;
+};
+
+// Sequence b of a cache call: n tokens at packed rows [row0, row0 + n), the
+// last ones of len.  False (and the error word set by the caller) for entries
+// out of range.
+struct CacheSeq {
+  int row0, n, len;
+};
+__device__ __forceinline__ bool cache_seq(const CacheParams& c, int b, CacheSeq* s) {
+  const int a = c.cu_seqlens[b], e = c.cu_seqlens[b + 1];
+  const int len = c.lens[b];
+  s->row0 = a;
+  s->n = e - a;
+  s->len = len;
+  return a >= 0 && e >= a && e <= c.total && e - a <= c.max_seqlen && len >= 0 &&
+         (long long)len <= (long long)c.table_width * c.block_size;
+}
+
 // Identity of the calling thread's current CUDA context (the device's primary
 // context under the runtime API): a process-unique id, 0 when no context is
 // current yet.  Per-device caches remember the context they were filled in and
@@ -152,6 +200,14 @@ cudaError_t launch_softmax_rows(const float* x, float* y, float* lse, long long 
 // Merge of split partials: lse = log sum_s exp(lse_s), o = sum_s exp(lse_s - lse) o_s (bf16).
 cudaError_t launch_merge(const float* o_part, const float* lse_part, int n_splits, long long rows,
                          int d, void* o, float* lse, cudaStream_t stream);
+
+// The 8-bit key/value cache (append, read back, attention over it).
+cudaError_t launch_cache_append(const CacheParams& c, const TokenView& k, const TokenView& v,
+                                cudaStream_t stream);
+cudaError_t launch_cache_read(const CacheParams& c, const TokenView& k, const TokenView& v,
+                              cudaStream_t stream);
+size_t cache_fwd_workspace(const CacheParams& c, int Hq, int n_sm);
+cudaError_t launch_cache_fwd(const CacheFwdParams& p, int n_sm, cudaStream_t stream);
 
 cudaError_t launch_bwd_preprocess(const void* o, const void* dout, float* delta, float* dq_acc,
                                   long long rows, int d, int n_sm, cudaStream_t stream);

@@ -9,9 +9,11 @@ allocate the outputs with torch and then call those entry points.
 The library is loaded on first use.  If ``libfattn.so`` is missing the
 binding raises: there is no fallback path.
 """
+import contextlib
 import ctypes
 import os
 import threading
+import typing
 
 import torch
 
@@ -24,6 +26,20 @@ STATUS_NAMES = {0: "FATTN_OK", 1: "FATTN_ERR_INVALID_ARG", 2: "FATTN_ERR_UNSUPPO
 
 # Every exported symbol of include/fattn.h: name -> (restype, argtypes)
 _vp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_ll = ctypes.c_longlong
+
+
+class _CCache(ctypes.Structure):  # fattn_cache
+    _fields_ = [("k", _vp), ("v", _vp), ("k_scale", _vp), ("v_scale", _vp), ("num_blocks", _i),
+                ("H", _i), ("block_size", _i), ("d", _i), ("format", _i)]
+
+
+class _CBatch(ctypes.Structure):  # fattn_cache_batch
+    _fields_ = [("block_table", _vp), ("lens", _vp), ("cu_seqlens", _vp), ("B", _i),
+                ("table_width", _i), ("total", _i), ("max_seqlen", _i)]
+
+
+_cp, _bp = ctypes.POINTER(_CCache), ctypes.POINTER(_CBatch)
 SIGNATURES = {
     "fattn_fwd": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _f, _i, _vp]),
     "fattn_fwd_ex": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _f, _i, _vp, _vp]),
@@ -47,6 +63,11 @@ SIGNATURES = {
     "fattn_fwd_bwd_host_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
     "fattn_fwd_bwd_host": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _f,
                                 _i, _i, _vp, _sz, _vp]),
+    "fattn_cache_append": (_i, [_cp, _bp, _vp, _ll, _ll, _vp, _ll, _ll, _vp]),
+    "fattn_cache_read": (_i, [_cp, _bp, _vp, _ll, _ll, _vp, _ll, _ll, _vp]),
+    "fattn_cache_fwd": (_i, [_cp, _bp, _vp, _ll, _ll, _vp, _ll, _ll, _vp, _i, _f, _i, _vp, _sz,
+                             _vp]),
+    "fattn_cache_fwd_workspace_bytes": (_sz, [_cp, _bp, _i]),
     "fattn_status_string": (ctypes.c_char_p, [_i]),
 }
 
@@ -349,3 +370,151 @@ def softmax_rows(x, with_lse=False, out=None, stream=None):
     _check("fattn_softmax_rows", load().fattn_softmax_rows(_ptr(x), _ptr(y), _ptr(lse), rows, cols,
                                                            _stream(stream)))
     return (y, lse) if with_lse else y
+
+
+# ------------------------------------------------------------------ 8-bit key/value cache
+
+CACHE_FORMATS = {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1}
+
+
+class KVCache(typing.NamedTuple):
+    """The pool of blocks of fattn_cache: k, v float8_e4m3fn or float8_e5m2
+    [num_blocks, H, block_size, d], k_scale, v_scale fp32 [num_blocks, H], all
+    contiguous on one device."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+
+
+class CacheBatch(typing.NamedTuple):
+    """The tokens a cache call works on (fattn_cache_batch): the last
+    cu_seqlens[b+1] - cu_seqlens[b] tokens of each sequence, packed into `total`
+    rows; lens[b] is a sequence's length including them, block_table [B, width]
+    names its blocks.  Contiguous device int32 tensors; max_seqlen is an upper
+    bound of the tokens of one sequence."""
+    block_table: torch.Tensor
+    lens: torch.Tensor
+    cu_seqlens: torch.Tensor
+    total: int
+    max_seqlen: int
+
+
+def new_cache(num_blocks, heads, block_size, d, dtype=torch.float8_e4m3fn, device="cuda"):
+    """An empty KVCache (codes and scales zero)."""
+    if dtype not in CACHE_FORMATS:
+        raise ValueError("a cache holds float8_e4m3fn or float8_e5m2, not %s" % dtype)
+    shape = (num_blocks, heads, block_size, d)
+    k, v = (torch.zeros(shape, dtype=torch.uint8, device=device).view(dtype) for _ in range(2))
+    ks, vs = (torch.zeros(shape[:2], dtype=torch.float32, device=device) for _ in range(2))
+    return KVCache(k, v, ks, vs)
+
+
+def _cache_args(cache, batch):
+    """The C descriptors of a cache and a batch, their tensors checked."""
+    k, v, ks, vs = cache
+    table, lens, cu, total, max_seqlen = batch
+    shape, dev = k.shape, k.device
+    if len(shape) != 4 or v.shape != shape or ks.shape != shape[:2] or vs.shape != shape[:2]:
+        raise ValueError("expected k, v [num_blocks, H, block_size, d] and scales [num_blocks, H]")
+    if k.dtype not in CACHE_FORMATS or v.dtype != k.dtype or ks.dtype != torch.float32 or \
+            vs.dtype != torch.float32:
+        raise ValueError("expected float8 codes of one type and fp32 scales")
+    if table.dim() != 2 or lens.shape != (table.shape[0],) or cu.shape != (table.shape[0] + 1,):
+        raise ValueError("expected block_table [B, width], lens [B], cu_seqlens [B + 1]")
+    if table.dtype != torch.int32 or lens.dtype != torch.int32 or cu.dtype != torch.int32:
+        raise ValueError("expected int32 block_table, lens and cu_seqlens")
+    for t in (k, v, ks, vs, table, lens, cu):
+        if not t.is_contiguous() or t.device != dev:
+            raise ValueError("expected contiguous tensors on one device")
+    if dev.type != "cuda":
+        raise ValueError("expected device tensors, got %s" % dev)
+    return (_CCache(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), shape[0], shape[1],
+                    shape[2], shape[3], CACHE_FORMATS[k.dtype]),
+            _CBatch(table.data_ptr(), lens.data_ptr(), cu.data_ptr(), table.shape[0],
+                    table.shape[1], total, max_seqlen))
+
+
+def _packed(x, total, heads, d, device):
+    """Pointer and token and head strides of a bf16 [total, heads, d] tensor."""
+    if x.shape != (total, heads, d) or x.dtype != torch.bfloat16 or x.device != device or \
+            (d > 1 and x.stride(2) != 1):
+        raise ValueError("expected a bf16 [%d, %d, %d] tensor on %s with a contiguous last axis"
+                         % (total, heads, d, device))
+    return x.data_ptr(), x.stride(0), x.stride(1)
+
+
+@contextlib.contextmanager
+def _on(device, stream):
+    """Work and allocations on `stream` of `device` (None: its current stream)."""
+    with torch.cuda.device(device):
+        if stream is None:
+            yield
+            return
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=device)
+        with torch.cuda.stream(stream):
+            yield
+
+
+def _cache_call(device, stream, call):
+    """call(raw stream) on the cache's device; the usual case (its current stream,
+    the current device) without a context switch."""
+    if stream is None and torch.cuda.current_device() == device.index:
+        return call(torch.cuda.current_stream(device).cuda_stream)
+    with _on(device, stream):
+        return call(torch.cuda.current_stream(device).cuda_stream)
+
+
+def cache_append(k, v, cache, batch, stream=None):
+    """Quantise new tokens' k, v (bf16 [total, H, d], any token and head strides)
+    into the cache."""
+    c, b = _cache_args(cache, batch)
+    dev = cache.k.device
+    ka, va = _packed(k, b.total, c.H, c.d, dev), _packed(v, b.total, c.H, c.d, dev)
+    _cache_call(dev, stream, lambda s: _check("fattn_cache_append", load().fattn_cache_append(
+        c, b, *ka, *va, s)))
+
+
+def cache_read(cache, batch, out=None, stream=None):
+    """k, v (bf16 [total, H, d]) of the batch's tokens, read back from the cache;
+    out: a pair of tensors to write to."""
+    c, b = _cache_args(cache, batch)
+    dev = cache.k.device
+
+    def call(s):
+        k, v = out if out is not None else (torch.empty((b.total, c.H, c.d), dtype=torch.bfloat16,
+                                                        device=dev) for _ in range(2))
+        _check("fattn_cache_read", load().fattn_cache_read(
+            c, b, *_packed(k, b.total, c.H, c.d, dev), *_packed(v, b.total, c.H, c.d, dev), s))
+        return k, v
+
+    return _cache_call(dev, stream, call)
+
+
+def cache_forward(q, cache, batch, scale, causal, out=None, workspace=None, stream=None):
+    """O (bf16 [total, Hq, d]) and LSE (fp32 [Hq, total]) of the batch's queries q
+    (bf16 [total, Hq, d], any token and head strides) over their sequences in the
+    cache.  out: a tensor to write O to."""
+    c, b = _cache_args(cache, batch)
+    dev = cache.k.device
+    if q.dim() != 3:
+        raise ValueError("expected q [total, Hq, d]")
+    Hq = q.shape[1]
+    qa = _packed(q, b.total, Hq, c.d, dev)
+
+    def call(s):
+        lib = load()
+        o = out if out is not None else torch.empty((b.total, Hq, c.d), dtype=torch.bfloat16,
+                                                    device=dev)
+        lse = torch.empty((Hq, b.total), dtype=torch.float32, device=dev)
+        ws = workspace
+        if ws is None:
+            ws = torch.empty(max(int(lib.fattn_cache_fwd_workspace_bytes(c, b, Hq)), 256),
+                             dtype=torch.uint8, device=dev)
+        _check("fattn_cache_fwd", lib.fattn_cache_fwd(
+            c, b, *qa, *_packed(o, b.total, Hq, c.d, dev), lse.data_ptr(), Hq, float(scale),
+            int(bool(causal)), ws.data_ptr(), ws.numel() * ws.element_size(), s))
+        return o, lse
+
+    return _cache_call(dev, stream, call)
