@@ -495,7 +495,8 @@ int check_cache_sizes(const fattn_cache* c, const fattn_cache_batch* b) {
     return FATTN_ERR_UNSUPPORTED;
   if (c->d != 64 && c->d != 128) return FATTN_ERR_UNSUPPORTED;
   if ((long long)b->table_width * c->block_size >= (1LL << 31) ||
-      (long long)c->H * b->total >= (1LL << 31) || b->B > (1 << 24))
+      (long long)c->H * b->total >= (1LL << 31) ||
+      (long long)c->num_blocks * c->H >= (1LL << 31) || b->B > (1 << 24))
     return FATTN_ERR_INVALID_ARG;
   return FATTN_OK;
 }
@@ -578,6 +579,14 @@ int cache_move(CacheMove launch, const fattn_cache* cache, const fattn_cache_bat
   return debug_post_call(e == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA, s);
 }
 
+// A cache's codes as {d, block_size, num_blocks * H} bytes, in boxes of 16 tokens
+// whose 16-byte pieces are swizzled over the banks.
+bool make_cache_map(CUtensorMap* m, const void* codes, const fattn_cache* c) {
+  return make_map(m, codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, c->d, c->block_size,
+                  (long long)c->num_blocks * c->H, c->d, 16,
+                  c->d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
 int check_cache_heads(const fattn_cache* c, const fattn_cache_batch* b, int Hq) {
   if (Hq < 1 || Hq % c->H != 0 || (long long)Hq * b->total >= (1LL << 31))
     return FATTN_ERR_INVALID_ARG;
@@ -643,9 +652,12 @@ extern "C" int fattn_cache_fwd(const fattn_cache* cache, const fattn_cache_batch
   p.causal = causal ? 1 : 0;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.workspace = workspace;
+  CUtensorMap tk, tv;
+  if (!make_cache_map(&tk, cache->k, cache) || !make_cache_map(&tv, cache->v, cache))
+    return FATTN_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return debug_post_call(
-      launch_cache_fwd(p, dev->n_sm, s) == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA, s);
+      launch_cache_fwd(tk, tv, p, dev->n_sm, s) == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA, s);
 }
 
 extern "C" size_t fattn_bwd_workspace_bytes(int B, int H, int N, int d) {

@@ -1,108 +1,768 @@
-// cache_fwd.cu -- attention over the paged 8-bit key/value cache.
+// cache_fwd.cu -- attention over the paged 8-bit key/value cache, few query rows
+// per key/value head (decoding, drafted tokens).
 //
-// One warp per (query token, query head): lanes take 32 keys at a time, then
-// the d columns of the values.
+// The mathematics.  With codes k, v and scales ks, vs of key j's block, in base 2:
+//   x_j = scale log2(e) ks_j (q . k_j),   O = sum_j 2^x_j vs_j v_j / sum_j 2^x_j.
+// The value scale is folded into the exponent: y_j = x_j + log2 vs_j, and with a
+// reference m >= max y - 7 carried along the keys (the running maximum of the
+// online softmax, moved lazily)
+//   acc = sum_j p_j v_j,  p_j = 2^(y_j - m + 8),   l = sum_j p_j 2^(b - log2 vs_j)
+// where b is the log2 vs of the first block: O = 2^b acc / l and
+// LSE = ln2 (m - 8 - b + log2 l).  So blocks of different scales need no rescale
+// of acc, and the weights p_j can be held in fp16: they lie below 2^15, the
+// largest at or above 2^8, so weights down to 2^-22 of it keep 11 bits and
+// what is flushed lies below 2^-33 of it.  Codes are exact in fp16, q is (each
+// row is multiplied by the power of two that brings its largest element to
+// [2^14, 2^15)), sums and statistics are fp32.
+//
+// The bound is memory: every code is read once.  At the measured copy
+// bandwidth an SM gets about 24 codes a clock, and a 16-key tile of keys and
+// values (4 KB at d = 128) costs 174 clocks, of which the arithmetic below takes
+// about a quarter of the issue slots.  With 1 to 16 rows per key/value head the
+// tensor work is far too small for a 128-row tcgen05 tile and its trip through
+// shared memory and TMEM; m16n8k16 mma.sync with the keys as the 16-row operand
+// takes the codes straight from shared memory into registers:
+//   S^T = K Q^T:   A = 16 keys x d codes, B = d x 8 query rows
+//   O^T += V^T P^T: A = d x 16 keys,      B = 16 keys x 8 query rows
+// The contraction index may be permuted at will (q is loaded to match), so a
+// lane's share of a key is 16 consecutive bytes; P goes from the first
+// product's layout to the second's by movmatrix.
+//
+// Work split.  A unit is (sequence, key/value head, block of R query rows); its
+// keys come in chunks of 64, one 16-key tile for each of the CTA's four warps.
+// The chunks of all units, in order, are cut into equal contiguous shares, one
+// per CTA of a grid that fills the machine once, so ragged batches load every
+// SM alike and no length is needed on the host.  A unit that lies inside one
+// share is finished by its CTA; the pieces of one that does not are merged by a
+// second kernel (at most two pieces per CTA, so the workspace does not depend
+// on the lengths).  Each warp runs its own ring of TMA loads (box: 16 tokens of
+// one block), addressed through page numbers and scales that its lanes fetch
+// 32 tiles ahead.
+#include <math.h>
+
+#include <algorithm>
+
 #include "cache.cuh"
 
 namespace fattn {
 namespace {
 
-template <int D, bool E5M2>
-__global__ void __launch_bounds__(128) cache_fwd_plain_kernel(const CacheFwdParams p) {
-  __shared__ float sq[4][D];
-  const CacheParams& c = p.c;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long row = (long long)blockIdx.x * 4 + warp;
-  if (row >= (long long)c.total * p.Hq) return;
-  const int t = (int)(row / p.Hq), hq = (int)(row % p.Hq);
-  const int h = hq / (p.Hq / c.H);
-  const int b = warp_search(c.B, t, [&](int i) { return (long long)c.cu_seqlens[i]; });
-  CacheSeq s;
-  if (!cache_seq(c, b, &s)) {
-    if (lane == 0 && c.err) atomicCAS(c.err, 0u, (unsigned)ERR_SITE_CACHE_FWD);
-    return;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kOff = 8.f;   // p = 2^(y - m + kOff)
+constexpr float kLazy = 7.f;  // the reference moves when a y exceeds it by more; kOff + kLazy < 16
+constexpr int kWarps = 4;
+constexpr int kTile = 16;               // keys per warp tile
+constexpr int kChunk = kWarps * kTile;  // keys per CTA step
+
+template <int D, int NT_>
+struct Dec {
+  static constexpr int NT = NT_;
+  static constexpr int R = 8 * NT;                // query rows per unit
+  static constexpr int TILE = kTile * D;          // bytes
+  static constexpr int STAGE = 2 * TILE;          // keys and values
+  static constexpr int ST = D == 128 ? 3 : 6;     // ring slots per warp
+  static constexpr int OFF_RED = kWarps * ST * STAGE;
+  static constexpr int BUFS = NT == 1 ? 1 : 2;    // where the warps' results are summed
+  static constexpr int OFF_STAT = OFF_RED + BUFS * R * D * 4;
+  static constexpr int OFF_BAR = OFF_STAT + kWarps * R * 4;
+  static constexpr int SMEM = OFF_BAR + kWarps * ST * 8 + 16 + 1024;
+  static constexpr int CTAS = NT == 1 ? 4 : 3;    // per SM
+};
+
+// What a CTA leaves for the merge kernel: the unit that starts in its share and
+// ends in a later CTA's (parts = 0: there is none).
+struct Record {
+  int parts, rows, h, row0, first_row;
+};
+
+// The key/value chunks of sequence b (0: nothing to do here).
+struct SeqWork {
+  int nch, units;  // chunks per unit, units
+};
+__device__ __forceinline__ SeqWork seq_work(const CacheFwdParams& p, int R, int b, CacheSeq* s) {
+  SeqWork w{0, 0};
+  if (!cache_seq(p.c, b, s)) {
+    if (p.c.err) atomicCAS(p.c.err, 0u, (unsigned)ERR_SITE_CACHE_FWD);
+    return w;
   }
-  if (t >= s.row0 + s.n) return;  // behind the last sequence
-  const int limit = p.causal ? s.len - s.n + (t - s.row0) + 1 : s.len;  // keys [0, limit)
-  const uint16_t* q = p.q.p + (long long)t * p.q.st + (long long)hq * p.q.sh;
-  for (int i = lane; i < D; i += 32) sq[warp][i] = __uint_as_float((uint32_t)q[i] << 16);
-  __syncwarp();
-  float m = -INFINITY, l = 0.f, acc[D / 32];
+  if (s->n == 0) return w;
+  const int G = p.Hq / p.c.H;
+  w.nch = max(1, (s->len + kChunk - 1) / kChunk);
+  w.units = p.c.H * ((s->n * G + R - 1) / R);
+  return w;
+}
+
+// A position in the list of all chunks: chunk `pos` of sequence b.
+struct Cursor {
+  int b;
+  long long pos;
+  CacheSeq seq;
+  SeqWork w;
+};
+__device__ __forceinline__ void advance(const CacheFwdParams& p, int R, Cursor* c, long long by) {
+  c->pos += by;
+  while (c->pos >= (long long)c->w.nch * c->w.units && c->b < p.c.B) {
+    c->pos -= (long long)c->w.nch * c->w.units;
+    if (++c->b < p.c.B) c->w = seq_work(p, R, c->b, &c->seq);
+  }
+}
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 ld_shared_v2(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+// Whether a code's magnitude byte stands for NaN (or infinity).
+template <bool E5M2>
+__device__ __forceinline__ bool code_is_nan(uint32_t c) {
+  return (c & 0x7fu) >= (E5M2 ? 0x7cu : 0x7fu);
+}
+
+template <int D, bool E5M2, int NT>
+__global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
+    cache_fwd_kernel(const __grid_constant__ CUtensorMap tm_k,
+                     const __grid_constant__ CUtensorMap tm_v, const CacheFwdParams p) {
+  using C = Dec<D, NT>;
+  constexpr int R = C::R;
+  constexpr int KW = D / 16;   // 4-byte words of a key that a lane holds (16 values per step)
+  constexpr int VW = D / 32;   // 4-byte words of a value row that a lane holds
+  constexpr int MT = D / 16;   // 16-row tiles of O^T
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t sbase = (raw + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (sbase - raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  float* red = reinterpret_cast<float*>(smem + C::OFF_RED);    // [BUFS][R][D]
+  float* stat = reinterpret_cast<float*>(smem + C::OFF_STAT);  // [warps][R]
+  const uint32_t bar0 = sbase + C::OFF_BAR + 8u * (uint32_t)(warp * C::ST);
+  volatile uint32_t* abort_flag =
+      reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + kWarps * C::ST * 8);
+  const WaitCtx wctx{abort_flag, p.c.err};
+  const uint32_t ring = sbase + (uint32_t)(warp * C::ST * C::STAGE);
+
+  if (lane == 0) {
+    for (int i = 0; i < C::ST; ++i) mbar_init(bar0 + 8u * i, 1);
+    if (warp == 0) *abort_flag = 0u;
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+
+  // ---------------------------------------------------------------- this CTA's share
+  const int B = p.c.B, G = p.Hq / p.c.H;
+  long long total = 0;
+  for (int b = lane; b < B; b += 32) {
+    CacheSeq s;
+    const SeqWork w = seq_work(p, R, b, &s);
+    total += (long long)w.nch * w.units;
+  }
 #pragma unroll
-  for (int i = 0; i < D / 32; ++i) acc[i] = 0.f;
-  for (int j0 = 0; j0 < limit; j0 += 32) {
-    const int j = j0 + lane;
-    float x = -INFINITY, vs = 0.f;
-    long long off = 0;
-    if (j < limit) {
-      const int page = c.block_table[(long long)b * c.table_width + j / c.block_size];
-      if (page < 0 || page >= c.num_blocks) {
-        if (c.err) atomicCAS(c.err, 0u, (unsigned)ERR_SITE_CACHE_FWD + 1);
-      } else {
-        const long long block = (long long)page * c.H + h;
-        off = (block * c.block_size + j % c.block_size) * D;
-        const uint16_t* k = reinterpret_cast<const uint16_t*>(c.k + off);
-        float dot = 0.f;
-        for (int i = 0; i < D / 2; ++i) {
-          const float2 f = f16x2_to_f32(codes_to_f16x2<E5M2>(k[i]));
-          dot = fmaf(f.x, sq[warp][2 * i], dot);
-          dot = fmaf(f.y, sq[warp][2 * i + 1], dot);
-        }
-        x = dot * c.k_scale[block] * p.scale_log2;
-        vs = c.v_scale[block];
+  for (int w = 16; w > 0; w >>= 1) total += __shfl_xor_sync(0xffffffffu, total, w);
+  const long long share = (total + gridDim.x - 1) / gridDim.x;  // 0: no work at all
+  const long long lo = blockIdx.x * share;
+  const long long F64 = max(0LL, min(share, total - lo));
+  Cursor cur{B, 0, CacheSeq{0, 0, 0}, SeqWork{0, 0}};
+  if (F64 > 0) {
+    long long before = 0;
+    for (int b0 = 0; b0 < B; b0 += 32) {
+      CacheSeq s{0, 0, 0};
+      SeqWork w{0, 0};
+      if (b0 + lane < B) w = seq_work(p, R, b0 + lane, &s);
+      const long long mine = (long long)w.nch * w.units;
+      long long upto = mine;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const long long o = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d) upto += o;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, before + upto > lo);
+      if (past) {
+        const int src = __ffs(past) - 1;
+        cur.b = b0 + src;
+        cur.pos = lo - __shfl_sync(0xffffffffu, before + upto - mine, src);
+        cur.w.nch = __shfl_sync(0xffffffffu, w.nch, src);
+        cur.w.units = __shfl_sync(0xffffffffu, w.units, src);
+        cur.seq.row0 = __shfl_sync(0xffffffffu, s.row0, src);
+        cur.seq.n = __shfl_sync(0xffffffffu, s.n, src);
+        cur.seq.len = __shfl_sync(0xffffffffu, s.len, src);
+        break;
+      }
+      before += __shfl_sync(0xffffffffu, upto, 31);
+    }
+  }
+  const int F = (int)F64;  // chunks of this CTA
+  Record* records = reinterpret_cast<Record*>(p.workspace);
+  float* part_lse = reinterpret_cast<float*>(static_cast<char*>(p.workspace) +
+                                             (((size_t)gridDim.x * sizeof(Record) + 255) & ~255u));
+  float* part_o = part_lse + (((size_t)gridDim.x * 2 * R + 63) & ~(size_t)63);
+  Record rec{0, 0, 0, 0, 0};
+  __syncthreads();  // barriers initialised
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  // ---------------------------------------------------------------- tile info, 32 ahead
+  // Lane i of a set holds tile i of 32: its block (-1: no keys there) and scales.
+  struct Info {
+    int slice;  // page * H + h, -1: nothing to load
+    int row;    // first row in the block
+    float ks, lv;
+  };
+  const int bs = p.c.block_size;
+  auto fetch = [&](Cursor at, int f0) {  // tiles f0 .. f0 + 31, `at` being tile f0
+    Info r{-1, 0, 0.f, 0.f};
+    if (f0 + lane >= F) return r;
+    advance(p, R, &at, lane);
+    const int unit = (int)(at.pos / at.w.nch), ch = (int)(at.pos % at.w.nch);
+    const int h = unit / (at.w.units / p.c.H);
+    const int key = ch * kChunk + warp * kTile;
+    if (key >= at.seq.len) return r;
+    const int page = p.c.block_table[(long long)at.b * p.c.table_width + key / bs];
+    if (page < 0 || page >= p.c.num_blocks) {
+      if (p.c.err) atomicCAS(p.c.err, 0u, (unsigned)ERR_SITE_CACHE_FWD + 1);
+      return r;
+    }
+    r.slice = page * p.c.H + h;
+    r.row = key % bs;
+    r.ks = p.c.k_scale[r.slice];
+    r.lv = lg2(p.c.v_scale[r.slice]);
+    return r;
+  };
+  Cursor ahead = cur;
+  Info now = fetch(ahead, 0), next{-1, 0, 0.f, 0.f};
+  if (F > 32) {
+    advance(p, R, &ahead, 32);
+    next = fetch(ahead, 32);
+  }
+
+  int fi = 0;                    // next tile to load
+  uint32_t issued = 0, done = 0;  // live tiles loaded and consumed
+  auto issue = [&](int f) {      // keep the ring full while consuming tile f
+    while (fi < F && issued - done < (uint32_t)C::ST && (fi >> 5) <= (f >> 5) + 1) {
+      const bool in_now = (fi >> 5) == (f >> 5);
+      const int slice = __shfl_sync(0xffffffffu, in_now ? now.slice : next.slice, fi & 31);
+      const int row = __shfl_sync(0xffffffffu, in_now ? now.row : next.row, fi & 31);
+      ++fi;
+      if (slice < 0) continue;
+      if (lane == 0) {
+        const uint32_t slot = issued % C::ST;
+        const uint32_t bar = bar0 + 8u * slot, dst = ring + slot * C::STAGE;
+        mbar_arrive_expect_tx(bar, C::STAGE);
+        tma_load_3d(dst, &tm_k, bar, 0, row, slice);
+        tma_load_3d(dst + C::TILE, &tm_v, bar, 0, row, slice);
+      }
+      ++issued;
+    }
+  };
+  bool ok = true;
+
+  // ---------------------------------------------------------------- per-segment state
+  uint32_t qf[NT][KW][2];        // B operand of S^T: query row g (+ 8 nt)
+  float acc[MT][NT][4];          // O^T
+  float ref[NT][2], lsum[NT][2], qinv[NT][2];  // columns (query rows) 2t, 2t + 1 (+ 8 nt)
+  int lim[NT][2];                // keys visible to those rows
+  int lim_lo = 0, lim_hi = 0;    // least and most over the unit's rows
+  float lvb = 0.f;
+  bool first_live = true;
+
+  // Lane layout of the operands.  d = 128: rows of 128 bytes, 16-byte pieces
+  // swizzled by row & 7; matrix row i stands for key (i & 1) * 4 + i / 2 (so the
+  // two rows of a load phase lie four apart and touch different banks), and a
+  // lane's value columns are piece (g & 1) * 4 + g / 2.  d = 64: rows of 64 bytes,
+  // pieces swizzled by (row / 2) & 3; keys in order, and lanes of odd t load the
+  // odd one of a pair of value rows first.
+  const int krow = D == 128 ? ((g & 1) << 2 | g >> 1) : g;
+  const int vcol = D == 128 ? ((g & 1) << 2 | g >> 1) * 16 : g * 8;  // first column
+
+  for (int f = 0; f < F; ++f) {
+    if (f > 0 && (f & 31) == 0) {
+      now = next;
+      next = Info{-1, 0, 0.f, 0.f};
+      if (f + 32 < F) {
+        advance(p, R, &ahead, 32);
+        next = fetch(ahead, f + 32);
       }
     }
-    const bool seen = x != -INFINITY;
-    float mb = x;
+    if (ok) issue(f);
+    const int unit = (int)(cur.pos / cur.w.nch), ch = (int)(cur.pos % cur.w.nch);
+    const int nrb = cur.w.units / p.c.H;
+    const int h = unit / nrb, rb = unit % nrb;
+    const int rows = min(R, cur.seq.n * G - rb * R);
+
+    if (f == 0 || ch == 0) {
+      // ------------------------------------------------------------ a unit (or piece) begins
+      const int seen0 = p.causal ? cur.seq.len - cur.seq.n + 1 : cur.seq.len;  // token 0's keys
+      auto limit_of = [&](int r) {
+        return p.causal ? seen0 + (rb * R + r) / G : seen0;
+      };
+      lim_lo = limit_of(0);
+      lim_hi = min(cur.seq.len, limit_of(rows - 1));
 #pragma unroll
-    for (int w = 16; w > 0; w >>= 1) mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, w));
-    const unsigned any = __ballot_sync(0xffffffffu, seen);
-    if (any == 0u) continue;
-    const float mn = fmaxf(m, mb);
-    const float ref = mn == -INFINITY ? 0.f : mn;
-    const float alpha = ex2(m - ref);
-    const float pj = seen ? ex2(x - ref) : 0.f;
-    float sum = pj;
+      for (int nt = 0; nt < NT; ++nt) {
+        const int r = nt * 8 + g;
+        uint4 v[D / 32];  // bf16: 16 of d = 128's first half, 16 of its second (d = 64: 16)
 #pragma unroll
-    for (int w = 16; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
-    l = l * alpha + sum;
-    m = mn;
+        for (int i = 0; i < D / 32; ++i) v[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (r < rows) {
+          const int i = rb * R + r;
+          const uint16_t* q = p.q.p + (long long)(cur.seq.row0 + i / G) * p.q.st +
+                              (long long)(h * G + i % G) * p.q.sh;
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) acc[i] *= alpha;
-    for (int k = 0; k < 32; ++k) {
-      if (!(any >> k & 1u)) continue;
-      const float w = __shfl_sync(0xffffffffu, pj, k) * __shfl_sync(0xffffffffu, vs, k);
-      const long long o = __shfl_sync(0xffffffffu, off, k);
+          for (int j = 0; j < D / 32; ++j)
+            v[j] = *reinterpret_cast<const uint4*>(q + (j >> 1) * 64 + t * 16 + (j & 1) * 8);
+        }
+        uint32_t mx = 0u;
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i)
-        acc[i] = fmaf(w, f16x2_to_f32(codes_to_f16x2<E5M2>(c.v[o + lane + 32 * i])).x, acc[i]);
+        for (int j = 0; j < D / 32; ++j)
+          mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(v[j].x & 0x7fff7fffu, v[j].y & 0x7fff7fffu),
+                                     __vmaxu2(v[j].z & 0x7fff7fffu, v[j].w & 0x7fff7fffu)));
+        mx = max(mx & 0xffffu, mx >> 16);
+        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        // 2^(14 - exponent of the largest element); rows of zeros or with inf or NaN stay
+        int e = (int)(mx >> 7);  // biased exponent
+        e = (mx == 0u || e == 255) ? 0 : min(14 - (e - 127), 126);
+        const float mul = __uint_as_float((uint32_t)(e + 127) << 23);
+        const float back = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+        for (int w = 0; w < KW; ++w) {
+          const uint32_t* x = &v[w >> 1].x + (w & 1) * 2;
+          qf[nt][w][0] = pack_f16x2(__uint_as_float(x[0] << 16) * mul,
+                                    __uint_as_float(x[0] & 0xffff0000u) * mul);
+          qf[nt][w][1] = pack_f16x2(__uint_as_float(x[1] << 16) * mul,
+                                    __uint_as_float(x[1] & 0xffff0000u) * mul);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int col = 2 * t + i;
+          qinv[nt][i] = __shfl_sync(0xffffffffu, back, col * 4) * p.scale_log2;
+          lim[nt][i] = nt * 8 + col < rows ? min(cur.seq.len, limit_of(nt * 8 + col)) : 0;
+          ref[nt][i] = -INFINITY;
+          lsum[nt][i] = 0.f;
+        }
+      }
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[mt][nt][i] = 0.f;
+      first_live = true;
+      lvb = 0.f;
     }
-  }
-  const bool has = limit > 0 && !(l == 0.f);
-  const float inv = has ? 1.f / l : 0.f;
-  uint16_t* o = p.o.p + (long long)t * p.o.st + (long long)hq * p.o.sh;
+
+    // ---------------------------------------------------------------- one tile of 16 keys
+    const int key0 = ch * kChunk + warp * kTile;
+    const int slice = __shfl_sync(0xffffffffu, now.slice, f & 31);
+    if (slice >= 0 && ok) {
+      const float ks = __shfl_sync(0xffffffffu, now.ks, f & 31);
+      const float lv = __shfl_sync(0xffffffffu, now.lv, f & 31);
+      const uint32_t slot = done % C::ST;
+      ok = __all_sync(0xffffffffu, mbar_wait(bar0 + 8u * slot, (done / C::ST) & 1u, wctx,
+                                             ERR_SITE_CACHE_FWD + 2));
+      if (ok) {
+        if (first_live) lvb = lv;
+        first_live = false;
+        const uint32_t ka = ring + slot * C::STAGE, va = ka + C::TILE;
+        // S^T
+        float s[NT][4];
 #pragma unroll
-  for (int i = 0; i < D / 32; ++i)
-    o[lane + 32 * i] = (uint16_t)(pack_bf16x2(has ? acc[i] * inv : 0.f, 0.f) & 0xffffu);
-  if (lane == 0)
-    p.lse[(long long)hq * c.total + t] =
-        has ? (m + lg2(l)) * 0.6931471805599453f : -INFINITY;
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[nt][i] = 0.f;
+#pragma unroll
+        for (int half = 0; half < D / 64; ++half) {
+          uint32_t a[2][4];  // keys krow and krow + 8: 16 bytes
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int row = krow + 8 * i;
+            const int piece = half * 4 + t;
+            const uint32_t addr = D == 128 ? ka + row * 128 + ((piece ^ (row & 7)) << 4)
+                                           : ka + row * 64 + ((piece ^ ((row >> 1) & 3)) << 4);
+            const uint4 x = ld_shared_v4(addr);
+            a[i][0] = x.x, a[i][1] = x.y, a[i][2] = x.z, a[i][3] = x.w;
+          }
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const uint32_t a0 = codes_to_f16x2<E5M2>((uint16_t)(a[0][w] & 0xffffu));
+            const uint32_t a1 = codes_to_f16x2<E5M2>((uint16_t)(a[1][w] & 0xffffu));
+            const uint32_t a2 = codes_to_f16x2<E5M2>((uint16_t)(a[0][w] >> 16));
+            const uint32_t a3 = codes_to_f16x2<E5M2>((uint16_t)(a[1][w] >> 16));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma_f16(s[nt], a0, a1, a2, a3, qf[nt][half * 4 + w][0], qf[nt][half * 4 + w][1]);
+          }
+        }
+        // y = x + log2 vs; masked keys before the maximum
+        const bool masked = key0 + kTile > lim_lo;
+        const int k0 = key0 + krow, k1 = k0 + 8;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            s[nt][i] = fmaf(s[nt][i], ks * qinv[nt][i & 1], lv);
+            if (masked && (i < 2 ? k0 : k1) >= lim[nt][i & 1]) s[nt][i] = -INFINITY;
+          }
+        bool move = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            // the difference first: far from zero, ref + kLazy would be rounded
+            move |= fmaxf(s[nt][i], s[nt][i + 2]) - ref[nt][i] > kLazy;
+        if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float alpha[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float m = fmaxf(s[nt][i], s[nt][i + 2]);
+#pragma unroll
+              for (int w = 4; w < 32; w <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
+              m = fmaxf(m, ref[nt][i]);
+              alpha[i] = m == -INFINITY ? 1.f : ex2(ref[nt][i] - m);
+              ref[nt][i] = m;
+              lsum[nt][i] *= alpha[i];
+            }
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) acc[mt][nt][i] *= alpha[i & 1];
+          }
+        }
+        const float w = ex2(lvb - lv);
+        uint32_t pf[NT][2];  // B operand of O^T
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float pr[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float r = ref[nt][i & 1];
+            pr[i] = ex2((s[nt][i] - (r == -INFINITY ? 0.f : r)) + kOff);
+            lsum[nt][i & 1] = fmaf(pr[i], w, lsum[nt][i & 1]);
+          }
+          pf[nt][0] = movmatrix(pack_f16x2(pr[0], pr[1]));
+          pf[nt][1] = movmatrix(pack_f16x2(pr[2], pr[3]));
+        }
+        // value rows of this lane: keys of matrix rows 2t, 2t + 1, 2t + 8, 2t + 9
+        uint32_t v[4][VW];
+        const int odd = D == 64 ? (t & 1) : 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = D == 128 ? t + 4 * i : 2 * t + ((i & 1) ^ odd) + 8 * (i >> 1);
+          if constexpr (D == 128) {
+            const uint4 x = ld_shared_v4(va + row * 128 + (((vcol >> 4) ^ (row & 7)) << 4));
+            v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
+          } else {
+            const uint2 x = ld_shared_v2(va + row * 64 + (((vcol >> 4) ^ ((row >> 1) & 3)) << 4) +
+                                         (vcol & 15));
+            v[i][0] = x.x, v[i][1] = x.y;
+          }
+          if (key0 + kTile > lim_hi && key0 + row >= lim_hi) {  // stale rows, whatever they hold
+#pragma unroll
+            for (int j = 0; j < VW; ++j) v[i][j] = 0u;
+          }
+        }
+        // keys that some rows see and others do not: a NaN there must reach the former
+        // only, and zero weights do not keep it out of the product
+        uint32_t nan_keys[4 * VW];  // per column: the tile's keys (bit = row) that hold NaN
+        bool poison = false;
+        if (lim_lo < min(key0 + kTile, lim_hi)) {
+          bool any = false;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4 * VW; ++j)
+              any |= code_is_nan<E5M2>(v[i][j >> 2] >> (8 * (j & 3)));
+          poison = __any_sync(0xffffffffu, any);
+          if (poison) {
+#pragma unroll
+            for (int j = 0; j < 4 * VW; ++j) {
+              uint32_t m = 0u;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int row = D == 128 ? t + 4 * i : 2 * t + ((i & 1) ^ odd) + 8 * (i >> 1);
+                if (code_is_nan<E5M2>(v[i][j >> 2] >> (8 * (j & 3)))) {
+                  m |= 1u << row;
+                  v[i][j >> 2] &= ~(0xffu << (8 * (j & 3)));
+                }
+              }
+              m |= __shfl_xor_sync(0xffffffffu, m, 1);
+              m |= __shfl_xor_sync(0xffffffffu, m, 2);
+              nan_keys[j] = m;
+            }
+          }
+        }
+        // O^T: bytes 2 mt, 2 mt + 1 of the lane's columns are rows g, g + 8 of tile mt
+        const uint32_t sel_lo = odd ? 0x1504u : 0x5140u, sel_hi = odd ? 0x3726u : 0x7362u;
+#pragma unroll
+        for (int j = 0; j < VW; ++j) {
+          const uint32_t lo01 = __byte_perm(v[0][j], v[1][j], sel_lo);
+          const uint32_t lo23 = __byte_perm(v[0][j], v[1][j], sel_hi);
+          const uint32_t hi01 = __byte_perm(v[2][j], v[3][j], sel_lo);
+          const uint32_t hi23 = __byte_perm(v[2][j], v[3][j], sel_hi);
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            const uint32_t x = m ? lo23 : lo01, y = m ? hi23 : hi01;
+            const uint32_t a0 = codes_to_f16x2<E5M2>((uint16_t)(x & 0xffffu));
+            const uint32_t a1 = codes_to_f16x2<E5M2>((uint16_t)(x >> 16));
+            const uint32_t a2 = codes_to_f16x2<E5M2>((uint16_t)(y & 0xffffu));
+            const uint32_t a3 = codes_to_f16x2<E5M2>((uint16_t)(y >> 16));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma_f16(acc[2 * j + m][nt], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+          }
+        }
+        if (poison) {  // rare
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int see = max(0, min(kTile, lim[nt][i] - key0));
+#pragma unroll
+              for (int j = 0; j < 4 * VW; ++j)
+                if (nan_keys[j] & ((1u << see) - 1u))
+                  acc[j >> 1][nt][(j & 1) * 2 + i] = __uint_as_float(0x7fffffffu);
+            }
+        }
+        __syncwarp();  // the slot may be loaded again
+        ++done;
+      }
+    }
+
+    // ---------------------------------------------------------------- a unit (or piece) ends
+    const bool unit_ends = ch == cur.w.nch - 1;
+    if (unit_ends || f == F - 1) {
+      // this warp's rows: normalised result and log2-sum-exp
+      float mine[NT][2], fac[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float l = lsum[nt][i];
+#pragma unroll
+          for (int w = 4; w < 32; w <<= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
+          lsum[nt][i] = l;
+          mine[nt][i] = l == 0.f ? -INFINITY : ref[nt][i] - kOff - lvb + lg2(l);
+          if (g == 0) stat[warp * R + nt * 8 + 2 * t + i] = mine[nt][i];
+        }
+      __syncthreads();
+      float top[NT][2], sum[NT][2];
+      const float up = ex2(lvb);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = nt * 8 + 2 * t + i;
+          float m = -INFINITY, z = 0.f;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) m = fmaxf(m, stat[w * R + r]);
+          const float mm = m == -INFINITY ? 0.f : m;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) z += ex2(stat[w * R + r] - mm);
+          top[nt][i] = m;
+          sum[nt][i] = z;
+          fac[nt][i] = lsum[nt][i] == 0.f ? 0.f : ex2(mine[nt][i] - mm) / (z * lsum[nt][i]);
+        }
+      // sum over the warps: the first ones write, the others add in turn
+#pragma unroll 1
+      for (int phase = 0; phase < kWarps / C::BUFS; ++phase) {
+        if (warp / C::BUFS == phase) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float4* dst = reinterpret_cast<float4*>(red + ((warp % C::BUFS) * R + nt * 8 + 2 * t + i) * D + vcol);
+#pragma unroll
+              for (int j = 0; j < VW; ++j) {
+                float4 x;
+                x.x = acc[2 * j][nt][i] * fac[nt][i] * up;
+                x.y = acc[2 * j][nt][i + 2] * fac[nt][i] * up;
+                x.z = acc[2 * j + 1][nt][i] * fac[nt][i] * up;
+                x.w = acc[2 * j + 1][nt][i + 2] * fac[nt][i] * up;
+                if (phase) {
+                  const float4 y = dst[j];
+                  x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+                }
+                dst[j] = x;
+              }
+            }
+        }
+        __syncthreads();
+      }
+      const bool starts_here = f >= ch;  // the unit's chunk 0 is in this share
+      const bool whole = starts_here && unit_ends;
+      const int slot = starts_here ? 1 : 0;
+      if (warp == 0 && g == 0) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int r = nt * 8 + 2 * t + i;
+            const float L = top[nt][i] == -INFINITY && sum[nt][i] == 0.f
+                                ? -INFINITY
+                                : (top[nt][i] + lg2(sum[nt][i])) * kLn2;
+            if (r < rows) {
+              if (whole) {
+                const int i0 = rb * R + r;
+                p.lse[(long long)(h * G + i0 % G) * p.c.total + cur.seq.row0 + i0 / G] = L;
+              } else {
+                part_lse[((size_t)blockIdx.x * 2 + slot) * R + r] = L;
+              }
+            }
+          }
+      }
+      for (int x = threadIdx.x; x < rows * (D / 4); x += 128) {
+        const int r = x / (D / 4), c4 = x % (D / 4);
+        float4 o = reinterpret_cast<const float4*>(red)[r * (D / 4) + c4];
+        if (C::BUFS == 2) {
+          const float4 b = reinterpret_cast<const float4*>(red)[(R + r) * (D / 4) + c4];
+          o.x += b.x, o.y += b.y, o.z += b.z, o.w += b.w;
+        }
+        if (whole) {
+          const int i0 = rb * R + r;
+          *reinterpret_cast<uint2*>(p.o.p + (long long)(cur.seq.row0 + i0 / G) * p.o.st +
+                                    (long long)(h * G + i0 % G) * p.o.sh + c4 * 4) =
+              make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+        } else {
+          reinterpret_cast<float4*>(part_o)[(((size_t)blockIdx.x * 2 + slot) * R + r) * (D / 4) +
+                                            c4] = o;
+        }
+      }
+      if (starts_here && !unit_ends) {  // later CTAs hold the rest
+        const long long u0 = lo + f - ch;
+        rec.parts = (int)((u0 + cur.w.nch - 1) / share - blockIdx.x) + 1;
+        rec.rows = rows;
+        rec.h = h;
+        rec.row0 = cur.seq.row0;
+        rec.first_row = rb * R;
+      }
+    }
+    advance(p, R, &cur, 1);
+  }
+  // loads in flight land before the CTA ends (only after a wait that ran out)
+  for (; done < issued; ++done)
+    mbar_drain(bar0 + 8u * (done % C::ST), (done / C::ST) & 1u, wctx, ERR_SITE_CACHE_FWD + 3);
+  if (threadIdx.x == 0) records[blockIdx.x] = rec;
+}
+
+// Joins the pieces of the unit that CTA blockIdx.x of the kernel above began and
+// did not finish: its own second slot, then the first slots of the CTAs behind.
+template <int D>
+__global__ void __launch_bounds__(256) cache_merge_kernel(const CacheFwdParams p, int R) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Record rec = reinterpret_cast<const Record*>(p.workspace)[blockIdx.x];
+  if (rec.parts == 0) return;
+  const float* part_lse = reinterpret_cast<const float*>(
+      static_cast<const char*>(p.workspace) + (((size_t)gridDim.x * sizeof(Record) + 255) & ~255u));
+  const float* part_o = part_lse + (((size_t)gridDim.x * 2 * R + 63) & ~(size_t)63);
+  const int G = p.Hq / p.c.H;
+  constexpr float kLog2e = 1.4426950408889634f;
+  for (int x = threadIdx.x; x < rec.rows * (D / 4); x += 256) {
+    const int r = x / (D / 4), c4 = x % (D / 4);
+    // piece i: slot 1 of this CTA, slot 0 of the next ones
+    auto at = [&](int i) { return ((size_t)(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * R + r; };
+    float m = -INFINITY;
+    for (int i = 0; i < rec.parts; ++i) m = fmaxf(m, part_lse[at(i)]);
+    const float mm = m == -INFINITY ? 0.f : m;
+    float sum = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < rec.parts; ++i) {
+      const float w = ex2((part_lse[at(i)] - mm) * kLog2e);
+      const float4 v = reinterpret_cast<const float4*>(part_o)[at(i) * (D / 4) + c4];
+      sum += w;
+      o.x = fmaf(w, v.x, o.x), o.y = fmaf(w, v.y, o.y);
+      o.z = fmaf(w, v.z, o.z), o.w = fmaf(w, v.w, o.w);
+    }
+    const bool any = !(sum == 0.f);
+    const float inv = any ? 1.f / sum : 0.f;
+    const int i0 = rec.first_row + r;
+    const long long token = rec.row0 + i0 / G;
+    const int hq = rec.h * G + i0 % G;
+    *reinterpret_cast<uint2*>(p.o.p + token * p.o.st + hq * p.o.sh + c4 * 4) = make_uint2(
+        pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    if (c4 == 0) p.lse[(long long)hq * p.c.total + token] = any ? mm + lg2(sum) * kLn2 : -INFINITY;
+  }
+}
+
+template <int D, bool E5M2, int NT>
+cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const CacheFwdParams& p, int n_sm,
+                   cudaStream_t stream) {
+  using C = Dec<D, NT>;
+  static_assert(C::CTAS * (C::SMEM + 1024) <= 233472, "shared memory of the CTAs sharing an SM");
+  static unsigned long long prepared[64];
+  const cudaError_t e = prepare_once(prepared, [] {
+    return cudaFuncSetAttribute(cache_fwd_kernel<D, E5M2, NT>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  });
+  if (e != cudaSuccess) return e;
+  const unsigned grid = (unsigned)(n_sm * C::CTAS);
+  cache_fwd_kernel<D, E5M2, NT><<<grid, 128, C::SMEM, stream>>>(tk, tv, p);
+  if (const cudaError_t r = cudaGetLastError()) return r;
+  // the merge starts while the last CTAs finish, and waits for them on the device
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, cache_merge_kernel<D>, p, (int)C::R);
+}
+
+template <int D, bool E5M2>
+cudaError_t launch_rows(const CUtensorMap& tk, const CUtensorMap& tv, const CacheFwdParams& p,
+                        int n_sm, cudaStream_t stream) {
+  const long long rows = (long long)p.c.max_seqlen * (p.Hq / p.c.H);
+  return rows <= 8 ? launch<D, E5M2, 1>(tk, tv, p, n_sm, stream)
+                   : launch<D, E5M2, 2>(tk, tv, p, n_sm, stream);
 }
 
 }  // namespace
 
-size_t cache_fwd_workspace(const CacheParams&, int, int) { return 256; }
+size_t cache_fwd_workspace(const CacheParams& c, int, int n_sm) {
+  // records, then LSE and O of two pieces per CTA, for the larger of the two variants
+  auto bytes = [&](int R, int ctas) {
+    const size_t grid = (size_t)n_sm * ctas;
+    return ((grid * sizeof(Record) + 255) & ~(size_t)255) +
+           ((grid * 2 * R + 63) & ~(size_t)63) * 4 + grid * 2 * R * c.d * 4;
+  };
+  return std::max(bytes(Dec<128, 1>::R, Dec<128, 1>::CTAS), bytes(Dec<128, 2>::R, Dec<128, 2>::CTAS));
+}
 
-cudaError_t launch_cache_fwd(const CacheFwdParams& p, int, cudaStream_t stream) {
-  const long long ctas = ((long long)p.c.total * p.Hq + 3) / 4;
-  if (p.c.d == 128) {
-    if (p.c.format) cache_fwd_plain_kernel<128, true><<<(unsigned)ctas, 128, 0, stream>>>(p);
-    else cache_fwd_plain_kernel<128, false><<<(unsigned)ctas, 128, 0, stream>>>(p);
-  } else {
-    if (p.c.format) cache_fwd_plain_kernel<64, true><<<(unsigned)ctas, 128, 0, stream>>>(p);
-    else cache_fwd_plain_kernel<64, false><<<(unsigned)ctas, 128, 0, stream>>>(p);
-  }
-  return cudaGetLastError();
+cudaError_t launch_cache_fwd(const CUtensorMap& tk, const CUtensorMap& tv, const CacheFwdParams& p,
+                             int n_sm, cudaStream_t stream) {
+  if (p.c.d == 128)
+    return p.c.format ? launch_rows<128, true>(tk, tv, p, n_sm, stream)
+                      : launch_rows<128, false>(tk, tv, p, n_sm, stream);
+  return p.c.format ? launch_rows<64, true>(tk, tv, p, n_sm, stream)
+                    : launch_rows<64, false>(tk, tv, p, n_sm, stream);
 }
 
 }  // namespace fattn

@@ -207,7 +207,9 @@ cudaError_t launch_cache_append(const CacheParams& c, const TokenView& k, const 
 cudaError_t launch_cache_read(const CacheParams& c, const TokenView& k, const TokenView& v,
                               cudaStream_t stream);
 size_t cache_fwd_workspace(const CacheParams& c, int Hq, int n_sm);
-cudaError_t launch_cache_fwd(const CacheFwdParams& p, int n_sm, cudaStream_t stream);
+// tk, tv: maps of the codes, {d, block_size, num_blocks * H}, boxes of 16 tokens
+cudaError_t launch_cache_fwd(const CUtensorMap& tk, const CUtensorMap& tv, const CacheFwdParams& p,
+                             int n_sm, cudaStream_t stream);
 
 cudaError_t launch_bwd_preprocess(const void* o, const void* dout, float* delta, float* dq_acc,
                                   long long rows, int d, int n_sm, cudaStream_t stream);
