@@ -44,6 +44,11 @@
 
 #include "cache.cuh"
 
+#ifndef FATTN_ST1
+#define FATTN_ST1 3
+#define FATTN_ST2 3
+#define FATTN_CTAS1 3
+#endif
 namespace fattn {
 namespace {
 
@@ -60,14 +65,19 @@ struct Dec {
   static constexpr int R = 8 * NT;                // query rows per unit
   static constexpr int TILE = kTile * D;          // bytes
   static constexpr int STAGE = 2 * TILE;          // keys and values
-  static constexpr int ST = D == 128 ? 3 : 6;     // ring slots per warp
+  static constexpr int ST = (D == 128 ? 1 : 2) * (NT == 1 ? FATTN_ST1 : FATTN_ST2);     // ring slots per warp
   static constexpr int OFF_RED = kWarps * ST * STAGE;
-  static constexpr int BUFS = NT == 1 ? 1 : 2;    // where the warps' results are summed
+  static constexpr int BUFS = 1;    // where the warps' results are summed
   static constexpr int OFF_STAT = OFF_RED + BUFS * R * D * 4;
   static constexpr int OFF_BAR = OFF_STAT + kWarps * R * 4;
   static constexpr int SMEM = OFF_BAR + kWarps * ST * 8 + 16 + 1024;
-  static constexpr int CTAS = NT == 1 ? 4 : 3;    // per SM
+  static constexpr int CTAS = NT == 1 ? FATTN_CTAS1 : 3;    // per SM
 };
+
+#ifndef FATTN_NARROW
+#define FATTN_NARROW 64
+#endif
+constexpr int kNarrowRows = FATTN_NARROW;
 
 // What a CTA leaves for the merge kernel: the unit that starts in its share and
 // ends in a later CTA's (parts = 0: there is none).
@@ -85,8 +95,8 @@ __device__ __forceinline__ SeqWork seq_work(const CacheFwdParams& p, int R, int 
     if (p.c.err) atomicCAS(p.c.err, 0u, (unsigned)ERR_SITE_CACHE_FWD);
     return w;
   }
-  if (s->n == 0) return w;
   const int G = p.Hq / p.c.H;
+  if (s->n == 0 || s->n * G > p.narrow_rows) return w;  // (or the wide kernel's)
   w.nch = max(1, (s->len + kChunk - 1) / kChunk);
   w.units = p.c.H * ((s->n * G + R - 1) / R);
   return w;
@@ -298,6 +308,13 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
   const int krow = D == 128 ? ((g & 1) << 2 | g >> 1) : g;
   const int vcol = D == 128 ? ((g & 1) << 2 | g >> 1) * 16 : g * 8;  // first column
 
+  int h = 0, rb = 0, ch = 0, nrb = 0;  // the current chunk: head, row block, chunk in the unit
+  if (F > 0) {
+    const int unit = (int)(cur.pos / cur.w.nch);
+    ch = (int)(cur.pos % cur.w.nch);
+    nrb = cur.w.units / p.c.H;
+    h = unit / nrb, rb = unit % nrb;
+  }
   for (int f = 0; f < F; ++f) {
     if (f > 0 && (f & 31) == 0) {
       now = next;
@@ -308,9 +325,6 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
       }
     }
     if (ok) issue(f);
-    const int unit = (int)(cur.pos / cur.w.nch), ch = (int)(cur.pos % cur.w.nch);
-    const int nrb = cur.w.units / p.c.H;
-    const int h = unit / nrb, rb = unit % nrb;
     const int rows = min(R, cur.seq.n * G - rb * R);
 
     if (f == 0 || ch == 0) {
@@ -469,53 +483,43 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
           pf[nt][1] = movmatrix(pack_f16x2(pr[2], pr[3]));
         }
         // value rows of this lane: keys of matrix rows 2t, 2t + 1, 2t + 8, 2t + 9
-        uint32_t v[4][VW];
         const int odd = D == 64 ? (t & 1) : 0;
+        auto value_row = [&](int i) {
+          return D == 128 ? t + 4 * i : 2 * t + ((i & 1) ^ odd) + 8 * (i >> 1);
+        };
+        auto load_values = [&](uint32_t (&v)[4][VW]) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int row = D == 128 ? t + 4 * i : 2 * t + ((i & 1) ^ odd) + 8 * (i >> 1);
-          if constexpr (D == 128) {
-            const uint4 x = ld_shared_v4(va + row * 128 + (((vcol >> 4) ^ (row & 7)) << 4));
-            v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
-          } else {
-            const uint2 x = ld_shared_v2(va + row * 64 + (((vcol >> 4) ^ ((row >> 1) & 3)) << 4) +
-                                         (vcol & 15));
-            v[i][0] = x.x, v[i][1] = x.y;
-          }
-          if (key0 + kTile > lim_hi && key0 + row >= lim_hi) {  // stale rows, whatever they hold
+          for (int i = 0; i < 4; ++i) {
+            const int row = value_row(i);
+            if constexpr (D == 128) {
+              const uint4 x = ld_shared_v4(va + row * 128 + (((vcol >> 4) ^ (row & 7)) << 4));
+              v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
+            } else {
+              const uint2 x = ld_shared_v2(va + row * 64 +
+                                           (((vcol >> 4) ^ ((row >> 1) & 3)) << 4) + (vcol & 15));
+              v[i][0] = x.x, v[i][1] = x.y;
+            }
+            if (key0 + kTile > lim_hi && key0 + row >= lim_hi) {  // stale rows, whatever they hold
 #pragma unroll
-            for (int j = 0; j < VW; ++j) v[i][j] = 0u;
+              for (int j = 0; j < VW; ++j) v[i][j] = 0u;
+            }
           }
-        }
+        };
+        uint32_t v[4][VW];
+        load_values(v);
         // keys that some rows see and others do not: a NaN there must reach the former
-        // only, and zero weights do not keep it out of the product
-        uint32_t nan_keys[4 * VW];  // per column: the tile's keys (bit = row) that hold NaN
+        // only, and a weight of zero does not keep it out of the product
         bool poison = false;
         if (lim_lo < min(key0 + kTile, lim_hi)) {
-          bool any = false;
 #pragma unroll
           for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int j = 0; j < 4 * VW; ++j)
-              any |= code_is_nan<E5M2>(v[i][j >> 2] >> (8 * (j & 3)));
-          poison = __any_sync(0xffffffffu, any);
-          if (poison) {
-#pragma unroll
-            for (int j = 0; j < 4 * VW; ++j) {
-              uint32_t m = 0u;
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int row = D == 128 ? t + 4 * i : 2 * t + ((i & 1) ^ odd) + 8 * (i >> 1);
-                if (code_is_nan<E5M2>(v[i][j >> 2] >> (8 * (j & 3)))) {
-                  m |= 1u << row;
-                  v[i][j >> 2] &= ~(0xffu << (8 * (j & 3)));
-                }
+              if (code_is_nan<E5M2>(v[i][j >> 2] >> (8 * (j & 3)))) {
+                poison = true;
+                v[i][j >> 2] &= ~(0xffu << (8 * (j & 3)));
               }
-              m |= __shfl_xor_sync(0xffffffffu, m, 1);
-              m |= __shfl_xor_sync(0xffffffffu, m, 2);
-              nan_keys[j] = m;
-            }
-          }
+          poison = __any_sync(0xffffffffu, poison);
         }
         // O^T: bytes 2 mt, 2 mt + 1 of the lane's columns are rows g, g + 8 of tile mt
         const uint32_t sel_lo = odd ? 0x1504u : 0x5140u, sel_hi = odd ? 0x3726u : 0x7362u;
@@ -537,17 +541,23 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
               mma_f16(acc[2 * j + m][nt], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
           }
         }
-        if (poison) {  // rare
+        if (poison) {  // rare: NaN for the rows that see it
+          load_values(v);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+          for (int j = 0; j < 4 * VW; ++j) {
+            uint32_t bad = 0u;  // the tile's keys whose value in this column is NaN
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int see = max(0, min(kTile, lim[nt][i] - key0));
+            for (int i = 0; i < 4; ++i)
+              if (code_is_nan<E5M2>(v[i][j >> 2] >> (8 * (j & 3)))) bad |= 1u << value_row(i);
+            bad |= __shfl_xor_sync(0xffffffffu, bad, 1);
+            bad |= __shfl_xor_sync(0xffffffffu, bad, 2);
 #pragma unroll
-              for (int j = 0; j < 4 * VW; ++j)
-                if (nan_keys[j] & ((1u << see) - 1u))
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                if (bad & ((1u << max(0, min(kTile, lim[nt][i] - key0))) - 1u))
                   acc[j >> 1][nt][(j & 1) * 2 + i] = __uint_as_float(0x7fffffffu);
-            }
+          }
         }
         __syncwarp();  // the slot may be loaded again
         ++done;
@@ -662,7 +672,20 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
         rec.first_row = rb * R;
       }
     }
-    advance(p, R, &cur, 1);
+    if (!unit_ends) {
+      ++ch;
+    } else {
+      ch = 0;
+      if (++rb == nrb) {
+        rb = 0;
+        if (++h == p.c.H) {  // the next sequence with work
+          h = 0;
+          cur.pos = (long long)cur.w.nch * cur.w.units;
+          advance(p, R, &cur, 0);
+          nrb = cur.w.units / p.c.H;
+        }
+      }
+    }
   }
   // loads in flight land before the CTA ends (only after a wait that ran out)
   for (; done < issued; ++done)
@@ -756,8 +779,14 @@ size_t cache_fwd_workspace(const CacheParams& c, int, int n_sm) {
   return std::max(bytes(Dec<128, 1>::R, Dec<128, 1>::CTAS), bytes(Dec<128, 2>::R, Dec<128, 2>::CTAS));
 }
 
-cudaError_t launch_cache_fwd(const CUtensorMap& tk, const CUtensorMap& tv, const CacheFwdParams& p,
-                             int n_sm, cudaStream_t stream) {
+cudaError_t launch_cache_fwd(const CUtensorMap& tk, const CUtensorMap& tv,
+                             const CacheFwdParams& params, int n_sm, cudaStream_t stream) {
+  CacheFwdParams p = params;
+  p.narrow_rows = kNarrowRows;
+  if ((long long)p.c.max_seqlen * (p.Hq / p.c.H) > kNarrowRows) {
+    const cudaError_t e = launch_cache_fwd_wide(p, stream);
+    if (e != cudaSuccess) return e;
+  }
   if (p.c.d == 128)
     return p.c.format ? launch_rows<128, true>(tk, tv, p, n_sm, stream)
                       : launch_rows<128, false>(tk, tv, p, n_sm, stream);

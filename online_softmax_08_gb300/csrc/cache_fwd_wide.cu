@@ -1,0 +1,662 @@
+// cache_fwd_wide.cu -- attention over the paged 8-bit key/value cache, many query
+// rows per key/value head (pieces of prompts): tcgen05 + TMEM.
+//
+// One CTA owns 256 rows of one (sequence, key/value head): two 128-row subtiles.
+// A row is a (token, query head of the group), token-major, so all heads that
+// share a key/value head share the CTA's keys.  The structure is that of the
+// dense forward kernel: keys and values of 128 tokens at a time pass through a
+// ring of shared-memory slots, S_s = Q_s K^T lives in TMEM, the softmax warps turn
+// it into P_s in place, and O_s += P_s V accumulates in TMEM.
+//
+// What differs is how a slot is filled.  The codes cannot feed the tensor core as
+// they are (q and P need more than 8 bits), so three warps load them from their
+// blocks, convert them to fp16 (exact) and store them into the slot in the
+// 128-byte-swizzled layout that a TMA load would leave.  A tile pair of 128 keys
+// is 16 pieces of 16 tokens (a piece lies in one block); the warps take pieces in
+// turn and keep three of them in flight.
+//
+// The scales are applied by the softmax, per piece, as in the kernel for few rows:
+// y = s * ks + log2 vs, p = 2^(y - r) (fp16), l += w p with w = 2^(b - log2 vs),
+// O = 2^b acc / l.  r is the running maximum of y less 8, moved only when a y
+// exceeds it by more than 15 (p stays below 2^16); where |y| >= 2^22 it is the
+// maximum itself, as 8 is then too near its rounding.
+//
+// Warps: 0-3 softmax of subtile 0, 4-7 of subtile 1 (thread t owns row t; they also
+// load Q and write O), 8 issues the MMAs, 9-11 fill the slots.  TMEM: S_0, S_1, O_0,
+// O_1.  Measured limits: see the launcher.
+#define FATTN_INLINE_WAIT_SLOW_PATH
+#include <math.h>
+
+#include "cache.cuh"
+
+namespace fattn {
+namespace {
+
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kOff = 8.f;    // the reference lies this far below the running maximum
+constexpr float kRoom = 15.f;  // and moves when a y exceeds it by more
+constexpr float kFar = 4194304.f;
+
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+// (r0, r1) = (a0, a1) * (b, b) + (c, c)
+__device__ __forceinline__ void fma_x2(float a0, float a1, float b, float c, float& r0, float& r1) {
+  asm("{\n\t.reg .b64 a, b, c, r;\n\t"
+      "mov.b64 a, {%2, %3};\n\t"
+      "mov.b64 b, {%4, %4};\n\t"
+      "mov.b64 c, {%5, %5};\n\t"
+      "fma.rn.f32x2 r, a, b, c;\n\t"
+      "mov.b64 {%0, %1}, r;\n\t}"
+      : "=f"(r0), "=f"(r1)
+      : "f"(a0), "f"(a1), "f"(b), "f"(c));
+}
+// (s0, s1) = (a0, a1) + (b0, b1)
+__device__ __forceinline__ void add_x2(float a0, float a1, float b0, float b1, float& s0,
+                                       float& s1) {
+  asm("{\n\t.reg .b64 s, a, b;\n\t"
+      "mov.b64 a, {%2, %3};\n\t"
+      "mov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 s, a, b;\n\t"
+      "mov.b64 {%0, %1}, s;\n\t}"
+      : "=f"(s0), "=f"(s1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+
+template <int D>
+struct Wide {
+  static constexpr int BM = 128;                // rows per subtile
+  static constexpr int ROWS = 2 * BM;           // rows per CTA
+  static constexpr int BN = 128;                // keys per tile
+  static constexpr int PIECES = BN / 16;
+  static constexpr int HALF = BM * 128;         // 64 columns of 128 rows (bytes)
+  static constexpr int TILE = BM * D * 2;       // fp16
+  // With at most 6 slots, K of tile j + 4 is filled only after S of tile j + 1 was
+  // issued or all PV of tile j, hence after the softmax read tile j's scales: a ring
+  // of four tiles' scales needs no barrier for its reuse
+  static constexpr int STAGES = D == 128 ? 5 : 6;
+  static constexpr int SCALE_TILES = 4;
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_KV = OFF_Q + 2 * TILE;
+  static constexpr int OFF_SCALE = OFF_KV + STAGES * TILE;  // [SCALE_TILES][PIECES] float4
+  static constexpr int OFF_BAR = OFF_SCALE + SCALE_TILES * PIECES * 16;
+  static constexpr int SMEM = OFF_BAR + 256 + 1024;
+  static constexpr int THREADS = 384;
+  static constexpr int W_MMA = 8, W_FILL = 9, N_FILL = 3;
+  static constexpr int REG_LAUNCH = 168, REG_SOFTMAX = 208, REG_CTRL = 88;
+  static_assert((2 * REG_SOFTMAX + REG_CTRL) * 128 <= THREADS * REG_LAUNCH, "register split");
+  static_assert(SMEM <= 232448, "shared memory budget");
+  static constexpr uint32_t TM_S = 0, TM_O = 256;
+  static constexpr uint32_t TMEM_COLS = 512;
+  // fp16 operands, fp32 result: as idesc_bf16_f32 with the formats' fields zero
+  static constexpr uint32_t kFormats = (1u << 7) | (1u << 10);
+  static constexpr uint32_t IDESC_S = idesc_bf16_f32(128, BN, false, false) & ~kFormats;
+  static constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, D, false, true) & ~kFormats;
+};
+
+enum {
+  B_Q = 0,        // softmax threads -> MMA: Q in shared memory
+  B_S_FULL = 1,   // [2] MMA -> softmax
+  B_P_FULL = 3,   // [2] softmax -> MMA: P_s in TMEM
+  B_PV_DONE = 5,  // [2] MMA -> epilogue
+  B_P_HALF = 7,   // [2] softmax -> MMA: keys 0-63 of P_s in TMEM and O_s rescaled
+  B_MMA_DONE = 9,
+  B_SCALE = 10,    // [SCALE_TILES] slot filling -> softmax: the scales of a tile
+  B_KV_FULL = 14,  // [STAGES], then kv_empty [STAGES]
+};
+static_assert(8 * (B_KV_FULL + 2 * Wide<64>::STAGES) + 16 <= 256, "barrier block");
+
+template <bool E5M2>
+__device__ __forceinline__ bool word_has_nan(uint32_t w) {  // any of four codes NaN (or infinite)
+  bool any = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) any |= ((w >> (8 * i)) & 0x7fu) >= (E5M2 ? 0x7cu : 0x7fu);
+  return any;
+}
+template <bool E5M2>
+__device__ __forceinline__ uint32_t without_nan(uint32_t w) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (((w >> (8 * i)) & 0x7fu) >= (E5M2 ? 0x7cu : 0x7fu)) w &= ~(0xffu << (8 * i));
+  return w;
+}
+
+template <int D, bool E5M2>
+__global__ void __launch_bounds__(Wide<D>::THREADS, 1)
+    cache_fwd_wide_kernel(const CacheFwdParams p) {
+  using C = Wide<D>;
+  constexpr int ST = C::STAGES;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t sbase = (raw + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (sbase - raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = p.Hq / p.c.H;
+
+  // Row blocks of sequence b sit at slots cu_seqlens[b] G / 256 + b and on, which
+  // is room for all of them; the later ones of a sequence, which see more keys, first.
+  const int h = (int)(blockIdx.x % (unsigned)p.c.H);
+  const long long slot = blockIdx.x / (unsigned)p.c.H;
+  const int b = warp_search(p.c.B, slot, [&](int i) {
+    return (long long)p.c.cu_seqlens[i] * G / C::ROWS + i;
+  });
+  CacheSeq seq;
+  if (!cache_seq(p.c, b, &seq)) {
+    if (threadIdx.x == 0 && p.c.err) atomicCAS(p.c.err, 0u, (unsigned)ERR_SITE_CACHE_FWD);
+    return;
+  }
+  const int n_rows = seq.n * G;
+  if (n_rows <= p.narrow_rows) return;  // the other kernel's
+  const int n_blocks = (n_rows + C::ROWS - 1) / C::ROWS;
+  const long long rank = slot - ((long long)seq.row0 * G / C::ROWS + b);
+  if (rank < 0 || rank >= n_blocks) return;
+  const int rb = n_blocks - 1 - (int)rank;
+
+  // keys seen by row r of the sequence
+  const int seen0 = p.causal ? seq.len - seq.n + 1 : seq.len;
+  auto limit_of = [&](int r) {
+    return max(0, min(seq.len, p.causal ? seen0 + r / G : seen0));
+  };
+  const int r0_0 = rb * C::ROWS, r0_1 = r0_0 + C::BM;
+  auto tiles_for = [&](int r0) {
+    return r0 >= n_rows ? 0 : (limit_of(min(r0 + C::BM, n_rows) - 1) + C::BN - 1) / C::BN;
+  };
+  const int nt0 = tiles_for(r0_0), nt1 = tiles_for(r0_1);
+  const int n_max = max(nt0, nt1);
+  const int lim_lo = limit_of(r0_0), lim_hi = limit_of(min(r0_0 + C::ROWS, n_rows) - 1);
+
+  const uint32_t bar0 = sbase + C::OFF_BAR;
+  auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
+  const uint32_t kv_full0 = bar(B_KV_FULL), kv_empty0 = bar(B_KV_FULL + ST);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + 8 * (B_KV_FULL + 2 * ST));
+  volatile uint32_t* abort_flag = tmem_slot + 1;
+  volatile uint32_t* poison = tmem_slot + 2;        // a NaN was kept out of some rows' sums
+  volatile float* base_lv = reinterpret_cast<float*>(tmem_slot + 3);  // b above
+  const WaitCtx wctx{abort_flag, p.c.err};
+  float4* scales = reinterpret_cast<float4*>(smem + C::OFF_SCALE);
+
+  if (threadIdx.x == 0) {
+    mbar_init(bar(B_Q), 256);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(bar(B_S_FULL + s), 1);
+      mbar_init(bar(B_P_FULL + s), 128);
+      mbar_init(bar(B_P_HALF + s), 128);
+      mbar_init(bar(B_PV_DONE + s), 1);
+    }
+    mbar_init(bar(B_MMA_DONE), 1);
+    for (int i = 0; i < C::SCALE_TILES; ++i) mbar_init(bar(B_SCALE + i), C::PIECES);
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(kv_full0 + 8u * i, C::PIECES);
+      mbar_init(kv_empty0 + 8u * i, 1);
+    }
+    *abort_flag = 0u;
+    *poison = 0u;
+    float lv = 0.f;  // any reference of the scales' size will do
+    if (n_max > 0) {
+      const int page = p.c.block_table[(long long)b * p.c.table_width];
+      if (page >= 0 && page < p.c.num_blocks) lv = lg2(p.c.v_scale[(long long)page * p.c.H + h]);
+    }
+    *base_lv = lv;
+    fence_mbar_init();
+  }
+  if (warp == C::W_MMA) {
+    tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp >= C::W_FILL) {
+    regs_dec<C::REG_CTRL>();
+    // ---------------------------------------------------------------- slot filling
+    const int bs = p.c.block_size;
+    const int me = warp - C::W_FILL;
+    const int n_pieces = 2 * n_max * C::PIECES;  // of both K and V, in the order of the loads
+    const float base = *base_lv;
+    // lane i of a set holds the block and scales of this warp's piece k0 + i
+    struct Info {
+      int slice, row;  // page * H + h (-1: nothing visible there), first row in the block
+      float ks, lv;
+    };
+    auto fetch = [&](int k0) {
+      Info r{-1, 0, 0.f, 0.f};
+      const int piece = me + C::N_FILL * (k0 + lane);
+      const int key = (piece / (2 * C::PIECES)) * C::BN + (piece % C::PIECES) * 16;
+      if (piece >= n_pieces || key >= lim_hi) return r;
+      const int page = p.c.block_table[(long long)b * p.c.table_width + key / bs];
+      if (page < 0 || page >= p.c.num_blocks) {
+        if (p.c.err) atomicCAS(p.c.err, 0u, (unsigned)ERR_SITE_CACHE_FWD + 1);
+        return r;
+      }
+      r.slice = page * p.c.H + h;
+      r.row = key % bs;
+      r.ks = p.c.k_scale[r.slice];
+      r.lv = lg2(p.c.v_scale[r.slice]);
+      return r;
+    };
+    constexpr int LD = D / 32;  // 16-byte loads per lane and piece
+    constexpr int AHEAD = 3;    // pieces in flight
+    // a load instruction covers whole rows; eight lanes of a store phase hold the
+    // same four 16-byte columns of two neighbouring rows, which the swizzle puts
+    // into different banks
+    const int row4 = D == 128 ? (lane >> 4) * 2 + ((lane >> 2) & 1) : lane >> 2;
+    const int col16 = D == 128 ? ((lane >> 3) & 1) * 4 + (lane & 3) : lane & 3;
+    constexpr int ROWS_LD = D == 128 ? 4 : 8;  // rows per load instruction
+    Info now = fetch(0), next = fetch(32);
+    uint4 buf[AHEAD][LD];
+    auto load = [&](int k, uint4 (&v)[LD], const Info& set) {
+      const int slice = __shfl_sync(0xffffffffu, set.slice, k & 31);
+      const int row = __shfl_sync(0xffffffffu, set.row, k & 31);
+      const int piece = me + C::N_FILL * k;
+      const uint8_t* src = ((piece / C::PIECES) & 1 ? p.c.v : p.c.k) +
+                           ((long long)max(slice, 0) * bs + row) * D;
+#pragma unroll
+      for (int i = 0; i < LD; ++i)
+        v[i] = slice < 0 ? make_uint4(0u, 0u, 0u, 0u)
+                         : __ldg(reinterpret_cast<const uint4*>(
+                               src + (i * ROWS_LD + row4) * D + col16 * 16));
+    };
+    const int mine = (n_pieces - me + C::N_FILL - 1) / C::N_FILL;  // pieces of this warp
+#pragma unroll
+    for (int a = 0; a < AHEAD; ++a)
+      if (a < mine) load(a, buf[a], now);
+    bool ok = true;
+    for (int k = 0; k < mine && ok; k += AHEAD) {
+#pragma unroll
+      for (int a = 0; a < AHEAD; ++a) {
+        const int kk = k + a;
+        if (kk >= mine || !ok) break;
+        if (kk > 0 && (kk & 31) == 0) {
+          now = next;
+          next = fetch(kk + 32);
+        }
+        const int piece = me + C::N_FILL * kk;
+        const int i = piece / C::PIECES, sub = piece % C::PIECES;  // load (K_j, V_j, ...), part
+        const int kv_slot = i % ST, use = i / ST;
+        const int key0 = (i >> 1) * C::BN + sub * 16;
+        ok = use == 0 ||
+             __all_sync(0xffffffffu, mbar_wait(kv_empty0 + 8u * kv_slot, (use - 1) & 1, wctx,
+                                               ERR_SITE_CACHE_FWD + 4));
+        if (!ok) break;
+        const bool value = (i & 1) != 0;
+        if (!value) {
+          const int slice = __shfl_sync(0xffffffffu, now.slice, kk & 31);
+          const float ks = __shfl_sync(0xffffffffu, now.ks, kk & 31);
+          const float lv = __shfl_sync(0xffffffffu, now.lv, kk & 31);
+          if (lane == 0) {
+            const int ring = (i >> 1) % C::SCALE_TILES;
+            scales[ring * C::PIECES + sub] =
+                slice < 0 ? make_float4(0.f, -INFINITY, 0.f, 0.f)
+                          : make_float4(ks * p.scale_log2, lv, ex2(base - lv), 0.f);
+            mbar_arrive(bar(B_SCALE + ring));
+          }
+        }
+        const bool edge = value && key0 + 16 > lim_lo;  // some row does not see all of it
+        if (edge) {
+          bool nan = false;
+#pragma unroll
+          for (int x = 0; x < LD; ++x) {
+            const int key = key0 + x * ROWS_LD + row4;
+            uint32_t* w = &buf[a][x].x;
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              if (key >= lim_hi) w[y] = 0u;  // stale rows, whatever they hold
+              if (word_has_nan<E5M2>(w[y])) {
+                nan = true;
+                w[y] = without_nan<E5M2>(w[y]);
+              }
+            }
+          }
+          if (nan) *poison = 1u;
+        }
+        const uint32_t dst = sbase + C::OFF_KV + kv_slot * C::TILE;
+#pragma unroll
+        for (int x = 0; x < LD; ++x) {
+          const int row = sub * 16 + x * ROWS_LD + row4;
+          const uint32_t* w = &buf[a][x].x;
+          const uint32_t line = dst + (col16 >> 2) * C::HALF + row * 128;
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const uint32_t c = (uint32_t)((col16 & 3) * 2 + y);
+            st_shared_v4(line + ((c ^ (row & 7)) << 4),
+                         codes_to_f16x2<E5M2>((uint16_t)(w[2 * y] & 0xffffu)),
+                         codes_to_f16x2<E5M2>((uint16_t)(w[2 * y] >> 16)),
+                         codes_to_f16x2<E5M2>((uint16_t)(w[2 * y + 1] & 0xffffu)),
+                         codes_to_f16x2<E5M2>((uint16_t)(w[2 * y + 1] >> 16)));
+          }
+        }
+        fence_proxy_async_smem();  // the MMAs read through the async proxy
+        __syncwarp();
+        if (lane == 0) mbar_arrive(kv_full0 + 8u * kv_slot);
+        // the next piece for this buffer: of this set of 32, or of the next
+        const int ahead = kk + AHEAD;
+        if (ahead < mine) load(ahead, buf[a], (ahead >> 5) == (kk >> 5) ? now : next);
+      }
+    }
+    __syncwarp();
+  } else if (warp == C::W_MMA) {
+    regs_dec<C::REG_CTRL>();
+    // ---------------------------------------------------------------- MMA issuer (whole warp)
+    auto kv_wait = [&](int i) {
+      return __all_sync(0xffffffffu, mbar_wait(kv_full0 + 8u * (i % ST), (i / ST) & 1, wctx,
+                                               ERR_SITE_CACHE_FWD + 5));
+    };
+    auto issue_s = [&](int s, int j) {  // S_s = Q_s K_j^T
+      const uint32_t a = sbase + C::OFF_Q + s * C::TILE;
+      const uint32_t bk = sbase + C::OFF_KV + ((2 * j) % ST) * C::TILE;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = (kk >> 2) * C::HALF + (kk & 3) * 32;
+        mma_bf16_ss_w(tmem + C::TM_S + s * 128, sdesc_sw128(a + off, 16, 1024),
+                      sdesc_sw128(bk + off, 16, 1024), C::IDESC_S, kk > 0);
+      }
+      mma_commit_w(bar(B_S_FULL + s));
+    };
+    auto issue_pv = [&](int s, int j, int half) {  // O_s += P_s V_j over 64 keys
+      const uint32_t bv = sbase + C::OFF_KV + ((2 * j + 1) % ST) * C::TILE;
+#pragma unroll
+      for (int k = 0; k < C::BN / 32; ++k) {
+        const int kk = half * (C::BN / 32) + k;
+        mma_bf16_ts_w(tmem + C::TM_O + s * D, tmem + C::TM_S + s * 128 + kk * 8,
+                      sdesc_sw128(bv + kk * 16 * 128, C::HALF, 1024), C::IDESC_PV,
+                      (j > 0 || kk > 0));
+      }
+      if (half == 1) mma_commit_w(bar(B_PV_DONE + s));
+    };
+    bool ok = __all_sync(0xffffffffu, mbar_wait(bar(B_Q), 0, wctx, ERR_SITE_CACHE_FWD + 6));
+    if (ok && n_max > 0) {
+      ok = kv_wait(0);
+      if (ok) {
+        tc_fence_after();
+        if (nt0 > 0) issue_s(0, 0);
+        if (nt1 > 0) issue_s(1, 0);
+        mma_commit_w(kv_empty0);
+      }
+    }
+    for (int j = 0; ok && j < n_max; ++j) {
+      const bool next = j + 1 < n_max;
+      bool k_next = false;
+      ok = kv_wait(2 * j + 1);
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const int nts = s ? nt1 : nt0;
+        if (ok && j < nts) {
+          ok = __all_sync(0xffffffffu, mbar_wait(bar(B_P_HALF + s), j & 1, wctx,
+                                                 ERR_SITE_CACHE_FWD + 7));
+          if (ok) {
+            tc_fence_after();
+            issue_pv(s, j, 0);
+            ok = __all_sync(0xffffffffu, mbar_wait(bar(B_P_FULL + s), j & 1, wctx,
+                                                   ERR_SITE_CACHE_FWD + 8));
+          }
+          if (ok) {
+            tc_fence_after();
+            issue_pv(s, j, 1);
+          }
+        }
+        if (ok && j + 1 < nts) {  // after the PV above: S_s is overwritten in pipe order
+          if (!k_next) {
+            ok = kv_wait(2 * (j + 1));
+            k_next = true;
+          }
+          if (ok) issue_s(s, j + 1);
+        }
+      }
+      if (!ok) break;
+      if (next) mma_commit_w(kv_empty0 + 8u * ((2 * (j + 1)) % ST));
+      mma_commit_w(kv_empty0 + 8u * ((2 * j + 1) % ST));
+    }
+    // drain: every MMA issued has finished before TMEM is freed
+    mma_commit_w(bar(B_MMA_DONE));
+    mbar_drain(bar(B_MMA_DONE), 0, wctx, ERR_SITE_CACHE_FWD + 9);
+    __syncwarp();
+  } else {
+    // ---------------------------------------------------------------- softmax (warps 0-7)
+    regs_inc<C::REG_SOFTMAX>();
+    const int s = warp >> 2;
+    const int t = threadIdx.x & 127;  // row in the subtile == TMEM lane
+    const int row = (s ? r0_1 : r0_0) + t;
+    const bool valid = row < n_rows;
+    const int lim = valid ? limit_of(row) : 0;
+    const int my_nt = s ? nt1 : nt0;
+    const int my_lo = limit_of(s ? r0_1 : r0_0);  // keys that every row of the subtile sees
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lane_off + C::TM_S + s * 128;
+    const uint32_t tO = tmem + lane_off + C::TM_O + s * D;
+    const uint32_t tP = tS;
+    // Q: this thread's row, times the power of two that brings its largest element
+    // to [2^14, 2^15), as fp16 (exact down to 2^-29 of that element, the quantum
+    // below it 2^-39)
+    float back = 1.f;
+    {
+      uint4 v[D / 8];
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) v[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (valid) {
+        const uint16_t* q = p.q.p + (long long)(seq.row0 + row / G) * p.q.st +
+                            (long long)(h * G + row % G) * p.q.sh;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) v[i] = *reinterpret_cast<const uint4*>(q + 8 * i);
+      }
+      uint32_t mx = 0u;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i)
+        mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(v[i].x & 0x7fff7fffu, v[i].y & 0x7fff7fffu),
+                                   __vmaxu2(v[i].z & 0x7fff7fffu, v[i].w & 0x7fff7fffu)));
+      mx = max(mx & 0xffffu, mx >> 16);
+      int e = (int)(mx >> 7);
+      e = (mx == 0u || e == 255) ? 0 : min(14 - (e - 127), 126);
+      const float mul = __uint_as_float((uint32_t)(e + 127) << 23);
+      back = __uint_as_float((uint32_t)(127 - e) << 23);
+      const uint32_t dst = sbase + C::OFF_Q + s * C::TILE + t * 128;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        const uint32_t* w = &v[i].x;
+        uint32_t o[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          asm("cvt.rn.f16x2.f32 %0, %1, %2;"
+              : "=r"(o[k])
+              : "f"(__uint_as_float(w[k] & 0xffff0000u) * mul),
+                "f"(__uint_as_float(w[k] << 16) * mul));
+        st_shared_v4(dst + (i >> 3) * C::HALF + (((i & 7) ^ (t & 7)) << 4), o[0], o[1], o[2], o[3]);
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(bar(B_Q));
+    }
+
+    float r_run = -INFINITY, l_run = 0.f;  // the reference r, and l
+    for (int j = 0; j < my_nt; ++j) {
+      mbar_wait(bar(B_S_FULL + s), j & 1, wctx, ERR_SITE_CACHE_FWD + 10);
+      mbar_wait(bar(B_SCALE + j % C::SCALE_TILES), (j / C::SCALE_TILES) & 1, wctx,
+                ERR_SITE_CACHE_FWD + 11);
+      tc_fence_after();
+      uint32_t u[4][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, u[c]);
+      tmem_wait_ld();
+#pragma unroll
+      for (int c = 0; c < 4; ++c) reg_fence32(u[c]);
+      const float4* sc = scales + (j % C::SCALE_TILES) * C::PIECES;
+      float sv[128];
+#pragma unroll
+      for (int g = 0; g < C::PIECES; ++g) {
+        const float4 x = sc[g];
+        const float ks = x.x * back;
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+          const int k = g * 16 + i;
+          fma_x2(__uint_as_float(u[k >> 5][k & 31]), __uint_as_float(u[k >> 5][(k & 31) + 1]), ks,
+                 x.y, sv[k], sv[k + 1]);
+        }
+      }
+      const int c0 = j * C::BN;
+      if (c0 + C::BN > my_lo) {
+        const int n = lim - c0;
+#pragma unroll
+        for (int k = 0; k < 128; ++k)
+          if (k >= n) sv[k] = -INFINITY;
+      }
+      float mx[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) mx[i] = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < 128; k += 16)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mx[i] = fmax3(mx[i], sv[k + 2 * i], sv[k + 2 * i + 1]);
+      const float m_blk = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]),
+                                fmaxf(mx[6], mx[7]));
+      // (-inf) - (-inf) is NaN, which moves nothing
+      const bool rescale = m_blk - r_run > kRoom;
+      const float r_new = rescale ? (fabsf(m_blk) < kFar ? m_blk - kOff : m_blk) : r_run;
+      const float shift = r_new == -INFINITY ? 0.f : -r_new;
+      const float alpha = rescale ? ex2(r_run + shift) : 1.f;
+      float lw = 0.f;
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        uint32_t pk[32];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
+#pragma unroll
+          for (int i = 0; i < 16; i += 4) {
+            const int k = g * 16 + i, kk = hh * 64 + k;
+            float p0, p1, p2, p3;
+            add_x2(sv[kk], sv[kk + 1], shift, shift, p0, p1);
+            add_x2(sv[kk + 2], sv[kk + 3], shift, shift, p2, p3);
+            p0 = ex2(p0);
+            p1 = ex2(p1);
+            p2 = ex2(p2);
+            p3 = ex2(p3);
+            add_x2(l0, l1, p0, p1, l0, l1);
+            add_x2(l2, l3, p2, p3, l2, l3);
+            asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(pk[k / 2]) : "f"(p1), "f"(p0));
+            asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(pk[k / 2 + 1]) : "f"(p3), "f"(p2));
+          }
+          lw = fmaf((l0 + l1) + (l2 + l3), sc[hh * 4 + g].z, lw);
+        }
+        tmem_st32(tP + hh * 32, pk);
+        if (hh == 0) {
+          if (j > 0 && __any_sync(0xffffffffu, rescale)) {
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32(tO + c * 32, o);
+              tmem_wait_ld(o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+              tmem_st32(tO + c * 32, o);
+            }
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(bar(B_P_HALF + s));
+        }
+      }
+      l_run = l_run * alpha + lw;
+      r_run = r_new;
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(bar(B_P_FULL + s));
+    }
+
+    // ------------------------------------------------------------ epilogue
+    uint16_t* o_row = p.o.p + (long long)(seq.row0 + row / G) * p.o.st +
+                      (long long)(h * G + row % G) * p.o.sh;
+    const bool has = my_nt > 0 && !(l_run == 0.f);
+    const float base = *base_lv;
+    const float inv = has ? 1.f / l_run : 0.f, up = ex2(base);
+    if (my_nt > 0) {
+      mbar_wait(bar(B_PV_DONE + s), (my_nt - 1) & 1, wctx, ERR_SITE_CACHE_FWD + 12);
+      tc_fence_after();
+    }
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) {
+      uint32_t o[32];
+      if (my_nt > 0) {  // subtile-uniform
+        tmem_ld32(tO + c * 32, o);
+        tmem_wait_ld(o);
+      }
+      if (valid) {
+#pragma unroll
+        for (int q4 = 0; q4 < 4; ++q4) {
+          uint4 w;
+          uint32_t* x = &w.x;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float a = has ? __uint_as_float(o[q4 * 8 + 2 * e]) * inv * up : 0.f;
+            const float z = has ? __uint_as_float(o[q4 * 8 + 2 * e + 1]) * inv * up : 0.f;
+            x[e] = pack_bf16x2(a, z);
+          }
+          *reinterpret_cast<uint4*>(o_row + c * 32 + q4 * 8) = w;
+        }
+      }
+    }
+    if (valid)
+      p.lse[(long long)(h * G + row % G) * p.c.total + seq.row0 + row / G] =
+          has ? (r_run - base + lg2(l_run)) * kLn2 : -INFINITY;
+    __syncwarp();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == C::W_MMA) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+  if (*poison && warp < 8) {
+    // rare: values that were NaN in keys that some rows see and others do not; they
+    // were left out of the sums, and here reach the rows that do see them
+    const int row = r0_0 + (int)threadIdx.x;
+    if (row < n_rows) {
+      const int lim = limit_of(row), bs = p.c.block_size;
+      uint16_t* o_row = p.o.p + (long long)(seq.row0 + row / G) * p.o.st +
+                        (long long)(h * G + row % G) * p.o.sh;
+      for (int key = lim_lo & ~15; key < lim; ++key) {
+        const int page = p.c.block_table[(long long)b * p.c.table_width + key / bs];
+        if (page < 0 || page >= p.c.num_blocks) continue;
+        const uint8_t* v = p.c.v + (((long long)page * p.c.H + h) * bs + key % bs) * D;
+        for (int c = 0; c < D; ++c)
+          if ((v[c] & 0x7fu) >= (E5M2 ? 0x7cu : 0x7fu)) o_row[c] = 0x7fffu;
+      }
+    }
+  }
+}
+
+template <int D, bool E5M2>
+cudaError_t launch(const CacheFwdParams& p, cudaStream_t stream) {
+  using C = Wide<D>;
+  static unsigned long long prepared[64];
+  const cudaError_t e = prepare_once(prepared, [] {
+    cudaError_t r = cudaFuncSetAttribute(cache_fwd_wide_kernel<D, E5M2>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (r != cudaSuccess) return r;
+    // the setmaxnreg split hands out at most the launch's registers
+    cudaFuncAttributes fa;
+    r = cudaFuncGetAttributes(&fa, cache_fwd_wide_kernel<D, E5M2>);
+    if (r != cudaSuccess) return r;
+    return fa.numRegs >= C::REG_LAUNCH ? cudaSuccess : cudaErrorInvalidConfiguration;
+  });
+  if (e != cudaSuccess) return e;
+  const int G = p.Hq / p.c.H;
+  const long long units = ((long long)p.c.total * G / C::ROWS + p.c.B) * p.c.H;
+  if (units > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  cache_fwd_wide_kernel<D, E5M2><<<(unsigned)units, C::THREADS, C::SMEM, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_cache_fwd_wide(const CacheFwdParams& p, cudaStream_t stream) {
+  if (p.c.d == 128) return p.c.format ? launch<128, true>(p, stream) : launch<128, false>(p, stream);
+  return p.c.format ? launch<64, true>(p, stream) : launch<64, false>(p, stream);
+}
+
+}  // namespace fattn

@@ -137,6 +137,8 @@ struct CacheFwdParams {
   int Hq;
   int causal;
   float scale_log2;  // scale * log2(e)
+  int narrow_rows;   // sequences with more query rows per key/value head (tokens x grouped heads)
+                     // than this go to the 256-row tcgen05 kernel, the others to the split one
   void* workspace;
 };
 
@@ -210,6 +212,7 @@ size_t cache_fwd_workspace(const CacheParams& c, int Hq, int n_sm);
 // tk, tv: maps of the codes, {d, block_size, num_blocks * H}, boxes of 16 tokens
 cudaError_t launch_cache_fwd(const CUtensorMap& tk, const CUtensorMap& tv, const CacheFwdParams& p,
                              int n_sm, cudaStream_t stream);
+cudaError_t launch_cache_fwd_wide(const CacheFwdParams& p, cudaStream_t stream);
 
 cudaError_t launch_bwd_preprocess(const void* o, const void* dout, float* delta, float* dq_acc,
                                   long long rows, int d, int n_sm, cudaStream_t stream);
