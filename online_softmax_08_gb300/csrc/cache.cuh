@@ -16,6 +16,19 @@ __device__ __forceinline__ uint32_t codes_to_f16x2(uint16_t c) {
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(c));
   return r;
 }
+// Four codes (low byte first) -> two pairs of fp16 values.
+template <bool E5M2>
+__device__ __forceinline__ void codes4_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if constexpr (E5M2)  // the upper byte of the fp16 value
+    lo = __byte_perm(w, 0u, 0x1404u), hi = __byte_perm(w, 0u, 0x3424u);
+  else
+    asm("{\n\t.reg .b16 a, b;\n\t"
+        "mov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+}
 __device__ __forceinline__ float2 f16x2_to_f32(uint32_t h) {
   float2 f;
   asm("{\n\t.reg .b16 lo, hi;\n\t"

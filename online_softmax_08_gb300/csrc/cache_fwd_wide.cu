@@ -9,11 +9,11 @@
 // it into P_s in place, and O_s += P_s V accumulates in TMEM.
 //
 // What differs is how a slot is filled.  The codes cannot feed the tensor core as
-// they are (q and P need more than 8 bits), so three warps load them from their
+// they are (q and P need more than 8 bits), so four warps load them from their
 // blocks, convert them to fp16 (exact) and store them into the slot in the
-// 128-byte-swizzled layout that a TMA load would leave.  A tile pair of 128 keys
-// is 16 pieces of 16 tokens (a piece lies in one block); the warps take pieces in
-// turn and keep three of them in flight.
+// 128-byte-swizzled layout that a TMA load would leave.  Each warp owns 32 rows of
+// every tile, two pieces of 16 tokens (a piece lies in one block), and has the next
+// tile's codes in flight.
 //
 // The scales are applied by the softmax, per piece, as in the kernel for few rows:
 // y = s * ks + log2 vs, p = 2^(y - r) (fp16), l += w p with w = 2^(b - log2 vs),
@@ -22,7 +22,7 @@
 // maximum itself, as 8 is then too near its rounding.
 //
 // Warps: 0-3 softmax of subtile 0, 4-7 of subtile 1 (thread t owns row t; they also
-// load Q and write O), 8 issues the MMAs, 9-11 fill the slots.  TMEM: S_0, S_1, O_0,
+// load Q and write O), 8-11 fill the slots, 12 issues the MMAs, 13-15 idle.  TMEM: S_0, S_1, O_0,
 // O_1.  Measured limits: see the launcher.
 #define FATTN_INLINE_WAIT_SLOW_PATH
 #include <math.h>
@@ -86,10 +86,11 @@ struct Wide {
   static constexpr int OFF_SCALE = OFF_KV + STAGES * TILE;  // [SCALE_TILES][PIECES] float4
   static constexpr int OFF_BAR = OFF_SCALE + SCALE_TILES * PIECES * 16;
   static constexpr int SMEM = OFF_BAR + 256 + 1024;
-  static constexpr int THREADS = 384;
-  static constexpr int W_MMA = 8, W_FILL = 9, N_FILL = 3;
-  static constexpr int REG_LAUNCH = 168, REG_SOFTMAX = 208, REG_CTRL = 88;
-  static_assert((2 * REG_SOFTMAX + REG_CTRL) * 128 <= THREADS * REG_LAUNCH, "register split");
+  static constexpr int THREADS = 512;
+  static constexpr int W_FILL = 8, N_FILL = 4, W_MMA = 12;
+  static constexpr int REG_LAUNCH = 128, REG_SOFTMAX = 192, REG_FILL = 88, REG_CTRL = 40;
+  static_assert((2 * REG_SOFTMAX + REG_FILL + REG_CTRL) * 128 <= THREADS * REG_LAUNCH,
+                "register split");
   static_assert(SMEM <= 232448, "shared memory budget");
   static constexpr uint32_t TM_S = 0, TM_O = 256;
   static constexpr uint32_t TMEM_COLS = 512;
@@ -191,7 +192,7 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
     mbar_init(bar(B_MMA_DONE), 1);
     for (int i = 0; i < C::SCALE_TILES; ++i) mbar_init(bar(B_SCALE + i), C::PIECES);
     for (int i = 0; i < ST; ++i) {
-      mbar_init(kv_full0 + 8u * i, C::PIECES);
+      mbar_init(kv_full0 + 8u * i, C::N_FILL);
       mbar_init(kv_empty0 + 8u * i, 1);
     }
     *abort_flag = 0u;
@@ -213,23 +214,24 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp >= C::W_FILL) {
-    regs_dec<C::REG_CTRL>();
+  if (warp > C::W_MMA) {
+    regs_dec<C::REG_CTRL>();  // idle
+  } else if (warp >= C::W_FILL && warp < C::W_FILL + C::N_FILL) {
+    regs_dec<C::REG_FILL>();
     // ---------------------------------------------------------------- slot filling
+    // Warp w fills rows [32 w, 32 w + 32) of every slot: two pieces of 16 tokens.
     const int bs = p.c.block_size;
     const int me = warp - C::W_FILL;
-    const int n_pieces = 2 * n_max * C::PIECES;  // of both K and V, in the order of the loads
     const float base = *base_lv;
-    // lane i of a set holds the block and scales of this warp's piece k0 + i
+    // lane i of a set holds the block and scales of this warp's piece i & 1 of tile i / 2
     struct Info {
       int slice, row;  // page * H + h (-1: nothing visible there), first row in the block
       float ks, lv;
     };
-    auto fetch = [&](int k0) {
+    auto fetch = [&](int j0) {
       Info r{-1, 0, 0.f, 0.f};
-      const int piece = me + C::N_FILL * (k0 + lane);
-      const int key = (piece / (2 * C::PIECES)) * C::BN + (piece % C::PIECES) * 16;
-      if (piece >= n_pieces || key >= lim_hi) return r;
+      const int key = (j0 + (lane >> 1)) * C::BN + me * 32 + (lane & 1) * 16;
+      if (key >= lim_hi) return r;
       const int page = p.c.block_table[(long long)b * p.c.table_width + key / bs];
       if (page < 0 || page >= p.c.num_blocks) {
         if (p.c.err) atomicCAS(p.c.err, 0u, (unsigned)ERR_SITE_CACHE_FWD + 1);
@@ -242,102 +244,110 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
       return r;
     };
     constexpr int LD = D / 32;  // 16-byte loads per lane and piece
-    constexpr int AHEAD = 3;    // pieces in flight
     // a load instruction covers whole rows; eight lanes of a store phase hold the
     // same four 16-byte columns of two neighbouring rows, which the swizzle puts
     // into different banks
     const int row4 = D == 128 ? (lane >> 4) * 2 + ((lane >> 2) & 1) : lane >> 2;
     const int col16 = D == 128 ? ((lane >> 3) & 1) * 4 + (lane & 3) : lane & 3;
     constexpr int ROWS_LD = D == 128 ? 4 : 8;  // rows per load instruction
-    Info now = fetch(0), next = fetch(32);
-    uint4 buf[AHEAD][LD];
-    auto load = [&](int k, uint4 (&v)[LD], const Info& set) {
-      const int slice = __shfl_sync(0xffffffffu, set.slice, k & 31);
-      const int row = __shfl_sync(0xffffffffu, set.row, k & 31);
-      const int piece = me + C::N_FILL * k;
-      const uint8_t* src = ((piece / C::PIECES) & 1 ? p.c.v : p.c.k) +
-                           ((long long)max(slice, 0) * bs + row) * D;
+    const int lane_src = row4 * D + col16 * 16;
+    // a lane's 16 codes become 32 bytes: two neighbouring 16-byte columns of its row
+    const uint32_t lane_dst = (uint32_t)((col16 >> 2) * C::HALF + (me * 32 + row4) * 128);
+    uint4 buf[2][2][LD];  // [K, V][piece]
+    auto load = [&](int j, int value, const Info& set) {
 #pragma unroll
-      for (int i = 0; i < LD; ++i)
-        v[i] = slice < 0 ? make_uint4(0u, 0u, 0u, 0u)
-                         : __ldg(reinterpret_cast<const uint4*>(
-                               src + (i * ROWS_LD + row4) * D + col16 * 16));
+      for (int pc = 0; pc < 2; ++pc) {
+        const int from = (j & 15) * 2 + pc;
+        const int slice = __shfl_sync(0xffffffffu, set.slice, from);
+        const int row = __shfl_sync(0xffffffffu, set.row, from);
+        const uint8_t* src = (value ? p.c.v : p.c.k) + ((long long)slice * bs + row) * D + lane_src;
+#pragma unroll
+        for (int i = 0; i < LD; ++i)
+          buf[value][pc][i] = slice < 0 ? make_uint4(0u, 0u, 0u, 0u)
+                                        : __ldg(reinterpret_cast<const uint4*>(src + i * ROWS_LD * D));
+      }
     };
-    const int mine = (n_pieces - me + C::N_FILL - 1) / C::N_FILL;  // pieces of this warp
-#pragma unroll
-    for (int a = 0; a < AHEAD; ++a)
-      if (a < mine) load(a, buf[a], now);
+    Info now{-1, 0, 0.f, 0.f}, next{-1, 0, 0.f, 0.f};
+    if (n_max > 0) {
+      now = fetch(0);
+      next = fetch(16);
+      load(0, 0, now);
+      load(0, 1, now);
+    }
     bool ok = true;
-    for (int k = 0; k < mine && ok; k += AHEAD) {
-#pragma unroll
-      for (int a = 0; a < AHEAD; ++a) {
-        const int kk = k + a;
-        if (kk >= mine || !ok) break;
-        if (kk > 0 && (kk & 31) == 0) {
-          now = next;
-          next = fetch(kk + 32);
-        }
-        const int piece = me + C::N_FILL * kk;
-        const int i = piece / C::PIECES, sub = piece % C::PIECES;  // load (K_j, V_j, ...), part
-        const int kv_slot = i % ST, use = i / ST;
-        const int key0 = (i >> 1) * C::BN + sub * 16;
+    for (int j = 0; ok && j < n_max; ++j) {
+      {  // the tile's scales
+        const float ks = __shfl_sync(0xffffffffu, now.ks, (j & 15) * 2 + (lane & 1));
+        const float lv = __shfl_sync(0xffffffffu, now.lv, (j & 15) * 2 + (lane & 1));
+        const int slice = __shfl_sync(0xffffffffu, now.slice, (j & 15) * 2 + (lane & 1));
+        // the slot of K_j is free: with it, the scales' (see SCALE_TILES)
+        const int i = 2 * j, use = i / ST;
         ok = use == 0 ||
-             __all_sync(0xffffffffu, mbar_wait(kv_empty0 + 8u * kv_slot, (use - 1) & 1, wctx,
+             __all_sync(0xffffffffu, mbar_wait(kv_empty0 + 8u * (i % ST), (use - 1) & 1, wctx,
                                                ERR_SITE_CACHE_FWD + 4));
         if (!ok) break;
-        const bool value = (i & 1) != 0;
-        if (!value) {
-          const int slice = __shfl_sync(0xffffffffu, now.slice, kk & 31);
-          const float ks = __shfl_sync(0xffffffffu, now.ks, kk & 31);
-          const float lv = __shfl_sync(0xffffffffu, now.lv, kk & 31);
-          if (lane == 0) {
-            const int ring = (i >> 1) % C::SCALE_TILES;
-            scales[ring * C::PIECES + sub] =
-                slice < 0 ? make_float4(0.f, -INFINITY, 0.f, 0.f)
-                          : make_float4(ks * p.scale_log2, lv, ex2(base - lv), 0.f);
-            mbar_arrive(bar(B_SCALE + ring));
+        const int ring = j % C::SCALE_TILES;
+        if (lane < 2) {
+          scales[ring * C::PIECES + me * 2 + lane] =
+              slice < 0 ? make_float4(0.f, -INFINITY, 0.f, 0.f)
+                        : make_float4(ks * p.scale_log2, lv, ex2(base - lv), 0.f);
+          mbar_arrive(bar(B_SCALE + ring));
+        }
+      }
+      if ((j & 15) == 15) {  // the loads below are for the next set's first tile
+        now = next;
+        next = fetch(j + 17);
+      }
+#pragma unroll
+      for (int value = 0; value < 2; ++value) {
+        const int i = 2 * j + value, use = i / ST;
+        const int kv_slot = i % ST;
+        if (value) {
+          ok = use == 0 ||
+               __all_sync(0xffffffffu, mbar_wait(kv_empty0 + 8u * kv_slot, (use - 1) & 1, wctx,
+                                                 ERR_SITE_CACHE_FWD + 4));
+          if (!ok) break;
+          const int key0 = j * C::BN + me * 32 + row4;
+          if (j * C::BN + me * 32 + 32 > lim_lo) {  // some row does not see all of it
+            bool nan = false;
+#pragma unroll
+            for (int pc = 0; pc < 2; ++pc)
+#pragma unroll
+              for (int x = 0; x < LD; ++x) {
+                uint32_t* w = &buf[1][pc][x].x;
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                  if (key0 + pc * 16 + x * ROWS_LD >= lim_hi) w[y] = 0u;  // stale, whatever it is
+                  if (word_has_nan<E5M2>(w[y])) {
+                    nan = true;
+                    w[y] = without_nan<E5M2>(w[y]);
+                  }
+                }
+              }
+            if (nan) *poison = 1u;
           }
         }
-        const bool edge = value && key0 + 16 > lim_lo;  // some row does not see all of it
-        if (edge) {
-          bool nan = false;
+        const uint32_t dst = sbase + C::OFF_KV + kv_slot * C::TILE + lane_dst;
+#pragma unroll
+        for (int pc = 0; pc < 2; ++pc)
 #pragma unroll
           for (int x = 0; x < LD; ++x) {
-            const int key = key0 + x * ROWS_LD + row4;
-            uint32_t* w = &buf[a][x].x;
+            const uint32_t* w = &buf[value][pc][x].x;
+            const int row = pc * 16 + x * ROWS_LD;  // + 32 me + row4; the swizzle takes it mod 8
+            const uint32_t line = dst + row * 128;
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              if (key >= lim_hi) w[y] = 0u;  // stale rows, whatever they hold
-              if (word_has_nan<E5M2>(w[y])) {
-                nan = true;
-                w[y] = without_nan<E5M2>(w[y]);
-              }
+            for (int y = 0; y < 2; ++y) {
+              const uint32_t c = (uint32_t)(((col16 & 3) * 2 + y) ^ ((row + row4) & 7));
+              uint32_t o[4];
+              codes4_to_f16<E5M2>(w[2 * y], o[0], o[1]);
+              codes4_to_f16<E5M2>(w[2 * y + 1], o[2], o[3]);
+              st_shared_v4(line + (c << 4), o[0], o[1], o[2], o[3]);
             }
           }
-          if (nan) *poison = 1u;
-        }
-        const uint32_t dst = sbase + C::OFF_KV + kv_slot * C::TILE;
-#pragma unroll
-        for (int x = 0; x < LD; ++x) {
-          const int row = sub * 16 + x * ROWS_LD + row4;
-          const uint32_t* w = &buf[a][x].x;
-          const uint32_t line = dst + (col16 >> 2) * C::HALF + row * 128;
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const uint32_t c = (uint32_t)((col16 & 3) * 2 + y);
-            st_shared_v4(line + ((c ^ (row & 7)) << 4),
-                         codes_to_f16x2<E5M2>((uint16_t)(w[2 * y] & 0xffffu)),
-                         codes_to_f16x2<E5M2>((uint16_t)(w[2 * y] >> 16)),
-                         codes_to_f16x2<E5M2>((uint16_t)(w[2 * y + 1] & 0xffffu)),
-                         codes_to_f16x2<E5M2>((uint16_t)(w[2 * y + 1] >> 16)));
-          }
-        }
         fence_proxy_async_smem();  // the MMAs read through the async proxy
         __syncwarp();
         if (lane == 0) mbar_arrive(kv_full0 + 8u * kv_slot);
-        // the next piece for this buffer: of this set of 32, or of the next
-        const int ahead = kk + AHEAD;
-        if (ahead < mine) load(ahead, buf[a], (ahead >> 5) == (kk >> 5) ? now : next);
+        if (j + 1 < n_max) load(j + 1, value, now);
       }
     }
     __syncwarp();
