@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
         const int ring = j % C::SCALE_TILES;
         if (lane < 2) {
           scales[ring * C::PIECES + me * 2 + lane] =
-              slice < 0 ? make_float4(0.f, -INFINITY, 0.f, 0.f)
+              slice < 0 ? make_float4(1.f, -INFINITY, 0.f, 0.f)
                         : make_float4(ks * p.scale_log2, lv, ex2(base - lv), 0.f);
           mbar_arrive(bar(B_SCALE + ring));
         }
@@ -497,16 +497,7 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
       const float4* sc = scales + (j % C::SCALE_TILES) * C::PIECES;
       float sv[128];
 #pragma unroll
-      for (int g = 0; g < C::PIECES; ++g) {
-        const float4 x = sc[g];
-        const float ks = x.x * back;
-#pragma unroll
-        for (int i = 0; i < 16; i += 2) {
-          const int k = g * 16 + i;
-          fma_x2(__uint_as_float(u[k >> 5][k & 31]), __uint_as_float(u[k >> 5][(k & 31) + 1]), ks,
-                 x.y, sv[k], sv[k + 1]);
-        }
-      }
+      for (int k = 0; k < 128; ++k) sv[k] = __uint_as_float(u[k >> 5][k & 31]);
       const int c0 = j * C::BN;
       if (c0 + C::BN > my_lo) {
         const int n = lim - c0;
@@ -514,20 +505,36 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
         for (int k = 0; k < 128; ++k)
           if (k >= n) sv[k] = -INFINITY;
       }
-      float mx[8];
+      // the largest y: of each piece the largest product, then its scale (positive)
+      float ks[C::PIECES], top[C::PIECES];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) mx[i] = -INFINITY;
-#pragma unroll
-      for (int k = 0; k < 128; k += 16)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) mx[i] = fmax3(mx[i], sv[k + 2 * i], sv[k + 2 * i + 1]);
-      const float m_blk = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]),
-                                fmaxf(mx[6], mx[7]));
+      for (int g = 0; g < C::PIECES; ++g) {
+        const float* x = sv + g * 16;
+        float m = fmax3(fmax3(x[0], x[1], x[2]), fmax3(x[3], x[4], x[5]), fmax3(x[6], x[7], x[8]));
+        m = fmax3(m, fmax3(x[9], x[10], x[11]), fmax3(x[12], x[13], x[14]));
+        const float2 kl = *reinterpret_cast<const float2*>(&sc[g]);
+        ks[g] = fmaxf(kl.x * back, 1.17549435e-38f);
+        top[g] = fmaf(fmaxf(m, x[15]), ks[g], kl.y);
+      }
+      const float m_blk = fmax3(fmax3(top[0], top[1], top[2]), fmax3(top[3], top[4], top[5]),
+                                fmaxf(top[6], top[7]));
       // (-inf) - (-inf) is NaN, which moves nothing
       const bool rescale = m_blk - r_run > kRoom;
       const float r_new = rescale ? (fabsf(m_blk) < kFar ? m_blk - kOff : m_blk) : r_run;
       const float shift = r_new == -INFINITY ? 0.f : -r_new;
       const float alpha = rescale ? ex2(r_run + shift) : 1.f;
+      // p = 2^(s ks + (log2 vs - r)).  Far from zero, the rounding of y that the check
+      // above saw is itself large: there p is formed from the rounded y
+      const bool far = __any_sync(0xffffffffu, fabsf(shift) >= kFar);
+      if (far) {  // warp-uniform, rare
+#pragma unroll
+        for (int g = 0; g < C::PIECES; ++g) {
+          const float lv = sc[g].y;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) sv[g * 16 + i] = fmaf(sv[g * 16 + i], ks[g], lv) + shift;
+          ks[g] = 1.f;
+        }
+      }
       float lw = 0.f;
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh) {
@@ -535,12 +542,13 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
+          const float c = far ? 0.f : sc[hh * 4 + g].y + shift;
 #pragma unroll
           for (int i = 0; i < 16; i += 4) {
             const int k = g * 16 + i, kk = hh * 64 + k;
             float p0, p1, p2, p3;
-            add_x2(sv[kk], sv[kk + 1], shift, shift, p0, p1);
-            add_x2(sv[kk + 2], sv[kk + 3], shift, shift, p2, p3);
+            fma_x2(sv[kk], sv[kk + 1], ks[hh * 4 + g], c, p0, p1);
+            fma_x2(sv[kk + 2], sv[kk + 3], ks[hh * 4 + g], c, p2, p3);
             p0 = ex2(p0);
             p1 = ex2(p1);
             p2 = ex2(p2);
