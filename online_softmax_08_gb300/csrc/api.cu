@@ -534,6 +534,7 @@ CacheParams cache_params(const fattn_cache* c, const fattn_cache_batch* b, unsig
   p.num_blocks = c->num_blocks;
   p.H = c->H;
   p.block_size = c->block_size;
+  p.block_log2 = c->block_size == 16 ? 4 : c->block_size == 32 ? 5 : c->block_size == 64 ? 6 : 7;
   p.d = c->d;
   p.format = c->format;
   p.block_table = b->block_table;
@@ -649,6 +650,8 @@ extern "C" int fattn_cache_fwd(const fattn_cache* cache, const fattn_cache_batch
   p.o = token_view(o, o_token_stride, o_head_stride, T, Hq);
   p.lse = lse;
   p.Hq = Hq;
+  p.G = Hq / cache->H;
+  p.by_G = FastDiv((unsigned)p.G);
   p.causal = causal ? 1 : 0;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.workspace = workspace;

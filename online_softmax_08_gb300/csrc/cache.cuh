@@ -50,6 +50,17 @@ __device__ __forceinline__ uint16_t f32_to_codes(float lo, float hi) {
   return r;
 }
 
+// 0x80 in the byte of each of four codes that stands for NaN (or, in e5m2, for
+// infinity): the magnitudes from the first such code on carry into the sign bit.
+template <bool E5M2>
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
+  return ((w & 0x7f7f7f7fu) + (E5M2 ? 0x04040404u : 0x01010101u)) & 0x80808080u;
+}
+// The four codes with zeros in the bytes that `m` (of nan_codes) marks.
+__device__ __forceinline__ uint32_t clear_codes(uint32_t w, uint32_t m) {
+  return w & ~(m | (m - (m >> 7)));
+}
+
 // The largest b in [0, B) with first(b) <= x, for a non-decreasing first() with
 // first(0) <= x, found by the whole warp: 32 probes a step, so one step serves
 // 32 sequences and two 1024 (a binary search would wait for 5 or 10 loads in

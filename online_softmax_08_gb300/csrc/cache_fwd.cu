@@ -44,11 +44,6 @@
 
 #include "cache.cuh"
 
-#ifndef FATTN_ST1
-#define FATTN_ST1 3
-#define FATTN_ST2 3
-#define FATTN_CTAS1 3
-#endif
 namespace fattn {
 namespace {
 
@@ -65,19 +60,15 @@ struct Dec {
   static constexpr int R = 8 * NT;                // query rows per unit
   static constexpr int TILE = kTile * D;          // bytes
   static constexpr int STAGE = 2 * TILE;          // keys and values
-  static constexpr int ST = (D == 128 ? 1 : 2) * (NT == 1 ? FATTN_ST1 : FATTN_ST2);     // ring slots per warp
+  static constexpr int ST = (D == 128 ? 1 : 2) * (NT == 1 ? 3 : 4);  // ring slots per warp
   static constexpr int OFF_RED = kWarps * ST * STAGE;
-  static constexpr int BUFS = 1;    // where the warps' results are summed
-  static constexpr int OFF_STAT = OFF_RED + BUFS * R * D * 4;
+  static constexpr int OFF_STAT = OFF_RED + kWarps * R * D * 4;  // behind the warps' results
   static constexpr int OFF_BAR = OFF_STAT + kWarps * R * 4;
   static constexpr int SMEM = OFF_BAR + kWarps * ST * 8 + 16 + 1024;
-  static constexpr int CTAS = NT == 1 ? FATTN_CTAS1 : 3;    // per SM
+  static constexpr int CTAS = NT == 1 ? 3 : 2;    // per SM
 };
 
-#ifndef FATTN_NARROW
-#define FATTN_NARROW 64
-#endif
-constexpr int kNarrowRows = FATTN_NARROW;
+constexpr int kNarrowRows = 64;
 
 // What a CTA leaves for the merge kernel: the unit that starts in its share and
 // ends in a later CTA's (parts = 0: there is none).
@@ -85,35 +76,42 @@ struct Record {
   int parts, rows, h, row0, first_row;
 };
 
-// The key/value chunks of sequence b (0: nothing to do here).
-struct SeqWork {
-  int nch, units;  // chunks per unit, units
-};
-__device__ __forceinline__ SeqWork seq_work(const CacheFwdParams& p, int R, int b, CacheSeq* s) {
-  SeqWork w{0, 0};
-  if (!cache_seq(p.c, b, s)) {
-    if (p.c.err) atomicCAS(p.c.err, 0u, (unsigned)ERR_SITE_CACHE_FWD);
-    return w;
-  }
-  const int G = p.Hq / p.c.H;
-  if (s->n == 0 || s->n * G > p.narrow_rows) return w;  // (or the wide kernel's)
-  w.nch = max(1, (s->len + kChunk - 1) / kChunk);
-  w.units = p.c.H * ((s->n * G + R - 1) / R);
-  return w;
-}
-
-// A position in the list of all chunks: chunk `pos` of sequence b.
+// A position in the list of all chunks: chunk ch of unit (sequence b, head h, row
+// block rb).  Sequence b has H x nrb units of nch chunks (none: nch = 0).
 struct Cursor {
-  int b;
-  long long pos;
+  int b, h, rb, ch;
+  int nch, nrb;
   CacheSeq seq;
-  SeqWork w;
 };
-__device__ __forceinline__ void advance(const CacheFwdParams& p, int R, Cursor* c, long long by) {
-  c->pos += by;
-  while (c->pos >= (long long)c->w.nch * c->w.units && c->b < p.c.B) {
-    c->pos -= (long long)c->w.nch * c->w.units;
-    if (++c->b < p.c.B) c->w = seq_work(p, R, c->b, &c->seq);
+__device__ __forceinline__ void load_seq(const CacheFwdParams& p, int R, int b, Cursor* c) {
+  c->b = b;
+  c->nch = c->nrb = 0;
+  if (!cache_seq(p.c, b, &c->seq)) {
+    if (p.c.err) atomicCAS(p.c.err, 0u, (unsigned)ERR_SITE_CACHE_FWD);
+    return;
+  }
+  const int rows = c->seq.n * p.G;
+  if (rows == 0 || rows > p.narrow_rows) return;  // (the other kernel's)
+  c->nch = max(1, (c->seq.len + kChunk - 1) / kChunk);
+  c->nrb = (rows + R - 1) / R;
+}
+__device__ __forceinline__ void advance(const CacheFwdParams& p, int R, Cursor* c, int by) {
+  c->ch += by;
+  while (c->ch >= c->nch) {
+    c->ch -= c->nch;
+    if (++c->rb < c->nrb) continue;
+    c->rb = 0;
+    if (++c->h < p.c.H) continue;
+    c->h = 0;
+    int b = c->b;
+    do {
+      if (++b >= p.c.B) {
+        c->b = b;
+        c->nch = 0x7fffffff;  // behind the last chunk
+        return;
+      }
+      load_seq(p, R, b, c);
+    } while (c->nch == 0);
   }
 }
 
@@ -147,12 +145,6 @@ __device__ __forceinline__ uint2 ld_shared_v2(uint32_t a) {
   asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
   return v;
 }
-// Whether a code's magnitude byte stands for NaN (or infinity).
-template <bool E5M2>
-__device__ __forceinline__ bool code_is_nan(uint32_t c) {
-  return (c & 0x7fu) >= (E5M2 ? 0x7cu : 0x7fu);
-}
-
 template <int D, bool E5M2, int NT>
 __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
     cache_fwd_kernel(const __grid_constant__ CUtensorMap tm_k,
@@ -168,7 +160,7 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
   uint8_t* smem = smem_raw + (sbase - raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  float* red = reinterpret_cast<float*>(smem + C::OFF_RED);    // [BUFS][R][D]
+  float* red = reinterpret_cast<float*>(smem + C::OFF_RED);    // [warps][R][D]
   float* stat = reinterpret_cast<float*>(smem + C::OFF_STAT);  // [warps][R]
   const uint32_t bar0 = sbase + C::OFF_BAR + 8u * (uint32_t)(warp * C::ST);
   volatile uint32_t* abort_flag =
@@ -185,26 +177,35 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
   }
 
   // ---------------------------------------------------------------- this CTA's share
-  const int B = p.c.B, G = p.Hq / p.c.H;
-  long long total = 0;
-  for (int b = lane; b < B; b += 32) {
-    CacheSeq s;
-    const SeqWork w = seq_work(p, R, b, &s);
-    total += (long long)w.nch * w.units;
+  const int B = p.c.B, G = p.G;
+  auto chunks = [&](const Cursor& c) { return (long long)c.nch * c.nrb * p.c.H; };
+  Cursor cur{};
+  long long mine = 0, total = 0;  // chunks of sequence `lane` of the last group, and of all
+  for (int b0 = 0; b0 < B; b0 += 32) {
+    mine = 0;
+    if (b0 + lane < B) {
+      load_seq(p, R, b0 + lane, &cur);
+      mine = chunks(cur);
+    }
+    total += mine;
   }
 #pragma unroll
   for (int w = 16; w > 0; w >>= 1) total += __shfl_xor_sync(0xffffffffu, total, w);
-  const long long share = (total + gridDim.x - 1) / gridDim.x;  // 0: no work at all
+  // (a 64-bit division takes ten times as long)
+  const long long share = total < 0x7fffffff ? ((unsigned)total + gridDim.x - 1) / gridDim.x
+                                             : (total + gridDim.x - 1) / gridDim.x;
   const long long lo = blockIdx.x * share;
-  const long long F64 = max(0LL, min(share, total - lo));
-  Cursor cur{B, 0, CacheSeq{0, 0, 0}, SeqWork{0, 0}};
-  if (F64 > 0) {
+  const int F = (int)max(0LL, min(share, total - lo));  // chunks of this CTA
+  if (F > 0) {
     long long before = 0;
     for (int b0 = 0; b0 < B; b0 += 32) {
-      CacheSeq s{0, 0, 0};
-      SeqWork w{0, 0};
-      if (b0 + lane < B) w = seq_work(p, R, b0 + lane, &s);
-      const long long mine = (long long)w.nch * w.units;
+      if (B > 32) {
+        mine = 0;
+        if (b0 + lane < B) {
+          load_seq(p, R, b0 + lane, &cur);
+          mine = chunks(cur);
+        }
+      }
       long long upto = mine;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
@@ -214,19 +215,23 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
       const unsigned past = __ballot_sync(0xffffffffu, before + upto > lo);
       if (past) {
         const int src = __ffs(past) - 1;
+        const long long pos = lo - __shfl_sync(0xffffffffu, before + upto - mine, src);
         cur.b = b0 + src;
-        cur.pos = lo - __shfl_sync(0xffffffffu, before + upto - mine, src);
-        cur.w.nch = __shfl_sync(0xffffffffu, w.nch, src);
-        cur.w.units = __shfl_sync(0xffffffffu, w.units, src);
-        cur.seq.row0 = __shfl_sync(0xffffffffu, s.row0, src);
-        cur.seq.n = __shfl_sync(0xffffffffu, s.n, src);
-        cur.seq.len = __shfl_sync(0xffffffffu, s.len, src);
+        cur.nch = __shfl_sync(0xffffffffu, cur.nch, src);
+        cur.nrb = __shfl_sync(0xffffffffu, cur.nrb, src);
+        cur.seq.row0 = __shfl_sync(0xffffffffu, cur.seq.row0, src);
+        cur.seq.n = __shfl_sync(0xffffffffu, cur.seq.n, src);
+        cur.seq.len = __shfl_sync(0xffffffffu, cur.seq.len, src);
+        const unsigned unit = pos < 0x7fffffff ? (unsigned)pos / (unsigned)cur.nch
+                                               : (unsigned)(pos / cur.nch);
+        cur.ch = (int)(pos - (long long)unit * cur.nch);
+        cur.h = (int)(unit / (unsigned)cur.nrb);
+        cur.rb = (int)(unit % (unsigned)cur.nrb);
         break;
       }
       before += __shfl_sync(0xffffffffu, upto, 31);
     }
   }
-  const int F = (int)F64;  // chunks of this CTA
   Record* records = reinterpret_cast<Record*>(p.workspace);
   float* part_lse = reinterpret_cast<float*>(static_cast<char*>(p.workspace) +
                                              (((size_t)gridDim.x * sizeof(Record) + 255) & ~255u));
@@ -240,26 +245,24 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
   struct Info {
     int slice;  // page * H + h, -1: nothing to load
     int row;    // first row in the block
-    float ks, lv;
+    float ks, vs;
   };
   const int bs = p.c.block_size;
   auto fetch = [&](Cursor at, int f0) {  // tiles f0 .. f0 + 31, `at` being tile f0
     Info r{-1, 0, 0.f, 0.f};
     if (f0 + lane >= F) return r;
     advance(p, R, &at, lane);
-    const int unit = (int)(at.pos / at.w.nch), ch = (int)(at.pos % at.w.nch);
-    const int h = unit / (at.w.units / p.c.H);
-    const int key = ch * kChunk + warp * kTile;
+    const int key = at.ch * kChunk + warp * kTile;
     if (key >= at.seq.len) return r;
-    const int page = p.c.block_table[(long long)at.b * p.c.table_width + key / bs];
+    const int page = p.c.block_table[(long long)at.b * p.c.table_width + (key >> p.c.block_log2)];
     if (page < 0 || page >= p.c.num_blocks) {
       if (p.c.err) atomicCAS(p.c.err, 0u, (unsigned)ERR_SITE_CACHE_FWD + 1);
       return r;
     }
-    r.slice = page * p.c.H + h;
-    r.row = key % bs;
-    r.ks = p.c.k_scale[r.slice];
-    r.lv = lg2(p.c.v_scale[r.slice]);
+    r.slice = page * p.c.H + at.h;
+    r.row = key & (bs - 1);
+    r.ks = p.c.k_scale[r.slice];  // not waited for here
+    r.vs = p.c.v_scale[r.slice];
     return r;
   };
   Cursor ahead = cur;
@@ -308,13 +311,6 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
   const int krow = D == 128 ? ((g & 1) << 2 | g >> 1) : g;
   const int vcol = D == 128 ? ((g & 1) << 2 | g >> 1) * 16 : g * 8;  // first column
 
-  int h = 0, rb = 0, ch = 0, nrb = 0;  // the current chunk: head, row block, chunk in the unit
-  if (F > 0) {
-    const int unit = (int)(cur.pos / cur.w.nch);
-    ch = (int)(cur.pos % cur.w.nch);
-    nrb = cur.w.units / p.c.H;
-    h = unit / nrb, rb = unit % nrb;
-  }
   for (int f = 0; f < F; ++f) {
     if (f > 0 && (f & 31) == 0) {
       now = next;
@@ -324,31 +320,37 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
         next = fetch(ahead, f + 32);
       }
     }
-    if (ok) issue(f);
+    const int h = cur.h, rb = cur.rb, ch = cur.ch;
     const int rows = min(R, cur.seq.n * G - rb * R);
-
-    if (f == 0 || ch == 0) {
-      // ------------------------------------------------------------ a unit (or piece) begins
+    const bool begins = f == 0 || ch == 0;  // a unit (or piece) begins
+    uint4 qraw[NT][D / 32];  // bf16: 16 of d = 128's first half, 16 of its second (d = 64: 16)
+    if (begins) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const int r = nt * 8 + g;
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) qraw[nt][j] = make_uint4(0u, 0u, 0u, 0u);
+        if (r < rows) {
+          const int i = rb * R + r;
+          const uint16_t* q = p.q.p + (long long)(cur.seq.row0 + p.by_G.div(i)) * p.q.st +
+                              (long long)(h * G + p.by_G.mod(i)) * p.q.sh;
+#pragma unroll
+          for (int j = 0; j < D / 32; ++j)
+            qraw[nt][j] = *reinterpret_cast<const uint4*>(q + (j >> 1) * 64 + t * 16 + (j & 1) * 8);
+        }
+      }
+    }
+    if (ok) issue(f);  // while q is on its way
+    if (begins) {
       const int seen0 = p.causal ? cur.seq.len - cur.seq.n + 1 : cur.seq.len;  // token 0's keys
       auto limit_of = [&](int r) {
-        return p.causal ? seen0 + (rb * R + r) / G : seen0;
+        return p.causal ? seen0 + p.by_G.div(rb * R + r) : seen0;
       };
       lim_lo = limit_of(0);
       lim_hi = min(cur.seq.len, limit_of(rows - 1));
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const int r = nt * 8 + g;
-        uint4 v[D / 32];  // bf16: 16 of d = 128's first half, 16 of its second (d = 64: 16)
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) v[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (r < rows) {
-          const int i = rb * R + r;
-          const uint16_t* q = p.q.p + (long long)(cur.seq.row0 + i / G) * p.q.st +
-                              (long long)(h * G + i % G) * p.q.sh;
-#pragma unroll
-          for (int j = 0; j < D / 32; ++j)
-            v[j] = *reinterpret_cast<const uint4*>(q + (j >> 1) * 64 + t * 16 + (j & 1) * 8);
-        }
+        const uint4* v = qraw[nt];
         uint32_t mx = 0u;
 #pragma unroll
         for (int j = 0; j < D / 32; ++j)
@@ -394,7 +396,7 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
     const int slice = __shfl_sync(0xffffffffu, now.slice, f & 31);
     if (slice >= 0 && ok) {
       const float ks = __shfl_sync(0xffffffffu, now.ks, f & 31);
-      const float lv = __shfl_sync(0xffffffffu, now.lv, f & 31);
+      const float lv = lg2(__shfl_sync(0xffffffffu, now.vs, f & 31));
       const uint32_t slot = done % C::ST;
       ok = __all_sync(0xffffffffu, mbar_wait(bar0 + 8u * slot, (done / C::ST) & 1u, wctx,
                                              ERR_SITE_CACHE_FWD + 2));
@@ -514,11 +516,11 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int j = 0; j < 4 * VW; ++j)
-              if (code_is_nan<E5M2>(v[i][j >> 2] >> (8 * (j & 3)))) {
-                poison = true;
-                v[i][j >> 2] &= ~(0xffu << (8 * (j & 3)));
-              }
+            for (int j = 0; j < VW; ++j) {
+              const uint32_t m = nan_codes<E5M2>(v[i][j]);
+              poison |= m != 0u;
+              v[i][j] = clear_codes(v[i][j], m);
+            }
           poison = __any_sync(0xffffffffu, poison);
         }
         // O^T: bytes 2 mt, 2 mt + 1 of the lane's columns are rows g, g + 8 of tile mt
@@ -544,11 +546,15 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
         if (poison) {  // rare: NaN for the rows that see it
           load_values(v);
 #pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < VW; ++j) v[i][j] = nan_codes<E5M2>(v[i][j]);
+#pragma unroll
           for (int j = 0; j < 4 * VW; ++j) {
             uint32_t bad = 0u;  // the tile's keys whose value in this column is NaN
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              if (code_is_nan<E5M2>(v[i][j >> 2] >> (8 * (j & 3)))) bad |= 1u << value_row(i);
+              if (v[i][j >> 2] >> (8 * (j & 3)) & 0x80u) bad |= 1u << value_row(i);
             bad |= __shfl_xor_sync(0xffffffffu, bad, 1);
             bad |= __shfl_xor_sync(0xffffffffu, bad, 2);
 #pragma unroll
@@ -565,7 +571,7 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
     }
 
     // ---------------------------------------------------------------- a unit (or piece) ends
-    const bool unit_ends = ch == cur.w.nch - 1;
+    const bool unit_ends = ch == cur.nch - 1;
     if (unit_ends || f == F - 1) {
       // this warp's rows: normalised result and log2-sum-exp
       float mine[NT][2], fac[NT][2];
@@ -598,32 +604,27 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
           sum[nt][i] = z;
           fac[nt][i] = lsum[nt][i] == 0.f ? 0.f : ex2(mine[nt][i] - mm) / (z * lsum[nt][i]);
         }
-      // sum over the warps: the first ones write, the others add in turn
-#pragma unroll 1
-      for (int phase = 0; phase < kWarps / C::BUFS; ++phase) {
-        if (warp / C::BUFS == phase) {
+      // the warps' results side by side; 16-byte columns are permuted so that the lanes
+      // of a store phase (two g, four t) touch different banks
+      auto column = [&](int r, int c4) {
+        const int k = r >> 1;  // t of the lane that holds row r
+        return D == 128 ? c4 ^ (((c4 >> 4) & 1) << 2 | (k & 3))
+                        : c4 ^ ((k & 1) << 2 | ((k >> 1) & 1));
+      };
+      float4* red4 = reinterpret_cast<float4*>(red);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              float4* dst = reinterpret_cast<float4*>(red + ((warp % C::BUFS) * R + nt * 8 + 2 * t + i) * D + vcol);
+        for (int i = 0; i < 2; ++i) {
+          const int r = nt * 8 + 2 * t + i;
 #pragma unroll
-              for (int j = 0; j < VW; ++j) {
-                float4 x;
-                x.x = acc[2 * j][nt][i] * fac[nt][i] * up;
-                x.y = acc[2 * j][nt][i + 2] * fac[nt][i] * up;
-                x.z = acc[2 * j + 1][nt][i] * fac[nt][i] * up;
-                x.w = acc[2 * j + 1][nt][i + 2] * fac[nt][i] * up;
-                if (phase) {
-                  const float4 y = dst[j];
-                  x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
-                }
-                dst[j] = x;
-              }
-            }
+          for (int j = 0; j < VW; ++j)
+            red4[(warp * R + r) * (D / 4) + column(r, vcol / 4 + j)] =
+                make_float4(acc[2 * j][nt][i] * fac[nt][i] * up, acc[2 * j][nt][i + 2] * fac[nt][i] * up,
+                            acc[2 * j + 1][nt][i] * fac[nt][i] * up,
+                            acc[2 * j + 1][nt][i + 2] * fac[nt][i] * up);
         }
-        __syncthreads();
-      }
+      __syncthreads();
       const bool starts_here = f >= ch;  // the unit's chunk 0 is in this share
       const bool whole = starts_here && unit_ends;
       const int slot = starts_here ? 1 : 0;
@@ -639,7 +640,7 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
             if (r < rows) {
               if (whole) {
                 const int i0 = rb * R + r;
-                p.lse[(long long)(h * G + i0 % G) * p.c.total + cur.seq.row0 + i0 / G] = L;
+                p.lse[(long long)(h * G + p.by_G.mod(i0)) * p.c.total + cur.seq.row0 + p.by_G.div(i0)] = L;
               } else {
                 part_lse[((size_t)blockIdx.x * 2 + slot) * R + r] = L;
               }
@@ -648,15 +649,16 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
       }
       for (int x = threadIdx.x; x < rows * (D / 4); x += 128) {
         const int r = x / (D / 4), c4 = x % (D / 4);
-        float4 o = reinterpret_cast<const float4*>(red)[r * (D / 4) + c4];
-        if (C::BUFS == 2) {
-          const float4 b = reinterpret_cast<const float4*>(red)[(R + r) * (D / 4) + c4];
-          o.x += b.x, o.y += b.y, o.z += b.z, o.w += b.w;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float4 y = red4[(w * R + r) * (D / 4) + column(r, c4)];
+          o.x += y.x, o.y += y.y, o.z += y.z, o.w += y.w;
         }
         if (whole) {
           const int i0 = rb * R + r;
-          *reinterpret_cast<uint2*>(p.o.p + (long long)(cur.seq.row0 + i0 / G) * p.o.st +
-                                    (long long)(h * G + i0 % G) * p.o.sh + c4 * 4) =
+          *reinterpret_cast<uint2*>(p.o.p + (long long)(cur.seq.row0 + p.by_G.div(i0)) * p.o.st +
+                                    (long long)(h * G + p.by_G.mod(i0)) * p.o.sh + c4 * 4) =
               make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
         } else {
           reinterpret_cast<float4*>(part_o)[(((size_t)blockIdx.x * 2 + slot) * R + r) * (D / 4) +
@@ -664,28 +666,14 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
         }
       }
       if (starts_here && !unit_ends) {  // later CTAs hold the rest
-        const long long u0 = lo + f - ch;
-        rec.parts = (int)((u0 + cur.w.nch - 1) / share - blockIdx.x) + 1;
+        rec.parts = 1 + (cur.nch - 1 - ch + (int)share - 1) / (int)share;
         rec.rows = rows;
         rec.h = h;
         rec.row0 = cur.seq.row0;
         rec.first_row = rb * R;
       }
     }
-    if (!unit_ends) {
-      ++ch;
-    } else {
-      ch = 0;
-      if (++rb == nrb) {
-        rb = 0;
-        if (++h == p.c.H) {  // the next sequence with work
-          h = 0;
-          cur.pos = (long long)cur.w.nch * cur.w.units;
-          advance(p, R, &cur, 0);
-          nrb = cur.w.units / p.c.H;
-        }
-      }
-    }
+    advance(p, R, &cur, 1);
   }
   // loads in flight land before the CTA ends (only after a wait that ran out)
   for (; done < issued; ++done)
@@ -693,42 +681,72 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
   if (threadIdx.x == 0) records[blockIdx.x] = rec;
 }
 
-// Joins the pieces of the unit that CTA blockIdx.x of the kernel above began and
-// did not finish: its own second slot, then the first slots of the CTAs behind.
+// Joins the pieces of the unit that CTA blockIdx.x of a split kernel began and did
+// not finish: its own second slot, then the first slots of the CTAs behind.  Latency
+// counts: the weights of 32 pieces are read by one instruction, and eight pieces'
+// rows are in flight at a time.
 template <int D>
 __global__ void __launch_bounds__(256) cache_merge_kernel(const CacheFwdParams p, int R) {
+  constexpr float kLog2e = 1.4426950408889634f;
+  constexpr int C4 = D / 4;  // 16-byte columns: one per lane (d = 64: two rows per warp)
+  constexpr int RPW = 32 / C4;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Record rec = reinterpret_cast<const Record*>(p.workspace)[blockIdx.x];
-  if (rec.parts == 0) return;
   const float* part_lse = reinterpret_cast<const float*>(
       static_cast<const char*>(p.workspace) + (((size_t)gridDim.x * sizeof(Record) + 255) & ~255u));
-  const float* part_o = part_lse + (((size_t)gridDim.x * 2 * R + 63) & ~(size_t)63);
-  const int G = p.Hq / p.c.H;
-  constexpr float kLog2e = 1.4426950408889634f;
-  for (int x = threadIdx.x; x < rec.rows * (D / 4); x += 256) {
-    const int r = x / (D / 4), c4 = x % (D / 4);
-    // piece i: slot 1 of this CTA, slot 0 of the next ones
-    auto at = [&](int i) { return ((size_t)(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * R + r; };
-    float m = -INFINITY;
-    for (int i = 0; i < rec.parts; ++i) m = fmaxf(m, part_lse[at(i)]);
-    const float mm = m == -INFINITY ? 0.f : m;
-    float sum = 0.f;
+  const float4* part_o =
+      reinterpret_cast<const float4*>(part_lse + (((size_t)gridDim.x * 2 * R + 63) & ~(size_t)63));
+  // piece i of row r: slot 1 of this CTA, slot 0 of the next ones
+  auto at = [&](int i, int r) {
+    return ((size_t)(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * R + r;
+  };
+  if (rec.parts == 0) return;
+  for (int r0 = warp * RPW; r0 < rec.rows; r0 += 8 * RPW) {
+    const int r = r0 + lane / C4, c4 = lane % C4;
+    const bool on = r < rec.rows;
+    float m = -INFINITY, sum = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i = 0; i < rec.parts; ++i) {
-      const float w = ex2((part_lse[at(i)] - mm) * kLog2e);
-      const float4 v = reinterpret_cast<const float4*>(part_o)[at(i) * (D / 4) + c4];
-      sum += w;
-      o.x = fmaf(w, v.x, o.x), o.y = fmaf(w, v.y, o.y);
-      o.z = fmaf(w, v.z, o.z), o.w = fmaf(w, v.w, o.w);
+    for (int i0 = 0; i0 < rec.parts; i0 += C4) {  // as many pieces as a row has lanes
+      const float l = on && i0 + c4 < rec.parts ? part_lse[at(i0 + c4, r)] * kLog2e : -INFINITY;
+      float top = l;
+#pragma unroll
+      for (int w = C4 / 2; w > 0; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+      top = fmaxf(top, m);
+      const float mm = top == -INFINITY ? 0.f : top;
+      const float alpha = ex2(m - mm);
+      m = top;
+      const float w = ex2(l - mm);  // 0 behind the last piece
+      float z = w;
+#pragma unroll
+      for (int k = C4 / 2; k > 0; k >>= 1) z += __shfl_xor_sync(0xffffffffu, z, k);
+      sum = sum * alpha + z;
+      o.x *= alpha, o.y *= alpha, o.z *= alpha, o.w *= alpha;
+      const int n = min(C4, rec.parts - i0);
+      for (int i = 0; i < n; i += 8) {
+        float4 v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          v[k] = on && i + k < n ? part_o[at(i0 + i + k, r) * C4 + c4] : make_float4(0, 0, 0, 0);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float x = __shfl_sync(0xffffffffu, w, (lane / C4) * C4 + ((i + k) & (C4 - 1)));
+          o.x = fmaf(x, v[k].x, o.x), o.y = fmaf(x, v[k].y, o.y);
+          o.z = fmaf(x, v[k].z, o.z), o.w = fmaf(x, v[k].w, o.w);
+        }
+      }
     }
+    if (!on) continue;
     const bool any = !(sum == 0.f);
     const float inv = any ? 1.f / sum : 0.f;
     const int i0 = rec.first_row + r;
-    const long long token = rec.row0 + i0 / G;
-    const int hq = rec.h * G + i0 % G;
+    const long long token = rec.row0 + p.by_G.div(i0);
+    const int hq = rec.h * p.G + p.by_G.mod(i0);
     *reinterpret_cast<uint2*>(p.o.p + token * p.o.st + hq * p.o.sh + c4 * 4) = make_uint2(
         pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-    if (c4 == 0) p.lse[(long long)hq * p.c.total + token] = any ? mm + lg2(sum) * kLn2 : -INFINITY;
+    if (c4 == 0)
+      p.lse[(long long)hq * p.c.total + token] =
+          any ? (m + lg2(sum)) * kLn2 : -INFINITY;
   }
 }
 

@@ -112,21 +112,6 @@ enum {
 };
 static_assert(8 * (B_KV_FULL + 2 * Wide<64>::STAGES) + 16 <= 256, "barrier block");
 
-template <bool E5M2>
-__device__ __forceinline__ bool word_has_nan(uint32_t w) {  // any of four codes NaN (or infinite)
-  bool any = false;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) any |= ((w >> (8 * i)) & 0x7fu) >= (E5M2 ? 0x7cu : 0x7fu);
-  return any;
-}
-template <bool E5M2>
-__device__ __forceinline__ uint32_t without_nan(uint32_t w) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (((w >> (8 * i)) & 0x7fu) >= (E5M2 ? 0x7cu : 0x7fu)) w &= ~(0xffu << (8 * i));
-  return w;
-}
-
 template <int D, bool E5M2>
 __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
     cache_fwd_wide_kernel(const CacheFwdParams p) {
@@ -137,7 +122,7 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
   const uint32_t sbase = (raw + 1023u) & ~1023u;
   uint8_t* smem = smem_raw + (sbase - raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int G = p.Hq / p.c.H;
+  const int G = p.G;
 
   // Row blocks of sequence b sit at slots cu_seqlens[b] G / 256 + b and on, which
   // is room for all of them; the later ones of a sequence, which see more keys, first.
@@ -161,7 +146,7 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
   // keys seen by row r of the sequence
   const int seen0 = p.causal ? seq.len - seq.n + 1 : seq.len;
   auto limit_of = [&](int r) {
-    return max(0, min(seq.len, p.causal ? seen0 + r / G : seen0));
+    return max(0, min(seq.len, p.causal ? seen0 + p.by_G.div(r) : seen0));
   };
   const int r0_0 = rb * C::ROWS, r0_1 = r0_0 + C::BM;
   auto tiles_for = [&](int r0) {
@@ -232,13 +217,13 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
       Info r{-1, 0, 0.f, 0.f};
       const int key = (j0 + (lane >> 1)) * C::BN + me * 32 + (lane & 1) * 16;
       if (key >= lim_hi) return r;
-      const int page = p.c.block_table[(long long)b * p.c.table_width + key / bs];
+      const int page = p.c.block_table[(long long)b * p.c.table_width + (key >> p.c.block_log2)];
       if (page < 0 || page >= p.c.num_blocks) {
         if (p.c.err) atomicCAS(p.c.err, 0u, (unsigned)ERR_SITE_CACHE_FWD + 1);
         return r;
       }
       r.slice = page * p.c.H + h;
-      r.row = key % bs;
+      r.row = key & (bs - 1);
       r.ks = p.c.k_scale[r.slice];
       r.lv = lg2(p.c.v_scale[r.slice]);
       return r;
@@ -318,10 +303,9 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {
                   if (key0 + pc * 16 + x * ROWS_LD >= lim_hi) w[y] = 0u;  // stale, whatever it is
-                  if (word_has_nan<E5M2>(w[y])) {
-                    nan = true;
-                    w[y] = without_nan<E5M2>(w[y]);
-                  }
+                  const uint32_t m = nan_codes<E5M2>(w[y]);
+                  nan |= m != 0u;
+                  w[y] = clear_codes(w[y], m);
                 }
               }
             if (nan) *poison = 1u;
@@ -450,8 +434,8 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
 #pragma unroll
       for (int i = 0; i < D / 8; ++i) v[i] = make_uint4(0u, 0u, 0u, 0u);
       if (valid) {
-        const uint16_t* q = p.q.p + (long long)(seq.row0 + row / G) * p.q.st +
-                            (long long)(h * G + row % G) * p.q.sh;
+        const uint16_t* q = p.q.p + (long long)(seq.row0 + p.by_G.div(row)) * p.q.st +
+                            (long long)(h * G + p.by_G.mod(row)) * p.q.sh;
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) v[i] = *reinterpret_cast<const uint4*>(q + 8 * i);
       }
@@ -586,8 +570,8 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
     }
 
     // ------------------------------------------------------------ epilogue
-    uint16_t* o_row = p.o.p + (long long)(seq.row0 + row / G) * p.o.st +
-                      (long long)(h * G + row % G) * p.o.sh;
+    uint16_t* o_row = p.o.p + (long long)(seq.row0 + p.by_G.div(row)) * p.o.st +
+                      (long long)(h * G + p.by_G.mod(row)) * p.o.sh;
     const bool has = my_nt > 0 && !(l_run == 0.f);
     const float base = *base_lv;
     const float inv = has ? 1.f / l_run : 0.f, up = ex2(base);
@@ -618,7 +602,7 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
       }
     }
     if (valid)
-      p.lse[(long long)(h * G + row % G) * p.c.total + seq.row0 + row / G] =
+      p.lse[(long long)(h * G + p.by_G.mod(row)) * p.c.total + seq.row0 + p.by_G.div(row)] =
           has ? (r_run - base + lg2(l_run)) * kLn2 : -INFINITY;
     __syncwarp();
   }
@@ -635,12 +619,12 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
     const int row = r0_0 + (int)threadIdx.x;
     if (row < n_rows) {
       const int lim = limit_of(row), bs = p.c.block_size;
-      uint16_t* o_row = p.o.p + (long long)(seq.row0 + row / G) * p.o.st +
-                        (long long)(h * G + row % G) * p.o.sh;
+      uint16_t* o_row = p.o.p + (long long)(seq.row0 + p.by_G.div(row)) * p.o.st +
+                        (long long)(h * G + p.by_G.mod(row)) * p.o.sh;
       for (int key = lim_lo & ~15; key < lim; ++key) {
-        const int page = p.c.block_table[(long long)b * p.c.table_width + key / bs];
+        const int page = p.c.block_table[(long long)b * p.c.table_width + (key >> p.c.block_log2)];
         if (page < 0 || page >= p.c.num_blocks) continue;
-        const uint8_t* v = p.c.v + (((long long)page * p.c.H + h) * bs + key % bs) * D;
+        const uint8_t* v = p.c.v + (((long long)page * p.c.H + h) * bs + (key & (bs - 1))) * D;
         for (int c = 0; c < D; ++c)
           if ((v[c] & 0x7fu) >= (E5M2 ? 0x7cu : 0x7fu)) o_row[c] = 0x7fffu;
       }
@@ -663,7 +647,7 @@ cudaError_t launch(const CacheFwdParams& p, cudaStream_t stream) {
     return fa.numRegs >= C::REG_LAUNCH ? cudaSuccess : cudaErrorInvalidConfiguration;
   });
   if (e != cudaSuccess) return e;
-  const int G = p.Hq / p.c.H;
+  const int G = p.G;
   const long long units = ((long long)p.c.total * G / C::ROWS + p.c.B) * p.c.H;
   if (units > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   cache_fwd_wide_kernel<D, E5M2><<<(unsigned)units, C::THREADS, C::SMEM, stream>>>(p);

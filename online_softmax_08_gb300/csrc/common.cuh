@@ -111,6 +111,24 @@ __device__ __forceinline__ bool seq_view(const Varlen& vl, int dense_N, int seq,
   return true;
 }
 
+// Division of 0 <= n < 2^31 by a fixed d >= 1 without the hardware's division
+// sequence: q = (n + floor(n mul / 2^32)) >> shift with 2^(shift - 1) < d <= 2^shift
+// and mul = floor(2^32 (2^shift - d) / d) + 1.
+struct FastDiv {
+  unsigned d, mul, shift;
+  FastDiv() = default;
+  explicit FastDiv(unsigned divisor) : d(divisor), shift(0) {
+    while ((1ull << shift) < d) ++shift;
+    mul = (unsigned)((((1ull << shift) - d) << 32) / d) + 1u;
+  }
+#ifdef __CUDACC__
+  __device__ __forceinline__ int div(int n) const {
+    return (int)((__umulhi((unsigned)n, mul) + (unsigned)n) >> shift);
+  }
+  __device__ __forceinline__ int mod(int n) const { return n - div(n) * (int)d; }
+#endif
+};
+
 // The 8-bit key/value cache: the pool of blocks and the tokens a call works on
 // (fattn_cache and fattn_cache_batch, with the device's error word).
 struct CacheParams {
@@ -119,6 +137,7 @@ struct CacheParams {
   float* k_scale;        // [num_blocks, H]
   float* v_scale;
   int num_blocks, H, block_size, d, format;
+  int block_log2;        // block_size = 1 << block_log2
   const int* block_table;
   const int* lens;
   const int* cu_seqlens;
@@ -135,6 +154,8 @@ struct CacheFwdParams {
   TokenView q, o;
   float* lse;        // [Hq, total]
   int Hq;
+  int G;             // Hq / H, the query heads of a key/value head
+  FastDiv by_G;
   int causal;
   float scale_log2;  // scale * log2(e)
   int narrow_rows;   // sequences with more query rows per key/value head (tokens x grouped heads)
