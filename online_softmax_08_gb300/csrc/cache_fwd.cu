@@ -60,12 +60,12 @@ struct Dec {
   static constexpr int R = 8 * NT;                // query rows per unit
   static constexpr int TILE = kTile * D;          // bytes
   static constexpr int STAGE = 2 * TILE;          // keys and values
-  static constexpr int ST = (D == 128 ? 1 : 2) * (NT == 1 ? 3 : 4);  // ring slots per warp
+  static constexpr int ST = D == 64 ? 6 : NT == 1 ? 3 : 4;  // ring slots per warp
   static constexpr int OFF_RED = kWarps * ST * STAGE;
   static constexpr int OFF_STAT = OFF_RED + kWarps * R * D * 4;  // behind the warps' results
   static constexpr int OFF_BAR = OFF_STAT + kWarps * R * 4;
   static constexpr int SMEM = OFF_BAR + kWarps * ST * 8 + 16 + 1024;
-  static constexpr int CTAS = NT == 1 ? 3 : 2;    // per SM
+  static constexpr int CTAS = NT == 1 || D == 64 ? 3 : 2;    // per SM
 };
 
 constexpr int kNarrowRows = 64;
@@ -83,10 +83,11 @@ struct Cursor {
   int nch, nrb;
   CacheSeq seq;
 };
-__device__ __forceinline__ void load_seq(const CacheFwdParams& p, int R, int b, Cursor* c) {
+__device__ __forceinline__ void set_seq(const CacheFwdParams& p, int R, int b, int row0, int end,
+                                        int len, Cursor* c) {
   c->b = b;
   c->nch = c->nrb = 0;
-  if (!cache_seq(p.c, b, &c->seq)) {
+  if (!cache_seq(p.c, row0, end, len, &c->seq)) {
     if (p.c.err) atomicCAS(p.c.err, 0u, (unsigned)ERR_SITE_CACHE_FWD);
     return;
   }
@@ -94,6 +95,9 @@ __device__ __forceinline__ void load_seq(const CacheFwdParams& p, int R, int b, 
   if (rows == 0 || rows > p.narrow_rows) return;  // (the other kernel's)
   c->nch = max(1, (c->seq.len + kChunk - 1) / kChunk);
   c->nrb = (rows + R - 1) / R;
+}
+__device__ __forceinline__ void load_seq(const CacheFwdParams& p, int R, int b, Cursor* c) {
+  set_seq(p, R, b, p.c.cu_seqlens[b], p.c.cu_seqlens[b + 1], p.c.lens[b], c);
 }
 __device__ __forceinline__ void advance(const CacheFwdParams& p, int R, Cursor* c, int by) {
   c->ch += by;
@@ -168,6 +172,13 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
   const WaitCtx wctx{abort_flag, p.c.err};
   const uint32_t ring = sbase + (uint32_t)(warp * C::ST * C::STAGE);
 
+  // this lane's sequence of the first group of 32, on its way during the set-up
+  int first_row0 = 0, first_end = 0, first_len = 0;
+  if (lane < p.c.B) {
+    first_row0 = p.c.cu_seqlens[lane];
+    first_end = p.c.cu_seqlens[lane + 1];
+    first_len = p.c.lens[lane];
+  }
   if (lane == 0) {
     for (int i = 0; i < C::ST; ++i) mbar_init(bar0 + 8u * i, 1);
     if (warp == 0) *abort_flag = 0u;
@@ -184,7 +195,10 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
   for (int b0 = 0; b0 < B; b0 += 32) {
     mine = 0;
     if (b0 + lane < B) {
-      load_seq(p, R, b0 + lane, &cur);
+      if (b0 == 0)
+        set_seq(p, R, lane, first_row0, first_end, first_len, &cur);
+      else
+        load_seq(p, R, b0 + lane, &cur);
       mine = chunks(cur);
     }
     total += mine;
@@ -794,7 +808,7 @@ size_t cache_fwd_workspace(const CacheParams& c, int, int n_sm) {
     return ((grid * sizeof(Record) + 255) & ~(size_t)255) +
            ((grid * 2 * R + 63) & ~(size_t)63) * 4 + grid * 2 * R * c.d * 4;
   };
-  return std::max(bytes(Dec<128, 1>::R, Dec<128, 1>::CTAS), bytes(Dec<128, 2>::R, Dec<128, 2>::CTAS));
+  return std::max(bytes(Dec<128, 1>::R, Dec<128, 1>::CTAS), bytes(Dec<64, 2>::R, Dec<64, 2>::CTAS));
 }
 
 cudaError_t launch_cache_fwd(const CUtensorMap& tk, const CUtensorMap& tv,

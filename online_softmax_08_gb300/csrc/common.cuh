@@ -169,14 +169,16 @@ struct CacheFwdParams {
 struct CacheSeq {
   int row0, n, len;
 };
-__device__ __forceinline__ bool cache_seq(const CacheParams& c, int b, CacheSeq* s) {
-  const int a = c.cu_seqlens[b], e = c.cu_seqlens[b + 1];
-  const int len = c.lens[b];
+__device__ __forceinline__ bool cache_seq(const CacheParams& c, int a, int e, int len,
+                                          CacheSeq* s) {
   s->row0 = a;
   s->n = e - a;
   s->len = len;
   return a >= 0 && e >= a && e <= c.total && e - a <= c.max_seqlen && len >= 0 &&
          (long long)len <= (long long)c.table_width * c.block_size;
+}
+__device__ __forceinline__ bool cache_seq(const CacheParams& c, int b, CacheSeq* s) {
+  return cache_seq(c, c.cu_seqlens[b], c.cu_seqlens[b + 1], c.lens[b], s);
 }
 
 // Identity of the calling thread's current CUDA context (the device's primary
