@@ -618,7 +618,7 @@ extern "C" size_t fattn_cache_fwd_workspace_bytes(const fattn_cache* cache,
     return 0;
   DeviceInfo* dev = nullptr;
   if (current_device(&dev) != FATTN_OK) return 0;
-  return cache_fwd_workspace(cache_params(cache, batch, nullptr), Hq, dev->n_sm);
+  return cache_fwd_workspace(cache_params(cache, batch, nullptr), Hq / cache->H, dev->n_sm);
 }
 
 extern "C" int fattn_cache_fwd(const fattn_cache* cache, const fattn_cache_batch* batch,
@@ -645,7 +645,7 @@ extern "C" int fattn_cache_fwd(const fattn_cache* cache, const fattn_cache_batch
   if (st != FATTN_OK) return st;
   CacheFwdParams p{};
   p.c = cache_params(cache, batch, dev->err);
-  if (workspace_bytes < cache_fwd_workspace(p.c, Hq, dev->n_sm)) return FATTN_ERR_WORKSPACE;
+  if (workspace_bytes < cache_fwd_workspace(p.c, Hq / cache->H, dev->n_sm)) return FATTN_ERR_WORKSPACE;
   p.q = token_view(q, q_token_stride, q_head_stride, T, Hq);
   p.o = token_view(o, o_token_stride, o_head_stride, T, Hq);
   p.lse = lse;

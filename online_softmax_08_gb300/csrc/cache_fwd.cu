@@ -69,12 +69,7 @@ struct Dec {
 };
 
 constexpr int kNarrowRows = 64;
-
-// What a CTA leaves for the merge kernel: the unit that starts in its share and
-// ends in a later CTA's (parts = 0: there is none).
-struct Record {
-  int parts, rows, h, row0, first_row;
-};
+constexpr int kWideMerge = 8;  // merge blocks per CTA of the 256-row kernel
 
 // A position in the list of all chunks: chunk ch of unit (sequence b, head h, row
 // block rb).  Sequence b has H x nrb units of nch chunks (none: nch = 0).
@@ -250,7 +245,7 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
   float* part_lse = reinterpret_cast<float*>(static_cast<char*>(p.workspace) +
                                              (((size_t)gridDim.x * sizeof(Record) + 255) & ~255u));
   float* part_o = part_lse + (((size_t)gridDim.x * 2 * R + 63) & ~(size_t)63);
-  Record rec{0, 0, 0, 0, 0};
+  Record rec{0, 0, 0, 0, 0, 0};
   __syncthreads();  // barriers initialised
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
@@ -693,30 +688,43 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
   for (; done < issued; ++done)
     mbar_drain(bar0 + 8u * (done % C::ST), (done / C::ST) & 1u, wctx, ERR_SITE_CACHE_FWD + 3);
   if (threadIdx.x == 0) records[blockIdx.x] = rec;
+  // launched behind the 256-row kernel, this one may overtake it; the merge must not
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-// Joins the pieces of the unit that CTA blockIdx.x of a split kernel began and did
-// not finish: its own second slot, then the first slots of the CTAs behind.  Latency
-// counts: the weights of 32 pieces are read by one instruction, and eight pieces'
-// rows are in flight at a time.
+// Joins the pieces of the unit that CTA blockIdx.x of an attention kernel began and
+// did not finish: its own second slot, then the first slots of the CTAs behind.
+// The first narrow_ctas blocks serve the kernel above, the others the 256-row one,
+// kWideMerge of them each of its CTAs.
+// Latency counts: the weights of 32 pieces are read by one instruction, and eight
+// pieces' rows are in flight at a time.
 template <int D>
-__global__ void __launch_bounds__(256) cache_merge_kernel(const CacheFwdParams p, int R) {
+__global__ void __launch_bounds__(256)
+    cache_merge_kernel(const CacheFwdParams p, int narrow_ctas, int narrow_R, int wide_ctas,
+                       int wide_R) {
   constexpr float kLog2e = 1.4426950408889634f;
   constexpr int C4 = D / 4;  // 16-byte columns: one per lane (d = 64: two rows per warp)
   constexpr int RPW = 32 / C4;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int behind = (int)blockIdx.x - narrow_ctas;
+  const bool wide = behind >= 0;
+  const int ctas = wide ? wide_ctas : narrow_ctas, R = wide ? wide_R : narrow_R;
+  const int cta = wide ? behind % wide_ctas : blockIdx.x;
+  const char* ws = static_cast<const char*>(wide ? p.wide_workspace : p.workspace);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const Record rec = reinterpret_cast<const Record*>(p.workspace)[blockIdx.x];
-  const float* part_lse = reinterpret_cast<const float*>(
-      static_cast<const char*>(p.workspace) + (((size_t)gridDim.x * sizeof(Record) + 255) & ~255u));
+  const Record rec = reinterpret_cast<const Record*>(ws)[cta];
+  const float* part_lse =
+      reinterpret_cast<const float*>(ws + (((size_t)ctas * sizeof(Record) + 255) & ~255u));
   const float4* part_o =
-      reinterpret_cast<const float4*>(part_lse + (((size_t)gridDim.x * 2 * R + 63) & ~(size_t)63));
-  // piece i of row r: slot 1 of this CTA, slot 0 of the next ones
+      reinterpret_cast<const float4*>(part_lse + (((size_t)ctas * 2 * R + 63) & ~(size_t)63));
+  // piece i of row r: slot 1 of this CTA, slot 0 of the next ones; wide: one behind another
   auto at = [&](int i, int r) {
-    return ((size_t)(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * R + r;
+    return (wide ? (size_t)rec.place + i : (size_t)(cta + i) * 2 + (i == 0 ? 1 : 0)) * R + r;
   };
   if (rec.parts == 0) return;
-  for (int r0 = warp * RPW; r0 < rec.rows; r0 += 8 * RPW) {
+  const int first = wide ? behind / wide_ctas * 8 + warp : warp;
+  const int step = wide ? kWideMerge * 8 : 8;
+  for (int r0 = first * RPW; r0 < rec.rows; r0 += step * RPW) {
     const int r = r0 + lane / C4, c4 = lane % C4;
     const bool on = r < rec.rows;
     float m = -INFINITY, sum = 0.f;
@@ -766,7 +774,7 @@ __global__ void __launch_bounds__(256) cache_merge_kernel(const CacheFwdParams p
 
 template <int D, bool E5M2, int NT>
 cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const CacheFwdParams& p, int n_sm,
-                   cudaStream_t stream) {
+                   bool wide, cudaStream_t stream) {
   using C = Dec<D, NT>;
   static_assert(C::CTAS * (C::SMEM + 1024) <= 233472, "shared memory of the CTAs sharing an SM");
   static unsigned long long prepared[64];
@@ -776,54 +784,78 @@ cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const CacheFwdP
   });
   if (e != cudaSuccess) return e;
   const unsigned grid = (unsigned)(n_sm * C::CTAS);
-  cache_fwd_kernel<D, E5M2, NT><<<grid, 128, C::SMEM, stream>>>(tk, tv, p);
-  if (const cudaError_t r = cudaGetLastError()) return r;
-  // the merge starts while the last CTAs finish, and waits for them on the device
+  // each kernel may start while the last CTAs of the one before finish; what depends
+  // on its results is waited for on the device
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(256);
-  cfg.stream = stream;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(128);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = stream;
+  if (wide) {
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+  }
+  const cudaError_t r = cudaLaunchKernelEx(&cfg, cache_fwd_kernel<D, E5M2, NT>, tk, tv, p);
+  if (r != cudaSuccess) return r;
+  cfg.gridDim = dim3(grid + (wide ? kWideMerge * n_sm : 0));
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cache_merge_kernel<D>, p, (int)C::R);
+  return cudaLaunchKernelEx(&cfg, cache_merge_kernel<D>, p, (int)grid, (int)C::R, n_sm,
+                            cache_fwd_wide_rows());
 }
 
 template <int D, bool E5M2>
 cudaError_t launch_rows(const CUtensorMap& tk, const CUtensorMap& tv, const CacheFwdParams& p,
-                        int n_sm, cudaStream_t stream) {
-  const long long rows = (long long)p.c.max_seqlen * (p.Hq / p.c.H);
-  return rows <= 8 ? launch<D, E5M2, 1>(tk, tv, p, n_sm, stream)
-                   : launch<D, E5M2, 2>(tk, tv, p, n_sm, stream);
+                        int n_sm, bool wide, cudaStream_t stream) {
+  const long long rows = (long long)p.c.max_seqlen * p.G;
+  return rows <= 8 ? launch<D, E5M2, 1>(tk, tv, p, n_sm, wide, stream)
+                   : launch<D, E5M2, 2>(tk, tv, p, n_sm, wide, stream);
+}
+
+// Bytes of the records, LSE and O of `ctas` CTAs with R rows per unit.
+size_t pieces_bytes(size_t ctas, int R, int d) {
+  return ((ctas * sizeof(Record) + 255) & ~(size_t)255) +
+         ((ctas * 2 * R + 63) & ~(size_t)63) * 4 + ctas * 2 * R * d * 4;
+}
+size_t narrow_bytes(int d, int n_sm) {  // the larger of the two variants
+  return std::max(pieces_bytes((size_t)n_sm * Dec<128, 1>::CTAS, Dec<128, 1>::R, d),
+                  pieces_bytes((size_t)n_sm * Dec<64, 2>::CTAS, Dec<64, 2>::R, d));
+}
+// Whether a call may have sequences for the 256-row kernel (whose row blocks hold
+// whole tokens: groups of more than 256 heads stay with the other one).
+bool takes_wide(const CacheParams& c, int G) {
+  return (long long)c.max_seqlen * G > kNarrowRows && G <= cache_fwd_wide_rows();
 }
 
 }  // namespace
 
-size_t cache_fwd_workspace(const CacheParams& c, int, int n_sm) {
-  // records, then LSE and O of two pieces per CTA, for the larger of the two variants
-  auto bytes = [&](int R, int ctas) {
-    const size_t grid = (size_t)n_sm * ctas;
-    return ((grid * sizeof(Record) + 255) & ~(size_t)255) +
-           ((grid * 2 * R + 63) & ~(size_t)63) * 4 + grid * 2 * R * c.d * 4;
-  };
-  return std::max(bytes(Dec<128, 1>::R, Dec<128, 1>::CTAS), bytes(Dec<64, 2>::R, Dec<64, 2>::CTAS));
+size_t cache_fwd_workspace(const CacheParams& c, int G, int n_sm) {
+  return narrow_bytes(c.d, n_sm) +
+         (takes_wide(c, G) ? pieces_bytes((size_t)n_sm, cache_fwd_wide_rows(), c.d) : 0);
 }
 
 cudaError_t launch_cache_fwd(const CUtensorMap& tk, const CUtensorMap& tv,
                              const CacheFwdParams& params, int n_sm, cudaStream_t stream) {
   CacheFwdParams p = params;
-  p.narrow_rows = kNarrowRows;
-  if ((long long)p.c.max_seqlen * (p.Hq / p.c.H) > kNarrowRows) {
+  const bool wide = takes_wide(p.c, p.G);
+  p.narrow_rows = wide ? kNarrowRows : 0x7fffffff;
+  if (wide) {
+    p.wide_tokens = cache_fwd_wide_rows() / p.G;
+    p.wide_ctas = n_sm;
+    p.wide_workspace = static_cast<char*>(p.workspace) + narrow_bytes(p.c.d, n_sm);
     const cudaError_t e = launch_cache_fwd_wide(p, stream);
     if (e != cudaSuccess) return e;
   }
   if (p.c.d == 128)
-    return p.c.format ? launch_rows<128, true>(tk, tv, p, n_sm, stream)
-                      : launch_rows<128, false>(tk, tv, p, n_sm, stream);
-  return p.c.format ? launch_rows<64, true>(tk, tv, p, n_sm, stream)
-                    : launch_rows<64, false>(tk, tv, p, n_sm, stream);
+    return p.c.format ? launch_rows<128, true>(tk, tv, p, n_sm, wide, stream)
+                      : launch_rows<128, false>(tk, tv, p, n_sm, wide, stream);
+  return p.c.format ? launch_rows<64, true>(tk, tv, p, n_sm, wide, stream)
+                    : launch_rows<64, false>(tk, tv, p, n_sm, wide, stream);
 }
 
 }  // namespace fattn

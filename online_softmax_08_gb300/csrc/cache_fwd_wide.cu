@@ -1,9 +1,15 @@
 // cache_fwd_wide.cu -- attention over the paged 8-bit key/value cache, many query
 // rows per key/value head (pieces of prompts): tcgen05 + TMEM.
 //
-// One CTA owns 256 rows of one (sequence, key/value head): two 128-row subtiles.
-// A row is a (token, query head of the group), token-major, so all heads that
-// share a key/value head share the CTA's keys.  The structure is that of the
+// A unit is up to 256 rows of one (sequence, key/value head), in two 128-row
+// subtiles.  A row is a (token, query head of the group), token-major, so all heads
+// that share a key/value head share the unit's keys.  A CTA (one per SM) owns one
+// piece of a unit: at most max(8, all tiles of 128 keys / SMs) of its tiles.  So one
+// long sequence is spread over the machine, while units that are short against the
+// machine's share are not cut and pay for no merge.  (A persistent grid with equal
+// shares, built and measured: the loop over pieces cost the MMA warp and the
+// registers more than the better balance gave, 432 us against 271 us for 2048 tokens
+// behind 8192, G = 4.)  Per piece the structure is that of the
 // dense forward kernel: keys and values of 128 tokens at a time pass through a
 // ring of shared-memory slots, S_s = Q_s K^T lives in TMEM, the softmax warps turn
 // it into P_s in place, and O_s += P_s V accumulates in TMEM.
@@ -112,6 +118,91 @@ enum {
 };
 static_assert(8 * (B_KV_FULL + 2 * Wide<64>::STAGES) + 16 <= 256, "barrier block");
 
+// A piece of a unit: tiles [t0, t0 + max(c0, c1)) of it, of which subtile s sees the
+// first c_s.
+struct Segment {
+  int row0, n, len, b;  // the sequence
+  int h, rb;            // head, row block (tb tokens each)
+  int t0, c0, c1;
+  int part;             // -1: the whole unit; else where its rows go in the workspace
+  int on;               // 0: nothing to do
+};
+
+// sum over i < n of floor((a i + b) / m), by the Euclidean reduction of (a, m)
+__device__ __forceinline__ long long floor_sum(unsigned n, unsigned m, unsigned a, unsigned b) {
+  long long r = 0;
+  while (n > 0) {
+    r += (long long)n * (n - 1) / 2 * (a / m) + (long long)n * (b / m);
+    a %= m;
+    b %= m;
+    const unsigned long long top = (unsigned long long)a * n + b;
+    if (top < m) break;
+    n = (unsigned)(top / m);
+    b = (unsigned)(top % m);
+    const unsigned x = m;
+    m = a;
+    a = x;
+  }
+  return r;
+}
+
+// The units of one sequence: nb row blocks of tb tokens, for each of H heads.
+struct Blocks {
+  CacheSeq seq;
+  int nb, tb;
+  int causal;
+  // keys that the last row of block rb sees
+  __device__ __forceinline__ int limit(int rb) const {
+    const int l = causal ? seq.len - seq.n + min(seq.n, (rb + 1) * tb) : seq.len;
+    return max(0, l);
+  }
+  // parts of at most m keys in block rb; one that sees nothing counts as one, to be written
+  __device__ __forceinline__ int parts(int rb, unsigned m) const {
+    return max(1, (int)(((unsigned)limit(rb) + m - 1) / m));
+  }
+  // of blocks 0 .. rb - 1
+  __device__ __forceinline__ long long before(int rb, unsigned m) const {
+    if (!causal) return (long long)rb * parts(0, m);
+    long long r = 0;
+    if (rb == nb) r += parts(--rb, m);
+    const int c = seq.len - seq.n + tb;  // limit(i) = c + i tb for i < nb - 1
+    const int blind = c > 0 ? 0 : min(rb, -c / tb + 1);
+    if (rb > blind) r += floor_sum(rb - blind, m, tb, (unsigned)(c + blind * tb) + m - 1);
+    return r + blind;
+  }
+};
+__device__ __forceinline__ void set_blocks(const CacheFwdParams& p, int b, Blocks* x) {
+  x->nb = 0;
+  x->tb = p.wide_tokens;
+  x->causal = p.causal;
+  if (!cache_seq(p.c, b, &x->seq)) {
+    if (p.c.err) atomicCAS(p.c.err, 0u, (unsigned)ERR_SITE_CACHE_FWD);
+    return;
+  }
+  if (x->seq.n * p.G > p.narrow_rows) x->nb = (x->seq.n + x->tb - 1) / x->tb;
+}
+
+// log2 of the value scale of a sequence's first block, the exponent that its sums are
+// kept relative to (any reference of the scales' size will do)
+__device__ __forceinline__ float unit_base(const CacheFwdParams& p, int b, int h) {
+  const int page = p.c.block_table[(long long)b * p.c.table_width];
+  return page >= 0 && page < p.c.num_blocks ? lg2(p.c.v_scale[(long long)page * p.c.H + h]) : 0.f;
+}
+
+// Where the rows of pieces go: LSE [places, ROWS], then O [places, ROWS, d], behind the
+// records.
+struct PieceView {
+  float* lse;
+  float* o;
+};
+__device__ __forceinline__ PieceView piece_view(const CacheFwdParams& p) {
+  float* lse = reinterpret_cast<float*>(static_cast<char*>(p.wide_workspace) +
+                                        (((size_t)p.wide_ctas * sizeof(Record) + 255) & ~(size_t)255));
+  return PieceView{lse, lse + (size_t)p.wide_ctas * 2 * Wide<128>::ROWS};
+}
+
+constexpr int kMinTiles = 8;  // a piece of fewer tiles would not repay its start and merge
+
 template <int D, bool E5M2>
 __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
     cache_fwd_wide_kernel(const CacheFwdParams p) {
@@ -124,37 +215,116 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = p.G;
 
-  // Row blocks of sequence b sit at slots cu_seqlens[b] G / 256 + b and on, which
-  // is room for all of them; the later ones of a sequence, which see more keys, first.
-  const int h = (int)(blockIdx.x % (unsigned)p.c.H);
-  const long long slot = blockIdx.x / (unsigned)p.c.H;
-  const int b = warp_search(p.c.B, slot, [&](int i) {
-    return (long long)p.c.cu_seqlens[i] * G / C::ROWS + i;
-  });
-  CacheSeq seq;
-  if (!cache_seq(p.c, b, &seq)) {
-    if (threadIdx.x == 0 && p.c.err) atomicCAS(p.c.err, 0u, (unsigned)ERR_SITE_CACHE_FWD);
-    return;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  __shared__ Segment seg_slot;
+  if (warp == 0) {
+    // ---------------------------------------------------------------- which piece
+    const int B = p.c.B, H = p.c.H;
+    Blocks x;
+    long long tiles = 0;
+    for (int b0 = lane; b0 < B; b0 += 32) {
+      set_blocks(p, b0, &x);
+      if (x.nb > 0) tiles += x.before(x.nb, C::BN) * H;
+    }
+#pragma unroll
+    for (int w = 16; w > 0; w >>= 1) tiles += __shfl_xor_sync(0xffffffffu, tiles, w);
+    const long long most = max((long long)kMinTiles, (tiles + p.wide_ctas - 1) / p.wide_ctas);
+    const unsigned m = (unsigned)min(most * C::BN, 0x7fffffffLL);  // keys of a piece
+    long long pieces = 0, units = 0;  // of all sequences; then of those before
+    for (int b0 = lane; b0 < B; b0 += 32) {
+      if (B > 32) set_blocks(p, b0, &x);
+      if (x.nb > 0) {
+        pieces += x.before(x.nb, m) * H;
+        units += (long long)x.nb * H;
+      }
+    }
+#pragma unroll
+    for (int w = 16; w > 0; w >>= 1) {
+      pieces += __shfl_xor_sync(0xffffffffu, pieces, w);
+      units += __shfl_xor_sync(0xffffffffu, units, w);
+    }
+    // the grid has room for every batch whose offsets ascend
+    if (pieces > gridDim.x) {
+      if (lane == 0 && p.c.err) atomicCAS(p.c.err, 0u, (unsigned)ERR_SITE_CACHE_FWD);
+      pieces = units = 0;
+    }
+    Segment g{};
+    // records that no cut unit uses
+    const long long extra = pieces - units;
+    Record* records = reinterpret_cast<Record*>(p.wide_workspace);
+    if (lane == 0 && blockIdx.x >= extra && blockIdx.x < p.wide_ctas)
+      records[blockIdx.x] = Record{0, 0, 0, 0, 0, 0};
+    long long pos = pieces - 1 - blockIdx.x;  // the later ones, which see more keys, first
+    if (pos >= 0) {
+      long long before = 0, units_before = 0;
+      for (int b0 = 0; b0 < B; b0 += 32) {
+        long long mine = 0, own = 0;
+        if (b0 + lane < B) {
+          if (B > 32) set_blocks(p, b0 + lane, &x);
+          if (x.nb > 0) mine = x.before(x.nb, m) * H, own = (long long)x.nb * H;
+        }
+        long long upto = mine, u = own;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const long long o = __shfl_up_sync(0xffffffffu, upto, d);
+          const long long v = __shfl_up_sync(0xffffffffu, u, d);
+          if (lane >= d) upto += o, u += v;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, before + upto > pos);
+        if (past) {
+          const int src = __ffs(past) - 1;
+          before = __shfl_sync(0xffffffffu, before + upto - mine, src);
+          units_before += __shfl_sync(0xffffffffu, u - own, src);
+          g.b = b0 + src;
+          break;
+        }
+        before += __shfl_sync(0xffffffffu, upto, 31);
+        units_before += __shfl_sync(0xffffffffu, u, 31);
+      }
+      set_blocks(p, g.b, &x);
+      const int rb = warp_search(x.nb, pos - before, [&](int i) { return x.before(i, m) * H; });
+      before += x.before(rb, m) * H;
+      const int k = x.parts(rb, m), rest = (int)(pos - before);
+      const int h = rest / k, part = rest % k;
+      const long long base = before + (long long)h * k - (units_before + (long long)rb * H + h);
+      const int n_tiles = x.parts(rb, C::BN);
+      const int t0 = (int)((long long)part * n_tiles / k);
+      const int take = (int)((long long)(part + 1) * n_tiles / k) - t0;
+      // tiles that the subtiles see: up to their last row's limit
+      const int rows = min(x.tb, x.seq.n - rb * x.tb) * G;
+      auto sees = [&](int last_row) {
+        const int i = rb * x.tb + p.by_G.div(last_row);
+        const int l = p.causal ? x.seq.len - x.seq.n + i + 1 : x.seq.len;
+        return (max(0, l) + C::BN - 1) / C::BN;
+      };
+      const int n0 = sees(min(rows, C::BM) - 1), n1 = rows > C::BM ? sees(rows - 1) : 0;
+      g.row0 = x.seq.row0, g.n = x.seq.n, g.len = x.seq.len;
+      g.h = h, g.rb = rb, g.t0 = t0;
+      g.c0 = max(0, min(take, n0 - t0));
+      g.c1 = max(0, min(take, n1 - t0));
+      // A unit of k > 1 pieces owns k - 1 records and 2 (k - 1) >= k places for rows,
+      // counted over the units before it: at most one record and two places per SM
+      g.part = k > 1 ? (int)(2 * base) + part : -1;
+      g.on = 1;
+      if (lane == 0 && k > 1 && part < k - 1)
+        records[base + part] = part > 0 ? Record{0, 0, 0, 0, 0, 0}
+                                        : Record{k, rows, h, g.row0, rb * x.tb * G, (int)(2 * base)};
+    }
+    if (lane == 0) seg_slot = g;
   }
-  const int n_rows = seq.n * G;
-  if (n_rows <= p.narrow_rows) return;  // the other kernel's
-  const int n_blocks = (n_rows + C::ROWS - 1) / C::ROWS;
-  const long long rank = slot - ((long long)seq.row0 * G / C::ROWS + b);
-  if (rank < 0 || rank >= n_blocks) return;
-  const int rb = n_blocks - 1 - (int)rank;
-
-  // keys seen by row r of the sequence
-  const int seen0 = p.causal ? seq.len - seq.n + 1 : seq.len;
+  __syncthreads();
+  if (seg_slot.on == 0) return;
+  const int b = seg_slot.b, h = seg_slot.h, t0 = seg_slot.t0, rb = seg_slot.rb;
+  const int len = seg_slot.len, n_new = seg_slot.n, row0 = seg_slot.row0, part = seg_slot.part;
+  const int n_rows = min(p.wide_tokens, n_new - rb * p.wide_tokens) * G;  // of the unit
+  // keys seen by row r of the unit
+  const int seen0 = p.causal ? len - n_new + rb * p.wide_tokens + 1 : len;
   auto limit_of = [&](int r) {
-    return max(0, min(seq.len, p.causal ? seen0 + p.by_G.div(r) : seen0));
+    return max(0, min(len, p.causal ? seen0 + p.by_G.div(r) : seen0));
   };
-  const int r0_0 = rb * C::ROWS, r0_1 = r0_0 + C::BM;
-  auto tiles_for = [&](int r0) {
-    return r0 >= n_rows ? 0 : (limit_of(min(r0 + C::BM, n_rows) - 1) + C::BN - 1) / C::BN;
-  };
-  const int nt0 = tiles_for(r0_0), nt1 = tiles_for(r0_1);
+  const int nt0 = seg_slot.c0, nt1 = seg_slot.c1;
   const int n_max = max(nt0, nt1);
-  const int lim_lo = limit_of(r0_0), lim_hi = limit_of(min(r0_0 + C::ROWS, n_rows) - 1);
+  const int lim_lo = limit_of(0), lim_hi = limit_of(n_rows - 1);
 
   const uint32_t bar0 = sbase + C::OFF_BAR;
   auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
@@ -182,12 +352,7 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
     }
     *abort_flag = 0u;
     *poison = 0u;
-    float lv = 0.f;  // any reference of the scales' size will do
-    if (n_max > 0) {
-      const int page = p.c.block_table[(long long)b * p.c.table_width];
-      if (page >= 0 && page < p.c.num_blocks) lv = lg2(p.c.v_scale[(long long)page * p.c.H + h]);
-    }
-    *base_lv = lv;
+    *base_lv = n_max > 0 ? unit_base(p, b, h) : 0.f;
     fence_mbar_init();
   }
   if (warp == C::W_MMA) {
@@ -215,7 +380,7 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
     };
     auto fetch = [&](int j0) {
       Info r{-1, 0, 0.f, 0.f};
-      const int key = (j0 + (lane >> 1)) * C::BN + me * 32 + (lane & 1) * 16;
+      const int key = (t0 + j0 + (lane >> 1)) * C::BN + me * 32 + (lane & 1) * 16;
       if (key >= lim_hi) return r;
       const int page = p.c.block_table[(long long)b * p.c.table_width + (key >> p.c.block_log2)];
       if (page < 0 || page >= p.c.num_blocks) {
@@ -292,8 +457,8 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
                __all_sync(0xffffffffu, mbar_wait(kv_empty0 + 8u * kv_slot, (use - 1) & 1, wctx,
                                                  ERR_SITE_CACHE_FWD + 4));
           if (!ok) break;
-          const int key0 = j * C::BN + me * 32 + row4;
-          if (j * C::BN + me * 32 + 32 > lim_lo) {  // some row does not see all of it
+          const int key0 = (t0 + j) * C::BN + me * 32 + row4;
+          if ((t0 + j) * C::BN + me * 32 + 32 > lim_lo) {  // some row does not see all of it
             bool nan = false;
 #pragma unroll
             for (int pc = 0; pc < 2; ++pc)
@@ -416,11 +581,13 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
     regs_inc<C::REG_SOFTMAX>();
     const int s = warp >> 2;
     const int t = threadIdx.x & 127;  // row in the subtile == TMEM lane
-    const int row = (s ? r0_1 : r0_0) + t;
+    const int row = s * C::BM + t;  // of the unit
+    const long long at = (long long)row0 + rb * p.wide_tokens + p.by_G.div(row);  // packed row
+    const int hq = h * G + p.by_G.mod(row);
     const bool valid = row < n_rows;
     const int lim = valid ? limit_of(row) : 0;
     const int my_nt = s ? nt1 : nt0;
-    const int my_lo = limit_of(s ? r0_1 : r0_0);  // keys that every row of the subtile sees
+    const int my_lo = limit_of(s * C::BM);  // keys that every row of the subtile sees
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lane_off + C::TM_S + s * 128;
     const uint32_t tO = tmem + lane_off + C::TM_O + s * D;
@@ -434,8 +601,7 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
 #pragma unroll
       for (int i = 0; i < D / 8; ++i) v[i] = make_uint4(0u, 0u, 0u, 0u);
       if (valid) {
-        const uint16_t* q = p.q.p + (long long)(seq.row0 + p.by_G.div(row)) * p.q.st +
-                            (long long)(h * G + p.by_G.mod(row)) * p.q.sh;
+        const uint16_t* q = p.q.p + at * p.q.st + (long long)hq * p.q.sh;
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) v[i] = *reinterpret_cast<const uint4*>(q + 8 * i);
       }
@@ -482,7 +648,7 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
       float sv[128];
 #pragma unroll
       for (int k = 0; k < 128; ++k) sv[k] = __uint_as_float(u[k >> 5][k & 31]);
-      const int c0 = j * C::BN;
+      const int c0 = (t0 + j) * C::BN;
       if (c0 + C::BN > my_lo) {
         const int n = lim - c0;
 #pragma unroll
@@ -570,15 +736,18 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
     }
 
     // ------------------------------------------------------------ epilogue
-    uint16_t* o_row = p.o.p + (long long)(seq.row0 + p.by_G.div(row)) * p.o.st +
-                      (long long)(h * G + p.by_G.mod(row)) * p.o.sh;
     const bool has = my_nt > 0 && !(l_run == 0.f);
     const float base = *base_lv;
     const float inv = has ? 1.f / l_run : 0.f, up = ex2(base);
+    const float lse = has ? (r_run - base + lg2(l_run)) * kLn2 : -INFINITY;
     if (my_nt > 0) {
       mbar_wait(bar(B_PV_DONE + s), (my_nt - 1) & 1, wctx, ERR_SITE_CACHE_FWD + 12);
       tc_fence_after();
     }
+    // a whole unit's rows go to o as bf16, a piece's to the workspace as fp32
+    uint16_t* o_row = p.o.p + at * p.o.st + (long long)hq * p.o.sh;
+    const PieceView out = piece_view(p);
+    const size_t place = (size_t)max(part, 0) * C::ROWS + row;
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) {
       uint32_t o[32];
@@ -586,24 +755,33 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
         tmem_ld32(tO + c * 32, o);
         tmem_wait_ld(o);
       }
-      if (valid) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        o[i] = has ? __float_as_uint(__uint_as_float(o[i]) * inv * up) : 0u;
+      if (valid && part < 0) {
 #pragma unroll
         for (int q4 = 0; q4 < 4; ++q4) {
           uint4 w;
           uint32_t* x = &w.x;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float a = has ? __uint_as_float(o[q4 * 8 + 2 * e]) * inv * up : 0.f;
-            const float z = has ? __uint_as_float(o[q4 * 8 + 2 * e + 1]) * inv * up : 0.f;
-            x[e] = pack_bf16x2(a, z);
-          }
+          for (int e = 0; e < 4; ++e)
+            x[e] = pack_bf16x2(__uint_as_float(o[q4 * 8 + 2 * e]),
+                               __uint_as_float(o[q4 * 8 + 2 * e + 1]));
           *reinterpret_cast<uint4*>(o_row + c * 32 + q4 * 8) = w;
         }
+      } else if (valid) {
+#pragma unroll
+        for (int q4 = 0; q4 < 8; ++q4)
+          *reinterpret_cast<uint4*>(out.o + place * D + c * 32 + q4 * 4) =
+              make_uint4(o[q4 * 4], o[q4 * 4 + 1], o[q4 * 4 + 2], o[q4 * 4 + 3]);
       }
     }
-    if (valid)
-      p.lse[(long long)(h * G + p.by_G.mod(row)) * p.c.total + seq.row0 + p.by_G.div(row)] =
-          has ? (r_run - base + lg2(l_run)) * kLn2 : -INFINITY;
+    if (valid) {
+      if (part < 0)
+        p.lse[(long long)hq * p.c.total + at] = lse;
+      else
+        out.lse[place] = lse;
+    }
     __syncwarp();
   }
 
@@ -616,17 +794,25 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
   if (*poison && warp < 8) {
     // rare: values that were NaN in keys that some rows see and others do not; they
     // were left out of the sums, and here reach the rows that do see them
-    const int row = r0_0 + (int)threadIdx.x;
+    const int row = (int)threadIdx.x;
     if (row < n_rows) {
-      const int lim = limit_of(row), bs = p.c.block_size;
-      uint16_t* o_row = p.o.p + (long long)(seq.row0 + p.by_G.div(row)) * p.o.st +
-                        (long long)(h * G + p.by_G.mod(row)) * p.o.sh;
-      for (int key = lim_lo & ~15; key < lim; ++key) {
+      const int bs = p.c.block_size;
+      const long long at = (long long)row0 + rb * p.wide_tokens + p.by_G.div(row);
+      uint16_t* o_row = p.o.p + at * p.o.st + (long long)(h * G + p.by_G.mod(row)) * p.o.sh;
+      float* part_row = piece_view(p).o + ((size_t)max(part, 0) * C::ROWS + row) * D;
+      const int from = max(t0 * C::BN, lim_lo & ~31);  // whole 32-row pieces were cleared
+      const int to = min(limit_of(row), (t0 + n_max) * C::BN);
+      for (int key = from; key < to; ++key) {
         const int page = p.c.block_table[(long long)b * p.c.table_width + (key >> p.c.block_log2)];
         if (page < 0 || page >= p.c.num_blocks) continue;
         const uint8_t* v = p.c.v + (((long long)page * p.c.H + h) * bs + (key & (bs - 1))) * D;
         for (int c = 0; c < D; ++c)
-          if ((v[c] & 0x7fu) >= (E5M2 ? 0x7cu : 0x7fu)) o_row[c] = 0x7fffu;
+          if ((v[c] & 0x7fu) >= (E5M2 ? 0x7cu : 0x7fu)) {
+            if (part < 0)
+              o_row[c] = 0x7fffu;
+            else
+              part_row[c] = __uint_as_float(0x7fffffffu);
+          }
       }
     }
   }
@@ -647,14 +833,18 @@ cudaError_t launch(const CacheFwdParams& p, cudaStream_t stream) {
     return fa.numRegs >= C::REG_LAUNCH ? cudaSuccess : cudaErrorInvalidConfiguration;
   });
   if (e != cudaSuccess) return e;
-  const int G = p.G;
-  const long long units = ((long long)p.c.total * G / C::ROWS + p.c.B) * p.c.H;
-  if (units > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  cache_fwd_wide_kernel<D, E5M2><<<(unsigned)units, C::THREADS, C::SMEM, stream>>>(p);
+  // room for every unit, and for the cuts: a unit of t tiles has at most
+  // 1 + t / (all tiles / SMs) pieces
+  const long long ctas =
+      ((long long)p.c.total / p.wide_tokens + p.c.B) * p.c.H + p.wide_ctas;
+  if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  cache_fwd_wide_kernel<D, E5M2><<<(unsigned)ctas, C::THREADS, C::SMEM, stream>>>(p);
   return cudaGetLastError();
 }
 
 }  // namespace
+
+int cache_fwd_wide_rows() { return Wide<128>::ROWS; }
 
 cudaError_t launch_cache_fwd_wide(const CacheFwdParams& p, cudaStream_t stream) {
   if (p.c.d == 128) return p.c.format ? launch<128, true>(p, stream) : launch<128, false>(p, stream);

@@ -160,7 +160,18 @@ struct CacheFwdParams {
   float scale_log2;  // scale * log2(e)
   int narrow_rows;   // sequences with more query rows per key/value head (tokens x grouped heads)
                      // than this go to the 256-row tcgen05 kernel, the others to the split one
-  void* workspace;
+  int wide_tokens;   // tokens per row block of the 256-row kernel: 256 / G
+  int wide_ctas;     // CTAs of it that run at a time: one per SM
+  void* workspace;   // of the split kernel
+  void* wide_workspace;
+};
+
+// What an attention kernel leaves for the merge: a unit that was cut into `parts`
+// pieces (0: none), its rows, and (256-row kernel) the place of its first piece.  A
+// workspace holds one record per CTA (256-row kernel: per SM), then LSE [n, 2, R] and
+// O [n, 2, R, d] of the pieces, fp32.
+struct Record {
+  int parts, rows, h, row0, first_row, place;
 };
 
 // Sequence b of a cache call: n tokens at packed rows [row0, row0 + n), the
@@ -231,10 +242,11 @@ cudaError_t launch_cache_append(const CacheParams& c, const TokenView& k, const 
                                 cudaStream_t stream);
 cudaError_t launch_cache_read(const CacheParams& c, const TokenView& k, const TokenView& v,
                               cudaStream_t stream);
-size_t cache_fwd_workspace(const CacheParams& c, int Hq, int n_sm);
+size_t cache_fwd_workspace(const CacheParams& c, int G, int n_sm);
 // tk, tv: maps of the codes, {d, block_size, num_blocks * H}, boxes of 16 tokens
 cudaError_t launch_cache_fwd(const CUtensorMap& tk, const CUtensorMap& tv, const CacheFwdParams& p,
                              int n_sm, cudaStream_t stream);
+int cache_fwd_wide_rows();  // rows per unit of the 256-row kernel
 cudaError_t launch_cache_fwd_wide(const CacheFwdParams& p, cudaStream_t stream);
 
 cudaError_t launch_bwd_preprocess(const void* o, const void* dout, float* delta, float* dq_acc,

@@ -12,6 +12,7 @@ binding raises: there is no fallback path.
 import contextlib
 import ctypes
 import os
+import struct
 import threading
 import typing
 
@@ -29,17 +30,11 @@ _vp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_
 _ll = ctypes.c_longlong
 
 
-class _CCache(ctypes.Structure):  # fattn_cache
-    _fields_ = [("k", _vp), ("v", _vp), ("k_scale", _vp), ("v_scale", _vp), ("num_blocks", _i),
-                ("H", _i), ("block_size", _i), ("d", _i), ("format", _i)]
+# fattn_cache and fattn_cache_batch, packed; a bytes object is passed by its address
+_pack_cache = struct.Struct("@4P5i").pack
+_pack_batch = struct.Struct("@3P4i").pack
+_cp = _bp = ctypes.c_char_p
 
-
-class _CBatch(ctypes.Structure):  # fattn_cache_batch
-    _fields_ = [("block_table", _vp), ("lens", _vp), ("cu_seqlens", _vp), ("B", _i),
-                ("table_width", _i), ("total", _i), ("max_seqlen", _i)]
-
-
-_cp, _bp = ctypes.POINTER(_CCache), ctypes.POINTER(_CBatch)
 SIGNATURES = {
     "fattn_fwd": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _f, _i, _vp]),
     "fattn_fwd_ex": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _f, _i, _vp, _vp]),
@@ -80,6 +75,15 @@ TESTING_SIGNATURES = {
 
 _lock = threading.Lock()
 _lib = None
+
+
+def _raw_stream(dev):
+    """The handle of device `dev`'s current stream."""
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+# the same without the Stream object, which costs as much as a short launch
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
 
 
 class FattnError(RuntimeError):
@@ -410,12 +414,11 @@ def new_cache(num_blocks, heads, block_size, d, dtype=torch.float8_e4m3fn, devic
     return KVCache(k, v, ks, vs)
 
 
-def _cache_args(cache, batch):
-    """The C descriptors of a cache and a batch, their tensors checked."""
+def _refuse_cache(cache, batch):
+    """Say what _cache_args found wrong."""
     k, v, ks, vs = cache
-    table, lens, cu, total, max_seqlen = batch
-    shape, dev = k.shape, k.device
-    if len(shape) != 4 or v.shape != shape or ks.shape != shape[:2] or vs.shape != shape[:2]:
+    table, lens, cu = batch[:3]
+    if k.dim() != 4 or v.shape != k.shape or ks.shape != k.shape[:2] or vs.shape != k.shape[:2]:
         raise ValueError("expected k, v [num_blocks, H, block_size, d] and scales [num_blocks, H]")
     if k.dtype not in CACHE_FORMATS or v.dtype != k.dtype or ks.dtype != torch.float32 or \
             vs.dtype != torch.float32:
@@ -424,97 +427,136 @@ def _cache_args(cache, batch):
         raise ValueError("expected block_table [B, width], lens [B], cu_seqlens [B + 1]")
     if table.dtype != torch.int32 or lens.dtype != torch.int32 or cu.dtype != torch.int32:
         raise ValueError("expected int32 block_table, lens and cu_seqlens")
-    for t in (k, v, ks, vs, table, lens, cu):
-        if not t.is_contiguous() or t.device != dev:
-            raise ValueError("expected contiguous tensors on one device")
-    if dev.type != "cuda":
-        raise ValueError("expected device tensors, got %s" % dev)
-    return (_CCache(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), shape[0], shape[1],
-                    shape[2], shape[3], CACHE_FORMATS[k.dtype]),
-            _CBatch(table.data_ptr(), lens.data_ptr(), cu.data_ptr(), table.shape[0],
-                    table.shape[1], total, max_seqlen))
+    raise ValueError("expected contiguous tensors on one CUDA device")
 
 
-def _packed(x, total, heads, d, device):
+def _cache_args(cache, batch):
+    """The C descriptors of a cache and a batch, their tensors checked, with the
+    device index, H and d.  (A decoding step's calls are as short as the launches
+    they make, so the checks take few attribute reads.)"""
+    k, v, ks, vs = cache
+    table, lens, cu, total, max_seqlen = batch
+    shape, dtype, dev = k.shape, k.dtype, k.get_device()
+    fmt = CACHE_FORMATS.get(dtype)
+    if len(shape) != 4 or fmt is None or dev < 0 or table.dim() != 2:
+        _refuse_cache(cache, batch)
+    B, width = table.shape
+    scales = shape[:2]
+    f32, i32 = torch.float32, torch.int32
+    if not (v.shape == shape and ks.shape == scales and vs.shape == scales and lens.dim() == 1
+            and lens.numel() == B and cu.dim() == 1 and cu.numel() == B + 1
+            and v.dtype is dtype and ks.dtype is f32 and vs.dtype is f32 and table.dtype is i32
+            and lens.dtype is i32 and cu.dtype is i32
+            and k.is_contiguous() and v.is_contiguous() and ks.is_contiguous()
+            and vs.is_contiguous() and table.is_contiguous() and lens.is_contiguous()
+            and cu.is_contiguous()
+            and v.get_device() == dev and ks.get_device() == dev and vs.get_device() == dev
+            and table.get_device() == dev and lens.get_device() == dev and cu.get_device() == dev):
+        _refuse_cache(cache, batch)
+    nb, H, bs, d = shape
+    return (_pack_cache(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), nb, H, bs, d, fmt),
+            _pack_batch(table.data_ptr(), lens.data_ptr(), cu.data_ptr(), B, width, total,
+                        max_seqlen), dev, H, d)
+
+
+def _packed(x, total, heads, d, dev):
     """Pointer and token and head strides of a bf16 [total, heads, d] tensor."""
-    if x.shape != (total, heads, d) or x.dtype != torch.bfloat16 or x.device != device or \
-            (d > 1 and x.stride(2) != 1):
-        raise ValueError("expected a bf16 [%d, %d, %d] tensor on %s with a contiguous last axis"
-                         % (total, heads, d, device))
-    return x.data_ptr(), x.stride(0), x.stride(1)
+    st = x.stride()
+    if len(st) != 3 or x.shape != (total, heads, d) or x.dtype is not torch.bfloat16 or \
+            x.get_device() != dev or st[2] != 1:
+        raise ValueError("expected a bf16 [%d, %d, %d] tensor on device %d with a contiguous last "
+                         "axis" % (total, heads, d, dev))
+    return x.data_ptr(), st[0], st[1]
 
 
 @contextlib.contextmanager
-def _on(device, stream):
-    """Work and allocations on `stream` of `device` (None: its current stream)."""
-    with torch.cuda.device(device):
+def _on(dev, stream):
+    """Work and allocations on `stream` of device `dev` (None: its current stream)."""
+    with torch.cuda.device(dev):
         if stream is None:
             yield
             return
         if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream, device=device)
+            stream = torch.cuda.ExternalStream(stream, device=dev)
         with torch.cuda.stream(stream):
             yield
 
 
-def _cache_call(device, stream, call):
-    """call(raw stream) on the cache's device; the usual case (its current stream,
-    the current device) without a context switch."""
-    if stream is None and torch.cuda.current_device() == device.index:
-        return call(torch.cuda.current_stream(device).cuda_stream)
-    with _on(device, stream):
-        return call(torch.cuda.current_stream(device).cuda_stream)
+def _elsewhere(dev, stream):
+    """Whether a call has to change the current device or stream first."""
+    return stream is not None or torch.cuda.current_device() != dev
 
 
 def cache_append(k, v, cache, batch, stream=None):
     """Quantise new tokens' k, v (bf16 [total, H, d], any token and head strides)
     into the cache."""
-    c, b = _cache_args(cache, batch)
-    dev = cache.k.device
-    ka, va = _packed(k, b.total, c.H, c.d, dev), _packed(v, b.total, c.H, c.d, dev)
-    _cache_call(dev, stream, lambda s: _check("fattn_cache_append", load().fattn_cache_append(
-        c, b, *ka, *va, s)))
+    c, b, dev, H, d = _cache_args(cache, batch)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return cache_append(k, v, cache, batch)
+    total = batch[3]
+    kp, kt, kh = _packed(k, total, H, d, dev)
+    vp, vt, vh = _packed(v, total, H, d, dev)
+    st = (_lib or load()).fattn_cache_append(c, b, kp, kt, kh, vp, vt, vh, _raw_stream(dev))
+    if st:
+        raise FattnError("fattn_cache_append", st)
 
 
 def cache_read(cache, batch, out=None, stream=None):
     """k, v (bf16 [total, H, d]) of the batch's tokens, read back from the cache;
     out: a pair of tensors to write to."""
-    c, b = _cache_args(cache, batch)
-    dev = cache.k.device
+    c, b, dev, H, d = _cache_args(cache, batch)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return cache_read(cache, batch, out)
+    total = batch[3]
+    if out is None:
+        shape = (total, H, d)
+        k = torch.empty(shape, dtype=torch.bfloat16, device=cache[0].device)
+        v = torch.empty_like(k)
+    else:
+        k, v = out
+    kp, kt, kh = _packed(k, total, H, d, dev)
+    vp, vt, vh = _packed(v, total, H, d, dev)
+    st = (_lib or load()).fattn_cache_read(c, b, kp, kt, kh, vp, vt, vh, _raw_stream(dev))
+    if st:
+        raise FattnError("fattn_cache_read", st)
+    return k, v
 
-    def call(s):
-        k, v = out if out is not None else (torch.empty((b.total, c.H, c.d), dtype=torch.bfloat16,
-                                                        device=dev) for _ in range(2))
-        _check("fattn_cache_read", load().fattn_cache_read(
-            c, b, *_packed(k, b.total, c.H, c.d, dev), *_packed(v, b.total, c.H, c.d, dev), s))
-        return k, v
 
-    return _cache_call(dev, stream, call)
+_ws_bytes = {}  # fattn_cache_fwd_workspace_bytes by all of its arguments
 
 
 def cache_forward(q, cache, batch, scale, causal, out=None, workspace=None, stream=None):
     """O (bf16 [total, Hq, d]) and LSE (fp32 [Hq, total]) of the batch's queries q
     (bf16 [total, Hq, d], any token and head strides) over their sequences in the
-    cache.  out: a tensor to write O to."""
-    c, b = _cache_args(cache, batch)
-    dev = cache.k.device
+    cache.  out: a tensor to write O to.  workspace: None (a torch allocation) or a
+    device tensor."""
+    c, b, dev, H, d = _cache_args(cache, batch)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return cache_forward(q, cache, batch, scale, causal, out, workspace)
     if q.dim() != 3:
         raise ValueError("expected q [total, Hq, d]")
-    Hq = q.shape[1]
-    qa = _packed(q, b.total, Hq, c.d, dev)
-
-    def call(s):
-        lib = load()
-        o = out if out is not None else torch.empty((b.total, Hq, c.d), dtype=torch.bfloat16,
-                                                    device=dev)
-        lse = torch.empty((Hq, b.total), dtype=torch.float32, device=dev)
-        ws = workspace
-        if ws is None:
-            ws = torch.empty(max(int(lib.fattn_cache_fwd_workspace_bytes(c, b, Hq)), 256),
-                             dtype=torch.uint8, device=dev)
-        _check("fattn_cache_fwd", lib.fattn_cache_fwd(
-            c, b, *qa, *_packed(o, b.total, Hq, c.d, dev), lse.data_ptr(), Hq, float(scale),
-            int(bool(causal)), ws.data_ptr(), ws.numel() * ws.element_size(), s))
-        return o, lse
-
-    return _cache_call(dev, stream, call)
+    total, Hq = batch[3], q.shape[1]
+    qp, qt, qh = _packed(q, total, Hq, d, dev)
+    lib = _lib or load()
+    on = q.device
+    o = torch.empty((total, Hq, d), dtype=torch.bfloat16, device=on) if out is None else out
+    lse = torch.empty((Hq, total), dtype=torch.float32, device=on)
+    if workspace is None:
+        key = (dev, cache[0].shape, batch[0].shape, total, batch[4], Hq)
+        nbytes = _ws_bytes.get(key)
+        if nbytes is None:
+            if len(_ws_bytes) > 4096:
+                _ws_bytes.clear()
+            nbytes = _ws_bytes[key] = int(lib.fattn_cache_fwd_workspace_bytes(c, b, Hq))
+        workspace = torch.empty((max(nbytes, 256),), dtype=torch.uint8, device=on)
+    else:
+        nbytes = workspace.numel() * workspace.element_size()
+    op, ot, oh = _packed(o, total, Hq, d, dev)
+    st = lib.fattn_cache_fwd(c, b, qp, qt, qh, op, ot, oh, lse.data_ptr(), Hq, scale,
+                             1 if causal else 0, workspace.data_ptr(), nbytes, _raw_stream(dev))
+    if st:
+        raise FattnError("fattn_cache_fwd", st)
+    return o, lse

@@ -6,6 +6,7 @@ import torch
 from online_softmax_08_gb300 import build as fbuild
 from online_softmax_08_gb300 import fattn
 
+# The descriptors are packed as the C structs are laid out (native alignment).
 A = 1 << 20  # 256-byte aligned, never dereferenced
 INVALID, UNSUPPORTED, CUDA, WORKSPACE = 1, 2, 3, 4
 
@@ -19,13 +20,13 @@ def lib():
 def _cache(**kw):
     f = dict(k=A, v=A, k_scale=A, v_scale=A, num_blocks=10, H=4, block_size=16, d=64, format=0)
     f.update(kw)
-    return fattn._CCache(**f)
+    return fattn._pack_cache(*f.values())
 
 
 def _batch(**kw):
     f = dict(block_table=A, lens=A, cu_seqlens=A, B=2, table_width=4, total=8, max_seqlen=5)
     f.update(kw)
-    return fattn._CBatch(**f)
+    return fattn._pack_batch(*f.values())
 
 
 def _append(lib, c, b, k=A, kst=256, ksh=64, v=A, vst=256, vsh=64):
@@ -41,13 +42,13 @@ def _fwd(lib, c, b, q=A, qst=512, qsh=64, o=A, ost=512, osh=64, lse=A, Hq=8, sca
     return lib.fattn_cache_fwd(c, b, q, qst, qsh, o, ost, osh, lse, Hq, scale, 1, ws, nbytes, None)
 
 
-BAD_CACHE = [(dict(k=None), INVALID), (dict(v=A + 8), INVALID), (dict(k_scale=None), INVALID),
+BAD_CACHE = [(dict(k=0), INVALID), (dict(v=A + 8), INVALID), (dict(k_scale=0), INVALID),
              (dict(v_scale=A + 4), INVALID), (dict(num_blocks=0), INVALID), (dict(H=0), INVALID),
              (dict(H=1 << 17), INVALID), (dict(block_size=48), UNSUPPORTED),
              (dict(block_size=0), UNSUPPORTED), (dict(d=96), UNSUPPORTED),
              (dict(format=2), UNSUPPORTED)]
-BAD_BATCH = [(dict(block_table=None), INVALID), (dict(lens=A + 2), INVALID),
-             (dict(cu_seqlens=None), INVALID), (dict(B=0), INVALID), (dict(table_width=0), INVALID),
+BAD_BATCH = [(dict(block_table=0), INVALID), (dict(lens=A + 2), INVALID),
+             (dict(cu_seqlens=0), INVALID), (dict(B=0), INVALID), (dict(table_width=0), INVALID),
              (dict(total=-1), INVALID), (dict(max_seqlen=9), INVALID),
              (dict(max_seqlen=-1), INVALID), (dict(table_width=1 << 27), INVALID),
              (dict(total=(1 << 31) - 1, max_seqlen=1), INVALID), (dict(B=1 << 25), INVALID)]

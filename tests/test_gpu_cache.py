@@ -561,7 +561,7 @@ def test_workspace_inside_sentinels():
     c = Case([(1, 900), (5, 300), (70, 10)], H, d, 64).fill()
     q = _bf16(c.rng, (c.T, H * G, d))
     cache, batch = c.on_device()
-    cc, bb = fattn._cache_args(cache, batch)
+    cc, bb = fattn._cache_args(cache, batch)[:2]
     need = int(fattn.load().fattn_cache_fwd_workspace_bytes(cc, bb, H * G))
     buf = torch.full((need + 1024,), 0xa5, dtype=torch.uint8, device=DEV)
     ws = buf[512:512 + need]
