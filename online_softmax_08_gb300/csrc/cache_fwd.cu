@@ -4,14 +4,15 @@
 // The mathematics.  With codes k, v and scales ks, vs of key j's block, in base 2:
 //   x_j = scale log2(e) ks_j (q . k_j),   O = sum_j 2^x_j vs_j v_j / sum_j 2^x_j.
 // The value scale is folded into the exponent: y_j = x_j + log2 vs_j, and with a
-// reference m >= max y - 7 carried along the keys (the running maximum of the
-// online softmax, moved lazily)
-//   acc = sum_j p_j v_j,  p_j = 2^(y_j - m + 8),   l = sum_j p_j 2^(b - log2 vs_j)
+// reference r carried along the keys (the running maximum of the online softmax,
+// less 8, moved when a y exceeds it by more than 15)
+//   acc = sum_j p_j v_j,  p_j = 2^(y_j - r),   l = sum_j p_j 2^(b - log2 vs_j)
 // where b is the log2 vs of the first block: O = 2^b acc / l and
-// LSE = ln2 (m - 8 - b + log2 l).  So blocks of different scales need no rescale
-// of acc, and the weights p_j can be held in fp16: they lie below 2^15, the
-// largest at or above 2^8, so weights down to 2^-22 of it keep 11 bits and
-// what is flushed lies below 2^-33 of it.  Codes are exact in fp16, q is (each
+// LSE = ln2 (r - b + log2 l).  So blocks of different scales need no rescale of
+// acc, and the weights p_j can be held in fp16: they lie at or below 2^15, the
+// largest at or above 2^8, so weights down to 2^-22 of it keep 11 bits and what is
+// flushed lies below 2^-33 of it.  (Where |y| >= 2^22 r is the maximum itself, as 8
+// is then too near its rounding.)  Codes are exact in fp16, q is (each
 // row is multiplied by the power of two that brings its largest element to
 // [2^14, 2^15)), sums and statistics are fp32.
 //
@@ -29,7 +30,8 @@
 // product's layout to the second's by movmatrix.
 //
 // Work split.  A unit is (sequence, key/value head, block of R query rows); its
-// keys come in chunks of 64, one 16-key tile for each of the CTA's four warps.
+// keys come in chunks, one tile of 16 keys (d = 64: 32) for each of the CTA's four
+// warps.
 // The chunks of all units, in order, are cut into equal contiguous shares, one
 // per CTA of a grid that fills the machine once, so ragged batches load every
 // SM alike and no length is needed on the host.  A unit that lies inside one
@@ -48,27 +50,31 @@ namespace fattn {
 namespace {
 
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kOff = 8.f;   // p = 2^(y - m + kOff)
-constexpr float kLazy = 7.f;  // the reference moves when a y exceeds it by more; kOff + kLazy < 16
+constexpr float kOff = 8.f;    // the reference lies this far below the running maximum
+constexpr float kRoom = 15.f;  // and moves when a y exceeds it by more
+constexpr float kFar = 4194304.f;
 constexpr int kWarps = 4;
-constexpr int kTile = 16;               // keys per warp tile
-constexpr int kChunk = kWarps * kTile;  // keys per CTA step
 
 template <int D, int NT_>
 struct Dec {
   static constexpr int NT = NT_;
   static constexpr int R = 8 * NT;                // query rows per unit
-  static constexpr int TILE = kTile * D;          // bytes
+  static constexpr int PARTS = D == 128 ? 1 : 2;  // of 16 keys in a warp's tile (4 KB with values)
+  static constexpr int KEYS = 16 * PARTS;
+  static constexpr int CHUNK = kWarps * KEYS;     // keys per CTA step
+  static constexpr int PART = 16 * D;             // bytes of 16 keys or values: one TMA box
+  static constexpr int TILE = KEYS * D;
   static constexpr int STAGE = 2 * TILE;          // keys and values
-  static constexpr int ST = D == 64 ? 6 : NT == 1 ? 3 : 4;  // ring slots per warp
+  static constexpr int ST = D == 64 && NT == 1 ? 4 : D == 128 && NT == 2 ? 4 : 3;  // ring slots per warp
   static constexpr int OFF_RED = kWarps * ST * STAGE;
-  static constexpr int OFF_STAT = OFF_RED + kWarps * R * D * 4;  // behind the warps' results
+  static constexpr int BUFS = kWarps;             // where the warps' results meet
+  static constexpr int OFF_SCL = OFF_RED + BUFS * R * D * 4;  // [warps][ST] scales of a tile
+  static constexpr int OFF_STAT = OFF_SCL + kWarps * ST * 16;
   static constexpr int OFF_BAR = OFF_STAT + kWarps * R * 4;
   static constexpr int SMEM = OFF_BAR + kWarps * ST * 8 + 16 + 1024;
   static constexpr int CTAS = NT == 1 || D == 64 ? 3 : 2;    // per SM
 };
 
-constexpr int kNarrowRows = 64;
 constexpr int kWideMerge = 8;  // merge blocks per CTA of the 256-row kernel
 
 // A position in the list of all chunks: chunk ch of unit (sequence b, head h, row
@@ -78,7 +84,8 @@ struct Cursor {
   int nch, nrb;
   CacheSeq seq;
 };
-__device__ __forceinline__ void set_seq(const CacheFwdParams& p, int R, int b, int row0, int end,
+template <typename C>
+__device__ __forceinline__ void set_seq(const CacheFwdParams& p, int b, int row0, int end,
                                         int len, Cursor* c) {
   c->b = b;
   c->nch = c->nrb = 0;
@@ -88,13 +95,15 @@ __device__ __forceinline__ void set_seq(const CacheFwdParams& p, int R, int b, i
   }
   const int rows = c->seq.n * p.G;
   if (rows == 0 || rows > p.narrow_rows) return;  // (the other kernel's)
-  c->nch = max(1, (c->seq.len + kChunk - 1) / kChunk);
-  c->nrb = (rows + R - 1) / R;
+  c->nch = max(1, (c->seq.len + C::CHUNK - 1) / C::CHUNK);
+  c->nrb = (rows + C::R - 1) / C::R;
 }
-__device__ __forceinline__ void load_seq(const CacheFwdParams& p, int R, int b, Cursor* c) {
-  set_seq(p, R, b, p.c.cu_seqlens[b], p.c.cu_seqlens[b + 1], p.c.lens[b], c);
+template <typename C>
+__device__ __forceinline__ void load_seq(const CacheFwdParams& p, int b, Cursor* c) {
+  set_seq<C>(p, b, p.c.cu_seqlens[b], p.c.cu_seqlens[b + 1], p.c.lens[b], c);
 }
-__device__ __forceinline__ void advance(const CacheFwdParams& p, int R, Cursor* c, int by) {
+template <typename C>
+__device__ __forceinline__ void advance(const CacheFwdParams& p, Cursor* c, int by) {
   c->ch += by;
   while (c->ch >= c->nch) {
     c->ch -= c->nch;
@@ -109,7 +118,7 @@ __device__ __forceinline__ void advance(const CacheFwdParams& p, int R, Cursor* 
         c->nch = 0x7fffffff;  // behind the last chunk
         return;
       }
-      load_seq(p, R, b, c);
+      load_seq<C>(p, b, c);
     } while (c->nch == 0);
   }
 }
@@ -159,7 +168,7 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
   uint8_t* smem = smem_raw + (sbase - raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  float* red = reinterpret_cast<float*>(smem + C::OFF_RED);    // [warps][R][D]
+  float* red = reinterpret_cast<float*>(smem + C::OFF_RED);    // [BUFS][R][D]
   float* stat = reinterpret_cast<float*>(smem + C::OFF_STAT);  // [warps][R]
   const uint32_t bar0 = sbase + C::OFF_BAR + 8u * (uint32_t)(warp * C::ST);
   volatile uint32_t* abort_flag =
@@ -191,9 +200,9 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
     mine = 0;
     if (b0 + lane < B) {
       if (b0 == 0)
-        set_seq(p, R, lane, first_row0, first_end, first_len, &cur);
+        set_seq<C>(p, lane, first_row0, first_end, first_len, &cur);
       else
-        load_seq(p, R, b0 + lane, &cur);
+        load_seq<C>(p, b0 + lane, &cur);
       mine = chunks(cur);
     }
     total += mine;
@@ -211,7 +220,7 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
       if (B > 32) {
         mine = 0;
         if (b0 + lane < B) {
-          load_seq(p, R, b0 + lane, &cur);
+          load_seq<C>(p, b0 + lane, &cur);
           mine = chunks(cur);
         }
       }
@@ -249,55 +258,81 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
   __syncthreads();  // barriers initialised
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // ---------------------------------------------------------------- tile info, 32 ahead
-  // Lane i of a set holds tile i of 32: its block (-1: no keys there) and scales.
+  // ---------------------------------------------------------------- tile info, 32 at a time
+  // Lane i holds tile i of a set of 32: the blocks of its parts of 16 keys (-1: no keys
+  // there) and their scales.
   struct Info {
-    int slice;  // page * H + h, -1: nothing to load
-    int row;    // first row in the block
-    float ks, vs;
+    int slice[2];  // page * H + h, of each part
+    int row;       // of the first key in its block
+    float ks[2], vs[2];
   };
   const int bs = p.c.block_size;
   auto fetch = [&](Cursor at, int f0) {  // tiles f0 .. f0 + 31, `at` being tile f0
-    Info r{-1, 0, 0.f, 0.f};
+    Info r{{-1, -1}, 0, {0.f, 0.f}, {0.f, 0.f}};
     if (f0 + lane >= F) return r;
-    advance(p, R, &at, lane);
-    const int key = at.ch * kChunk + warp * kTile;
-    if (key >= at.seq.len) return r;
-    const int page = p.c.block_table[(long long)at.b * p.c.table_width + (key >> p.c.block_log2)];
-    if (page < 0 || page >= p.c.num_blocks) {
-      if (p.c.err) atomicCAS(p.c.err, 0u, (unsigned)ERR_SITE_CACHE_FWD + 1);
-      return r;
-    }
-    r.slice = page * p.c.H + at.h;
+    advance<C>(p, &at, lane);
+    const int key = at.ch * C::CHUNK + warp * C::KEYS;
     r.row = key & (bs - 1);
-    r.ks = p.c.k_scale[r.slice];  // not waited for here
-    r.vs = p.c.v_scale[r.slice];
+    const int* table = p.c.block_table + (long long)at.b * p.c.table_width;
+#pragma unroll
+    for (int i = 0; i < C::PARTS; ++i)
+      if (key + 16 * i < at.seq.len) {
+        const int page = table[(key + 16 * i) >> p.c.block_log2];
+        if (page < 0 || page >= p.c.num_blocks) {
+          if (p.c.err) atomicCAS(p.c.err, 0u, (unsigned)ERR_SITE_CACHE_FWD + 1);
+        } else {
+          r.slice[i] = page * p.c.H + at.h;
+          r.ks[i] = p.c.k_scale[r.slice[i]];  // not waited for here
+          r.vs[i] = p.c.v_scale[r.slice[i]];
+        }
+      }
     return r;
   };
   Cursor ahead = cur;
-  Info now = fetch(ahead, 0), next{-1, 0, 0.f, 0.f};
-  if (F > 32) {
-    advance(p, R, &ahead, 32);
-    next = fetch(ahead, 32);
-  }
+  int set = 0;  // the one that `info` holds
+  Info info = fetch(ahead, 0);
+  unsigned live0 = __ballot_sync(0xffffffffu, info.slice[0] >= 0);
+  unsigned live1 = C::PARTS == 2 ? __ballot_sync(0xffffffffu, info.slice[1] >= 0) : 0u;
+  unsigned now0 = live0, now1 = live1;  // of the set being consumed
+  auto next_set = [&]() {
+    advance<C>(p, &ahead, 32);
+    ++set;
+    info = fetch(ahead, 32 * set);
+    live0 = __ballot_sync(0xffffffffu, info.slice[0] >= 0);
+    if (C::PARTS == 2) live1 = __ballot_sync(0xffffffffu, info.slice[1] >= 0);
+  };
 
-  int fi = 0;                    // next tile to load
+  int fi = 0;                     // next tile to load
   uint32_t issued = 0, done = 0;  // live tiles loaded and consumed
-  auto issue = [&](int f) {      // keep the ring full while consuming tile f
-    while (fi < F && issued - done < (uint32_t)C::ST && (fi >> 5) <= (f >> 5) + 1) {
-      const bool in_now = (fi >> 5) == (f >> 5);
-      const int slice = __shfl_sync(0xffffffffu, in_now ? now.slice : next.slice, fi & 31);
-      const int row = __shfl_sync(0xffffffffu, in_now ? now.row : next.row, fi & 31);
-      ++fi;
-      if (slice < 0) continue;
-      if (lane == 0) {
-        const uint32_t slot = issued % C::ST;
-        const uint32_t bar = bar0 + 8u * slot, dst = ring + slot * C::STAGE;
-        mbar_arrive_expect_tx(bar, C::STAGE);
-        tma_load_3d(dst, &tm_k, bar, 0, row, slice);
-        tma_load_3d(dst + C::TILE, &tm_v, bar, 0, row, slice);
+  const uint32_t scl0 = sbase + C::OFF_SCL + (uint32_t)(warp * C::ST) * 16u;
+  auto issue = [&](int f) {       // keep the ring full while consuming tile f
+    while (fi < F && issued - done < (uint32_t)C::ST) {
+      if ((fi >> 5) > set) {
+        if (set > (f >> 5)) break;  // at most one set ahead
+        next_set();
       }
-      ++issued;
+      const unsigned bit = 1u << (fi & 31);
+      if ((live0 | live1) & bit) {
+        if (lane == (fi & 31)) {
+          const uint32_t slot = issued % C::ST;
+          const uint32_t bar = bar0 + 8u * slot, dst = ring + slot * C::STAGE;
+          st_shared_v4(scl0 + slot * 16u, __float_as_uint(info.ks[0]), __float_as_uint(info.ks[1]),
+                       __float_as_uint(info.vs[0]), __float_as_uint(info.vs[1]));
+          const bool l0 = info.slice[0] >= 0, l1 = C::PARTS == 2 && info.slice[1] >= 0;
+          mbar_arrive_expect_tx(bar, (uint32_t)(l0 + l1) * 2u * C::PART);
+          if (l0) {
+            tma_load_3d(dst, &tm_k, bar, 0, info.row, info.slice[0]);
+            tma_load_3d(dst + C::TILE, &tm_v, bar, 0, info.row, info.slice[0]);
+          }
+          if (l1) {
+            const int row = (info.row + 16) & (bs - 1);
+            tma_load_3d(dst + C::PART, &tm_k, bar, 0, row, info.slice[1]);
+            tma_load_3d(dst + C::TILE + C::PART, &tm_v, bar, 0, row, info.slice[1]);
+          }
+        }
+        ++issued;
+      }
+      ++fi;
     }
   };
   bool ok = true;
@@ -322,12 +357,8 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
 
   for (int f = 0; f < F; ++f) {
     if (f > 0 && (f & 31) == 0) {
-      now = next;
-      next = Info{-1, 0, 0.f, 0.f};
-      if (f + 32 < F) {
-        advance(p, R, &ahead, 32);
-        next = fetch(ahead, f + 32);
-      }
+      if (set < (f >> 5)) next_set();
+      now0 = live0, now1 = live1;
     }
     const int h = cur.h, rb = cur.rb, ch = cur.ch;
     const int rows = min(R, cur.seq.n * G - rb * R);
@@ -400,77 +431,93 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
       lvb = 0.f;
     }
 
-    // ---------------------------------------------------------------- one tile of 16 keys
-    const int key0 = ch * kChunk + warp * kTile;
-    const int slice = __shfl_sync(0xffffffffu, now.slice, f & 31);
-    if (slice >= 0 && ok) {
-      const float ks = __shfl_sync(0xffffffffu, now.ks, f & 31);
-      const float lv = lg2(__shfl_sync(0xffffffffu, now.vs, f & 31));
+    // ---------------------------------------------------------------- one tile
+    const int key0 = ch * C::CHUNK + warp * C::KEYS;
+    const bool on[2] = {(now0 >> (f & 31) & 1u) != 0u, (now1 >> (f & 31) & 1u) != 0u};
+    if ((on[0] || on[1]) && ok) {
       const uint32_t slot = done % C::ST;
       ok = __all_sync(0xffffffffu, mbar_wait(bar0 + 8u * slot, (done / C::ST) & 1u, wctx,
                                              ERR_SITE_CACHE_FWD + 2));
       if (ok) {
-        if (first_live) lvb = lv;
+        const uint4 sc = ld_shared_v4(scl0 + slot * 16u);
+        const float ks[2] = {__uint_as_float(sc.x), __uint_as_float(sc.y)};
+        const float lv[2] = {lg2(__uint_as_float(sc.z)), lg2(__uint_as_float(sc.w))};
+        if (first_live) lvb = on[0] ? lv[0] : lv[1];
         first_live = false;
         const uint32_t ka = ring + slot * C::STAGE, va = ka + C::TILE;
-        // S^T
-        float s[NT][4];
+        const bool masked = key0 + C::KEYS > lim_lo;  // some row does not see all of it
+        // S^T, 16 keys at a time; y = x + log2 vs, masked keys before the maximum
+        float s[C::PARTS][NT][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int pt = 0; pt < C::PARTS; ++pt) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) s[nt][i] = 0.f;
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int half = 0; half < D / 64; ++half) {
-          uint32_t a[2][4];  // keys krow and krow + 8: 16 bytes
+            for (int i = 0; i < 4; ++i) s[pt][nt][i] = on[pt] ? 0.f : -INFINITY;
+          if (!on[pt]) continue;
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int row = krow + 8 * i;
-            const int piece = half * 4 + t;
-            const uint32_t addr = D == 128 ? ka + row * 128 + ((piece ^ (row & 7)) << 4)
-                                           : ka + row * 64 + ((piece ^ ((row >> 1) & 3)) << 4);
-            const uint4 x = ld_shared_v4(addr);
-            a[i][0] = x.x, a[i][1] = x.y, a[i][2] = x.z, a[i][3] = x.w;
+          for (int half = 0; half < D / 64; ++half) {
+            uint32_t a[2][4];  // keys krow and krow + 8: 16 bytes
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int row = krow + 8 * i;
+              const int piece = half * 4 + t;
+              const uint32_t at = ka + pt * C::PART;
+              const uint32_t addr = D == 128 ? at + row * 128 + ((piece ^ (row & 7)) << 4)
+                                             : at + row * 64 + ((piece ^ ((row >> 1) & 3)) << 4);
+              const uint4 x = ld_shared_v4(addr);
+              a[i][0] = x.x, a[i][1] = x.y, a[i][2] = x.z, a[i][3] = x.w;
+            }
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              uint32_t a0, a1, a2, a3;
+              codes4_to_f16<E5M2>(a[0][w], a0, a2);
+              codes4_to_f16<E5M2>(a[1][w], a1, a3);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma_f16(s[pt][nt], a0, a1, a2, a3, qf[nt][half * 4 + w][0],
+                        qf[nt][half * 4 + w][1]);
+            }
           }
+          const int k0 = key0 + pt * 16 + krow, k1 = k0 + 8;
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const uint32_t a0 = codes_to_f16x2<E5M2>((uint16_t)(a[0][w] & 0xffffu));
-            const uint32_t a1 = codes_to_f16x2<E5M2>((uint16_t)(a[1][w] & 0xffffu));
-            const uint32_t a2 = codes_to_f16x2<E5M2>((uint16_t)(a[0][w] >> 16));
-            const uint32_t a3 = codes_to_f16x2<E5M2>((uint16_t)(a[1][w] >> 16));
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              s[pt][nt][i] = fmaf(s[pt][nt][i], ks[pt] * qinv[nt][i & 1], lv[pt]);
+          if (masked) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-              mma_f16(s[nt], a0, a1, a2, a3, qf[nt][half * 4 + w][0], qf[nt][half * 4 + w][1]);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if ((i < 2 ? k0 : k1) >= lim[nt][i & 1]) s[pt][nt][i] = -INFINITY;
           }
         }
-        // y = x + log2 vs; masked keys before the maximum
-        const bool masked = key0 + kTile > lim_lo;
-        const int k0 = key0 + krow, k1 = k0 + 8;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            s[nt][i] = fmaf(s[nt][i], ks * qinv[nt][i & 1], lv);
-            if (masked && (i < 2 ? k0 : k1) >= lim[nt][i & 1]) s[nt][i] = -INFINITY;
-          }
+        float top[NT][2];  // this lane's largest y
         bool move = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-            // the difference first: far from zero, ref + kLazy would be rounded
-            move |= fmaxf(s[nt][i], s[nt][i + 2]) - ref[nt][i] > kLazy;
+          for (int i = 0; i < 2; ++i) {
+            top[nt][i] = fmaxf(s[0][nt][i], s[0][nt][i + 2]);
+            if (C::PARTS == 2)
+              top[nt][i] = fmaxf(top[nt][i], fmaxf(s[C::PARTS - 1][nt][i],
+                                                   s[C::PARTS - 1][nt][i + 2]));
+            move |= top[nt][i] - ref[nt][i] > kRoom;  // (-inf) - (-inf) moves nothing
+          }
         if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             float alpha[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              float m = fmaxf(s[nt][i], s[nt][i + 2]);
+              float m = top[nt][i];
 #pragma unroll
               for (int w = 4; w < 32; w <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
-              m = fmaxf(m, ref[nt][i]);
-              alpha[i] = m == -INFINITY ? 1.f : ex2(ref[nt][i] - m);
-              ref[nt][i] = m;
+              const float r = fabsf(m) < kFar ? m - kOff : m;
+              const float to = fmaxf(r, ref[nt][i]);
+              alpha[i] = to == -INFINITY ? 1.f : ex2(ref[nt][i] - to);
+              ref[nt][i] = to;
               lsum[nt][i] *= alpha[i];
             }
 #pragma unroll
@@ -479,99 +526,104 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
               for (int i = 0; i < 4; ++i) acc[mt][nt][i] *= alpha[i & 1];
           }
         }
-        const float w = ex2(lvb - lv);
-        uint32_t pf[NT][2];  // B operand of O^T
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float pr[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float r = ref[nt][i & 1];
-            pr[i] = ex2((s[nt][i] - (r == -INFINITY ? 0.f : r)) + kOff);
-            lsum[nt][i & 1] = fmaf(pr[i], w, lsum[nt][i & 1]);
-          }
-          pf[nt][0] = movmatrix(pack_f16x2(pr[0], pr[1]));
-          pf[nt][1] = movmatrix(pack_f16x2(pr[2], pr[3]));
-        }
-        // value rows of this lane: keys of matrix rows 2t, 2t + 1, 2t + 8, 2t + 9
         const int odd = D == 64 ? (t & 1) : 0;
-        auto value_row = [&](int i) {
-          return D == 128 ? t + 4 * i : 2 * t + ((i & 1) ^ odd) + 8 * (i >> 1);
-        };
-        auto load_values = [&](uint32_t (&v)[4][VW]) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int row = value_row(i);
-            if constexpr (D == 128) {
-              const uint4 x = ld_shared_v4(va + row * 128 + (((vcol >> 4) ^ (row & 7)) << 4));
-              v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
-            } else {
-              const uint2 x = ld_shared_v2(va + row * 64 +
-                                           (((vcol >> 4) ^ ((row >> 1) & 3)) << 4) + (vcol & 15));
-              v[i][0] = x.x, v[i][1] = x.y;
-            }
-            if (key0 + kTile > lim_hi && key0 + row >= lim_hi) {  // stale rows, whatever they hold
+        for (int pt = 0; pt < C::PARTS; ++pt) {
+          if (!on[pt]) continue;
+          const float w = ex2(lvb - lv[pt]);
+          uint32_t pf[NT][2];  // B operand of O^T
 #pragma unroll
-              for (int j = 0; j < VW; ++j) v[i][j] = 0u;
+          for (int nt = 0; nt < NT; ++nt) {
+            float pr[4];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float r = ref[nt][i] == -INFINITY ? 0.f : ref[nt][i];
+              pr[i] = ex2(s[pt][nt][i] - r);
+              pr[i + 2] = ex2(s[pt][nt][i + 2] - r);
+              lsum[nt][i] = fmaf(pr[i] + pr[i + 2], w, lsum[nt][i]);
             }
+            pf[nt][0] = movmatrix(pack_f16x2(pr[0], pr[1]));
+            pf[nt][1] = movmatrix(pack_f16x2(pr[2], pr[3]));
           }
-        };
-        uint32_t v[4][VW];
-        load_values(v);
-        // keys that some rows see and others do not: a NaN there must reach the former
-        // only, and a weight of zero does not keep it out of the product
-        bool poison = false;
-        if (lim_lo < min(key0 + kTile, lim_hi)) {
+          // value rows of this lane: keys of matrix rows 2t, 2t + 1, 2t + 8, 2t + 9
+          const int first = key0 + pt * 16;
+          auto value_row = [&](int i) {
+            return D == 128 ? t + 4 * i : 2 * t + ((i & 1) ^ odd) + 8 * (i >> 1);
+          };
+          auto load_values = [&](uint32_t (&v)[4][VW]) {
+            const uint32_t at = va + pt * C::PART;
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < VW; ++j) {
-              const uint32_t m = nan_codes<E5M2>(v[i][j]);
-              poison |= m != 0u;
-              v[i][j] = clear_codes(v[i][j], m);
+            for (int i = 0; i < 4; ++i) {
+              const int row = value_row(i);
+              if constexpr (D == 128) {
+                const uint4 x = ld_shared_v4(at + row * 128 + (((vcol >> 4) ^ (row & 7)) << 4));
+                v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
+              } else {
+                const uint2 x = ld_shared_v2(at + row * 64 +
+                                             (((vcol >> 4) ^ ((row >> 1) & 3)) << 4) + (vcol & 15));
+                v[i][0] = x.x, v[i][1] = x.y;
+              }
             }
-          poison = __any_sync(0xffffffffu, poison);
-        }
-        // O^T: bytes 2 mt, 2 mt + 1 of the lane's columns are rows g, g + 8 of tile mt
-        const uint32_t sel_lo = odd ? 0x1504u : 0x5140u, sel_hi = odd ? 0x3726u : 0x7362u;
+            if (masked) {  // stale rows, whatever they hold
 #pragma unroll
-        for (int j = 0; j < VW; ++j) {
-          const uint32_t lo01 = __byte_perm(v[0][j], v[1][j], sel_lo);
-          const uint32_t lo23 = __byte_perm(v[0][j], v[1][j], sel_hi);
-          const uint32_t hi01 = __byte_perm(v[2][j], v[3][j], sel_lo);
-          const uint32_t hi23 = __byte_perm(v[2][j], v[3][j], sel_hi);
+              for (int i = 0; i < 4; ++i)
+                if (first + value_row(i) >= lim_hi) {
 #pragma unroll
-          for (int m = 0; m < 2; ++m) {
-            const uint32_t x = m ? lo23 : lo01, y = m ? hi23 : hi01;
-            const uint32_t a0 = codes_to_f16x2<E5M2>((uint16_t)(x & 0xffffu));
-            const uint32_t a1 = codes_to_f16x2<E5M2>((uint16_t)(x >> 16));
-            const uint32_t a2 = codes_to_f16x2<E5M2>((uint16_t)(y & 0xffffu));
-            const uint32_t a3 = codes_to_f16x2<E5M2>((uint16_t)(y >> 16));
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma_f16(acc[2 * j + m][nt], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
-          }
-        }
-        if (poison) {  // rare: NaN for the rows that see it
+                  for (int j = 0; j < VW; ++j) v[i][j] = 0u;
+                }
+            }
+          };
+          uint32_t v[4][VW];
           load_values(v);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < VW; ++j) v[i][j] = nan_codes<E5M2>(v[i][j]);
-#pragma unroll
-          for (int j = 0; j < 4 * VW; ++j) {
-            uint32_t bad = 0u;  // the tile's keys whose value in this column is NaN
+          // keys that some rows see and others do not: a NaN there must reach the former
+          // only, and a weight of zero does not keep it out of the product
+          bool poison = false;
+          if (masked && lim_lo < min(first + 16, lim_hi)) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              if (v[i][j >> 2] >> (8 * (j & 3)) & 0x80u) bad |= 1u << value_row(i);
-            bad |= __shfl_xor_sync(0xffffffffu, bad, 1);
-            bad |= __shfl_xor_sync(0xffffffffu, bad, 2);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+              for (int j = 0; j < VW; ++j) {
+                const uint32_t m = nan_codes<E5M2>(v[i][j]);
+                poison |= m != 0u;
+                v[i][j] = clear_codes(v[i][j], m);
+              }
+            poison = __any_sync(0xffffffffu, poison);
+          }
+          // O^T: bytes 2 mt, 2 mt + 1 of the lane's columns are rows g, g + 8 of tile mt
+          const uint32_t sel_lo = odd ? 0x1504u : 0x5140u, sel_hi = odd ? 0x3726u : 0x7362u;
 #pragma unroll
-              for (int i = 0; i < 2; ++i)
-                if (bad & ((1u << max(0, min(kTile, lim[nt][i] - key0))) - 1u))
-                  acc[j >> 1][nt][(j & 1) * 2 + i] = __uint_as_float(0x7fffffffu);
+          for (int j = 0; j < VW; ++j) {
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+              uint32_t a0, a1, a2, a3;
+              codes4_to_f16<E5M2>(__byte_perm(v[0][j], v[1][j], m ? sel_hi : sel_lo), a0, a1);
+              codes4_to_f16<E5M2>(__byte_perm(v[2][j], v[3][j], m ? sel_hi : sel_lo), a2, a3);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma_f16(acc[2 * j + m][nt], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+            }
+          }
+          if (poison) {  // rare: NaN for the rows that see it
+            load_values(v);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int j = 0; j < VW; ++j) v[i][j] = nan_codes<E5M2>(v[i][j]);
+#pragma unroll
+            for (int j = 0; j < 4 * VW; ++j) {
+              uint32_t bad = 0u;  // the part's keys whose value in this column is NaN
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (v[i][j >> 2] >> (8 * (j & 3)) & 0x80u) bad |= 1u << value_row(i);
+              bad |= __shfl_xor_sync(0xffffffffu, bad, 1);
+              bad |= __shfl_xor_sync(0xffffffffu, bad, 2);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                  if (bad & ((1u << max(0, min(16, lim[nt][i] - first))) - 1u))
+                    acc[j >> 1][nt][(j & 1) * 2 + i] = __uint_as_float(0x7fffffffu);
+            }
           }
         }
         __syncwarp();  // the slot may be loaded again
@@ -592,7 +644,7 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
 #pragma unroll
           for (int w = 4; w < 32; w <<= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
           lsum[nt][i] = l;
-          mine[nt][i] = l == 0.f ? -INFINITY : ref[nt][i] - kOff - lvb + lg2(l);
+          mine[nt][i] = l == 0.f ? -INFINITY : ref[nt][i] - lvb + lg2(l);
           if (g == 0) stat[warp * R + nt * 8 + 2 * t + i] = mine[nt][i];
         }
       __syncthreads();
@@ -622,18 +674,30 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
       };
       float4* red4 = reinterpret_cast<float4*>(red);
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int turn = 0; turn < kWarps / C::BUFS; ++turn) {
+        if (warp / C::BUFS == turn) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int r = nt * 8 + 2 * t + i;
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int j = 0; j < VW; ++j)
-            red4[(warp * R + r) * (D / 4) + column(r, vcol / 4 + j)] =
-                make_float4(acc[2 * j][nt][i] * fac[nt][i] * up, acc[2 * j][nt][i + 2] * fac[nt][i] * up,
-                            acc[2 * j + 1][nt][i] * fac[nt][i] * up,
-                            acc[2 * j + 1][nt][i + 2] * fac[nt][i] * up);
+            for (int i = 0; i < 2; ++i) {
+              const int r = nt * 8 + 2 * t + i;
+#pragma unroll
+              for (int j = 0; j < VW; ++j) {
+                float4* to = &red4[(warp % C::BUFS * R + r) * (D / 4) + column(r, vcol / 4 + j)];
+                float4 x = make_float4(
+                    acc[2 * j][nt][i] * fac[nt][i] * up, acc[2 * j][nt][i + 2] * fac[nt][i] * up,
+                    acc[2 * j + 1][nt][i] * fac[nt][i] * up,
+                    acc[2 * j + 1][nt][i + 2] * fac[nt][i] * up);
+                if (turn > 0) {
+                  const float4 y = *to;
+                  x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+                }
+                *to = x;
+              }
+            }
         }
-      __syncthreads();
+        __syncthreads();
+      }
       const bool starts_here = f >= ch;  // the unit's chunk 0 is in this share
       const bool whole = starts_here && unit_ends;
       const int slot = starts_here ? 1 : 0;
@@ -660,7 +724,7 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
         const int r = x / (D / 4), c4 = x % (D / 4);
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
+        for (int w = 0; w < C::BUFS; ++w) {
           const float4 y = red4[(w * R + r) * (D / 4) + column(r, c4)];
           o.x += y.x, o.y += y.y, o.z += y.z, o.w += y.w;
         }
@@ -682,7 +746,7 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
         rec.first_row = rb * R;
       }
     }
-    advance(p, R, &cur, 1);
+    advance<C>(p, &cur, 1);
   }
   // loads in flight land before the CTA ends (only after a wait that ran out)
   for (; done < issued; ++done)
@@ -826,24 +890,33 @@ size_t narrow_bytes(int d, int n_sm) {  // the larger of the two variants
   return std::max(pieces_bytes((size_t)n_sm * Dec<128, 1>::CTAS, Dec<128, 1>::R, d),
                   pieces_bytes((size_t)n_sm * Dec<64, 2>::CTAS, Dec<64, 2>::R, d));
 }
+// The most query rows per key/value head (tokens x grouped heads) of a sequence that
+// stays with the kernel above.  From 33 rows on it reads the keys three times and
+// more, and the 256-row kernel costs less of the machine, but finishes a small batch
+// later.  Measured at d = 64: 16 sequences of 1 to 1000 tokens, 16 key heads, 83 us
+// with a limit of 32 rows and 110 us with 64; 24 sequences of 5 tokens, 2 key heads of
+// 8 query heads, 23 us and 17 us.
+int narrow_limit(const CacheParams& c, int n_sm) {
+  return (long long)c.B * c.H >= n_sm ? 32 : 64;
+}
 // Whether a call may have sequences for the 256-row kernel (whose row blocks hold
 // whole tokens: groups of more than 256 heads stay with the other one).
-bool takes_wide(const CacheParams& c, int G) {
-  return (long long)c.max_seqlen * G > kNarrowRows && G <= cache_fwd_wide_rows();
+bool takes_wide(const CacheParams& c, int G, int n_sm) {
+  return (long long)c.max_seqlen * G > narrow_limit(c, n_sm) && G <= cache_fwd_wide_rows();
 }
 
 }  // namespace
 
 size_t cache_fwd_workspace(const CacheParams& c, int G, int n_sm) {
   return narrow_bytes(c.d, n_sm) +
-         (takes_wide(c, G) ? pieces_bytes((size_t)n_sm, cache_fwd_wide_rows(), c.d) : 0);
+         (takes_wide(c, G, n_sm) ? pieces_bytes((size_t)n_sm, cache_fwd_wide_rows(), c.d) : 0);
 }
 
 cudaError_t launch_cache_fwd(const CUtensorMap& tk, const CUtensorMap& tv,
                              const CacheFwdParams& params, int n_sm, cudaStream_t stream) {
   CacheFwdParams p = params;
-  const bool wide = takes_wide(p.c, p.G);
-  p.narrow_rows = wide ? kNarrowRows : 0x7fffffff;
+  const bool wide = takes_wide(p.c, p.G, n_sm);
+  p.narrow_rows = wide ? narrow_limit(p.c, n_sm) : 0x7fffffff;
   if (wide) {
     p.wide_tokens = cache_fwd_wide_rows() / p.G;
     p.wide_ctas = n_sm;
