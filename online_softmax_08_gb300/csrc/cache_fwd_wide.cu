@@ -128,17 +128,23 @@ struct Segment {
   int on;               // 0: nothing to do
 };
 
-// sum over i < n of floor((a i + b) / m), by the Euclidean reduction of (a, m)
+// sum over i < n of floor((a i + b) / m), by the Euclidean reduction of (a, m).
+// a n + b < 2^32 (keys of a sequence), which the reduction only lowers.
 __device__ __forceinline__ long long floor_sum(unsigned n, unsigned m, unsigned a, unsigned b) {
   long long r = 0;
   while (n > 0) {
-    r += (long long)n * (n - 1) / 2 * (a / m) + (long long)n * (b / m);
-    a %= m;
-    b %= m;
-    const unsigned long long top = (unsigned long long)a * n + b;
+    if (a >= m) {
+      r += (long long)n * (n - 1) / 2 * (a / m);
+      a %= m;
+    }
+    if (b >= m) {
+      r += (long long)n * (b / m);
+      b %= m;
+    }
+    const unsigned top = a * n + b;
     if (top < m) break;
-    n = (unsigned)(top / m);
-    b = (unsigned)(top % m);
+    n = top / m;
+    b = top % m;
     const unsigned x = m;
     m = a;
     a = x;
@@ -221,27 +227,34 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
     // ---------------------------------------------------------------- which piece
     const int B = p.c.B, H = p.c.H;
     Blocks x;
-    long long tiles = 0;
+    long long tiles = 0, units = 0;
+    int largest = 0;
     for (int b0 = lane; b0 < B; b0 += 32) {
       set_blocks(p, b0, &x);
-      if (x.nb > 0) tiles += x.before(x.nb, C::BN) * H;
-    }
-#pragma unroll
-    for (int w = 16; w > 0; w >>= 1) tiles += __shfl_xor_sync(0xffffffffu, tiles, w);
-    const long long most = max((long long)kMinTiles, (tiles + p.wide_ctas - 1) / p.wide_ctas);
-    const unsigned m = (unsigned)min(most * C::BN, 0x7fffffffLL);  // keys of a piece
-    long long pieces = 0, units = 0;  // of all sequences; then of those before
-    for (int b0 = lane; b0 < B; b0 += 32) {
-      if (B > 32) set_blocks(p, b0, &x);
       if (x.nb > 0) {
-        pieces += x.before(x.nb, m) * H;
+        tiles += x.before(x.nb, C::BN) * H;
         units += (long long)x.nb * H;
+        largest = max(largest, x.parts(x.nb - 1, C::BN));  // the last block sees the most
       }
     }
+    largest = __reduce_max_sync(0xffffffffu, largest);
 #pragma unroll
     for (int w = 16; w > 0; w >>= 1) {
-      pieces += __shfl_xor_sync(0xffffffffu, pieces, w);
+      tiles += __shfl_xor_sync(0xffffffffu, tiles, w);
       units += __shfl_xor_sync(0xffffffffu, units, w);
+    }
+    const long long most = max((long long)kMinTiles, (tiles + p.wide_ctas - 1) / p.wide_ctas);
+    const bool cut = largest > most;  // some unit is
+    const unsigned m = cut ? (unsigned)(most * C::BN) : 0x7fffffffu;  // keys of a piece
+    long long pieces = units;
+    if (cut) {
+      pieces = 0;
+      for (int b0 = lane; b0 < B; b0 += 32) {
+        if (B > 32) set_blocks(p, b0, &x);
+        if (x.nb > 0) pieces += x.before(x.nb, m) * H;
+      }
+#pragma unroll
+      for (int w = 16; w > 0; w >>= 1) pieces += __shfl_xor_sync(0xffffffffu, pieces, w);
     }
     // the grid has room for every batch whose offsets ascend
     if (pieces > gridDim.x) {
@@ -261,7 +274,10 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
         long long mine = 0, own = 0;
         if (b0 + lane < B) {
           if (B > 32) set_blocks(p, b0 + lane, &x);
-          if (x.nb > 0) mine = x.before(x.nb, m) * H, own = (long long)x.nb * H;
+          if (x.nb > 0) {
+            own = (long long)x.nb * H;
+            mine = cut ? x.before(x.nb, m) * H : own;
+          }
         }
         long long upto = mine, u = own;
 #pragma unroll
@@ -282,9 +298,11 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
         units_before += __shfl_sync(0xffffffffu, u, 31);
       }
       set_blocks(p, g.b, &x);
-      const int rb = warp_search(x.nb, pos - before, [&](int i) { return x.before(i, m) * H; });
-      before += x.before(rb, m) * H;
-      const int k = x.parts(rb, m), rest = (int)(pos - before);
+      auto block_start = [&](int i) { return (cut ? x.before(i, m) : (long long)i) * H; };
+      const int rb = cut ? warp_search(x.nb, pos - before, block_start)
+                         : (int)((pos - before) / H);
+      before += block_start(rb);
+      const int k = cut ? x.parts(rb, m) : 1, rest = (int)(pos - before);
       const int h = rest / k, part = rest % k;
       const long long base = before + (long long)h * k - (units_before + (long long)rb * H + h);
       const int n_tiles = x.parts(rb, C::BN);
