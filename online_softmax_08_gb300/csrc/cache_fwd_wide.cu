@@ -82,9 +82,9 @@ struct Wide {
   static constexpr int PIECES = BN / 16;
   static constexpr int HALF = BM * 128;         // 64 columns of 128 rows (bytes)
   static constexpr int TILE = BM * D * 2;       // fp16
-  // With at most 6 slots, K of tile j + 4 is filled only after S of tile j + 1 was
-  // issued or all PV of tile j, hence after the softmax read tile j's scales: a ring
-  // of four tiles' scales needs no barrier for its reuse
+  // With at most 7 slots V of tile j + 3, and K of tile j + 4 behind it, are filled only
+  // after all PV of tile j, hence after the softmax read tile j's scales: a ring of four
+  // tiles' scales needs no barrier for its reuse
   static constexpr int STAGES = D == 128 ? 5 : 6;
   static constexpr int SCALE_TILES = 4;
   static constexpr int OFF_Q = 0;
@@ -99,6 +99,11 @@ struct Wide {
                 "register split");
   static_assert(SMEM <= 232448, "shared memory budget");
   static constexpr uint32_t TM_S = 0, TM_O = 256;
+  // At d = 64 the columns behind O_1 hold P_0 and P_1, so S_s of the next tile can be
+  // issued as soon as the softmax holds this tile's in registers; at d = 128 P_s takes
+  // the place of S_s.
+  static constexpr bool DEC = D == 64;
+  static constexpr uint32_t TM_P = DEC ? TM_O + 2 * D : TM_S, P_STRIDE = DEC ? 64 : 128;
   static constexpr uint32_t TMEM_COLS = 512;
   // fp16 operands, fp32 result: as idesc_bf16_f32 with the formats' fields zero
   static constexpr uint32_t kFormats = (1u << 7) | (1u << 10);
@@ -114,9 +119,11 @@ enum {
   B_P_HALF = 7,   // [2] softmax -> MMA: keys 0-63 of P_s in TMEM and O_s rescaled
   B_MMA_DONE = 9,
   B_SCALE = 10,    // [SCALE_TILES] slot filling -> softmax: the scales of a tile
-  B_KV_FULL = 14,  // [STAGES], then kv_empty [STAGES]
+  B_S_READ = 14,   // [2] softmax -> MMA (d = 64): S_s is in registers
+  B_KV_FULL = 16,  // [STAGES], then kv_empty [STAGES]
 };
 static_assert(8 * (B_KV_FULL + 2 * Wide<64>::STAGES) + 16 <= 256, "barrier block");
+static_assert(Wide<64>::STAGES <= 7 && Wide<128>::STAGES <= 7, "reuse of the scales' ring");
 
 // A piece of a unit: tiles [t0, t0 + max(c0, c1)) of it, of which subtile s sees the
 // first c_s.
@@ -222,6 +229,38 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
   const int G = p.G;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const uint32_t bar0 = sbase + C::OFF_BAR;
+  auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
+  const uint32_t kv_full0 = bar(B_KV_FULL), kv_empty0 = bar(B_KV_FULL + ST);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + 8 * (B_KV_FULL + 2 * ST));
+  volatile uint32_t* abort_flag = tmem_slot + 1;
+  volatile uint32_t* poison = tmem_slot + 2;        // a NaN was kept out of some rows' sums
+  const WaitCtx wctx{abort_flag, p.c.err};
+  float4* scales = reinterpret_cast<float4*>(smem + C::OFF_SCALE);
+
+  if (threadIdx.x == 32) {
+    mbar_init(bar(B_Q), 256);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(bar(B_S_FULL + s), 1);
+      mbar_init(bar(B_P_FULL + s), 128);
+      mbar_init(bar(B_P_HALF + s), 128);
+      mbar_init(bar(B_PV_DONE + s), 1);
+      mbar_init(bar(B_S_READ + s), 128);
+    }
+    mbar_init(bar(B_MMA_DONE), 1);
+    for (int i = 0; i < C::SCALE_TILES; ++i) mbar_init(bar(B_SCALE + i), C::PIECES);
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(kv_full0 + 8u * i, C::N_FILL);
+      mbar_init(kv_empty0 + 8u * i, 1);
+    }
+    *abort_flag = 0u;
+    *poison = 0u;
+    fence_mbar_init();
+  }
+  if (warp == C::W_MMA) {
+    tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
+    tmem_relinquish();
+  }
   __shared__ Segment seg_slot;
   if (warp == 0) {
     // ---------------------------------------------------------------- which piece
@@ -243,7 +282,11 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
       tiles += __shfl_xor_sync(0xffffffffu, tiles, w);
       units += __shfl_xor_sync(0xffffffffu, units, w);
     }
-    const long long most = max((long long)kMinTiles, (tiles + p.wide_ctas - 1) / p.wide_ctas);
+    // (a 64-bit division takes ten times as long)
+    const long long share = tiles < 0x7fffffff
+                                ? ((unsigned)tiles + p.wide_ctas - 1) / (unsigned)p.wide_ctas
+                                : (tiles + p.wide_ctas - 1) / p.wide_ctas;
+    const long long most = max((long long)kMinTiles, share);
     const bool cut = largest > most;  // some unit is
     const unsigned m = cut ? (unsigned)(most * C::BN) : 0x7fffffffu;  // keys of a piece
     long long pieces = units;
@@ -300,14 +343,15 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
       set_blocks(p, g.b, &x);
       auto block_start = [&](int i) { return (cut ? x.before(i, m) : (long long)i) * H; };
       const int rb = cut ? warp_search(x.nb, pos - before, block_start)
-                         : (int)((pos - before) / H);
+                         : (int)((unsigned)(pos - before) / (unsigned)H);  // < the grid
       before += block_start(rb);
       const int k = cut ? x.parts(rb, m) : 1, rest = (int)(pos - before);
       const int h = rest / k, part = rest % k;
       const long long base = before + (long long)h * k - (units_before + (long long)rb * H + h);
       const int n_tiles = x.parts(rb, C::BN);
-      const int t0 = (int)((long long)part * n_tiles / k);
-      const int take = (int)((long long)(part + 1) * n_tiles / k) - t0;
+      // k is at most one more than the SMs, so the products stay below 2^32
+      const int t0 = (int)((unsigned)part * (unsigned)n_tiles / (unsigned)k);
+      const int take = (int)((unsigned)(part + 1) * (unsigned)n_tiles / (unsigned)k) - t0;
       // tiles that the subtiles see: up to their last row's limit
       const int rows = min(x.tb, x.seq.n - rb * x.tb) * G;
       auto sees = [&](int last_row) {
@@ -330,8 +374,14 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
     }
     if (lane == 0) seg_slot = g;
   }
+  tc_fence_before();
   __syncthreads();
-  if (seg_slot.on == 0) return;
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  if (seg_slot.on == 0) {
+    if (warp == C::W_MMA) tmem_dealloc(tmem, C::TMEM_COLS);
+    return;
+  }
   const int b = seg_slot.b, h = seg_slot.h, t0 = seg_slot.t0, rb = seg_slot.rb;
   const int len = seg_slot.len, n_new = seg_slot.n, row0 = seg_slot.row0, part = seg_slot.part;
   const int n_rows = min(p.wide_tokens, n_new - rb * p.wide_tokens) * G;  // of the unit
@@ -344,43 +394,6 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
   const int n_max = max(nt0, nt1);
   const int lim_lo = limit_of(0), lim_hi = limit_of(n_rows - 1);
 
-  const uint32_t bar0 = sbase + C::OFF_BAR;
-  auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
-  const uint32_t kv_full0 = bar(B_KV_FULL), kv_empty0 = bar(B_KV_FULL + ST);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + 8 * (B_KV_FULL + 2 * ST));
-  volatile uint32_t* abort_flag = tmem_slot + 1;
-  volatile uint32_t* poison = tmem_slot + 2;        // a NaN was kept out of some rows' sums
-  volatile float* base_lv = reinterpret_cast<float*>(tmem_slot + 3);  // b above
-  const WaitCtx wctx{abort_flag, p.c.err};
-  float4* scales = reinterpret_cast<float4*>(smem + C::OFF_SCALE);
-
-  if (threadIdx.x == 0) {
-    mbar_init(bar(B_Q), 256);
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(bar(B_S_FULL + s), 1);
-      mbar_init(bar(B_P_FULL + s), 128);
-      mbar_init(bar(B_P_HALF + s), 128);
-      mbar_init(bar(B_PV_DONE + s), 1);
-    }
-    mbar_init(bar(B_MMA_DONE), 1);
-    for (int i = 0; i < C::SCALE_TILES; ++i) mbar_init(bar(B_SCALE + i), C::PIECES);
-    for (int i = 0; i < ST; ++i) {
-      mbar_init(kv_full0 + 8u * i, C::N_FILL);
-      mbar_init(kv_empty0 + 8u * i, 1);
-    }
-    *abort_flag = 0u;
-    *poison = 0u;
-    *base_lv = n_max > 0 ? unit_base(p, b, h) : 0.f;
-    fence_mbar_init();
-  }
-  if (warp == C::W_MMA) {
-    tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
 
   if (warp > C::W_MMA) {
     regs_dec<C::REG_CTRL>();  // idle
@@ -390,7 +403,7 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
     // Warp w fills rows [32 w, 32 w + 32) of every slot: two pieces of 16 tokens.
     const int bs = p.c.block_size;
     const int me = warp - C::W_FILL;
-    const float base = *base_lv;
+    const float base = n_max > 0 ? unit_base(p, b, h) : 0.f;  // b above
     // lane i of a set holds the block and scales of this warp's piece i & 1 of tile i / 2
     struct Info {
       int slice, row;  // page * H + h (-1: nothing visible there), first row in the block
@@ -541,7 +554,7 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
 #pragma unroll
       for (int k = 0; k < C::BN / 32; ++k) {
         const int kk = half * (C::BN / 32) + k;
-        mma_bf16_ts_w(tmem + C::TM_O + s * D, tmem + C::TM_S + s * 128 + kk * 8,
+        mma_bf16_ts_w(tmem + C::TM_O + s * D, tmem + C::TM_P + s * C::P_STRIDE + kk * 8,
                       sdesc_sw128(bv + kk * 16 * 128, C::HALF, 1024), C::IDESC_PV,
                       (j > 0 || kk > 0));
       }
@@ -557,7 +570,45 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
         mma_commit_w(kv_empty0);
       }
     }
-    for (int j = 0; ok && j < n_max; ++j) {
+    for (int j = 0; C::DEC && ok && j < n_max; ++j) {
+      // S_s(j + 1) once the softmax holds S_s(j) in registers; O_s += P_s V_j once P_s(j)
+      // is in its own columns.  The pipe runs them in issue order.
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        if (ok && j + 1 < (s ? nt1 : nt0)) {
+          ok = kv_wait(2 * (j + 1)) &&
+               __all_sync(0xffffffffu, mbar_wait(bar(B_S_READ + s), j & 1, wctx,
+                                                 ERR_SITE_CACHE_FWD + 13));
+          if (ok) {
+            tc_fence_after();
+            issue_s(s, j + 1);
+          }
+        }
+      }
+      if (!ok) break;
+      if (j + 1 < n_max) mma_commit_w(kv_empty0 + 8u * ((2 * (j + 1)) % ST));
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        if (ok && j < (s ? nt1 : nt0)) {
+          ok = kv_wait(2 * j + 1) &&
+               __all_sync(0xffffffffu, mbar_wait(bar(B_P_HALF + s), j & 1, wctx,
+                                                 ERR_SITE_CACHE_FWD + 7));
+          if (ok) {
+            tc_fence_after();
+            issue_pv(s, j, 0);
+            ok = __all_sync(0xffffffffu, mbar_wait(bar(B_P_FULL + s), j & 1, wctx,
+                                                   ERR_SITE_CACHE_FWD + 8));
+          }
+          if (ok) {
+            tc_fence_after();
+            issue_pv(s, j, 1);
+          }
+        }
+      }
+      if (!ok) break;
+      mma_commit_w(kv_empty0 + 8u * ((2 * j + 1) % ST));
+    }
+    for (int j = 0; !C::DEC && ok && j < n_max; ++j) {
       const bool next = j + 1 < n_max;
       bool k_next = false;
       ok = kv_wait(2 * j + 1);
@@ -600,8 +651,6 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
     const int s = warp >> 2;
     const int t = threadIdx.x & 127;  // row in the subtile == TMEM lane
     const int row = s * C::BM + t;  // of the unit
-    const long long at = (long long)row0 + rb * p.wide_tokens + p.by_G.div(row);  // packed row
-    const int hq = h * G + p.by_G.mod(row);
     const bool valid = row < n_rows;
     const int lim = valid ? limit_of(row) : 0;
     const int my_nt = s ? nt1 : nt0;
@@ -609,46 +658,73 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lane_off + C::TM_S + s * 128;
     const uint32_t tO = tmem + lane_off + C::TM_O + s * D;
-    const uint32_t tP = tS;
-    // Q: this thread's row, times the power of two that brings its largest element
-    // to [2^14, 2^15), as fp16 (exact down to 2^-29 of that element, the quantum
-    // below it 2^-39)
-    float back = 1.f;
-    {
-      uint4 v[D / 8];
+    const uint32_t tP = tmem + lane_off + C::TM_P + s * C::P_STRIDE;
+    const float base = my_nt > 0 ? unit_base(p, b, h) : 0.f;  // needed at the end only
+    // A row of q and o is LPR pieces of 16 bytes; a warp moves RPI of its 32 rows at a
+    // time, piece by lane (a thread that moved its own row would touch 32 lines with
+    // every instruction).
+    constexpr int LPR = D / 8, RPI = 32 / LPR, IT = 32 / RPI;
+    const int sub = lane / LPR, piece = lane % LPR;
+    const int first_row = s * C::BM + (warp & 3) * 32;  // of the warp, in the unit
+    const long long token0 = (long long)row0 + rb * p.wide_tokens;  // packed row of the unit's first
+    const uint32_t rows_smem = sbase + C::OFF_Q + s * C::TILE + (piece >> 3) * C::HALF;
+    auto row_piece = [&](int i) {  // where piece `piece` of the warp's row i RPI + sub lies
+      const int r = (warp & 3) * 32 + i * RPI + sub;
+      return rows_smem + r * 128 + (((piece & 7) ^ (r & 7)) << 4);
+    };
+    // Q: a row times the power of two that brings its largest element to [2^14, 2^15),
+    // as fp16 (exact down to 2^-29 of that element, the quantum below it 2^-39)
+    // (Loops that run once per piece are kept short: straight-line code of their length
+    // is bound by its instruction fetches.)
+    float back = 1.f;  // of this thread's row
+#pragma unroll 1
+    for (int i0 = 0; i0 < IT; i0 += 4) {
+      uint4 v[4];
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) v[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (valid) {
-        const uint16_t* q = p.q.p + at * p.q.st + (long long)hq * p.q.sh;
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) v[i] = *reinterpret_cast<const uint4*>(q + 8 * i);
+      for (int i = 0; i < 4; ++i) {
+        const int r = first_row + (i0 + i) * RPI + sub;
+        v[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (r < n_rows)
+          v[i] = *reinterpret_cast<const uint4*>(
+              p.q.p + (token0 + p.by_G.div(r)) * p.q.st +
+              (long long)(h * G + p.by_G.mod(r)) * p.q.sh + 8 * piece);
       }
-      uint32_t mx = 0u;
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i)
-        mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(v[i].x & 0x7fff7fffu, v[i].y & 0x7fff7fffu),
-                                   __vmaxu2(v[i].z & 0x7fff7fffu, v[i].w & 0x7fff7fffu)));
-      mx = max(mx & 0xffffu, mx >> 16);
-      int e = (int)(mx >> 7);
-      e = (mx == 0u || e == 255) ? 0 : min(14 - (e - 127), 126);
-      const float mul = __uint_as_float((uint32_t)(e + 127) << 23);
-      back = __uint_as_float((uint32_t)(127 - e) << 23);
-      const uint32_t dst = sbase + C::OFF_Q + s * C::TILE + t * 128;
+      for (int i = 0; i < 4; i += 2) {  // two rows' maxima in the halves of a word
+        uint32_t m2[2];
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        const uint32_t* w = &v[i].x;
-        uint32_t o[4];
+        for (int k = 0; k < 2; ++k) {
+          const uint4 x = v[i + k];
+          const uint32_t m = __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
+                                      __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
+          m2[k] = max(m & 0xffffu, m >> 16);
+        }
+        uint32_t m = m2[0] | m2[1] << 16;
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          asm("cvt.rn.f16x2.f32 %0, %1, %2;"
-              : "=r"(o[k])
-              : "f"(__uint_as_float(w[k] & 0xffff0000u) * mul),
-                "f"(__uint_as_float(w[k] << 16) * mul));
-        st_shared_v4(dst + (i >> 3) * C::HALF + (((i & 7) ^ (t & 7)) << 4), o[0], o[1], o[2], o[3]);
+        for (int w = 1; w < LPR; w <<= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, w));
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const uint32_t mx = k ? m >> 16 : m & 0xffffu;
+          int e = (int)(mx >> 7);
+          e = (mx == 0u || e == 255) ? 0 : min(14 - (e - 127), 126);
+          const float mul = __uint_as_float((uint32_t)(e + 127) << 23);
+          const float own = __shfl_sync(0xffffffffu, __uint_as_float((uint32_t)(127 - e) << 23),
+                                        (lane % RPI) * LPR);
+          if (lane / RPI == i0 + i + k) back = own;
+          const uint32_t* w = &v[i + k].x;
+          uint32_t o[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            asm("cvt.rn.f16x2.f32 %0, %1, %2;"
+                : "=r"(o[x])
+                : "f"(__uint_as_float(w[x] & 0xffff0000u) * mul),
+                  "f"(__uint_as_float(w[x] << 16) * mul));
+          st_shared_v4(row_piece(i0 + i + k), o[0], o[1], o[2], o[3]);
+        }
       }
-      fence_proxy_async_smem();
-      mbar_arrive(bar(B_Q));
     }
+    fence_proxy_async_smem();
+    mbar_arrive(bar(B_Q));
 
     float r_run = -INFINITY, l_run = 0.f;  // the reference r, and l
     for (int j = 0; j < my_nt; ++j) {
@@ -666,6 +742,10 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
       float sv[128];
 #pragma unroll
       for (int k = 0; k < 128; ++k) sv[k] = __uint_as_float(u[k >> 5][k & 31]);
+      if (C::DEC) {  // its columns may take S_s(j + 1)
+        tc_fence_before();
+        mbar_arrive(bar(B_S_READ + s));
+      }
       const int c0 = (t0 + j) * C::BN;
       if (c0 + C::BN > my_lo) {
         const int n = lim - c0;
@@ -728,6 +808,11 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
           }
           lw = fmaf((l0 + l1) + (l2 + l3), sc[hh * 4 + g].z, lw);
         }
+        if (C::DEC && hh == 0 && j > 0) {
+          // O_s += P_s V_{j-1} has finished: P_s's columns are free and O_s complete
+          mbar_wait(bar(B_PV_DONE + s), (j - 1) & 1, wctx, ERR_SITE_CACHE_FWD + 14);
+          tc_fence_after();
+        }
         tmem_st32(tP + hh * 32, pk);
         if (hh == 0) {
           if (j > 0 && __any_sync(0xffffffffu, rescale)) {
@@ -755,7 +840,6 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
 
     // ------------------------------------------------------------ epilogue
     const bool has = my_nt > 0 && !(l_run == 0.f);
-    const float base = *base_lv;
     const float inv = has ? 1.f / l_run : 0.f, up = ex2(base);
     const float lse = has ? (r_run - base + lg2(l_run)) * kLn2 : -INFINITY;
     if (my_nt > 0) {
@@ -763,10 +847,9 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
       tc_fence_after();
     }
     // a whole unit's rows go to o as bf16, a piece's to the workspace as fp32
-    uint16_t* o_row = p.o.p + at * p.o.st + (long long)hq * p.o.sh;
     const PieceView out = piece_view(p);
     const size_t place = (size_t)max(part, 0) * C::ROWS + row;
-#pragma unroll
+#pragma unroll 1
     for (int c = 0; c < D / 32; ++c) {
       uint32_t o[32];
       if (my_nt > 0) {  // subtile-uniform
@@ -776,16 +859,18 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
 #pragma unroll
       for (int i = 0; i < 32; ++i)
         o[i] = has ? __float_as_uint(__uint_as_float(o[i]) * inv * up) : 0u;
-      if (valid && part < 0) {
+      if (part < 0) {  // into Q_s's place, which no MMA reads any more
 #pragma unroll
         for (int q4 = 0; q4 < 4; ++q4) {
-          uint4 w;
-          uint32_t* x = &w.x;
+          const int k = c * 4 + q4;
+          uint32_t x[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             x[e] = pack_bf16x2(__uint_as_float(o[q4 * 8 + 2 * e]),
                                __uint_as_float(o[q4 * 8 + 2 * e + 1]));
-          *reinterpret_cast<uint4*>(o_row + c * 32 + q4 * 8) = w;
+          st_shared_v4(sbase + C::OFF_Q + s * C::TILE + (k >> 3) * C::HALF + t * 128 +
+                           (((k & 7) ^ (t & 7)) << 4),
+                       x[0], x[1], x[2], x[3]);
         }
       } else if (valid) {
 #pragma unroll
@@ -794,9 +879,24 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
               make_uint4(o[q4 * 4], o[q4 * 4 + 1], o[q4 * 4 + 2], o[q4 * 4 + 3]);
       }
     }
+    if (part < 0) {
+      __syncwarp();
+#pragma unroll 4
+      for (int i = 0; i < IT; ++i) {
+        const int r = first_row + i * RPI + sub;
+        uint4 x;
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                     : "r"(row_piece(i)));
+        if (r < n_rows)
+          *reinterpret_cast<uint4*>(
+              p.o.p + (token0 + p.by_G.div(r)) * p.o.st +
+              (long long)(h * G + p.by_G.mod(r)) * p.o.sh + 8 * piece) = x;
+      }
+    }
     if (valid) {
       if (part < 0)
-        p.lse[(long long)hq * p.c.total + at] = lse;
+        p.lse[(long long)(h * G + p.by_G.mod(row)) * p.c.total + token0 + p.by_G.div(row)] = lse;
       else
         out.lse[place] = lse;
     }
