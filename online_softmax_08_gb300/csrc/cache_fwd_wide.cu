@@ -94,7 +94,7 @@ struct Wide {
   static constexpr int SMEM = OFF_BAR + 256 + 1024;
   static constexpr int THREADS = 512;
   static constexpr int W_FILL = 8, N_FILL = 4, W_MMA = 12;
-  static constexpr int REG_LAUNCH = 128, REG_SOFTMAX = 192, REG_FILL = 88, REG_CTRL = 40;
+  static constexpr int REG_LAUNCH = 128, REG_SOFTMAX = 184, REG_FILL = 104, REG_CTRL = 40;
   static_assert((2 * REG_SOFTMAX + REG_FILL + REG_CTRL) * 128 <= THREADS * REG_LAUNCH,
                 "register split");
   static_assert(SMEM <= 232448, "shared memory budget");
