@@ -271,8 +271,10 @@ int fattn_fwd_bwd_host(const void* q, const void* k, const void* v, const void* 
  * key/value heads, [num_blocks, H, block_size, d], one 8-bit floating code per
  * value; k_scale and v_scale hold one fp32 scale per (block, head),
  * [num_blocks, H].  The value that code c of a block stands for is scale * c.
- * All four are DEVICE pointers owned by the caller, contiguous, 16-byte
- * aligned.  block_size is 16, 32, 64 or 128, d 64 or 128.
+ * All four are DEVICE pointers owned by the caller, contiguous, the codes
+ * 16-byte aligned and the scales 4-byte aligned (so one layer's part of a larger
+ * array will do).  block_size is 16, 32, 64 or 128, d 64 or 128, num_blocks x H
+ * below 2^31.
  * fattn_cache_append writes powers of two as scales; the reader and the
  * attention take any positive normal fp32 (scales of one sequence and head
  * that lie within 2^100 of each other). */
@@ -306,7 +308,8 @@ typedef struct {
  * no call appends to it.
  * Entries are checked on the device.  A sequence with offsets out of range or
  * decreasing, n_b > max_seqlen, or a length that is negative, beyond its table
- * row or (append, read) below n_b is skipped; a block number outside
+ * row or (append, read) below n_b is skipped (where offsets do not ascend, any
+ * sequence of the call may be); a block number outside
  * [0, num_blocks) drops its tokens (they are not written; read gives zeros for
  * them; they are not visible to the attention).  Both are reported through the
  * device error word (0x440 and 0x441 append, 0x450 and 0x451 read, 0x460 and

@@ -504,7 +504,7 @@ int check_cache_sizes(const fattn_cache* c, const fattn_cache_batch* b) {
 bool aligned4(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 int check_cache_pointers(const fattn_cache* c, const fattn_cache_batch* b) {
-  if (!aligned16(c->k) || !aligned16(c->v) || !aligned16(c->k_scale) || !aligned16(c->v_scale) ||
+  if (!aligned16(c->k) || !aligned16(c->v) || !aligned4(c->k_scale) || !aligned4(c->v_scale) ||
       !aligned4(b->block_table) || !aligned4(b->lens) || !aligned4(b->cu_seqlens))
     return FATTN_ERR_INVALID_ARG;
   return FATTN_OK;

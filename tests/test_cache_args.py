@@ -43,7 +43,7 @@ def _fwd(lib, c, b, q=A, qst=512, qsh=64, o=A, ost=512, osh=64, lse=A, Hq=8, sca
 
 
 BAD_CACHE = [(dict(k=0), INVALID), (dict(v=A + 8), INVALID), (dict(k_scale=0), INVALID),
-             (dict(v_scale=A + 4), INVALID), (dict(num_blocks=0), INVALID), (dict(H=0), INVALID),
+             (dict(v_scale=A + 2), INVALID), (dict(num_blocks=1 << 30), INVALID), (dict(num_blocks=0), INVALID), (dict(H=0), INVALID),
              (dict(H=1 << 17), INVALID), (dict(block_size=48), UNSUPPORTED),
              (dict(block_size=0), UNSUPPORTED), (dict(d=96), UNSUPPORTED),
              (dict(format=2), UNSUPPORTED)]

@@ -12,12 +12,11 @@ u = 2^-24 (half a step of fp32):
   factors scale, log2(e) and the block's scale; the exponent's error is that
   plus 4 u |score| <= 4 u S for the shift by the maximum, plus 2^-22 for ex2;
   the sums add n u;
-  a weight is held in 16 bits with at least 11 of precision: 2^-12 A, as a
-  rounding is off by half a step;
+  a weight is rounded to fp16, half a step being 2^-11 of it: 2^-11 A (the weights
+  below fp16's normal range, under 2^-22 of the largest, are off by 2^-33 of it);
   the result is rounded to bf16, half a step being 2^-8 of the value.
   |O - O_ref| <= 2^-8 |O_ref| + A (2^-11 + 2 eps),  eps = (d + 12) u S + n u + 2^-21
   |LSE - LSE_ref| <= eps + 2^-22 (1 + |LSE_ref|)
-(2^-11 leaves a factor of two for the weights' 2^-12.)
 """
 import numpy as np
 import pytest
@@ -245,6 +244,18 @@ FORWARD = [
     ([(128, 128), (300, 1)], 1, 2, 64, 32, "e5m2", True),
     ([(260, 13)], 1, 3, 128, 128, "e4m3", False),
     ([(257, 130)], 1, 1, 128, 64, "e5m2", True),
+    # groups larger than a row block of either kernel, and ones that do not divide it
+    ([(1, 50), (3, 40)], 1, 300, 64, 16, "e4m3", True),
+    ([(2, 30), (1, 77)], 1, 256, 64, 32, "e4m3", True),
+    ([(3, 30)], 1, 129, 128, 16, "e5m2", True),
+    ([(5, 200)], 2, 100, 64, 64, "e4m3", True),
+    # more than 32 sequences, of which every kernel's search takes two steps
+    ([(i % 4, 5 * i) for i in range(70)], 2, 2, 64, 16, "e4m3", True),
+    ([(1 if i % 9 else 40, 2 * i + 1) for i in range(60)], 1, 2, 128, 32, "e4m3", True),
+    ([(i % 2, i % 50) for i in range(1100)], 1, 1, 64, 16, "e5m2", True),
+    # a unit of the 256-row kernel cut into pieces
+    ([(130, 3000), (1, 70), (70, 5000)], 1, 1, 64, 64, "e4m3", True),
+    ([(33, 2600)], 1, 3, 128, 16, "e4m3", False),
 ]
 
 
@@ -359,6 +370,152 @@ def test_scales_that_are_no_powers_of_two():
     _check_forward(c, q, 0.125, True, o, lse)
     for got, ref in zip(fattn.cache_read(cache, batch), oc.read(c.cache, c.fmt, c.batch)):
         assert np.all(np.abs(got.cpu().double().numpy() - ref) <= (2.0 ** -8 + 2.0 ** -23) * np.abs(ref))
+
+
+def _torch_reference(c, cache, q, scale, causal):
+    """O, LSE, A, S and the visible keys as oc.forward gives them, in 64 bits on the device."""
+    k = cache.k.view(torch.uint8).view(TYPES[c.fmt]).double() * cache.k_scale.double()[..., None, None]
+    v = cache.v.view(torch.uint8).view(TYPES[c.fmt]).double() * cache.v_scale.double()[..., None, None]
+    T, Hq, d = q.shape
+    G = Hq // c.H
+    out = [torch.zeros((T, Hq, d)).double(), torch.full((Hq, T), -np.inf).double(),
+           torch.zeros((T, Hq, d)).double(), torch.zeros((Hq, T)).double(), np.zeros(T, dtype=int)]
+    for b, length in enumerate(c.lens):
+        lo, n = int(c.cu[b]), int(c.cu[b + 1] - c.cu[b])
+        rows = torch.tensor(c.table[b][:-(-int(length) // c.bs)].astype(np.int64), device=DEV)
+        kb = k[rows].transpose(0, 1).reshape(c.H, -1, d)[:, :length]
+        vb = v[rows].transpose(0, 1).reshape(c.H, -1, d)[:, :length]
+        at = torch.arange(int(length), device=DEV)
+        for i in range(n):
+            lim = int(length) - n + i + 1 if causal else int(length)
+            x = q[lo + i].double().reshape(c.H, G, d)
+            s = scale * x @ kb.transpose(1, 2)
+            s = s.masked_fill(at >= lim, -np.inf)
+            w = torch.softmax(s, 2)
+            out[0][lo + i] = (w @ vb).reshape(Hq, d).cpu()
+            out[1][:, lo + i] = torch.logsumexp(s, 2).reshape(Hq).cpu()
+            out[2][lo + i] = (w @ vb.abs()).reshape(Hq, d).cpu()
+            out[3][:, lo + i] = (scale * x.abs() @ kb.abs().transpose(1, 2)).masked_fill(
+                at >= lim, 0).amax(2).reshape(Hq).cpu()
+            out[4][lo + i] = lim
+    return [x if isinstance(x, np.ndarray) else x.numpy() for x in out]
+
+
+@pytest.mark.parametrize("pairs,H,G,d,bs,fmt", [
+    ([(1, 9000), (2, 17000), (1, 300)], 40, 1, 128, 16, "e4m3"),
+    ([(1, 20000), (3, 30000)], 48, 2, 64, 64, "e4m3"),
+    ([(9, 7000), (12, 900)], 16, 1, 128, 128, "e5m2"),
+])
+def test_long_shares(pairs, H, G, d, bs, fmt):
+    """Enough keys that every CTA's share runs through several sets of 32 tiles, and
+    through whole units and pieces of them."""
+    c = Case(pairs, H, d, bs, fmt, nan_slots=False)
+    g = torch.Generator(device=DEV).manual_seed(4)
+    q = _bf16(c.rng, (c.T, H * G, d)).to(DEV)
+    cache, batch = c.on_device()
+    for codes, scale in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)):
+        x = torch.randn(codes.shape, generator=g, device=DEV)
+        codes.copy_((x * 8).to(codes.dtype))
+        scale.fill_(0.125)
+    o, lse = fattn.cache_forward(q, cache, batch, d ** -0.5, True)
+    ref, lse_ref, A, S, seen = _torch_reference(c, cache, q, d ** -0.5, True)
+    u = 2.0 ** -24
+    eps = (d + 12) * u * S + seen[None, :] * u + 2.0 ** -21
+    bar = 2.0 ** -8 * np.abs(ref) + A * (2.0 ** -11 + 2 * eps.T[:, :, None])
+    assert np.all(np.abs(o.cpu().double().numpy() - ref) <= bar)
+    assert np.all(np.abs(lse.cpu().double().numpy() - lse_ref) <= eps + 2.0 ** -22 * (1 + np.abs(lse_ref)))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_nan_in_a_unit_cut_into_pieces(d):
+    H, bs, n, prior = 1, 32, 80, 3000
+    c = Case([(n, prior)], H, d, bs, seed=d).fill()
+    q = _bf16(c.rng, (n, H, d))
+    bad = prior + 41
+    c.cache["v"][c.table[0, bad // bs], 0, bad % bs, 7] = 0x7f
+    early = 500  # seen by every row, in another piece
+    c.cache["v"][c.table[0, early // bs], 0, early % bs, 9] = 0xff
+    cache, batch = c.on_device()
+    o, _ = fattn.cache_forward(q.to(DEV), cache, batch, d ** -0.5, True)
+    nan = np.zeros((n, H, d), dtype=bool)
+    nan[41:, :, 7] = True
+    nan[:, :, 9] = True
+    np.testing.assert_array_equal(np.isnan(o.cpu().double().numpy()), nan)
+
+
+def test_graph_of_a_mixed_batch():
+    """Pieces of prompts and single tokens captured together; lengths and offsets move
+    between replays, and a replay with fewer tokens leaves the rows behind them alone."""
+    H, G, d, bs = 2, 4, 64, 16
+    c = Case([(100, 30), (1, 400), (20, 60), (1, 9)], H, d, bs, nan_slots=False).fill()
+    q = _bf16(c.rng, (c.T, H * G, d))
+    cache, batch = c.on_device()
+    qd = q.to(DEV)
+    out = torch.full_like(qd, 7.0)
+    graph = torch.cuda.CUDAGraph()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    fattn.cache_forward(qd, cache, batch, 0.125, True)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        _, lse = fattn.cache_forward(qd, cache, batch, 0.125, True, out=out)
+    for n, lens in (((100, 1, 20, 1), (130, 401, 80, 10)), ((2, 70, 0, 5), (100, 390, 80, 10)),
+                    ((1, 1, 1, 1), (130, 401, 80, 10)), ((90, 1, 30, 1), (130, 300, 30, 1))):
+        c.lens = np.array(lens, dtype=np.int32)
+        c.cu = np.concatenate([[0], np.cumsum(n)]).astype(np.int32)
+        batch.lens.copy_(torch.tensor(c.lens))
+        batch.cu_seqlens.copy_(torch.tensor(c.cu))
+        out.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        _check_forward(c, q, 0.125, True, out, lse)
+        assert bool((out[int(c.cu[-1]):] == 7.0).all())
+
+
+def test_offsets_that_do_not_ascend():
+    """Nothing is written out of place, and the word is set."""
+    H, G, d, bs = 1, 2, 64, 16
+    c = Case([(40, 30), (50, 40), (60, 50), (1, 3)], H, d, bs).fill()
+    q = _bf16(c.rng, (c.T, H * G, d)).to(DEV)
+    x = _bf16(c.rng, (c.T, H, d)).to(DEV)
+    cache, batch = c.on_device()
+    for cu in ([0, 60, 0, 60, 0], [0, 40, 90, 40, 151], [5, 5, 2 ** 31 - 1, 90, -7],
+               [0, 60, 10, 70, 20]):
+        bad = batch._replace(cu_seqlens=torch.tensor(cu, dtype=torch.int32, device=DEV))
+        base = torch.full((c.T + 2, H * G, d), 7.0, dtype=torch.bfloat16, device=DEV)
+        fattn.cache_forward(q, cache, bad, 0.125, True, out=base[1:-1])
+        assert fattn.fattn_device_error() != 0
+        assert bool((base[0] == 7.0).all()) and bool((base[-1] == 7.0).all())
+        kv = [torch.full((c.T + 2, H, d), 7.0, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+        fattn.cache_read(cache, bad, out=(kv[0][1:-1], kv[1][1:-1]))
+        assert fattn.fattn_device_error() != 0
+        for t in kv:
+            assert bool((t[0] == 7.0).all()) and bool((t[-1] == 7.0).all())
+        fattn.cache_append(x, x, cache, bad)
+        assert fattn.fattn_device_error() != 0
+
+
+def test_nothing_to_do():
+    c = Case([(0, 40), (0, 0)], 2, 64, 16).fill()
+    cache, batch = c.on_device()
+    q = torch.empty((0, 4, 64), dtype=torch.bfloat16, device=DEV)
+    x = torch.empty((0, 2, 64), dtype=torch.bfloat16, device=DEV)
+    before = _host(cache)
+    o, lse = fattn.cache_forward(q, cache, batch, 0.1, True)
+    assert o.shape == (0, 4, 64) and lse.shape == (4, 0)
+    fattn.cache_append(x, x, cache, batch)
+    assert fattn.cache_read(cache, batch)[0].shape == (0, 2, 64)
+    after = _host(cache)
+    for name in before:
+        np.testing.assert_array_equal(before[name], after[name])
+    # padded rows only
+    c = Case([(0, 40), (0, 5)], 2, 64, 16, pad_tokens=3).fill()
+    cache, batch = c.on_device()
+    out = torch.full((3, 4, 64), 7.0, dtype=torch.bfloat16, device=DEV)
+    for most in (0, 3):
+        fattn.cache_forward(torch.zeros_like(out), cache, batch._replace(max_seqlen=most), 0.1, True,
+                            out=out)
+    assert bool((out == 7.0).all())
 
 
 def test_shared_prefix():
