@@ -659,14 +659,22 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
     const uint32_t tS = tmem + lane_off + C::TM_S + s * 128;
     const uint32_t tO = tmem + lane_off + C::TM_O + s * D;
     const uint32_t tP = tmem + lane_off + C::TM_P + s * C::P_STRIDE;
-    const float base = my_nt > 0 ? unit_base(p, b, h) : 0.f;  // needed at the end only
+    float base = my_nt > 0 ? unit_base(p, b, h) : 0.f;  // needed at the end only
     // A row of q and o is LPR pieces of 16 bytes; a warp moves RPI of its 32 rows at a
     // time, piece by lane (a thread that moved its own row would touch 32 lines with
     // every instruction).
     constexpr int LPR = D / 8, RPI = 32 / LPR, IT = 32 / RPI;
     const int sub = lane / LPR, piece = lane % LPR;
-    const int first_row = s * C::BM + (warp & 3) * 32;  // of the warp, in the unit
-    const long long token0 = (long long)row0 + rb * p.wide_tokens;  // packed row of the unit's first
+    // offsets of this thread's row in q, o and lse (-1: no such row); the lanes that
+    // move the row take them from here
+    long long q_off = -1, o_off = -1, lse_off = 0;
+    if (valid) {
+      const long long token = (long long)row0 + rb * p.wide_tokens + p.by_G.div(row);
+      const long long hq = h * G + p.by_G.mod(row);
+      q_off = token * p.q.st + hq * p.q.sh;
+      o_off = token * p.o.st + hq * p.o.sh;
+      lse_off = hq * p.c.total + token;
+    }
     const uint32_t rows_smem = sbase + C::OFF_Q + s * C::TILE + (piece >> 3) * C::HALF;
     auto row_piece = [&](int i) {  // where piece `piece` of the warp's row i RPI + sub lies
       const int r = (warp & 3) * 32 + i * RPI + sub;
@@ -677,18 +685,22 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
     // (Loops that run once per piece are kept short: straight-line code of their length
     // is bound by its instruction fetches.)
     float back = 1.f;  // of this thread's row
+    uint4 ahead[4];  // the next four pieces
+    auto load_q = [&](int i0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const long long off = __shfl_sync(0xffffffffu, q_off, (i0 + i) * RPI + sub);
+        ahead[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (off >= 0) ahead[i] = *reinterpret_cast<const uint4*>(p.q.p + off + 8 * piece);
+      }
+    };
+    load_q(0);
 #pragma unroll 1
     for (int i0 = 0; i0 < IT; i0 += 4) {
       uint4 v[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = first_row + (i0 + i) * RPI + sub;
-        v[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (r < n_rows)
-          v[i] = *reinterpret_cast<const uint4*>(
-              p.q.p + (token0 + p.by_G.div(r)) * p.q.st +
-              (long long)(h * G + p.by_G.mod(r)) * p.q.sh + 8 * piece);
-      }
+      for (int i = 0; i < 4; ++i) v[i] = ahead[i];
+      if (i0 + 4 < IT) load_q(i0 + 4);
 #pragma unroll
       for (int i = 0; i < 4; i += 2) {  // two rows' maxima in the halves of a word
         uint32_t m2[2];
@@ -725,6 +737,7 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
     }
     fence_proxy_async_smem();
     mbar_arrive(bar(B_Q));
+    asm volatile("" : "+f"(base));  // loaded by now, not behind the loop
 
     float r_run = -INFINITY, l_run = 0.f;  // the reference r, and l
     for (int j = 0; j < my_nt; ++j) {
@@ -883,20 +896,17 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
       __syncwarp();
 #pragma unroll 4
       for (int i = 0; i < IT; ++i) {
-        const int r = first_row + i * RPI + sub;
         uint4 x;
         asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                      : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
                      : "r"(row_piece(i)));
-        if (r < n_rows)
-          *reinterpret_cast<uint4*>(
-              p.o.p + (token0 + p.by_G.div(r)) * p.o.st +
-              (long long)(h * G + p.by_G.mod(r)) * p.o.sh + 8 * piece) = x;
+        const long long off = __shfl_sync(0xffffffffu, o_off, i * RPI + sub);
+        if (off >= 0) *reinterpret_cast<uint4*>(p.o.p + off + 8 * piece) = x;
       }
     }
     if (valid) {
       if (part < 0)
-        p.lse[(long long)(h * G + p.by_G.mod(row)) * p.c.total + token0 + p.by_G.div(row)] = lse;
+        p.lse[lse_off] = lse;
       else
         out.lse[place] = lse;
     }

@@ -405,12 +405,14 @@ class CacheBatch(typing.NamedTuple):
 
 
 def new_cache(num_blocks, heads, block_size, d, dtype=torch.float8_e4m3fn, device="cuda"):
-    """An empty KVCache (codes and scales zero)."""
+    """An empty KVCache: codes zero, scales 2^-100, what fattn_cache_append writes for
+    a block of zeros."""
     if dtype not in CACHE_FORMATS:
         raise ValueError("a cache holds float8_e4m3fn or float8_e5m2, not %s" % dtype)
     shape = (num_blocks, heads, block_size, d)
     k, v = (torch.zeros(shape, dtype=torch.uint8, device=device).view(dtype) for _ in range(2))
-    ks, vs = (torch.zeros(shape[:2], dtype=torch.float32, device=device) for _ in range(2))
+    ks, vs = (torch.full(shape[:2], 2.0 ** -100, dtype=torch.float32, device=device)
+              for _ in range(2))
     return KVCache(k, v, ks, vs)
 
 
