@@ -18,7 +18,13 @@
 // and lets the values be read back exactly as bf16.
 //
 // Memory-bound: the item's values stay in registers (64 per lane) between the
-// maximum and the conversion, so every value is read once and written once.
+// maximum and the conversion, so every value is read once and written once.  Measured
+// (d = 128): 32768 tokens of 16 heads written in 64.5 us, 92 % of the measured copy
+// bandwidth; 16 sequences of 512 to 8192 tokens of 16 heads read back in 85 us, 98 %;
+// one token of each of 256 sequences, 8 heads, 7 us, which is the search for the
+// sequence, its block and its values one after the other.  Streaming loads and stores
+// brought the first to 62 us but would push the new codes out of L2, where the
+// attention that follows looks for them.
 #include "cache.cuh"
 
 namespace fattn {

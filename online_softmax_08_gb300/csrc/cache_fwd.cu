@@ -19,7 +19,13 @@
 // The bound is memory: every code is read once.  At the measured copy
 // bandwidth an SM gets about 24 codes a clock, and a 16-key tile of keys and
 // values (4 KB at d = 128) costs 174 clocks, of which the arithmetic below takes
-// about a quarter of the issue slots.  With 1 to 16 rows per key/value head the
+// about half of the issue slots.  Measured: 4 sequences of 32768 tokens, 32 heads,
+// d = 128 (1.07 GB) 169 us, 94 % of the measured copy bandwidth; 32 sequences of 512
+// to 8192 tokens, 32 query and 8 key heads (186 MB) 40 us, 68 %: the start of a share
+// (offsets, block table, first codes, one after the other) takes 3 us, its end and
+// the merge 3 us; one sequence of 1000 tokens 8 us.  Three CTAs per SM and three ring
+// slots a warp: with four CTAs the registers spilled (221 us for the first case), with
+// two the loads in flight fell short (211 us).  With 1 to 16 rows per key/value head the
 // tensor work is far too small for a 128-row tcgen05 tile and its trip through
 // shared memory and TMEM; m16n8k16 mma.sync with the keys as the 16-row operand
 // takes the codes straight from shared memory into registers:
@@ -39,7 +45,7 @@
 // second kernel (at most two pieces per CTA, so the workspace does not depend
 // on the lengths).  Each warp runs its own ring of TMA loads (box: 16 tokens of
 // one block), addressed through page numbers and scales that its lanes fetch
-// 32 tiles ahead.
+// 32 tiles at a time.
 #include <math.h>
 
 #include <algorithm>
@@ -65,10 +71,10 @@ struct Dec {
   static constexpr int PART = 16 * D;             // bytes of 16 keys or values: one TMA box
   static constexpr int TILE = KEYS * D;
   static constexpr int STAGE = 2 * TILE;          // keys and values
-  static constexpr int ST = D == 64 && NT == 1 ? 4 : D == 128 && NT == 2 ? 4 : 3;  // ring slots per warp
+  // ring slots per warp, CTAs per SM: as much as the shared memory and registers take
+  static constexpr int ST = D == 64 && NT == 1 ? 4 : D == 128 && NT == 2 ? 4 : 3;
   static constexpr int OFF_RED = kWarps * ST * STAGE;
-  static constexpr int BUFS = kWarps;             // where the warps' results meet
-  static constexpr int OFF_SCL = OFF_RED + BUFS * R * D * 4;  // [warps][ST] scales of a tile
+  static constexpr int OFF_SCL = OFF_RED + kWarps * R * D * 4;  // [warps][ST] scales of a tile
   static constexpr int OFF_STAT = OFF_SCL + kWarps * ST * 16;
   static constexpr int OFF_BAR = OFF_STAT + kWarps * R * 4;
   static constexpr int SMEM = OFF_BAR + kWarps * ST * 8 + 16 + 1024;
@@ -168,7 +174,7 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
   uint8_t* smem = smem_raw + (sbase - raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  float* red = reinterpret_cast<float*>(smem + C::OFF_RED);    // [BUFS][R][D]
+  float* red = reinterpret_cast<float*>(smem + C::OFF_RED);    // [warps][R][D]
   float* stat = reinterpret_cast<float*>(smem + C::OFF_STAT);  // [warps][R]
   const uint32_t bar0 = sbase + C::OFF_BAR + 8u * (uint32_t)(warp * C::ST);
   volatile uint32_t* abort_flag =
@@ -674,30 +680,18 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
       };
       float4* red4 = reinterpret_cast<float4*>(red);
 #pragma unroll
-      for (int turn = 0; turn < kWarps / C::BUFS; ++turn) {
-        if (warp / C::BUFS == turn) {
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+        for (int i = 0; i < 2; ++i) {
+          const int r = nt * 8 + 2 * t + i;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int r = nt * 8 + 2 * t + i;
-#pragma unroll
-              for (int j = 0; j < VW; ++j) {
-                float4* to = &red4[(warp % C::BUFS * R + r) * (D / 4) + column(r, vcol / 4 + j)];
-                float4 x = make_float4(
-                    acc[2 * j][nt][i] * fac[nt][i] * up, acc[2 * j][nt][i + 2] * fac[nt][i] * up,
-                    acc[2 * j + 1][nt][i] * fac[nt][i] * up,
-                    acc[2 * j + 1][nt][i + 2] * fac[nt][i] * up);
-                if (turn > 0) {
-                  const float4 y = *to;
-                  x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
-                }
-                *to = x;
-              }
-            }
+          for (int j = 0; j < VW; ++j)
+            red4[(warp * R + r) * (D / 4) + column(r, vcol / 4 + j)] = make_float4(
+                acc[2 * j][nt][i] * fac[nt][i] * up, acc[2 * j][nt][i + 2] * fac[nt][i] * up,
+                acc[2 * j + 1][nt][i] * fac[nt][i] * up,
+                acc[2 * j + 1][nt][i + 2] * fac[nt][i] * up);
         }
-        __syncthreads();
-      }
+      __syncthreads();
       const bool starts_here = f >= ch;  // the unit's chunk 0 is in this share
       const bool whole = starts_here && unit_ends;
       const int slot = starts_here ? 1 : 0;
@@ -724,7 +718,7 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
         const int r = x / (D / 4), c4 = x % (D / 4);
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < C::BUFS; ++w) {
+        for (int w = 0; w < kWarps; ++w) {
           const float4 y = red4[(w * R + r) * (D / 4) + column(r, c4)];
           o.x += y.x, o.y += y.y, o.z += y.z, o.w += y.w;
         }

@@ -8,11 +8,11 @@
 // long sequence is spread over the machine, while units that are short against the
 // machine's share are not cut and pay for no merge.  (A persistent grid with equal
 // shares, built and measured: the loop over pieces cost the MMA warp and the
-// registers more than the better balance gave, 432 us against 271 us for 2048 tokens
-// behind 8192, G = 4.)  Per piece the structure is that of the
-// dense forward kernel: keys and values of 128 tokens at a time pass through a
-// ring of shared-memory slots, S_s = Q_s K^T lives in TMEM, the softmax warps turn
-// it into P_s in place, and O_s += P_s V accumulates in TMEM.
+// registers more than the better balance gave, 371 us against 250 us for 2048 tokens
+// behind 8192 with 32 query and 8 key heads, d = 128.)  Per piece the structure is
+// that of the dense forward kernel: keys and values of 128 tokens at a time pass
+// through a ring of shared-memory slots, S_s = Q_s K^T lives in TMEM, the softmax
+// warps turn it into P_s (at d = 128 in place), and O_s += P_s V accumulates in TMEM.
 //
 // What differs is how a slot is filled.  The codes cannot feed the tensor core as
 // they are (q and P need more than 8 bits), so four warps load them from their
@@ -28,8 +28,16 @@
 // maximum itself, as 8 is then too near its rounding.
 //
 // Warps: 0-3 softmax of subtile 0, 4-7 of subtile 1 (thread t owns row t; they also
-// load Q and write O), 8-11 fill the slots, 12 issues the MMAs, 13-15 idle.  TMEM: S_0, S_1, O_0,
-// O_1.  Measured limits: see the launcher.
+// load Q and write O), 8-11 fill the slots, 12 issues the MMAs, 13-15 idle.  TMEM:
+// S_0, S_1, O_0, O_1 (d = 64: P_0, P_1).
+//
+// Measured, 2048 tokens behind 8192 (32 query, 8 key heads, d = 128): 250 us, 1237
+// TFLOP/s, tensor pipe 50 % active.  256 units on 152 SMs are two rounds where 1.7
+// would do (16 %); a tile of 128 keys takes 3100 clocks against the MMAs' 2048, the
+// MMA warp's own issue (1750) and its waits for P (1350) alternating; the start and
+// end of a piece take 15,000 and 4,000 clocks of 250,000.  At d = 64 (16 sequences of
+// 1 to 1000 tokens behind 300 to 7000, 16 heads) a tile takes 2200 to 2900 clocks,
+// bound by the softmax, and the starts are a fifth of the time.
 #define FATTN_INLINE_WAIT_SLOW_PATH
 #include <math.h>
 
