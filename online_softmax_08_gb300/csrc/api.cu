@@ -10,6 +10,7 @@
 #include <mutex>
 
 #include "../../include/fattn.h"
+#include "cache.cuh"
 #include "common.cuh"
 #include "ptx.cuh"
 
