@@ -576,8 +576,10 @@ int cache_move(CacheMove launch, const fattn_cache* cache, const fattn_cache_bat
   st = current_device(&dev);
   if (st != FATTN_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = launch(cache_params(cache, batch, dev->err), token_view(k, kst, ksh, T, H),
-                               token_view(v, vst, vsh, T, H), s);
+  CacheParams p = cache_params(cache, batch, dev->err);
+  p.l2_bytes = dev->l2_bytes;
+  const cudaError_t e =
+      launch(p, token_view(k, kst, ksh, T, H), token_view(v, vst, vsh, T, H), s);
   return debug_post_call(e == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA, s);
 }
 

@@ -45,6 +45,7 @@ struct CacheParams {
   const int* lens;
   const int* cu_seqlens;
   int B, table_width, total, max_seqlen;
+  long long l2_bytes;    // of the device (append)
   unsigned int* err;
 };
 // A packed [total, heads, d] tensor by element strides.

@@ -166,6 +166,30 @@ def test_append_then_read(pairs, H, d, bs, fmt, layout):
         assert bool((base == 7.0).all())
 
 
+@pytest.mark.parametrize("bs,d", [(64, 128), (16, 64)])
+def test_append_of_more_than_the_caches_hold(bs, d):
+    """A prompt whose codes exceed half of L2, written in one call and block by block."""
+    H, T, steps = 32, 20480 * 128 // d, 8
+    g = torch.Generator(device=DEV).manual_seed(6)
+    k, v = (torch.randn((T, H, d), generator=g, device=DEV).bfloat16() for _ in range(2))
+    table = torch.randperm(T // bs, generator=g, device=DEV).int()[None].contiguous()
+    i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device=DEV)
+    one, many = (fattn.new_cache(T // bs, H, bs, d, device=DEV) for _ in range(2))
+    fattn.cache_append(k, v, one, fattn.CacheBatch(table, i32(T), i32(0, T), T, T))
+    n = T // steps
+    for i in range(steps):
+        part = slice(i * n, (i + 1) * n)
+        fattn.cache_append(k[part], v[part], many,
+                           fattn.CacheBatch(table, i32((i + 1) * n), i32(0, n), n, n))
+    for a, b in zip(one, many):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    # and against the definition, in 64 bits: a block's values are off by half a step
+    rk, _ = fattn.cache_read(one, fattn.CacheBatch(table, i32(T), i32(0, T), T, T))
+    err = (rk.double() - k.double()).abs()
+    floor = one.k_scale[table[0].long()].repeat_interleave(bs, 0)[:, :, None].double() * 2.0 ** -10
+    assert bool((err <= 2.0 ** -4 * k.double().abs() + floor).all())
+
+
 @pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
 def test_append_special_values(fmt):
     """Zeros, NaN, infinities, subnormals, the largest bf16, and values at the
