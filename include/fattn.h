@@ -304,8 +304,8 @@ typedef struct {
  * non-decreasing offsets from 0, at most `total`; rows at and behind
  * cu_seqlens[B] are neither read nor written, so a captured graph can be sized
  * for more tokens than a replay has.  max_seqlen >= every n_b (it sizes the
- * grids).  A block may appear in several sequences (a shared prefix) as long as
- * no call appends to it.
+ * grids).  table_width x block_size is at most 2^31 - 65536.  A block may appear
+ * in several sequences (a shared prefix) as long as no call appends to it.
  * Entries are checked on the device.  A sequence with offsets out of range or
  * decreasing, n_b > max_seqlen, or a length that is negative, beyond its table
  * row or (append, read) below n_b is skipped (where offsets do not ascend, any
@@ -339,8 +339,8 @@ typedef struct {
  * their value).  New values are divided by the scale (exact) and rounded to
  * nearest even.  NaN and infinities are stored as NaN and do not enter amax.
  * A call that is repeated with the same arguments leaves the same cache.
- * No two sequences of a call may append to the same block (the writes would
- * race; nothing out of range is touched). */
+ * No block may be named twice among those that a call appends to (the writes
+ * would race; nothing out of range is touched). */
 int fattn_cache_append(const fattn_cache* cache, const fattn_cache_batch* batch, const void* k,
                        long long k_token_stride, long long k_head_stride, const void* v,
                        long long v_token_stride, long long v_head_stride, void* stream);
@@ -360,7 +360,8 @@ int fattn_cache_read(const fattn_cache* cache, const fattn_cache_batch* batch, v
  * causal it sees keys at or before its position, else every key of the
  * sequence.  A query that sees no key gets o = 0 and lse = -inf.  n_b may
  * exceed lens[b].  Values of keys that a query does not see never reach its
- * row, whatever they are (NaN included).
+ * row, whatever they are (NaN included); an e5m2 infinity, which append never
+ * writes, gives the rows that see it an infinity or NaN.
  * Scores, statistics and sums are fp32.
  * workspace: DEVICE memory of fattn_cache_fwd_workspace_bytes(...) bytes,
  * 256-byte aligned, owned by the caller, its contents on entry do not matter;

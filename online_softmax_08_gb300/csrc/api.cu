@@ -495,7 +495,8 @@ int check_cache_sizes(const fattn_cache* c, const fattn_cache_batch* b) {
   if (c->block_size != 16 && c->block_size != 32 && c->block_size != 64 && c->block_size != 128)
     return FATTN_ERR_UNSUPPORTED;
   if (c->d != 64 && c->d != 128) return FATTN_ERR_UNSUPPORTED;
-  if ((long long)b->table_width * c->block_size >= (1LL << 31) ||
+  // (65536: the kernels look up blocks some tiles ahead, by 32-bit key numbers)
+  if ((long long)b->table_width * c->block_size > (1LL << 31) - 65536 ||
       (long long)c->H * b->total >= (1LL << 31) ||
       (long long)c->num_blocks * c->H >= (1LL << 31) || b->B > (1 << 24))
     return FATTN_ERR_INVALID_ARG;

@@ -15,8 +15,9 @@ enum : uint32_t {
 };
 
 // Division of 0 <= n < 2^31 by a fixed d >= 1 as a multiplication (Granlund and
-// Montgomery, "Division by invariant integers using multiplication"): q = (n + floor(n mul / 2^32)) >> shift with 2^(shift - 1) < d <= 2^shift
-// and mul = floor(2^32 (2^shift - d) / d) + 1.
+// Montgomery, "Division by invariant integers using multiplication"):
+// q = (n + floor(n mul / 2^32)) >> shift with 2^(shift - 1) < d <= 2^shift and
+// mul = floor(2^32 (2^shift - d) / d) + 1.
 struct FastDiv {
   unsigned d, mul, shift;
   FastDiv() = default;

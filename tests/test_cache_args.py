@@ -51,6 +51,7 @@ BAD_BATCH = [(dict(block_table=0), INVALID), (dict(lens=A + 2), INVALID),
              (dict(cu_seqlens=0), INVALID), (dict(B=0), INVALID), (dict(table_width=0), INVALID),
              (dict(total=-1), INVALID), (dict(max_seqlen=9), INVALID),
              (dict(max_seqlen=-1), INVALID), (dict(table_width=1 << 27), INVALID),
+             (dict(table_width=(1 << 27) - 1), INVALID), (dict(table_width=(1 << 27) - 4095), INVALID),
              (dict(total=(1 << 31) - 1, max_seqlen=1), INVALID), (dict(B=1 << 25), INVALID)]
 
 
@@ -84,6 +85,12 @@ def test_overlapping_outputs_are_refused(lib):
         for st, sh in ((256, 64), (64, 512), (1024, 128)):
             assert _read(lib, c, b, kst=st, ksh=sh) == CUDA, (st, sh)
         assert _append(lib, c, b, kst=0, ksh=64) == CUDA  # inputs may be broadcast
+
+
+def test_longest_table(lib):
+    b = _batch(table_width=(1 << 27) - 4096)  # 2^31 - 65536 tokens
+    if not torch.cuda.is_available():  # accepted: the calls go on to the device
+        assert _append(lib, _cache(), b) == _read(lib, _cache(), b) == _fwd(lib, _cache(), b) == CUDA
 
 
 def test_bad_attention_arguments(lib):
