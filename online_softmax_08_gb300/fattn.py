@@ -555,6 +555,8 @@ def cache_forward(q, cache, batch, scale, causal, out=None, workspace=None, stre
             nbytes = _ws_bytes[key] = int(lib.fattn_cache_fwd_workspace_bytes(c, b, Hq))
         workspace = torch.empty((max(nbytes, 256),), dtype=torch.uint8, device=on)
     else:
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError("expected a contiguous workspace on device %d" % dev)
         nbytes = workspace.numel() * workspace.element_size()
     op, ot, oh = _packed(o, total, Hq, d, dev)
     st = lib.fattn_cache_fwd(c, b, qp, qt, qh, op, ot, oh, lse.data_ptr(), Hq, scale,

@@ -467,6 +467,42 @@ def test_nan_in_a_unit_cut_into_pieces(d):
     np.testing.assert_array_equal(np.isnan(o.cpu().double().numpy()), nan)
 
 
+@pytest.mark.parametrize("d,fmt", [(64, "e5m2"), (128, "e4m3")])
+@pytest.mark.parametrize("n,G", [(65, 1), (41, 3), (128, 1)])
+def test_units_of_at_most_128_rows(n, G, d, fmt):
+    """The second subtile has no rows, or few: one tile to many, whole and cut, with an odd
+    and an even number of tiles, ends inside a tile, and the first rows blind."""
+    lens = [n // 2, n, 128, 129, 256, 300, 385, 640, 900, 1025, 3001]
+    c = Case([(n, length - n) for length in lens], 1, d, 32, fmt, seed=n + d).fill()
+    q = _bf16(c.rng, (c.T, G, d), 1.5)
+    cache, batch = c.on_device()
+    for causal in (True, False):
+        o, lse = fattn.cache_forward(q.to(DEV), cache, batch, d ** -0.5, causal)
+        _check_forward(c, q, d ** -0.5, causal, o, lse)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("tile", [0, 1, 2, 3])
+def test_nan_in_values_of_no_weight(d, tile):
+    """A value that is NaN reaches every row that sees it, even one whose weight of that
+    tile is zero: the keys of one tile win by more than fp32 holds."""
+    n, bs = 100, 16
+    c = Case([(n, 500)], 1, d, bs, seed=d + tile).fill()
+    for i in range(128 // bs):  # of the neighbouring tile
+        block = c.table[0, (tile ^ 1) * 128 // bs + i]
+        c.cache["k"][block] = 0x70  # 128
+        c.cache["k_scale"][block] = 1.0
+    at = tile * 128 + 5
+    c.cache["v"][c.table[0, at // bs], 0, at % bs, 11] = 0x7f
+    q = torch.ones((n, 1, d), dtype=torch.bfloat16)
+    cache, batch = c.on_device()
+    o, lse = fattn.cache_forward(q.to(DEV), cache, batch, 1.0, True)
+    nan = np.zeros((n, 1, d), dtype=bool)
+    nan[:, :, 11] = True
+    np.testing.assert_array_equal(np.isnan(o.cpu().double().numpy()), nan)
+    assert bool(torch.isfinite(lse).all())
+
+
 def test_graph_of_a_mixed_batch():
     """Pieces of prompts and single tokens captured together; lengths and offsets move
     between replays, and a replay with fewer tokens leaves the rows behind them alone."""
@@ -735,6 +771,20 @@ def test_other_stream_and_repeatability():
         s.synchronize()
         k2, v2 = fattn.cache_read(cache, batch)
         assert torch.equal(k, k2) and torch.equal(v, v2)
+
+
+def test_workspaces_that_are_refused():
+    c = Case([(1, 20)], 1, 64, 16).fill()
+    q = _bf16(c.rng, (c.T, 2, 64)).to(DEV)
+    cache, batch = c.on_device()
+    big = torch.empty((2, 64 << 20), dtype=torch.uint8, device=DEV)
+    for ws in (torch.empty(64 << 20, dtype=torch.uint8), big[:, ::2]):
+        with pytest.raises(ValueError):
+            fattn.cache_forward(q, cache, batch, 0.125, True, workspace=ws)
+    with pytest.raises(fattn.FattnError):
+        fattn.cache_forward(q, cache, batch, 0.125, True, workspace=big[0, :256])
+    o, lse = fattn.cache_forward(q, cache, batch, 0.125, True, workspace=big[0])
+    _check_forward(c, q.cpu(), 0.125, True, o, lse)
 
 
 def test_workspace_inside_sentinels():
