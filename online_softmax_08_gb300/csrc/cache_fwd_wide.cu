@@ -19,7 +19,7 @@
 // blocks, convert them to fp16 (exact) and store them into the slot in the
 // 128-byte-swizzled layout that a TMA load would leave.  Each warp owns 32 rows of
 // every tile, two pieces of 16 tokens (a piece lies in one block), and has the next
-// tile's codes in flight.
+// tile's codes in flight; block numbers are read 16 to 32 tiles ahead, scales 8 to 24.
 //
 // The scales are applied by the softmax, per piece, as in the kernel for few rows:
 // y = s * ks + log2 vs, p = 2^(y - r) (fp16), l += w p with w = 2^(b - log2 vs),
@@ -80,6 +80,20 @@ __device__ __forceinline__ void add_x2(float a0, float a1, float b0, float b1, f
       "mov.b64 {%0, %1}, s;\n\t}"
       : "=f"(s0), "=f"(s1)
       : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+
+// 16 bytes to shared memory, or zeros
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(on ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t a) {
+  uint4 x;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+               : "r"(a));
+  return x;
 }
 
 template <int D>
@@ -203,11 +217,10 @@ __device__ __forceinline__ void set_blocks(const CacheFwdParams& p, int b, Block
   if (x->seq.n * p.G > p.narrow_rows) x->nb = (x->seq.n + x->tb - 1) / x->tb;
 }
 
-// log2 of the value scale of a sequence's first block, the exponent that its sums are
-// kept relative to (any reference of the scales' size will do)
-__device__ __forceinline__ float unit_base(const CacheFwdParams& p, int b, int h) {
-  const int page = p.c.block_table[(long long)b * p.c.table_width];
-  return page >= 0 && page < p.c.num_blocks ? lg2(p.c.v_scale[(long long)page * p.c.H + h]) : 0.f;
+// The value scale of a sequence's first block, the power that its sums are kept
+// relative to (any reference of the scales' size will do)
+__device__ __forceinline__ float unit_scale(const CacheFwdParams& p, int page, int h) {
+  return page >= 0 && page < p.c.num_blocks ? p.c.v_scale[(long long)page * p.c.H + h] : 1.f;
 }
 
 // Where the rows of pieces go: LSE [places, ROWS], then O [places, ROWS, d], behind the
@@ -411,25 +424,38 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
     // Warp w fills rows [32 w, 32 w + 32) of every slot: two pieces of 16 tokens.
     const int bs = p.c.block_size;
     const int me = warp - C::W_FILL;
-    const float base = n_max > 0 ? unit_base(p, b, h) : 0.f;  // b above
-    // lane i of a set holds the block and scales of this warp's piece i & 1 of tile i / 2
+    float base = 0.f;  // b above
+    // lane i of a set of 16 tiles holds the place and scales of this warp's piece i & 1 of
+    // tile i / 2.  They are fetched in steps, none of which waits for its own loads (in one
+    // step: 16 sequences of 1 to 1000 tokens 82.5 us, against 81.5).
     struct Info {
-      int slice, row;  // page * H + h (-1: nothing visible there), first row in the block
-      float ks, lv;
+      int piece;        // number of its 16 tokens in the pool (-1: nothing visible there)
+      float ks, lv, w;  // as the softmax takes them
     };
-    auto fetch = [&](int j0) {
-      Info r{-1, 0, 0.f, 0.f};
-      const int key = (t0 + j0 + (lane >> 1)) * C::BN + me * 32 + (lane & 1) * 16;
+    auto key_of = [&](int j0) { return (t0 + j0 + (lane >> 1)) * C::BN + me * 32 + (lane & 1) * 16; };
+    auto page_of = [&](int j0) {
+      const int key = key_of(j0);
+      return key < lim_hi ? p.c.block_table[(long long)b * p.c.table_width + (key >> p.c.block_log2)]
+                          : 0;
+    };
+    auto scales_of = [&](int j0, int page) {  // ks, lv: the scales themselves
+      Info r{-1, 1.f, 0.f, 0.f};
+      const int key = key_of(j0);
       if (key >= lim_hi) return r;
-      const int page = p.c.block_table[(long long)b * p.c.table_width + (key >> p.c.block_log2)];
       if (page < 0 || page >= p.c.num_blocks) {
         if (p.c.err) atomicCAS(p.c.err, 0u, (unsigned)ERR_SITE_CACHE_FWD + 1);
         return r;
       }
-      r.slice = page * p.c.H + h;
-      r.row = key & (bs - 1);
-      r.ks = p.c.k_scale[r.slice];
-      r.lv = lg2(p.c.v_scale[r.slice]);
+      const int slice = page * p.c.H + h;
+      r.piece = (slice << (p.c.block_log2 - 4)) + ((key & (bs - 1)) >> 4);  // 1 KB or more each
+      r.ks = p.c.k_scale[slice];
+      r.lv = p.c.v_scale[slice];
+      return r;
+    };
+    auto finish = [&](Info r) {
+      r.ks = r.piece < 0 ? 1.f : r.ks * p.scale_log2;
+      r.lv = r.piece < 0 ? -INFINITY : lg2(r.lv);
+      r.w = r.piece < 0 ? 0.f : ex2(base - r.lv);
       return r;
     };
     constexpr int LD = D / 32;  // 16-byte loads per lane and piece
@@ -443,32 +469,36 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
     // a lane's 16 codes become 32 bytes: two neighbouring 16-byte columns of its row
     const uint32_t lane_dst = (uint32_t)((col16 >> 2) * C::HALF + (me * 32 + row4) * 128);
     uint4 buf[2][2][LD];  // [K, V][piece]
-    auto load = [&](int j, int value, const Info& set) {
+    int at[2];  // the pieces of the next tile
+    auto load = [&](int value) {
 #pragma unroll
       for (int pc = 0; pc < 2; ++pc) {
-        const int from = (j & 15) * 2 + pc;
-        const int slice = __shfl_sync(0xffffffffu, set.slice, from);
-        const int row = __shfl_sync(0xffffffffu, set.row, from);
-        const uint8_t* src = (value ? p.c.v : p.c.k) + ((long long)slice * bs + row) * D + lane_src;
+        const uint8_t* src = (value ? p.c.v : p.c.k) + (long long)at[pc] * (16 * D) + lane_src;
 #pragma unroll
         for (int i = 0; i < LD; ++i)
-          buf[value][pc][i] = slice < 0 ? make_uint4(0u, 0u, 0u, 0u)
-                                        : __ldg(reinterpret_cast<const uint4*>(src + i * ROWS_LD * D));
+          buf[value][pc][i] = at[pc] < 0 ? make_uint4(0u, 0u, 0u, 0u)
+                                         : __ldg(reinterpret_cast<const uint4*>(src + i * ROWS_LD * D));
       }
     };
-    Info now{-1, 0, 0.f, 0.f}, next{-1, 0, 0.f, 0.f};
+    auto look_up = [&](int j, const Info& set) {
+#pragma unroll
+      for (int pc = 0; pc < 2; ++pc) at[pc] = __shfl_sync(0xffffffffu, set.piece, (j & 15) * 2 + pc);
+    };
+    Info now{-1, 1.f, -INFINITY, 0.f}, next = now;
+    int page = 0;
     if (n_max > 0) {
-      now = fetch(0);
-      next = fetch(16);
-      load(0, 0, now);
-      load(0, 1, now);
+      const int page0 = p.c.block_table[(long long)b * p.c.table_width];  // for base
+      now = scales_of(0, page_of(0));
+      const float scale0 = unit_scale(p, page0, h);
+      look_up(0, now);
+      load(0);
+      load(1);
+      base = lg2(scale0);
+      now = finish(now);
     }
     bool ok = true;
     for (int j = 0; ok && j < n_max; ++j) {
       {  // the tile's scales
-        const float ks = __shfl_sync(0xffffffffu, now.ks, (j & 15) * 2 + (lane & 1));
-        const float lv = __shfl_sync(0xffffffffu, now.lv, (j & 15) * 2 + (lane & 1));
-        const int slice = __shfl_sync(0xffffffffu, now.slice, (j & 15) * 2 + (lane & 1));
         // the slot of K_j is free: with it, the scales' (see SCALE_TILES)
         const int i = 2 * j, use = i / ST;
         ok = use == 0 ||
@@ -476,17 +506,15 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
                                                ERR_SITE_CACHE_FWD + 4));
         if (!ok) break;
         const int ring = j % C::SCALE_TILES;
-        if (lane < 2) {
-          scales[ring * C::PIECES + me * 2 + lane] =
-              slice < 0 ? make_float4(1.f, -INFINITY, 0.f, 0.f)
-                        : make_float4(ks * p.scale_log2, lv, ex2(base - lv), 0.f);
+        if ((lane >> 1) == (j & 15)) {
+          scales[ring * C::PIECES + me * 2 + (lane & 1)] = make_float4(now.ks, now.lv, now.w, 0.f);
           mbar_arrive(bar(B_SCALE + ring));
         }
       }
-      if ((j & 15) == 15) {  // the loads below are for the next set's first tile
-        now = next;
-        next = fetch(j + 17);
-      }
+      if ((j & 15) == 0) page = page_of(j + 16);
+      if ((j & 15) == 8) next = scales_of(j + 8, page);
+      if ((j & 15) == 15) now = finish(next);  // the loads below are for its first tile
+      look_up(j + 1, now);
 #pragma unroll
       for (int value = 0; value < 2; ++value) {
         const int i = 2 * j + value, use = i / ST;
@@ -535,7 +563,7 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
         fence_proxy_async_smem();  // the MMAs read through the async proxy
         __syncwarp();
         if (lane == 0) mbar_arrive(kv_full0 + 8u * kv_slot);
-        if (j + 1 < n_max) load(j + 1, value, now);
+        if (j + 1 < n_max) load(value);
       }
     }
     __syncwarp();
@@ -667,7 +695,8 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
     const uint32_t tS = tmem + lane_off + C::TM_S + s * 128;
     const uint32_t tO = tmem + lane_off + C::TM_O + s * D;
     const uint32_t tP = tmem + lane_off + C::TM_P + s * C::P_STRIDE;
-    float base = my_nt > 0 ? unit_base(p, b, h) : 0.f;  // needed at the end only
+    // the first block, for b above, which is needed at the end only
+    const int page0 = my_nt > 0 ? p.c.block_table[(long long)b * p.c.table_width] : -1;
     // A row of q and o is LPR pieces of 16 bytes; a warp moves RPI of its 32 rows at a
     // time, piece by lane (a thread that moved its own row would touch 32 lines with
     // every instruction).
@@ -688,64 +717,50 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
       const int r = (warp & 3) * 32 + i * RPI + sub;
       return rows_smem + r * 128 + (((piece & 7) ^ (r & 7)) << 4);
     };
-    // Q: a row times the power of two that brings its largest element to [2^14, 2^15),
-    // as fp16 (exact down to 2^-29 of that element, the quantum below it 2^-39)
+    // Q: copied as it is, then each thread multiplies its row by the power of two that
+    // brings its largest element to [2^14, 2^15), as fp16 in place (exact down to 2^-29 of
+    // that element, the quantum below it 2^-39).
     // (Loops that run once per piece are kept short: straight-line code of their length
     // is bound by its instruction fetches.)
-    float back = 1.f;  // of this thread's row
-    uint4 ahead[4];  // the next four pieces
-    auto load_q = [&](int i0) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const long long off = __shfl_sync(0xffffffffu, q_off, (i0 + i) * RPI + sub);
-        ahead[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (off >= 0) ahead[i] = *reinterpret_cast<const uint4*>(p.q.p + off + 8 * piece);
-      }
+#pragma unroll 4
+    for (int i = 0; i < IT; ++i) {
+      const long long off = __shfl_sync(0xffffffffu, q_off, i * RPI + sub);
+      copy16_async(row_piece(i), p.q.p + (off >= 0 ? off + 8 * piece : 0), off >= 0);
+    }
+    float scale0 = unit_scale(p, page0, h);
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncwarp();
+    auto own_piece = [&](int k) {
+      return sbase + C::OFF_Q + s * C::TILE + (k >> 3) * C::HALF + t * 128 +
+             (((k & 7) ^ (t & 7)) << 4);
     };
-    load_q(0);
-#pragma unroll 1
-    for (int i0 = 0; i0 < IT; i0 += 4) {
-      uint4 v[4];
+    uint32_t m2 = 0u;  // the largest elements in the halves of the words
+#pragma unroll 4
+    for (int k = 0; k < D / 8; ++k) {
+      const uint4 x = ld_shared_v4(own_piece(k));
+      m2 = __vmaxu2(m2, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
+                                 __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
+    }
+    const uint32_t mx = max(m2 & 0xffffu, m2 >> 16);
+    int e = (int)(mx >> 7);
+    e = (mx == 0u || e == 255) ? 0 : min(14 - (e - 127), 126);
+    const float mul = __uint_as_float((uint32_t)(e + 127) << 23);
+    const float back = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll 2
+    for (int k = 0; k < D / 8; ++k) {
+      const uint4 x = ld_shared_v4(own_piece(k));
+      const uint32_t* w = &x.x;
+      uint32_t o[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = ahead[i];
-      if (i0 + 4 < IT) load_q(i0 + 4);
-#pragma unroll
-      for (int i = 0; i < 4; i += 2) {  // two rows' maxima in the halves of a word
-        uint32_t m2[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const uint4 x = v[i + k];
-          const uint32_t m = __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
-                                      __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
-          m2[k] = max(m & 0xffffu, m >> 16);
-        }
-        uint32_t m = m2[0] | m2[1] << 16;
-#pragma unroll
-        for (int w = 1; w < LPR; w <<= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, w));
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const uint32_t mx = k ? m >> 16 : m & 0xffffu;
-          int e = (int)(mx >> 7);
-          e = (mx == 0u || e == 255) ? 0 : min(14 - (e - 127), 126);
-          const float mul = __uint_as_float((uint32_t)(e + 127) << 23);
-          const float own = __shfl_sync(0xffffffffu, __uint_as_float((uint32_t)(127 - e) << 23),
-                                        (lane % RPI) * LPR);
-          if (lane / RPI == i0 + i + k) back = own;
-          const uint32_t* w = &v[i + k].x;
-          uint32_t o[4];
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            asm("cvt.rn.f16x2.f32 %0, %1, %2;"
-                : "=r"(o[x])
-                : "f"(__uint_as_float(w[x] & 0xffff0000u) * mul),
-                  "f"(__uint_as_float(w[x] << 16) * mul));
-          st_shared_v4(row_piece(i0 + i + k), o[0], o[1], o[2], o[3]);
-        }
-      }
+      for (int i = 0; i < 4; ++i)
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;"
+            : "=r"(o[i])
+            : "f"(__uint_as_float(w[i] & 0xffff0000u) * mul), "f"(__uint_as_float(w[i] << 16) * mul));
+      st_shared_v4(own_piece(k), o[0], o[1], o[2], o[3]);
     }
     fence_proxy_async_smem();
     mbar_arrive(bar(B_Q));
-    asm volatile("" : "+f"(base));  // loaded by now, not behind the loop
+    asm volatile("" : "+f"(scale0));  // loaded by now, not behind the loop
 
     float r_run = -INFINITY, l_run = 0.f;  // the reference r, and l
     for (int j = 0; j < my_nt; ++j) {
@@ -860,6 +875,7 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
     }
 
     // ------------------------------------------------------------ epilogue
+    const float base = lg2(scale0);
     const bool has = my_nt > 0 && !(l_run == 0.f);
     const float inv = has ? 1.f / l_run : 0.f, up = ex2(base);
     const float lse = has ? (r_run - base + lg2(l_run)) * kLn2 : -INFINITY;
@@ -889,9 +905,7 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
           for (int e = 0; e < 4; ++e)
             x[e] = pack_bf16x2(__uint_as_float(o[q4 * 8 + 2 * e]),
                                __uint_as_float(o[q4 * 8 + 2 * e + 1]));
-          st_shared_v4(sbase + C::OFF_Q + s * C::TILE + (k >> 3) * C::HALF + t * 128 +
-                           (((k & 7) ^ (t & 7)) << 4),
-                       x[0], x[1], x[2], x[3]);
+          st_shared_v4(own_piece(k), x[0], x[1], x[2], x[3]);
         }
       } else if (valid) {
 #pragma unroll
@@ -904,10 +918,7 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
       __syncwarp();
 #pragma unroll 4
       for (int i = 0; i < IT; ++i) {
-        uint4 x;
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
-                     : "r"(row_piece(i)));
+        const uint4 x = ld_shared_v4(row_piece(i));
         const long long off = __shfl_sync(0xffffffffu, o_off, i * RPI + sub);
         if (off >= 0) *reinterpret_cast<uint4*>(p.o.p + off + 8 * piece) = x;
       }
