@@ -67,6 +67,7 @@ struct CacheFwdParams {
                      // than this go to the 256-row tcgen05 kernel, the others to the split one
   int wide_tokens;   // tokens per row block of the 256-row kernel: 256 / G
   int wide_ctas;     // CTAs of it that run at a time: one per SM
+  int wide_grid;     // CTAs of it
   void* workspace;   // of the split kernel
   void* wide_workspace;
 };
@@ -107,6 +108,10 @@ size_t cache_fwd_workspace(const CacheParams& c, int G, int n_sm);
 cudaError_t launch_cache_fwd(const CUtensorMap& tk, const CUtensorMap& tv, const CacheFwdParams& p,
                              int n_sm, cudaStream_t stream);
 int cache_fwd_wide_rows();  // rows per unit of the 256-row kernel
+// CTAs that the 256-row kernel is launched with for the sequences of more than
+// narrow_rows rows, and the bytes of their pieces' descriptors
+long long cache_fwd_wide_grid(const CacheParams& c, int G, int narrow_rows, int n_sm);
+size_t cache_fwd_wide_plan_bytes(long long grid);
 cudaError_t launch_cache_fwd_wide(const CacheFwdParams& p, cudaStream_t stream);
 
 // Two 8-bit codes (low byte first) -> two fp16 values (low half first), exact.

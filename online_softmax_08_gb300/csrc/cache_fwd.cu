@@ -903,7 +903,10 @@ bool takes_wide(const CacheParams& c, int G, int n_sm) {
 
 size_t cache_fwd_workspace(const CacheParams& c, int G, int n_sm) {
   return narrow_bytes(c.d, n_sm) +
-         (takes_wide(c, G, n_sm) ? pieces_bytes((size_t)n_sm, cache_fwd_wide_rows(), c.d) : 0);
+         (takes_wide(c, G, n_sm) ? pieces_bytes((size_t)n_sm, cache_fwd_wide_rows(), c.d) +
+                                       cache_fwd_wide_plan_bytes(cache_fwd_wide_grid(
+                                           c, G, narrow_limit(c, n_sm), n_sm))
+                                 : 0);
 }
 
 cudaError_t launch_cache_fwd(const CUtensorMap& tk, const CUtensorMap& tv,
@@ -914,6 +917,9 @@ cudaError_t launch_cache_fwd(const CUtensorMap& tk, const CUtensorMap& tv,
   if (wide) {
     p.wide_tokens = cache_fwd_wide_rows() / p.G;
     p.wide_ctas = n_sm;
+    const long long grid = cache_fwd_wide_grid(p.c, p.G, p.narrow_rows, n_sm);
+    if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    p.wide_grid = (int)grid;
     p.wide_workspace = static_cast<char*>(p.workspace) + narrow_bytes(p.c.d, n_sm);
     const cudaError_t e = launch_cache_fwd_wide(p, stream);
     if (e != cudaSuccess) return e;

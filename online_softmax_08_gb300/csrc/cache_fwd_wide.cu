@@ -35,11 +35,13 @@
 // TFLOP/s, tensor pipe 50 % active.  256 units on 152 SMs are two rounds where 1.7
 // would do (16 %); a tile of 128 keys takes 3100 clocks against the MMAs' 2048, the
 // MMA warp's own issue (1750) and its waits for P (1350) alternating; the start and
-// end of a piece take 15,000 and 4,000 clocks of 250,000.  At d = 64 (16 sequences of
+// end of a piece take 11,000 and 5,000 clocks of 250,000.  At d = 64 (16 sequences of
 // 1 to 1000 tokens behind 300 to 7000, 16 heads) a tile takes 2200 to 2900 clocks,
-// bound by the softmax, and the starts are a fifth of the time.
+// bound by the softmax, and the starts and ends are a fifth of the time.
 #define FATTN_INLINE_WAIT_SLOW_PATH
 #include <math.h>
+
+#include <algorithm>
 
 #include "cache.cuh"
 
@@ -149,73 +151,13 @@ static_assert(Wide<64>::STAGES <= 7 && Wide<128>::STAGES <= 7, "reuse of the sca
 
 // A piece of a unit: tiles [t0, t0 + max(c0, c1)) of it, of which subtile s sees the
 // first c_s.
-struct Segment {
+struct __align__(16) Segment {
   int row0, n, len, b;  // the sequence
   int h, rb;            // head, row block (tb tokens each)
   int t0, c0, c1;
   int part;             // -1: the whole unit; else where its rows go in the workspace
-  int on;               // 0: nothing to do
+  int unused[2];
 };
-
-// sum over i < n of floor((a i + b) / m), by the Euclidean reduction of (a, m).
-// a n + b < 2^32 (keys of a sequence), which the reduction only lowers.
-__device__ __forceinline__ long long floor_sum(unsigned n, unsigned m, unsigned a, unsigned b) {
-  long long r = 0;
-  while (n > 0) {
-    if (a >= m) {
-      r += (long long)n * (n - 1) / 2 * (a / m);
-      a %= m;
-    }
-    if (b >= m) {
-      r += (long long)n * (b / m);
-      b %= m;
-    }
-    const unsigned top = a * n + b;
-    if (top < m) break;
-    n = top / m;
-    b = top % m;
-    const unsigned x = m;
-    m = a;
-    a = x;
-  }
-  return r;
-}
-
-// The units of one sequence: nb row blocks of tb tokens, for each of H heads.
-struct Blocks {
-  CacheSeq seq;
-  int nb, tb;
-  int causal;
-  // keys that the last row of block rb sees
-  __device__ __forceinline__ int limit(int rb) const {
-    const int l = causal ? seq.len - seq.n + min(seq.n, (rb + 1) * tb) : seq.len;
-    return max(0, l);
-  }
-  // parts of at most m keys in block rb; one that sees nothing counts as one, to be written
-  __device__ __forceinline__ int parts(int rb, unsigned m) const {
-    return max(1, (int)(((unsigned)limit(rb) + m - 1) / m));
-  }
-  // of blocks 0 .. rb - 1
-  __device__ __forceinline__ long long before(int rb, unsigned m) const {
-    if (!causal) return (long long)rb * parts(0, m);
-    long long r = 0;
-    if (rb == nb) r += parts(--rb, m);
-    const int c = seq.len - seq.n + tb;  // limit(i) = c + i tb for i < nb - 1
-    const int blind = c > 0 ? 0 : min(rb, -c / tb + 1);
-    if (rb > blind) r += floor_sum(rb - blind, m, tb, (unsigned)(c + blind * tb) + m - 1);
-    return r + blind;
-  }
-};
-__device__ __forceinline__ void set_blocks(const CacheFwdParams& p, int b, Blocks* x) {
-  x->nb = 0;
-  x->tb = p.wide_tokens;
-  x->causal = p.causal;
-  if (!cache_seq(p.c, b, &x->seq)) {
-    if (p.c.err) atomicCAS(p.c.err, 0u, (unsigned)ERR_SITE_CACHE_FWD);
-    return;
-  }
-  if (x->seq.n * p.G > p.narrow_rows) x->nb = (x->seq.n + x->tb - 1) / x->tb;
-}
 
 // The value scale of a sequence's first block, the power that its sums are kept
 // relative to (any reference of the scales' size will do)
@@ -235,7 +177,185 @@ __device__ __forceinline__ PieceView piece_view(const CacheFwdParams& p) {
   return PieceView{lse, lse + (size_t)p.wide_ctas * 2 * Wide<128>::ROWS};
 }
 
+// Behind them: the number of pieces (256 bytes), then the pieces.
+struct PlanView {
+  int* pieces;
+  Segment* seg;
+};
+__device__ __forceinline__ PlanView plan_view(const CacheFwdParams& p, int d) {
+  char* at = reinterpret_cast<char*>(piece_view(p).o + (size_t)p.wide_ctas * 2 * Wide<128>::ROWS * d);
+  return PlanView{reinterpret_cast<int*>(at), reinterpret_cast<Segment*>(at + 256)};
+}
+
 constexpr int kMinTiles = 8;  // a piece of fewer tiles would not repay its start and merge
+
+// The plan: one CTA writes a descriptor for each piece, in about 4 us, behind which a
+// piece starts 0.7 us after its CTA.  (With every CTA of the attention finding its own
+// piece that took 3 to 5 us each time: 16 sequences of 1 to 1000 tokens, two rounds of
+// CTAs, 81.5 us against 79.0; 116 of 1320 tokens, one head of two, nine rounds, 192 us
+// against 165.  With 1024 threads instead of 256 the plan took 1.5 us longer.)
+// Sequences and their row blocks are taken from the last, which sees the most keys, to
+// the first, a block's pieces head by head; 256 sequences at a time, then 256 of their
+// row blocks.  Two passes: all tiles, which give the pieces' size, and the pieces.
+struct Plan {
+  static constexpr int T = 256;
+  long long part[T / 32];
+  long long start[T];            // row blocks of the sequences before
+  int row0[T], n[T], len[T];
+  long long first[T];            // pieces of the row blocks before
+  int seq[T], rb[T], tiles[T];   // of a row block
+};
+
+// the sum of v over the threads before this one, and over all
+__device__ __noinline__ long long sum_before(long long v, long long* part, long long* total) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  long long upto = v;
+#pragma unroll
+  for (int w = 1; w < 32; w <<= 1) {
+    const long long o = __shfl_up_sync(0xffffffffu, upto, w);
+    if (lane >= w) upto += o;
+  }
+  if (lane == 31) part[warp] = upto;
+  __syncthreads();
+  long long all = lane < Plan::T / 32 ? part[lane] : 0, low = lane < warp ? all : 0;
+#pragma unroll
+  for (int w = Plan::T / 64; w > 0; w >>= 1) {
+    all += __shfl_xor_sync(0xffffffffu, all, w);
+    low += __shfl_xor_sync(0xffffffffu, low, w);
+  }
+  __syncthreads();
+  *total = __shfl_sync(0xffffffffu, all, 0);
+  return upto - v + __shfl_sync(0xffffffffu, low, 0);
+}
+// the last i < n with at[i] <= x, of ascending at with at[0] <= x
+__device__ __forceinline__ int last_at_most(const long long* at, int n, long long x) {
+  int lo = 0;
+  while (n - lo > 1) {
+    const int mid = (lo + n) >> 1;
+    if (at[mid] <= x)
+      lo = mid;
+    else
+      n = mid;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(Plan::T) cache_fwd_plan_kernel(const CacheFwdParams p) {
+  constexpr int BN = Wide<128>::BN, BM = Wide<128>::BM;
+  static_assert(Wide<64>::BN == BN && Wide<64>::BM == BM, "tile");
+  extern __shared__ uint8_t smem_raw[];
+  Plan& plan = *reinterpret_cast<Plan*>(smem_raw);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int B = p.c.B, H = p.c.H, G = p.G, tb = p.wide_tokens, T = Plan::T, t = threadIdx.x;
+  const PlanView out = plan_view(p, p.c.d);
+  Record* records = reinterpret_cast<Record*>(p.wide_workspace);
+  for (int i = t; i < p.wide_ctas; i += T) records[i] = Record{0, 0, 0, 0, 0, 0};
+  long long tiles = 0, blocks = 0, pieces = 0, most = 0, ng = 0;
+  bool room = true;
+  int mine = 0;  // tiles of this thread's row block
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+    blocks = 0;
+#pragma unroll 1
+    for (int c0 = 0; c0 < B; c0 += T) {
+      if (pass == 0 || B > T) {
+        CacheSeq x{};
+        int nb = 0;
+        if (c0 + t < B) {
+          if (!cache_seq(p.c, B - 1 - c0 - t, &x)) {
+            if (p.c.err) atomicCAS(p.c.err, 0u, (unsigned)ERR_SITE_CACHE_FWD);
+          } else if (x.n * G > p.narrow_rows) {
+            nb = (x.n + tb - 1) / tb;
+          }
+        }
+        __syncthreads();  // the last ones have been read
+        plan.row0[t] = x.row0, plan.n[t] = x.n, plan.len[t] = x.len;
+        plan.start[t] = sum_before(nb, plan.part, &ng);
+      }
+#pragma unroll 1
+      for (long long g0 = 0; g0 < ng; g0 += T) {
+        const bool on = g0 + t < ng;
+        if (pass == 0 || B > T || ng > T) {
+          __syncthreads();
+          mine = 0;
+        }
+        if (on && (pass == 0 || B > T || ng > T)) {
+          const int seq = last_at_most(plan.start, min(T, B - c0), g0 + t);
+          const int n = plan.n[seq], len = plan.len[seq];
+          const int rb = (n + tb - 1) / tb - 1 - (int)(g0 + t - plan.start[seq]);
+          const int limit = max(1, p.causal ? len - n + min(n, (rb + 1) * tb) : len);
+          // (one that sees nothing counts as one tile, to be written)
+          mine = (limit + BN - 1) / BN;
+          plan.seq[t] = seq, plan.rb[t] = rb, plan.tiles[t] = mine;
+        }
+        if (pass == 0) {
+          tiles += mine;
+          continue;
+        }
+        // parts of a unit: at most one more than the SMs, so the products below stay
+        // below 2^32
+        auto parts_of = [&](int n) {
+          return n <= most ? 1 : (int)(((unsigned)n + (unsigned)most - 1) / (unsigned)most);
+        };
+        long long all;
+        plan.first[t] = sum_before(on ? (long long)parts_of(mine) * H : 0, plan.part, &all);
+        __syncthreads();
+        // the grid has room for every batch whose offsets ascend
+        room = room && pieces + all <= p.wide_grid;
+        if (!room) {
+          if (t == 0 && p.c.err) atomicCAS(p.c.err, 0u, (unsigned)ERR_SITE_CACHE_FWD);
+          all = 0;
+        }
+        for (int i = t; i < all; i += T) {
+          const int x = last_at_most(plan.first, (int)min((long long)T, ng - g0), i);
+          const int seq = plan.seq[x], rb = plan.rb[x], n_tiles = plan.tiles[x];
+          const int k = parts_of(n_tiles);
+          int h = i - (int)plan.first[x], part = 0, take = n_tiles;
+          const int n = plan.n[seq], len = plan.len[seq];
+          Segment g{};
+          g.row0 = plan.row0[seq], g.n = n, g.len = len, g.b = B - 1 - c0 - seq;
+          if (k > 1) {
+            part = h % k, h /= k;
+            g.t0 = (int)((unsigned)part * (unsigned)n_tiles / (unsigned)k);
+            take = (int)((unsigned)(part + 1) * (unsigned)n_tiles / (unsigned)k) - g.t0;
+          }
+          g.h = h, g.rb = rb;
+          // tiles that the subtiles see: up to their last row's limit
+          const int rows = min(tb, n - rb * tb) * G;
+          auto sees = [&](int last_row) {
+            const int j = rb * tb + p.by_G.div(last_row);
+            return (max(0, p.causal ? len - n + j + 1 : len) + BN - 1) / BN;
+          };
+          g.c0 = max(0, min(take, sees(min(rows, BM) - 1) - g.t0));
+          g.c1 = rows > BM ? max(0, min(take, sees(rows - 1) - g.t0)) : 0;
+          // A unit of k > 1 pieces owns k - 1 records and 2 (k - 1) >= k places for rows,
+          // counted over the units before it: at most one record and two places per SM
+          const long long place =
+              pieces + plan.first[x] + (long long)h * k - ((blocks + g0 + x) * H + h);
+          g.part = -1;
+          if (k > 1) {
+            g.part = (int)(2 * place) + part;
+            if (part == 0 && place < p.wide_ctas)
+              records[place] = Record{k, rows, h, g.row0, rb * tb * G, (int)(2 * place)};
+          }
+          out.seg[pieces + i] = g;
+        }
+        pieces += all;
+      }
+      blocks += ng;
+    }
+    if (pass == 0) {
+      sum_before(tiles, plan.part, &tiles);
+      tiles *= H;
+      // (a 64-bit division takes ten times as long)
+      const long long share = tiles < 0x7fffffff
+                                  ? ((unsigned)tiles + p.wide_ctas - 1) / (unsigned)p.wide_ctas
+                                  : (tiles + p.wide_ctas - 1) / p.wide_ctas;
+      most = max((long long)kMinTiles, share);
+    }
+  }
+  if (t == 0) *out.pieces = (int)pieces;
+}
 
 template <int D, bool E5M2>
 __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
@@ -250,6 +370,10 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
   const int G = p.G;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the plan
+  const PlanView plan = plan_view(p, D);
+  const Segment seg = plan.seg[blockIdx.x];
+  if ((int)blockIdx.x >= *plan.pieces) return;
   const uint32_t bar0 = sbase + C::OFF_BAR;
   auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
   const uint32_t kv_full0 = bar(B_KV_FULL), kv_empty0 = bar(B_KV_FULL + ST);
@@ -282,136 +406,19 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
     tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
     tmem_relinquish();
   }
-  __shared__ Segment seg_slot;
-  if (warp == 0) {
-    // ---------------------------------------------------------------- which piece
-    const int B = p.c.B, H = p.c.H;
-    Blocks x;
-    long long tiles = 0, units = 0;
-    int largest = 0;
-    for (int b0 = lane; b0 < B; b0 += 32) {
-      set_blocks(p, b0, &x);
-      if (x.nb > 0) {
-        tiles += x.before(x.nb, C::BN) * H;
-        units += (long long)x.nb * H;
-        largest = max(largest, x.parts(x.nb - 1, C::BN));  // the last block sees the most
-      }
-    }
-    largest = __reduce_max_sync(0xffffffffu, largest);
-#pragma unroll
-    for (int w = 16; w > 0; w >>= 1) {
-      tiles += __shfl_xor_sync(0xffffffffu, tiles, w);
-      units += __shfl_xor_sync(0xffffffffu, units, w);
-    }
-    // (a 64-bit division takes ten times as long)
-    const long long share = tiles < 0x7fffffff
-                                ? ((unsigned)tiles + p.wide_ctas - 1) / (unsigned)p.wide_ctas
-                                : (tiles + p.wide_ctas - 1) / p.wide_ctas;
-    const long long most = max((long long)kMinTiles, share);
-    const bool cut = largest > most;  // some unit is
-    const unsigned m = cut ? (unsigned)(most * C::BN) : 0x7fffffffu;  // keys of a piece
-    long long pieces = units;
-    if (cut) {
-      pieces = 0;
-      for (int b0 = lane; b0 < B; b0 += 32) {
-        if (B > 32) set_blocks(p, b0, &x);
-        if (x.nb > 0) pieces += x.before(x.nb, m) * H;
-      }
-#pragma unroll
-      for (int w = 16; w > 0; w >>= 1) pieces += __shfl_xor_sync(0xffffffffu, pieces, w);
-    }
-    // the grid has room for every batch whose offsets ascend
-    if (pieces > gridDim.x) {
-      if (lane == 0 && p.c.err) atomicCAS(p.c.err, 0u, (unsigned)ERR_SITE_CACHE_FWD);
-      pieces = units = 0;
-    }
-    Segment g{};
-    // records that no cut unit uses
-    const long long extra = pieces - units;
-    Record* records = reinterpret_cast<Record*>(p.wide_workspace);
-    if (lane == 0 && blockIdx.x >= extra && blockIdx.x < p.wide_ctas)
-      records[blockIdx.x] = Record{0, 0, 0, 0, 0, 0};
-    long long pos = pieces - 1 - blockIdx.x;  // the later ones, which see more keys, first
-    if (pos >= 0) {
-      long long before = 0, units_before = 0;
-      for (int b0 = 0; b0 < B; b0 += 32) {
-        long long mine = 0, own = 0;
-        if (b0 + lane < B) {
-          if (B > 32) set_blocks(p, b0 + lane, &x);
-          if (x.nb > 0) {
-            own = (long long)x.nb * H;
-            mine = cut ? x.before(x.nb, m) * H : own;
-          }
-        }
-        long long upto = mine, u = own;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const long long o = __shfl_up_sync(0xffffffffu, upto, d);
-          const long long v = __shfl_up_sync(0xffffffffu, u, d);
-          if (lane >= d) upto += o, u += v;
-        }
-        const unsigned past = __ballot_sync(0xffffffffu, before + upto > pos);
-        if (past) {
-          const int src = __ffs(past) - 1;
-          before = __shfl_sync(0xffffffffu, before + upto - mine, src);
-          units_before += __shfl_sync(0xffffffffu, u - own, src);
-          g.b = b0 + src;
-          break;
-        }
-        before += __shfl_sync(0xffffffffu, upto, 31);
-        units_before += __shfl_sync(0xffffffffu, u, 31);
-      }
-      set_blocks(p, g.b, &x);
-      auto block_start = [&](int i) { return (cut ? x.before(i, m) : (long long)i) * H; };
-      const int rb = cut ? warp_search(x.nb, pos - before, block_start)
-                         : (int)((unsigned)(pos - before) / (unsigned)H);  // < the grid
-      before += block_start(rb);
-      const int k = cut ? x.parts(rb, m) : 1, rest = (int)(pos - before);
-      const int h = rest / k, part = rest % k;
-      const long long base = before + (long long)h * k - (units_before + (long long)rb * H + h);
-      const int n_tiles = x.parts(rb, C::BN);
-      // k is at most one more than the SMs, so the products stay below 2^32
-      const int t0 = (int)((unsigned)part * (unsigned)n_tiles / (unsigned)k);
-      const int take = (int)((unsigned)(part + 1) * (unsigned)n_tiles / (unsigned)k) - t0;
-      // tiles that the subtiles see: up to their last row's limit
-      const int rows = min(x.tb, x.seq.n - rb * x.tb) * G;
-      auto sees = [&](int last_row) {
-        const int i = rb * x.tb + p.by_G.div(last_row);
-        const int l = p.causal ? x.seq.len - x.seq.n + i + 1 : x.seq.len;
-        return (max(0, l) + C::BN - 1) / C::BN;
-      };
-      const int n0 = sees(min(rows, C::BM) - 1), n1 = rows > C::BM ? sees(rows - 1) : 0;
-      g.row0 = x.seq.row0, g.n = x.seq.n, g.len = x.seq.len;
-      g.h = h, g.rb = rb, g.t0 = t0;
-      g.c0 = max(0, min(take, n0 - t0));
-      g.c1 = max(0, min(take, n1 - t0));
-      // A unit of k > 1 pieces owns k - 1 records and 2 (k - 1) >= k places for rows,
-      // counted over the units before it: at most one record and two places per SM
-      g.part = k > 1 ? (int)(2 * base) + part : -1;
-      g.on = 1;
-      if (lane == 0 && k > 1 && part < k - 1)
-        records[base + part] = part > 0 ? Record{0, 0, 0, 0, 0, 0}
-                                        : Record{k, rows, h, g.row0, rb * x.tb * G, (int)(2 * base)};
-    }
-    if (lane == 0) seg_slot = g;
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  if (seg_slot.on == 0) {
-    if (warp == C::W_MMA) tmem_dealloc(tmem, C::TMEM_COLS);
-    return;
-  }
-  const int b = seg_slot.b, h = seg_slot.h, t0 = seg_slot.t0, rb = seg_slot.rb;
-  const int len = seg_slot.len, n_new = seg_slot.n, row0 = seg_slot.row0, part = seg_slot.part;
+  const int b = seg.b, h = seg.h, t0 = seg.t0, rb = seg.rb;
+  const int len = seg.len, n_new = seg.n, row0 = seg.row0, part = seg.part;
   const int n_rows = min(p.wide_tokens, n_new - rb * p.wide_tokens) * G;  // of the unit
   // keys seen by row r of the unit
   const int seen0 = p.causal ? len - n_new + rb * p.wide_tokens + 1 : len;
   auto limit_of = [&](int r) {
     return max(0, min(len, p.causal ? seen0 + p.by_G.div(r) : seen0));
   };
-  const int nt0 = seg_slot.c0, nt1 = seg_slot.c1;
+  const int nt0 = seg.c0, nt1 = seg.c1;
   const int n_max = max(nt0, nt1);
   const int lim_lo = limit_of(0), lim_hi = limit_of(n_rows - 1);
 
@@ -980,18 +987,36 @@ cudaError_t launch(const CacheFwdParams& p, cudaStream_t stream) {
     return fa.numRegs >= C::REG_LAUNCH ? cudaSuccess : cudaErrorInvalidConfiguration;
   });
   if (e != cudaSuccess) return e;
-  // room for every unit, and for the cuts: a unit of t tiles has at most
-  // 1 + t / (all tiles / SMs) pieces
-  const long long ctas =
-      ((long long)p.c.total / p.wide_tokens + p.c.B) * p.c.H + p.wide_ctas;
-  if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  cache_fwd_wide_kernel<D, E5M2><<<(unsigned)ctas, C::THREADS, C::SMEM, stream>>>(p);
-  return cudaGetLastError();
+  cache_fwd_plan_kernel<<<1, Plan::T, sizeof(Plan), stream>>>(p);
+  const cudaError_t r = cudaGetLastError();
+  if (r != cudaSuccess) return r;
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((unsigned)p.wide_grid);
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, cache_fwd_wide_kernel<D, E5M2>, p);
 }
 
 }  // namespace
 
 int cache_fwd_wide_rows() { return Wide<128>::ROWS; }
+
+// Room for every unit, and for the cuts: a unit of t tiles has at most
+// 1 + t / (all tiles / SMs) pieces.  A sequence of n > narrow_rows / G tokens has
+// ceil(n / tb) <= n / tb + 1 row blocks, which is also at most n / least for n <= tb and
+// 2 n / (tb + 1) for n > tb.  (A CTA without a piece costs about 1 us of an SM.)
+long long cache_fwd_wide_grid(const CacheParams& c, int G, int narrow_rows, int n_sm) {
+  const long long total = c.total, tb = cache_fwd_wide_rows() / G, least = narrow_rows / G + 1;
+  const long long blocks = std::min(total / tb + c.B, std::max(total / least, 2 * total / (tb + 1)));
+  return blocks * c.H + n_sm;
+}
+size_t cache_fwd_wide_plan_bytes(long long grid) { return 256 + (size_t)grid * sizeof(Segment); }
 
 cudaError_t launch_cache_fwd_wide(const CacheFwdParams& p, cudaStream_t stream) {
   if (p.c.d == 128) return p.c.format ? launch<128, true>(p, stream) : launch<128, false>(p, stream);
