@@ -158,6 +158,7 @@ struct __align__(16) Segment {
   int part;             // -1: the whole unit; else where its rows go in the workspace
   int unused[2];
 };
+static_assert(sizeof(Segment) == 48, "three 16-byte loads");
 
 // The value scale of a sequence's first block, the power that its sums are kept
 // relative to (any reference of the scales' size will do)
@@ -372,8 +373,13 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the plan
   const PlanView plan = plan_view(p, D);
-  const Segment seg = plan.seg[blockIdx.x];
-  if ((int)blockIdx.x >= *plan.pieces) return;
+  Segment seg;
+  {
+    const int4* from = reinterpret_cast<const int4*>(plan.seg + blockIdx.x);
+    const int4 x = __ldcg(from), y = __ldcg(from + 1), z = __ldcg(from + 2);
+    seg = Segment{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w, z.x, z.y, {}};
+  }
+  if ((int)blockIdx.x >= __ldcg(plan.pieces)) return;
   const uint32_t bar0 = sbase + C::OFF_BAR;
   auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
   const uint32_t kv_full0 = bar(B_KV_FULL), kv_empty0 = bar(B_KV_FULL + ST);

@@ -280,6 +280,10 @@ FORWARD = [
     # a unit of the 256-row kernel cut into pieces
     ([(130, 3000), (1, 70), (70, 5000)], 1, 1, 64, 64, "e4m3", True),
     ([(33, 2600)], 1, 3, 128, 16, "e4m3", False),
+    # more than 256 sequences or row blocks for its plan, whole and with one that is cut
+    ([(40, i % 90) for i in range(300)], 1, 1, 64, 16, "e4m3", True),
+    ([(600, 2000)] + [(40 if i % 3 else 1, i) for i in range(280)], 1, 1, 64, 32, "e5m2", True),
+    ([(520, 7)], 1, 128, 64, 64, "e4m3", True),
 ]
 
 
