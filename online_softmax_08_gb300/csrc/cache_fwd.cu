@@ -887,9 +887,11 @@ size_t narrow_bytes(int d, int n_sm) {  // the larger of the two variants
 // The most query rows per key/value head (tokens x grouped heads) of a sequence that
 // stays with the kernel above.  From 33 rows on it reads the keys three times and
 // more, and the 256-row kernel costs less of the machine, but finishes a small batch
-// later.  Measured at d = 64: 16 sequences of 1 to 1000 tokens, 16 key heads, 83 us
-// with a limit of 32 rows and 110 us with 64; 24 sequences of 5 tokens, 2 key heads of
-// 8 query heads, 23 us and 17 us.
+// later.  Measured with limits of 32 and 64 rows: 16 sequences of 1 to 1000 tokens, 16
+// key heads, d = 64, 79 and 102 us; 150 of 50 to 100 tokens, 4 heads, d = 128, 82 and
+// 148 us; 24 of 5 tokens, 2 key heads of 8 query heads, d = 64, 24 and 17 us.  (Many
+// sequences of very few keys lose by it, 134 of 7 keys, 8 heads of 7, 59 and 34 us: their
+// lengths are not known on the host.)
 int narrow_limit(const CacheParams& c, int n_sm) {
   return (long long)c.B * c.H >= n_sm ? 32 : 64;
 }
