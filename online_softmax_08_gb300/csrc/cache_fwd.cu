@@ -3,27 +3,32 @@
 //
 // The mathematics.  With codes k, v and scales ks, vs of key j's block, in base 2:
 //   x_j = scale log2(e) ks_j (q . k_j),   O = sum_j 2^x_j vs_j v_j / sum_j 2^x_j.
-// The value scale is folded into the exponent: y_j = x_j + log2 vs_j, and with a
-// reference r carried along the keys (the running maximum of the online softmax,
-// less 8, moved when a y exceeds it by more than 15)
-//   acc = sum_j p_j v_j,  p_j = 2^(y_j - r),   l = sum_j p_j 2^(b - log2 vs_j)
-// where b is the log2 vs of the first block: O = 2^b acc / l and
-// LSE = ln2 (r - b + log2 l).  So blocks of different scales need no rescale of
-// acc, and the weights p_j can be held in fp16: they lie at or below 2^15, the
+// The value scale is folded into the exponent: y_j = x_j + log2 vs_j - b, b the log2 vs
+// of the first block, and with a reference r carried along the keys (the running
+// maximum of the online softmax, less 8, moved when a y exceeds it by more than 15)
+//   acc = sum_j p_j v_j,  p_j = 2^(y_j - r),   l = sum_j p_j 2^(b - log2 vs_j):
+// O = 2^b acc / l and LSE = ln2 (r + log2 l).  So blocks of different scales need no
+// rescale of acc, and the weights p_j can be held in fp16: they lie at or below 2^15, the
 // largest at or above 2^8, so weights down to 2^-22 of it keep 11 bits and what is
 // flushed lies below 2^-33 of it.  (Where |y| >= 2^22 r is the maximum itself, as 8
-// is then too near its rounding.)  Codes are exact in fp16, q is (each
-// row is multiplied by the power of two that brings its largest element to
-// [2^14, 2^15)), sums and statistics are fp32.
+// is then too near its rounding.)
+// As a scale takes its part of that range, only blocks whose log2 vs lies within 10 of
+// b share sums.  At another one the warp puts its sums aside, joins them with what is
+// there by their log-sum-exp, and starts again from that block's scale.  Values whose
+// scale lies more than 2^60 below count as zeros (and need no new start: a block of
+// zeros has the scale 2^-100).
+// Codes are exact in fp16; q is down to 2^-29 of its row's largest element (each row is
+// multiplied by the power of two that brings that to [2^14, 2^15)), sums and statistics
+// are fp32.
 //
 // The bound is memory: every code is read once.  At the measured copy
 // bandwidth an SM gets about 24 codes a clock, and a 16-key tile of keys and
 // values (4 KB at d = 128) costs 174 clocks, of which the arithmetic below takes
 // about half of the issue slots.  Measured: 4 sequences of 32768 tokens, 32 heads,
-// d = 128 (1.07 GB) 169 us, 94 % of the measured copy bandwidth; 32 sequences of 512
-// to 8192 tokens, 32 query and 8 key heads (186 MB) 40 us, 68 %: the start of a share
+// d = 128 (1.07 GB) 164 us, 97 % of the measured copy bandwidth; 32 sequences of 512
+// to 8192 tokens, 32 query and 8 key heads (186 MB) 41 us, 67 %: the start of a share
 // (offsets, block table, first codes, one after the other) takes 3 us, its end and
-// the merge 3 us; one sequence of 1000 tokens 8 us.  Three CTAs per SM and three ring
+// the merge 3 us; one sequence of 1000 tokens 8.5 us.  Three CTAs per SM and three ring
 // slots a warp: with four CTAs the registers spilled (221 us for the first case), with
 // two the loads in flight fell short (211 us).  With 1 to 16 rows per key/value head the
 // tensor work is far too small for a 128-row tcgen05 tile and its trip through
@@ -59,6 +64,8 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kOff = 8.f;    // the reference lies this far below the running maximum
 constexpr float kRoom = 15.f;  // and moves when a y exceeds it by more
 constexpr float kFar = 4194304.f;
+constexpr float kWindow = 10.f;    // log2 vs - b of the blocks that share sums
+constexpr float kNothing = -60.f;  // values below it count as zeros
 constexpr int kWarps = 4;
 
 template <int D, int NT_>
@@ -179,6 +186,7 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
   const uint32_t bar0 = sbase + C::OFF_BAR + 8u * (uint32_t)(warp * C::ST);
   volatile uint32_t* abort_flag =
       reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + kWarps * C::ST * 8);
+  const uint32_t red_bar = sbase + C::OFF_BAR + kWarps * C::ST * 8 + 8;  // `red` has been read
   const WaitCtx wctx{abort_flag, p.c.err};
   const uint32_t ring = sbase + (uint32_t)(warp * C::ST * C::STAGE);
 
@@ -191,7 +199,10 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
   }
   if (lane == 0) {
     for (int i = 0; i < C::ST; ++i) mbar_init(bar0 + 8u * i, 1);
-    if (warp == 0) *abort_flag = 0u;
+    if (warp == 0) {
+      mbar_init(red_bar, kWarps);
+      *abort_flag = 0u;
+    }
     fence_mbar_init();
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
@@ -311,10 +322,10 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
   int fi = 0;                     // next tile to load
   uint32_t issued = 0, done = 0;  // live tiles loaded and consumed
   const uint32_t scl0 = sbase + C::OFF_SCL + (uint32_t)(warp * C::ST) * 16u;
-  auto issue = [&](int f) {       // keep the ring full while consuming tile f
+  auto issue = [&](int f, bool more) {  // keep the ring full while consuming tile f
     while (fi < F && issued - done < (uint32_t)C::ST) {
       if ((fi >> 5) > set) {
-        if (set > (f >> 5)) break;  // at most one set ahead
+        if (!more || set > (f >> 5)) break;  // at most one set ahead
         next_set();
       }
       const unsigned bit = 1u << (fi & 31);
@@ -322,9 +333,12 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
         if (lane == (fi & 31)) {
           const uint32_t slot = issued % C::ST;
           const uint32_t bar = bar0 + 8u * slot, dst = ring + slot * C::STAGE;
-          st_shared_v4(scl0 + slot * 16u, __float_as_uint(info.ks[0]), __float_as_uint(info.ks[1]),
-                       __float_as_uint(info.vs[0]), __float_as_uint(info.vs[1]));
           const bool l0 = info.slice[0] >= 0, l1 = C::PARTS == 2 && info.slice[1] >= 0;
+          uint32_t v0 = __float_as_uint(info.vs[0]), v1 = __float_as_uint(info.vs[1]);
+          if (!l1) v1 = v0;  // a part without keys takes the other one's value scale
+          if (!l0) v0 = v1;
+          st_shared_v4(scl0 + slot * 16u, __float_as_uint(info.ks[0]), __float_as_uint(info.ks[1]),
+                       v0, v1);
           mbar_arrive_expect_tx(bar, (uint32_t)(l0 + l1) * 2u * C::PART);
           if (l0) {
             tma_load_3d(dst, &tm_k, bar, 0, info.row, info.slice[0]);
@@ -349,8 +363,10 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
   float ref[NT][2], lsum[NT][2], qinv[NT][2];  // columns (query rows) 2t, 2t + 1 (+ 8 nt)
   int lim[NT][2];                // keys visible to those rows
   int lim_lo = 0, lim_hi = 0;    // least and most over the unit's rows
-  float lvb = 0.f;
+  float lvb = 0.f;               // b
   bool first_live = true;
+  bool parked = false;           // sums of another b are in shared memory
+  uint32_t ended = 0;            // units
 
   // Lane layout of the operands.  d = 128: rows of 128 bytes, 16-byte pieces
   // swizzled by row & 7; matrix row i stands for key (i & 1) * 4 + i / 2 (so the
@@ -361,16 +377,80 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
   const int krow = D == 128 ? ((g & 1) << 2 | g >> 1) : g;
   const int vcol = D == 128 ? ((g & 1) << 2 | g >> 1) * 16 : g * 8;  // first column
 
-  for (int f = 0; f < F; ++f) {
-    if (f > 0 && (f & 31) == 0) {
-      if (set < (f >> 5)) next_set();
-      now0 = live0, now1 = live1;
+  // Sums that are put aside (rare): a normalised O in the warp's part of `red`, each lane its
+  // own elements, and a log2-sum-exp in `stat`.  Joined with the running sums, row by row:
+  // O = keep O_aside + add acc, and the result's log2-sum-exp.
+  float* aside = red + warp * R * D + lane;
+  auto join = [&](float (&keep)[NT][2], float (&add)[NT][2], float (&lse)[NT][2]) {
+    const float up = ex2(lvb);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float l = lsum[nt][i];
+#pragma unroll
+        for (int w = 4; w < 32; w <<= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
+        const float a = parked ? stat[warp * R + nt * 8 + 2 * t + i] : -INFINITY;
+        const float c = l == 0.f ? -INFINITY : ref[nt][i] + lg2(l);
+        const float m = fmaxf(a, c), mm = m == -INFINITY ? 0.f : m;
+        const float wa = ex2(a - mm), wc = ex2(c - mm), z = wa + wc;
+        keep[nt][i] = z == 0.f ? 0.f : wa / z;
+        add[nt][i] = z == 0.f || l == 0.f ? 0.f : wc / z / l * up;
+        lse[nt][i] = z == 0.f ? -INFINITY : mm + lg2(z);
+      }
+    __syncwarp();
+  };
+  auto park = [&]() {
+    if (ended > 0)  // the other warps have read the last unit's results
+      mbar_wait(red_bar, (ended - 1) & 1u, wctx, ERR_SITE_CACHE_FWD + 15);
+    float keep[NT][2], add[NT][2], lse[NT][2];
+    join(keep, add, lse);
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float* at = aside + ((mt * NT + nt) * 4 + i) * 32;
+          *at = (parked ? *at : 0.f) * keep[nt][i & 1] + acc[mt][nt][i] * add[nt][i & 1];
+          acc[mt][nt][i] = 0.f;
+        }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (g == 0) stat[warp * R + nt * 8 + 2 * t + i] = lse[nt][i];
+        lsum[nt][i] = 0.f;
+        ref[nt][i] = -INFINITY;
+      }
+    __syncwarp();
+    parked = true;
+  };
+
+  // The 16 rows of values at `at` count as zeros, but for NaN (rare; each lane its own pieces)
+  auto void_values = [&](uint32_t at) {
+    for (uint32_t x = lane * 16; x < (uint32_t)C::PART; x += 512) {
+      uint4 v = ld_shared_v4(at + x);
+      uint32_t* w = &v.x;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] ^= clear_codes(w[i], nan_codes<E5M2>(w[i]));
+      st_shared_v4(at + x, v.x, v.y, v.z, v.w);
     }
-    const int h = cur.h, rb = cur.rb, ch = cur.ch;
+    fence_proxy_async_smem();  // before the slot is loaded again
+    __syncwarp();
+  };
+
+  int f = 0;             // the tile (of all warps) that comes next
+  bool resumed = false;  // in the middle of a unit
+  bool calm = false;     // its scale is settled:
+  float calm_lv = 0.f;   // log2 vs - b
+  int only = 0;          // 1, 2: only the first, the second part of it
+  while (f < F) {
+    const int h = cur.h, rb = cur.rb;
     const int rows = min(R, cur.seq.n * G - rb * R);
-    const bool begins = f == 0 || ch == 0;  // a unit (or piece) begins
+    const int last = f + min(cur.nch - cur.ch, F - f) - 1;  // of this unit in the share
     uint4 qraw[NT][D / 32];  // bf16: 16 of d = 128's first half, 16 of its second (d = 64: 16)
-    if (begins) {
+    if (!resumed) {  // a unit (or piece) begins
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const int r = nt * 8 + g;
@@ -385,9 +465,7 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
             qraw[nt][j] = *reinterpret_cast<const uint4*>(q + (j >> 1) * 64 + t * 16 + (j & 1) * 8);
         }
       }
-    }
-    if (ok) issue(f);  // while q is on its way
-    if (begins) {
+      if (f == 0) issue(0, false);  // while q is on its way
       const int seen0 = p.causal ? cur.seq.len - cur.seq.n + 1 : cur.seq.len;  // token 0's keys
       auto limit_of = [&](int r) {
         return p.causal ? seen0 + p.by_G.div(rb * R + r) : seen0;
@@ -435,211 +513,280 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
           for (int i = 0; i < 4; ++i) acc[mt][nt][i] = 0.f;
       first_live = true;
       lvb = 0.f;
+      parked = false;
     }
 
-    // ---------------------------------------------------------------- one tile
-    const int key0 = ch * C::CHUNK + warp * C::KEYS;
-    const bool on[2] = {(now0 >> (f & 31) & 1u) != 0u, (now1 >> (f & 31) & 1u) != 0u};
-    if ((on[0] || on[1]) && ok) {
-      const uint32_t slot = done % C::ST;
-      ok = __all_sync(0xffffffffu, mbar_wait(bar0 + 8u * slot, (done / C::ST) & 1u, wctx,
-                                             ERR_SITE_CACHE_FWD + 2));
-      if (ok) {
-        const uint4 sc = ld_shared_v4(scl0 + slot * 16u);
-        const float ks[2] = {__uint_as_float(sc.x), __uint_as_float(sc.y)};
-        const float lv[2] = {lg2(__uint_as_float(sc.z)), lg2(__uint_as_float(sc.w))};
-        if (first_live) lvb = on[0] ? lv[0] : lv[1];
-        first_live = false;
-        const uint32_t ka = ring + slot * C::STAGE, va = ka + C::TILE;
-        const bool masked = key0 + C::KEYS > lim_lo;  // some row does not see all of it
-        // S^T, 16 keys at a time; y = x + log2 vs, masked keys before the maximum
-        float s[C::PARTS][NT][4];
-#pragma unroll
-        for (int pt = 0; pt < C::PARTS; ++pt) {
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[pt][nt][i] = on[pt] ? 0.f : -INFINITY;
-          if (!on[pt]) continue;
-#pragma unroll
-          for (int half = 0; half < D / 64; ++half) {
-            uint32_t a[2][4];  // keys krow and krow + 8: 16 bytes
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int row = krow + 8 * i;
-              const int piece = half * 4 + t;
-              const uint32_t at = ka + pt * C::PART;
-              const uint32_t addr = D == 128 ? at + row * 128 + ((piece ^ (row & 7)) << 4)
-                                             : at + row * 64 + ((piece ^ ((row >> 1) & 3)) << 4);
-              const uint4 x = ld_shared_v4(addr);
-              a[i][0] = x.x, a[i][1] = x.y, a[i][2] = x.z, a[i][3] = x.w;
+    // ---------------------------------------------------------------- its tiles
+    bool event = false;  // a block whose scale is too far from b
+    while (true) {
+      const int key0 = cur.ch * C::CHUNK + warp * C::KEYS;
+      bool on[2] = {(now0 >> (f & 31) & 1u) != 0u, (now1 >> (f & 31) & 1u) != 0u};
+      if ((on[0] || on[1]) && ok) {
+        const uint32_t slot = done % C::ST;
+        ok = __all_sync(0xffffffffu, mbar_wait(bar0 + 8u * slot, (done / C::ST) & 1u, wctx,
+                                               ERR_SITE_CACHE_FWD + 2));
+        if (ok) {
+          const uint4 sc = ld_shared_v4(scl0 + slot * 16u);
+          const float ks[2] = {__uint_as_float(sc.x), __uint_as_float(sc.y)};
+          float lv[2] = {lg2(__uint_as_float(sc.z)), lg2(__uint_as_float(sc.w))};
+          if (first_live) lvb = lv[0];
+          first_live = false;
+          lv[0] -= lvb, lv[1] -= lvb;
+          const float far = C::PARTS == 2 ? fmaxf(fabsf(lv[0]), fabsf(lv[1])) : fabsf(lv[0]);
+          if (__builtin_expect(far > kWindow || (C::PARTS == 2 && only != 0), 0)) {
+            if (!calm) {  // rare, warp-uniform
+              event = true;
+              break;
             }
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              uint32_t a0, a1, a2, a3;
-              codes4_to_f16<E5M2>(a[0][w], a0, a2);
-              codes4_to_f16<E5M2>(a[1][w], a1, a3);
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-                mma_f16(s[pt][nt], a0, a1, a2, a3, qf[nt][half * 4 + w][0],
-                        qf[nt][half * 4 + w][1]);
-            }
+            if (only == 1) on[1] = false;
+            if (only == 2) on[0] = false;
+            lv[0] = lv[1] = calm_lv;
           }
-          const int k0 = key0 + pt * 16 + krow, k1 = k0 + 8;
+          const uint32_t ka = ring + slot * C::STAGE, va = ka + C::TILE;
+          const bool masked = key0 + C::KEYS > lim_lo;  // some row does not see all of it
+          // S^T, 16 keys at a time; y = x + log2 vs - b, masked keys before the maximum
+          float s[C::PARTS][NT][4];
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+          for (int pt = 0; pt < C::PARTS; ++pt) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              s[pt][nt][i] = fmaf(s[pt][nt][i], ks[pt] * qinv[nt][i & 1], lv[pt]);
-          if (masked) {
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) s[pt][nt][i] = on[pt] ? 0.f : -INFINITY;
+            if (!on[pt]) continue;
+#pragma unroll
+            for (int half = 0; half < D / 64; ++half) {
+              uint32_t a[2][4];  // keys krow and krow + 8: 16 bytes
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const int row = krow + 8 * i;
+                const int piece = half * 4 + t;
+                const uint32_t at = ka + pt * C::PART;
+                const uint32_t addr = D == 128 ? at + row * 128 + ((piece ^ (row & 7)) << 4)
+                                               : at + row * 64 + ((piece ^ ((row >> 1) & 3)) << 4);
+                const uint4 x = ld_shared_v4(addr);
+                a[i][0] = x.x, a[i][1] = x.y, a[i][2] = x.z, a[i][3] = x.w;
+              }
+#pragma unroll
+              for (int w = 0; w < 4; ++w) {
+                uint32_t a0, a1, a2, a3;
+                codes4_to_f16<E5M2>(a[0][w], a0, a2);
+                codes4_to_f16<E5M2>(a[1][w], a1, a3);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                  mma_f16(s[pt][nt], a0, a1, a2, a3, qf[nt][half * 4 + w][0],
+                          qf[nt][half * 4 + w][1]);
+              }
+            }
+            const int k0 = key0 + pt * 16 + krow, k1 = k0 + 8;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                if ((i < 2 ? k0 : k1) >= lim[nt][i & 1]) s[pt][nt][i] = -INFINITY;
+                s[pt][nt][i] = fmaf(s[pt][nt][i], ks[pt] * qinv[nt][i & 1], lv[pt]);
+            if (masked) {
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  if ((i < 2 ? k0 : k1) >= lim[nt][i & 1]) s[pt][nt][i] = -INFINITY;
+            }
           }
+          float top[NT][2];  // this lane's largest y
+          bool move = false;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              top[nt][i] = fmaxf(s[0][nt][i], s[0][nt][i + 2]);
+              if (C::PARTS == 2)
+                top[nt][i] = fmaxf(top[nt][i], fmaxf(s[C::PARTS - 1][nt][i],
+                                                     s[C::PARTS - 1][nt][i + 2]));
+              move |= top[nt][i] - ref[nt][i] > kRoom;  // (-inf) - (-inf) moves nothing
+            }
+          if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              float alpha[2];
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                float m = top[nt][i];
+#pragma unroll
+                for (int w = 4; w < 32; w <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
+                const float r = fabsf(m) < kFar ? m - kOff : m;
+                const float to = fmaxf(r, ref[nt][i]);
+                alpha[i] = to == -INFINITY ? 1.f : ex2(ref[nt][i] - to);
+                ref[nt][i] = to;
+                lsum[nt][i] *= alpha[i];
+              }
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[mt][nt][i] *= alpha[i & 1];
+            }
+          }
+          const int odd = D == 64 ? (t & 1) : 0;
+#pragma unroll
+          for (int pt = 0; pt < C::PARTS; ++pt) {
+            if (!on[pt]) continue;
+            const float w = ex2(-lv[pt]);
+            uint32_t pf[NT][2];  // B operand of O^T
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              float pr[4];
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const float r = ref[nt][i] == -INFINITY ? 0.f : ref[nt][i];
+                pr[i] = ex2(s[pt][nt][i] - r);
+                pr[i + 2] = ex2(s[pt][nt][i + 2] - r);
+                lsum[nt][i] = fmaf(pr[i] + pr[i + 2], w, lsum[nt][i]);
+              }
+              pf[nt][0] = movmatrix(pack_f16x2(pr[0], pr[1]));
+              pf[nt][1] = movmatrix(pack_f16x2(pr[2], pr[3]));
+            }
+            // value rows of this lane: keys of matrix rows 2t, 2t + 1, 2t + 8, 2t + 9
+            const int first = key0 + pt * 16;
+            auto value_row = [&](int i) {
+              return D == 128 ? t + 4 * i : 2 * t + ((i & 1) ^ odd) + 8 * (i >> 1);
+            };
+            auto load_values = [&](uint32_t (&v)[4][VW]) {
+              const uint32_t at = va + pt * C::PART;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int row = value_row(i);
+                if constexpr (D == 128) {
+                  const uint4 x = ld_shared_v4(at + row * 128 + (((vcol >> 4) ^ (row & 7)) << 4));
+                  v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
+                } else {
+                  const uint2 x = ld_shared_v2(at + row * 64 +
+                                               (((vcol >> 4) ^ ((row >> 1) & 3)) << 4) + (vcol & 15));
+                  v[i][0] = x.x, v[i][1] = x.y;
+                }
+              }
+              if (masked) {  // stale rows, whatever they hold
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  if (first + value_row(i) >= lim_hi) {
+#pragma unroll
+                    for (int j = 0; j < VW; ++j) v[i][j] = 0u;
+                  }
+              }
+            };
+            uint32_t v[4][VW];
+            load_values(v);
+            // keys that some rows see and others do not: a NaN there must reach the former
+            // only, and a weight of zero does not keep it out of the product
+            bool poison = false;
+            if (masked && lim_lo < min(first + 16, lim_hi)) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < VW; ++j) {
+                  const uint32_t m = nan_codes<E5M2>(v[i][j]);
+                  poison |= m != 0u;
+                  v[i][j] = clear_codes(v[i][j], m);
+                }
+              poison = __any_sync(0xffffffffu, poison);
+            }
+            // O^T: bytes 2 mt, 2 mt + 1 of the lane's columns are rows g, g + 8 of tile mt
+            const uint32_t sel_lo = odd ? 0x1504u : 0x5140u, sel_hi = odd ? 0x3726u : 0x7362u;
+#pragma unroll
+            for (int j = 0; j < VW; ++j) {
+#pragma unroll
+              for (int m = 0; m < 2; ++m) {
+                uint32_t a0, a1, a2, a3;
+                codes4_to_f16<E5M2>(__byte_perm(v[0][j], v[1][j], m ? sel_hi : sel_lo), a0, a1);
+                codes4_to_f16<E5M2>(__byte_perm(v[2][j], v[3][j], m ? sel_hi : sel_lo), a2, a3);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                  mma_f16(acc[2 * j + m][nt], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+              }
+            }
+            if (poison) {  // rare: NaN for the rows that see it
+              load_values(v);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < VW; ++j) v[i][j] = nan_codes<E5M2>(v[i][j]);
+#pragma unroll
+              for (int j = 0; j < 4 * VW; ++j) {
+                uint32_t bad = 0u;  // the part's keys whose value in this column is NaN
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  if (v[i][j >> 2] >> (8 * (j & 3)) & 0x80u) bad |= 1u << value_row(i);
+                bad |= __shfl_xor_sync(0xffffffffu, bad, 1);
+                bad |= __shfl_xor_sync(0xffffffffu, bad, 2);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                  for (int i = 0; i < 2; ++i)
+                    if (bad & ((1u << max(0, min(16, lim[nt][i] - first))) - 1u))
+                      acc[j >> 1][nt][(j & 1) * 2 + i] = __uint_as_float(0x7fffffffu);
+              }
+            }
+          }
+          calm = false;
+          if (C::PARTS == 2 && only == 1) {
+            only = 2;
+            continue;
+          }
+          only = 0;
+          __syncwarp();  // the slot may be loaded again
+          ++done;
         }
-        float top[NT][2];  // this lane's largest y
-        bool move = false;
+      }
+      const bool ends = f == last;
+      if (++f < F) {
+        if ((f & 31) == 0) {
+          if (set < (f >> 5)) next_set();
+          now0 = live0, now1 = live1;
+        }
+        if (ok) issue(f, true);
+      }
+      if (ends) break;
+      ++cur.ch;
+    }
+    resumed = event;
+    if (__builtin_expect(event, 0)) {
+      const uint32_t slot = done % C::ST;
+      const uint4 sc = ld_shared_v4(scl0 + slot * 16u);
+      const bool on0 = (now0 >> (f & 31) & 1u) != 0u, on1 = (now1 >> (f & 31) & 1u) != 0u;
+      if (C::PARTS == 2 && only == 0 && on0 && on1) only = 1;
+      const bool second = C::PARTS == 2 && (only == 2 || !on0);
+      const float lvs = lg2(__uint_as_float(second ? sc.w : sc.z));
+      calm = true;
+      calm_lv = lvs - lvb;
+      if (calm_lv < kNothing) {
+        calm_lv = kNothing;
+        void_values(ring + slot * C::STAGE + C::TILE + (second ? C::PART : 0));
+      } else if (fabsf(calm_lv) > kWindow) {
+        park();
+        lvb = lvs;
+        calm_lv = 0.f;
+      }
+      continue;
+    }
+
+    // ---------------------------------------------------------------- the unit (or piece) ends
+    const int ch = cur.ch;
+    const bool unit_ends = ch == cur.nch - 1;
+    {
+      if (__builtin_expect(parked, 0)) {  // rare: all of it as if it were one key's
+        float keep[NT][2], add[NT][2];
+        join(keep, add, ref);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              acc[mt][nt][i] = aside[((mt * NT + nt) * 4 + i) * 32] * keep[nt][i & 1] +
+                               acc[mt][nt][i] * add[nt][i & 1];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            top[nt][i] = fmaxf(s[0][nt][i], s[0][nt][i + 2]);
-            if (C::PARTS == 2)
-              top[nt][i] = fmaxf(top[nt][i], fmaxf(s[C::PARTS - 1][nt][i],
-                                                   s[C::PARTS - 1][nt][i + 2]));
-            move |= top[nt][i] - ref[nt][i] > kRoom;  // (-inf) - (-inf) moves nothing
-          }
-        if (__any_sync(0xffffffffu, move)) {
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float alpha[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              float m = top[nt][i];
-#pragma unroll
-              for (int w = 4; w < 32; w <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
-              const float r = fabsf(m) < kFar ? m - kOff : m;
-              const float to = fmaxf(r, ref[nt][i]);
-              alpha[i] = to == -INFINITY ? 1.f : ex2(ref[nt][i] - to);
-              ref[nt][i] = to;
-              lsum[nt][i] *= alpha[i];
-            }
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) acc[mt][nt][i] *= alpha[i & 1];
-          }
-        }
-        const int odd = D == 64 ? (t & 1) : 0;
-#pragma unroll
-        for (int pt = 0; pt < C::PARTS; ++pt) {
-          if (!on[pt]) continue;
-          const float w = ex2(lvb - lv[pt]);
-          uint32_t pf[NT][2];  // B operand of O^T
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float pr[4];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const float r = ref[nt][i] == -INFINITY ? 0.f : ref[nt][i];
-              pr[i] = ex2(s[pt][nt][i] - r);
-              pr[i + 2] = ex2(s[pt][nt][i + 2] - r);
-              lsum[nt][i] = fmaf(pr[i] + pr[i + 2], w, lsum[nt][i]);
-            }
-            pf[nt][0] = movmatrix(pack_f16x2(pr[0], pr[1]));
-            pf[nt][1] = movmatrix(pack_f16x2(pr[2], pr[3]));
-          }
-          // value rows of this lane: keys of matrix rows 2t, 2t + 1, 2t + 8, 2t + 9
-          const int first = key0 + pt * 16;
-          auto value_row = [&](int i) {
-            return D == 128 ? t + 4 * i : 2 * t + ((i & 1) ^ odd) + 8 * (i >> 1);
-          };
-          auto load_values = [&](uint32_t (&v)[4][VW]) {
-            const uint32_t at = va + pt * C::PART;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int row = value_row(i);
-              if constexpr (D == 128) {
-                const uint4 x = ld_shared_v4(at + row * 128 + (((vcol >> 4) ^ (row & 7)) << 4));
-                v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
-              } else {
-                const uint2 x = ld_shared_v2(at + row * 64 +
-                                             (((vcol >> 4) ^ ((row >> 1) & 3)) << 4) + (vcol & 15));
-                v[i][0] = x.x, v[i][1] = x.y;
-              }
-            }
-            if (masked) {  // stale rows, whatever they hold
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (first + value_row(i) >= lim_hi) {
-#pragma unroll
-                  for (int j = 0; j < VW; ++j) v[i][j] = 0u;
-                }
-            }
-          };
-          uint32_t v[4][VW];
-          load_values(v);
-          // keys that some rows see and others do not: a NaN there must reach the former
-          // only, and a weight of zero does not keep it out of the product
-          bool poison = false;
-          if (masked && lim_lo < min(first + 16, lim_hi)) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-              for (int j = 0; j < VW; ++j) {
-                const uint32_t m = nan_codes<E5M2>(v[i][j]);
-                poison |= m != 0u;
-                v[i][j] = clear_codes(v[i][j], m);
-              }
-            poison = __any_sync(0xffffffffu, poison);
-          }
-          // O^T: bytes 2 mt, 2 mt + 1 of the lane's columns are rows g, g + 8 of tile mt
-          const uint32_t sel_lo = odd ? 0x1504u : 0x5140u, sel_hi = odd ? 0x3726u : 0x7362u;
-#pragma unroll
-          for (int j = 0; j < VW; ++j) {
-#pragma unroll
-            for (int m = 0; m < 2; ++m) {
-              uint32_t a0, a1, a2, a3;
-              codes4_to_f16<E5M2>(__byte_perm(v[0][j], v[1][j], m ? sel_hi : sel_lo), a0, a1);
-              codes4_to_f16<E5M2>(__byte_perm(v[2][j], v[3][j], m ? sel_hi : sel_lo), a2, a3);
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-                mma_f16(acc[2 * j + m][nt], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
-            }
-          }
-          if (poison) {  // rare: NaN for the rows that see it
-            load_values(v);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-              for (int j = 0; j < VW; ++j) v[i][j] = nan_codes<E5M2>(v[i][j]);
-#pragma unroll
-            for (int j = 0; j < 4 * VW; ++j) {
-              uint32_t bad = 0u;  // the part's keys whose value in this column is NaN
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (v[i][j >> 2] >> (8 * (j & 3)) & 0x80u) bad |= 1u << value_row(i);
-              bad |= __shfl_xor_sync(0xffffffffu, bad, 1);
-              bad |= __shfl_xor_sync(0xffffffffu, bad, 2);
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                  if (bad & ((1u << max(0, min(16, lim[nt][i] - first))) - 1u))
-                    acc[j >> 1][nt][(j & 1) * 2 + i] = __uint_as_float(0x7fffffffu);
-            }
-          }
-        }
-        __syncwarp();  // the slot may be loaded again
-        ++done;
+          for (int i = 0; i < 2; ++i) lsum[nt][i] = g == 0 && ref[nt][i] != -INFINITY ? 1.f : 0.f;
+        lvb = 0.f;
       }
-    }
-
-    // ---------------------------------------------------------------- a unit (or piece) ends
-    const bool unit_ends = ch == cur.nch - 1;
-    if (unit_ends || f == F - 1) {
       // this warp's rows: normalised result and log2-sum-exp
       float mine[NT][2], fac[NT][2];
 #pragma unroll
@@ -650,7 +797,7 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
 #pragma unroll
           for (int w = 4; w < 32; w <<= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
           lsum[nt][i] = l;
-          mine[nt][i] = l == 0.f ? -INFINITY : ref[nt][i] - lvb + lg2(l);
+          mine[nt][i] = l == 0.f ? -INFINITY : ref[nt][i] + lg2(l);
           if (g == 0) stat[warp * R + nt * 8 + 2 * t + i] = mine[nt][i];
         }
       __syncthreads();
@@ -692,7 +839,7 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
                 acc[2 * j + 1][nt][i + 2] * fac[nt][i] * up);
         }
       __syncthreads();
-      const bool starts_here = f >= ch;  // the unit's chunk 0 is in this share
+      const bool starts_here = f > ch;  // the unit's chunk 0 is in this share
       const bool whole = starts_here && unit_ends;
       const int slot = starts_here ? 1 : 0;
       if (warp == 0 && g == 0) {
@@ -739,6 +886,9 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
         rec.row0 = cur.seq.row0;
         rec.first_row = rb * R;
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(red_bar);
+      ++ended;
     }
     advance<C>(p, &cur, 1);
   }
