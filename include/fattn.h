@@ -276,8 +276,9 @@ int fattn_fwd_bwd_host(const void* q, const void* k, const void* v, const void* 
  * array will do).  block_size is 16, 32, 64 or 128, d 64 or 128, num_blocks x H
  * below 2^31.
  * fattn_cache_append writes powers of two as scales; the reader and the
- * attention take any positive normal fp32 (scales of one sequence and head
- * that lie within 2^100 of each other). */
+ * attention take any positive normal fp32.  Where value scales of one sequence
+ * and head differ by more than 2^60 (a block of zeros has the smallest one,
+ * 2^-100), the attention takes the smaller as 2^-60 of the larger. */
 typedef enum {
   FATTN_CACHE_E4M3 = 0, /* 4 exponent, 3 mantissa bits, largest value 448, no infinities */
   FATTN_CACHE_E5M2 = 1  /* 5 exponent, 2 mantissa bits, largest value 57344 */
@@ -362,7 +363,10 @@ int fattn_cache_read(const fattn_cache* cache, const fattn_cache_batch* batch, v
  * exceed lens[b].  Values of keys that a query does not see never reach its
  * row, whatever they are (NaN included); an e5m2 infinity, which append never
  * writes, gives the rows that see it an infinity or NaN.
- * Scores, statistics and sums are fp32.
+ * Scores, statistics and sums are fp32.  A weight, times its value scale, is
+ * rounded to fp16 relative to the largest of its row among blocks whose scales
+ * lie within 2^20 of each other or below: 11 bits down to 2^-22 of that, an
+ * error of 2^-33 of it below.
  * workspace: DEVICE memory of fattn_cache_fwd_workspace_bytes(...) bytes,
  * 256-byte aligned, owned by the caller, its contents on entry do not matter;
  * calls that overlap on the GPU need one each.  Returns FATTN_OK,

@@ -14,9 +14,10 @@
 // is then too near its rounding.)
 // As a scale takes its part of that range, only blocks whose log2 vs lies within 10 of
 // b share sums.  At another one the warp puts its sums aside, joins them with what is
-// there by their log-sum-exp, and starts again from that block's scale.  Values whose
-// scale lies more than 2^60 below count as zeros (and need no new start: a block of
-// zeros has the scale 2^-100).
+// there by their log-sum-exp, and starts again from that block's scale.  A scale more
+// than 2^60 below 2^b is taken as 2^(b - 60), which needs no new start: a block of zeros
+// has the scale 2^-100.  With one block in eight 2^30 smaller the first case below takes
+// 14 % longer, with one in eight of zeros 3 %.
 // Codes are exact in fp16; q is down to 2^-29 of its row's largest element (each row is
 // multiplied by the power of two that brings that to [2^14, 2^15)), sums and statistics
 // are fp32.
@@ -65,7 +66,7 @@ constexpr float kOff = 8.f;    // the reference lies this far below the running 
 constexpr float kRoom = 15.f;  // and moves when a y exceeds it by more
 constexpr float kFar = 4194304.f;
 constexpr float kWindow = 10.f;    // log2 vs - b of the blocks that share sums
-constexpr float kNothing = -60.f;  // values below it count as zeros
+constexpr float kNothing = -60.f;  // what lies below it is taken as it
 constexpr int kWarps = 4;
 
 template <int D, int NT_>
@@ -427,19 +428,6 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
     parked = true;
   };
 
-  // The 16 rows of values at `at` count as zeros, but for NaN (rare; each lane its own pieces)
-  auto void_values = [&](uint32_t at) {
-    for (uint32_t x = lane * 16; x < (uint32_t)C::PART; x += 512) {
-      uint4 v = ld_shared_v4(at + x);
-      uint32_t* w = &v.x;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] ^= clear_codes(w[i], nan_codes<E5M2>(w[i]));
-      st_shared_v4(at + x, v.x, v.y, v.z, v.w);
-    }
-    fence_proxy_async_smem();  // before the slot is loaded again
-    __syncwarp();
-  };
-
   int f = 0;             // the tile (of all warps) that comes next
   bool resumed = false;  // in the middle of a unit
   bool calm = false;     // its scale is settled:
@@ -757,7 +745,6 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
       calm_lv = lvs - lvb;
       if (calm_lv < kNothing) {
         calm_lv = kNothing;
-        void_values(ring + slot * C::STAGE + C::TILE + (second ? C::PART : 0));
       } else if (fabsf(calm_lv) > kWindow) {
         park();
         lvb = lvs;

@@ -22,16 +22,27 @@
 // tile's codes in flight; block numbers are read 16 to 32 tiles ahead, scales 8 to 24.
 //
 // The scales are applied by the softmax, per piece, as in the kernel for few rows:
-// y = s * ks + log2 vs, p = 2^(y - r) (fp16), l += w p with w = 2^(b - log2 vs),
+// y = s * ks + log2 vs - b, p = 2^(y - r) (fp16), l += w p with w = 2^(b - log2 vs),
 // O = 2^b acc / l.  r is the running maximum of y less 8, moved only when a y
 // exceeds it by more than 15 (p stays below 2^16); where |y| >= 2^22 it is the
 // maximum itself, as 8 is then too near its rounding.
+// b is the smallest exponent of the piece's value scales, which three warps look up
+// while the others start.  fp16 weights hold scales up to 2^20 above it.  Where they
+// differ more, the piece's tiles are gone through two or three times, each time with
+// the keys of 21 exponents, the smallest first: O and r go on, so what is there when
+// larger values come is scaled down in fp32, and each pass's l joins the log-sum-exp.
+// Scales more than 2^60 below the largest (blocks of zeros) are taken as 2^(b - 60).
+// With one block in eight 2^30 smaller the case measured below takes 490 us, with one in
+// eight of zeros no longer than without.  (Relative to the first block's scale alone, as
+// once, a first block of zeros made O zero or NaN.  The look-up costs 1 us a piece: 16
+// sequences of 70 to 128 tokens behind 300 to 7000, 16 heads, 62 us instead of 59 at
+// d = 64, 81 instead of 79 at d = 128.)
 //
 // Warps: 0-3 softmax of subtile 0, 4-7 of subtile 1 (thread t owns row t; they also
-// load Q and write O), 8-11 fill the slots, 12 issues the MMAs, 13-15 idle.  TMEM:
-// S_0, S_1, O_0, O_1 (d = 64: P_0, P_1).
+// load Q and write O), 8-11 fill the slots, 12 issues the MMAs, 13-15 look up the value
+// scales.  TMEM: S_0, S_1, O_0, O_1 (d = 64: P_0, P_1).
 //
-// Measured, 2048 tokens behind 8192 (32 query, 8 key heads, d = 128): 250 us, 1237
+// Measured, 2048 tokens behind 8192 (32 query, 8 key heads, d = 128): 253 us, 1222
 // TFLOP/s, tensor pipe 50 % active.  256 units on 152 SMs are two rounds where 1.7
 // would do (16 %); a tile of 128 keys takes 3100 clocks against the MMAs' 2048, the
 // MMA warp's own issue (1750) and its waits for P (1350) alternating; the start and
@@ -52,6 +63,9 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kOff = 8.f;    // the reference lies this far below the running maximum
 constexpr float kRoom = 15.f;  // and moves when a y exceeds it by more
 constexpr float kFar = 4194304.f;
+constexpr int kWindow = 20;        // exponents of the value scales that share a pass: b ... b + 20
+constexpr float kNothing = -60.f;  // log2 vs - b of blocks far below the others
+constexpr int kMaxPasses = 3;      // 61 exponents, 21 at a time
 
 template <int N>
 __device__ __forceinline__ void regs_inc() {
@@ -82,6 +96,19 @@ __device__ __forceinline__ void add_x2(float a0, float a1, float b0, float b1, f
       "mov.b64 {%0, %1}, s;\n\t}"
       : "=f"(s0), "=f"(s1)
       : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+
+// r + log2 l of a positive l, whose exponent meets r before either is rounded
+__device__ __forceinline__ float add_log2(float r, float l) {
+  const uint32_t u = __float_as_uint(l);
+  if (!(l < INFINITY)) return r + l;  // NaN stays
+  return (r + (float)((int)(u >> 23) - 127)) + lg2(__uint_as_float((u & 0x7fffffu) | 0x3f800000u));
+}
+
+// log2(2^a + 2^b)
+__device__ __forceinline__ float log2_add(float a, float b) {
+  const float m = fmaxf(a, b), mm = m == -INFINITY ? 0.f : m;
+  return m == -INFINITY ? a + b : add_log2(mm, ex2(a - mm) + ex2(b - mm));
 }
 
 // 16 bytes to shared memory, or zeros
@@ -115,7 +142,9 @@ struct Wide {
   static constexpr int OFF_KV = OFF_Q + 2 * TILE;
   static constexpr int OFF_SCALE = OFF_KV + STAGES * TILE;  // [SCALE_TILES][PIECES] float4
   static constexpr int OFF_BAR = OFF_SCALE + SCALE_TILES * PIECES * 16;
-  static constexpr int SMEM = OFF_BAR + 256 + 1024;
+  static constexpr int OFF_SCAN = OFF_BAR + 256;  // Scan
+  static constexpr int OFF_LSE = OFF_SCAN + 32;   // [ROWS], used by units of several passes
+  static constexpr int SMEM = OFF_LSE + ROWS * 4 + 1024;
   static constexpr int THREADS = 512;
   static constexpr int W_FILL = 8, N_FILL = 4, W_MMA = 12;
   static constexpr int REG_LAUNCH = 128, REG_SOFTMAX = 184, REG_FILL = 104, REG_CTRL = 40;
@@ -144,7 +173,8 @@ enum {
   B_MMA_DONE = 9,
   B_SCALE = 10,    // [SCALE_TILES] slot filling -> softmax: the scales of a tile
   B_S_READ = 14,   // [2] softmax -> MMA (d = 64): S_s is in registers
-  B_KV_FULL = 16,  // [STAGES], then kv_empty [STAGES]
+  B_SCAN = 16,     // the scan of the value scales -> all
+  B_KV_FULL = 17,  // [STAGES], then kv_empty [STAGES]
 };
 static_assert(8 * (B_KV_FULL + 2 * Wide<64>::STAGES) + 16 <= 256, "barrier block");
 static_assert(Wide<64>::STAGES <= 7 && Wide<128>::STAGES <= 7, "reuse of the scales' ring");
@@ -160,11 +190,15 @@ struct __align__(16) Segment {
 };
 static_assert(sizeof(Segment) == 48, "three 16-byte loads");
 
-// The value scale of a sequence's first block, the power that its sums are kept
-// relative to (any reference of the scales' size will do)
-__device__ __forceinline__ float unit_scale(const CacheFwdParams& p, int page, int h) {
-  return page >= 0 && page < p.c.num_blocks ? p.c.v_scale[(long long)page * p.c.H + h] : 1.f;
-}
+// What the idle warps find out about the value scales of a piece's blocks: their largest
+// and smallest (biased) exponent, and the passes over its tiles that they ask for.
+struct Scan {
+  int hi, lo;
+  unsigned set[2];  // bit i: there are blocks of exponent hi - i (only where hi - lo is large)
+  int passes;
+  int b[kMaxPasses];
+};
+static_assert(sizeof(Scan) == 32, "room in shared memory");
 
 // Where the rows of pieces go: LSE [places, ROWS], then O [places, ROWS, d], behind the
 // records.
@@ -406,6 +440,7 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + 8 * (B_KV_FULL + 2 * ST));
   volatile uint32_t* abort_flag = tmem_slot + 1;
   volatile uint32_t* poison = tmem_slot + 2;        // a NaN was kept out of some rows' sums
+  volatile Scan* scan = reinterpret_cast<volatile Scan*>(smem + C::OFF_SCAN);
   const WaitCtx wctx{abort_flag, p.c.err};
   float4* scales = reinterpret_cast<float4*>(smem + C::OFF_SCALE);
 
@@ -419,6 +454,9 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
       mbar_init(bar(B_S_READ + s), 128);
     }
     mbar_init(bar(B_MMA_DONE), 1);
+    mbar_init(bar(B_SCAN), 1);
+    scan->hi = 0, scan->lo = 255;
+    scan->set[0] = scan->set[1] = 0u;
     for (int i = 0; i < C::SCALE_TILES; ++i) mbar_init(bar(B_SCALE + i), C::PIECES);
     for (int i = 0; i < ST; ++i) {
       mbar_init(kv_full0 + 8u * i, C::N_FILL);
@@ -444,20 +482,86 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
   auto limit_of = [&](int r) {
     return max(0, min(len, p.causal ? seen0 + p.by_G.div(r) : seen0));
   };
-  const int nt0 = seg.c0, nt1 = seg.c1;
-  const int n_max = max(nt0, nt1);
+  const int n_tiles = max(seg.c0, seg.c1);
   const int lim_lo = limit_of(0), lim_hi = limit_of(n_rows - 1);
-
+  // Several passes run through all of the tiles, one after the other
+  auto scanned = [&]() {
+    return mbar_wait(bar(B_SCAN), 0, wctx, ERR_SITE_CACHE_FWD + 15);
+  };
+  auto tiles_of = [&](int c) {  // of a subtile, over all passes
+    const int passes = scan->passes;
+    return passes == 1 || c == 0 ? c : passes * n_tiles;
+  };
 
   if (warp > C::W_MMA) {
-    regs_dec<C::REG_CTRL>();  // idle
+    regs_dec<C::REG_CTRL>();
+    // ---------------------------------------------------------------- scan of the value scales
+    constexpr int N = 96;
+    const int me = (int)threadIdx.x - (C::W_MMA + 1) * 32;
+    const int end = min(lim_hi, (t0 + n_tiles) * C::BN);
+    const int past = end > 0 ? ((end - 1) >> p.c.block_log2) + 1 : 0;
+    int hi = 0, lo = 255;
+    for (int again = 0;; ++again) {  // the second time (rare) for the set
+      unsigned set0 = 0u, set1 = 0u;
+      int most = 0, least = 255;
+#pragma unroll 1
+      for (int i0 = ((t0 * C::BN) >> p.c.block_log2) + me; i0 < past; i0 += 2 * N) {
+        int page[2];
+        float vs[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          page[k] = i0 + k * N < past
+                        ? p.c.block_table[(long long)b * p.c.table_width + i0 + k * N]
+                        : -1;
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          vs[k] = page[k] >= 0 && page[k] < p.c.num_blocks
+                      ? p.c.v_scale[(long long)page[k] * p.c.H + h]
+                      : -1.f;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          if (!(vs[k] > 0.f)) continue;
+          const int e = (int)(__float_as_uint(vs[k]) >> 23), i = hi - e;
+          most = max(most, e), least = min(least, e);
+          const unsigned bit = 1u << (i & 31);
+          if (i < 32)
+            set0 |= bit;
+          else if (i <= -(int)kNothing)
+            set1 |= bit;
+        }
+      }
+      if (again) {
+        atomicOr(const_cast<unsigned*>(&scan->set[0]), set0);
+        atomicOr(const_cast<unsigned*>(&scan->set[1]), set1);
+      } else {
+        atomicMax(const_cast<int*>(&scan->hi), most);
+        atomicMin(const_cast<int*>(&scan->lo), least);
+      }
+      named_bar_sync(1, N);
+      hi = scan->hi, lo = scan->lo;
+      if (again || hi - lo <= kWindow) break;
+    }
+    if (me == 0) {
+      int passes = 1;
+      scan->b[0] = lo <= hi ? lo : 127;
+      if (hi - lo > kWindow) {  // from the smallest on
+        passes = 0;
+        unsigned long long set = (unsigned long long)scan->set[1] << 32 | scan->set[0];
+        while (set != 0ull && passes < kMaxPasses) {
+          const int i = 63 - __clzll((long long)set);
+          scan->b[passes++] = hi - i;
+          set = i > kWindow ? set & ((1ull << (i - kWindow)) - 1ull) : 0ull;
+        }
+      }
+      scan->passes = passes;
+      mbar_arrive(bar(B_SCAN));
+    }
   } else if (warp >= C::W_FILL && warp < C::W_FILL + C::N_FILL) {
     regs_dec<C::REG_FILL>();
     // ---------------------------------------------------------------- slot filling
     // Warp w fills rows [32 w, 32 w + 32) of every slot: two pieces of 16 tokens.
     const int bs = p.c.block_size;
     const int me = warp - C::W_FILL;
-    float base = 0.f;  // b above
     // lane i of a set of 16 tiles holds the place and scales of this warp's piece i & 1 of
     // tile i / 2.  They are fetched in steps, none of which waits for its own loads (in one
     // step: 16 sequences of 1 to 1000 tokens 82.5 us, against 81.5).
@@ -465,7 +569,11 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
       int piece;        // number of its 16 tokens in the pool (-1: nothing visible there)
       float ks, lv, w;  // as the softmax takes them
     };
-    auto key_of = [&](int j0) { return (t0 + j0 + (lane >> 1)) * C::BN + me * 32 + (lane & 1) * 16; };
+    auto pass_of = [&](int j) { return (j >= n_tiles ? 1 : 0) + (j >= 2 * n_tiles ? 1 : 0); };
+    auto key_of = [&](int j0) {
+      const int j = j0 + (lane >> 1);
+      return (t0 + j - pass_of(j) * n_tiles) * C::BN + me * 32 + (lane & 1) * 16;
+    };
     auto page_of = [&](int j0) {
       const int key = key_of(j0);
       return key < lim_hi ? p.c.block_table[(long long)b * p.c.table_width + (key >> p.c.block_log2)]
@@ -485,10 +593,17 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
       r.lv = p.c.v_scale[slice];
       return r;
     };
-    auto finish = [&](Info r) {
+    auto finish = [&](Info r, int j0) {  // the scales as the softmax takes them
+      const int pass = pass_of(j0 + (lane >> 1));
+      const int e = (int)(__float_as_uint(r.lv) >> 23), base = scan->b[pass];
+      // of this pass; or of none, as the values are next to nothing
+      const bool in = e >= base && e <= base + kWindow;
+      const bool nothing = pass == 0 && e < scan->hi + (int)kNothing;
+      float lv = -INFINITY;
+      if (r.piece >= 0) lv = nothing ? kNothing : in ? lg2(r.lv) - (float)(base - 127) : lv;
       r.ks = r.piece < 0 ? 1.f : r.ks * p.scale_log2;
-      r.lv = r.piece < 0 ? -INFINITY : lg2(r.lv);
-      r.w = r.piece < 0 ? 0.f : ex2(base - r.lv);
+      r.lv = lv;
+      r.w = lv == -INFINITY ? 0.f : ex2(-lv);
       return r;
     };
     constexpr int LD = D / 32;  // 16-byte loads per lane and piece
@@ -519,18 +634,19 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
     };
     Info now{-1, 1.f, -INFINITY, 0.f}, next = now;
     int page = 0;
-    if (n_max > 0) {
-      const int page0 = p.c.block_table[(long long)b * p.c.table_width];  // for base
+    bool ok = true;
+    if (n_tiles > 0) {
       now = scales_of(0, page_of(0));
-      const float scale0 = unit_scale(p, page0, h);
       look_up(0, now);
       load(0);
       load(1);
-      base = lg2(scale0);
-      now = finish(now);
+      ok = __all_sync(0xffffffffu, scanned());
+      now = finish(now, 0);
     }
-    bool ok = true;
+    int first = t0;  // of tile 0, less the tiles of the passes before
+    const int n_max = ok && n_tiles > 0 ? scan->passes * n_tiles : 0;
     for (int j = 0; ok && j < n_max; ++j) {
+      if (first + j == t0 + n_tiles) first -= n_tiles;
       {  // the tile's scales
         // the slot of K_j is free: with it, the scales' (see SCALE_TILES)
         const int i = 2 * j, use = i / ST;
@@ -546,7 +662,7 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
       }
       if ((j & 15) == 0) page = page_of(j + 16);
       if ((j & 15) == 8) next = scales_of(j + 8, page);
-      if ((j & 15) == 15) now = finish(next);  // the loads below are for its first tile
+      if ((j & 15) == 15) now = finish(next, j + 1);  // the loads below are for its first tile
       look_up(j + 1, now);
 #pragma unroll
       for (int value = 0; value < 2; ++value) {
@@ -557,8 +673,8 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
                __all_sync(0xffffffffu, mbar_wait(kv_empty0 + 8u * kv_slot, (use - 1) & 1, wctx,
                                                  ERR_SITE_CACHE_FWD + 4));
           if (!ok) break;
-          const int key0 = (t0 + j) * C::BN + me * 32 + row4;
-          if ((t0 + j) * C::BN + me * 32 + 32 > lim_lo) {  // some row does not see all of it
+          const int key0 = (first + j) * C::BN + me * 32 + row4;
+          if ((first + j) * C::BN + me * 32 + 32 > lim_lo) {  // some row does not see all of it
             bool nan = false;
 #pragma unroll
             for (int pc = 0; pc < 2; ++pc)
@@ -629,7 +745,10 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
       }
       if (half == 1) mma_commit_w(bar(B_PV_DONE + s));
     };
-    bool ok = __all_sync(0xffffffffu, mbar_wait(bar(B_Q), 0, wctx, ERR_SITE_CACHE_FWD + 6));
+    bool ok = __all_sync(0xffffffffu, mbar_wait(bar(B_Q), 0, wctx, ERR_SITE_CACHE_FWD + 6) &&
+                                          scanned());
+    const int nt0 = ok ? tiles_of(seg.c0) : 0, nt1 = ok ? tiles_of(seg.c1) : 0;
+    const int n_max = max(nt0, nt1);
     if (ok && n_max > 0) {
       ok = kv_wait(0);
       if (ok) {
@@ -722,14 +841,12 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
     const int row = s * C::BM + t;  // of the unit
     const bool valid = row < n_rows;
     const int lim = valid ? limit_of(row) : 0;
-    const int my_nt = s ? nt1 : nt0;
+    const int my_c = s ? seg.c1 : seg.c0;
     const int my_lo = limit_of(s * C::BM);  // keys that every row of the subtile sees
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lane_off + C::TM_S + s * 128;
     const uint32_t tO = tmem + lane_off + C::TM_O + s * D;
     const uint32_t tP = tmem + lane_off + C::TM_P + s * C::P_STRIDE;
-    // the first block, for b above, which is needed at the end only
-    const int page0 = my_nt > 0 ? p.c.block_table[(long long)b * p.c.table_width] : -1;
     // A row of q and o is LPR pieces of 16 bytes; a warp moves RPI of its 32 rows at a
     // time, piece by lane (a thread that moved its own row would touch 32 lines with
     // every instruction).
@@ -760,7 +877,6 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
       const long long off = __shfl_sync(0xffffffffu, q_off, i * RPI + sub);
       copy16_async(row_piece(i), p.q.p + (off >= 0 ? off + 8 * piece : 0), off >= 0);
     }
-    float scale0 = unit_scale(p, page0, h);
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncwarp();
     auto own_piece = [&](int k) {
@@ -793,125 +909,144 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
     }
     fence_proxy_async_smem();
     mbar_arrive(bar(B_Q));
-    asm volatile("" : "+f"(scale0));  // loaded by now, not behind the loop
+    const int my_nt = scanned() ? tiles_of(my_c) : 0;
 
     float r_run = -INFINITY, l_run = 0.f;  // the reference r, and l
-    for (int j = 0; j < my_nt; ++j) {
-      mbar_wait(bar(B_S_FULL + s), j & 1, wctx, ERR_SITE_CACHE_FWD + 10);
-      mbar_wait(bar(B_SCALE + j % C::SCALE_TILES), (j / C::SCALE_TILES) & 1, wctx,
-                ERR_SITE_CACHE_FWD + 11);
-      tc_fence_after();
-      uint32_t u[4][32];
+    int first = t0;  // of tile 0, less the tiles of the passes before
+    for (int j = 0;;) {
+      const int stop = my_nt > my_c ? j + n_tiles : my_nt;  // the pass's
+      for (; j < stop; ++j) {
+        mbar_wait(bar(B_S_FULL + s), j & 1, wctx, ERR_SITE_CACHE_FWD + 10);
+        mbar_wait(bar(B_SCALE + j % C::SCALE_TILES), (j / C::SCALE_TILES) & 1, wctx,
+                  ERR_SITE_CACHE_FWD + 11);
+        tc_fence_after();
+        uint32_t u[4][32];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, u[c]);
-      tmem_wait_ld();
+        for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, u[c]);
+        tmem_wait_ld();
 #pragma unroll
-      for (int c = 0; c < 4; ++c) reg_fence32(u[c]);
-      const float4* sc = scales + (j % C::SCALE_TILES) * C::PIECES;
-      float sv[128];
+        for (int c = 0; c < 4; ++c) reg_fence32(u[c]);
+        const float4* sc = scales + (j % C::SCALE_TILES) * C::PIECES;
+        float sv[128];
 #pragma unroll
-      for (int k = 0; k < 128; ++k) sv[k] = __uint_as_float(u[k >> 5][k & 31]);
-      if (C::DEC) {  // its columns may take S_s(j + 1)
-        tc_fence_before();
-        mbar_arrive(bar(B_S_READ + s));
-      }
-      const int c0 = (t0 + j) * C::BN;
-      if (c0 + C::BN > my_lo) {
-        const int n = lim - c0;
+        for (int k = 0; k < 128; ++k) sv[k] = __uint_as_float(u[k >> 5][k & 31]);
+        if (C::DEC) {  // its columns may take S_s(j + 1)
+          tc_fence_before();
+          mbar_arrive(bar(B_S_READ + s));
+        }
+        const int c0 = (first + j) * C::BN;
+        if (c0 + C::BN > my_lo) {
+          const int n = lim - c0;
 #pragma unroll
-        for (int k = 0; k < 128; ++k)
-          if (k >= n) sv[k] = -INFINITY;
-      }
-      // the largest y: of each piece the largest product, then its scale (positive)
-      float ks[C::PIECES], top[C::PIECES];
-#pragma unroll
-      for (int g = 0; g < C::PIECES; ++g) {
-        const float* x = sv + g * 16;
-        float m = fmax3(fmax3(x[0], x[1], x[2]), fmax3(x[3], x[4], x[5]), fmax3(x[6], x[7], x[8]));
-        m = fmax3(m, fmax3(x[9], x[10], x[11]), fmax3(x[12], x[13], x[14]));
-        const float2 kl = *reinterpret_cast<const float2*>(&sc[g]);
-        ks[g] = fmaxf(kl.x * back, 1.17549435e-38f);
-        top[g] = fmaf(fmaxf(m, x[15]), ks[g], kl.y);
-      }
-      const float m_blk = fmax3(fmax3(top[0], top[1], top[2]), fmax3(top[3], top[4], top[5]),
-                                fmaxf(top[6], top[7]));
-      // (-inf) - (-inf) is NaN, which moves nothing
-      const bool rescale = m_blk - r_run > kRoom;
-      const float r_new = rescale ? (fabsf(m_blk) < kFar ? m_blk - kOff : m_blk) : r_run;
-      const float shift = r_new == -INFINITY ? 0.f : -r_new;
-      const float alpha = rescale ? ex2(r_run + shift) : 1.f;
-      // p = 2^(s ks + (log2 vs - r)).  Far from zero, the rounding of y that the check
-      // above saw is itself large: there p is formed from the rounded y
-      const bool far = __any_sync(0xffffffffu, fabsf(shift) >= kFar);
-      if (far) {  // warp-uniform, rare
+          for (int k = 0; k < 128; ++k)
+            if (k >= n) sv[k] = -INFINITY;
+        }
+        // the largest y: of each piece the largest product, then its scale (positive)
+        float ks[C::PIECES], top[C::PIECES];
 #pragma unroll
         for (int g = 0; g < C::PIECES; ++g) {
-          const float lv = sc[g].y;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) sv[g * 16 + i] = fmaf(sv[g * 16 + i], ks[g], lv) + shift;
-          ks[g] = 1.f;
+          const float* x = sv + g * 16;
+          float m = fmax3(fmax3(x[0], x[1], x[2]), fmax3(x[3], x[4], x[5]), fmax3(x[6], x[7], x[8]));
+          m = fmax3(m, fmax3(x[9], x[10], x[11]), fmax3(x[12], x[13], x[14]));
+          const float2 kl = *reinterpret_cast<const float2*>(&sc[g]);
+          ks[g] = fmaxf(kl.x * back, 1.17549435e-38f);
+          top[g] = fmaf(fmaxf(m, x[15]), ks[g], kl.y);
         }
-      }
-      float lw = 0.f;
+        const float m_blk = fmax3(fmax3(top[0], top[1], top[2]), fmax3(top[3], top[4], top[5]),
+                                  fmaxf(top[6], top[7]));
+        // (-inf) - (-inf) is NaN, which moves nothing
+        const bool rescale = m_blk - r_run > kRoom;
+        const float r_new = rescale ? (fabsf(m_blk) < kFar ? m_blk - kOff : m_blk) : r_run;
+        const float shift = r_new == -INFINITY ? 0.f : -r_new;
+        const float alpha = rescale ? ex2(r_run + shift) : 1.f;
+        // p = 2^(s ks + (log2 vs - r)).  Far from zero, the rounding of y that the check
+        // above saw is itself large: there p is formed from the rounded y
+        const bool far = __any_sync(0xffffffffu, fabsf(shift) >= kFar);
+        if (far) {  // warp-uniform, rare
 #pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        uint32_t pk[32];
+          for (int g = 0; g < C::PIECES; ++g) {
+            const float lv = sc[g].y;
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
-          const float c = far ? 0.f : sc[hh * 4 + g].y + shift;
-#pragma unroll
-          for (int i = 0; i < 16; i += 4) {
-            const int k = g * 16 + i, kk = hh * 64 + k;
-            float p0, p1, p2, p3;
-            fma_x2(sv[kk], sv[kk + 1], ks[hh * 4 + g], c, p0, p1);
-            fma_x2(sv[kk + 2], sv[kk + 3], ks[hh * 4 + g], c, p2, p3);
-            p0 = ex2(p0);
-            p1 = ex2(p1);
-            p2 = ex2(p2);
-            p3 = ex2(p3);
-            add_x2(l0, l1, p0, p1, l0, l1);
-            add_x2(l2, l3, p2, p3, l2, l3);
-            asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(pk[k / 2]) : "f"(p1), "f"(p0));
-            asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(pk[k / 2 + 1]) : "f"(p3), "f"(p2));
+            for (int i = 0; i < 16; ++i) sv[g * 16 + i] = fmaf(sv[g * 16 + i], ks[g], lv) + shift;
+            ks[g] = 1.f;
           }
-          lw = fmaf((l0 + l1) + (l2 + l3), sc[hh * 4 + g].z, lw);
         }
-        if (C::DEC && hh == 0 && j > 0) {
-          // O_s += P_s V_{j-1} has finished: P_s's columns are free and O_s complete
-          mbar_wait(bar(B_PV_DONE + s), (j - 1) & 1, wctx, ERR_SITE_CACHE_FWD + 14);
-          tc_fence_after();
-        }
-        tmem_st32(tP + hh * 32, pk);
-        if (hh == 0) {
-          if (j > 0 && __any_sync(0xffffffffu, rescale)) {
+        float lw = 0.f;
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t o[32];
-              tmem_ld32(tO + c * 32, o);
-              tmem_wait_ld(o);
+        for (int hh = 0; hh < 2; ++hh) {
+          uint32_t pk[32];
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-              tmem_st32(tO + c * 32, o);
+          for (int g = 0; g < 4; ++g) {
+            float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
+            const float c = far ? 0.f : sc[hh * 4 + g].y + shift;
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+              const int k = g * 16 + i, kk = hh * 64 + k;
+              float p0, p1, p2, p3;
+              fma_x2(sv[kk], sv[kk + 1], ks[hh * 4 + g], c, p0, p1);
+              fma_x2(sv[kk + 2], sv[kk + 3], ks[hh * 4 + g], c, p2, p3);
+              p0 = ex2(p0);
+              p1 = ex2(p1);
+              p2 = ex2(p2);
+              p3 = ex2(p3);
+              add_x2(l0, l1, p0, p1, l0, l1);
+              add_x2(l2, l3, p2, p3, l2, l3);
+              asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(pk[k / 2]) : "f"(p1), "f"(p0));
+              asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(pk[k / 2 + 1]) : "f"(p3), "f"(p2));
             }
+            lw = fmaf((l0 + l1) + (l2 + l3), sc[hh * 4 + g].z, lw);
           }
-          tmem_wait_st();
-          tc_fence_before();
-          mbar_arrive(bar(B_P_HALF + s));
+          if (C::DEC && hh == 0 && j > 0) {
+            // O_s += P_s V_{j-1} has finished: P_s's columns are free and O_s complete
+            mbar_wait(bar(B_PV_DONE + s), (j - 1) & 1, wctx, ERR_SITE_CACHE_FWD + 14);
+            tc_fence_after();
+          }
+          tmem_st32(tP + hh * 32, pk);
+          if (hh == 0) {
+            if (j > 0 && __any_sync(0xffffffffu, rescale)) {
+#pragma unroll
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld32(tO + c * 32, o);
+                tmem_wait_ld(o);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                tmem_st32(tO + c * 32, o);
+              }
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(bar(B_P_HALF + s));
+          }
         }
+        l_run = l_run * alpha + lw;
+        r_run = r_new;
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(bar(B_P_FULL + s));
       }
-      l_run = l_run * alpha + lw;
-      r_run = r_new;
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(bar(B_P_FULL + s));
+      if (j == my_nt) break;
+      // (rare) another pass, from another b
+      first -= n_tiles;
+      const int pass = j / n_tiles;
+      float* lse_part = reinterpret_cast<float*>(smem + C::OFF_LSE) + threadIdx.x;
+      const float more = l_run == 0.f ? -INFINITY : add_log2(r_run, l_run);
+      *lse_part = pass == 1 ? more : log2_add(*lse_part, more);
+      l_run = 0.f;
+      r_run += (float)(scan->b[pass - 1] - scan->b[pass]);
     }
 
     // ------------------------------------------------------------ epilogue
-    const float base = lg2(scale0);
-    const bool has = my_nt > 0 && !(l_run == 0.f);
-    const float inv = has ? 1.f / l_run : 0.f, up = ex2(base);
-    const float lse = has ? (r_run - base + lg2(l_run)) * kLn2 : -INFINITY;
+    bool has = my_nt > 0 && !(l_run == 0.f);
+    float inv = has ? 1.f / l_run : 0.f, up = ex2((float)(scan->b[0] - 127));
+    float lse = has ? add_log2(r_run, l_run) : -INFINITY;
+    if (__builtin_expect(my_nt > my_c, 0)) {  // several passes: O = 2^(r + b - LSE) acc
+      const float more = lse, b_last = (float)(scan->b[scan->passes - 1] - 127);
+      lse = log2_add(reinterpret_cast<float*>(smem + C::OFF_LSE)[threadIdx.x], more);
+      has = !(lse == -INFINITY);
+      inv = up = ex2(0.5f * (r_run + b_last - lse));
+    }
+    lse *= kLn2;
     if (my_nt > 0) {
       mbar_wait(bar(B_PV_DONE + s), (my_nt - 1) & 1, wctx, ERR_SITE_CACHE_FWD + 12);
       tc_fence_after();
@@ -981,7 +1116,7 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
       uint16_t* o_row = p.o.p + at * p.o.st + (long long)(h * G + p.by_G.mod(row)) * p.o.sh;
       float* part_row = piece_view(p).o + ((size_t)max(part, 0) * C::ROWS + row) * D;
       const int from = max(t0 * C::BN, lim_lo & ~31);  // whole 32-row pieces were cleared
-      const int to = min(limit_of(row), (t0 + n_max) * C::BN);
+      const int to = min(limit_of(row), (t0 + n_tiles) * C::BN);
       for (int key = from; key < to; ++key) {
         const int page = p.c.block_table[(long long)b * p.c.table_width + (key >> p.c.block_log2)];
         if (page < 0 || page >= p.c.num_blocks) continue;
