@@ -550,9 +550,11 @@ def cache_forward(q, cache, batch, scale, causal, out=None, workspace=None, stre
         key = (dev, cache[0].shape, batch[0].shape, total, batch[4], Hq)
         nbytes = _ws_bytes.get(key)
         if nbytes is None:
+            nbytes = int(lib.fattn_cache_fwd_workspace_bytes(c, b, Hq))
             if len(_ws_bytes) > 4096:
                 _ws_bytes.clear()
-            nbytes = _ws_bytes[key] = int(lib.fattn_cache_fwd_workspace_bytes(c, b, Hq))
+            if nbytes:  # (0: a failure, which the call below reports)
+                _ws_bytes[key] = nbytes
         workspace = torch.empty((max(nbytes, 256),), dtype=torch.uint8, device=on)
     else:
         if workspace.get_device() != dev or not workspace.is_contiguous():

@@ -128,3 +128,31 @@ def test_binding_refuses_wrong_tensors():
         fattn.cache_forward(x[0], cache, batch, 0.1, True)
     with pytest.raises(ValueError):
         fattn.new_cache(6, 2, 16, 64, dtype=torch.bfloat16, device="cpu")
+
+
+def test_a_failed_workspace_query_is_not_remembered(monkeypatch):
+    """0 bytes is the query's failure; the next call of the same sizes asks again."""
+    class Lib:
+        answers, calls = [0, 4096], []
+
+        def fattn_cache_fwd_workspace_bytes(self, c, b, Hq):
+            return self.answers.pop(0)
+
+        def fattn_cache_fwd(self, *args):
+            self.calls.append(args[13])
+            return WORKSPACE if args[13] < 4096 else 0
+
+    cache = fattn.new_cache(6, 2, 16, 64, device="cpu")
+    i32 = lambda *a: torch.tensor(a, dtype=torch.int32)
+    batch = fattn.CacheBatch(i32([0, 1], [2, 3]), i32(20, 9), i32(0, 3, 5), 5, 3)
+    q = torch.zeros((5, 4, 64), dtype=torch.bfloat16)
+    monkeypatch.setattr(fattn, "_cache_args", lambda c, b: (b"", b"", -1, 2, 64))
+    monkeypatch.setattr(fattn, "_elsewhere", lambda dev, stream: False)
+    monkeypatch.setattr(fattn, "_raw_stream", lambda dev: 0)
+    monkeypatch.setattr(fattn, "_ws_bytes", {})
+    monkeypatch.setattr(fattn, "_lib", Lib())
+    with pytest.raises(fattn.FattnError):
+        fattn.cache_forward(q, cache, batch, 0.1, True)
+    for _ in range(2):  # the answer is asked for once
+        fattn.cache_forward(q, cache, batch, 0.1, True)
+    assert Lib.calls[1:] == [4096, 4096] and not Lib.answers
