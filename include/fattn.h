@@ -304,9 +304,9 @@ typedef struct {
  * The three arrays are DEVICE int32, 4-byte aligned: cu_seqlens B + 1
  * non-decreasing offsets from 0, at most `total`; rows at and behind
  * cu_seqlens[B] are neither read nor written, so a captured graph can be sized
- * for more tokens than a replay has.  max_seqlen >= every n_b (it sizes the
- * grids).  table_width x block_size is at most 2^31 - 65536.  A block may appear
- * in several sequences (a shared prefix) as long as no call appends to it.
+ * for more tokens than a replay has.  max_seqlen >= every n_b and at most
+ * `total` (it sizes the grids; 0 launches nothing).  table_width x block_size is
+ * at most 2^31 - 65536.  A block may appear in several sequences (a shared prefix) as long as no call appends to it.
  * Entries are checked on the device.  A sequence with offsets out of range or
  * decreasing, n_b > max_seqlen, or a length that is negative, beyond its table
  * row or (append, read) below n_b is skipped (where offsets do not ascend, any
@@ -348,14 +348,16 @@ int fattn_cache_append(const fattn_cache* cache, const fattn_cache_batch* batch,
 
 /* The inverse: the last n_b tokens of each sequence as bf16(scale * code), into
  * k and v laid out as for fattn_cache_append (strides >= d here).  Exact for
- * the scales that append writes. */
+ * the scales that append writes (but for bf16 values next to 2^128, whose code
+ * rounds up to it and becomes an infinity here). */
 int fattn_cache_read(const fattn_cache* cache, const fattn_cache_batch* batch, void* k,
                      long long k_token_stride, long long k_head_stride, void* v,
                      long long v_token_stride, long long v_head_stride, void* stream);
 
 /* Attention of the last n_b tokens of each sequence over its cache.
  * q, o: DEVICE bf16 [total, Hq, d] by strides as above (o's strides >= d); Hq a
- * multiple of H, query head h reads key/value head h / (Hq / H).  lse: DEVICE
+ * multiple of H, query head h reads key/value head h / (Hq / H); o may be q
+ * itself, with its strides.  lse: DEVICE
  * fp32 [Hq, total], contiguous (the layout of fattn_fwd_varlen), 16-byte
  * aligned.  Query i of sequence b stands at position lens[b] - n_b + i; with
  * causal it sees keys at or before its position, else every key of the
@@ -363,7 +365,8 @@ int fattn_cache_read(const fattn_cache* cache, const fattn_cache_batch* batch, v
  * exceed lens[b].  Values of keys that a query does not see never reach its
  * row, whatever they are (NaN included); an e5m2 infinity, which append never
  * writes, gives the rows that see it an infinity or NaN.
- * Scores, statistics and sums are fp32.  A weight, times its value scale, is
+ * Scores, statistics and sums are fp32, of q exact down to 2^-29 of the largest
+ * element of its row.  A weight, times its value scale, is
  * rounded to fp16 relative to the largest of its row among blocks whose scales
  * lie within 2^20 of each other or below: 11 bits down to 2^-22 of that, an
  * error of 2^-33 of it below.
