@@ -306,7 +306,8 @@ typedef struct {
  * cu_seqlens[B] are neither read nor written, so a captured graph can be sized
  * for more tokens than a replay has.  max_seqlen >= every n_b and at most
  * `total` (it sizes the grids; 0 launches nothing).  table_width x block_size is
- * at most 2^31 - 65536.  A block may appear in several sequences (a shared prefix) as long as no call appends to it.
+ * at most 2^31 - 65536.  A block may appear in several sequences (a shared
+ * prefix) as long as no call appends to it.
  * Entries are checked on the device.  A sequence with offsets out of range or
  * decreasing, n_b > max_seqlen, or a length that is negative, beyond its table
  * row or (append, read) below n_b is skipped (where offsets do not ascend, any
