@@ -19,8 +19,8 @@
 //
 // Memory-bound: the item's values stay in registers (64 per lane) between the
 // maximum and the conversion, so every value is read once and written once.  Measured
-// (d = 128): 32768 tokens of 16 heads written in 62.3 us, 95 % of the measured copy
-// bandwidth; 16 sequences of 512 to 8192 tokens of 16 heads read back in 85 us, 98 %;
+// (d = 128): 32768 tokens of 16 heads written in 62.8 us, 95 % of the measured copy
+// bandwidth; 16 sequences of 512 to 8192 tokens of 16 heads read back in 86 us, 97 %;
 // one token of each of 256 sequences, 8 heads, 7 us, which is the search for the
 // sequence, its block and its values one after the other.
 #include "cache.cuh"

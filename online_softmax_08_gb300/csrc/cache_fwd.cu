@@ -26,10 +26,10 @@
 // bandwidth an SM gets about 24 codes a clock, and a 16-key tile of keys and
 // values (4 KB at d = 128) costs 174 clocks, of which the arithmetic below takes
 // about half of the issue slots.  Measured: 4 sequences of 32768 tokens, 32 heads,
-// d = 128 (1.07 GB) 164 us, 97 % of the measured copy bandwidth; 32 sequences of 512
-// to 8192 tokens, 32 query and 8 key heads (186 MB) 41 us, 67 %: the start of a share
+// d = 128 (1.07 GB) 163 us, 97 % of the measured copy bandwidth; 32 sequences of 512
+// to 8192 tokens, 32 query and 8 key heads (185 MB) 41.5 us, 66 %: the start of a share
 // (offsets, block table, first codes, one after the other) takes 3 us, its end and
-// the merge 3 us; one sequence of 1000 tokens 8.5 us.  Three CTAs per SM and three ring
+// the merge 3 us; one sequence of 1000 tokens 8.6 us.  Three CTAs per SM and three ring
 // slots a warp: with four CTAs the registers spilled (221 us for the first case), with
 // two the loads in flight fell short (211 us).  With 1 to 16 rows per key/value head the
 // tensor work is far too small for a 128-row tcgen05 tile and its trip through
@@ -1025,9 +1025,9 @@ size_t narrow_bytes(int d, int n_sm) {  // the larger of the two variants
 // stays with the kernel above.  From 33 rows on it reads the keys three times and
 // more, and the 256-row kernel costs less of the machine, but finishes a small batch
 // later.  Measured with limits of 32 and 64 rows: 16 sequences of 1 to 1000 tokens, 16
-// key heads, d = 64, 79 and 102 us; 150 of 50 to 100 tokens, 4 heads, d = 128, 82 and
-// 148 us; 24 of 5 tokens, 2 key heads of 8 query heads, d = 64, 24 and 17 us.  (Many
-// sequences of very few keys lose by it, 134 of 7 keys, 8 heads of 7, 59 and 34 us: their
+// key heads, d = 64, 79 and 102 us; 150 of 50 to 100 tokens, 4 heads, d = 128, 84 and
+// 154 us; 24 of 5 tokens, 2 key heads of 8 query heads, d = 64, 24 and 17 us.  (Many
+// sequences of very few keys lose by it, 134 of 7 keys, 8 heads of 7, 61 and 35 us: their
 // lengths are not known on the host.)
 int narrow_limit(const CacheParams& c, int n_sm) {
   return (long long)c.B * c.H >= n_sm ? 32 : 64;

@@ -42,8 +42,8 @@
 // load Q and write O), 8-11 fill the slots, 12 issues the MMAs, 13-15 look up the value
 // scales.  TMEM: S_0, S_1, O_0, O_1 (d = 64: P_0, P_1).
 //
-// Measured, 2048 tokens behind 8192 (32 query, 8 key heads, d = 128): 253 us, 1222
-// TFLOP/s, tensor pipe 50 % active.  256 units on 152 SMs are two rounds where 1.7
+// Measured, 2048 tokens behind 8192 (32 query, 8 key heads, d = 128): 255 us, 1212
+// TFLOP/s, tensor pipe 51 % active.  256 units on 152 SMs are two rounds where 1.7
 // would do (16 %); a tile of 128 keys takes 3100 clocks against the MMAs' 2048, the
 // MMA warp's own issue (1750) and its waits for P (1350) alternating; the start and
 // end of a piece take 11,000 and 5,000 clocks of 250,000.  At d = 64 (16 sequences of
