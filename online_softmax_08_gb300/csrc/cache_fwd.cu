@@ -430,8 +430,8 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
 
   int f = 0;             // the tile (of all warps) that comes next
   bool resumed = false;  // in the middle of a unit
-  bool calm = false;     // its scale is settled:
-  float calm_lv = 0.f;   // log2 vs - b
+  bool calm = false;     // that tile's scale is settled:
+  float calm_lv = 0.f;   // its log2 vs - b
   int only = 0;          // 1, 2: only the first, the second part of it
   while (f < F) {
     const int h = cur.h, rb = cur.rb;
@@ -756,127 +756,126 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
     // ---------------------------------------------------------------- the unit (or piece) ends
     const int ch = cur.ch;
     const bool unit_ends = ch == cur.nch - 1;
-    {
-      if (__builtin_expect(parked, 0)) {  // rare: all of it as if it were one key's
-        float keep[NT][2], add[NT][2];
-        join(keep, add, ref);
+    if (__builtin_expect(parked, 0)) {  // rare: all of it as if it were one key's
+      float keep[NT][2], add[NT][2];
+      join(keep, add, ref);
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              acc[mt][nt][i] = aside[((mt * NT + nt) * 4 + i) * 32] * keep[nt][i & 1] +
-                               acc[mt][nt][i] * add[nt][i & 1];
+      for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) lsum[nt][i] = g == 0 && ref[nt][i] != -INFINITY ? 1.f : 0.f;
-        lvb = 0.f;
+          for (int i = 0; i < 4; ++i)
+            acc[mt][nt][i] = aside[((mt * NT + nt) * 4 + i) * 32] * keep[nt][i & 1] +
+                             acc[mt][nt][i] * add[nt][i & 1];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) lsum[nt][i] = g == 0 && ref[nt][i] != -INFINITY ? 1.f : 0.f;
+      lvb = 0.f;
+    }
+    // this warp's rows: normalised result and log2-sum-exp
+    float mine[NT][2], fac[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float l = lsum[nt][i];
+#pragma unroll
+        for (int w = 4; w < 32; w <<= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
+        lsum[nt][i] = l;
+        mine[nt][i] = l == 0.f ? -INFINITY : ref[nt][i] + lg2(l);
+        if (g == 0) stat[warp * R + nt * 8 + 2 * t + i] = mine[nt][i];
       }
-      // this warp's rows: normalised result and log2-sum-exp
-      float mine[NT][2], fac[NT][2];
+    __syncthreads();
+    float top[NT][2], sum[NT][2];
+    const float up = ex2(lvb);
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float l = lsum[nt][i];
+      for (int i = 0; i < 2; ++i) {
+        const int r = nt * 8 + 2 * t + i;
+        float m = -INFINITY, z = 0.f;
 #pragma unroll
-          for (int w = 4; w < 32; w <<= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
-          lsum[nt][i] = l;
-          mine[nt][i] = l == 0.f ? -INFINITY : ref[nt][i] + lg2(l);
-          if (g == 0) stat[warp * R + nt * 8 + 2 * t + i] = mine[nt][i];
-        }
-      __syncthreads();
-      float top[NT][2], sum[NT][2];
-      const float up = ex2(lvb);
+        for (int w = 0; w < kWarps; ++w) m = fmaxf(m, stat[w * R + r]);
+        const float mm = m == -INFINITY ? 0.f : m;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) z += ex2(stat[w * R + r] - mm);
+        top[nt][i] = m;
+        sum[nt][i] = z;
+        fac[nt][i] = lsum[nt][i] == 0.f ? 0.f : ex2(mine[nt][i] - mm) / (z * lsum[nt][i]);
+      }
+    // the warps' results side by side; 16-byte columns are permuted so that the lanes
+    // of a store phase (two g, four t) touch different banks
+    auto column = [&](int r, int c4) {
+      const int k = r >> 1;  // t of the lane that holds row r
+      return D == 128 ? c4 ^ (((c4 >> 4) & 1) << 2 | (k & 3))
+                      : c4 ^ ((k & 1) << 2 | ((k >> 1) & 1));
+    };
+    float4* red4 = reinterpret_cast<float4*>(red);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = nt * 8 + 2 * t + i;
+#pragma unroll
+        for (int j = 0; j < VW; ++j)
+          red4[(warp * R + r) * (D / 4) + column(r, vcol / 4 + j)] = make_float4(
+              acc[2 * j][nt][i] * fac[nt][i] * up, acc[2 * j][nt][i + 2] * fac[nt][i] * up,
+              acc[2 * j + 1][nt][i] * fac[nt][i] * up,
+              acc[2 * j + 1][nt][i + 2] * fac[nt][i] * up);
+      }
+    __syncthreads();
+    const bool starts_here = f > ch;  // the unit's chunk 0 is in this share
+    const bool whole = starts_here && unit_ends;
+    const int slot = starts_here ? 1 : 0;
+    if (warp == 0 && g == 0) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int r = nt * 8 + 2 * t + i;
-          float m = -INFINITY, z = 0.f;
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) m = fmaxf(m, stat[w * R + r]);
-          const float mm = m == -INFINITY ? 0.f : m;
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) z += ex2(stat[w * R + r] - mm);
-          top[nt][i] = m;
-          sum[nt][i] = z;
-          fac[nt][i] = lsum[nt][i] == 0.f ? 0.f : ex2(mine[nt][i] - mm) / (z * lsum[nt][i]);
-        }
-      // the warps' results side by side; 16-byte columns are permuted so that the lanes
-      // of a store phase (two g, four t) touch different banks
-      auto column = [&](int r, int c4) {
-        const int k = r >> 1;  // t of the lane that holds row r
-        return D == 128 ? c4 ^ (((c4 >> 4) & 1) << 2 | (k & 3))
-                        : c4 ^ ((k & 1) << 2 | ((k >> 1) & 1));
-      };
-      float4* red4 = reinterpret_cast<float4*>(red);
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int r = nt * 8 + 2 * t + i;
-#pragma unroll
-          for (int j = 0; j < VW; ++j)
-            red4[(warp * R + r) * (D / 4) + column(r, vcol / 4 + j)] = make_float4(
-                acc[2 * j][nt][i] * fac[nt][i] * up, acc[2 * j][nt][i + 2] * fac[nt][i] * up,
-                acc[2 * j + 1][nt][i] * fac[nt][i] * up,
-                acc[2 * j + 1][nt][i + 2] * fac[nt][i] * up);
-        }
-      __syncthreads();
-      const bool starts_here = f > ch;  // the unit's chunk 0 is in this share
-      const bool whole = starts_here && unit_ends;
-      const int slot = starts_here ? 1 : 0;
-      if (warp == 0 && g == 0) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int r = nt * 8 + 2 * t + i;
-            const float L = top[nt][i] == -INFINITY && sum[nt][i] == 0.f
-                                ? -INFINITY
-                                : (top[nt][i] + lg2(sum[nt][i])) * kLn2;
-            if (r < rows) {
-              if (whole) {
-                const int i0 = rb * R + r;
-                p.lse[(long long)(h * G + p.by_G.mod(i0)) * p.c.total + cur.seq.row0 + p.by_G.div(i0)] = L;
-              } else {
-                part_lse[((size_t)blockIdx.x * 2 + slot) * R + r] = L;
-              }
+          const float L = top[nt][i] == -INFINITY && sum[nt][i] == 0.f
+                              ? -INFINITY
+                              : (top[nt][i] + lg2(sum[nt][i])) * kLn2;
+          if (r < rows) {
+            if (whole) {
+              const int i0 = rb * R + r;
+              p.lse[(long long)(h * G + p.by_G.mod(i0)) * p.c.total + cur.seq.row0 +
+                    p.by_G.div(i0)] = L;
+            } else {
+              part_lse[((size_t)blockIdx.x * 2 + slot) * R + r] = L;
             }
           }
-      }
-      for (int x = threadIdx.x; x < rows * (D / 4); x += 128) {
-        const int r = x / (D / 4), c4 = x % (D / 4);
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float4 y = red4[(w * R + r) * (D / 4) + column(r, c4)];
-          o.x += y.x, o.y += y.y, o.z += y.z, o.w += y.w;
         }
-        if (whole) {
-          const int i0 = rb * R + r;
-          *reinterpret_cast<uint2*>(p.o.p + (long long)(cur.seq.row0 + p.by_G.div(i0)) * p.o.st +
-                                    (long long)(h * G + p.by_G.mod(i0)) * p.o.sh + c4 * 4) =
-              make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
-        } else {
-          reinterpret_cast<float4*>(part_o)[(((size_t)blockIdx.x * 2 + slot) * R + r) * (D / 4) +
-                                            c4] = o;
-        }
-      }
-      if (starts_here && !unit_ends) {  // later CTAs hold the rest
-        rec.parts = 1 + (cur.nch - 1 - ch + (int)share - 1) / (int)share;
-        rec.rows = rows;
-        rec.h = h;
-        rec.row0 = cur.seq.row0;
-        rec.first_row = rb * R;
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(red_bar);
-      ++ended;
     }
+    for (int x = threadIdx.x; x < rows * (D / 4); x += 128) {
+      const int r = x / (D / 4), c4 = x % (D / 4);
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float4 y = red4[(w * R + r) * (D / 4) + column(r, c4)];
+        o.x += y.x, o.y += y.y, o.z += y.z, o.w += y.w;
+      }
+      if (whole) {
+        const int i0 = rb * R + r;
+        *reinterpret_cast<uint2*>(p.o.p + (long long)(cur.seq.row0 + p.by_G.div(i0)) * p.o.st +
+                                  (long long)(h * G + p.by_G.mod(i0)) * p.o.sh + c4 * 4) =
+            make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+      } else {
+        reinterpret_cast<float4*>(part_o)[(((size_t)blockIdx.x * 2 + slot) * R + r) * (D / 4) +
+                                          c4] = o;
+      }
+    }
+    if (starts_here && !unit_ends) {  // later CTAs hold the rest
+      rec.parts = 1 + (cur.nch - 1 - ch + (int)share - 1) / (int)share;
+      rec.rows = rows;
+      rec.h = h;
+      rec.row0 = cur.seq.row0;
+      rec.first_row = rb * R;
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(red_bar);
+    ++ended;
     advance<C>(p, &cur, 1);
   }
   // loads in flight land before the CTA ends (only after a wait that ran out)
