@@ -260,14 +260,15 @@ int fattn_fwd_bwd_host(const void* q, const void* k, const void* v, const void* 
                        float scale, int causal, int heads_per_chunk, void* workspace,
                        size_t workspace_bytes, void* stream);
 
-/* ------------------------------------------------------------------ 8-bit key/value cache
+/* ------------------------------------------------------------------ key/value cache
  *
- * A paged cache of keys and values in 8 bits, its writer, its reader and the
+ * A paged cache of keys and values in 8 or 4 bits, its writer, its reader and the
  * attention over it, for serving: the keys and values of `fattn_decode` kept
- * from step to step at half the bytes, with grouped heads.  The pages have no
- * counterpart to the storage; the attention is their recurrence over it.
+ * from step to step at half the bytes or 0.28 of them, with grouped heads.  The
+ * pages have no counterpart to the storage; the attention is their recurrence
+ * over it.
  *
- * The pool.  k and v hold num_blocks blocks of block_size tokens for each of H
+ * The pool, 8 bits.  k and v hold num_blocks blocks of block_size tokens for each of H
  * key/value heads, [num_blocks, H, block_size, d], one 8-bit floating code per
  * value; k_scale and v_scale hold one fp32 scale per (block, head),
  * [num_blocks, H].  The value that code c of a block stands for is scale * c.
@@ -278,17 +279,27 @@ int fattn_fwd_bwd_host(const void* q, const void* k, const void* v, const void* 
  * fattn_cache_append writes powers of two as scales; the reader and the
  * attention take any positive normal fp32.  Where value scales of one sequence
  * and head differ by more than 2^60 (a block of zeros has the smallest one,
- * 2^-100), the attention takes the smaller as 2^-60 of the larger. */
+ * 2^-100), the attention takes the smaller as 2^-60 of the larger.
+ *
+ * The pool, 4 bits.  k and v hold two codes a byte, [num_blocks, H, block_size,
+ * d / 2], the even channel in the low half; k_scale and v_scale hold an e5m2 scale
+ * for every 16 neighbouring channels of a token, bytes [num_blocks, H, block_size,
+ * d / 16].  The value that code c (0 to 15) stands for is (c - 8) * scale.  All four
+ * are 16-byte aligned.  Every token has its own scales, so nothing that is written
+ * later changes what is there.  The reader takes any scale; for the attention its
+ * magnitude is at most 7168, the largest that append writes (a row that sees a
+ * larger one, an infinity or a NaN gets values of no meaning; others do not). */
 typedef enum {
   FATTN_CACHE_E4M3 = 0, /* 4 exponent, 3 mantissa bits, largest value 448, no infinities */
-  FATTN_CACHE_E5M2 = 1  /* 5 exponent, 2 mantissa bits, largest value 57344 */
+  FATTN_CACHE_E5M2 = 1, /* 5 exponent, 2 mantissa bits, largest value 57344 */
+  FATTN_CACHE_INT4 = 4  /* whole numbers from -8 to 7, a scale for 16 channels of a token */
 } fattn_cache_format;
 
 typedef struct {
   void* k;
   void* v;
-  float* k_scale;
-  float* v_scale;
+  void* k_scale; /* float; 4 bits: e5m2 bytes */
+  void* v_scale;
   int num_blocks;
   int H; /* key/value heads */
   int block_size;
@@ -340,6 +351,13 @@ typedef struct {
  * (the ratio is a power of two, so only codes that become subnormal change
  * their value).  New values are divided by the scale (exact) and rounded to
  * nearest even.  NaN and infinities are stored as NaN and do not enter amax.
+ * 4 bits: with a the largest magnitude of 16 neighbouring channels, their scale is
+ * a / 8 rounded to the nearest e5m2 value, with a negative sign if one of them is +a,
+ * else a positive one, and c - 8 is x / scale rounded to the nearest whole number,
+ * ties to even, within [-8, 7].  Where the scale is at least 2^-14, a value that this
+ * range cuts is off by at most one scale if it has the largest one's sign, else by at
+ * most two, and every other by at most half of one.  Magnitudes beyond 57344 and
+ * infinities count as 57344, NaN as zero.
  * A call that is repeated with the same arguments leaves the same cache.
  * No block may be named twice among those that a call appends to (the writes
  * would race; nothing out of range is touched). */
@@ -347,10 +365,10 @@ int fattn_cache_append(const fattn_cache* cache, const fattn_cache_batch* batch,
                        long long k_token_stride, long long k_head_stride, const void* v,
                        long long v_token_stride, long long v_head_stride, void* stream);
 
-/* The inverse: the last n_b tokens of each sequence as bf16(scale * code), into
+/* The inverse: the last n_b tokens of each sequence as bf16 of their values, into
  * k and v laid out as for fattn_cache_append (strides >= d here).  Exact for
  * the scales that append writes (but for bf16 values next to 2^128, whose code
- * rounds up to it and becomes an infinity here). */
+ * rounds up to it and becomes an infinity here), and always in 4 bits. */
 int fattn_cache_read(const fattn_cache* cache, const fattn_cache_batch* batch, void* k,
                      long long k_token_stride, long long k_head_stride, void* v,
                      long long v_token_stride, long long v_head_stride, void* stream);
@@ -370,7 +388,7 @@ int fattn_cache_read(const fattn_cache* cache, const fattn_cache_batch* batch, v
  * element of its row.  A weight, times its value scale, is
  * rounded to fp16 relative to the largest of its row among blocks whose scales
  * lie within 2^20 of each other or below: 11 bits down to 2^-22 of that, an
- * error of 2^-33 of it below.
+ * error of 2^-33 of it below.  (4 bits: no scales, the weights alone.)
  * workspace: DEVICE memory of fattn_cache_fwd_workspace_bytes(...) bytes,
  * 256-byte aligned, owned by the caller, its contents on entry do not matter;
  * calls that overlap on the GPU need one each.  Returns FATTN_OK,

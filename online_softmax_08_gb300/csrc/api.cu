@@ -491,7 +491,9 @@ int check_cache_sizes(const fattn_cache* c, const fattn_cache_batch* b) {
   if (c->num_blocks < 1 || c->H < 1 || c->H > 65535 || b->B < 1 || b->table_width < 1 ||
       b->total < 0 || b->max_seqlen < 0 || b->max_seqlen > b->total)
     return FATTN_ERR_INVALID_ARG;
-  if (c->format != FATTN_CACHE_E4M3 && c->format != FATTN_CACHE_E5M2) return FATTN_ERR_UNSUPPORTED;
+  if (c->format != FATTN_CACHE_E4M3 && c->format != FATTN_CACHE_E5M2 &&
+      c->format != FATTN_CACHE_INT4)
+    return FATTN_ERR_UNSUPPORTED;
   if (c->block_size != 16 && c->block_size != 32 && c->block_size != 64 && c->block_size != 128)
     return FATTN_ERR_UNSUPPORTED;
   if (c->d != 64 && c->d != 128) return FATTN_ERR_UNSUPPORTED;
@@ -506,7 +508,10 @@ int check_cache_sizes(const fattn_cache* c, const fattn_cache_batch* b) {
 bool aligned4(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 int check_cache_pointers(const fattn_cache* c, const fattn_cache_batch* b) {
-  if (!aligned16(c->k) || !aligned16(c->v) || !aligned4(c->k_scale) || !aligned4(c->v_scale) ||
+  const bool scales = c->format == FATTN_CACHE_INT4
+                          ? aligned16(c->k_scale) && aligned16(c->v_scale)
+                          : aligned4(c->k_scale) && aligned4(c->v_scale);
+  if (!aligned16(c->k) || !aligned16(c->v) || !scales ||
       !aligned4(b->block_table) || !aligned4(b->lens) || !aligned4(b->cu_seqlens))
     return FATTN_ERR_INVALID_ARG;
   return FATTN_OK;
@@ -531,14 +536,20 @@ CacheParams cache_params(const fattn_cache* c, const fattn_cache_batch* b, unsig
   CacheParams p{};
   p.k = static_cast<uint8_t*>(c->k);
   p.v = static_cast<uint8_t*>(c->v);
-  p.k_scale = c->k_scale;
-  p.v_scale = c->v_scale;
+  const bool int4 = c->format == FATTN_CACHE_INT4;
+  if (int4) {
+    p.k_scale4 = static_cast<uint8_t*>(c->k_scale);
+    p.v_scale4 = static_cast<uint8_t*>(c->v_scale);
+  } else {
+    p.k_scale = static_cast<float*>(c->k_scale);
+    p.v_scale = static_cast<float*>(c->v_scale);
+  }
   p.num_blocks = c->num_blocks;
   p.H = c->H;
   p.block_size = c->block_size;
   p.block_log2 = c->block_size == 16 ? 4 : c->block_size == 32 ? 5 : c->block_size == 64 ? 6 : 7;
   p.d = c->d;
-  p.format = c->format;
+  p.format = int4 ? FMT_INT4 : c->format == FATTN_CACHE_E5M2 ? FMT_E5M2 : FMT_E4M3;
   p.block_table = b->block_table;
   p.lens = b->lens;
   p.cu_seqlens = b->cu_seqlens;
@@ -584,12 +595,18 @@ int cache_move(CacheMove launch, const fattn_cache* cache, const fattn_cache_bat
   return debug_post_call(e == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA, s);
 }
 
-// A cache's codes as {d, block_size, num_blocks * H} bytes, in boxes of 16 tokens
+// A cache's codes as {bytes of a row, block_size, num_blocks * H}, in boxes of 16 tokens
+// (4 bits: of 32 where a block has them)
 // whose 16-byte pieces are swizzled over the banks.
 bool make_cache_map(CUtensorMap* m, const void* codes, const fattn_cache* c) {
-  return make_map(m, codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, c->d, c->block_size,
-                  (long long)c->num_blocks * c->H, c->d, 16,
-                  c->d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+  const bool int4 = c->format == FATTN_CACHE_INT4;
+  const int row = int4 ? c->d / 2 : c->d;
+  const int tokens = int4 && c->block_size >= 32 ? 32 : 16;
+  return make_map(m, codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, row, c->block_size,
+                  (long long)c->num_blocks * c->H, row, tokens,
+                  row == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+                  : row == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                              : CU_TENSOR_MAP_SWIZZLE_32B);
 }
 
 int check_cache_heads(const fattn_cache* c, const fattn_cache_batch* b, int Hq) {
@@ -605,15 +622,17 @@ extern "C" int fattn_cache_append(const fattn_cache* cache, const fattn_cache_ba
                                   const void* k, long long k_token_stride, long long k_head_stride,
                                   const void* v, long long v_token_stride, long long v_head_stride,
                                   void* stream) {
-  return cache_move(launch_cache_append, cache, batch, k, k_token_stride, k_head_stride, v,
-                    v_token_stride, v_head_stride, 0, stream);
+  const bool int4 = cache && cache->format == FATTN_CACHE_INT4;
+  return cache_move(int4 ? launch_cache4_append : launch_cache_append, cache, batch, k,
+                    k_token_stride, k_head_stride, v, v_token_stride, v_head_stride, 0, stream);
 }
 
 extern "C" int fattn_cache_read(const fattn_cache* cache, const fattn_cache_batch* batch, void* k,
                                 long long k_token_stride, long long k_head_stride, void* v,
                                 long long v_token_stride, long long v_head_stride, void* stream) {
-  return cache_move(launch_cache_read, cache, batch, k, k_token_stride, k_head_stride, v,
-                    v_token_stride, v_head_stride, 1, stream);
+  const bool int4 = cache && cache->format == FATTN_CACHE_INT4;
+  return cache_move(int4 ? launch_cache4_read : launch_cache_read, cache, batch, k, k_token_stride,
+                    k_head_stride, v, v_token_stride, v_head_stride, 1, stream);
 }
 
 extern "C" size_t fattn_cache_fwd_workspace_bytes(const fattn_cache* cache,

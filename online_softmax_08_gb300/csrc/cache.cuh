@@ -1,6 +1,5 @@
-// cache.cuh -- what the host API and the kernels of the 8-bit key/value cache share:
-// launch parameters, the 8-bit formats' conversions and the search for a packed
-// token's sequence.
+// cache.cuh -- what the host API and the kernels of the key/value cache share: launch
+// parameters, the formats' conversions and the search for a packed token's sequence.
 #pragma once
 #include "common.cuh"
 #include "ptx.cuh"
@@ -33,13 +32,18 @@ struct FastDiv {
 #endif
 };
 
-// The 8-bit key/value cache: the pool of blocks and the tokens a call works on
+// CacheParams::format and the kernels' template argument
+enum : int { FMT_E4M3 = 0, FMT_E5M2 = 1, FMT_INT4 = 2 };
+
+// The key/value cache: the pool of blocks and the tokens a call works on
 // (fattn_cache and fattn_cache_batch, with the device's error word).
 struct CacheParams {
-  uint8_t* k;            // [num_blocks, H, block_size, d] codes
+  uint8_t* k;            // [num_blocks, H, block_size, d] codes (4 bits: d / 2 bytes)
   uint8_t* v;
   float* k_scale;        // [num_blocks, H]
   float* v_scale;
+  uint8_t* k_scale4;     // 4 bits, in their place: [num_blocks, H, block_size, d / 16], e5m2
+  uint8_t* v_scale4;
   int num_blocks, H, block_size, d, format;
   int block_log2;        // block_size = 1 << block_log2
   const int* block_table;
@@ -98,13 +102,18 @@ __device__ __forceinline__ bool cache_seq(const CacheParams& c, int b, CacheSeq*
   return cache_seq(c, c.cu_seqlens[b], c.cu_seqlens[b + 1], c.lens[b], s);
 }
 
-// The 8-bit key/value cache (append, read back, attention over it).
+// The cache in 8 bits and in 4: append, read back, attention over it.
 cudaError_t launch_cache_append(const CacheParams& c, const TokenView& k, const TokenView& v,
                                 cudaStream_t stream);
 cudaError_t launch_cache_read(const CacheParams& c, const TokenView& k, const TokenView& v,
                               cudaStream_t stream);
+cudaError_t launch_cache4_append(const CacheParams& c, const TokenView& k, const TokenView& v,
+                                 cudaStream_t stream);
+cudaError_t launch_cache4_read(const CacheParams& c, const TokenView& k, const TokenView& v,
+                               cudaStream_t stream);
 size_t cache_fwd_workspace(const CacheParams& c, int G, int n_sm);
-// tk, tv: maps of the codes, {d, block_size, num_blocks * H}, boxes of 16 tokens
+// tk, tv: maps of the codes, {bytes of a row, block_size, num_blocks * H}, boxes of 16
+// tokens (4 bits: of 32 where block_size is at least that)
 cudaError_t launch_cache_fwd(const CUtensorMap& tk, const CUtensorMap& tv, const CacheFwdParams& p,
                              int n_sm, cudaStream_t stream);
 int cache_fwd_wide_rows();  // rows per unit of the 256-row kernel
@@ -156,6 +165,54 @@ __device__ __forceinline__ uint16_t f32_to_codes(float lo, float hi) {
   else
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
+}
+
+// ---- 4 bits.  The value of code c with the e5m2 scale s is (c - 8) s: at most 7
+// significant bits, exact in fp16 (and bf16).  The kernels form it times 2^-7, in one
+// fused multiply-add per pair of codes: a code put into the mantissa of 1024 (0x6400) is
+// 1024 + c, one four bits higher into that of 64 (0x5400) is 64 + c, and
+//   (1024 + c) s' - 1032 s' = (64 + c) s' - 72 s' = (c - 8) s',   s' = 2^-7 s,
+// with every term exact: 1032 s' has 10 bits and stays below 2^16 for |s| <= 7168, the
+// largest scale that is written, and the smallest, 2^-16, leaves s' = 2^-23.
+// (An e2m1 code takes four logic instructions where this takes 1.25, and with an e4m3
+// scale it misses normal values by 0.0090 of their variance, this by 0.0066.)
+constexpr float kInt4Unit = 128.f;    // 2^7, which the results are multiplied by
+constexpr int kInt4UnitLog2 = 7;
+constexpr uint32_t kInt4MaxScale = 0x6fu;  // 7168 as e5m2
+struct Int4Scale {
+  uint32_t s, lo, hi;  // pairs of fp16: s', -1032 s', -72 s'
+};
+__device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// of two e5m2 scales in the upper bytes of the halves (an e5m2 value is the upper byte of
+// the fp16 one)
+__device__ __forceinline__ Int4Scale int4_scale(uint32_t e5m2_hi) {
+  Int4Scale r;
+  r.s = mul_f16x2(e5m2_hi, 0x20002000u);     // 2^-7
+  r.lo = mul_f16x2(r.s, 0xe408e408u);        // -1032
+  r.hi = mul_f16x2(r.s, 0xd480d480u);        // -72
+  return r;
+}
+// Eight codes, four in each half of w -> (c_i, c_i+4) of i = 0 ... 3 as pairs of fp16.
+__device__ __forceinline__ void int4_values(uint32_t w, const Int4Scale& s, uint32_t (&o)[4]) {
+  const uint32_t u = w >> 8;
+  o[0] = fma_f16x2((w & 0x000f000fu) | 0x64006400u, s.s, s.lo);
+  o[1] = fma_f16x2((w & 0x00f000f0u) | 0x54005400u, s.s, s.hi);
+  o[2] = fma_f16x2((u & 0x000f000fu) | 0x64006400u, s.s, s.lo);
+  o[3] = fma_f16x2((u & 0x00f000f0u) | 0x54005400u, s.s, s.hi);
+}
+// The scales of a word that append never writes (above 7168, infinite, NaN) as zeros.
+__device__ __forceinline__ uint32_t int4_sane(uint32_t bytes) {
+  const uint32_t m = ((bytes & 0x7f7f7f7fu) + (0x7fu - kInt4MaxScale) * 0x01010101u) & 0x80808080u;
+  return bytes & ~(m | (m - (m >> 7)));
 }
 
 // 0x80 in the byte of each of four codes that stands for NaN (or, in e5m2, for

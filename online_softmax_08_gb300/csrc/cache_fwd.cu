@@ -1,5 +1,5 @@
-// cache_fwd.cu -- attention over the paged 8-bit key/value cache, few query rows
-// per key/value head (decoding, drafted tokens).
+// cache_fwd.cu -- attention over the paged key/value cache in 8 or 4 bits, few query
+// rows per key/value head (decoding, drafted tokens).
 //
 // The mathematics.  With codes k, v and scales ks, vs of key j's block, in base 2:
 //   x_j = scale log2(e) ks_j (q . k_j),   O = sum_j 2^x_j vs_j v_j / sum_j 2^x_j.
@@ -69,18 +69,21 @@ constexpr float kWindow = 10.f;    // log2 vs - b of the blocks that share sums
 constexpr float kNothing = -60.f;  // what lies below it is taken as it
 constexpr int kWarps = 4;
 
-template <int D, int NT_>
+template <int D, int NT_, bool I4>
 struct Dec {
   static constexpr int NT = NT_;
   static constexpr int R = 8 * NT;                // query rows per unit
-  static constexpr int PARTS = D == 128 ? 1 : 2;  // of 16 keys in a warp's tile (4 KB with values)
+  static constexpr int PARTS = D == 128 && !I4 ? 1 : 2;  // of 16 keys in a warp's tile
   static constexpr int KEYS = 16 * PARTS;
   static constexpr int CHUNK = kWarps * KEYS;     // keys per CTA step
-  static constexpr int PART = 16 * D;             // bytes of 16 keys or values: one TMA box
-  static constexpr int TILE = KEYS * D;
-  static constexpr int STAGE = 2 * TILE;          // keys and values
+  static constexpr int ROW = I4 ? D / 2 : D;      // bytes of a key's or value's codes
+  static constexpr int PART = 16 * ROW;           // of 16 keys: one TMA box
+  static constexpr int TILE = KEYS * ROW;
+  static constexpr int PART_SCL = I4 ? D : 0;     // bytes of 16 keys' scales
+  static constexpr int TILE_SCL = PARTS * PART_SCL;
+  static constexpr int STAGE = 2 * TILE + 2 * TILE_SCL;  // keys and values, scales behind both
   // ring slots per warp, CTAs per SM: as much as the shared memory and registers take
-  static constexpr int ST = D == 64 && NT == 1 ? 4 : D == 128 && NT == 2 ? 4 : 3;
+  static constexpr int ST = I4 && D == 64 ? 6 : D == 64 && NT == 1 ? 4 : D == 128 && NT == 2 ? 4 : 3;
   static constexpr int OFF_RED = kWarps * ST * STAGE;
   static constexpr int OFF_SCL = OFF_RED + kWarps * R * D * 4;  // [warps][ST] scales of a tile
   static constexpr int OFF_STAT = OFF_SCL + kWarps * ST * 16;
@@ -167,11 +170,27 @@ __device__ __forceinline__ uint2 ld_shared_v2(uint32_t a) {
   asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
   return v;
 }
-template <int D, bool E5M2, int NT>
-__global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
+__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_shared_u16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_shared_u8(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+template <int D, int FMT, int NT>
+__global__ void __launch_bounds__(128, Dec<D, NT, FMT == FMT_INT4>::CTAS)
     cache_fwd_kernel(const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const CacheFwdParams p) {
-  using C = Dec<D, NT>;
+  constexpr bool I4 = FMT == FMT_INT4, E5M2 = FMT == FMT_E5M2;
+  using C = Dec<D, NT, I4>;
   constexpr int R = C::R;
   constexpr int KW = D / 16;   // 4-byte words of a key that a lane holds (16 values per step)
   constexpr int VW = D / 32;   // 4-byte words of a value row that a lane holds
@@ -300,8 +319,10 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
           if (p.c.err) atomicCAS(p.c.err, 0u, (unsigned)ERR_SITE_CACHE_FWD + 1);
         } else {
           r.slice[i] = page * p.c.H + at.h;
-          r.ks[i] = p.c.k_scale[r.slice[i]];  // not waited for here
-          r.vs[i] = p.c.v_scale[r.slice[i]];
+          if constexpr (!I4) {
+            r.ks[i] = p.c.k_scale[r.slice[i]];  // not waited for here
+            r.vs[i] = p.c.v_scale[r.slice[i]];
+          }
         }
       }
     return r;
@@ -335,20 +356,40 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
           const uint32_t slot = issued % C::ST;
           const uint32_t bar = bar0 + 8u * slot, dst = ring + slot * C::STAGE;
           const bool l0 = info.slice[0] >= 0, l1 = C::PARTS == 2 && info.slice[1] >= 0;
-          uint32_t v0 = __float_as_uint(info.vs[0]), v1 = __float_as_uint(info.vs[1]);
-          if (!l1) v1 = v0;  // a part without keys takes the other one's value scale
-          if (!l0) v0 = v1;
-          st_shared_v4(scl0 + slot * 16u, __float_as_uint(info.ks[0]), __float_as_uint(info.ks[1]),
-                       v0, v1);
-          mbar_arrive_expect_tx(bar, (uint32_t)(l0 + l1) * 2u * C::PART);
-          if (l0) {
-            tma_load_3d(dst, &tm_k, bar, 0, info.row, info.slice[0]);
-            tma_load_3d(dst + C::TILE, &tm_v, bar, 0, info.row, info.slice[0]);
-          }
-          if (l1) {
-            const int row = (info.row + 16) & (bs - 1);
-            tma_load_3d(dst + C::PART, &tm_k, bar, 0, row, info.slice[1]);
-            tma_load_3d(dst + C::TILE + C::PART, &tm_v, bar, 0, row, info.slice[1]);
+          if constexpr (I4) {
+            // the codes through the tensor maps, swizzled, the scales as they lie; a block of
+            // 32 tokens or more holds the whole tile, of which one copy takes both parts
+            const bool both = bs >= 32;
+            mbar_arrive_expect_tx(bar, (uint32_t)(both ? 2 : l0 + l1) * 2u *
+                                           (C::PART + C::PART_SCL));
+#pragma unroll
+            for (int i = 0; i < C::PARTS; ++i) {
+              if (info.slice[i] < 0 || (i > 0 && both)) continue;
+              const int row = (info.row + 16 * i) & (bs - 1);
+              const long long scl = (((long long)info.slice[i] << p.c.block_log2) + row) * (D / 16);
+              const uint32_t ds = dst + 2 * C::TILE + i * C::PART_SCL;
+              const uint32_t bytes = both ? 2 * C::PART_SCL : C::PART_SCL;
+              tma_load_3d(dst + i * C::PART, &tm_k, bar, 0, row, info.slice[i]);
+              tma_load_3d(dst + C::TILE + i * C::PART, &tm_v, bar, 0, row, info.slice[i]);
+              bulk_load(ds, p.c.k_scale4 + scl, bytes, bar);
+              bulk_load(ds + C::TILE_SCL, p.c.v_scale4 + scl, bytes, bar);
+            }
+          } else {
+            uint32_t v0 = __float_as_uint(info.vs[0]), v1 = __float_as_uint(info.vs[1]);
+            if (!l1) v1 = v0;  // a part without keys takes the other one's value scale
+            if (!l0) v0 = v1;
+            st_shared_v4(scl0 + slot * 16u, __float_as_uint(info.ks[0]),
+                         __float_as_uint(info.ks[1]), v0, v1);
+            mbar_arrive_expect_tx(bar, (uint32_t)(l0 + l1) * 2u * C::PART);
+            if (l0) {
+              tma_load_3d(dst, &tm_k, bar, 0, info.row, info.slice[0]);
+              tma_load_3d(dst + C::TILE, &tm_v, bar, 0, info.row, info.slice[0]);
+            }
+            if (l1) {
+              const int row = (info.row + 16) & (bs - 1);
+              tma_load_3d(dst + C::PART, &tm_k, bar, 0, row, info.slice[1]);
+              tma_load_3d(dst + C::TILE + C::PART, &tm_v, bar, 0, row, info.slice[1]);
+            }
           }
         }
         ++issued;
@@ -375,8 +416,17 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
   // lane's value columns are piece (g & 1) * 4 + g / 2.  d = 64: rows of 64 bytes,
   // pieces swizzled by (row / 2) & 3; keys in order, and lanes of odd t load the
   // odd one of a pair of value rows first.
-  const int krow = D == 128 ? ((g & 1) << 2 | g >> 1) : g;
-  const int vcol = D == 128 ? ((g & 1) << 2 | g >> 1) * 16 : g * 8;  // first column
+  // 4 bits: a lane's share of a key is a quarter of its channels, of a value row an eighth.
+  // d = 128: rows of 64 bytes, pieces swizzled by (row / 2) & 3; d = 64: of 32, by
+  // (row / 4) & 1.  With matrix row 2 i + e for the key of krow4 below, the rows of a load
+  // phase touch different banks, those of the keys' products (two or four g, all t) and
+  // those of the values' (one e, all t) alike.
+  auto krow4 = [](int i, int e) {
+    return D == 128 ? ((i ^ e) & 1) | e << 1 | (i >> 1) << 2 : (i ^ e << 1) | e << 2;
+  };
+  const int krow = I4 ? krow4(g >> 1, g & 1) : D == 128 ? ((g & 1) << 2 | g >> 1) : g;
+  const int vcol = I4 ? g * (D / 8)
+                      : D == 128 ? ((g & 1) << 2 | g >> 1) * 16 : g * 8;  // first column
 
   // Sums that are put aside (rare): a normalised O in the warp's part of `red`, each lane its
   // own elements, and a log2-sum-exp in `stat`.  Joined with the running sums, row by row:
@@ -450,7 +500,8 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
                               (long long)(h * G + p.by_G.mod(i)) * p.q.sh;
 #pragma unroll
           for (int j = 0; j < D / 32; ++j)
-            qraw[nt][j] = *reinterpret_cast<const uint4*>(q + (j >> 1) * 64 + t * 16 + (j & 1) * 8);
+            qraw[nt][j] = *reinterpret_cast<const uint4*>(
+                I4 ? q + t * (D / 4) + j * 8 : q + (j >> 1) * 64 + t * 16 + (j & 1) * 8);
         }
       }
       if (f == 0) issue(0, false);  // while q is on its way
@@ -478,7 +529,14 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
         const float back = __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
         for (int w = 0; w < KW; ++w) {
-          const uint32_t* x = &v[w >> 1].x + (w & 1) * 2;
+          const uint32_t* x = &v[w >> 1].x + (I4 ? w & 1 : (w & 1) * 2);
+          if constexpr (I4) {  // channels i and i + 4 of eight, as int4_values gives them
+            qf[nt][w][0] = pack_f16x2(__uint_as_float(x[0] << 16) * mul,
+                                      __uint_as_float(x[2] << 16) * mul);
+            qf[nt][w][1] = pack_f16x2(__uint_as_float(x[0] & 0xffff0000u) * mul,
+                                      __uint_as_float(x[2] & 0xffff0000u) * mul);
+            continue;
+          }
           qf[nt][w][0] = pack_f16x2(__uint_as_float(x[0] << 16) * mul,
                                     __uint_as_float(x[0] & 0xffff0000u) * mul);
           qf[nt][w][1] = pack_f16x2(__uint_as_float(x[1] << 16) * mul,
@@ -500,7 +558,7 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
 #pragma unroll
           for (int i = 0; i < 4; ++i) acc[mt][nt][i] = 0.f;
       first_live = true;
-      lvb = 0.f;
+      lvb = I4 ? (float)kInt4UnitLog2 : 0.f;
       parked = false;
     }
 
@@ -514,21 +572,24 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
         ok = __all_sync(0xffffffffu, mbar_wait(bar0 + 8u * slot, (done / C::ST) & 1u, wctx,
                                                ERR_SITE_CACHE_FWD + 2));
         if (ok) {
-          const uint4 sc = ld_shared_v4(scl0 + slot * 16u);
-          const float ks[2] = {__uint_as_float(sc.x), __uint_as_float(sc.y)};
-          float lv[2] = {lg2(__uint_as_float(sc.z)), lg2(__uint_as_float(sc.w))};
-          if (first_live) lvb = lv[0];
-          first_live = false;
-          lv[0] -= lvb, lv[1] -= lvb;
-          const float far = C::PARTS == 2 ? fmaxf(fabsf(lv[0]), fabsf(lv[1])) : fabsf(lv[0]);
-          if (__builtin_expect(far > kWindow || (C::PARTS == 2 && only != 0), 0)) {
-            if (!calm) {  // rare, warp-uniform
-              event = true;
-              break;
+          float ks[2] = {kInt4Unit, kInt4Unit}, lv[2] = {0.f, 0.f};
+          if constexpr (!I4) {
+            const uint4 sc = ld_shared_v4(scl0 + slot * 16u);
+            ks[0] = __uint_as_float(sc.x), ks[1] = __uint_as_float(sc.y);
+            lv[0] = lg2(__uint_as_float(sc.z)), lv[1] = lg2(__uint_as_float(sc.w));
+            if (first_live) lvb = lv[0];
+            first_live = false;
+            lv[0] -= lvb, lv[1] -= lvb;
+            const float far = C::PARTS == 2 ? fmaxf(fabsf(lv[0]), fabsf(lv[1])) : fabsf(lv[0]);
+            if (__builtin_expect(far > kWindow || (C::PARTS == 2 && only != 0), 0)) {
+              if (!calm) {  // rare, warp-uniform
+                event = true;
+                break;
+              }
+              if (only == 1) on[1] = false;
+              if (only == 2) on[0] = false;
+              lv[0] = lv[1] = calm_lv;
             }
-            if (only == 1) on[1] = false;
-            if (only == 2) on[0] = false;
-            lv[0] = lv[1] = calm_lv;
           }
           const uint32_t ka = ring + slot * C::STAGE, va = ka + C::TILE;
           const bool masked = key0 + C::KEYS > lim_lo;  // some row does not see all of it
@@ -541,28 +602,63 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
 #pragma unroll
               for (int i = 0; i < 4; ++i) s[pt][nt][i] = on[pt] ? 0.f : -INFINITY;
             if (!on[pt]) continue;
-#pragma unroll
-            for (int half = 0; half < D / 64; ++half) {
-              uint32_t a[2][4];  // keys krow and krow + 8: 16 bytes
+            if constexpr (I4) {
+              constexpr int W = D / 32;  // words of eight codes: a quarter of a key
+              uint32_t a[2][W];          // keys krow and krow + 8
+              Int4Scale ksc[2][W / 2];   // of their groups of 16
+              const uint32_t at = ka + pt * C::PART, sa = ka + 2 * C::TILE + pt * C::PART_SCL;
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
                 const int row = krow + 8 * i;
-                const int piece = half * 4 + t;
-                const uint32_t at = ka + pt * C::PART;
-                const uint32_t addr = D == 128 ? at + row * 128 + ((piece ^ (row & 7)) << 4)
-                                               : at + row * 64 + ((piece ^ ((row >> 1) & 3)) << 4);
-                const uint4 x = ld_shared_v4(addr);
-                a[i][0] = x.x, a[i][1] = x.y, a[i][2] = x.z, a[i][3] = x.w;
+                if constexpr (D == 128) {
+                  const uint4 x = ld_shared_v4(at + row * 64 + ((t ^ ((row >> 1) & 3)) << 4));
+                  a[i][0] = x.x, a[i][1] = x.y, a[i][W - 2] = x.z, a[i][W - 1] = x.w;
+                  const uint32_t s2 = ld_shared_u16(sa + row * 8 + t * 2);
+                  ksc[i][0] = int4_scale(__byte_perm(s2, 0u, 0x0404u));
+                  ksc[i][W / 2 - 1] = int4_scale(__byte_perm(s2, 0u, 0x1414u));
+                } else {
+                  const uint2 x = ld_shared_v2(at + row * 32 + (((t >> 1) ^ ((row >> 2) & 1)) << 4) +
+                                               (t & 1) * 8);
+                  a[i][0] = x.x, a[i][1] = x.y;
+                  ksc[i][0] = int4_scale(__byte_perm(ld_shared_u8(sa + row * 4 + t), 0u, 0x0404u));
+                }
               }
 #pragma unroll
-              for (int w = 0; w < 4; ++w) {
-                uint32_t a0, a1, a2, a3;
-                codes4_to_f16<E5M2>(a[0][w], a0, a2);
-                codes4_to_f16<E5M2>(a[1][w], a1, a3);
+              for (int w = 0; w < W; ++w) {
+                uint32_t lo[4], hi[4];
+                int4_values(a[0][w], ksc[0][w >> 1], lo);
+                int4_values(a[1][w], ksc[1][w >> 1], hi);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                  mma_f16(s[pt][nt], a0, a1, a2, a3, qf[nt][half * 4 + w][0],
-                          qf[nt][half * 4 + w][1]);
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                  for (int nt = 0; nt < NT; ++nt)
+                    mma_f16(s[pt][nt], lo[2 * m], hi[2 * m], lo[2 * m + 1], hi[2 * m + 1],
+                            qf[nt][2 * w + m][0], qf[nt][2 * w + m][1]);
+              }
+            } else {
+#pragma unroll
+              for (int half = 0; half < D / 64; ++half) {
+                uint32_t a[2][4];  // keys krow and krow + 8: 16 bytes
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  const int row = krow + 8 * i;
+                  const int piece = half * 4 + t;
+                  const uint32_t at = ka + pt * C::PART;
+                  const uint32_t addr = D == 128 ? at + row * 128 + ((piece ^ (row & 7)) << 4)
+                                                 : at + row * 64 + ((piece ^ ((row >> 1) & 3)) << 4);
+                  const uint4 x = ld_shared_v4(addr);
+                  a[i][0] = x.x, a[i][1] = x.y, a[i][2] = x.z, a[i][3] = x.w;
+                }
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                  uint32_t a0, a1, a2, a3;
+                  codes4_to_f16<E5M2>(a[0][w], a0, a2);
+                  codes4_to_f16<E5M2>(a[1][w], a1, a3);
+#pragma unroll
+                  for (int nt = 0; nt < NT; ++nt)
+                    mma_f16(s[pt][nt], a0, a1, a2, a3, qf[nt][half * 4 + w][0],
+                            qf[nt][half * 4 + w][1]);
+                }
               }
             }
             const int k0 = key0 + pt * 16 + krow, k1 = k0 + 8;
@@ -633,6 +729,46 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
             }
             // value rows of this lane: keys of matrix rows 2t, 2t + 1, 2t + 8, 2t + 9
             const int first = key0 + pt * 16;
+            if constexpr (I4) {
+              constexpr int W = D / 64;  // words of eight codes: an eighth of a value row
+              const uint32_t at = va + pt * C::PART;
+              const uint32_t sa = ka + 2 * C::TILE + C::TILE_SCL + pt * C::PART_SCL;
+              uint32_t v[4][W], sc[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int row = krow4(t, i & 1) + 8 * (i >> 1);
+                if constexpr (D == 128) {
+                  const uint2 x = ld_shared_v2(at + row * 64 + (((g >> 1) ^ ((row >> 1) & 3)) << 4) +
+                                               (g & 1) * 8);
+                  v[i][0] = x.x, v[i][W - 1] = x.y;
+                  sc[i] = ld_shared_u8(sa + row * 8 + g);
+                } else {
+                  v[i][0] = ld_shared_u32(at + row * 32 + (((g >> 2) ^ ((row >> 2) & 1)) << 4) +
+                                          (g & 3) * 4);
+                  sc[i] = ld_shared_u8(sa + row * 4 + (g >> 1));
+                }
+                // rows that no query sees hold anything; a scale that is none must not reach
+                // the queries that do not see its row
+                if (masked) sc[i] = first + row >= lim_hi ? 0u : int4_sane(sc[i]);
+              }
+              const Int4Scale s0 = int4_scale(__byte_perm(sc[0], sc[1], 0x4101u));
+              const Int4Scale s1 = int4_scale(__byte_perm(sc[2], sc[3], 0x4101u));
+#pragma unroll
+              for (int j = 0; j < W; ++j)
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                  uint32_t lo[4], hi[4];  // keys 2t, 2t + 1 and 2t + 8, 2t + 9
+                  int4_values(__byte_perm(v[0][j], v[1][j], half ? 0x7632u : 0x5410u), s0, lo);
+                  int4_values(__byte_perm(v[2][j], v[3][j], half ? 0x7632u : 0x5410u), s1, hi);
+#pragma unroll
+                  for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                      mma_f16(acc[j * 4 + half * 2 + m][nt], lo[2 * m], lo[2 * m + 1], hi[2 * m],
+                              hi[2 * m + 1], pf[nt][0], pf[nt][1]);
+                }
+              continue;
+            }
             auto value_row = [&](int i) {
               return D == 128 ? t + 4 * i : 2 * t + ((i & 1) ^ odd) + 8 * (i >> 1);
             };
@@ -966,14 +1102,14 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-template <int D, bool E5M2, int NT>
+template <int D, int FMT, int NT>
 cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const CacheFwdParams& p, int n_sm,
                    bool wide, cudaStream_t stream) {
-  using C = Dec<D, NT>;
+  using C = Dec<D, NT, FMT == FMT_INT4>;
   static_assert(C::CTAS * (C::SMEM + 1024) <= 233472, "shared memory of the CTAs sharing an SM");
   static unsigned long long prepared[64];
   const cudaError_t e = prepare_once(prepared, [] {
-    return cudaFuncSetAttribute(cache_fwd_kernel<D, E5M2, NT>,
+    return cudaFuncSetAttribute(cache_fwd_kernel<D, FMT, NT>,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   });
   if (e != cudaSuccess) return e;
@@ -992,7 +1128,7 @@ cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const CacheFwdP
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
   }
-  const cudaError_t r = cudaLaunchKernelEx(&cfg, cache_fwd_kernel<D, E5M2, NT>, tk, tv, p);
+  const cudaError_t r = cudaLaunchKernelEx(&cfg, cache_fwd_kernel<D, FMT, NT>, tk, tv, p);
   if (r != cudaSuccess) return r;
   cfg.gridDim = dim3(grid + (wide ? kWideMerge * n_sm : 0));
   cfg.blockDim = dim3(256);
@@ -1003,12 +1139,12 @@ cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const CacheFwdP
                             cache_fwd_wide_rows());
 }
 
-template <int D, bool E5M2>
+template <int D, int FMT>
 cudaError_t launch_rows(const CUtensorMap& tk, const CUtensorMap& tv, const CacheFwdParams& p,
                         int n_sm, bool wide, cudaStream_t stream) {
   const long long rows = (long long)p.c.max_seqlen * p.G;
-  return rows <= 8 ? launch<D, E5M2, 1>(tk, tv, p, n_sm, wide, stream)
-                   : launch<D, E5M2, 2>(tk, tv, p, n_sm, wide, stream);
+  return rows <= 8 ? launch<D, FMT, 1>(tk, tv, p, n_sm, wide, stream)
+                   : launch<D, FMT, 2>(tk, tv, p, n_sm, wide, stream);
 }
 
 // Bytes of the records, LSE and O of `ctas` CTAs with R rows per unit.
@@ -1017,8 +1153,8 @@ size_t pieces_bytes(size_t ctas, int R, int d) {
          ((ctas * 2 * R + 63) & ~(size_t)63) * 4 + ctas * 2 * R * d * 4;
 }
 size_t narrow_bytes(int d, int n_sm) {  // the larger of the two variants
-  return std::max(pieces_bytes((size_t)n_sm * Dec<128, 1>::CTAS, Dec<128, 1>::R, d),
-                  pieces_bytes((size_t)n_sm * Dec<64, 2>::CTAS, Dec<64, 2>::R, d));
+  return std::max(pieces_bytes((size_t)n_sm * Dec<128, 1, false>::CTAS, Dec<128, 1, false>::R, d),
+                  pieces_bytes((size_t)n_sm * Dec<64, 2, false>::CTAS, Dec<64, 2, false>::R, d));
 }
 // The most query rows per key/value head (tokens x grouped heads) of a sequence that
 // stays with the kernel above.  From 33 rows on it reads the keys three times and
@@ -1062,11 +1198,18 @@ cudaError_t launch_cache_fwd(const CUtensorMap& tk, const CUtensorMap& tv,
     const cudaError_t e = launch_cache_fwd_wide(p, stream);
     if (e != cudaSuccess) return e;
   }
-  if (p.c.d == 128)
-    return p.c.format ? launch_rows<128, true>(tk, tv, p, n_sm, wide, stream)
-                      : launch_rows<128, false>(tk, tv, p, n_sm, wide, stream);
-  return p.c.format ? launch_rows<64, true>(tk, tv, p, n_sm, wide, stream)
-                    : launch_rows<64, false>(tk, tv, p, n_sm, wide, stream);
+  const bool d128 = p.c.d == 128;
+  switch (p.c.format) {
+    case FMT_E4M3:
+      return d128 ? launch_rows<128, FMT_E4M3>(tk, tv, p, n_sm, wide, stream)
+                  : launch_rows<64, FMT_E4M3>(tk, tv, p, n_sm, wide, stream);
+    case FMT_E5M2:
+      return d128 ? launch_rows<128, FMT_E5M2>(tk, tv, p, n_sm, wide, stream)
+                  : launch_rows<64, FMT_E5M2>(tk, tv, p, n_sm, wide, stream);
+    default:
+      return d128 ? launch_rows<128, FMT_INT4>(tk, tv, p, n_sm, wide, stream)
+                  : launch_rows<64, FMT_INT4>(tk, tv, p, n_sm, wide, stream);
+  }
 }
 
 }  // namespace fattn

@@ -1,4 +1,4 @@
-// cache_fwd_wide.cu -- attention over the paged 8-bit key/value cache, many query
+// cache_fwd_wide.cu -- attention over the paged key/value cache in 8 or 4 bits, many query
 // rows per key/value head (pieces of prompts): tcgen05 + TMEM.
 //
 // A unit is up to 256 rows of one (sequence, key/value head), in two 128-row
@@ -412,10 +412,11 @@ __global__ void __launch_bounds__(Plan::T) cache_fwd_plan_kernel(const CacheFwdP
   if (t == 0) *out.pieces = (int)pieces;
 }
 
-template <int D, bool E5M2>
+template <int D, int FMT>
 __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
     cache_fwd_wide_kernel(const CacheFwdParams p) {
   using C = Wide<D>;
+  constexpr bool I4 = FMT == FMT_INT4, E5M2 = FMT == FMT_E5M2;
   constexpr int ST = C::STAGES;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -501,7 +502,11 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
     const int end = min(lim_hi, (t0 + n_tiles) * C::BN);
     const int past = end > 0 ? ((end - 1) >> p.c.block_log2) + 1 : 0;
     int hi = 0, lo = 255;
-    for (int again = 0;; ++again) {  // the second time (rare) for the set
+    if (I4) {  // one scale for all
+      hi = lo = 127 + kInt4UnitLog2;
+      if (me == 0) scan->hi = hi, scan->lo = lo;
+    }
+    for (int again = 0; !I4; ++again) {  // the second time (rare) for the set
       unsigned set0 = 0u, set1 = 0u;
       int most = 0, least = 255;
 #pragma unroll 1
@@ -589,8 +594,8 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
       }
       const int slice = page * p.c.H + h;
       r.piece = (slice << (p.c.block_log2 - 4)) + ((key & (bs - 1)) >> 4);  // 1 KB or more each
-      r.ks = p.c.k_scale[slice];
-      r.lv = p.c.v_scale[slice];
+      r.ks = I4 ? kInt4Unit : p.c.k_scale[slice];
+      r.lv = I4 ? kInt4Unit : p.c.v_scale[slice];
       return r;
     };
     auto finish = [&](Info r, int j0) {  // the scales as the softmax takes them
@@ -606,26 +611,43 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
       r.w = lv == -INFINITY ? 0.f : ex2(-lv);
       return r;
     };
-    constexpr int LD = D / 32;  // 16-byte loads per lane and piece
+    constexpr int RB = I4 ? D / 2 : D;  // bytes of a row
+    constexpr int LD = RB / 32;  // 16-byte loads per lane and piece
     // a load instruction covers whole rows; eight lanes of a store phase hold the
     // same four 16-byte columns of two neighbouring rows, which the swizzle puts
     // into different banks
-    const int row4 = D == 128 ? (lane >> 4) * 2 + ((lane >> 2) & 1) : lane >> 2;
-    const int col16 = D == 128 ? ((lane >> 3) & 1) * 4 + (lane & 3) : lane & 3;
-    constexpr int ROWS_LD = D == 128 ? 4 : 8;  // rows per load instruction
-    const int lane_src = row4 * D + col16 * 16;
-    // a lane's 16 codes become 32 bytes: two neighbouring 16-byte columns of its row
-    const uint32_t lane_dst = (uint32_t)((col16 >> 2) * C::HALF + (me * 32 + row4) * 128);
+    // (4 bits: the eight lanes hold one column of eight neighbouring rows)
+    constexpr int ROWS_LD = 512 / RB;  // rows per load instruction
+    const int row4 = I4 ? lane & (ROWS_LD - 1)
+                        : D == 128 ? (lane >> 4) * 2 + ((lane >> 2) & 1) : lane >> 2;
+    const int col16 = I4 ? lane / ROWS_LD
+                         : D == 128 ? ((lane >> 3) & 1) * 4 + (lane & 3) : lane & 3;
+    const int lane_src = row4 * RB + col16 * 16;
+    // a lane's 16 codes become 32 bytes: two neighbouring 16-byte columns of its row (4 bits:
+    // its 32 become 64 bytes, four columns)
+    constexpr int COLS = I4 ? 4 : 2;
+    const uint32_t lane_dst =
+        (uint32_t)(col16 / (8 / COLS) * C::HALF + (me * 32 + row4) * 128);
     uint4 buf[2][2][LD];  // [K, V][piece]
+    uint32_t scl[2][2][LD];  // 4 bits: the scales of its two groups of 16
     int at[2];  // the pieces of the next tile
     auto load = [&](int value) {
 #pragma unroll
       for (int pc = 0; pc < 2; ++pc) {
-        const uint8_t* src = (value ? p.c.v : p.c.k) + (long long)at[pc] * (16 * D) + lane_src;
+        const uint8_t* src = (value ? p.c.v : p.c.k) + (long long)at[pc] * (16 * RB) + lane_src;
 #pragma unroll
         for (int i = 0; i < LD; ++i)
           buf[value][pc][i] = at[pc] < 0 ? make_uint4(0u, 0u, 0u, 0u)
-                                         : __ldg(reinterpret_cast<const uint4*>(src + i * ROWS_LD * D));
+                                         : __ldg(reinterpret_cast<const uint4*>(src + i * ROWS_LD * RB));
+        if constexpr (I4) {
+          const uint8_t* from = (value ? p.c.v_scale4 : p.c.k_scale4) + (long long)at[pc] * D +
+                                row4 * (D / 16) + col16 * 2;
+#pragma unroll
+          for (int i = 0; i < LD; ++i)
+            scl[value][pc][i] =
+                at[pc] < 0 ? 0u
+                           : __ldg(reinterpret_cast<const uint16_t*>(from + i * ROWS_LD * (D / 16)));
+        }
       }
     };
     auto look_up = [&](int j, const Info& set) {
@@ -680,13 +702,18 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
             for (int pc = 0; pc < 2; ++pc)
 #pragma unroll
               for (int x = 0; x < LD; ++x) {
-                uint32_t* w = &buf[1][pc][x].x;
+                if constexpr (I4) {
+                  uint32_t& s2 = scl[1][pc][x];
+                  s2 = key0 + pc * 16 + x * ROWS_LD >= lim_hi ? 0u : int4_sane(s2);
+                } else {
+                  uint32_t* w = &buf[1][pc][x].x;
 #pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                  if (key0 + pc * 16 + x * ROWS_LD >= lim_hi) w[y] = 0u;  // stale, whatever it is
-                  const uint32_t m = nan_codes<E5M2>(w[y]);
-                  nan |= m != 0u;
-                  w[y] = clear_codes(w[y], m);
+                  for (int y = 0; y < 4; ++y) {
+                    if (key0 + pc * 16 + x * ROWS_LD >= lim_hi) w[y] = 0u;  // stale, whatever it is
+                    const uint32_t m = nan_codes<E5M2>(w[y]);
+                    nan |= m != 0u;
+                    w[y] = clear_codes(w[y], m);
+                  }
                 }
               }
             if (nan) *poison = 1u;
@@ -700,13 +727,27 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
             const uint32_t* w = &buf[value][pc][x].x;
             const int row = pc * 16 + x * ROWS_LD;  // + 32 me + row4; the swizzle takes it mod 8
             const uint32_t line = dst + row * 128;
+            if constexpr (I4) {
+              // channels in the order that int4_values gives (0 4 1 5 2 6 3 7 of eight):
+              // Q is stored alike, and O's columns come out so
+              Int4Scale s;
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const uint32_t c = (uint32_t)(((col16 & 3) * 2 + y) ^ ((row + row4) & 7));
-              uint32_t o[4];
-              codes4_to_f16<E5M2>(w[2 * y], o[0], o[1]);
-              codes4_to_f16<E5M2>(w[2 * y + 1], o[2], o[3]);
-              st_shared_v4(line + (c << 4), o[0], o[1], o[2], o[3]);
+              for (int y = 0; y < 4; ++y) {
+                if ((y & 1) == 0) s = int4_scale(__byte_perm(scl[value][pc][x], 0u, y ? 0x1414u : 0x0404u));
+                uint32_t o[4];
+                int4_values(w[y], s, o);
+                const uint32_t c = (uint32_t)(((col16 & 1) * 4 + y) ^ ((row + row4) & 7));
+                st_shared_v4(line + (c << 4), o[0], o[1], o[2], o[3]);
+              }
+            } else {
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                const uint32_t c = (uint32_t)(((col16 & 3) * 2 + y) ^ ((row + row4) & 7));
+                uint32_t o[4];
+                codes4_to_f16<E5M2>(w[2 * y], o[0], o[1]);
+                codes4_to_f16<E5M2>(w[2 * y + 1], o[2], o[3]);
+                st_shared_v4(line + (c << 4), o[0], o[1], o[2], o[3]);
+              }
             }
           }
         fence_proxy_async_smem();  // the MMAs read through the async proxy
@@ -901,10 +942,13 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
       const uint32_t* w = &x.x;
       uint32_t o[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 4; ++i) {
+        // 4 bits: channels i and i + 4 side by side, as the keys have them
+        const uint32_t lo = I4 ? __byte_perm(w[i >> 1], w[2 + (i >> 1)], i & 1 ? 0x7632u : 0x5410u) : w[i];
         asm("cvt.rn.f16x2.f32 %0, %1, %2;"
             : "=r"(o[i])
-            : "f"(__uint_as_float(w[i] & 0xffff0000u) * mul), "f"(__uint_as_float(w[i] << 16) * mul));
+            : "f"(__uint_as_float(lo & 0xffff0000u) * mul), "f"(__uint_as_float(lo << 16) * mul));
+      }
       st_shared_v4(own_piece(k), o[0], o[1], o[2], o[3]);
     }
     fence_proxy_async_smem();
@@ -1064,6 +1108,14 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
 #pragma unroll
       for (int i = 0; i < 32; ++i)
         o[i] = has ? __float_as_uint(__uint_as_float(o[i]) * inv * up) : 0u;
+      if constexpr (I4) {  // columns in their order again
+#pragma unroll
+        for (int k = 0; k < 32; k += 8) {
+          const uint32_t x[8] = {o[k], o[k + 2], o[k + 4], o[k + 6], o[k + 1], o[k + 3], o[k + 5], o[k + 7]};
+#pragma unroll
+          for (int i = 0; i < 8; ++i) o[k + i] = x[i];
+        }
+      }
       if (part < 0) {  // into Q_s's place, which no MMA reads any more
 #pragma unroll
         for (int q4 = 0; q4 < 4; ++q4) {
@@ -1106,7 +1158,7 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
     tc_fence_after();
     tmem_dealloc(tmem, C::TMEM_COLS);
   }
-  if (*poison && warp < 8) {
+  if (!I4 && *poison && warp < 8) {
     // rare: values that were NaN in keys that some rows see and others do not; they
     // were left out of the sums, and here reach the rows that do see them
     const int row = (int)threadIdx.x;
@@ -1133,17 +1185,17 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
   }
 }
 
-template <int D, bool E5M2>
+template <int D, int FMT>
 cudaError_t launch(const CacheFwdParams& p, cudaStream_t stream) {
   using C = Wide<D>;
   static unsigned long long prepared[64];
   const cudaError_t e = prepare_once(prepared, [] {
-    cudaError_t r = cudaFuncSetAttribute(cache_fwd_wide_kernel<D, E5M2>,
+    cudaError_t r = cudaFuncSetAttribute(cache_fwd_wide_kernel<D, FMT>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (r != cudaSuccess) return r;
     // the setmaxnreg split hands out at most the launch's registers
     cudaFuncAttributes fa;
-    r = cudaFuncGetAttributes(&fa, cache_fwd_wide_kernel<D, E5M2>);
+    r = cudaFuncGetAttributes(&fa, cache_fwd_wide_kernel<D, FMT>);
     if (r != cudaSuccess) return r;
     return fa.numRegs >= C::REG_LAUNCH ? cudaSuccess : cudaErrorInvalidConfiguration;
   });
@@ -1161,7 +1213,7 @@ cudaError_t launch(const CacheFwdParams& p, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cache_fwd_wide_kernel<D, E5M2>, p);
+  return cudaLaunchKernelEx(&cfg, cache_fwd_wide_kernel<D, FMT>, p);
 }
 
 }  // namespace
@@ -1180,8 +1232,15 @@ long long cache_fwd_wide_grid(const CacheParams& c, int G, int narrow_rows, int 
 size_t cache_fwd_wide_plan_bytes(long long grid) { return 256 + (size_t)grid * sizeof(Segment); }
 
 cudaError_t launch_cache_fwd_wide(const CacheFwdParams& p, cudaStream_t stream) {
-  if (p.c.d == 128) return p.c.format ? launch<128, true>(p, stream) : launch<128, false>(p, stream);
-  return p.c.format ? launch<64, true>(p, stream) : launch<64, false>(p, stream);
+  const bool d128 = p.c.d == 128;
+  switch (p.c.format) {
+    case FMT_E4M3:
+      return d128 ? launch<128, FMT_E4M3>(p, stream) : launch<64, FMT_E4M3>(p, stream);
+    case FMT_E5M2:
+      return d128 ? launch<128, FMT_E5M2>(p, stream) : launch<64, FMT_E5M2>(p, stream);
+    default:
+      return d128 ? launch<128, FMT_INT4>(p, stream) : launch<64, FMT_INT4>(p, stream);
+  }
 }
 
 }  // namespace fattn

@@ -376,15 +376,16 @@ def softmax_rows(x, with_lse=False, out=None, stream=None):
     return (y, lse) if with_lse else y
 
 
-# ------------------------------------------------------------------ 8-bit key/value cache
+# ------------------------------------------------------------------ 8-bit and 4-bit key/value cache
 
-CACHE_FORMATS = {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1}
+CACHE_FORMATS = {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1, torch.uint8: 4}
 
 
 class KVCache(typing.NamedTuple):
-    """The pool of blocks of fattn_cache: k, v float8_e4m3fn or float8_e5m2
-    [num_blocks, H, block_size, d], k_scale, v_scale fp32 [num_blocks, H], all
-    contiguous on one device."""
+    """The pool of blocks of fattn_cache, all contiguous on one device.  8 bits: k, v
+    float8_e4m3fn or float8_e5m2 [num_blocks, H, block_size, d], k_scale, v_scale fp32
+    [num_blocks, H].  4 bits: k, v uint8 [num_blocks, H, block_size, d / 2], two codes a
+    byte, k_scale, v_scale float8_e5m2 [num_blocks, H, block_size, d / 16]."""
     k: torch.Tensor
     v: torch.Tensor
     k_scale: torch.Tensor
@@ -405,11 +406,19 @@ class CacheBatch(typing.NamedTuple):
 
 
 def new_cache(num_blocks, heads, block_size, d, dtype=torch.float8_e4m3fn, device="cuda"):
-    """An empty KVCache: codes zero, scales 2^-100, what fattn_cache_append writes for
-    a block of zeros."""
+    """An empty KVCache, as fattn_cache_append leaves it for zeros.  dtype: float8_e4m3fn
+    or float8_e5m2 (codes zero, scales 2^-100), or uint8 for 4 bits (codes 8, scales 0)."""
     if dtype not in CACHE_FORMATS:
-        raise ValueError("a cache holds float8_e4m3fn or float8_e5m2, not %s" % dtype)
+        raise ValueError("a cache holds float8_e4m3fn, float8_e5m2 or uint8 (4 bits), not %s" % dtype)
     shape = (num_blocks, heads, block_size, d)
+    if dtype is torch.uint8:
+        if d % 16:
+            raise ValueError("a 4-bit cache has a scale for every 16 channels, not d = %d" % d)
+        k, v = (torch.full(shape[:3] + (d // 2,), 0x88, dtype=dtype, device=device)
+                for _ in range(2))
+        ks, vs = (torch.zeros(shape[:3] + (d // 16,), dtype=dtype, device=device)
+                  .view(torch.float8_e5m2) for _ in range(2))
+        return KVCache(k, v, ks, vs)
     k, v = (torch.zeros(shape, dtype=torch.uint8, device=device).view(dtype) for _ in range(2))
     ks, vs = (torch.full(shape[:2], 2.0 ** -100, dtype=torch.float32, device=device)
               for _ in range(2))
@@ -420,10 +429,18 @@ def _refuse_cache(cache, batch):
     """Say what _cache_args found wrong."""
     k, v, ks, vs = cache
     table, lens, cu = batch[:3]
-    if k.dim() != 4 or v.shape != k.shape or ks.shape != k.shape[:2] or vs.shape != k.shape[:2]:
+    if k.dtype is torch.uint8 and k.dim() == 4:
+        scales = k.shape[:3] + (k.shape[3] // 8,)
+        if v.dtype is not k.dtype or ks.dtype is not torch.float8_e5m2 or vs.dtype is not ks.dtype:
+            raise ValueError("expected uint8 codes (two a byte) and float8_e5m2 scales")
+        if k.shape[3] % 8 or v.shape != k.shape or ks.shape != scales or vs.shape != scales:
+            raise ValueError("expected k, v [num_blocks, H, block_size, d / 2] and scales "
+                             "[num_blocks, H, block_size, d / 16]")
+    elif k.dim() != 4 or v.shape != k.shape or ks.shape != k.shape[:2] or vs.shape != k.shape[:2]:
         raise ValueError("expected k, v [num_blocks, H, block_size, d] and scales [num_blocks, H]")
-    if k.dtype not in CACHE_FORMATS or v.dtype != k.dtype or ks.dtype != torch.float32 or \
-            vs.dtype != torch.float32:
+    if k.dtype is not torch.uint8 and (
+            k.dtype not in CACHE_FORMATS or v.dtype != k.dtype or ks.dtype != torch.float32
+            or vs.dtype != torch.float32):
         raise ValueError("expected float8 codes of one type and fp32 scales")
     if table.dim() != 2 or lens.shape != (table.shape[0],) or cu.shape != (table.shape[0] + 1,):
         raise ValueError("expected block_table [B, width], lens [B], cu_seqlens [B + 1]")
@@ -443,11 +460,14 @@ def _cache_args(cache, batch):
     if len(shape) != 4 or fmt is None or dev < 0 or table.dim() != 2:
         _refuse_cache(cache, batch)
     B, width = table.shape
-    scales = shape[:2]
-    f32, i32 = torch.float32, torch.int32
+    i32 = torch.int32
+    if fmt == 4:
+        scales, kind = shape[:3] + (shape[3] // 8,), torch.float8_e5m2
+    else:
+        scales, kind = shape[:2], torch.float32
     if not (v.shape == shape and ks.shape == scales and vs.shape == scales and lens.dim() == 1
             and lens.numel() == B and cu.dim() == 1 and cu.numel() == B + 1
-            and v.dtype is dtype and ks.dtype is f32 and vs.dtype is f32 and table.dtype is i32
+            and v.dtype is dtype and ks.dtype is kind and vs.dtype is kind and table.dtype is i32
             and lens.dtype is i32 and cu.dtype is i32
             and k.is_contiguous() and v.is_contiguous() and ks.is_contiguous()
             and vs.is_contiguous() and table.is_contiguous() and lens.is_contiguous()
@@ -456,6 +476,8 @@ def _cache_args(cache, batch):
             and table.get_device() == dev and lens.get_device() == dev and cu.get_device() == dev):
         _refuse_cache(cache, batch)
     nb, H, bs, d = shape
+    if fmt == 4:
+        d *= 2
     return (_pack_cache(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), nb, H, bs, d, fmt),
             _pack_batch(table.data_ptr(), lens.data_ptr(), cu.data_ptr(), B, width, total,
                         max_seqlen), dev, H, d)
@@ -547,7 +569,7 @@ def cache_forward(q, cache, batch, scale, causal, out=None, workspace=None, stre
     o = torch.empty((total, Hq, d), dtype=torch.bfloat16, device=on) if out is None else out
     lse = torch.empty((Hq, total), dtype=torch.float32, device=on)
     if workspace is None:
-        key = (dev, cache[0].shape, batch[0].shape, total, batch[4], Hq)
+        key = (dev, cache[0].shape, cache[0].dtype, batch[0].shape, total, batch[4], Hq)
         nbytes = _ws_bytes.get(key)
         if nbytes is None:
             nbytes = int(lib.fattn_cache_fwd_workspace_bytes(c, b, Hq))

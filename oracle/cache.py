@@ -103,10 +103,10 @@ def read(cache, fmt, batch):
                                  for b in range(len(lens))]) for side in ("k", "v"))
 
 
-def forward(cache, fmt, batch, q, scale, causal, d_error=False):
+def forward(cache, fmt, batch, q, scale, causal, d_error=False, tokens=tokens):
     """O [T, Hq, d], LSE [Hq, T] of q [T, Hq, d]; with d_error also A [T, Hq, d] =
     sum_j P_j |v_j|, S [Hq, T] = the largest scale * sum_c |q_c k_c| of a visible
-    key, and the number of visible keys [T]."""
+    key, and the number of visible keys [T].  tokens: how the cache's values are read."""
     table, lens, cu = batch
     T, Hq, d = q.shape
     H = cache["k"].shape[1]
