@@ -406,6 +406,105 @@ int fattn_cache_fwd(const fattn_cache* cache, const fattn_cache_batch* batch, co
 size_t fattn_cache_fwd_workspace_bytes(const fattn_cache* cache, const fattn_cache_batch* batch,
                                        int Hq);
 
+/* The attention weight that every cached key receives, for choosing what to keep:
+ *     W[b, h, j] = (W_in[b, h, j], or 0) + sum exp(scale q . k_j - lse)
+ * over the batch's queries of sequence b that see key j (as in fattn_cache_fwd) and the heads
+ * of group h; the batch's own tokens (positions from lens[b] - n_b on) start at 0.  Weights are
+ * kept by sequence, not by block, as a shared block's keys have others in every sequence.
+ * q as for fattn_cache_fwd, lse DEVICE fp32 [Hq, total] as it wrote it (a row with -inf adds
+ * nothing).  weights (NULL: zeros) and weights_out: DEVICE fp32, 4-byte aligned, element
+ * (b, h, j) at b * sequence stride + h * head stride + j, strides in elements and not negative,
+ * rows of `width` elements, those of weights_out not overlapping; they may be the same, with the
+ * same strides.  Elements at and behind lens[b], and sequences with n_b = 0, are not touched.
+ * A sequence whose entries are bad (as above) or whose length exceeds width is skipped (code
+ * 0x470), keys of a bad block number get 0 from the queries (0x471).  Every sum is formed in
+ * one order: repeated calls agree bit for bit.  Scores, exponentials and sums are fp32.
+ * A NaN key makes its weight NaN and, by way of lse, those of the keys whose queries see it. */
+int fattn_cache_weights(const fattn_cache* cache, const fattn_cache_batch* batch, const void* q,
+                        long long q_token_stride, long long q_head_stride, const float* lse,
+                        int Hq, float scale, int causal, const float* weights,
+                        long long weights_seq_stride, long long weights_head_stride,
+                        float* weights_out, long long out_seq_stride, long long out_head_stride,
+                        int width, void* stream);
+
+/* Eviction by weight: for every sequence b longer than `keep` tokens and every key/value head,
+ * the last `recent` tokens and, of the others, the keep - recent with the largest weights are
+ * copied in their order to positions 0 ... keep - 1 of the blocks of table_out; a sequence of at
+ * most keep tokens is copied whole.  Heads keep different tokens.  NaN counts as the largest
+ * weight, of equal ones the earlier token is kept; -0 equals 0.
+ * batch: block_table, lens, B and table_width are used; cu_seqlens, total and max_seqlen are not
+ * looked at.  weights as above (one row of `width` per sequence and head).  table_out: DEVICE int32
+ * [B, table_out_width] with room for min(keep, width) tokens.  Its blocks belong to the same
+ * pool and must not be among those that the call reads, nor twice among those that it writes,
+ * but for a sequence of at most keep tokens, which may be given its own.  The blocks read stay
+ * as they are, so prefixes that other sequences share stay whole.
+ * Written: lens_out [B] (int32, not lens itself) = min(lens, keep); kept [B, H, keep] (int32) the
+ * positions kept, ascending, -1 behind the last; weights_out (as above, not weights itself,
+ * rows of out_width >= min(keep, width)) their weights, elements behind the last untouched.
+ * 8 bits: the scale of a destination block is the largest of its tokens' scales, and codes that
+ * had a smaller one are rounded for it to nearest even (exact but for codes that become
+ * subnormal, where the scales are powers of two).  4 bits: codes and scales as they are.
+ * A length that is negative or beyond its table row or width counts as 0 (code 0x480); a token
+ * whose block number is bad becomes zeros, a bad number in table_out drops its tokens (0x481).
+ * 1 <= keep, 0 <= recent <= keep. */
+int fattn_cache_evict(const fattn_cache* cache, const fattn_cache_batch* batch,
+                      const float* weights, long long weights_seq_stride,
+                      long long weights_head_stride, int width, const int* table_out,
+                      int table_out_width, int keep, int recent, int* lens_out, int* kept,
+                      float* weights_out, long long out_seq_stride, long long out_head_stride,
+                      int out_width, void* stream);
+
+/* ------------------------------------------------------------------ rotary positions
+ *
+ * Pairs of channels of queries and keys are turned by angles that grow with a token's
+ * position, before the attention (and before keys go into a cache).  The pages have no
+ * counterpart.  Channel pair i of a token at position p turns by the angle p w_i:
+ *     a' = m (a cos(p w_i) - b sin(p w_i)),   b' = m (a sin(p w_i) + b cos(p w_i)). */
+typedef enum {
+  FATTN_ROPE_HALF = 0,       /* pair i: channels i and rot / 2 + i */
+  FATTN_ROPE_INTERLEAVED = 1 /* pair i: channels 2 i and 2 i + 1 */
+} fattn_rope_layout;
+
+/* How the frequencies w_i = base^(-2 i / rot) are changed for contexts `factor` times as
+ * long as the `length` that a model was trained with. */
+typedef enum {
+  FATTN_ROPE_NONE = 0,
+  FATTN_ROPE_LINEAR = 1, /* w_i / factor */
+  FATTN_ROPE_BASE = 2,   /* base times factor^(rot / (rot - 2)), so the slowest pair is divided by
+                            factor and the fastest is kept */
+  FATTN_ROPE_YARN = 3,   /* w_i where the pair makes more than about `fast` turns over `length`,
+                            w_i / factor where fewer than `slow`, a ramp over the pairs between
+                            (floor and ceiling of the two pairs); m = 0.1 ln(factor) + 1 */
+  FATTN_ROPE_BANDS = 4   /* the same by turns n_i = length w_i / 2 pi: the share of w_i is
+                            (n_i - slow) / (fast - slow), cut to [0, 1]; m = 1 */
+} fattn_rope_scaling;
+
+/* The frequencies as fractions of a turn, on the HOST (no device is touched): turns[i] =
+ * 2^64 frac(w_i / 2 pi) for i < rot / 2, and *magnitude = m.  rot even, base > 1; factor is
+ * read unless kind is NONE, length, fast and slow (fast > slow > 0) by YARN and BANDS.
+ * Formed in double precision: an angle at position p is off by about 2^-52 p turns at most. */
+int fattn_rope_turns(unsigned long long* turns, float* magnitude, int rot, double base, int kind,
+                     double factor, int length, double fast, double slow);
+
+/* Turns the first rot channels of every row of q [total, Hq, d] and k [total, Hk, d] (bf16,
+ * DEVICE, 16-byte aligned, strides in elements as for fattn_cache_append, those of the outputs
+ * as for fattn_cache_read) and writes rows of d channels to q_out and k_out; the channels from
+ * rot on are copied.  An output may be its input, with the same strides; otherwise they must not
+ * overlap.  Hq and Hk are at most 65535; one may be 0 (its pointers are not looked at).  positions: DEVICE int32
+ * [total], of either sign; turns: DEVICE [rot / 2] of 64 bits, 8-byte aligned, as
+ * fattn_rope_turns gives them; magnitude m finite and > 0.  d is 64 or 128, rot a multiple of
+ * 16 up to d.  The angle is exact in turns (64-bit arithmetic modulo one turn) up to the
+ * fractions given; sines, products and sums are fp32, rounded once to bf16.
+ * backward != 0: the gradient, i.e. the transposed map (q and k are dL/dq_out and dL/dk_out).
+ * Returns FATTN_OK, FATTN_ERR_INVALID_ARG, FATTN_ERR_UNSUPPORTED or FATTN_ERR_CUDA; launches
+ * nothing on an argument error or when total = 0. */
+int fattn_rope(const void* q, long long q_token_stride, long long q_head_stride, void* q_out,
+               long long q_out_token_stride, long long q_out_head_stride, int Hq, const void* k,
+               long long k_token_stride, long long k_head_stride, void* k_out,
+               long long k_out_token_stride, long long k_out_head_stride, int Hk,
+               const int* positions, const unsigned long long* turns, float magnitude, int total,
+               int d, int rot, int layout, int backward, void* stream);
+
 /* Tile shape used by a pass (0 = forward, 1 = backward) for head size d:
  * rows of Q per tile and keys per K/V tile; 128 x 128, the tile of "Decoding
  * flash attention" ("The idea: never build the matrix").  block_q and block_k may be NULL.

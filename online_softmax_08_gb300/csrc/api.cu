@@ -12,7 +12,9 @@
 #include "../../include/fattn.h"
 #include "cache.cuh"
 #include "common.cuh"
+#include "evict.cuh"
 #include "ptx.cuh"
+#include "rope.cuh"
 
 namespace fattn {
 namespace {
@@ -684,6 +686,216 @@ extern "C" int fattn_cache_fwd(const fattn_cache* cache, const fattn_cache_batch
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return debug_post_call(
       launch_cache_fwd(tk, tv, p, dev->n_sm, s) == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA, s);
+}
+
+namespace fattn {
+namespace {
+
+// Rows of `width` weights by sequence and head; written: no two overlap.
+int check_weights(const void* p, long long sb, long long sh, int B, int H, int width,
+                  bool written) {
+  if (!aligned4(p)) return FATTN_ERR_INVALID_ARG;
+  if (B <= 1) sb = 0;
+  if (H <= 1) sh = 0;
+  if (sb < 0 || sh < 0 || sb >= (1LL << 38) || sh >= (1LL << 40)) return FATTN_ERR_INVALID_ARG;
+  if (!written) return FATTN_OK;
+  // (compared by quotients, which cannot overflow)
+  auto spans = [&](long long inner, int n, long long outer, int m) {  // m sets of n rows
+    return (n <= 1 || inner >= width) &&
+           (m <= 1 || (outer >= width && (outer - width) / std::max(inner, 1LL) >= n - 1));
+  };
+  const bool by_seq = spans(sh, H, sb, B), by_head = spans(sb, B, sh, H);
+  return by_seq || by_head ? FATTN_OK : FATTN_ERR_INVALID_ARG;
+}
+
+}  // namespace
+}  // namespace fattn
+
+extern "C" int fattn_cache_weights(const fattn_cache* cache, const fattn_cache_batch* batch,
+                                   const void* q, long long q_token_stride,
+                                   long long q_head_stride, const float* lse, int Hq, float scale,
+                                   int causal, const float* weights, long long weights_seq_stride,
+                                   long long weights_head_stride, float* weights_out,
+                                   long long out_seq_stride, long long out_head_stride, int width,
+                                   void* stream) {
+  int st = check_cache_sizes(cache, batch);
+  if (st != FATTN_OK) return st;
+  st = check_cache_heads(cache, batch, Hq);
+  if (st != FATTN_OK) return st;
+  if (!(scale > 0.f) || !isfinite(scale) || width < 0) return FATTN_ERR_INVALID_ARG;
+  st = check_cache_pointers(cache, batch);
+  if (st != FATTN_OK) return st;
+  const int T = batch->total, B = batch->B, H = cache->H;
+  if (T == 0 || batch->max_seqlen == 0) return FATTN_OK;  // no queries: nothing to add
+  if (!aligned16(q) || !aligned4(lse)) return FATTN_ERR_INVALID_ARG;
+  st = check_strides(q_token_stride, q_head_stride, T, Hq, 0);
+  if (st == FATTN_OK)
+    st = check_weights(weights_out, out_seq_stride, out_head_stride, B, H, width, true);
+  if (st == FATTN_OK && weights)
+    st = check_weights(weights, weights_seq_stride, weights_head_stride, B, H, width, false);
+  if (st != FATTN_OK) return st;
+  if (weights == weights_out && ((B > 1 && weights_seq_stride != out_seq_stride) ||
+                                 (H > 1 && weights_head_stride != out_head_stride)))
+    return FATTN_ERR_INVALID_ARG;  // in place is element by element
+  DeviceInfo* dev = nullptr;
+  st = current_device(&dev);
+  if (st != FATTN_OK) return st;
+  WeightParams p{};
+  p.c = cache_params(cache, batch, dev->err);
+  p.q = token_view(q, q_token_stride, q_head_stride, T, Hq);
+  p.lse = lse;
+  p.in = WeightView{const_cast<float*>(weights), weights_seq_stride, weights_head_stride};
+  p.out = WeightView{weights_out, out_seq_stride, out_head_stride};
+  p.accumulate = weights ? 1 : 0;
+  p.width = width;
+  p.G = Hq / H;
+  p.by_G = FastDiv((unsigned)p.G);
+  p.causal = causal ? 1 : 0;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return debug_post_call(
+      launch_cache_weights(p, dev->n_sm, s) == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA, s);
+}
+
+extern "C" int fattn_cache_evict(const fattn_cache* cache, const fattn_cache_batch* batch,
+                                 const float* weights, long long weights_seq_stride,
+                                 long long weights_head_stride, int width, const int* table_out,
+                                 int table_out_width, int keep, int recent, int* lens_out,
+                                 int* kept, float* weights_out, long long out_seq_stride,
+                                 long long out_head_stride, int out_width, void* stream) {
+  if (!cache || !batch) return FATTN_ERR_INVALID_ARG;
+  fattn_cache_batch b = *batch;  // no packed tokens here
+  b.total = b.max_seqlen = 0;
+  b.cu_seqlens = b.lens;
+  int st = check_cache_sizes(cache, &b);
+  if (st != FATTN_OK) return st;
+  st = check_cache_pointers(cache, &b);
+  if (st != FATTN_OK) return st;
+  if (width < 1 || keep < 1 || recent < 0 || recent > keep || table_out_width < 1)
+    return FATTN_ERR_INVALID_ARG;
+  const long long most = std::min(keep, width);
+  const long long blocks = (most + cache->block_size - 1) / cache->block_size;
+  if (out_width < most || table_out_width < blocks ||
+      (long long)b.B * cache->H * blocks > 0x7fffffffLL)
+    return FATTN_ERR_INVALID_ARG;
+  if (!aligned4(table_out) || !aligned4(lens_out) || !aligned4(kept) || lens_out == b.lens ||
+      weights_out == weights)
+    return FATTN_ERR_INVALID_ARG;
+  st = check_weights(weights, weights_seq_stride, weights_head_stride, b.B, cache->H, width, false);
+  if (st == FATTN_OK)
+    st = check_weights(weights_out, out_seq_stride, out_head_stride, b.B, cache->H, (int)most, true);
+  if (st != FATTN_OK) return st;
+  DeviceInfo* dev = nullptr;
+  st = current_device(&dev);
+  if (st != FATTN_OK) return st;
+  EvictParams p{};
+  p.c = cache_params(cache, &b, dev->err);
+  p.in = WeightView{const_cast<float*>(weights), weights_seq_stride, weights_head_stride};
+  p.out = WeightView{weights_out, out_seq_stride, out_head_stride};
+  p.width = width;
+  p.out_width = out_width;
+  p.table_out = table_out;
+  p.table_out_width = table_out_width;
+  p.keep = keep;
+  p.recent = recent;
+  p.lens_out = lens_out;
+  p.kept = kept;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return debug_post_call(launch_cache_evict(p, s) == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA, s);
+}
+
+extern "C" int fattn_rope_turns(unsigned long long* turns, float* magnitude, int rot, double base,
+                                int kind, double factor, int length, double fast, double slow) {
+  constexpr double kTwoPi = 6.283185307179586477;
+  if (!turns || !magnitude || rot < 2 || (rot & 1) || rot > 65536) return FATTN_ERR_INVALID_ARG;
+  if (!(base > 1.0) || !isfinite(base)) return FATTN_ERR_INVALID_ARG;
+  if (kind < FATTN_ROPE_NONE || kind > FATTN_ROPE_BANDS) return FATTN_ERR_UNSUPPORTED;
+  if (kind != FATTN_ROPE_NONE && (!(factor > 0.0) || !isfinite(factor))) return FATTN_ERR_INVALID_ARG;
+  const bool by_length = kind == FATTN_ROPE_YARN || kind == FATTN_ROPE_BANDS;
+  if (by_length && (length < 1 || !(slow > 0.0) || !(fast > slow) || !isfinite(fast)))
+    return FATTN_ERR_INVALID_ARG;
+  if (kind == FATTN_ROPE_YARN && factor < 1.0) return FATTN_ERR_INVALID_ARG;
+  if (kind == FATTN_ROPE_BASE && rot > 2) base *= pow(factor, rot / (rot - 2.0));
+  if (!(base > 1.0) || !isfinite(base)) return FATTN_ERR_INVALID_ARG;
+  *magnitude = kind == FATTN_ROPE_YARN ? (float)(0.1 * log(factor) + 1.0) : 1.f;
+  double lo = 0.0, hi = 0.0;  // pairs between which the scaling sets in
+  if (kind == FATTN_ROPE_YARN) {
+    auto pair_of = [&](double n) {  // the pair that makes n turns over the original length
+      return rot * log(length / (n * kTwoPi)) / (2.0 * log(base));
+    };
+    lo = std::max(floor(pair_of(fast)), 0.0);
+    hi = std::min(ceil(pair_of(slow)), rot - 1.0);
+  }
+  for (int i = 0; i < rot / 2; ++i) {
+    double w = pow(base, -2.0 * i / rot);
+    double keep = 1.0;  // share of the unscaled frequency
+    if (kind == FATTN_ROPE_LINEAR) keep = 0.0;
+    if (kind == FATTN_ROPE_YARN)
+      keep = 1.0 - std::min(std::max((i - lo) / std::max(hi - lo, 0.001), 0.0), 1.0);
+    if (kind == FATTN_ROPE_BANDS)
+      keep = std::min(std::max((length * w / kTwoPi - slow) / (fast - slow), 0.0), 1.0);
+    if (keep < 1.0) w = w * keep + w / factor * (1.0 - keep);
+    double t = w / kTwoPi;
+    t -= floor(t);
+    turns[i] = (unsigned long long)ldexp(t, 64);  // t < 1
+  }
+  return FATTN_OK;
+}
+
+extern "C" int fattn_rope(const void* q, long long q_token_stride, long long q_head_stride,
+                          void* q_out, long long q_out_token_stride, long long q_out_head_stride,
+                          int Hq, const void* k, long long k_token_stride, long long k_head_stride,
+                          void* k_out, long long k_out_token_stride, long long k_out_head_stride,
+                          int Hk, const int* positions, const unsigned long long* turns,
+                          float magnitude, int total, int d, int rot, int layout, int backward,
+                          void* stream) {
+  if (total < 0 || Hq < 0 || Hk < 0 || Hq > 65535 || Hk > 65535 || Hq + Hk < 1 ||
+      (long long)(Hq + Hk) * total >= (1LL << 31))
+    return FATTN_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return FATTN_ERR_UNSUPPORTED;
+  if (layout != FATTN_ROPE_HALF && layout != FATTN_ROPE_INTERLEAVED) return FATTN_ERR_UNSUPPORTED;
+  if (rot < 16 || rot > d) return FATTN_ERR_INVALID_ARG;
+  if (rot & 15) return FATTN_ERR_UNSUPPORTED;
+  if (!(magnitude > 0.f) || !isfinite(magnitude)) return FATTN_ERR_INVALID_ARG;
+  if (!turns || (reinterpret_cast<uintptr_t>(turns) & 7u)) return FATTN_ERR_INVALID_ARG;
+  if (total == 0) return FATTN_OK;
+  if (!aligned4(positions)) return FATTN_ERR_INVALID_ARG;
+  auto check = [&](const void* in, long long st, long long sh, const void* out, long long ost,
+                   long long osh, int heads) -> int {
+    if (heads == 0) return FATTN_OK;
+    if (!aligned16(in) || !aligned16(out)) return FATTN_ERR_INVALID_ARG;
+    const int r = check_strides(st, sh, total, heads, 0);
+    if (r != FATTN_OK) return r;
+    if (in == out && ((total > 1 && st != ost) || (heads > 1 && sh != osh)))
+      return FATTN_ERR_INVALID_ARG;  // in place is row by row
+    return check_strides(ost, osh, total, heads, d);
+  };
+  int st = check(q, q_token_stride, q_head_stride, q_out, q_out_token_stride, q_out_head_stride, Hq);
+  if (st == FATTN_OK)
+    st = check(k, k_token_stride, k_head_stride, k_out, k_out_token_stride, k_out_head_stride, Hk);
+  if (st != FATTN_OK) return st;
+  DeviceInfo* dev = nullptr;
+  st = current_device(&dev);
+  if (st != FATTN_OK) return st;
+  RopeParams p{};
+  p.q = token_view(q, q_token_stride, q_head_stride, total, Hq);
+  p.k = token_view(k, k_token_stride, k_head_stride, total, Hk);
+  p.q_out = token_view(q_out, q_out_token_stride, q_out_head_stride, total, Hq);
+  p.k_out = token_view(k_out, k_out_token_stride, k_out_head_stride, total, Hk);
+  p.T = total;
+  p.Hq = Hq;
+  p.Hk = Hk;
+  p.rot = rot;
+  p.positions = positions;
+  p.turns = turns;
+  p.magnitude = magnitude;
+  p.back = backward ? 1 : 0;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return debug_post_call(launch_rope(p, d, layout == FATTN_ROPE_INTERLEAVED, dev->n_sm, s) ==
+                                 cudaSuccess
+                             ? FATTN_OK
+                             : FATTN_ERR_CUDA,
+                         s);
 }
 
 extern "C" size_t fattn_bwd_workspace_bytes(int B, int H, int N, int d) {

@@ -1,0 +1,291 @@
+// cache_evict.cu -- the copy of a cache's most attended tokens into other blocks.
+//
+// Of a sequence of L > keep tokens every key/value head keeps its last `recent` tokens and,
+// among the others, the keep - recent of the largest weight (NaN counts as the largest, of
+// equal ones the first); their order stays.  Shorter sequences are copied whole.
+//
+// 1. Selection, one CTA per (sequence, head).  Weights are taken as unsigned numbers of the
+// same order.  The smallest kept one is found digit by digit, 11 + 11 + 10 bits from the top:
+// a histogram in shared memory of the next digit among the weights that agree so far, and the
+// bin in which the count from above reaches what is to be kept.  A last pass in the tokens'
+// order numbers the kept ones by prefix sums.  Every pass reads the weights, which L2 holds.
+// 2. Copy.  The destination blocks are nobody's source, so every one is filled on its own: a
+// CTA per (sequence, head, block).  In 4 bits a token's codes and scales move as they are; in
+// 8 bits the block's scale is the largest of its tokens', and codes of a smaller one are
+// rounded for it, as when append raises a block's scale.
+#include <algorithm>
+#include <type_traits>
+
+#include "evict.cuh"
+
+namespace fattn {
+namespace {
+
+constexpr int kSelect = 1024;  // threads of a selection
+constexpr int kBins = 2048;
+constexpr int kCopy = 128;     // threads of a copy
+
+__device__ __forceinline__ uint32_t order_of(float w) {
+  const uint32_t u = __float_as_uint(w + 0.f);  // -0 as 0
+  if ((u & 0x7fffffffu) > 0x7f800000u) return 0xffffffffu;
+  return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
+}
+
+// Length of sequence b, or -1 (reported).
+__device__ __forceinline__ int length_of(const EvictParams& p, int b) {
+  const int len = p.c.lens[b];
+  if (len < 0 || len > p.width || (long long)len > (long long)p.c.table_width * p.c.block_size) {
+    if (p.c.err) atomicCAS(p.c.err, 0u, (unsigned)ERR_SITE_CACHE_EVICT);
+    return -1;
+  }
+  return len;
+}
+
+// Sum of v over the threads before this one (their order), and over all.
+__device__ __forceinline__ int sum_before(int v, int* part, int* total) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int upto = v;
+#pragma unroll
+  for (int w = 1; w < 32; w <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, upto, w);
+    if (lane >= w) upto += o;
+  }
+  __syncthreads();  // part has been read
+  if (lane == 31) part[warp] = upto;
+  __syncthreads();
+  int all = part[lane], low = lane < warp ? all : 0;
+#pragma unroll
+  for (int w = 16; w > 0; w >>= 1) {
+    all += __shfl_xor_sync(0xffffffffu, all, w);
+    low += __shfl_xor_sync(0xffffffffu, low, w);
+  }
+  *total = all;
+  return upto - v + low;
+}
+
+__global__ void __launch_bounds__(kSelect) cache_select_kernel(const EvictParams p) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  __shared__ int hist[kBins];
+  __shared__ int part[32];
+  __shared__ int found_bin, found_above;
+  const int b = blockIdx.x / p.c.H, h = blockIdx.x % p.c.H;
+  const int t = threadIdx.x;
+  int* kept = p.kept + (long long)blockIdx.x * p.keep;
+  const int len = length_of(p, b);
+  const int n = max(0, min(len, p.keep));
+  if (h == 0 && t == 0) p.lens_out[b] = n;
+  const float* w = p.in.p + b * p.in.sb + h * p.in.sh;
+  float* w_out = p.out.p + b * p.out.sb + h * p.out.sh;
+  for (int j = n + t; j < p.keep; j += kSelect) kept[j] = -1;
+  if (len <= p.keep) {
+    for (int j = t; j < n; j += kSelect) {
+      kept[j] = j;
+      w_out[j] = w[j];
+    }
+    return;
+  }
+  const int old = len - p.recent;        // those that compete
+  const int top = p.keep - p.recent;     // for so many places
+  for (int j = t; j < p.recent; j += kSelect) {
+    kept[top + j] = old + j;
+    w_out[top + j] = w[old + j];
+  }
+  if (top == 0) return;
+
+  // ---------------------------------------------------------------- the smallest kept weight
+  uint32_t prefix = 0u, mask = 0u;  // the digits found
+  int need = top;                   // places for the weights that agree with them
+#pragma unroll 1
+  for (int digit = 0; digit < 3; ++digit) {
+    const int shift = digit == 0 ? 21 : digit == 1 ? 10 : 0;
+    const uint32_t low = digit == 2 ? 0x3ffu : 0x7ffu;
+    for (int i = t; i < kBins; i += kSelect) hist[i] = 0;
+    __syncthreads();
+    for (int j0 = 0; j0 < old; j0 += kSelect) {
+      const int j = j0 + t;
+      const uint32_t u = j < old ? order_of(w[j]) : 0u;
+      const bool on = j < old && (u & mask) == prefix;
+      const int bin = (int)(u >> shift & low);
+      // lanes that agree with the first of them count as one (many weights are zero)
+      const unsigned act = __ballot_sync(0xffffffffu, on);
+      if (act == 0u) continue;
+      const int leader = __ffs(act) - 1;
+      const int lead = __shfl_sync(0xffffffffu, bin, leader);
+      const unsigned same = __ballot_sync(0xffffffffu, on && bin == lead);
+      if ((t & 31) == leader) atomicAdd(&hist[lead], __popc(same));
+      if (on && bin != lead) atomicAdd(&hist[bin], 1);
+    }
+    __syncthreads();
+    // bins from the top: this thread's two are kBins - 1 - 2 t and the one below
+    const int h0 = hist[kBins - 1 - 2 * t], h1 = hist[kBins - 2 - 2 * t];
+    int total;
+    const int above = sum_before(h0 + h1, part, &total);
+    if (above < need && above + h0 >= need) found_bin = kBins - 1 - 2 * t, found_above = above;
+    if (above + h0 < need && above + h0 + h1 >= need)
+      found_bin = kBins - 2 - 2 * t, found_above = above + h0;
+    __syncthreads();
+    prefix |= (uint32_t)found_bin << shift;
+    mask |= low << shift;
+    need -= found_above;
+    __syncthreads();
+  }
+
+  // ---------------------------------------------------------------- the kept ones, in order
+  int placed = 0, equal = 0;  // before this step: kept, equal to the smallest
+#pragma unroll 1
+  for (int j0 = 0; j0 < old; j0 += kSelect) {
+    const int j = j0 + t;
+    const float x = j < old ? w[j] : 0.f;
+    const uint32_t u = j < old ? order_of(x) : 0u;
+    const bool more = j < old && u > prefix, tie = j < old && u == prefix;
+    int both;  // at most kSelect of either: two sums in one
+    const int sums = sum_before((more ? 1 : 0) | (tie ? 1 << 16 : 0), part, &both);
+    const int ties = equal + (sums >> 16);
+    const bool on = more || (tie && ties < need);
+    const int at = placed + (sums & 0xffff) + min(ties, need) - min(equal, need);
+    if (on) {
+      kept[at] = j;
+      w_out[at] = x;
+    }
+    placed += (both & 0xffff) + min(equal + (both >> 16), need) - min(equal, need);
+    equal += both >> 16;
+  }
+}
+
+struct Source {
+  long long row;  // (block * H + h) * block_size + row in the pool; -1: none
+  float ks, vs;   // 8 bits: its block's scales
+};
+
+template <int D, int FMT>
+__global__ void __launch_bounds__(kCopy) cache_copy_kernel(const EvictParams p, int blocks) {
+  constexpr bool I4 = FMT == FMT_INT4, E5M2 = FMT == FMT_E5M2;
+  const CacheParams& c = p.c;
+  __shared__ long long row_of[128];
+  __shared__ float ks_of[128], vs_of[128];
+  __shared__ float part[2][kCopy / 32];
+  const int t = threadIdx.x, bs = c.block_size;
+  const int blk = (int)(blockIdx.x % (unsigned)blocks);
+  const int bh = (int)(blockIdx.x / (unsigned)blocks);
+  const int b = bh / c.H, h = bh % c.H;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the selection
+  const int n = p.lens_out[b];
+  const int count = min(bs, n - blk * bs);  // tokens of this block
+  if (count <= 0) return;
+  const int page_out = p.table_out[(long long)b * p.table_out_width + blk];
+  if (page_out < 0 || page_out >= c.num_blocks) {
+    if (t == 0 && c.err) atomicCAS(c.err, 0u, (unsigned)ERR_SITE_CACHE_EVICT + 1);
+    return;
+  }
+  float ks_max = 0.f, vs_max = 0.f;
+  if (t < count) {  // (a block has at most 128 tokens)
+    const int pos = p.kept[(long long)bh * p.keep + blk * bs + t];
+    const int page = c.block_table[(long long)b * c.table_width + (pos >> c.block_log2)];
+    Source s{-1, 0.f, 0.f};
+    if (page < 0 || page >= c.num_blocks) {
+      if (c.err) atomicCAS(c.err, 0u, (unsigned)ERR_SITE_CACHE_EVICT + 1);
+    } else {
+      const long long block = (long long)page * c.H + h;
+      s.row = (block << c.block_log2) + (pos & (bs - 1));
+      if constexpr (!I4) s.ks = c.k_scale[block], s.vs = c.v_scale[block];
+    }
+    row_of[t] = s.row;
+    if constexpr (!I4) {
+      ks_of[t] = s.ks, vs_of[t] = s.vs;
+      ks_max = s.ks, vs_max = s.vs;
+    }
+  }
+  const long long block_out = (long long)page_out * c.H + h;
+  if constexpr (!I4) {
+#pragma unroll
+    for (int w = 16; w > 0; w >>= 1) {
+      ks_max = fmaxf(ks_max, __shfl_xor_sync(0xffffffffu, ks_max, w));
+      vs_max = fmaxf(vs_max, __shfl_xor_sync(0xffffffffu, vs_max, w));
+    }
+    if ((t & 31) == 0) part[0][t >> 5] = ks_max, part[1][t >> 5] = vs_max;
+  }
+  __syncthreads();
+  if constexpr (!I4) {
+#pragma unroll
+    for (int w = 0; w < kCopy / 32; ++w)
+      ks_max = fmaxf(ks_max, part[0][w]), vs_max = fmaxf(vs_max, part[1][w]);
+    if (!(ks_max > 0.f)) ks_max = 7.888609052210118e-31f;  // 2^-100: no token has a block
+    if (!(vs_max > 0.f)) vs_max = 7.888609052210118e-31f;
+    if (t == 0) c.k_scale[block_out] = ks_max, c.v_scale[block_out] = vs_max;
+  }
+  constexpr int RB = I4 ? D / 2 : D, PIECES = RB / 16;  // 16-byte pieces of a row
+  const long long out0 = block_out << c.block_log2;
+  for (int x = t; x < count * PIECES * 2; x += kCopy) {
+    const bool value = x >= count * PIECES;
+    const int y = value ? x - count * PIECES : x;
+    const int r = y / PIECES, piece = y % PIECES;
+    const long long row = row_of[r];
+    uint8_t* codes = value ? c.v : c.k;
+    uint4 v = I4 ? make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u)
+                 : make_uint4(0u, 0u, 0u, 0u);
+    if (row >= 0) v = *reinterpret_cast<const uint4*>(codes + row * RB + piece * 16);
+    if constexpr (!I4) {
+      const float from = value ? vs_of[r] : ks_of[r], to = value ? vs_max : ks_max;
+      if (from != to && row >= 0) {  // rounded for the larger scale
+        const float f = from / to;
+        uint32_t* w = &v.x;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 lo = f16x2_to_f32(codes_to_f16x2<E5M2>((uint16_t)(w[k] & 0xffffu)));
+          const float2 hi = f16x2_to_f32(codes_to_f16x2<E5M2>((uint16_t)(w[k] >> 16)));
+          w[k] = (uint32_t)f32_to_codes<E5M2>(lo.x * f, lo.y * f) |
+                 (uint32_t)f32_to_codes<E5M2>(hi.x * f, hi.y * f) << 16;
+        }
+      }
+    }
+    *reinterpret_cast<uint4*>(codes + (out0 + r) * RB + piece * 16) = v;
+  }
+  if constexpr (I4) {
+    using S = typename std::conditional<D == 128, uint2, uint32_t>::type;  // a token's scales
+    for (int x = t; x < count * 2; x += kCopy) {
+      const bool value = x >= count;
+      const int r = value ? x - count : x;
+      uint8_t* scales = value ? c.v_scale4 : c.k_scale4;
+      S s{};
+      if (row_of[r] >= 0) s = *reinterpret_cast<const S*>(scales + row_of[r] * (D / 16));
+      *reinterpret_cast<S*>(scales + (out0 + r) * (D / 16)) = s;
+    }
+  }
+}
+
+template <int D, int FMT>
+cudaError_t start(const EvictParams& p, cudaStream_t stream) {
+  const long long units = (long long)p.c.B * p.c.H;
+  const long long most = std::min<long long>(p.keep, p.width);  // tokens of a sequence
+  const int blocks = (int)((most + p.c.block_size - 1) / p.c.block_size);
+  if (units * blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  cache_select_kernel<<<(unsigned)units, kSelect, 0, stream>>>(p);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((unsigned)(units * blocks));
+  cfg.blockDim = dim3(kCopy);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, cache_copy_kernel<D, FMT>, p, blocks);
+}
+
+}  // namespace
+
+cudaError_t launch_cache_evict(const EvictParams& p, cudaStream_t stream) {
+  const bool d128 = p.c.d == 128;
+  switch (p.c.format) {
+    case FMT_E4M3:
+      return d128 ? start<128, FMT_E4M3>(p, stream) : start<64, FMT_E4M3>(p, stream);
+    case FMT_E5M2:
+      return d128 ? start<128, FMT_E5M2>(p, stream) : start<64, FMT_E5M2>(p, stream);
+    default:
+      return d128 ? start<128, FMT_INT4>(p, stream) : start<64, FMT_INT4>(p, stream);
+  }
+}
+
+}  // namespace fattn

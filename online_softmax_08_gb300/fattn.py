@@ -63,6 +63,14 @@ SIGNATURES = {
     "fattn_cache_fwd": (_i, [_cp, _bp, _vp, _ll, _ll, _vp, _ll, _ll, _vp, _i, _f, _i, _vp, _sz,
                              _vp]),
     "fattn_cache_fwd_workspace_bytes": (_sz, [_cp, _bp, _i]),
+    "fattn_cache_weights": (_i, [_cp, _bp, _vp, _ll, _ll, _vp, _i, _f, _i, _vp, _ll, _ll, _vp, _ll,
+                                 _ll, _i, _vp]),
+    "fattn_cache_evict": (_i, [_cp, _bp, _vp, _ll, _ll, _i, _vp, _i, _i, _i, _vp, _vp, _vp, _ll, _ll,
+                               _i, _vp]),
+    "fattn_rope_turns": (_i, [_vp, ctypes.POINTER(_f), _i, ctypes.c_double, _i, ctypes.c_double, _i,
+                              ctypes.c_double, ctypes.c_double]),
+    "fattn_rope": (_i, [_vp, _ll, _ll, _vp, _ll, _ll, _i, _vp, _ll, _ll, _vp, _ll, _ll, _i, _vp, _vp,
+                        _f, _i, _i, _i, _i, _i, _vp]),
     "fattn_status_string": (ctypes.c_char_p, [_i]),
 }
 
@@ -428,7 +436,6 @@ def new_cache(num_blocks, heads, block_size, d, dtype=torch.float8_e4m3fn, devic
 def _refuse_cache(cache, batch):
     """Say what _cache_args found wrong."""
     k, v, ks, vs = cache
-    table, lens, cu = batch[:3]
     if k.dtype is torch.uint8 and k.dim() == 4:
         scales = k.shape[:3] + (k.shape[3] // 8,)
         if v.dtype is not k.dtype or ks.dtype is not torch.float8_e5m2 or vs.dtype is not ks.dtype:
@@ -442,6 +449,9 @@ def _refuse_cache(cache, batch):
             k.dtype not in CACHE_FORMATS or v.dtype != k.dtype or ks.dtype != torch.float32
             or vs.dtype != torch.float32):
         raise ValueError("expected float8 codes of one type and fp32 scales")
+    if batch is None:
+        raise ValueError("expected contiguous tensors on one CUDA device")
+    table, lens, cu = batch[:3]
     if table.dim() != 2 or lens.shape != (table.shape[0],) or cu.shape != (table.shape[0] + 1,):
         raise ValueError("expected block_table [B, width], lens [B], cu_seqlens [B + 1]")
     if table.dtype != torch.int32 or lens.dtype != torch.int32 or cu.dtype != torch.int32:
@@ -449,38 +459,47 @@ def _refuse_cache(cache, batch):
     raise ValueError("expected contiguous tensors on one CUDA device")
 
 
-def _cache_args(cache, batch):
-    """The C descriptors of a cache and a batch, their tensors checked, with the
-    device index, H and d.  (A decoding step's calls are as short as the launches
-    they make, so the checks take few attribute reads.)"""
+def _pool_args(cache, batch=None):
+    """The C descriptor of a cache, its tensors checked, with the device index, H and d."""
     k, v, ks, vs = cache
-    table, lens, cu, total, max_seqlen = batch
     shape, dtype, dev = k.shape, k.dtype, k.get_device()
     fmt = CACHE_FORMATS.get(dtype)
-    if len(shape) != 4 or fmt is None or dev < 0 or table.dim() != 2:
+    if len(shape) != 4 or fmt is None or dev < 0:
         _refuse_cache(cache, batch)
-    B, width = table.shape
-    i32 = torch.int32
     if fmt == 4:
         scales, kind = shape[:3] + (shape[3] // 8,), torch.float8_e5m2
     else:
         scales, kind = shape[:2], torch.float32
-    if not (v.shape == shape and ks.shape == scales and vs.shape == scales and lens.dim() == 1
-            and lens.numel() == B and cu.dim() == 1 and cu.numel() == B + 1
-            and v.dtype is dtype and ks.dtype is kind and vs.dtype is kind and table.dtype is i32
-            and lens.dtype is i32 and cu.dtype is i32
+    if not (v.shape == shape and ks.shape == scales and vs.shape == scales
+            and v.dtype is dtype and ks.dtype is kind and vs.dtype is kind
             and k.is_contiguous() and v.is_contiguous() and ks.is_contiguous()
-            and vs.is_contiguous() and table.is_contiguous() and lens.is_contiguous()
-            and cu.is_contiguous()
-            and v.get_device() == dev and ks.get_device() == dev and vs.get_device() == dev
-            and table.get_device() == dev and lens.get_device() == dev and cu.get_device() == dev):
+            and vs.is_contiguous()
+            and v.get_device() == dev and ks.get_device() == dev and vs.get_device() == dev):
         _refuse_cache(cache, batch)
     nb, H, bs, d = shape
     if fmt == 4:
         d *= 2
     return (_pack_cache(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), nb, H, bs, d, fmt),
-            _pack_batch(table.data_ptr(), lens.data_ptr(), cu.data_ptr(), B, width, total,
-                        max_seqlen), dev, H, d)
+            dev, H, d)
+
+
+def _cache_args(cache, batch):
+    """The C descriptors of a cache and a batch, their tensors checked, with the
+    device index, H and d.  (A decoding step's calls are as short as the launches
+    they make, so the checks take few attribute reads.)"""
+    c, dev, H, d = _pool_args(cache, batch)
+    table, lens, cu, total, max_seqlen = batch
+    if table.dim() != 2:
+        _refuse_cache(cache, batch)
+    B, width = table.shape
+    i32 = torch.int32
+    if not (lens.dim() == 1 and lens.numel() == B and cu.dim() == 1 and cu.numel() == B + 1
+            and table.dtype is i32 and lens.dtype is i32 and cu.dtype is i32
+            and table.is_contiguous() and lens.is_contiguous() and cu.is_contiguous()
+            and table.get_device() == dev and lens.get_device() == dev and cu.get_device() == dev):
+        _refuse_cache(cache, batch)
+    return (c, _pack_batch(table.data_ptr(), lens.data_ptr(), cu.data_ptr(), B, width, total,
+                           max_seqlen), dev, H, d)
 
 
 def _packed(x, total, heads, d, dev):
@@ -588,3 +607,171 @@ def cache_forward(q, cache, batch, scale, causal, out=None, workspace=None, stre
     if st:
         raise FattnError("fattn_cache_fwd", st)
     return o, lse
+
+
+# ------------------------------------------------------------------ weights of cached keys, eviction
+
+def _weights_of(w, B, H, dev):
+    """Pointer, sequence and head strides and width of fp32 weights [B, H, width]."""
+    st = w.stride()
+    if len(st) != 3 or w.shape[:2] != (B, H) or w.dtype is not torch.float32 or \
+            w.get_device() != dev or (st[2] != 1 and w.shape[2] > 1):
+        raise ValueError("expected fp32 weights [%d, %d, width] on device %d with a contiguous last "
+                         "axis" % (B, H, dev))
+    return w.data_ptr(), st[0], st[1], w.shape[2]
+
+
+def cache_weights(q, lse, cache, batch, scale, causal, weights=None, out=None, stream=None):
+    """The attention weight that every key of the batch's sequences gets from its queries q
+    (bf16 [total, Hq, d]), whose log-sum-exp lse (fp32 [Hq, total]) cache_forward gave: fp32
+    [B, H, width], summed over the queries and the heads of a group.  weights: what the keys
+    had before, which is added to (None: nothing); the batch's own tokens start anew.  out: a
+    tensor to write to (None: `weights`, in place, or a new one with room for the table).
+    Entries behind a sequence's length stay as they are (new: zero)."""
+    c, b, dev, H, d = _cache_args(cache, batch)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return cache_weights(q, lse, cache, batch, scale, causal, weights, out)
+    if q.dim() != 3:
+        raise ValueError("expected q [total, Hq, d]")
+    total, Hq = batch[3], q.shape[1]
+    qp, qt, qh = _packed(q, total, Hq, d, dev)
+    if lse.shape != (Hq, total) or lse.dtype is not torch.float32 or not lse.is_contiguous() or \
+            lse.get_device() != dev:
+        raise ValueError("expected contiguous fp32 lse [%d, %d] on device %d" % (Hq, total, dev))
+    B, width = batch[0].shape
+    if out is None:
+        out = weights if weights is not None else torch.zeros(
+            (B, H, width * cache[0].shape[2]), dtype=torch.float32, device=q.device)
+    op, ob, oh, width = _weights_of(out, B, H, dev)
+    if weights is None:
+        wp, wb, wh = None, 0, 0
+    else:
+        wp, wb, wh, had = _weights_of(weights, B, H, dev)
+        width = min(width, had)
+    st = (_lib or load()).fattn_cache_weights(c, b, qp, qt, qh, lse.data_ptr(), Hq, scale,
+                                              1 if causal else 0, wp, wb, wh, op, ob, oh, width,
+                                              _raw_stream(dev))
+    if st:
+        raise FattnError("fattn_cache_weights", st)
+    return out
+
+
+def cache_evict(cache, weights, block_table, lens, table_out, keep, recent=0, out=None, stream=None):
+    """Copies, for every sequence and key/value head, the last `recent` tokens and those of the
+    largest weights (fp32 [B, H, width]), `keep` in all and in their order, into the blocks of
+    table_out (int32 [B, width]); a sequence of at most `keep` tokens is copied whole.  Returns
+    the new lengths (int32 [B]), the positions of the kept tokens (int32 [B, H, keep], -1 behind
+    the last) and their weights (fp32 [B, H, keep], or `out`).  The source blocks stay as they
+    are."""
+    c, dev, H, d = _pool_args(cache)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return cache_evict(cache, weights, block_table, lens, table_out, keep, recent, out)
+    i32 = torch.int32
+    if block_table.dim() != 2 or table_out.dim() != 2 or lens.dim() != 1 or \
+            not lens.shape[0] == block_table.shape[0] == table_out.shape[0]:
+        raise ValueError("expected block_table and table_out [B, width], lens [B]")
+    for x in (block_table, table_out, lens):
+        if x.dtype is not i32 or not x.is_contiguous() or x.get_device() != dev:
+            raise ValueError("expected contiguous int32 tables and lengths on device %d" % dev)
+    if keep < 1:
+        raise ValueError("expected keep >= 1")
+    B, width = block_table.shape
+    wp, wb, wh, w_width = _weights_of(weights, B, H, dev)
+    on = weights.device
+    if out is None:
+        out = torch.zeros((B, H, keep), dtype=torch.float32, device=on)
+    op, ob, oh, o_width = _weights_of(out, B, H, dev)
+    lens_out = torch.empty((B,), dtype=i32, device=on)
+    kept = torch.empty((B, H, keep), dtype=i32, device=on)
+    b = _pack_batch(block_table.data_ptr(), lens.data_ptr(), lens.data_ptr(), B, width, 0, 0)
+    st = (_lib or load()).fattn_cache_evict(c, b, wp, wb, wh, w_width, table_out.data_ptr(),
+                                            table_out.shape[1], keep, recent, lens_out.data_ptr(),
+                                            kept.data_ptr(), op, ob, oh, o_width, _raw_stream(dev))
+    if st:
+        raise FattnError("fattn_cache_evict", st)
+    return lens_out, kept, out
+
+
+# ------------------------------------------------------------------ rotary positions
+
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+# how the frequencies are scaled: number, default fast and slow (turns over the original length)
+ROPE_SCALINGS = {"none": (0, 0.0, 0.0), "linear": (1, 0.0, 0.0), "base": (2, 0.0, 0.0),
+                 "yarn": (3, 32.0, 1.0), "bands": (4, 4.0, 1.0)}
+
+
+class RopeTable(typing.NamedTuple):
+    """What fattn_rope takes its angles from: a device int64 tensor of rot / 2 fractions of a
+    turn (2^-64 each), and the magnitude that the turned channels are multiplied by."""
+    turns: torch.Tensor
+    magnitude: float
+
+
+def rope_table(rot, base=10000.0, kind="none", factor=1.0, length=0, fast=None, slow=None,
+               device="cuda"):
+    """The RopeTable of the frequencies base^(-2 i / rot), scaled by `factor` from an original
+    length as fattn_rope_scaling says (kind: "none", "linear", "base", "yarn" or "bands")."""
+    if kind not in ROPE_SCALINGS:
+        raise ValueError("kind is one of %s, not %r" % (", ".join(ROPE_SCALINGS), kind))
+    number, f, s = ROPE_SCALINGS[kind]
+    turns = torch.empty((max(rot // 2, 1),), dtype=torch.int64)
+    m = ctypes.c_float(0.0)
+    _check("fattn_rope_turns", load().fattn_rope_turns(
+        turns.data_ptr(), ctypes.byref(m), rot, base, number, factor, length,
+        f if fast is None else fast, s if slow is None else slow))
+    return RopeTable(turns.to(device), m.value)
+
+
+def _rope(q, k, positions, table, layout, backward, out, stream):
+    turns, magnitude = table
+    dev = q.get_device()
+    if layout not in ROPE_LAYOUTS:
+        raise ValueError("layout is 'half' or 'interleaved', not %r" % (layout,))
+    if q.dim() != 3 or dev < 0:
+        raise ValueError("expected q [total, Hq, d] on a CUDA device")
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return _rope(q, k, positions, table, layout, backward, out, None)
+    T, Hq, d = q.shape
+    if positions.dtype is not torch.int32 or positions.shape != (T,) or \
+            not positions.is_contiguous() or positions.get_device() != dev:
+        raise ValueError("expected contiguous int32 positions [%d] on device %d" % (T, dev))
+    if turns.dtype is not torch.int64 or turns.dim() != 1 or not turns.is_contiguous() or \
+            turns.get_device() != dev:
+        raise ValueError("expected the table of rope_table on device %d" % dev)
+    if k is not None and k.dim() != 3:
+        raise ValueError("expected k [total, Hk, d]")
+    Hk = 0 if k is None else k.shape[1]
+    qo, ko = (None, None) if out is None else out
+    qp = qop = kp = kop = (None, 0, 0)
+    if qo is None:
+        qo = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=q.device)
+    if Hq:
+        qp, qop = _packed(q, T, Hq, d, dev), _packed(qo, T, Hq, d, dev)
+    if k is None:
+        ko = None
+    elif ko is None:
+        ko = torch.empty((T, Hk, d), dtype=torch.bfloat16, device=q.device)
+    if Hk:
+        kp, kop = _packed(k, T, Hk, d, dev), _packed(ko, T, Hk, d, dev)
+    st = (_lib or load()).fattn_rope(*qp, *qop, Hq, *kp, *kop, Hk, positions.data_ptr(),
+                                     turns.data_ptr(), magnitude, T, d, 2 * turns.shape[0],
+                                     ROPE_LAYOUTS[layout], 1 if backward else 0, _raw_stream(dev))
+    if st:
+        raise FattnError("fattn_rope", st)
+    return qo, ko
+
+
+def rope(q, k, positions, table, layout="half", out=None, stream=None):
+    """q [total, Hq, d] and k [total, Hk, d] (bf16, any token and head strides; k may be None)
+    with their first rot channels turned to `positions` (device int32 [total]) by a RopeTable.
+    layout: "half" pairs channels i and rot / 2 + i, "interleaved" 2 i and 2 i + 1.  out: a pair
+    of tensors to write to, the inputs themselves for in place."""
+    return _rope(q, k, positions, table, layout, False, out, stream)
+
+
+def rope_backward(dq, dk, positions, table, layout="half", out=None, stream=None):
+    """The gradients with respect to rope's q and k, of those with respect to its results."""
+    return _rope(dq, dk, positions, table, layout, True, out, stream)

@@ -1,0 +1,371 @@
+"""The attention weights of cached keys, and eviction by them, against the fp64 oracle.
+
+Bar of a weight, for what the queries add to it: a term exp(s - lse) has the score's error,
+(d + 12) u S as in test_gpu_cache.py, that of taking s - lse to base 2 in fp32, 4 u (S + |lse|),
+and 2^-22 of ex2, all relative to it; the terms are positive, so n of them summed in fp32 add
+n u.  With Z the largest S + |lse| of the rows that see the key and n rows:
+  |W - W_ref| <= new ((d + 16) u Z + n u + 2^-21) + u |W_ref|,
+u = 2^-24, the last term the sum with the weight from before; terms below 2^-126 are flushed:
+n 2^-126 more.  Eviction copies: positions, weights, codes and scales are compared bit for bit.
+"""
+import numpy as np
+import pytest
+import torch
+
+import test_gpu_cache as base8
+import test_gpu_cache4 as base4
+from online_softmax_08_gb300 import fattn
+from oracle import cache as oc
+from oracle import evict as oe
+
+pytestmark = pytest.mark.gpu
+
+DEV = base8.DEV
+_bf16, _strided = base8._bf16, base8._strided
+
+
+@pytest.fixture(autouse=True)
+def _no_device_error():
+    fattn.fattn_device_error()
+    yield
+    torch.cuda.synchronize()
+    assert fattn.fattn_device_error() == 0
+
+
+def _case(pairs, H, d, bs, fmt, **kw):
+    if fmt == "int4":
+        return base4.Case(pairs, H, d, bs, **kw)
+    return base8.Case(pairs, H, d, bs, fmt, nan_slots=False, **kw)
+
+
+def _check_weights(c, fmt, q, lse, scale, causal, before, was, got):
+    n = int(c.cu[-1])
+    ref, Z = oe.weights(c.cache, fmt, c.batch, q.double().cpu().numpy()[:n],
+                        lse.double().cpu().numpy()[:, :n], scale, causal, before, was)
+    zero = None if before is None else np.zeros_like(before)
+    new, _ = oe.weights(c.cache, fmt, c.batch, q.double().cpu().numpy()[:n],
+                        lse.double().cpu().numpy()[:, :n], scale, causal, zero, np.zeros_like(was))
+    rows = max(a for a, _ in c.pairs) * (q.shape[1] // c.H)
+    u = 2.0 ** -24
+    touched = np.zeros(ref.shape, dtype=bool)
+    for b, length in enumerate(c.lens):
+        if c.cu[b + 1] > c.cu[b]:
+            touched[b, :, :length] = True
+    bar = new * ((c.d + 16) * u * Z + rows * u + 2.0 ** -21) + u * np.abs(ref) + rows * 2.0 ** -126
+    err = np.abs(got.double().cpu().numpy() - ref)
+    assert np.all(err[touched] <= bar[touched]), (err / bar)[touched].max()
+    assert np.all(err[~touched] == 0)
+
+
+WEIGHTS = [
+    # (pairs, H, G, d, bs, fmt, causal)
+    ([(1, 0)], 1, 1, 64, 16, "int4", True),
+    ([(1, 16)], 2, 1, 128, 16, "e4m3", True),
+    ([(1, 1), (1, 14), (1, 127), (1, 128), (1, 300)], 2, 4, 128, 16, "int4", True),
+    ([(1, 700), (1, 0), (1, 2100)], 2, 7, 64, 32, "e5m2", True),
+    ([(1, 999)], 2, 8, 128, 128, "int4", False),
+    ([(1, 200)], 1, 33, 64, 64, "e4m3", True),
+    ([(4, 60), (0, 9), (3, 0), (7, 250), (0, 0)], 2, 3, 128, 32, "int4", True),
+    ([(40, 0), (17, 100), (1, 64)], 2, 2, 128, 64, "e4m3", True),
+    ([(130, 0)], 2, 1, 64, 64, "int4", True),
+    ([(32, 100), (31, 97)], 1, 1, 128, 16, "int4", True),
+    ([(129, 200), (1, 90), (65, 0)], 1, 4, 128, 16, "int4", True),
+    ([(260, 13)], 1, 3, 128, 128, "e5m2", False),
+    ([(1, 50), (3, 40)], 1, 300, 64, 16, "e4m3", True),
+    ([(i % 4, 5 * i) for i in range(70)], 2, 2, 64, 16, "int4", True),
+    ([(i % 2, i % 50) for i in range(1100)], 1, 1, 64, 16, "int4", True),
+]
+
+
+@pytest.mark.parametrize("layout", ["own", "slice", "heads"])
+@pytest.mark.parametrize("pairs,H,G,d,bs,fmt,causal", WEIGHTS)
+def test_weights_match_oracle(pairs, H, G, d, bs, fmt, causal, layout):
+    c = _case(pairs, H, d, bs, fmt, seed=d + bs + G + len(pairs), pad_tokens=2).fill()
+    q = _bf16(c.rng, (c.T, H * G, d), 1.5)
+    cache, batch = c.on_device()
+    scale = d ** -0.5
+    dq = _strided(q, layout)
+    _, lse = fattn.cache_forward(dq, cache, batch, scale, causal)
+    B, width = len(pairs), int(c.lens.max()) + 5
+    # new, added to what was there, in place, and into rows apart
+    new = fattn.cache_weights(dq, lse, cache, batch, scale, causal)
+    assert new.shape == (B, H, batch.block_table.shape[1] * bs)
+    _check_weights(c, fmt, q, lse, scale, causal, None, np.zeros(new.shape), new)
+    before = torch.tensor(c.rng.uniform(0, 3, (H, B, width)), dtype=torch.float32, device=DEV).transpose(0, 1)
+    keep = before.clone()
+    whole = torch.full((B, H + 2, width + 3), 7.0, device=DEV)
+    out = fattn.cache_weights(dq, lse, cache, batch, scale, causal, before, out=whole[:, 1:1 + H, 1:])
+    assert torch.equal(before, keep)
+    was = np.full((B, H, width + 2), 7.0)
+    padded = np.concatenate([keep.cpu().numpy(), np.zeros((B, H, 2))], axis=2)
+    _check_weights(c, fmt, q, lse, scale, causal, padded, was, out)
+    whole[:, 1:1 + H, 1:] = 7.0
+    assert bool((whole == 7.0).all())
+    again = fattn.cache_weights(dq, lse, cache, batch, scale, causal, before)
+    assert again is before
+    _check_weights(c, fmt, q, lse, scale, causal, keep.cpu().numpy(), keep.cpu().numpy(), before)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("n,length,G", [(5, 2, 2), (3, 0, 1), (40, 7, 4), (300, 20, 1)])
+def test_weights_of_more_queries_than_tokens(n, length, G, causal):
+    H, d = 2, 64
+    c = _case([(1, 40), (n, length - n), (1, 3)], H, d, 16, "int4").fill()
+    q = _bf16(c.rng, (c.T, H * G, d)).to(DEV)
+    cache, batch = c.on_device()
+    _, lse = fattn.cache_forward(q, cache, batch, 0.125, causal)
+    w = fattn.cache_weights(q, lse, cache, batch, 0.125, causal)
+    _check_weights(c, "int4", q, lse, 0.125, causal, None, np.zeros(w.shape), w)
+    # every row that sees something gives one in all
+    total = w.sum(dim=2).cpu().double()
+    live = n if length > 0 and not causal else min(n, length)
+    assert abs(float(total[1, 0]) - live * G) <= 1e-4 * max(1, live * G)
+
+
+def test_nan_key_and_repeated_calls():
+    """A NaN key of one head makes NaN of the weights of the keys that its queries see, and of no
+    other head's or sequence's.  Repeated calls agree bit for bit."""
+    H, G, d, bs = 2, 2, 128, 16
+    c = _case([(3, 50), (2, 20)], H, d, bs, "e4m3").fill()
+    q = _bf16(c.rng, (c.T, H * G, d)).to(DEV)
+    cache, batch = c.on_device()
+    _, lse = fattn.cache_forward(q, cache, batch, 0.1, True)
+    w = fattn.cache_weights(q, lse, cache, batch, 0.1, True)
+    assert torch.equal(w, fattn.cache_weights(q, lse, cache, batch, 0.1, True))
+    c.cache["k"][c.table[0, 3], 0, 4, 7] = 0x7f  # position 52, which the last query sees
+    cache, batch = c.on_device()
+    _, lse = fattn.cache_forward(q, cache, batch, 0.1, True)
+    got = fattn.cache_weights(q, lse, cache, batch, 0.1, True)
+    assert torch.equal(got[0, 1], w[0, 1]) and torch.equal(got[1], w[1])
+    assert bool(torch.isnan(got[0, 0, :53]).all()) and bool((got[0, 0, 53:] == 0).all())
+
+
+def _scatter(c, new, bs):
+    """A table of blocks that no sequence has, for `new` tokens each; the pool grows by them."""
+    need = [-(-x // bs) for x in new]
+    nb = c.cache["k"].shape[0]
+    for name, a in c.cache.items():
+        more = c.rng.integers(0, 100, (sum(need),) + a.shape[1:])
+        c.cache[name] = np.concatenate([a, more.astype(a.dtype)])
+    order = (nb + c.rng.permutation(sum(need))).tolist()
+    table = np.full((len(new), max(max(need), 1) + 1), 2 ** 30, dtype=np.int32)
+    for b, n in enumerate(need):
+        table[b, :n] = [order.pop() for _ in range(n)]
+    return table
+
+
+EVICT = [
+    # (lens, H, d, bs, fmt, keep, recent)
+    ([1], 1, 64, 16, "int4", 1, 0),
+    ([2, 3], 1, 128, 16, "int4", 1, 1),
+    ([17, 16, 15, 0, 40], 2, 64, 16, "int4", 16, 4),
+    ([1000, 3, 500, 257], 3, 128, 64, "int4", 100, 30),
+    ([1025, 2049, 64], 2, 128, 32, "int4", 1024, 0),
+    ([5000, 4999], 1, 64, 128, "int4", 1500, 1500),
+    ([300, 77], 2, 128, 16, "e4m3", 50, 10),
+    ([300, 77, 512], 1, 64, 64, "e5m2", 200, 100),
+    ([400, 90], 2, 64, 128, "e4m3", 129, 0),
+    ([i * 7 % 200 for i in range(150)], 2, 64, 16, "int4", 33, 5),
+]
+
+
+def _weights_for(c, lens, H, kind):
+    w = c.rng.exponential(1.0, (len(lens), H, max(max(lens), 1) + 3)) ** 3
+    if kind == "ties":
+        w = np.floor(w * 2) / 2
+    if kind == "special":
+        w = w * 10.0 ** c.rng.integers(-40, 30, w.shape)
+        r = c.rng.random(w.shape)
+        w[r < 0.02] = np.inf
+        w[(r > 0.02) & (r < 0.04)] = np.nan
+        w[(r > 0.04) & (r < 0.06)] = -np.inf
+        w[(r > 0.1) & (r < 0.4)] *= -1.0
+        w[(r > 0.4) & (r < 0.5)] = 0.0
+        w[(r > 0.5) & (r < 0.6)] = -0.0
+    return w.astype(np.float32)
+
+
+@pytest.mark.parametrize("kind", ["plain", "ties", "special"])
+@pytest.mark.parametrize("lens,H,d,bs,fmt,keep,recent", EVICT)
+def test_evict_matches_oracle(lens, H, d, bs, fmt, keep, recent, kind):
+    c = _case([(0, x) for x in lens], H, d, bs, fmt, seed=len(lens) + keep).fill()
+    new = [min(x, keep) for x in lens]
+    table_out = _scatter(c, new, bs)
+    w = _weights_for(c, lens, H, kind)
+    want, kept, new = oe.evict(c.cache, fmt, c.table, c.lens, w, table_out, keep, recent)
+    cache, batch = c.on_device()
+    dev = lambda a: torch.tensor(a, device=DEV)
+    whole = torch.full((len(lens), H + 1, keep + 2), 7.0, device=DEV)
+    out = whole[:, 1:, 2:]
+    for _ in range(2):  # the second call changes nothing
+        got_lens, got_kept, got_w = fattn.cache_evict(cache, dev(w), batch.block_table, batch.lens,
+                                                      dev(table_out), keep, recent, out=out)
+        np.testing.assert_array_equal(got_lens.cpu().numpy(), new)
+        for b in range(len(lens)):
+            for h in range(H):
+                k = got_kept[b, h].cpu().numpy()
+                np.testing.assert_array_equal(k[:new[b]], kept[b][h])
+                assert np.all(k[new[b]:] == -1)
+                x = got_w[b, h].cpu().numpy()
+                np.testing.assert_array_equal(x[:new[b]], w[b, h, kept[b][h]])
+                assert np.all(x[new[b]:] == 7.0)
+        if fmt == "int4":
+            base4._assert_cache(cache, want)
+        else:
+            base8._assert_cache(cache, want, fmt)
+    whole[:, 1:, 2:] = 7.0
+    assert bool((whole == 7.0).all())
+
+
+def test_evict_of_a_long_sequence():
+    """More tokens than any pass holds at once, nearly all weights alike in their upper digits."""
+    H, d, bs, L, keep, recent = 2, 64, 128, 150001, 70000, 123
+    g = torch.Generator(device=DEV).manual_seed(1)
+    w = (1.0 + torch.rand((1, H, L), generator=g, device=DEV) * 2.0 ** -12)
+    w[:, 1] = 0.5
+    nb = -(-L // bs)
+    cache = fattn.new_cache(nb + -(-keep // bs), H, bs, d, dtype=torch.uint8, device=DEV)
+    for x in (cache.k, cache.v, cache.k_scale.view(torch.uint8)):
+        x.copy_(torch.randint(0, 256, x.shape, generator=g, device=DEV))
+    i32 = dict(dtype=torch.int32, device=DEV)
+    table = torch.randperm(nb, generator=g, device=DEV).int()[None].contiguous()
+    out_table = torch.arange(nb, nb + -(-keep // bs), **i32)[None].contiguous()
+    lens, kept, moved = fattn.cache_evict(cache, w, table, torch.tensor([L], **i32), out_table, keep,
+                                          recent)
+    assert int(lens[0]) == keep
+    order = torch.sort(w[0, :, :L - recent].double(), dim=1, descending=True, stable=True).indices
+    want = torch.cat((order[:, :keep - recent].sort(dim=1).values,
+                      torch.arange(L - recent, L, device=DEV).expand(H, -1)), dim=1)
+    assert torch.equal(kept[0].long(), want)
+    assert torch.equal(moved[0], w[0].gather(1, want))
+    for x in (cache.k, cache.v, cache.k_scale.view(torch.uint8)):
+        src = x[table[0].long()].transpose(0, 1).reshape(H, -1, x.shape[-1])
+        dst = x[out_table[0].long()].transpose(0, 1).reshape(H, -1, x.shape[-1])[:, :keep]
+        at = want[..., None].expand(-1, -1, x.shape[-1])
+        assert torch.equal(dst, src.gather(1, at))
+
+
+def test_evict_to_its_own_blocks():
+    """A sequence that is short enough may be given its own blocks: it stays as it is."""
+    c = _case([(0, 30), (0, 100)], 2, 64, 16, "e4m3").fill()
+    table_out = _scatter(c, [0, 40], 16)
+    table_out[0, :2] = c.table[0, :2]
+    w = _weights_for(c, [30, 100], 2, "plain")
+    want, kept, new = oe.evict(c.cache, "e4m3", c.table, c.lens, w, table_out, 40, 8)
+    cache, batch = c.on_device()
+    dev = lambda a: torch.tensor(a, device=DEV)
+    fattn.cache_evict(cache, dev(w), batch.block_table, batch.lens, dev(table_out), 40, 8)
+    base8._assert_cache(cache, want, "e4m3")
+
+
+def test_bad_entries_are_reported():
+    H, d, bs = 2, 64, 16
+    c = _case([(1, 30), (2, 50), (1, 20)], H, d, bs, "int4").fill()
+    q = _bf16(c.rng, (c.T, H, d)).to(DEV)
+    cache, batch = c.on_device()
+    _, lse = fattn.cache_forward(q, cache, batch, 0.1, True)
+    ref = fattn.cache_weights(q, lse, cache, batch, 0.1, True)
+    dev = lambda a: torch.tensor(a, dtype=torch.int32, device=DEV)
+    lens = batch.lens.clone()
+    lens[1] = 10 ** 6
+    w = torch.full_like(ref, 7.0)
+    fattn.cache_weights(q, lse, cache, batch._replace(lens=lens), 0.1, True, out=w)
+    assert fattn.fattn_device_error() == 0x470
+    assert torch.equal(w[0, :, :31], ref[0, :, :31]) and torch.equal(w[2, :, :21], ref[2, :, :21])
+    assert bool((w[1] == 7.0).all())
+    narrow = torch.zeros((3, H, 40), device=DEV)  # no room for sequence 1
+    fattn.cache_weights(q, lse, cache, batch, 0.1, True, out=narrow)
+    assert fattn.fattn_device_error() == 0x470 and bool((narrow[1] == 0).all())
+    table = batch.block_table.clone()
+    table[1, 1] = -5
+    got = fattn.cache_weights(q, lse, cache, batch._replace(block_table=table), 0.1, True)
+    assert fattn.fattn_device_error() == 0x471
+    assert bool((got[1, :, 16:32] == 0).all()) and torch.equal(got[1, :, :16], ref[1, :, :16])
+    # eviction
+    table_out = dev(_scatter(c, [10, 10, 10], bs))
+    cache, batch = c.on_device()
+    w = torch.rand((3, H, 60), device=DEV)
+    good = fattn.cache_evict(cache, w, batch.block_table, batch.lens, table_out, 10, 2)
+    bad_lens = fattn.cache_evict(cache, w, batch.block_table, lens, table_out, 10, 2)
+    assert fattn.fattn_device_error() == 0x480 and bad_lens[0].tolist() == [10, 0, 10]
+    assert torch.equal(bad_lens[1][0], good[1][0]) and bool((bad_lens[1][1] == -1).all())
+    fattn.cache_evict(cache, w, table, batch.lens, table_out, 10, 2)
+    assert fattn.fattn_device_error() in (0, 0x481)
+    wrong = table_out.clone()
+    wrong[2, 0] = 10 ** 8
+    fattn.cache_evict(cache, w, batch.block_table, batch.lens, wrong, 10, 2)
+    assert fattn.fattn_device_error() == 0x481
+
+
+def test_serving_run():
+    """What they are for, together: queries and keys are turned, the keys and values go into the
+    4-bit cache, the queries attend and weigh the keys, the cache is cut to its most attended
+    tokens in other blocks, and the next step, captured in a graph, goes on from there."""
+    H, G, d, bs, n = 2, 4, 128, 16, 200
+    keep, recent, steps = 64, 16, 3
+    rng = np.random.default_rng(7)
+    scale = d ** -0.5
+    table = fattn.rope_table(d, 1e4, "yarn", 4.0, 64, device=DEV)
+    pool = fattn.new_cache(60, H, bs, d, dtype=torch.uint8, device=DEV)
+    i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device=DEV)
+    blocks = torch.arange(40, dtype=torch.int32, device=DEV).flip(0).reshape(2, 20).contiguous()
+    others = torch.arange(40, 60, dtype=torch.int32, device=DEV).reshape(2, 10).contiguous()
+    lens = i32(n, n - 30)
+    batch = fattn.CacheBatch(blocks, lens, i32(0, n, 2 * n - 30), 2 * n - 30, n)
+    pos = torch.cat((torch.arange(n), torch.arange(n - 30))).int().to(DEV)
+    x = _bf16(rng, (2 * n - 30, H * (G + 2), d)).to(DEV)
+    q, k = fattn.rope(x[:, :H * G], x[:, H * G:H * (G + 1)], pos, table)
+    fattn.cache_append(k, x[:, H * (G + 1):], pool, batch)
+    o, lse = fattn.cache_forward(q, pool, batch, scale, True)
+    w = fattn.cache_weights(q, lse, pool, batch, scale, True)
+    rows = torch.tensor([n, n - 30], device=DEV) * G
+    assert torch.allclose(w.sum(dim=2), rows[:, None].float().expand(2, H), rtol=1e-4)
+    before = fattn.cache_read(pool, batch)
+    lens2, kept, w2 = fattn.cache_evict(pool, w, blocks, lens, others, keep, recent)
+    w2 = torch.cat((w2, torch.zeros((2, H, 96), device=DEV)), dim=2).contiguous()
+    after = fattn.cache_read(pool, fattn.CacheBatch(others, lens2, i32(0, keep, 2 * keep), 2 * keep, keep))
+    for a, b in zip(before, after):
+        for s, first in enumerate((0, n)):
+            for h in range(H):
+                assert torch.equal(b[s * keep:(s + 1) * keep, h], a[first + kept[s, h].long(), h])
+    # single tokens on what is left
+    step = fattn.CacheBatch(others, lens2, i32(0, 1, 2), 2, 1)
+    place = i32(n, n - 30)
+    xs = torch.zeros((2, H * (G + 2), d), dtype=torch.bfloat16, device=DEV)
+    ws = torch.empty(1 << 26, dtype=torch.uint8, device=DEV)
+
+    def one():
+        lens2.add_(1)
+        q, k = fattn.rope(xs[:, :H * G], xs[:, H * G:H * (G + 1)], place, table)
+        fattn.cache_append(k, xs[:, H * (G + 1):], pool, step)
+        o, lse = fattn.cache_forward(q, pool, step, scale, True, workspace=ws)
+        fattn.cache_weights(q, lse, pool, step, scale, True, w2)
+        place.add_(1)
+        return q, o, lse
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        with torch.cuda.graph(graph, stream=side):
+            q1, o1, lse1 = one()
+    torch.cuda.synchronize()
+    for i in range(steps):
+        xs.copy_(_bf16(rng, tuple(xs.shape)))
+        old = w2.clone()
+        graph.replay()
+        torch.cuda.synchronize()
+        # in 64 bits, of the cache's own values
+        L = keep + i + 1
+        kv = fattn.cache_read(pool, fattn.CacheBatch(others, lens2, i32(0, L, 2 * L), 2 * L, L))
+        for s in range(2):
+            ks, vs = (t[s * L:(s + 1) * L].double().transpose(0, 1) for t in kv)  # [H, L, d]
+            z = scale * torch.einsum("hgd,hld->hgl", q1[s].double().reshape(H, G, d), ks)
+            p = torch.softmax(z, dim=2)
+            ref = torch.einsum("hgl,hld->hgd", p, vs).reshape(H * G, d)
+            assert float((o1[s].double() - ref).abs().max()) <= 2e-2
+            want = old[s, :, :L].double()
+            want[:, L - 1] = 0.0
+            want += p.sum(dim=1)
+            assert float((w2[s, :, :L].double() - want).abs().max()) <= 1e-4
+            assert torch.equal(w2[s, :, L:], old[s, :, L:])
