@@ -597,18 +597,12 @@ int cache_move(CacheMove launch, const fattn_cache* cache, const fattn_cache_bat
   return debug_post_call(e == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA, s);
 }
 
-// A cache's codes as {bytes of a row, block_size, num_blocks * H}, in boxes of 16 tokens
-// (4 bits: of 32 where a block has them)
+// An 8-bit cache's codes as {d, block_size, num_blocks * H} bytes, in boxes of 16 tokens
 // whose 16-byte pieces are swizzled over the banks.
 bool make_cache_map(CUtensorMap* m, const void* codes, const fattn_cache* c) {
-  const bool int4 = c->format == FATTN_CACHE_INT4;
-  const int row = int4 ? c->d / 2 : c->d;
-  const int tokens = int4 && c->block_size >= 32 ? 32 : 16;
-  return make_map(m, codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, row, c->block_size,
-                  (long long)c->num_blocks * c->H, row, tokens,
-                  row == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
-                  : row == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
-                              : CU_TENSOR_MAP_SWIZZLE_32B);
+  return make_map(m, codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, c->d, c->block_size,
+                  (long long)c->num_blocks * c->H, c->d, 16,
+                  c->d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 int check_cache_heads(const fattn_cache* c, const fattn_cache_batch* b, int Hq) {
@@ -680,8 +674,9 @@ extern "C" int fattn_cache_fwd(const fattn_cache* cache, const fattn_cache_batch
   p.causal = causal ? 1 : 0;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.workspace = workspace;
-  CUtensorMap tk, tv;
-  if (!make_cache_map(&tk, cache->k, cache) || !make_cache_map(&tv, cache->v, cache))
+  CUtensorMap tk{}, tv{};  // (4 bits: not used)
+  if (cache->format != FATTN_CACHE_INT4 &&
+      (!make_cache_map(&tk, cache->k, cache) || !make_cache_map(&tv, cache->v, cache)))
     return FATTN_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return debug_post_call(

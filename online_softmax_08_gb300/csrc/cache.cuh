@@ -112,8 +112,7 @@ cudaError_t launch_cache4_append(const CacheParams& c, const TokenView& k, const
 cudaError_t launch_cache4_read(const CacheParams& c, const TokenView& k, const TokenView& v,
                                cudaStream_t stream);
 size_t cache_fwd_workspace(const CacheParams& c, int G, int n_sm);
-// tk, tv: maps of the codes, {bytes of a row, block_size, num_blocks * H}, boxes of 16
-// tokens (4 bits: of 32 where block_size is at least that)
+// tk, tv: maps of the codes, {d, block_size, num_blocks * H}, boxes of 16 tokens (8 bits)
 cudaError_t launch_cache_fwd(const CUtensorMap& tk, const CUtensorMap& tv, const CacheFwdParams& p,
                              int n_sm, cudaStream_t stream);
 int cache_fwd_wide_rows();  // rows per unit of the 256-row kernel
@@ -201,13 +200,32 @@ __device__ __forceinline__ Int4Scale int4_scale(uint32_t e5m2_hi) {
   r.hi = mul_f16x2(r.s, 0xd480d480u);        // -72
   return r;
 }
+// The two constants, in registers and opaque to the compiler, which would load them at every
+// use (an instruction takes one immediate operand; and of (w & mask) | magic it makes two).
+struct Int4Magic {
+  uint32_t m1024, m64;
+  __device__ __forceinline__ Int4Magic() {
+    asm volatile("mov.b32 %0, 0x64006400;" : "=r"(m1024));
+    asm volatile("mov.b32 %0, 0x54005400;" : "=r"(m64));
+  }
+};
+// The lowest (N = 0) or the second code of each half of w, put into the mantissas of `magic`.
+template <int N>
+__device__ __forceinline__ uint32_t nibbles(uint32_t w, uint32_t magic) {
+  uint32_t r;  // (a & b) | c
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;"
+      : "=r"(r)
+      : "r"(w), "n"(N ? 0x00f000f0 : 0x000f000f), "r"(magic));
+  return r;
+}
 // Eight codes, four in each half of w -> (c_i, c_i+4) of i = 0 ... 3 as pairs of fp16.
-__device__ __forceinline__ void int4_values(uint32_t w, const Int4Scale& s, uint32_t (&o)[4]) {
+__device__ __forceinline__ void int4_values(uint32_t w, const Int4Scale& s, const Int4Magic& m,
+                                            uint32_t (&o)[4]) {
   const uint32_t u = w >> 8;
-  o[0] = fma_f16x2((w & 0x000f000fu) | 0x64006400u, s.s, s.lo);
-  o[1] = fma_f16x2((w & 0x00f000f0u) | 0x54005400u, s.s, s.hi);
-  o[2] = fma_f16x2((u & 0x000f000fu) | 0x64006400u, s.s, s.lo);
-  o[3] = fma_f16x2((u & 0x00f000f0u) | 0x54005400u, s.s, s.hi);
+  o[0] = fma_f16x2(nibbles<0>(w, m.m1024), s.s, s.lo);
+  o[1] = fma_f16x2(nibbles<1>(w, m.m64), s.s, s.hi);
+  o[2] = fma_f16x2(nibbles<0>(u, m.m1024), s.s, s.lo);
+  o[3] = fma_f16x2(nibbles<1>(u, m.m64), s.s, s.hi);
 }
 // The scales of a word that append never writes (above 7168, infinite, NaN) as zeros.
 __device__ __forceinline__ uint32_t int4_sane(uint32_t bytes) {

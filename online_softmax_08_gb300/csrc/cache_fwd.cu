@@ -1,5 +1,5 @@
-// cache_fwd.cu -- attention over the paged key/value cache in 8 or 4 bits, few query
-// rows per key/value head (decoding, drafted tokens).
+// cache_fwd.cu -- attention over the paged 8-bit key/value cache, few query rows
+// per key/value head (decoding, drafted tokens).
 //
 // The mathematics.  With codes k, v and scales ks, vs of key j's block, in base 2:
 //   x_j = scale log2(e) ks_j (q . k_j),   O = sum_j 2^x_j vs_j v_j / sum_j 2^x_j.
@@ -56,34 +56,26 @@
 
 #include <algorithm>
 
-#include "cache.cuh"
+#include "cache_split.cuh"
 
 namespace fattn {
 namespace {
 
-constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kOff = 8.f;    // the reference lies this far below the running maximum
-constexpr float kRoom = 15.f;  // and moves when a y exceeds it by more
-constexpr float kFar = 4194304.f;
 constexpr float kWindow = 10.f;    // log2 vs - b of the blocks that share sums
 constexpr float kNothing = -60.f;  // what lies below it is taken as it
-constexpr int kWarps = 4;
 
-template <int D, int NT_, bool I4>
+template <int D, int NT_>
 struct Dec {
   static constexpr int NT = NT_;
   static constexpr int R = 8 * NT;                // query rows per unit
-  static constexpr int PARTS = D == 128 && !I4 ? 1 : 2;  // of 16 keys in a warp's tile
+  static constexpr int PARTS = D == 128 ? 1 : 2;  // of 16 keys in a warp's tile (4 KB with values)
   static constexpr int KEYS = 16 * PARTS;
   static constexpr int CHUNK = kWarps * KEYS;     // keys per CTA step
-  static constexpr int ROW = I4 ? D / 2 : D;      // bytes of a key's or value's codes
-  static constexpr int PART = 16 * ROW;           // of 16 keys: one TMA box
-  static constexpr int TILE = KEYS * ROW;
-  static constexpr int PART_SCL = I4 ? D : 0;     // bytes of 16 keys' scales
-  static constexpr int TILE_SCL = PARTS * PART_SCL;
-  static constexpr int STAGE = 2 * TILE + 2 * TILE_SCL;  // keys and values, scales behind both
+  static constexpr int PART = 16 * D;             // bytes of 16 keys or values: one TMA box
+  static constexpr int TILE = KEYS * D;
+  static constexpr int STAGE = 2 * TILE;          // keys and values
   // ring slots per warp, CTAs per SM: as much as the shared memory and registers take
-  static constexpr int ST = I4 && D == 64 ? 6 : D == 64 && NT == 1 ? 4 : D == 128 && NT == 2 ? 4 : 3;
+  static constexpr int ST = D == 64 && NT == 1 ? 4 : D == 128 && NT == 2 ? 4 : 3;
   static constexpr int OFF_RED = kWarps * ST * STAGE;
   static constexpr int OFF_SCL = OFF_RED + kWarps * R * D * 4;  // [warps][ST] scales of a tile
   static constexpr int OFF_STAT = OFF_SCL + kWarps * ST * 16;
@@ -94,103 +86,11 @@ struct Dec {
 
 constexpr int kWideMerge = 8;  // merge blocks per CTA of the 256-row kernel
 
-// A position in the list of all chunks: chunk ch of unit (sequence b, head h, row
-// block rb).  Sequence b has H x nrb units of nch chunks (none: nch = 0).
-struct Cursor {
-  int b, h, rb, ch;
-  int nch, nrb;
-  CacheSeq seq;
-};
-template <typename C>
-__device__ __forceinline__ void set_seq(const CacheFwdParams& p, int b, int row0, int end,
-                                        int len, Cursor* c) {
-  c->b = b;
-  c->nch = c->nrb = 0;
-  if (!cache_seq(p.c, row0, end, len, &c->seq)) {
-    if (p.c.err) atomicCAS(p.c.err, 0u, (unsigned)ERR_SITE_CACHE_FWD);
-    return;
-  }
-  const int rows = c->seq.n * p.G;
-  if (rows == 0 || rows > p.narrow_rows) return;  // (the other kernel's)
-  c->nch = max(1, (c->seq.len + C::CHUNK - 1) / C::CHUNK);
-  c->nrb = (rows + C::R - 1) / C::R;
-}
-template <typename C>
-__device__ __forceinline__ void load_seq(const CacheFwdParams& p, int b, Cursor* c) {
-  set_seq<C>(p, b, p.c.cu_seqlens[b], p.c.cu_seqlens[b + 1], p.c.lens[b], c);
-}
-template <typename C>
-__device__ __forceinline__ void advance(const CacheFwdParams& p, Cursor* c, int by) {
-  c->ch += by;
-  while (c->ch >= c->nch) {
-    c->ch -= c->nch;
-    if (++c->rb < c->nrb) continue;
-    c->rb = 0;
-    if (++c->h < p.c.H) continue;
-    c->h = 0;
-    int b = c->b;
-    do {
-      if (++b >= p.c.B) {
-        c->b = b;
-        c->nch = 0x7fffffff;  // behind the last chunk
-        return;
-      }
-      load_seq<C>(p, b, c);
-    } while (c->nch == 0);
-  }
-}
-
-__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                        uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
-  uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
-  return r;
-}
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ uint4 ld_shared_v4(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint2 ld_shared_v2(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint32_t ld_shared_u16(uint32_t a) {
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint32_t ld_shared_u8(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
-  return v;
-}
-template <int D, int FMT, int NT>
-__global__ void __launch_bounds__(128, Dec<D, NT, FMT == FMT_INT4>::CTAS)
+template <int D, bool E5M2, int NT>
+__global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
     cache_fwd_kernel(const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const CacheFwdParams p) {
-  constexpr bool I4 = FMT == FMT_INT4, E5M2 = FMT == FMT_E5M2;
-  using C = Dec<D, NT, I4>;
+  using C = Dec<D, NT>;
   constexpr int R = C::R;
   constexpr int KW = D / 16;   // 4-byte words of a key that a lane holds (16 values per step)
   constexpr int VW = D / 32;   // 4-byte words of a value row that a lane holds
@@ -229,64 +129,10 @@ __global__ void __launch_bounds__(128, Dec<D, NT, FMT == FMT_INT4>::CTAS)
   }
 
   // ---------------------------------------------------------------- this CTA's share
-  const int B = p.c.B, G = p.G;
-  auto chunks = [&](const Cursor& c) { return (long long)c.nch * c.nrb * p.c.H; };
-  Cursor cur{};
-  long long mine = 0, total = 0;  // chunks of sequence `lane` of the last group, and of all
-  for (int b0 = 0; b0 < B; b0 += 32) {
-    mine = 0;
-    if (b0 + lane < B) {
-      if (b0 == 0)
-        set_seq<C>(p, lane, first_row0, first_end, first_len, &cur);
-      else
-        load_seq<C>(p, b0 + lane, &cur);
-      mine = chunks(cur);
-    }
-    total += mine;
-  }
-#pragma unroll
-  for (int w = 16; w > 0; w >>= 1) total += __shfl_xor_sync(0xffffffffu, total, w);
-  // (a 64-bit division takes ten times as long)
-  const long long share = total < 0x7fffffff ? ((unsigned)total + gridDim.x - 1) / gridDim.x
-                                             : (total + gridDim.x - 1) / gridDim.x;
-  const long long lo = blockIdx.x * share;
-  const int F = (int)max(0LL, min(share, total - lo));  // chunks of this CTA
-  if (F > 0) {
-    long long before = 0;
-    for (int b0 = 0; b0 < B; b0 += 32) {
-      if (B > 32) {
-        mine = 0;
-        if (b0 + lane < B) {
-          load_seq<C>(p, b0 + lane, &cur);
-          mine = chunks(cur);
-        }
-      }
-      long long upto = mine;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const long long o = __shfl_up_sync(0xffffffffu, upto, d);
-        if (lane >= d) upto += o;
-      }
-      const unsigned past = __ballot_sync(0xffffffffu, before + upto > lo);
-      if (past) {
-        const int src = __ffs(past) - 1;
-        const long long pos = lo - __shfl_sync(0xffffffffu, before + upto - mine, src);
-        cur.b = b0 + src;
-        cur.nch = __shfl_sync(0xffffffffu, cur.nch, src);
-        cur.nrb = __shfl_sync(0xffffffffu, cur.nrb, src);
-        cur.seq.row0 = __shfl_sync(0xffffffffu, cur.seq.row0, src);
-        cur.seq.n = __shfl_sync(0xffffffffu, cur.seq.n, src);
-        cur.seq.len = __shfl_sync(0xffffffffu, cur.seq.len, src);
-        const unsigned unit = pos < 0x7fffffff ? (unsigned)pos / (unsigned)cur.nch
-                                               : (unsigned)(pos / cur.nch);
-        cur.ch = (int)(pos - (long long)unit * cur.nch);
-        cur.h = (int)(unit / (unsigned)cur.nrb);
-        cur.rb = (int)(unit % (unsigned)cur.nrb);
-        break;
-      }
-      before += __shfl_sync(0xffffffffu, upto, 31);
-    }
-  }
+  const int G = p.G;
+  Cursor cur;
+  long long share;
+  const int F = find_share<C>(p, first_row0, first_end, first_len, &cur, &share);
   Record* records = reinterpret_cast<Record*>(p.workspace);
   float* part_lse = reinterpret_cast<float*>(static_cast<char*>(p.workspace) +
                                              (((size_t)gridDim.x * sizeof(Record) + 255) & ~255u));
@@ -319,10 +165,8 @@ __global__ void __launch_bounds__(128, Dec<D, NT, FMT == FMT_INT4>::CTAS)
           if (p.c.err) atomicCAS(p.c.err, 0u, (unsigned)ERR_SITE_CACHE_FWD + 1);
         } else {
           r.slice[i] = page * p.c.H + at.h;
-          if constexpr (!I4) {
-            r.ks[i] = p.c.k_scale[r.slice[i]];  // not waited for here
-            r.vs[i] = p.c.v_scale[r.slice[i]];
-          }
+          r.ks[i] = p.c.k_scale[r.slice[i]];  // not waited for here
+          r.vs[i] = p.c.v_scale[r.slice[i]];
         }
       }
     return r;
@@ -356,40 +200,20 @@ __global__ void __launch_bounds__(128, Dec<D, NT, FMT == FMT_INT4>::CTAS)
           const uint32_t slot = issued % C::ST;
           const uint32_t bar = bar0 + 8u * slot, dst = ring + slot * C::STAGE;
           const bool l0 = info.slice[0] >= 0, l1 = C::PARTS == 2 && info.slice[1] >= 0;
-          if constexpr (I4) {
-            // the codes through the tensor maps, swizzled, the scales as they lie; a block of
-            // 32 tokens or more holds the whole tile, of which one copy takes both parts
-            const bool both = bs >= 32;
-            mbar_arrive_expect_tx(bar, (uint32_t)(both ? 2 : l0 + l1) * 2u *
-                                           (C::PART + C::PART_SCL));
-#pragma unroll
-            for (int i = 0; i < C::PARTS; ++i) {
-              if (info.slice[i] < 0 || (i > 0 && both)) continue;
-              const int row = (info.row + 16 * i) & (bs - 1);
-              const long long scl = (((long long)info.slice[i] << p.c.block_log2) + row) * (D / 16);
-              const uint32_t ds = dst + 2 * C::TILE + i * C::PART_SCL;
-              const uint32_t bytes = both ? 2 * C::PART_SCL : C::PART_SCL;
-              tma_load_3d(dst + i * C::PART, &tm_k, bar, 0, row, info.slice[i]);
-              tma_load_3d(dst + C::TILE + i * C::PART, &tm_v, bar, 0, row, info.slice[i]);
-              bulk_load(ds, p.c.k_scale4 + scl, bytes, bar);
-              bulk_load(ds + C::TILE_SCL, p.c.v_scale4 + scl, bytes, bar);
-            }
-          } else {
-            uint32_t v0 = __float_as_uint(info.vs[0]), v1 = __float_as_uint(info.vs[1]);
-            if (!l1) v1 = v0;  // a part without keys takes the other one's value scale
-            if (!l0) v0 = v1;
-            st_shared_v4(scl0 + slot * 16u, __float_as_uint(info.ks[0]),
-                         __float_as_uint(info.ks[1]), v0, v1);
-            mbar_arrive_expect_tx(bar, (uint32_t)(l0 + l1) * 2u * C::PART);
-            if (l0) {
-              tma_load_3d(dst, &tm_k, bar, 0, info.row, info.slice[0]);
-              tma_load_3d(dst + C::TILE, &tm_v, bar, 0, info.row, info.slice[0]);
-            }
-            if (l1) {
-              const int row = (info.row + 16) & (bs - 1);
-              tma_load_3d(dst + C::PART, &tm_k, bar, 0, row, info.slice[1]);
-              tma_load_3d(dst + C::TILE + C::PART, &tm_v, bar, 0, row, info.slice[1]);
-            }
+          uint32_t v0 = __float_as_uint(info.vs[0]), v1 = __float_as_uint(info.vs[1]);
+          if (!l1) v1 = v0;  // a part without keys takes the other one's value scale
+          if (!l0) v0 = v1;
+          st_shared_v4(scl0 + slot * 16u, __float_as_uint(info.ks[0]), __float_as_uint(info.ks[1]),
+                       v0, v1);
+          mbar_arrive_expect_tx(bar, (uint32_t)(l0 + l1) * 2u * C::PART);
+          if (l0) {
+            tma_load_3d(dst, &tm_k, bar, 0, info.row, info.slice[0]);
+            tma_load_3d(dst + C::TILE, &tm_v, bar, 0, info.row, info.slice[0]);
+          }
+          if (l1) {
+            const int row = (info.row + 16) & (bs - 1);
+            tma_load_3d(dst + C::PART, &tm_k, bar, 0, row, info.slice[1]);
+            tma_load_3d(dst + C::TILE + C::PART, &tm_v, bar, 0, row, info.slice[1]);
           }
         }
         ++issued;
@@ -416,17 +240,8 @@ __global__ void __launch_bounds__(128, Dec<D, NT, FMT == FMT_INT4>::CTAS)
   // lane's value columns are piece (g & 1) * 4 + g / 2.  d = 64: rows of 64 bytes,
   // pieces swizzled by (row / 2) & 3; keys in order, and lanes of odd t load the
   // odd one of a pair of value rows first.
-  // 4 bits: a lane's share of a key is a quarter of its channels, of a value row an eighth.
-  // d = 128: rows of 64 bytes, pieces swizzled by (row / 2) & 3; d = 64: of 32, by
-  // (row / 4) & 1.  With matrix row 2 i + e for the key of krow4 below, the rows of a load
-  // phase touch different banks, those of the keys' products (two or four g, all t) and
-  // those of the values' (one e, all t) alike.
-  auto krow4 = [](int i, int e) {
-    return D == 128 ? ((i ^ e) & 1) | e << 1 | (i >> 1) << 2 : (i ^ e << 1) | e << 2;
-  };
-  const int krow = I4 ? krow4(g >> 1, g & 1) : D == 128 ? ((g & 1) << 2 | g >> 1) : g;
-  const int vcol = I4 ? g * (D / 8)
-                      : D == 128 ? ((g & 1) << 2 | g >> 1) * 16 : g * 8;  // first column
+  const int krow = D == 128 ? ((g & 1) << 2 | g >> 1) : g;
+  const int vcol = D == 128 ? ((g & 1) << 2 | g >> 1) * 16 : g * 8;  // first column
 
   // Sums that are put aside (rare): a normalised O in the warp's part of `red`, each lane its
   // own elements, and a log2-sum-exp in `stat`.  Joined with the running sums, row by row:
@@ -500,8 +315,7 @@ __global__ void __launch_bounds__(128, Dec<D, NT, FMT == FMT_INT4>::CTAS)
                               (long long)(h * G + p.by_G.mod(i)) * p.q.sh;
 #pragma unroll
           for (int j = 0; j < D / 32; ++j)
-            qraw[nt][j] = *reinterpret_cast<const uint4*>(
-                I4 ? q + t * (D / 4) + j * 8 : q + (j >> 1) * 64 + t * 16 + (j & 1) * 8);
+            qraw[nt][j] = *reinterpret_cast<const uint4*>(q + (j >> 1) * 64 + t * 16 + (j & 1) * 8);
         }
       }
       if (f == 0) issue(0, false);  // while q is on its way
@@ -529,14 +343,7 @@ __global__ void __launch_bounds__(128, Dec<D, NT, FMT == FMT_INT4>::CTAS)
         const float back = __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
         for (int w = 0; w < KW; ++w) {
-          const uint32_t* x = &v[w >> 1].x + (I4 ? w & 1 : (w & 1) * 2);
-          if constexpr (I4) {  // channels i and i + 4 of eight, as int4_values gives them
-            qf[nt][w][0] = pack_f16x2(__uint_as_float(x[0] << 16) * mul,
-                                      __uint_as_float(x[2] << 16) * mul);
-            qf[nt][w][1] = pack_f16x2(__uint_as_float(x[0] & 0xffff0000u) * mul,
-                                      __uint_as_float(x[2] & 0xffff0000u) * mul);
-            continue;
-          }
+          const uint32_t* x = &v[w >> 1].x + (w & 1) * 2;
           qf[nt][w][0] = pack_f16x2(__uint_as_float(x[0] << 16) * mul,
                                     __uint_as_float(x[0] & 0xffff0000u) * mul);
           qf[nt][w][1] = pack_f16x2(__uint_as_float(x[1] << 16) * mul,
@@ -558,7 +365,7 @@ __global__ void __launch_bounds__(128, Dec<D, NT, FMT == FMT_INT4>::CTAS)
 #pragma unroll
           for (int i = 0; i < 4; ++i) acc[mt][nt][i] = 0.f;
       first_live = true;
-      lvb = I4 ? (float)kInt4UnitLog2 : 0.f;
+      lvb = 0.f;
       parked = false;
     }
 
@@ -572,24 +379,21 @@ __global__ void __launch_bounds__(128, Dec<D, NT, FMT == FMT_INT4>::CTAS)
         ok = __all_sync(0xffffffffu, mbar_wait(bar0 + 8u * slot, (done / C::ST) & 1u, wctx,
                                                ERR_SITE_CACHE_FWD + 2));
         if (ok) {
-          float ks[2] = {kInt4Unit, kInt4Unit}, lv[2] = {0.f, 0.f};
-          if constexpr (!I4) {
-            const uint4 sc = ld_shared_v4(scl0 + slot * 16u);
-            ks[0] = __uint_as_float(sc.x), ks[1] = __uint_as_float(sc.y);
-            lv[0] = lg2(__uint_as_float(sc.z)), lv[1] = lg2(__uint_as_float(sc.w));
-            if (first_live) lvb = lv[0];
-            first_live = false;
-            lv[0] -= lvb, lv[1] -= lvb;
-            const float far = C::PARTS == 2 ? fmaxf(fabsf(lv[0]), fabsf(lv[1])) : fabsf(lv[0]);
-            if (__builtin_expect(far > kWindow || (C::PARTS == 2 && only != 0), 0)) {
-              if (!calm) {  // rare, warp-uniform
-                event = true;
-                break;
-              }
-              if (only == 1) on[1] = false;
-              if (only == 2) on[0] = false;
-              lv[0] = lv[1] = calm_lv;
+          const uint4 sc = ld_shared_v4(scl0 + slot * 16u);
+          const float ks[2] = {__uint_as_float(sc.x), __uint_as_float(sc.y)};
+          float lv[2] = {lg2(__uint_as_float(sc.z)), lg2(__uint_as_float(sc.w))};
+          if (first_live) lvb = lv[0];
+          first_live = false;
+          lv[0] -= lvb, lv[1] -= lvb;
+          const float far = C::PARTS == 2 ? fmaxf(fabsf(lv[0]), fabsf(lv[1])) : fabsf(lv[0]);
+          if (__builtin_expect(far > kWindow || (C::PARTS == 2 && only != 0), 0)) {
+            if (!calm) {  // rare, warp-uniform
+              event = true;
+              break;
             }
+            if (only == 1) on[1] = false;
+            if (only == 2) on[0] = false;
+            lv[0] = lv[1] = calm_lv;
           }
           const uint32_t ka = ring + slot * C::STAGE, va = ka + C::TILE;
           const bool masked = key0 + C::KEYS > lim_lo;  // some row does not see all of it
@@ -602,63 +406,28 @@ __global__ void __launch_bounds__(128, Dec<D, NT, FMT == FMT_INT4>::CTAS)
 #pragma unroll
               for (int i = 0; i < 4; ++i) s[pt][nt][i] = on[pt] ? 0.f : -INFINITY;
             if (!on[pt]) continue;
-            if constexpr (I4) {
-              constexpr int W = D / 32;  // words of eight codes: a quarter of a key
-              uint32_t a[2][W];          // keys krow and krow + 8
-              Int4Scale ksc[2][W / 2];   // of their groups of 16
-              const uint32_t at = ka + pt * C::PART, sa = ka + 2 * C::TILE + pt * C::PART_SCL;
+#pragma unroll
+            for (int half = 0; half < D / 64; ++half) {
+              uint32_t a[2][4];  // keys krow and krow + 8: 16 bytes
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
                 const int row = krow + 8 * i;
-                if constexpr (D == 128) {
-                  const uint4 x = ld_shared_v4(at + row * 64 + ((t ^ ((row >> 1) & 3)) << 4));
-                  a[i][0] = x.x, a[i][1] = x.y, a[i][W - 2] = x.z, a[i][W - 1] = x.w;
-                  const uint32_t s2 = ld_shared_u16(sa + row * 8 + t * 2);
-                  ksc[i][0] = int4_scale(__byte_perm(s2, 0u, 0x0404u));
-                  ksc[i][W / 2 - 1] = int4_scale(__byte_perm(s2, 0u, 0x1414u));
-                } else {
-                  const uint2 x = ld_shared_v2(at + row * 32 + (((t >> 1) ^ ((row >> 2) & 1)) << 4) +
-                                               (t & 1) * 8);
-                  a[i][0] = x.x, a[i][1] = x.y;
-                  ksc[i][0] = int4_scale(__byte_perm(ld_shared_u8(sa + row * 4 + t), 0u, 0x0404u));
-                }
+                const int piece = half * 4 + t;
+                const uint32_t at = ka + pt * C::PART;
+                const uint32_t addr = D == 128 ? at + row * 128 + ((piece ^ (row & 7)) << 4)
+                                               : at + row * 64 + ((piece ^ ((row >> 1) & 3)) << 4);
+                const uint4 x = ld_shared_v4(addr);
+                a[i][0] = x.x, a[i][1] = x.y, a[i][2] = x.z, a[i][3] = x.w;
               }
 #pragma unroll
-              for (int w = 0; w < W; ++w) {
-                uint32_t lo[4], hi[4];
-                int4_values(a[0][w], ksc[0][w >> 1], lo);
-                int4_values(a[1][w], ksc[1][w >> 1], hi);
+              for (int w = 0; w < 4; ++w) {
+                uint32_t a0, a1, a2, a3;
+                codes4_to_f16<E5M2>(a[0][w], a0, a2);
+                codes4_to_f16<E5M2>(a[1][w], a1, a3);
 #pragma unroll
-                for (int m = 0; m < 2; ++m)
-#pragma unroll
-                  for (int nt = 0; nt < NT; ++nt)
-                    mma_f16(s[pt][nt], lo[2 * m], hi[2 * m], lo[2 * m + 1], hi[2 * m + 1],
-                            qf[nt][2 * w + m][0], qf[nt][2 * w + m][1]);
-              }
-            } else {
-#pragma unroll
-              for (int half = 0; half < D / 64; ++half) {
-                uint32_t a[2][4];  // keys krow and krow + 8: 16 bytes
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                  const int row = krow + 8 * i;
-                  const int piece = half * 4 + t;
-                  const uint32_t at = ka + pt * C::PART;
-                  const uint32_t addr = D == 128 ? at + row * 128 + ((piece ^ (row & 7)) << 4)
-                                                 : at + row * 64 + ((piece ^ ((row >> 1) & 3)) << 4);
-                  const uint4 x = ld_shared_v4(addr);
-                  a[i][0] = x.x, a[i][1] = x.y, a[i][2] = x.z, a[i][3] = x.w;
-                }
-#pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                  uint32_t a0, a1, a2, a3;
-                  codes4_to_f16<E5M2>(a[0][w], a0, a2);
-                  codes4_to_f16<E5M2>(a[1][w], a1, a3);
-#pragma unroll
-                  for (int nt = 0; nt < NT; ++nt)
-                    mma_f16(s[pt][nt], a0, a1, a2, a3, qf[nt][half * 4 + w][0],
-                            qf[nt][half * 4 + w][1]);
-                }
+                for (int nt = 0; nt < NT; ++nt)
+                  mma_f16(s[pt][nt], a0, a1, a2, a3, qf[nt][half * 4 + w][0],
+                          qf[nt][half * 4 + w][1]);
               }
             }
             const int k0 = key0 + pt * 16 + krow, k1 = k0 + 8;
@@ -729,46 +498,6 @@ __global__ void __launch_bounds__(128, Dec<D, NT, FMT == FMT_INT4>::CTAS)
             }
             // value rows of this lane: keys of matrix rows 2t, 2t + 1, 2t + 8, 2t + 9
             const int first = key0 + pt * 16;
-            if constexpr (I4) {
-              constexpr int W = D / 64;  // words of eight codes: an eighth of a value row
-              const uint32_t at = va + pt * C::PART;
-              const uint32_t sa = ka + 2 * C::TILE + C::TILE_SCL + pt * C::PART_SCL;
-              uint32_t v[4][W], sc[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int row = krow4(t, i & 1) + 8 * (i >> 1);
-                if constexpr (D == 128) {
-                  const uint2 x = ld_shared_v2(at + row * 64 + (((g >> 1) ^ ((row >> 1) & 3)) << 4) +
-                                               (g & 1) * 8);
-                  v[i][0] = x.x, v[i][W - 1] = x.y;
-                  sc[i] = ld_shared_u8(sa + row * 8 + g);
-                } else {
-                  v[i][0] = ld_shared_u32(at + row * 32 + (((g >> 2) ^ ((row >> 2) & 1)) << 4) +
-                                          (g & 3) * 4);
-                  sc[i] = ld_shared_u8(sa + row * 4 + (g >> 1));
-                }
-                // rows that no query sees hold anything; a scale that is none must not reach
-                // the queries that do not see its row
-                if (masked) sc[i] = first + row >= lim_hi ? 0u : int4_sane(sc[i]);
-              }
-              const Int4Scale s0 = int4_scale(__byte_perm(sc[0], sc[1], 0x4101u));
-              const Int4Scale s1 = int4_scale(__byte_perm(sc[2], sc[3], 0x4101u));
-#pragma unroll
-              for (int j = 0; j < W; ++j)
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                  uint32_t lo[4], hi[4];  // keys 2t, 2t + 1 and 2t + 8, 2t + 9
-                  int4_values(__byte_perm(v[0][j], v[1][j], half ? 0x7632u : 0x5410u), s0, lo);
-                  int4_values(__byte_perm(v[2][j], v[3][j], half ? 0x7632u : 0x5410u), s1, hi);
-#pragma unroll
-                  for (int m = 0; m < 2; ++m)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                      mma_f16(acc[j * 4 + half * 2 + m][nt], lo[2 * m], lo[2 * m + 1], hi[2 * m],
-                              hi[2 * m + 1], pf[nt][0], pf[nt][1]);
-                }
-              continue;
-            }
             auto value_row = [&](int i) {
               return D == 128 ? t + 4 * i : 2 * t + ((i & 1) ^ odd) + 8 * (i >> 1);
             };
@@ -890,8 +619,6 @@ __global__ void __launch_bounds__(128, Dec<D, NT, FMT == FMT_INT4>::CTAS)
     }
 
     // ---------------------------------------------------------------- the unit (or piece) ends
-    const int ch = cur.ch;
-    const bool unit_ends = ch == cur.nch - 1;
     if (__builtin_expect(parked, 0)) {  // rare: all of it as if it were one key's
       float keep[NT][2], add[NT][2];
       join(keep, add, ref);
@@ -909,106 +636,7 @@ __global__ void __launch_bounds__(128, Dec<D, NT, FMT == FMT_INT4>::CTAS)
         for (int i = 0; i < 2; ++i) lsum[nt][i] = g == 0 && ref[nt][i] != -INFINITY ? 1.f : 0.f;
       lvb = 0.f;
     }
-    // this warp's rows: normalised result and log2-sum-exp
-    float mine[NT][2], fac[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float l = lsum[nt][i];
-#pragma unroll
-        for (int w = 4; w < 32; w <<= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
-        lsum[nt][i] = l;
-        mine[nt][i] = l == 0.f ? -INFINITY : ref[nt][i] + lg2(l);
-        if (g == 0) stat[warp * R + nt * 8 + 2 * t + i] = mine[nt][i];
-      }
-    __syncthreads();
-    float top[NT][2], sum[NT][2];
-    const float up = ex2(lvb);
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = nt * 8 + 2 * t + i;
-        float m = -INFINITY, z = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) m = fmaxf(m, stat[w * R + r]);
-        const float mm = m == -INFINITY ? 0.f : m;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) z += ex2(stat[w * R + r] - mm);
-        top[nt][i] = m;
-        sum[nt][i] = z;
-        fac[nt][i] = lsum[nt][i] == 0.f ? 0.f : ex2(mine[nt][i] - mm) / (z * lsum[nt][i]);
-      }
-    // the warps' results side by side; 16-byte columns are permuted so that the lanes
-    // of a store phase (two g, four t) touch different banks
-    auto column = [&](int r, int c4) {
-      const int k = r >> 1;  // t of the lane that holds row r
-      return D == 128 ? c4 ^ (((c4 >> 4) & 1) << 2 | (k & 3))
-                      : c4 ^ ((k & 1) << 2 | ((k >> 1) & 1));
-    };
-    float4* red4 = reinterpret_cast<float4*>(red);
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = nt * 8 + 2 * t + i;
-#pragma unroll
-        for (int j = 0; j < VW; ++j)
-          red4[(warp * R + r) * (D / 4) + column(r, vcol / 4 + j)] = make_float4(
-              acc[2 * j][nt][i] * fac[nt][i] * up, acc[2 * j][nt][i + 2] * fac[nt][i] * up,
-              acc[2 * j + 1][nt][i] * fac[nt][i] * up,
-              acc[2 * j + 1][nt][i + 2] * fac[nt][i] * up);
-      }
-    __syncthreads();
-    const bool starts_here = f > ch;  // the unit's chunk 0 is in this share
-    const bool whole = starts_here && unit_ends;
-    const int slot = starts_here ? 1 : 0;
-    if (warp == 0 && g == 0) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int r = nt * 8 + 2 * t + i;
-          const float L = top[nt][i] == -INFINITY && sum[nt][i] == 0.f
-                              ? -INFINITY
-                              : (top[nt][i] + lg2(sum[nt][i])) * kLn2;
-          if (r < rows) {
-            if (whole) {
-              const int i0 = rb * R + r;
-              p.lse[(long long)(h * G + p.by_G.mod(i0)) * p.c.total + cur.seq.row0 +
-                    p.by_G.div(i0)] = L;
-            } else {
-              part_lse[((size_t)blockIdx.x * 2 + slot) * R + r] = L;
-            }
-          }
-        }
-    }
-    for (int x = threadIdx.x; x < rows * (D / 4); x += 128) {
-      const int r = x / (D / 4), c4 = x % (D / 4);
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float4 y = red4[(w * R + r) * (D / 4) + column(r, c4)];
-        o.x += y.x, o.y += y.y, o.z += y.z, o.w += y.w;
-      }
-      if (whole) {
-        const int i0 = rb * R + r;
-        *reinterpret_cast<uint2*>(p.o.p + (long long)(cur.seq.row0 + p.by_G.div(i0)) * p.o.st +
-                                  (long long)(h * G + p.by_G.mod(i0)) * p.o.sh + c4 * 4) =
-            make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
-      } else {
-        reinterpret_cast<float4*>(part_o)[(((size_t)blockIdx.x * 2 + slot) * R + r) * (D / 4) +
-                                          c4] = o;
-      }
-    }
-    if (starts_here && !unit_ends) {  // later CTAs hold the rest
-      rec.parts = 1 + (cur.nch - 1 - ch + (int)share - 1) / (int)share;
-      rec.rows = rows;
-      rec.h = h;
-      rec.row0 = cur.seq.row0;
-      rec.first_row = rb * R;
-    }
+    end_unit<C, D>(p, cur, f, share, rows, acc, ref, lsum, lvb, vcol, red, stat, part_lse, part_o, &rec);
     __syncwarp();
     if (lane == 0) mbar_arrive(red_bar);
     ++ended;
@@ -1102,49 +730,47 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-template <int D, int FMT, int NT>
-cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const CacheFwdParams& p, int n_sm,
-                   bool wide, cudaStream_t stream) {
-  using C = Dec<D, NT, FMT == FMT_INT4>;
-  static_assert(C::CTAS * (C::SMEM + 1024) <= 233472, "shared memory of the CTAs sharing an SM");
-  static unsigned long long prepared[64];
-  const cudaError_t e = prepare_once(prepared, [] {
-    return cudaFuncSetAttribute(cache_fwd_kernel<D, FMT, NT>,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-  });
-  if (e != cudaSuccess) return e;
-  const unsigned grid = (unsigned)(n_sm * C::CTAS);
-  // each kernel may start while the last CTAs of the one before finish; what depends
-  // on its results is waited for on the device
+// Joins the pieces that the kernel for few rows (`grid` CTAs, R rows per unit) and the
+// 256-row kernel left.
+cudaError_t launch_merge(const CacheFwdParams& p, int grid, int R, int n_sm, bool wide,
+                         cudaStream_t stream) {
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(128);
-  cfg.dynamicSmemBytes = C::SMEM;
-  cfg.stream = stream;
-  if (wide) {
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-  }
-  const cudaError_t r = cudaLaunchKernelEx(&cfg, cache_fwd_kernel<D, FMT, NT>, tk, tv, p);
-  if (r != cudaSuccess) return r;
-  cfg.gridDim = dim3(grid + (wide ? kWideMerge * n_sm : 0));
+  cfg.gridDim = dim3((unsigned)(grid + (wide ? kWideMerge * n_sm : 0)));
   cfg.blockDim = dim3(256);
-  cfg.dynamicSmemBytes = 0;
+  cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cache_merge_kernel<D>, p, (int)grid, (int)C::R, n_sm,
-                            cache_fwd_wide_rows());
+  return p.c.d == 128
+             ? cudaLaunchKernelEx(&cfg, cache_merge_kernel<128>, p, grid, R, n_sm, cache_fwd_wide_rows())
+             : cudaLaunchKernelEx(&cfg, cache_merge_kernel<64>, p, grid, R, n_sm, cache_fwd_wide_rows());
 }
 
-template <int D, int FMT>
+template <int D, bool E5M2, int NT>
+cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const CacheFwdParams& p, int n_sm,
+                   bool wide, cudaStream_t stream) {
+  using C = Dec<D, NT>;
+  static_assert(C::CTAS * (C::SMEM + 1024) <= 233472, "shared memory of the CTAs sharing an SM");
+  static unsigned long long prepared[64];
+  const cudaError_t e = prepare_once(prepared, [] {
+    return cudaFuncSetAttribute(cache_fwd_kernel<D, E5M2, NT>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  });
+  if (e != cudaSuccess) return e;
+  const int grid = n_sm * C::CTAS;
+  const cudaError_t r =
+      launch_split(cache_fwd_kernel<D, E5M2, NT>, grid, C::SMEM, wide, stream, tk, tv, p);
+  return r != cudaSuccess ? r : launch_merge(p, grid, C::R, n_sm, wide, stream);
+}
+
+template <int D, bool E5M2>
 cudaError_t launch_rows(const CUtensorMap& tk, const CUtensorMap& tv, const CacheFwdParams& p,
                         int n_sm, bool wide, cudaStream_t stream) {
   const long long rows = (long long)p.c.max_seqlen * p.G;
-  return rows <= 8 ? launch<D, FMT, 1>(tk, tv, p, n_sm, wide, stream)
-                   : launch<D, FMT, 2>(tk, tv, p, n_sm, wide, stream);
+  return rows <= 8 ? launch<D, E5M2, 1>(tk, tv, p, n_sm, wide, stream)
+                   : launch<D, E5M2, 2>(tk, tv, p, n_sm, wide, stream);
 }
 
 // Bytes of the records, LSE and O of `ctas` CTAs with R rows per unit.
@@ -1152,9 +778,9 @@ size_t pieces_bytes(size_t ctas, int R, int d) {
   return ((ctas * sizeof(Record) + 255) & ~(size_t)255) +
          ((ctas * 2 * R + 63) & ~(size_t)63) * 4 + ctas * 2 * R * d * 4;
 }
-size_t narrow_bytes(int d, int n_sm) {  // the larger of the two variants
-  return std::max(pieces_bytes((size_t)n_sm * Dec<128, 1, false>::CTAS, Dec<128, 1, false>::R, d),
-                  pieces_bytes((size_t)n_sm * Dec<64, 2, false>::CTAS, Dec<64, 2, false>::R, d));
+size_t narrow_bytes(int d, int n_sm) {  // the larger of the two variants (4 bits: the same)
+  return std::max(pieces_bytes((size_t)n_sm * Dec<128, 1>::CTAS, Dec<128, 1>::R, d),
+                  pieces_bytes((size_t)n_sm * Dec<64, 2>::CTAS, Dec<64, 2>::R, d));
 }
 // The most query rows per key/value head (tokens x grouped heads) of a sequence that
 // stays with the kernel above.  From 33 rows on it reads the keys three times and
@@ -1198,18 +824,16 @@ cudaError_t launch_cache_fwd(const CUtensorMap& tk, const CUtensorMap& tv,
     const cudaError_t e = launch_cache_fwd_wide(p, stream);
     if (e != cudaSuccess) return e;
   }
-  const bool d128 = p.c.d == 128;
-  switch (p.c.format) {
-    case FMT_E4M3:
-      return d128 ? launch_rows<128, FMT_E4M3>(tk, tv, p, n_sm, wide, stream)
-                  : launch_rows<64, FMT_E4M3>(tk, tv, p, n_sm, wide, stream);
-    case FMT_E5M2:
-      return d128 ? launch_rows<128, FMT_E5M2>(tk, tv, p, n_sm, wide, stream)
-                  : launch_rows<64, FMT_E5M2>(tk, tv, p, n_sm, wide, stream);
-    default:
-      return d128 ? launch_rows<128, FMT_INT4>(tk, tv, p, n_sm, wide, stream)
-                  : launch_rows<64, FMT_INT4>(tk, tv, p, n_sm, wide, stream);
+  if (p.c.format == FMT_INT4) {
+    int grid, R;
+    const cudaError_t e = launch_cache4_fwd(p, n_sm, wide, stream, &grid, &R);
+    return e != cudaSuccess ? e : launch_merge(p, grid, R, n_sm, wide, stream);
   }
+  if (p.c.d == 128)
+    return p.c.format ? launch_rows<128, true>(tk, tv, p, n_sm, wide, stream)
+                      : launch_rows<128, false>(tk, tv, p, n_sm, wide, stream);
+  return p.c.format ? launch_rows<64, true>(tk, tv, p, n_sm, wide, stream)
+                    : launch_rows<64, false>(tk, tv, p, n_sm, wide, stream);
 }
 
 }  // namespace fattn

@@ -654,6 +654,7 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
 #pragma unroll
       for (int pc = 0; pc < 2; ++pc) at[pc] = __shfl_sync(0xffffffffu, set.piece, (j & 15) * 2 + pc);
     };
+    const Int4Magic magic;
     Info now{-1, 1.f, -INFINITY, 0.f}, next = now;
     int page = 0;
     bool ok = true;
@@ -735,7 +736,7 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
               for (int y = 0; y < 4; ++y) {
                 if ((y & 1) == 0) s = int4_scale(__byte_perm(scl[value][pc][x], 0u, y ? 0x1414u : 0x0404u));
                 uint32_t o[4];
-                int4_values(w[y], s, o);
+                int4_values(w[y], s, magic, o);
                 const uint32_t c = (uint32_t)(((col16 & 1) * 4 + y) ^ ((row + row4) & 7));
                 st_shared_v4(line + (c << 4), o[0], o[1], o[2], o[3]);
               }

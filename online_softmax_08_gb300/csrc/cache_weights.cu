@@ -109,6 +109,7 @@ __global__ void __launch_bounds__(32 * kWarpsW, kCtasW)
   }
   long long mine = units_of(b, &seq);
 
+  const Int4Magic magic;
   int staged_b = -1, staged_h = -1;  // whose rows (all of them) lie in shared memory
   for (long long unit = lo; unit < hi; ++unit) {
     while (unit >= before + mine) {
@@ -157,7 +158,7 @@ __global__ void __launch_bounds__(32 * kWarpsW, kCtasW)
 #pragma unroll
           for (int u = 0; u < C::U; ++u) {
             uint32_t o[4];
-            int4_values(w[u], int4_scale(__byte_perm(s2, 0u, u < 2 ? 0x0404u : 0x1414u)), o);
+            int4_values(w[u], int4_scale(__byte_perm(s2, 0u, u < 2 ? 0x0404u : 0x1414u)), magic, o);
             a[m][2 * u][i] = o[0], a[m][2 * u][i + 2] = o[1];
             a[m][2 * u + 1][i] = o[2], a[m][2 * u + 1][i + 2] = o[3];
           }
