@@ -748,6 +748,31 @@ extern "C" int fattn_cache_weights(const fattn_cache* cache, const fattn_cache_b
   p.causal = causal ? 1 : 0;
   p.scale_log2 = scale * 1.4426950408889634f;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  // Sequences of more than 32 rows go to the kernel whose tiles have 128 of them, 128 / G
+  // tokens of a group of G heads; not those of larger groups, nor a q whose rows lie on one
+  // another, which a tensor map cannot describe.
+  p.narrow_rows = 0x7fffffff;
+  const TokenView& v = p.q;
+  const bool mapped = (T == 1 || v.st > 0) && (Hq == 1 || v.sh > 0);
+  if ((long long)batch->max_seqlen * p.G > 32 && p.G <= 128 && mapped) {
+    p.narrow_rows = 32;
+    p.tile_tokens = 128 / p.G;
+    CUtensorMap tq;
+    const cuuint64_t dims[3] = {(cuuint64_t)cache->d, (cuuint64_t)Hq, (cuuint64_t)T};
+    const cuuint64_t strides[2] = {(cuuint64_t)(Hq > 1 ? v.sh : cache->d) * 2,
+                                   (cuuint64_t)(T > 1 ? v.st : cache->d) * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)p.G, (cuuint32_t)p.tile_tokens};
+    const cuuint32_t one[3] = {1, 1, 1};
+    if (strides[0] < (1ull << 40) && strides[1] < (1ull << 40) &&
+        g_encode(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box,
+                 one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS) {
+      if (launch_cache_weights_wide(tq, p, dev->n_sm, s) != cudaSuccess) return FATTN_ERR_CUDA;
+    } else {
+      p.narrow_rows = 0x7fffffff;
+    }
+  }
   return debug_post_call(
       launch_cache_weights(p, dev->n_sm, s) == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA, s);
 }

@@ -1,5 +1,5 @@
 // cache_weights.cu -- the attention weight that every cached key receives from a batch's
-// queries.
+// queries, for sequences with few query rows per key/value head.
 //
 // For sequence b and key/value head h, over its rows (token i, query head g of the group):
 //   W_j (+)= sum_rows exp(scale q_row . k_j - lse_row),   row sees key j,
@@ -75,7 +75,10 @@ __global__ void __launch_bounds__(32 * kWarpsW, kCtasW)
       if (c.err) atomicCAS(c.err, 0u, (unsigned)ERR_SITE_CACHE_WEIGHTS);
       return 0;
     }
-    return seq->n == 0 ? 0 : (long long)((seq->len + kKeys - 1) / kKeys) * c.H;
+    // (more rows: the other kernel's)
+    return seq->n == 0 || (long long)seq->n * p.G > p.narrow_rows
+               ? 0
+               : (long long)((seq->len + kKeys - 1) / kKeys) * c.H;
   };
   long long total = 0;
   CacheSeq seq;

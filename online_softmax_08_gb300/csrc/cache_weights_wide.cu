@@ -1,0 +1,474 @@
+// cache_weights_wide.cu -- the attention weight that every cached key receives, for sequences
+// with many query rows (pieces of prompts): tcgen05 + TMEM.
+//
+// S^T = K Q^T with the keys as the 128 lanes of a TMEM tile and 128 query rows as its columns,
+// so a thread owns a key and adds exp(s f - lse) over the columns it reads, in their order.
+// Both operands are bf16 without a rounding: codes and 4-bit values have at most 7 significant
+// bits, q is what it is (a block's scale and the softmax scale make f, by key).
+//
+// A CTA (one per SM) goes through its share of the units, each 256 keys of one (sequence,
+// key/value head), in two tiles, against all rows that see some of them:
+//   warps 0-3, 4-7  the keys of tile 0, 1: their codes are loaded during the unit before's last
+//                   rows, converted and stored in the 128-byte-swizzled layout that a TMA load
+//                   would leave; then S by S: tcgen05.ld, exponential, sum
+//   warp 8          Q, 128 rows at a time, by TMA straight from the caller's tensor: a tile is
+//                   tb = 128 / G tokens of the group's G heads, which a box {64, G, tb} leaves as
+//                   rows; and the rows' log-sum-exp
+//   warp 9          the MMAs, into four S tiles: two of keys by two in turn
+// The bound is the special-function unit: 128 x 128 exponentials take 1024 clocks at 16 a clock,
+// the products of that tile 256.
+#define FATTN_INLINE_WAIT_SLOW_PATH
+#include <math.h>
+
+#include <algorithm>
+
+#include "evict.cuh"
+
+namespace fattn {
+namespace {
+
+constexpr float kLog2eV = 1.4426950408889634f;
+
+template <int D>
+struct Ww {
+  static constexpr int BM = 128, KEYS = 2 * BM, BN = 128;
+  static constexpr int HALF = BM * 128;      // 64 channels of 128 rows (bytes)
+  static constexpr int TILE = BM * D * 2;
+  static constexpr int ST = D == 128 ? 4 : 6;
+  static constexpr int OFF_K = 0;
+  static constexpr int OFF_Q = 2 * TILE;
+  static constexpr int OFF_INFO = OFF_Q + ST * TILE;  // [ST][BN] -lse log2(e)
+  static constexpr int OFF_BAR = OFF_INFO + ST * BN * 4;
+  static constexpr int SMEM = OFF_BAR + 256 + 1024;
+  static constexpr int W_LOAD = 8, W_MMA = 9, THREADS = 320;
+  static constexpr uint32_t IDESC = idesc_bf16_f32(128, BN, false, false);
+  static_assert(SMEM <= 232448, "shared memory budget");
+};
+enum {
+  X_K_FULL = 0,    // [2] keys in shared memory (128 threads)
+  X_S_FULL = 2,    // [2 tiles][2]
+  X_S_EMPTY = 6,   // [2 tiles][2], 4 warps
+  X_DONE = 10,
+  X_Q_FULL = 11,   // [ST], then q_empty [ST]: the MMAs and 8 warps
+};
+
+__device__ __forceinline__ void fma_x2(float a0, float a1, float b, float c0, float c1, float& r0,
+                                       float& r1) {
+  asm("{\n\t.reg .b64 a, b, c, r;\n\t"
+      "mov.b64 a, {%2, %3};\n\t"
+      "mov.b64 b, {%4, %4};\n\t"
+      "mov.b64 c, {%5, %6};\n\t"
+      "fma.rn.f32x2 r, a, b, c;\n\t"
+      "mov.b64 {%0, %1}, r;\n\t}"
+      : "=f"(r0), "=f"(r1)
+      : "f"(a0), "f"(a1), "f"(b), "f"(c0), "f"(c1));
+}
+__device__ __forceinline__ void add_x2(float& s0, float& s1, float a0, float a1) {
+  asm("{\n\t.reg .b64 s, a;\n\t"
+      "mov.b64 s, {%0, %1};\n\t"
+      "mov.b64 a, {%2, %3};\n\t"
+      "add.rn.f32x2 s, s, a;\n\t"
+      "mov.b64 {%0, %1}, s;\n\t}"
+      : "+f"(s0), "+f"(s1)
+      : "f"(a0), "f"(a1));
+}
+__device__ __forceinline__ float4 ld_shared_f4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(a));
+  return v;
+}
+
+// A unit of this CTA's share, found alike by every warp.  The units of a sequence cost as many
+// row tiles as it has; a share is an equal part of all cost, to which the units belong that
+// begin in it.
+template <int KEYS>
+struct Walk {
+  const WeightParams& p;
+  long long before, hi;  // cost of the sequences before; end of the share
+  int b;                 // sequence
+  long long u;           // unit in it
+  CacheSeq seq;
+  int tiles, row_tiles;  // 256-key tiles; tiles of rows
+  __device__ __forceinline__ long long cost_of(int b) {
+    row_tiles = tiles = 0;
+    if (!cache_seq(p.c, b, &seq) || seq.len > p.width) return 0;  // (reported by the other kernel)
+    if ((long long)seq.n * p.G <= p.narrow_rows) return 0;
+    tiles = (seq.len + KEYS - 1) / KEYS;
+    row_tiles = (seq.n + p.tile_tokens - 1) / p.tile_tokens;
+    return (long long)tiles * p.c.H * row_tiles;
+  }
+  __device__ __forceinline__ explicit Walk(const WeightParams& p_) : p(p_) {
+    const int lane = threadIdx.x & 31;
+    long long total = 0;
+    for (int b0 = 0; b0 < p.c.B; b0 += 32) {
+      long long n = b0 + lane < p.c.B ? cost_of(b0 + lane) : 0;
+#pragma unroll
+      for (int w = 16; w > 0; w >>= 1) n += __shfl_xor_sync(0xffffffffu, n, w);
+      total += n;
+    }
+    const long long share = (total + gridDim.x - 1) / gridDim.x, lo = blockIdx.x * share;
+    hi = min(total, lo + share);
+    b = p.c.B, u = 0, before = total;
+    if (lo >= hi) return;
+    before = 0;
+    for (int b0 = 0; b0 < p.c.B; b0 += 32) {
+      const long long n = b0 + lane < p.c.B ? cost_of(b0 + lane) : 0;
+      long long upto = n;
+#pragma unroll
+      for (int w = 1; w < 32; w <<= 1) {
+        const long long o = __shfl_up_sync(0xffffffffu, upto, w);
+        if (lane >= w) upto += o;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, before + upto > lo);
+      if (past) {
+        const int src = __ffs(past) - 1;
+        b = b0 + src;
+        before += __shfl_sync(0xffffffffu, upto - n, src);
+        break;
+      }
+      before += __shfl_sync(0xffffffffu, upto, 31);
+    }
+    const long long n = cost_of(b);
+    u = (lo - before + row_tiles - 1) / row_tiles;
+    skip(n);
+  }
+  __device__ __forceinline__ void skip(long long n) {  // n: the cost of sequence b
+    while (u * row_tiles >= n) {
+      before += n;
+      u = 0;
+      if (++b >= p.c.B) return;
+      n = cost_of(b);
+    }
+  }
+  __device__ __forceinline__ bool valid() const {
+    return b < p.c.B && before + u * row_tiles < hi;
+  }
+  __device__ __forceinline__ void next() {
+    ++u;
+    skip((long long)tiles * p.c.H * row_tiles);
+  }
+  __device__ __forceinline__ int head() const { return (int)(u / tiles); }
+  __device__ __forceinline__ int key0() const { return (int)(u % tiles) * KEYS; }
+  // the first tile of rows that see some of the unit's keys
+  __device__ __forceinline__ int first_rows() const {
+    return p.causal ? max(0, key0() - (seq.len - seq.n)) / p.tile_tokens : 0;
+  }
+  __device__ __forceinline__ int key_tiles() const { return key0() + 128 < seq.len ? 2 : 1; }
+};
+
+template <int D, int FMT>
+__global__ void __launch_bounds__(Ww<D>::THREADS, 1)
+    cache_weights_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const WeightParams p) {
+  using C = Ww<D>;
+  constexpr bool I4 = FMT == FMT_INT4, E5M2 = FMT == FMT_E5M2;
+  constexpr int ST = C::ST;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t sbase = (raw + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (sbase - raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const CacheParams& c = p.c;
+  auto bar = [&](int i) { return sbase + C::OFF_BAR + 8u * (uint32_t)i; };
+  const uint32_t q_full0 = bar(X_Q_FULL), q_empty0 = bar(X_Q_FULL + ST);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + 8 * (X_Q_FULL + 2 * ST));
+  volatile uint32_t* abort_flag = tmem_slot + 1;
+  const WaitCtx wctx{abort_flag, c.err};
+  static_assert(8 * (X_Q_FULL + 2 * ST) + 8 <= 256, "barrier block");
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) mbar_init(bar(X_K_FULL + i), 128);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(bar(X_S_FULL + i), 1);
+      mbar_init(bar(X_S_EMPTY + i), 4);
+    }
+    mbar_init(bar(X_DONE), 1);
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(q_full0 + 8u * i, 1);
+      mbar_init(q_empty0 + 8u * i, 1 + 8);
+    }
+    *abort_flag = 0u;
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_q);
+  }
+  if (warp == C::W_MMA) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  Walk<C::KEYS> walk(p);
+
+  if (warp == C::W_LOAD) {
+    // ---------------------------------------------------------------- Q and log-sum-exp
+    int i = 0;  // tiles of rows so far
+    bool ok = true;
+    for (; ok && walk.valid(); walk.next()) {
+      const int h = walk.head(), n = walk.seq.n, row0 = walk.seq.row0;
+      for (int j = walk.first_rows(); j < walk.row_tiles; ++j, ++i) {
+        const int stage = i % ST, use = i / ST;
+        ok = use == 0 || __all_sync(0xffffffffu, mbar_wait(q_empty0 + 8u * stage, (use - 1) & 1, wctx,
+                                                           ERR_SITE_CACHE_WEIGHTS + 2));
+        if (!ok) break;
+        const int tok0 = j * p.tile_tokens;
+        const int rows = min(p.tile_tokens, n - tok0) * p.G;
+#pragma unroll
+        for (int k = 0; k < C::BN / 32; ++k) {
+          const int r = k * 32 + lane;
+          float l = -INFINITY;
+          if (r < rows) {
+            l = p.lse[(long long)(h * p.G + p.by_G.mod(r)) * c.total + row0 + tok0 + p.by_G.div(r)];
+            l = l == -INFINITY ? -INFINITY : -l * kLog2eV;  // a row that saw nothing adds nothing
+          }
+          reinterpret_cast<float*>(smem + C::OFF_INFO)[stage * C::BN + r] = l;
+        }
+        __syncwarp();
+        if (lane == 0) {
+          const uint32_t dst = sbase + C::OFF_Q + stage * C::TILE;
+          // (what lies outside of the tensor counts as loaded zeros)
+          mbar_arrive_expect_tx(q_full0 + 8u * stage, (uint32_t)(p.tile_tokens * p.G * D * 2));
+#pragma unroll
+          for (int x = 0; x < D / 64; ++x)
+            tma_load_3d(dst + x * C::HALF, &tm_q, q_full0 + 8u * stage, x * 64, h * p.G, row0 + tok0);
+        }
+        __syncwarp();
+      }
+    }
+    // copies in flight land before the CTA ends (only after a wait that ran out)
+    for (int k = max(0, i - ST); k < i; ++k)
+      mbar_drain(q_full0 + 8u * (k % ST), (k / ST) & 1, wctx, ERR_SITE_CACHE_WEIGHTS + 3);
+  } else if (warp == C::W_MMA) {
+    // ---------------------------------------------------------------- MMA issuer (whole warp)
+    int i = 0, units = 0;
+    int second = 0;  // row tiles that had a second tile of keys
+    bool ok = true;
+    for (; ok && walk.valid(); walk.next(), ++units) {
+      const int tiles = walk.key_tiles();
+      for (int a = 0; ok && a < 2; ++a)
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(X_K_FULL + a), units & 1, wctx,
+                                               ERR_SITE_CACHE_WEIGHTS + 4));
+      for (int j = walk.first_rows(); ok && j < walk.row_tiles; ++j, ++i) {
+        const int stage = i % ST;
+        ok = __all_sync(0xffffffffu, mbar_wait(q_full0 + 8u * stage, (i / ST) & 1, wctx,
+                                               ERR_SITE_CACHE_WEIGHTS + 5));
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+          if (!ok || a >= tiles) break;
+          const int n = a ? second : i, buf = n & 1, use = n >> 1;
+          ok = use == 0 || __all_sync(0xffffffffu, mbar_wait(bar(X_S_EMPTY + a * 2 + buf), (use - 1) & 1,
+                                                             wctx, ERR_SITE_CACHE_WEIGHTS + 6));
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t ka = sbase + C::OFF_K + a * C::TILE, qb = sbase + C::OFF_Q + stage * C::TILE;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * C::HALF + (kk & 3) * 32;
+            mma_bf16_ss_w(tmem + (a * 2 + buf) * C::BN, sdesc_sw128(ka + off, 16, 1024),
+                          sdesc_sw128(qb + off, 16, 1024), C::IDESC, kk > 0);
+          }
+          mma_commit_w(bar(X_S_FULL + a * 2 + buf));
+          if (a) ++second;
+        }
+        if (ok) mma_commit_w(q_empty0 + 8u * stage);
+      }
+    }
+    mma_commit_w(bar(X_DONE));  // drain before TMEM is freed
+    mbar_drain(bar(X_DONE), 0, wctx, ERR_SITE_CACHE_WEIGHTS + 7);
+    __syncwarp();
+  } else {
+    // ---------------------------------------------------------------- keys, exponentials, sums
+    const int a = warp >> 2, t = threadIdx.x & 127;
+    constexpr int RB = I4 ? D / 2 : D, PPR = RB / 16;  // bytes, 16-byte pieces of a row
+    constexpr int RPI = 128 / PPR;                     // rows of a load by all threads
+    const int prow = t / PPR, piece = t % PPR;
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    uint4 raw_codes[PPR];
+    uint32_t raw_scale[PPR];
+    float ks = 0.f;     // of key t; 0: it has no block
+    auto page_of = [&](int key) {
+      if (key >= walk.seq.len) return -1;
+      const int page = c.block_table[(long long)walk.b * c.table_width + (key >> c.block_log2)];
+      if (page >= 0 && page < c.num_blocks) return page;
+      if (c.err) atomicCAS(c.err, 0u, (unsigned)ERR_SITE_CACHE_WEIGHTS + 1);
+      return -1;
+    };
+    auto load = [&]() {  // the codes of the unit that `walk` is at
+      const int h = walk.head(), key0 = walk.key0() + a * C::BM;
+#pragma unroll
+      for (int x = 0; x < PPR; ++x) {
+        const int key = key0 + x * RPI + prow;
+        const int page = page_of(key);
+        raw_codes[x] = make_uint4(0u, 0u, 0u, 0u);
+        raw_scale[x] = 0u;
+        if (page < 0) continue;
+        const long long row = (((long long)page * c.H + h) << c.block_log2) + (key & (c.block_size - 1));
+        raw_codes[x] = __ldg(reinterpret_cast<const uint4*>(c.k + row * RB + piece * 16));
+        if constexpr (I4)
+          raw_scale[x] =
+              __ldg(reinterpret_cast<const uint16_t*>(c.k_scale4 + row * (D / 16) + piece * 2));
+      }
+      const int page = page_of(key0 + t);
+      ks = page < 0 ? 0.f : I4 ? 1.f : c.k_scale[(long long)page * c.H + h];
+    };
+    auto store = [&]() {  // as bf16, rows of 128 bytes, 16-byte columns swizzled by row & 7
+      const uint32_t tile = sbase + C::OFF_K + a * C::TILE;
+#pragma unroll
+      for (int x = 0; x < PPR; ++x) {
+        const int row = x * RPI + prow;
+        const uint32_t w[4] = {raw_codes[x].x, raw_codes[x].y, raw_codes[x].z, raw_codes[x].w};
+        auto put = [&](int ch, const uint32_t (&o)[4]) {  // eight channels from ch on
+          const uint32_t at = tile + (ch >> 6) * C::HALF + row * 128 +
+                              ((((ch >> 3) & 7) ^ (row & 7)) << 4);
+          st_shared_v4(at, o[0], o[1], o[2], o[3]);
+        };
+        if constexpr (I4) {
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {  // a word: eight codes
+            const float s = f16x2_to_f32((raw_scale[x] >> (8 * (y >> 1)) & 0xffu) << 8).x;
+            uint32_t o[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              o[k] = pack_bf16x2((float)((int)(w[y] >> (8 * k) & 15u) - 8) * s,
+                                 (float)((int)(w[y] >> (8 * k + 4) & 15u) - 8) * s);
+            put(piece * 32 + y * 8, o);
+          }
+        } else {
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {  // two words: eight codes
+            uint32_t o[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float2 v = f16x2_to_f32(
+                  codes_to_f16x2<E5M2>((uint16_t)(w[2 * y + (k >> 1)] >> (16 * (k & 1)) & 0xffffu)));
+              o[k] = pack_bf16x2(v.x, v.y);
+            }
+            put(piece * 16 + y * 8, o);
+          }
+        }
+      }
+      fence_proxy_async_smem();
+    };
+    int i = 0;     // tiles of rows so far, those in which this tile of keys took part
+    int mine = 0;
+    bool ok = true;
+    if (walk.valid()) load();
+    while (ok && walk.valid()) {
+      store();
+      const float k_scale = ks, f = ks * p.scale_log2;
+      mbar_arrive(bar(X_K_FULL + a));
+      // the unit at hand; `walk` goes on to the next one
+      const int b = walk.b, h = walk.head(), len = walk.seq.len, n = walk.seq.n;
+      const int key = walk.key0() + a * C::BM + t;
+      const int first = walk.first_rows(), row_tiles = walk.row_tiles;
+      const bool part = a < walk.key_tiles();
+      const int key_last = walk.key0() + a * C::BM + 127;
+      walk.next();
+      float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+      for (int j = first; ok && j < row_tiles; ++j, ++i) {
+        if (j == row_tiles - 1 && walk.valid()) load();
+        const int stage = i % ST;
+        if (!part) {  // (warp-uniform) nothing but its share of the slot's release
+          ok = __all_sync(0xffffffffu, mbar_wait(q_full0 + 8u * stage, (i / ST) & 1, wctx,
+                                                 ERR_SITE_CACHE_WEIGHTS + 8));
+          if (ok && lane == 0) mbar_arrive(q_empty0 + 8u * stage);
+          continue;
+        }
+        const int buf = mine & 1;
+        ok = __all_sync(0xffffffffu, mbar_wait(q_full0 + 8u * stage, (i / ST) & 1, wctx,
+                                               ERR_SITE_CACHE_WEIGHTS + 8) &&
+                                         mbar_wait(bar(X_S_FULL + a * 2 + buf), (mine >> 1) & 1, wctx,
+                                                   ERR_SITE_CACHE_WEIGHTS + 9));
+        ++mine;
+        if (!ok) break;
+        tc_fence_after();
+        const int tok0 = j * p.tile_tokens;
+        const int rows = min(p.tile_tokens, n - tok0) * p.G;
+        // this key is seen by rows from `from` on
+        const int ahead = p.causal ? key - (len - n) - tok0 : 0;
+        const int from = ahead >= p.tile_tokens ? C::BN : max(0, ahead) * p.G;
+        const bool diagonal = p.causal && key_last - (len - n) > tok0;
+        const uint32_t info = sbase + C::OFF_INFO + (uint32_t)(stage * C::BN) * 4u;
+        const uint32_t tS = tmem + lane_off + (a * 2 + buf) * C::BN;
+        uint32_t v[2][32];
+        tmem_ld32(tS, v[0]);
+#pragma unroll
+        for (int x = 0; x < C::BN / 32; ++x) {
+          if (x * 32 >= rows) break;  // uniform
+          tmem_wait_ld(v[x & 1]);
+          if (x + 1 < C::BN / 32) tmem_ld32(tS + (x + 1) * 32, v[(x + 1) & 1]);
+          const uint32_t(&s)[32] = v[x & 1];
+          const bool cut = diagonal || x * 32 + 32 > rows;
+#pragma unroll
+          for (int k = 0; k < 32; k += 4) {
+            const float4 l = ld_shared_f4(info + (uint32_t)(x * 32 + k) * 4u);
+            float e0, e1, e2, e3;
+            fma_x2(__uint_as_float(s[k]), __uint_as_float(s[k + 1]), f, l.x, l.y, e0, e1);
+            fma_x2(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3]), f, l.z, l.w, e2, e3);
+            e0 = ex2(e0), e1 = ex2(e1), e2 = ex2(e2), e3 = ex2(e3);
+            if (cut) {
+              const int col = x * 32 + k;
+              if (col < from || col >= rows) e0 = 0.f;
+              if (col + 1 < from || col + 1 >= rows) e1 = 0.f;
+              if (col + 2 < from || col + 2 >= rows) e2 = 0.f;
+              if (col + 3 < from || col + 3 >= rows) e3 = 0.f;
+            }
+            add_x2(s0, s1, e0, e1);
+            add_x2(s2, s3, e2, e3);
+          }
+        }
+        tmem_wait_ld();  // (one load more than was used, where the rows end early)
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(X_S_EMPTY + a * 2 + buf));
+          mbar_arrive(q_empty0 + 8u * stage);
+        }
+      }
+      if (ok && key < len) {
+        float w = k_scale == 0.f ? 0.f : (s0 + s1) + (s2 + s3);
+        if (p.accumulate && key < len - n) w += p.in.p[b * p.in.sb + h * p.in.sh + key];
+        p.out.p[b * p.out.sb + h * p.out.sh + key] = w;
+      }
+    }
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == C::W_MMA) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D, int FMT>
+cudaError_t start(const CUtensorMap& tq, const WeightParams& p, int n_sm, cudaStream_t stream) {
+  using C = Ww<D>;
+  static unsigned long long prepared[64];
+  const cudaError_t e = prepare_once(prepared, [] {
+    return cudaFuncSetAttribute(cache_weights_wide_kernel<D, FMT>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  });
+  if (e != cudaSuccess) return e;
+  cache_weights_wide_kernel<D, FMT><<<(unsigned)n_sm, C::THREADS, C::SMEM, stream>>>(tq, p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_cache_weights_wide(const CUtensorMap& tq, const WeightParams& p, int n_sm,
+                                      cudaStream_t stream) {
+  const bool d128 = p.c.d == 128;
+  switch (p.c.format) {
+    case FMT_E4M3:
+      return d128 ? start<128, FMT_E4M3>(tq, p, n_sm, stream) : start<64, FMT_E4M3>(tq, p, n_sm, stream);
+    case FMT_E5M2:
+      return d128 ? start<128, FMT_E5M2>(tq, p, n_sm, stream) : start<64, FMT_E5M2>(tq, p, n_sm, stream);
+    default:
+      return d128 ? start<128, FMT_INT4>(tq, p, n_sm, stream) : start<64, FMT_INT4>(tq, p, n_sm, stream);
+  }
+}
+
+}  // namespace fattn

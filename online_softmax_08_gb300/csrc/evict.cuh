@@ -25,8 +25,13 @@ struct WeightParams {
   FastDiv by_G;
   int causal;
   float scale_log2;
+  int narrow_rows;   // sequences with more query rows per key/value head go to the tcgen05 kernel
+  int tile_tokens;   // of its tiles of rows: 128 / G
 };
 cudaError_t launch_cache_weights(const WeightParams& p, int n_sm, cudaStream_t stream);
+// tq: map of q, {d, Hq, total}, boxes {64, G, tile_tokens}
+cudaError_t launch_cache_weights_wide(const CUtensorMap& tq, const WeightParams& p, int n_sm,
+                                      cudaStream_t stream);
 
 struct EvictParams {
   CacheParams c;       // cu_seqlens, total and max_seqlen are not used

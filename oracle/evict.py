@@ -24,16 +24,19 @@ def weights(cache, fmt, batch, q, lse, scale, causal, before, out):
         out[b, :, start:length] = 0.0
         out[b, :, :start] = 0.0 if before is None else before[b, :, :start]
         k = _tokens(fmt)(cache, fmt, table[b], "k", 0, length)
-        for i in range(n):
-            lim = max(0, length - n + i + 1) if causal else length
-            t = int(cu[b]) + i
-            for hq in range(Hq):
-                h = hq // (Hq // H)
-                if lse[hq, t] == -np.inf:
-                    continue
-                out[b, h, :lim] += np.exp(scale * (k[:lim, h] @ q[t, hq]) - lse[hq, t])
-                s = scale * (np.abs(k[:lim, h]) @ np.abs(q[t, hq])) + abs(lse[hq, t])
-                size[b, h, :lim] = np.maximum(size[b, h, :lim], s)
+        t = np.arange(int(cu[b]), int(cu[b + 1]))
+        at = np.arange(length)
+        sees = at[None, :] <= (length - n + np.arange(n))[:, None] if causal else \
+            np.ones((n, length), dtype=bool)
+        for hq in range(Hq):
+            h = hq // (Hq // H)
+            rows = lse[hq, t] != -np.inf
+            see = sees[rows]
+            x, l = q[t[rows], hq], lse[hq, t[rows]][:, None]
+            with np.errstate(invalid="ignore", over="ignore"):
+                out[b, h, :length] += np.where(see, np.exp(scale * (x @ k[:, h].T) - l), 0.0).sum(axis=0)
+            s = np.where(see, scale * (np.abs(x) @ np.abs(k[:, h].T)) + np.abs(l), 0.0)
+            size[b, h, :length] = np.maximum(size[b, h, :length], s.max(axis=0, initial=0.0))
     return out, size
 
 

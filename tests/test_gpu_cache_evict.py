@@ -74,6 +74,16 @@ WEIGHTS = [
     ([(1, 50), (3, 40)], 1, 300, 64, 16, "e4m3", True),
     ([(i % 4, 5 * i) for i in range(70)], 2, 2, 64, 16, "int4", True),
     ([(i % 2, i % 50) for i in range(1100)], 1, 1, 64, 16, "int4", True),
+    # the tcgen05 kernel: groups that divide its tiles and that do not, units cut by the shares,
+    # second tiles of keys with and without tokens, mixed with sequences of few rows
+    ([(33, 0)], 1, 1, 128, 16, "int4", True),
+    ([(600, 3000)], 2, 4, 128, 64, "e4m3", True),
+    ([(100, 0), (1, 50), (513, 200), (0, 40)], 1, 5, 64, 16, "int4", True),
+    ([(9, 300)], 1, 128, 128, 32, "int4", True),
+    ([(300, 600), (33, 1), (40, 216)], 2, 3, 128, 128, "e5m2", False),
+    ([(35 + i, 90 * i) for i in range(40)], 1, 2, 64, 32, "e4m3", True),
+    ([(1 if i % 3 else 129, 7 * i) for i in range(70)], 3, 1, 128, 16, "int4", True),
+    ([(257, 5000)], 1, 7, 64, 64, "int4", False),
 ]
 
 
@@ -122,11 +132,38 @@ def test_weights_of_more_queries_than_tokens(n, length, G, causal):
     assert abs(float(total[1, 0]) - live * G) <= 1e-4 * max(1, live * G)
 
 
+@pytest.mark.parametrize("n,G", [(3, 2), (50, 3)])
+def test_weights_of_a_broadcast_query(n, G):
+    """One query for all tokens, and one for all heads, by strides of zero."""
+    H, d = 2, 64
+    c = _case([(n, 70), (1, 20)], H, d, 16, "int4").fill()
+    cache, batch = c.on_device()
+    row = _bf16(c.rng, (1, H * G, d)).to(DEV)
+    for q in (row.expand(n + 1, H * G, d), row[:, :1].expand(n + 1, H * G, d),
+              _bf16(c.rng, (n + 1, 1, d)).to(DEV).expand(n + 1, H * G, d)):
+        _, lse = fattn.cache_forward(q, cache, batch, 0.125, True)
+        got = fattn.cache_weights(q, lse, cache, batch, 0.125, True)
+        _check_weights(c, "int4", q.contiguous(), lse, 0.125, True, None, np.zeros(got.shape), got)
+
+
+def test_nan_queries_stay_with_their_sequence():
+    """Rows of the next sequence, which a tile of queries may hold as well, do not count."""
+    H, G, d = 1, 2, 128
+    c = _case([(50, 30), (40, 20)], H, d, 16, "e4m3").fill()
+    cache, batch = c.on_device()
+    q = _bf16(c.rng, (90, G, d)).to(DEV)
+    _, lse = fattn.cache_forward(q, cache, batch, 0.1, True)
+    ref = fattn.cache_weights(q, lse, cache, batch, 0.1, True)
+    q[50:] = float("nan")
+    got = fattn.cache_weights(q, lse, cache, batch, 0.1, True)
+    assert torch.equal(got[0], ref[0])
+
+
 def test_nan_key_and_repeated_calls():
     """A NaN key of one head makes NaN of the weights of the keys that its queries see, and of no
     other head's or sequence's.  Repeated calls agree bit for bit."""
     H, G, d, bs = 2, 2, 128, 16
-    c = _case([(3, 50), (2, 20)], H, d, bs, "e4m3").fill()
+    c = _case([(3, 50), (40, 20)], H, d, bs, "e4m3").fill()
     q = _bf16(c.rng, (c.T, H * G, d)).to(DEV)
     cache, batch = c.on_device()
     _, lse = fattn.cache_forward(q, cache, batch, 0.1, True)
