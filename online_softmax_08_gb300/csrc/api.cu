@@ -748,15 +748,15 @@ extern "C" int fattn_cache_weights(const fattn_cache* cache, const fattn_cache_b
   p.causal = causal ? 1 : 0;
   p.scale_log2 = scale * 1.4426950408889634f;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  // Sequences of more than 32 rows go to the kernel whose tiles have 128 of them, 128 / G
+  // Sequences of more than 32 rows go to the kernel whose tiles have 256 of them, 256 / G
   // tokens of a group of G heads; not those of larger groups, nor a q whose rows lie on one
   // another, which a tensor map cannot describe.
   p.narrow_rows = 0x7fffffff;
   const TokenView& v = p.q;
   const bool mapped = (T == 1 || v.st > 0) && (Hq == 1 || v.sh > 0);
-  if ((long long)batch->max_seqlen * p.G > 32 && p.G <= 128 && mapped) {
+  if ((long long)batch->max_seqlen * p.G > 32 && p.G <= 256 && mapped) {
     p.narrow_rows = 32;
-    p.tile_tokens = 128 / p.G;
+    p.tile_tokens = 256 / p.G;
     CUtensorMap tq;
     const cuuint64_t dims[3] = {(cuuint64_t)cache->d, (cuuint64_t)Hq, (cuuint64_t)T};
     const cuuint64_t strides[2] = {(cuuint64_t)(Hq > 1 ? v.sh : cache->d) * 2,

@@ -1,22 +1,28 @@
 // cache_weights_wide.cu -- the attention weight that every cached key receives, for sequences
 // with many query rows (pieces of prompts): tcgen05 + TMEM.
 //
-// S^T = K Q^T with the keys as the 128 lanes of a TMEM tile and 128 query rows as its columns,
+// S^T = K Q^T with the keys as the 128 lanes of a TMEM tile and 256 query rows as its columns,
 // so a thread owns a key and adds exp(s f - lse) over the columns it reads, in their order.
 // Both operands are bf16 without a rounding: codes and 4-bit values have at most 7 significant
 // bits, q is what it is (a block's scale and the softmax scale make f, by key).
 //
 // A CTA (one per SM) goes through its share of the units, each 256 keys of one (sequence,
 // key/value head), in two tiles, against all rows that see some of them:
-//   warps 0-3, 4-7  the keys of tile 0, 1: their codes are loaded during the unit before's last
-//                   rows, converted and stored in the 128-byte-swizzled layout that a TMA load
-//                   would leave; then S by S: tcgen05.ld, exponential, sum
-//   warp 8          Q, 128 rows at a time, by TMA straight from the caller's tensor: a tile is
-//                   tb = 128 / G tokens of the group's G heads, which a box {64, G, tb} leaves as
-//                   rows; and the rows' log-sum-exp
-//   warp 9          the MMAs, into four S tiles: two of keys by two in turn
-// The bound is the special-function unit: 128 x 128 exponentials take 1024 clocks at 16 a clock,
-// the products of that tile 256.
+//   warps 0-15      the keys: four warps each the columns 0-127 of tile 0, of tile 1, and the
+//                   columns 128-255.  Their codes are loaded during the unit before's last rows,
+//                   converted and stored in the 128-byte-swizzled layout that a TMA load would
+//                   leave; then S by S: tcgen05.ld, exponential, sum
+//   warp 16         Q, 256 rows at a time, by TMA straight from the caller's tensor: a tile is
+//                   tb = 256 / G tokens of the group's G heads, which a box {64, G, tb} leaves as
+//                   rows
+//   warp 17         the MMAs, into the S of the two tiles of keys in turn
+//   warp 18         the rows' log-sum-exp, in a ring of their own, as Q's slots are free again
+//                   once the MMAs have read them
+// The bound is the special-function unit: 128 x 256 exponentials take 1024 clocks at the 32 a
+// clock that were measured, the products of that tile 768 (A and B come from shared memory at
+// 128 bytes a clock).  With tiles of 128 rows, S in two buffers, the thread that issues the MMAs
+// was the bound: its waits and 16 instructions took 2250 clocks a tile of 2 x 128 keys, as it
+// shares its issue slots with the exponentials.
 #define FATTN_INLINE_WAIT_SLOW_PATH
 #include <math.h>
 
@@ -31,25 +37,32 @@ constexpr float kLog2eV = 1.4426950408889634f;
 
 template <int D>
 struct Ww {
-  static constexpr int BM = 128, KEYS = 2 * BM, BN = 128;
-  static constexpr int HALF = BM * 128;      // 64 channels of 128 rows (bytes)
+  static constexpr int BM = 128, KEYS = 2 * BM, BN = 256;
+  static constexpr int HALF = BM * 128;      // 64 channels of 128 keys (bytes)
   static constexpr int TILE = BM * D * 2;
-  static constexpr int ST = D == 128 ? 4 : 6;
+  static constexpr int Q_HALF = BN * 128, Q_TILE = BN * D * 2;
+  static constexpr int ST = D == 128 ? 2 : 4;
   static constexpr int OFF_K = 0;
   static constexpr int OFF_Q = 2 * TILE;
-  static constexpr int OFF_INFO = OFF_Q + ST * TILE;  // [ST][BN] -lse log2(e)
-  static constexpr int OFF_BAR = OFF_INFO + ST * BN * 4;
-  static constexpr int SMEM = OFF_BAR + 256 + 1024;
-  static constexpr int W_LOAD = 8, W_MMA = 9, THREADS = 320;
+  static constexpr int OFF_INFO = OFF_Q + ST * Q_TILE;  // [INFO][BN] -lse log2(e)
+  static constexpr int INFO = 8;                          // tiles of rows
+  static constexpr int OFF_SUM = OFF_INFO + INFO * BN * 4;  // [2][BM] sums of columns 128-255
+  static constexpr int OFF_BAR = OFF_SUM + 2 * BM * 4;
+  static constexpr int SMEM = OFF_BAR + 512 + 1024;
+  static constexpr int W_LOAD = 16, W_MMA = 17, W_INFO = 18, THREADS = 608;
   static constexpr uint32_t IDESC = idesc_bf16_f32(128, BN, false, false);
+  static constexpr uint32_t IDESC_128 = idesc_bf16_f32(128, 128, false, false);
   static_assert(SMEM <= 232448, "shared memory budget");
 };
 enum {
-  X_K_FULL = 0,    // [2] keys in shared memory (128 threads)
-  X_S_FULL = 2,    // [2 tiles][2]
-  X_S_EMPTY = 6,   // [2 tiles][2], 4 warps
-  X_DONE = 10,
-  X_Q_FULL = 11,   // [ST], then q_empty [ST]: the MMAs and 8 warps
+  X_K_FULL = 0,    // [2] keys in shared memory (256 threads)
+  X_S_FULL = 2,    // [2]
+  X_S_EMPTY = 4,   // [2], 8 warps
+  X_DONE = 6,
+  X_SUM = 7,       // [2] the sums of columns 128-255 (128 threads)
+  X_I_FULL = 9,    // [INFO] the rows' log-sum-exp
+  X_I_EMPTY = 17,  // [INFO], 16 warps
+  X_Q_FULL = 25,   // [ST], then q_empty [ST]
 };
 
 __device__ __forceinline__ void fma_x2(float a0, float a1, float b, float c0, float c1, float& r0,
@@ -175,18 +188,26 @@ __global__ void __launch_bounds__(Ww<D>::THREADS, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + 8 * (X_Q_FULL + 2 * ST));
   volatile uint32_t* abort_flag = tmem_slot + 1;
   const WaitCtx wctx{abort_flag, c.err};
-  static_assert(8 * (X_Q_FULL + 2 * ST) + 8 <= 256, "barrier block");
+  static_assert(8 * (X_Q_FULL + 2 * ST) + 8 <= 512, "barrier block");
+  static_assert(X_I_EMPTY - X_I_FULL == C::INFO && X_Q_FULL - X_I_EMPTY == C::INFO, "barriers");
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 2; ++i) mbar_init(bar(X_K_FULL + i), 128);
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(X_K_FULL + i), 256);
+      mbar_init(bar(X_SUM + i), 128);
+    }
+    for (int i = 0; i < 2; ++i) {
       mbar_init(bar(X_S_FULL + i), 1);
-      mbar_init(bar(X_S_EMPTY + i), 4);
+      mbar_init(bar(X_S_EMPTY + i), 8);
     }
     mbar_init(bar(X_DONE), 1);
     for (int i = 0; i < ST; ++i) {
       mbar_init(q_full0 + 8u * i, 1);
-      mbar_init(q_empty0 + 8u * i, 1 + 8);
+      mbar_init(q_empty0 + 8u * i, 1);
+    }
+    for (int i = 0; i < C::INFO; ++i) {
+      mbar_init(bar(X_I_FULL + i), 1);
+      mbar_init(bar(X_I_EMPTY + i), 16);
     }
     *abort_flag = 0u;
     fence_mbar_init();
@@ -203,90 +224,117 @@ __global__ void __launch_bounds__(Ww<D>::THREADS, 1)
   Walk<C::KEYS> walk(p);
 
   if (warp == C::W_LOAD) {
-    // ---------------------------------------------------------------- Q and log-sum-exp
-    int i = 0;  // tiles of rows so far
-    bool ok = true;
-    for (; ok && walk.valid(); walk.next()) {
-      const int h = walk.head(), n = walk.seq.n, row0 = walk.seq.row0;
-      for (int j = walk.first_rows(); j < walk.row_tiles; ++j, ++i) {
-        const int stage = i % ST, use = i / ST;
-        ok = use == 0 || __all_sync(0xffffffffu, mbar_wait(q_empty0 + 8u * stage, (use - 1) & 1, wctx,
-                                                           ERR_SITE_CACHE_WEIGHTS + 2));
-        if (!ok) break;
-        const int tok0 = j * p.tile_tokens;
-        const int rows = min(p.tile_tokens, n - tok0) * p.G;
-#pragma unroll
-        for (int k = 0; k < C::BN / 32; ++k) {
-          const int r = k * 32 + lane;
-          float l = -INFINITY;
-          if (r < rows) {
-            l = p.lse[(long long)(h * p.G + p.by_G.mod(r)) * c.total + row0 + tok0 + p.by_G.div(r)];
-            l = l == -INFINITY ? -INFINITY : -l * kLog2eV;  // a row that saw nothing adds nothing
-          }
-          reinterpret_cast<float*>(smem + C::OFF_INFO)[stage * C::BN + r] = l;
-        }
-        __syncwarp();
-        if (lane == 0) {
-          const uint32_t dst = sbase + C::OFF_Q + stage * C::TILE;
+    // ---------------------------------------------------------------- Q (one thread)
+    if (lane == 0) {
+      int i = 0;  // tiles of rows so far
+      bool ok = true;
+      for (; ok && walk.valid(); walk.next()) {
+        const int h = walk.head(), row0 = walk.seq.row0;
+        for (int j = walk.first_rows(); j < walk.row_tiles; ++j, ++i) {
+          const int stage = i % ST, use = i / ST;
+          ok = use == 0 || mbar_wait(q_empty0 + 8u * stage, (use - 1) & 1, wctx,
+                                     ERR_SITE_CACHE_WEIGHTS + 2);
+          if (!ok) break;
+          const uint32_t dst = sbase + C::OFF_Q + stage * C::Q_TILE;
           // (what lies outside of the tensor counts as loaded zeros)
           mbar_arrive_expect_tx(q_full0 + 8u * stage, (uint32_t)(p.tile_tokens * p.G * D * 2));
 #pragma unroll
           for (int x = 0; x < D / 64; ++x)
-            tma_load_3d(dst + x * C::HALF, &tm_q, q_full0 + 8u * stage, x * 64, h * p.G, row0 + tok0);
+            tma_load_3d(dst + x * C::Q_HALF, &tm_q, q_full0 + 8u * stage, x * 64, h * p.G,
+                        row0 + j * p.tile_tokens);
         }
-        __syncwarp();
       }
+      // copies in flight land before the CTA ends (only after a wait that ran out)
+      for (int k = max(0, i - ST); k < i; ++k)
+        mbar_drain(q_full0 + 8u * (k % ST), (k / ST) & 1, wctx, ERR_SITE_CACHE_WEIGHTS + 3);
     }
-    // copies in flight land before the CTA ends (only after a wait that ran out)
-    for (int k = max(0, i - ST); k < i; ++k)
-      mbar_drain(q_full0 + 8u * (k % ST), (k / ST) & 1, wctx, ERR_SITE_CACHE_WEIGHTS + 3);
-  } else if (warp == C::W_MMA) {
-    // ---------------------------------------------------------------- MMA issuer (whole warp)
-    int i = 0, units = 0;
-    int second = 0;  // row tiles that had a second tile of keys
+    __syncwarp();
+  } else if (warp == C::W_INFO) {
+    // ---------------------------------------------------------------- log-sum-exp
+    int i = 0;
     bool ok = true;
-    for (; ok && walk.valid(); walk.next(), ++units) {
-      const int tiles = walk.key_tiles();
-      for (int a = 0; ok && a < 2; ++a)
-        ok = __all_sync(0xffffffffu, mbar_wait(bar(X_K_FULL + a), units & 1, wctx,
-                                               ERR_SITE_CACHE_WEIGHTS + 4));
-      for (int j = walk.first_rows(); ok && j < walk.row_tiles; ++j, ++i) {
-        const int stage = i % ST;
-        ok = __all_sync(0xffffffffu, mbar_wait(q_full0 + 8u * stage, (i / ST) & 1, wctx,
-                                               ERR_SITE_CACHE_WEIGHTS + 5));
+    for (; ok && walk.valid(); walk.next()) {
+      const int h = walk.head(), n = walk.seq.n, row0 = walk.seq.row0;
+      for (int j = walk.first_rows(); j < walk.row_tiles; ++j, ++i) {
+        const int stage = i % C::INFO, use = i / C::INFO;
+        const int tok0 = j * p.tile_tokens;
+        const int rows = min(p.tile_tokens, n - tok0) * p.G;
+        float l[C::BN / 32];
 #pragma unroll
-        for (int a = 0; a < 2; ++a) {
-          if (!ok || a >= tiles) break;
-          const int n = a ? second : i, buf = n & 1, use = n >> 1;
-          ok = use == 0 || __all_sync(0xffffffffu, mbar_wait(bar(X_S_EMPTY + a * 2 + buf), (use - 1) & 1,
-                                                             wctx, ERR_SITE_CACHE_WEIGHTS + 6));
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t ka = sbase + C::OFF_K + a * C::TILE, qb = sbase + C::OFF_Q + stage * C::TILE;
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * C::HALF + (kk & 3) * 32;
-            mma_bf16_ss_w(tmem + (a * 2 + buf) * C::BN, sdesc_sw128(ka + off, 16, 1024),
-                          sdesc_sw128(qb + off, 16, 1024), C::IDESC, kk > 0);
-          }
-          mma_commit_w(bar(X_S_FULL + a * 2 + buf));
-          if (a) ++second;
+        for (int k = 0; k < C::BN / 32; ++k) {
+          const int r = k * 32 + lane;
+          l[k] = -INFINITY;
+          if (r < rows)
+            l[k] = p.lse[(long long)(h * p.G + p.by_G.mod(r)) * c.total + row0 + tok0 + p.by_G.div(r)];
         }
-        if (ok) mma_commit_w(q_empty0 + 8u * stage);
+        ok = use == 0 || __all_sync(0xffffffffu, mbar_wait(bar(X_I_EMPTY + stage), (use - 1) & 1, wctx,
+                                                           ERR_SITE_CACHE_WEIGHTS + 11));
+        if (!ok) break;
+#pragma unroll
+        for (int k = 0; k < C::BN / 32; ++k)  // a row that saw nothing adds nothing
+          reinterpret_cast<float*>(smem + C::OFF_INFO)[stage * C::BN + k * 32 + lane] =
+              l[k] == -INFINITY ? -INFINITY : -l[k] * kLog2eV;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(X_I_FULL + stage));
       }
     }
-    mma_commit_w(bar(X_DONE));  // drain before TMEM is freed
-    mbar_drain(bar(X_DONE), 0, wctx, ERR_SITE_CACHE_WEIGHTS + 7);
+    __syncwarp();
+  } else if (warp == C::W_MMA) {
+    // ---------------------------------------------------------------- MMA issuer (one thread:
+    // electing one of the warp for every instruction took longer than the products)
+    if (lane == 0) {
+      int i = 0, units[2] = {0, 0};  // units that have keys in each tile
+      int second = 0;  // row tiles that had a second tile of keys
+      const uint64_t ka0 = sdesc_sw128(sbase + C::OFF_K, 16, 1024);
+      const uint64_t qb0 = sdesc_sw128(sbase + C::OFF_Q, 16, 1024);
+      bool ok = true;
+      for (; ok && walk.valid(); walk.next()) {
+        const int tiles = walk.key_tiles();
+        for (int j = walk.first_rows(), j0 = j; ok && j < walk.row_tiles; ++j, ++i) {
+          const int stage = i % ST;
+          const bool half = (walk.seq.n - j * p.tile_tokens) * p.G <= 128;
+          ok = mbar_wait(q_full0 + 8u * stage, (i / ST) & 1, wctx, ERR_SITE_CACHE_WEIGHTS + 5);
+#pragma unroll
+          for (int a = 0; a < 2; ++a) {
+            if (!ok || a >= tiles) break;
+            if (j == j0) {
+              ok = mbar_wait(bar(X_K_FULL + a), units[a] & 1, wctx, ERR_SITE_CACHE_WEIGHTS + 4);
+              ++units[a];
+              if (!ok) break;
+            }
+            const int n = a ? second : i;
+            ok = n == 0 ||
+                 mbar_wait(bar(X_S_EMPTY + a), (n - 1) & 1, wctx, ERR_SITE_CACHE_WEIGHTS + 6);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t ka = ka0 + (uint32_t)(a * C::TILE >> 4);
+            const uint64_t qb = qb0 + (uint32_t)(stage * C::Q_TILE >> 4);
+            const uint32_t idesc = half ? C::IDESC_128 : C::IDESC;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+              mma_bf16_ss(tmem + a * C::BN,
+                          ka + (uint32_t)(((kk >> 2) * C::HALF + (kk & 3) * 32) >> 4),
+                          qb + (uint32_t)(((kk >> 2) * C::Q_HALF + (kk & 3) * 32) >> 4), idesc, kk > 0);
+            mma_commit(bar(X_S_FULL + a));
+            if (a) ++second;
+          }
+          if (ok) mma_commit(q_empty0 + 8u * stage);
+        }
+      }
+      mma_commit(bar(X_DONE));  // drain before TMEM is freed
+      mbar_drain(bar(X_DONE), 0, wctx, ERR_SITE_CACHE_WEIGHTS + 7);
+    }
     __syncwarp();
   } else {
     // ---------------------------------------------------------------- keys, exponentials, sums
-    const int a = warp >> 2, t = threadIdx.x & 127;
+    const int a = warp >> 2 & 1, part = warp >> 3, t = threadIdx.x & 127;
     constexpr int RB = I4 ? D / 2 : D, PPR = RB / 16;  // bytes, 16-byte pieces of a row
-    constexpr int RPI = 128 / PPR;                     // rows of a load by all threads
-    const int prow = t / PPR, piece = t % PPR;
+    constexpr int RPI = 256 / PPR;                     // rows of a load by all threads of a tile
+    constexpr int LD = 128 / RPI;
+    const int prow = (part * 128 + t) / PPR, piece = t % PPR;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-    uint4 raw_codes[PPR];
-    uint32_t raw_scale[PPR];
+    uint4 raw_codes[LD];
+    uint32_t raw_scale[LD];
     float ks = 0.f;     // of key t; 0: it has no block
     auto page_of = [&](int key) {
       if (key >= walk.seq.len) return -1;
@@ -298,7 +346,7 @@ __global__ void __launch_bounds__(Ww<D>::THREADS, 1)
     auto load = [&]() {  // the codes of the unit that `walk` is at
       const int h = walk.head(), key0 = walk.key0() + a * C::BM;
 #pragma unroll
-      for (int x = 0; x < PPR; ++x) {
+      for (int x = 0; x < LD; ++x) {
         const int key = key0 + x * RPI + prow;
         const int page = page_of(key);
         raw_codes[x] = make_uint4(0u, 0u, 0u, 0u);
@@ -316,7 +364,7 @@ __global__ void __launch_bounds__(Ww<D>::THREADS, 1)
     auto store = [&]() {  // as bf16, rows of 128 bytes, 16-byte columns swizzled by row & 7
       const uint32_t tile = sbase + C::OFF_K + a * C::TILE;
 #pragma unroll
-      for (int x = 0; x < PPR; ++x) {
+      for (int x = 0; x < LD; ++x) {
         const int row = x * RPI + prow;
         const uint32_t w[4] = {raw_codes[x].x, raw_codes[x].y, raw_codes[x].z, raw_codes[x].w};
         auto put = [&](int ch, const uint32_t (&o)[4]) {  // eight channels from ch on
@@ -352,34 +400,37 @@ __global__ void __launch_bounds__(Ww<D>::THREADS, 1)
       fence_proxy_async_smem();
     };
     int i = 0;     // tiles of rows so far, those in which this tile of keys took part
-    int mine = 0;
+    int mine = 0, units = 0;  // and the units in which it did
     bool ok = true;
     if (walk.valid()) load();
     while (ok && walk.valid()) {
-      store();
+      // A tile without keys has no part in the barriers of its keys and of S: its warps may run
+      // ahead of the MMAs by the ring of Q, and would lap them
+      const bool live = a < walk.key_tiles();
+      if (live) {
+        store();
+        mbar_arrive(bar(X_K_FULL + a));
+      }
       const float k_scale = ks, f = ks * p.scale_log2;
-      mbar_arrive(bar(X_K_FULL + a));
       // the unit at hand; `walk` goes on to the next one
       const int b = walk.b, h = walk.head(), len = walk.seq.len, n = walk.seq.n;
       const int key = walk.key0() + a * C::BM + t;
       const int first = walk.first_rows(), row_tiles = walk.row_tiles;
-      const bool part = a < walk.key_tiles();
       const int key_last = walk.key0() + a * C::BM + 127;
       walk.next();
       float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
       for (int j = first; ok && j < row_tiles; ++j, ++i) {
         if (j == row_tiles - 1 && walk.valid()) load();
-        const int stage = i % ST;
-        if (!part) {  // (warp-uniform) nothing but its share of the slot's release
-          ok = __all_sync(0xffffffffu, mbar_wait(q_full0 + 8u * stage, (i / ST) & 1, wctx,
+        const int stage = i % C::INFO;
+        if (!live) {  // (warp-uniform) nothing but its share of the slot's release
+          ok = __all_sync(0xffffffffu, mbar_wait(bar(X_I_FULL + stage), (i / C::INFO) & 1, wctx,
                                                  ERR_SITE_CACHE_WEIGHTS + 8));
-          if (ok && lane == 0) mbar_arrive(q_empty0 + 8u * stage);
+          if (ok && lane == 0) mbar_arrive(bar(X_I_EMPTY + stage));
           continue;
         }
-        const int buf = mine & 1;
-        ok = __all_sync(0xffffffffu, mbar_wait(q_full0 + 8u * stage, (i / ST) & 1, wctx,
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(X_I_FULL + stage), (i / C::INFO) & 1, wctx,
                                                ERR_SITE_CACHE_WEIGHTS + 8) &&
-                                         mbar_wait(bar(X_S_FULL + a * 2 + buf), (mine >> 1) & 1, wctx,
+                                         mbar_wait(bar(X_S_FULL + a), mine & 1, wctx,
                                                    ERR_SITE_CACHE_WEIGHTS + 9));
         ++mine;
         if (!ok) break;
@@ -390,45 +441,68 @@ __global__ void __launch_bounds__(Ww<D>::THREADS, 1)
         const int ahead = p.causal ? key - (len - n) - tok0 : 0;
         const int from = ahead >= p.tile_tokens ? C::BN : max(0, ahead) * p.G;
         const bool diagonal = p.causal && key_last - (len - n) > tok0;
-        const uint32_t info = sbase + C::OFF_INFO + (uint32_t)(stage * C::BN) * 4u;
-        const uint32_t tS = tmem + lane_off + (a * 2 + buf) * C::BN;
-        uint32_t v[2][32];
-        tmem_ld32(tS, v[0]);
+        const uint32_t info = sbase + C::OFF_INFO + (uint32_t)(stage * C::BN + part * 128) * 4u;
+        const uint32_t tS = tmem + lane_off + a * C::BN + part * 128;
+        uint32_t v[32];
+#pragma unroll 1
+        for (int x = 0; x < 4; ++x) {
+          const int col0 = part * 128 + x * 32;
+          if (col0 >= rows) break;  // uniform
+          tmem_ld32(tS + x * 32, v);
+          tmem_wait_ld(v);
+          // exponents of columns k, k + 1 at a time
+          auto term = [&](int k, float l0, float l1, float& e0, float& e1) {
+            fma_x2(__uint_as_float(v[k]), __uint_as_float(v[k + 1]), f, l0, l1, e0, e1);
+            e0 = ex2(e0), e1 = ex2(e1);
+          };
+          const uint32_t li = info + (uint32_t)(x * 32) * 4u;
+          if (diagonal || col0 + 32 > rows) {
 #pragma unroll
-        for (int x = 0; x < C::BN / 32; ++x) {
-          if (x * 32 >= rows) break;  // uniform
-          tmem_wait_ld(v[x & 1]);
-          if (x + 1 < C::BN / 32) tmem_ld32(tS + (x + 1) * 32, v[(x + 1) & 1]);
-          const uint32_t(&s)[32] = v[x & 1];
-          const bool cut = diagonal || x * 32 + 32 > rows;
+            for (int k = 0; k < 32; k += 4) {
+              const float4 l = ld_shared_f4(li + k * 4u);
+              float e[4];
+              term(k, l.x, l.y, e[0], e[1]);
+              term(k + 2, l.z, l.w, e[2], e[3]);
 #pragma unroll
-          for (int k = 0; k < 32; k += 4) {
-            const float4 l = ld_shared_f4(info + (uint32_t)(x * 32 + k) * 4u);
-            float e0, e1, e2, e3;
-            fma_x2(__uint_as_float(s[k]), __uint_as_float(s[k + 1]), f, l.x, l.y, e0, e1);
-            fma_x2(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3]), f, l.z, l.w, e2, e3);
-            e0 = ex2(e0), e1 = ex2(e1), e2 = ex2(e2), e3 = ex2(e3);
-            if (cut) {
-              const int col = x * 32 + k;
-              if (col < from || col >= rows) e0 = 0.f;
-              if (col + 1 < from || col + 1 >= rows) e1 = 0.f;
-              if (col + 2 < from || col + 2 >= rows) e2 = 0.f;
-              if (col + 3 < from || col + 3 >= rows) e3 = 0.f;
+              for (int y = 0; y < 4; ++y)
+                if (col0 + k + y < from || col0 + k + y >= rows) e[y] = 0.f;
+              add_x2(s0, s1, e[0], e[1]);
+              add_x2(s2, s3, e[2], e[3]);
             }
-            add_x2(s0, s1, e0, e1);
-            add_x2(s2, s3, e2, e3);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 32; k += 4) {
+              const float4 l = ld_shared_f4(li + k * 4u);
+              float e0, e1, e2, e3;
+              term(k, l.x, l.y, e0, e1);
+              term(k + 2, l.z, l.w, e2, e3);
+              add_x2(s0, s1, e0, e1);
+              add_x2(s2, s3, e2, e3);
+            }
           }
         }
-        tmem_wait_ld();  // (one load more than was used, where the rows end early)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(bar(X_S_EMPTY + a * 2 + buf));
-          mbar_arrive(q_empty0 + 8u * stage);
+          mbar_arrive(bar(X_S_EMPTY + a));
+          mbar_arrive(bar(X_I_EMPTY + stage));
         }
       }
+      // The sums of columns 128-255 join the others.  (Their place is free: this unit's S came
+      // after both halves had stored its keys, hence after the last unit's sums were read.)
+      float w = (s0 + s1) + (s2 + s3);
+      float* sums = reinterpret_cast<float*>(smem + C::OFF_SUM) + a * C::BM + t;
+      if (!live) continue;
+      if (part == 1) {
+        *sums = w;
+        mbar_arrive(bar(X_SUM + a));
+        continue;
+      }
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(bar(X_SUM + a), units & 1, wctx,
+                                                   ERR_SITE_CACHE_WEIGHTS + 10));
+      ++units;
       if (ok && key < len) {
-        float w = k_scale == 0.f ? 0.f : (s0 + s1) + (s2 + s3);
+        w = k_scale == 0.f ? 0.f : w + *sums;
         if (p.accumulate && key < len - n) w += p.in.p[b * p.in.sb + h * p.in.sh + key];
         p.out.p[b * p.out.sb + h * p.out.sh + key] = w;
       }
