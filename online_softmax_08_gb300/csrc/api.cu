@@ -821,7 +821,7 @@ extern "C" int fattn_cache_evict(const fattn_cache* cache, const fattn_cache_bat
   p.lens_out = lens_out;
   p.kept = kept;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return debug_post_call(launch_cache_evict(p, s) == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA, s);
+  return debug_post_call(launch_cache_evict(p, dev->n_sm, s) == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA, s);
 }
 
 extern "C" int fattn_rope_turns(unsigned long long* turns, float* magnitude, int rot, double base,

@@ -4,15 +4,21 @@
 // among the others, the keep - recent of the largest weight (NaN counts as the largest, of
 // equal ones the first); their order stays.  Shorter sequences are copied whole.
 //
-// 1. Selection, one CTA per (sequence, head).  Weights are taken as unsigned numbers of the
+// 1. Selection, a cluster of CTAs per (sequence, head).  Weights are taken as unsigned numbers of the
 // same order.  The smallest kept one is found digit by digit, 11 + 11 + 10 bits from the top:
 // a histogram in shared memory of the next digit among the weights that agree so far, and the
 // bin in which the count from above reaches what is to be kept.  A last pass in the tokens'
-// order numbers the kept ones by prefix sums.  Every pass reads the weights, which L2 holds.
+// order numbers the kept ones.  The CTAs of a cluster add up their histograms and counts
+// through distributed shared memory, and hold up to 32768 weights each in registers between
+// the passes.  What bounds it is a long row's chain of passes: 8 x 8 rows of up to 32768 weights
+// took 31 us with one CTA a row (54 us when every pass read the weights anew, a thread one at
+// a time).
 // 2. Copy.  The destination blocks are nobody's source, so every one is filled on its own: a
 // CTA per (sequence, head, block).  In 4 bits a token's codes and scales move as they are; in
 // 8 bits the block's scale is the largest of its tokens', and codes of a smaller one are
 // rounded for it, as when append raises a block's scale.
+#include <cooperative_groups.h>
+
 #include <algorithm>
 #include <type_traits>
 
@@ -23,6 +29,8 @@ namespace {
 
 constexpr int kSelect = 1024;  // threads of a selection
 constexpr int kBins = 2048;
+constexpr int kRun = 32;       // weights that a thread of it holds at a time
+constexpr uint32_t kZero = 0x80000000u;  // a weight of zero, as an ordered number
 constexpr int kCopy = 128;     // threads of a copy
 
 __device__ __forceinline__ uint32_t order_of(float w) {
@@ -63,22 +71,40 @@ __device__ __forceinline__ int sum_before(int v, int* part, int* total) {
   return upto - v + low;
 }
 
+// CS: CTAs of a cluster.
+template <int CS>
 __global__ void __launch_bounds__(kSelect) cache_select_kernel(const EvictParams p) {
+  namespace cg = cooperative_groups;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  __shared__ int hist[kBins];
+  __shared__ alignas(8) int hist[2][kBins];  // by turns: a neighbour may still read the last one
   __shared__ int part[32];
   __shared__ int found_bin, found_above;
-  const int b = blockIdx.x / p.c.H, h = blockIdx.x % p.c.H;
-  const int t = threadIdx.x;
-  int* kept = p.kept + (long long)blockIdx.x * p.keep;
+  __shared__ int counts[2][2];    // larger than the smallest kept, equal to it, of a segment
+  const int unit = blockIdx.x / CS, rank = blockIdx.x % CS;
+  const int b = unit / p.c.H, h = unit % p.c.H;
+  const int t = threadIdx.x + rank * kSelect;  // of the cluster's threads
+  constexpr int T = CS * kSelect;
+  int* kept = p.kept + (long long)unit * p.keep;
+  auto cluster_sync = [] {
+    if constexpr (CS > 1)
+      cg::this_cluster().sync();
+    else
+      __syncthreads();
+  };
+  auto of_rank = [](int* x, int r) {
+    if constexpr (CS > 1)
+      return cg::this_cluster().map_shared_rank(x, r);
+    else
+      return x;
+  };
   const int len = length_of(p, b);
   const int n = max(0, min(len, p.keep));
   if (h == 0 && t == 0) p.lens_out[b] = n;
   const float* w = p.in.p + b * p.in.sb + h * p.in.sh;
   float* w_out = p.out.p + b * p.out.sb + h * p.out.sh;
-  for (int j = n + t; j < p.keep; j += kSelect) kept[j] = -1;
+  for (int j = n + t; j < p.keep; j += T) kept[j] = -1;
   if (len <= p.keep) {
-    for (int j = t; j < n; j += kSelect) {
+    for (int j = t; j < n; j += T) {
       kept[j] = j;
       w_out[j] = w[j];
     }
@@ -86,11 +112,29 @@ __global__ void __launch_bounds__(kSelect) cache_select_kernel(const EvictParams
   }
   const int old = len - p.recent;        // those that compete
   const int top = p.keep - p.recent;     // for so many places
-  for (int j = t; j < p.recent; j += kSelect) {
+  for (int j = t; j < p.recent; j += T) {
     kept[top + j] = old + j;
     w_out[top + j] = w[old + j];
   }
   if (top == 0) return;
+
+  // A warp holds a run of `steps` x 32 neighbouring weights of a segment (kRun x kSelect of them;
+  // a sequence that is no longer than that is read once), so the kept ones are numbered by
+  // ballots, and the warps' totals by one prefix sum a segment.
+  const int warp = t >> 5, lane = t & 31;
+  const int steps = min(kRun, (old + T - 1) / T), segment = steps * T;
+  uint32_t u[kRun];
+  auto index = [&](int seg, int i) { return seg + (warp * steps + i) * 32 + lane; };
+  auto load = [&](int seg) {
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) {
+      const int j = index(seg, i);
+      u[i] = i < steps && j < old ? __float_as_uint(w[j]) : 0xffffffffu;  // (NaN, see below)
+    }
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) u[i] = order_of(__uint_as_float(u[i]));
+  };
+  load(0);
 
   // ---------------------------------------------------------------- the smallest kept weight
   uint32_t prefix = 0u, mask = 0u;  // the digits found
@@ -99,30 +143,36 @@ __global__ void __launch_bounds__(kSelect) cache_select_kernel(const EvictParams
   for (int digit = 0; digit < 3; ++digit) {
     const int shift = digit == 0 ? 21 : digit == 1 ? 10 : 0;
     const uint32_t low = digit == 2 ? 0x3ffu : 0x7ffu;
-    for (int i = t; i < kBins; i += kSelect) hist[i] = 0;
+    int* bins = hist[digit & 1];
+    for (int i = threadIdx.x; i < kBins; i += kSelect) bins[i] = 0;
     __syncthreads();
-    for (int j0 = 0; j0 < old; j0 += kSelect) {
-      const int j = j0 + t;
-      const uint32_t u = j < old ? order_of(w[j]) : 0u;
-      const bool on = j < old && (u & mask) == prefix;
-      const int bin = (int)(u >> shift & low);
-      // lanes that agree with the first of them count as one (many weights are zero)
-      const unsigned act = __ballot_sync(0xffffffffu, on);
-      if (act == 0u) continue;
-      const int leader = __ffs(act) - 1;
-      const int lead = __shfl_sync(0xffffffffu, bin, leader);
-      const unsigned same = __ballot_sync(0xffffffffu, on && bin == lead);
-      if ((t & 31) == leader) atomicAdd(&hist[lead], __popc(same));
-      if (on && bin != lead) atomicAdd(&hist[bin], 1);
+    int zeros = 0;  // many weights are zero, and would all add to one bin: counted by the warp
+#pragma unroll 1
+    for (int seg = 0; seg < old; seg += segment) {
+      if (old > segment) load(seg);
+#pragma unroll
+      for (int i = 0; i < kRun; ++i) {
+        if (i >= steps) break;
+        const bool on = index(seg, i) < old && (u[i] & mask) == prefix, zero = u[i] == kZero;
+        zeros += __popc(__ballot_sync(0xffffffffu, on && zero));
+        if (on && !zero) atomicAdd(&bins[u[i] >> shift & low], 1);
+      }
     }
-    __syncthreads();
-    // bins from the top: this thread's two are kBins - 1 - 2 t and the one below
-    const int h0 = hist[kBins - 1 - 2 * t], h1 = hist[kBins - 2 - 2 * t];
+    if (lane == 0 && zeros > 0) atomicAdd(&bins[kZero >> shift & low], zeros);
+    cluster_sync();
+    // bins from the top: this thread's two are kBins - 1 - 2 i and the one below
+    const int top_bin = kBins - 1 - 2 * (int)threadIdx.x;
+    int h0 = 0, h1 = 0;
+#pragma unroll
+    for (int r = 0; r < CS; ++r) {
+      const int2 x = *reinterpret_cast<const int2*>(of_rank(bins, r) + top_bin - 1);
+      h0 += x.y, h1 += x.x;
+    }
     int total;
     const int above = sum_before(h0 + h1, part, &total);
-    if (above < need && above + h0 >= need) found_bin = kBins - 1 - 2 * t, found_above = above;
+    if (above < need && above + h0 >= need) found_bin = top_bin, found_above = above;
     if (above + h0 < need && above + h0 + h1 >= need)
-      found_bin = kBins - 2 - 2 * t, found_above = above + h0;
+      found_bin = top_bin - 1, found_above = above + h0;
     __syncthreads();
     prefix |= (uint32_t)found_bin << shift;
     mask |= low << shift;
@@ -131,25 +181,54 @@ __global__ void __launch_bounds__(kSelect) cache_select_kernel(const EvictParams
   }
 
   // ---------------------------------------------------------------- the kept ones, in order
-  int placed = 0, equal = 0;  // before this step: kept, equal to the smallest
+  int more0 = 0, ties0 = 0;  // in the segments before: larger than the smallest kept, equal to it
 #pragma unroll 1
-  for (int j0 = 0; j0 < old; j0 += kSelect) {
-    const int j = j0 + t;
-    const float x = j < old ? w[j] : 0.f;
-    const uint32_t u = j < old ? order_of(x) : 0u;
-    const bool more = j < old && u > prefix, tie = j < old && u == prefix;
-    int both;  // at most kSelect of either: two sums in one
-    const int sums = sum_before((more ? 1 : 0) | (tie ? 1 << 16 : 0), part, &both);
-    const int ties = equal + (sums >> 16);
-    const bool on = more || (tie && ties < need);
-    const int at = placed + (sums & 0xffff) + min(ties, need) - min(equal, need);
-    if (on) {
-      kept[at] = j;
-      w_out[at] = x;
+  for (int seg = 0, turn = 0; seg < old; seg += segment, turn ^= 1) {
+    if (old > segment) load(seg);
+    int more = 0, ties = 0;  // of the warp
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) {
+      if (i >= steps) break;
+      const bool in = index(seg, i) < old;
+      more += __popc(__ballot_sync(0xffffffffu, in && u[i] > prefix));
+      ties += __popc(__ballot_sync(0xffffffffu, in && u[i] == prefix));
     }
-    placed += (both & 0xffff) + min(equal + (both >> 16), need) - min(equal, need);
-    equal += both >> 16;
+    int all_more, all_ties;
+    more = more0 + sum_before(lane == 0 ? more : 0, part, &all_more);
+    ties = ties0 + sum_before(lane == 0 ? ties : 0, part, &all_ties);
+    more = __shfl_sync(0xffffffffu, more, 0);
+    ties = __shfl_sync(0xffffffffu, ties, 0);
+    if constexpr (CS > 1) {  // and of the CTAs in front
+      if (threadIdx.x == 0) counts[turn][0] = all_more, counts[turn][1] = all_ties;
+      cluster_sync();
+      all_more = all_ties = 0;
+#pragma unroll
+      for (int r = 0; r < CS; ++r) {
+        const int* x = of_rank(counts[turn], r);
+        const int m = x[0], e = x[1];
+        if (r < rank) more += m, ties += e;
+        all_more += m, all_ties += e;
+      }
+    }
+    const unsigned before = (1u << lane) - 1u;
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) {
+      if (i >= steps) break;
+      const int j = index(seg, i);
+      const bool in = j < old;
+      const unsigned m = __ballot_sync(0xffffffffu, in && u[i] > prefix);
+      const unsigned e = __ballot_sync(0xffffffffu, in && u[i] == prefix);
+      const int ties_here = ties + __popc(e & before);
+      if ((m >> lane & 1u) || ((e >> lane & 1u) && ties_here < need)) {
+        const int at = more + __popc(m & before) + min(ties_here, need);
+        kept[at] = j;
+        w_out[at] = w[j];
+      }
+      more += __popc(m), ties += __popc(e);
+    }
+    more0 += all_more, ties0 += all_ties;
   }
+  if constexpr (CS > 1) cluster_sync();  // nobody's shared memory goes while it is read
 }
 
 struct Source {
@@ -253,14 +332,34 @@ __global__ void __launch_bounds__(kCopy) cache_copy_kernel(const EvictParams p, 
   }
 }
 
+template <int CS>
+cudaError_t launch_select(const EvictParams& p, long long units, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = CS;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.gridDim = dim3((unsigned)(units * CS));
+  cfg.blockDim = dim3(kSelect);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, cache_select_kernel<CS>, p);
+}
+
 template <int D, int FMT>
-cudaError_t start(const EvictParams& p, cudaStream_t stream) {
+cudaError_t start(const EvictParams& p, int n_sm, cudaStream_t stream) {
   const long long units = (long long)p.c.B * p.c.H;
   const long long most = std::min<long long>(p.keep, p.width);  // tokens of a sequence
   const int blocks = (int)((most + p.c.block_size - 1) / p.c.block_size);
   if (units * blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  cache_select_kernel<<<(unsigned)units, kSelect, 0, stream>>>(p);
-  cudaError_t e = cudaGetLastError();
+  // As many CTAs a row (up to 8) as leave none waiting for an SM, which one fills, and as have
+  // two weights a thread.
+  const auto fits = [&](int cs) { return units * cs <= n_sm && p.width >= 2 * cs * kSelect; };
+  cudaError_t e = fits(8)   ? launch_select<8>(p, units, stream)
+                  : fits(4) ? launch_select<4>(p, units, stream)
+                  : fits(2) ? launch_select<2>(p, units, stream)
+                            : launch_select<1>(p, units, stream);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr{};
@@ -276,15 +375,15 @@ cudaError_t start(const EvictParams& p, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_cache_evict(const EvictParams& p, cudaStream_t stream) {
+cudaError_t launch_cache_evict(const EvictParams& p, int n_sm, cudaStream_t stream) {
   const bool d128 = p.c.d == 128;
   switch (p.c.format) {
     case FMT_E4M3:
-      return d128 ? start<128, FMT_E4M3>(p, stream) : start<64, FMT_E4M3>(p, stream);
+      return d128 ? start<128, FMT_E4M3>(p, n_sm, stream) : start<64, FMT_E4M3>(p, n_sm, stream);
     case FMT_E5M2:
-      return d128 ? start<128, FMT_E5M2>(p, stream) : start<64, FMT_E5M2>(p, stream);
+      return d128 ? start<128, FMT_E5M2>(p, n_sm, stream) : start<64, FMT_E5M2>(p, n_sm, stream);
     default:
-      return d128 ? start<128, FMT_INT4>(p, stream) : start<64, FMT_INT4>(p, stream);
+      return d128 ? start<128, FMT_INT4>(p, n_sm, stream) : start<64, FMT_INT4>(p, n_sm, stream);
   }
 }
 

@@ -43,6 +43,6 @@ struct EvictParams {
   int* lens_out;
   int* kept;           // [B, H, keep]
 };
-cudaError_t launch_cache_evict(const EvictParams& p, cudaStream_t stream);
+cudaError_t launch_cache_evict(const EvictParams& p, int n_sm, cudaStream_t stream);
 
 }  // namespace fattn
