@@ -26,7 +26,7 @@ namespace {
 constexpr int kWarpsW = 4;
 constexpr int kKeys = 128;     // of a unit
 constexpr int kRows = 32;      // staged at a time
-constexpr int kCtasW = 4;      // per SM
+constexpr int ctas_w(int d) { return d == 128 ? 3 : 4; }  // per SM: as the registers allow
 constexpr float kLog2eW = 1.4426950408889634f;
 
 template <int D>
@@ -57,14 +57,14 @@ __device__ __forceinline__ int piece_channel(int u, int t) {
 }
 
 template <int D, int FMT>
-__global__ void __launch_bounds__(32 * kWarpsW, kCtasW)
+__global__ void __launch_bounds__(32 * kWarpsW, ctas_w(D))
     cache_weights_kernel(const WeightParams p) {
   constexpr bool I4 = FMT == FMT_INT4, E5M2 = FMT == FMT_E5M2;
   using C = Wt<D>;
   constexpr int KS = D / 16;  // k16 steps
   __shared__ alignas(128) uint8_t rows_smem[kRows * C::STRIDE];
-  __shared__ float row_scale[kRows], row_lse[kRows];
-  __shared__ int row_lim[kRows];
+  __shared__ alignas(8) float row_scale[kRows], row_lse[kRows];
+  __shared__ alignas(8) int row_lim[kRows];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const CacheParams& c = p.c;
   const uint32_t qs = smem_u32(rows_smem);
@@ -110,79 +110,147 @@ __global__ void __launch_bounds__(32 * kWarpsW, kCtasW)
     }
     before += __shfl_sync(0xffffffffu, upto, 31);
   }
-  long long mine = units_of(b, &seq);
-
   const Int4Magic magic;
-  int staged_b = -1, staged_h = -1;  // whose rows (all of them) lie in shared memory
-  for (long long unit = lo; unit < hi; ++unit) {
-    while (unit >= before + mine) {
-      before += mine;
-      mine = units_of(++b, &seq);
+  const float factor = p.scale_log2 * (I4 ? kInt4Unit : 1.f);
+  // A place in the list of units.  Three are alive: the one at hand, the next one, whose codes
+  // are on their way, and the one behind it, whose block numbers are.
+  struct At {
+    long long left;  // units of the share from here on
+    int b, h, key, keys;  // sequence, head, first key; keys of the sequence's units
+    CacheSeq seq;
+  };
+  auto advance = [&](At* at) {
+    if (--at->left <= 0 || (at->key += kKeys) < at->keys) return;
+    at->key = 0;
+    if (++at->h < c.H) return;
+    at->h = 0;
+    while (units_of(++at->b, &at->seq) == 0) {
     }
-    const int tiles = (seq.len + kKeys - 1) / kKeys;
-    const int h = (int)((unit - before) / tiles);
-    const int key0 = (int)((unit - before) % tiles) * kKeys + warp * 32;
+    at->keys = (at->seq.len + kKeys - 1) / kKeys * kKeys;
+  };
+  constexpr int RB = I4 ? D / 2 : D;      // bytes of a key's codes
+  constexpr int RW = I4 ? C::U : D / 16;  // words of codes that a lane has of a key
+  int pages[2];
+  uint32_t codes[2][2][RW], scales[2][2];
+  float ks_next[2] = {1.f, 1.f};
+  bool live[2];
+  auto look_up = [&](const At& at) {
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      pages[m] = -1;
+      if (at.left <= 0) continue;
+      const int key = at.key + warp * 32 + 16 * m;
+      if (key >= at.seq.len) continue;
+      const int page = c.block_table[(long long)at.b * c.table_width + (key >> c.block_log2)];
+      pages[m] = page == -1 ? -2 : page;  // (-1: no keys there)
+    }
+  };
+  auto load = [&](const At& at) {  // from the pages looked up for it
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      const int key = at.key + warp * 32 + 16 * m;
+      int page = pages[m];
+      if (page != -1 && (page < 0 || page >= c.num_blocks)) {
+        if (c.err) atomicCAS(c.err, 0u, (unsigned)ERR_SITE_CACHE_WEIGHTS + 1);
+        page = -1;
+      }
+      live[m] = page >= 0;
+      if constexpr (!I4) ks_next[m] = page < 0 ? 1.f : c.k_scale[(long long)page * c.H + at.h];
+      // (rows behind the sequence's end are read as well: they lie in its block)
+      const long long row =
+          ((((long long)page * c.H + at.h) << c.block_log2) + (key & (c.block_size - 1))) + g;
+      const uint8_t* from = c.k + row * RB + t * (I4 ? D / 8 : 16);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        uint32_t(&w)[RW] = codes[m][i];
+#pragma unroll
+        for (int x = 0; x < RW; ++x) w[x] = 0u;
+        scales[m][i] = 0u;
+        if (page < 0) continue;
+        if constexpr (I4 && D == 128) {
+          const uint4 x = __ldg(reinterpret_cast<const uint4*>(from + i * 8 * RB));
+          w[0] = x.x, w[1] = x.y, w[RW - 2] = x.z, w[RW - 1] = x.w;
+          scales[m][i] = __ldg(reinterpret_cast<const uint16_t*>(c.k_scale4 + row * 8 + t * 2 + i * 64));
+        } else if constexpr (I4) {
+          const uint2 x = __ldg(reinterpret_cast<const uint2*>(from + i * 8 * RB));
+          w[0] = x.x, w[1] = x.y;
+          scales[m][i] = __ldg(c.k_scale4 + row * 4 + t + i * 32);
+        } else {
+#pragma unroll
+          for (int half = 0; half < D / 64; ++half) {
+            const uint4 x = __ldg(reinterpret_cast<const uint4*>(from + i * 8 * RB + half * 64));
+            w[half * 4] = x.x, w[half * 4 + 1] = x.y, w[half * 4 + 2] = x.z, w[half * 4 + 3] = x.w;
+          }
+        }
+      }
+    }
+  };
+  At now{hi - lo, b, 0, 0, 0, {}};
+  {
+    units_of(b, &now.seq);
+    const int tiles = (now.seq.len + kKeys - 1) / kKeys;
+    now.h = (int)((lo - before) / tiles);
+    now.key = (int)((lo - before) % tiles) * kKeys;
+    now.keys = tiles * kKeys;
+  }
+  At next = now;
+  look_up(now);
+  load(now);
+  advance(&next);
+  look_up(next);
+
+  int staged_b = -1, staged_h = -1;  // whose rows (all of them) lie in shared memory
+  while (now.left > 0) {
+    const int b = now.b, h = now.h, cta_key0 = now.key, key0 = cta_key0 + warp * 32;
+    const CacheSeq seq = now.seq;
     const int n_rows = seq.n * p.G;
     const int seen0 = p.causal ? seq.len - seq.n + 1 : seq.len;  // token 0's keys
 
     // ------------------------------------------------------------ the warp's keys
     uint32_t a[2][KS][4];
-    float ks[2];
+    const float ks[2] = {ks_next[0], ks_next[1]};
+    const bool there[2] = {live[0], live[1]};
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
-      const int key = key0 + 16 * m;
-      int page = -1;
-      if (key < seq.len) {
-        page = c.block_table[(long long)b * c.table_width + (key >> c.block_log2)];
-        if (page < 0 || page >= c.num_blocks) {
-          if (c.err) atomicCAS(c.err, 0u, (unsigned)ERR_SITE_CACHE_WEIGHTS + 1);
-          page = -1;
-        }
-      }
-      ks[m] = page < 0 ? 0.f : I4 ? kInt4Unit : c.k_scale[(long long)page * c.H + h];
-      const long long row0 =
-          ((((long long)max(page, 0) * c.H + h) << c.block_log2) + (key & (c.block_size - 1)));
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const long long row = row0 + g + 8 * i;
-        const bool on = page >= 0 && key + g + 8 * i < seq.len;
         if constexpr (I4) {
-          uint32_t w[C::U], s2 = 0u;
-          const uint8_t* at = c.k + row * (D / 2) + t * (D / 8);
-#pragma unroll
-          for (int u = 0; u < C::U; u += 2) {
-            const uint2 x = on ? __ldg(reinterpret_cast<const uint2*>(at + u * 4)) : make_uint2(0u, 0u);
-            w[u] = x.x, w[u + 1] = x.y;
-          }
-          if (on) {
-            const uint8_t* s = c.k_scale4 + row * (D / 16) + t * (D / 64);
-            s2 = D == 128 ? (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(s)) : (uint32_t)__ldg(s);
-          }
+          const Int4Scale s0 = int4_scale(__byte_perm(scales[m][i], 0u, 0x0404u));
+          const Int4Scale s1 = D == 128 ? int4_scale(__byte_perm(scales[m][i], 0u, 0x1414u)) : s0;
 #pragma unroll
           for (int u = 0; u < C::U; ++u) {
             uint32_t o[4];
-            int4_values(w[u], int4_scale(__byte_perm(s2, 0u, u < 2 ? 0x0404u : 0x1414u)), magic, o);
+            int4_values(codes[m][i][u], u < 2 ? s0 : s1, magic, o);
             a[m][2 * u][i] = o[0], a[m][2 * u][i + 2] = o[1];
             a[m][2 * u + 1][i] = o[2], a[m][2 * u + 1][i + 2] = o[3];
           }
         } else {
 #pragma unroll
-          for (int half = 0; half < D / 64; ++half) {
-            const uint4 x =
-                on ? __ldg(reinterpret_cast<const uint4*>(c.k + row * D + half * 64 + t * 16))
-                   : make_uint4(0u, 0u, 0u, 0u);
-            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              codes4_to_f16<E5M2>(w[j], a[m][half * 4 + j][i], a[m][half * 4 + j][i + 2]);
-          }
+          for (int w = 0; w < RW; ++w)
+            codes4_to_f16<E5M2>(codes[m][i][w], a[m][w][i], a[m][w][i + 2]);
         }
       }
     }
+    const long long first = key0 + g;
+    float* const out = p.out.p + (b * p.out.sb + h * p.out.sh + first);
+    const float* const in = p.in.p + (b * p.in.sb + h * p.in.sh + first);
+    const int ends = seq.len - (int)first;                // keys of this lane behind it
+    const int older = p.accumulate ? ends - seq.n : 0;    // those that had a weight before
+    float was[2][2];  // of the lanes that write
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int x = 16 * m + 8 * i;
+        was[m][i] = t == 0 && x < older ? in[x] : 0.f;
+      }
+    load(next);
+    now = next;
+    advance(&next);
+    look_up(next);
 
     // ------------------------------------------------------------ all rows that see some of them
     float sum[2][2] = {{0.f, 0.f}, {0.f, 0.f}};  // of keys g, g + 8 (+ 16 m), this lane's columns
-    const int cta_key0 = (int)((unit - before) % tiles) * kKeys;
     // (in 64 bits: a token's number times the group's size.)  Rows that are kept are all there
     const int r_first = p.causal && n_rows > kRows
                             ? (int)((long long)max(0, cta_key0 - (seq.len - seq.n)) * p.G / 8 * 8)
@@ -192,8 +260,10 @@ __global__ void __launch_bounds__(32 * kWarpsW, kCtasW)
         __syncthreads();  // the rows before have been used
         // a row is taken by PIECES lanes, 16 bytes each
         constexpr int RPP = 32 * kWarpsW / C::PIECES;  // rows a pass
+        const int staged = min(kRows, n_rows - r0);
 #pragma unroll
         for (int pass = 0; pass < kRows / RPP; ++pass) {
+          if (pass * RPP >= staged) break;
           const int r = pass * RPP + threadIdx.x / C::PIECES, piece = threadIdx.x % C::PIECES;
           const int i = r0 + r;
           const int u = piece % C::U, tt = piece / C::U;
@@ -226,7 +296,7 @@ __global__ void __launch_bounds__(32 * kWarpsW, kCtasW)
           st_shared_v4(qs + r * C::STRIDE + (u * 4 + tt) * 16, o[0], o[1], o[2], o[3]);
           if (piece == 0) {
             const float l = i < n_rows ? p.lse[(long long)hq * c.total + token] : -INFINITY;
-            row_scale[r] = __uint_as_float((uint32_t)(127 - e) << 23) * p.scale_log2;
+            row_scale[r] = __uint_as_float((uint32_t)(127 - e) << 23) * factor;
             row_lse[r] = l == -INFINITY ? INFINITY : l * kLog2eW;  // a row that saw nothing
             row_lim[r] = i < n_rows ? min(seq.len, p.causal ? seen0 + p.by_G.div(i) : seen0) : 0;
           }
@@ -256,23 +326,26 @@ __global__ void __launch_bounds__(32 * kWarpsW, kCtasW)
           }
         }
         // columns 2 t, 2 t + 1
-        float f[2], l[2];
-        int lim[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          f[i] = row_scale[nt * 8 + 2 * t + i];
-          l[i] = row_lse[nt * 8 + 2 * t + i];
-          lim[i] = row_lim[nt * 8 + 2 * t + i];
-        }
-        const bool masked = key0 + 32 > min(lim[0], lim[1]);
+        const float2 f2 = *reinterpret_cast<const float2*>(&row_scale[nt * 8 + 2 * t]);
+        const float2 l2 = *reinterpret_cast<const float2*>(&row_lse[nt * 8 + 2 * t]);
+        const float f[2] = {f2.x, f2.y}, l[2] = {l2.x, l2.y};
 #pragma unroll
         for (int m = 0; m < 2; ++m)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float w = ex2(fmaf(s[m][i], ks[m] * f[i & 1], -l[i & 1]));
-            if (masked && key0 + 16 * m + g + 8 * (i >> 1) >= lim[i & 1]) w = 0.f;
-            sum[m][i >> 1] += w;
-          }
+          for (int i = 0; i < 4; ++i) s[m][i] = ex2(fmaf(s[m][i], I4 ? f[i & 1] : ks[m] * f[i & 1], -l[i & 1]));
+        if (key0 + 32 > seen0) {  // some row may not see all of them
+          const int2 lim2 = *reinterpret_cast<const int2*>(&row_lim[nt * 8 + 2 * t]);
+          const int lim[2] = {lim2.x, lim2.y};
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (key0 + 16 * m + g + 8 * (i >> 1) >= lim[i & 1]) s[m][i] = 0.f;
+        }
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) sum[m][i] += s[m][2 * i] + s[m][2 * i + 1];
       }
     }
 #pragma unroll
@@ -282,19 +355,15 @@ __global__ void __launch_bounds__(32 * kWarpsW, kCtasW)
         float x = sum[m][i];
         x += __shfl_xor_sync(0xffffffffu, x, 1);
         x += __shfl_xor_sync(0xffffffffu, x, 2);
-        const int key = key0 + 16 * m + g + 8 * i;
-        if (t == 0 && key < seq.len) {
-          if (ks[m] == 0.f) x = 0.f;  // no block there
-          if (p.accumulate && key < seq.len - seq.n) x += p.in.p[b * p.in.sb + h * p.in.sh + key];
-          p.out.p[b * p.out.sb + h * p.out.sh + key] = x;
-        }
+        // (no block there: nothing from the queries)
+        if (t == 0 && 16 * m + 8 * i < ends) out[16 * m + 8 * i] = was[m][i] + (there[m] ? x : 0.f);
       }
   }
 }
 
 template <int D, int FMT>
 cudaError_t start(const WeightParams& p, int n_sm, cudaStream_t stream) {
-  cache_weights_kernel<D, FMT><<<(unsigned)(n_sm * kCtasW), 32 * kWarpsW, 0, stream>>>(p);
+  cache_weights_kernel<D, FMT><<<(unsigned)(n_sm * ctas_w(D)), 32 * kWarpsW, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
