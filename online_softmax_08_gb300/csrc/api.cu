@@ -592,6 +592,7 @@ int cache_move(CacheMove launch, const fattn_cache* cache, const fattn_cache_bat
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   CacheParams p = cache_params(cache, batch, dev->err);
   p.l2_bytes = dev->l2_bytes;
+  p.n_sm = dev->n_sm;
   const cudaError_t e =
       launch(p, token_view(k, kst, ksh, T, H), token_view(v, vst, vsh, T, H), s);
   return debug_post_call(e == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA, s);

@@ -51,6 +51,7 @@ struct CacheParams {
   const int* cu_seqlens;
   int B, table_width, total, max_seqlen;
   long long l2_bytes;    // of the device (append)
+  int n_sm;              // of the device (append and read in 4 bits)
   unsigned int* err;
 };
 // A packed [total, heads, d] tensor by element strides.
@@ -226,6 +227,27 @@ __device__ __forceinline__ void int4_values(uint32_t w, const Int4Scale& s, cons
   o[1] = fma_f16x2(nibbles<1>(w, m.m64), s.s, s.hi);
   o[2] = fma_f16x2(nibbles<0>(u, m.m1024), s.s, s.lo);
   o[3] = fma_f16x2(nibbles<1>(u, m.m64), s.s, s.hi);
+}
+// The same in bf16, eight codes of one scale in their order: a code in the mantissa of 128
+// (0x4300) is 128 + c, and (128 + c) s - 136 s = (c - 8) s, every term exact for any scale.
+struct Bf16Scale {
+  uint32_t s, off;  // pairs: s, -136 s
+};
+__device__ __forceinline__ Bf16Scale bf16_scale(uint32_t e5m2) {
+  const float s = f16x2_to_f32(e5m2 << 8).x;
+  return Bf16Scale{pack_bf16x2(s, s), pack_bf16x2(-136.f * s, -136.f * s)};
+}
+__device__ __forceinline__ void bf16_values(uint32_t w, const Bf16Scale& s, uint32_t* o) {
+  uint32_t v[4];  // (c_i, c_i+4)
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;"  // (a & b) | c
+        : "=r"(v[i])
+        : "r"(w >> (4 * i)), "n"(0x000f000f), "r"(0x43004300u));
+    asm("fma.rn.bf16x2 %0, %0, %1, %2;" : "+r"(v[i]) : "r"(s.s), "r"(s.off));
+  }
+  o[0] = __byte_perm(v[0], v[1], 0x5410u), o[1] = __byte_perm(v[2], v[3], 0x5410u);
+  o[2] = __byte_perm(v[0], v[1], 0x7632u), o[3] = __byte_perm(v[2], v[3], 0x7632u);
 }
 // The scales of a word that append never writes (above 7168, infinite, NaN) as zeros.
 __device__ __forceinline__ uint32_t int4_sane(uint32_t bytes) {

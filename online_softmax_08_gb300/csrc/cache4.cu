@@ -15,11 +15,15 @@
 // nothing else becomes one; adding 1544 rounds that to the nearest whole number, ties to
 // even, and leaves the code in the low four bits.
 //
-// The bound is memory.  A thread holds one group: 32 bytes of bf16 and 8 + 1 of the cache.
+// The bound is memory, and next to it the logic pipe, which the quantising of a group takes
+// 70 % of while it is written (measured: 32768 tokens of 16 heads, d = 128, 60 us written, 57
+// read back, 84 and 89 % of the measured copy bandwidth).
+// A thread holds one group: 32 bytes of bf16 and 8 + 1 of the cache.
 // A warp takes kIter x 32 groups of one head: the rows of 16 (d = 64: 32) packed tokens one
-// behind another, so a prompt's codes and scales are written as whole lines.  The values are
-// on their way while the tokens' places are looked up.  Bad entries of the batch are looked
-// for by the first warps, so that one without tokens is found as well.
+// behind another, so a prompt's codes and scales are written as whole lines, then the same of
+// its further heads, for which the tokens' places need not be looked up again.  The first
+// values are on their way while they are.  Bad entries of the batch are looked for by the
+// first warps, so that one without tokens is found as well.
 #include "cache.cuh"
 
 namespace fattn {
@@ -35,9 +39,9 @@ struct Quad {
   static constexpr int TOK = kIter * RPI;   // tokens of a warp
 };
 
-// Row of packed token `tok` in the pool, (block * H + h) * block_size + row; -1: no such
+// Row of packed token `tok` of head 0 in the pool, block * H * block_size + row; -1: no such
 // token, -2: a token without a place.  Called by whole warps for tok0 + lane.
-__device__ __forceinline__ long long place_of(const CacheParams& c, int h, int tok0, int count,
+__device__ __forceinline__ long long place_of(const CacheParams& c, int tok0, int count,
                                               uint32_t site) {
   const int lane = threadIdx.x & 31, tok = tok0 + lane;
   const int b0 = warp_search(c.B, (long long)tok0, [&](int b) { return (long long)c.cu_seqlens[b]; });
@@ -74,7 +78,7 @@ __device__ __forceinline__ long long place_of(const CacheParams& c, int h, int t
     if (c.err) atomicCAS(c.err, 0u, site + 1);
     return -2;
   }
-  return (((long long)page * c.H + h) << c.block_log2) + (pos & (c.block_size - 1));
+  return (((long long)page * c.H) << c.block_log2) + (pos & (c.block_size - 1));
 }
 
 __device__ __forceinline__ void check_batch(const CacheParams& c, long long first, long long step,
@@ -86,22 +90,39 @@ __device__ __forceinline__ void check_batch(const CacheParams& c, long long firs
   }
 }
 
-// The side, head and first token of a warp's work.
+// A warp's work: the side, `heads` heads from h on, and the tokens.
 struct Work {
   bool value;
-  int h, tok0, count;
+  int h, h_end, tok0, count;
 };
 template <int D>
-__device__ __forceinline__ bool find_work(const CacheParams& c, Work* w) {
-  long long i = (long long)blockIdx.x * kWarps4 + (threadIdx.x >> 5);
-  const int side_head = (int)(i % (2 * c.H));
-  i /= 2 * c.H;
-  w->value = side_head >= c.H;
-  w->h = side_head - (w->value ? c.H : 0);
-  if (i * Quad<D>::TOK >= c.total) return false;
-  w->tok0 = (int)i * Quad<D>::TOK;
+__device__ __forceinline__ bool find_work(const CacheParams& c, int heads, Work* w) {
+  w->value = blockIdx.z != 0;
+  w->h = ((int)blockIdx.y * kWarps4 + (int)(threadIdx.x >> 5)) * heads;
+  w->h_end = min(c.H, w->h + heads);
+  w->tok0 = (int)blockIdx.x * Quad<D>::TOK;
   w->count = min(Quad<D>::TOK, c.total - w->tok0);
-  return true;
+  return w->h < c.H;
+}
+__device__ __forceinline__ void check_entries(const CacheParams& c, uint32_t site) {
+  if (blockIdx.y == 0 && blockIdx.z == 0)
+    check_batch(c, (long long)blockIdx.x * blockDim.x + threadIdx.x,
+                (long long)gridDim.x * blockDim.x, site);
+}
+
+// 32 bytes, in one store (V8: 32-byte aligned) or two, each of which leaves half of every
+// sector to the other (reading back the prompt above: 57 us and 61).
+template <bool V8>
+__device__ __forceinline__ void store32(uint16_t* p, const uint32_t (&x)[8]) {
+  if constexpr (V8) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]),
+                 "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+                 : "memory");
+  } else {
+    uint4* to = reinterpret_cast<uint4*>(p);
+    to[0] = make_uint4(x[0], x[1], x[2], x[3]);
+    to[1] = make_uint4(x[4], x[5], x[6], x[7]);
+  }
 }
 
 // bf16 pairs with NaN as zero and magnitudes beyond 57344 as that
@@ -119,127 +140,160 @@ __device__ __forceinline__ void tame(uint32_t (&x)[8], uint32_t* mx) {
 
 template <int D>
 __global__ void __launch_bounds__(32 * kWarps4)
-    cache4_append_kernel(const CacheParams c, const TokenView kv, const TokenView vv) {
+    cache4_append_kernel(const CacheParams c, const TokenView kv, const TokenView vv, int heads) {
   using Q = Quad<D>;
-  check_batch(c, (long long)blockIdx.x * blockDim.x + threadIdx.x,
-              (long long)gridDim.x * blockDim.x, ERR_SITE_CACHE_APPEND);
+  check_entries(c, ERR_SITE_CACHE_APPEND);
   Work w;
-  if (!find_work<D>(c, &w)) return;
+  if (!find_work<D>(c, heads, &w)) return;
   const int lane = threadIdx.x & 31, group = lane % Q::LPR;
   const TokenView& from = w.value ? vv : kv;
-  const uint16_t* src = from.p + (long long)w.tok0 * from.st + (long long)w.h * from.sh + group * 16;
+  const uint16_t* src = from.p + (long long)(w.tok0 + lane / Q::LPR) * from.st +
+                        (long long)w.h * from.sh + group * 16;
+  const long long step = Q::RPI * from.st;
   uint32_t x[kIter][8];
+  auto load = [&]() {
 #pragma unroll
-  for (int j = 0; j < kIter; ++j) {
-    const int r = j * Q::RPI + lane / Q::LPR;
-    uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
-    if (r < w.count) {
-      const uint4* at = reinterpret_cast<const uint4*>(src + (long long)r * from.st);
-      a = __ldg(at);
-      b = __ldg(at + 1);
+    for (int j = 0; j < kIter; ++j) {
+      uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
+      if (j * Q::RPI + lane / Q::LPR < w.count) {
+        const uint4* at = reinterpret_cast<const uint4*>(src + j * step);
+        a = __ldg(at);
+        b = __ldg(at + 1);
+      }
+      x[j][0] = a.x, x[j][1] = a.y, x[j][2] = a.z, x[j][3] = a.w;
+      x[j][4] = b.x, x[j][5] = b.y, x[j][6] = b.z, x[j][7] = b.w;
     }
-    x[j][0] = a.x, x[j][1] = a.y, x[j][2] = a.z, x[j][3] = a.w;
-    x[j][4] = b.x, x[j][5] = b.y, x[j][6] = b.z, x[j][7] = b.w;
-  }
-  const long long place = place_of(c, w.h, w.tok0, w.count, ERR_SITE_CACHE_APPEND);
+  };
+  load();
+  const long long place = place_of(c, w.tok0, w.count, ERR_SITE_CACHE_APPEND);
   uint8_t* codes = w.value ? c.v : c.k;
   uint8_t* scales = w.value ? c.v_scale4 : c.k_scale4;
+  long long places[kIter];
 #pragma unroll
   for (int j = 0; j < kIter; ++j) {
-    const long long at = __shfl_sync(0xffffffffu, place, j * Q::RPI + lane / Q::LPR);
-    uint32_t m2 = 0u, s2 = 0x80008000u;  // largest magnitudes; largest values
+    places[j] = __shfl_sync(0xffffffffu, place, j * Q::RPI + lane / Q::LPR);
+    if (places[j] >= 0) places[j] += (long long)w.h << c.block_log2;
+  }
+  for (int h = w.h;;) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m2 = __vmaxu2(m2, x[j][i] & 0x7fff7fffu);
-    uint32_t mx = max(m2 & 0xffffu, m2 >> 16);
-    if (mx > 0x4760u) tame(x[j], &mx);
+    for (int j = 0; j < kIter; ++j) {
+      const long long at = places[j];
+      if (at >= 0) places[j] += c.block_size;  // the next head's
+      uint32_t m2 = 0u, s2 = 0x80008000u;  // largest magnitudes; largest values
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s2 = __vmaxs2(s2, x[j][i]);
-    const int top = max((int)(short)(s2 & 0xffffu), (int)(short)(s2 >> 16));
-    const float a = __uint_as_float(mx << 16) * 0.125f;
-    const float signed_a = top == (int)mx ? -a : a;
-    const uint32_t s8 = f32_to_codes<true>(signed_a, 0.f) & 0xffu;
-    // the scale's value: the upper byte of an fp16
-    const float s = f16x2_to_f32(s8 << 8).x;
-    const float inv = s == 0.f ? 0.f : __frcp_rn(s);
-    uint32_t word[2];
+      for (int i = 0; i < 8; ++i) m2 = __vmaxu2(m2, x[j][i] & 0x7fff7fffu);
+      uint32_t mx = max(m2 & 0xffffu, m2 >> 16);
+      if (mx > 0x4760u) tame(x[j], &mx);
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      uint32_t bytes[4];
+      for (int i = 0; i < 8; ++i) s2 = __vmaxs2(s2, x[j][i]);
+      const int top = max((int)(short)(s2 & 0xffffu), (int)(short)(s2 >> 16));
+      const float a = __uint_as_float(mx << 16) * 0.125f;
+      const float signed_a = top == (int)mx ? -a : a;
+      const uint32_t s8 = f32_to_codes<true>(signed_a, 0.f) & 0xffu;
+      // the scale's value: the upper byte of an fp16
+      const float s = f16x2_to_f32(s8 << 8).x;
+      const float inv = s == 0.f ? 0.f : __frcp_rn(s);
+      uint32_t word[2];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t v = x[j][k * 4 + i];
-        uint32_t h, r;
-        asm("cvt.rn.f16x2.f32 %0, %1, %2;"
-            : "=r"(h)
-            : "f"(__uint_as_float(v & 0xffff0000u) * inv), "f"(__uint_as_float(v << 16) * inv));
-        asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(h), "r"(0x66086608u));  // 1544
-        asm("max.f16x2 %0, %0, %1;" : "+r"(r) : "r"(0x66006600u));              // 1536
-        asm("min.f16x2 %0, %0, %1;" : "+r"(r) : "r"(0x660f660fu));              // 1551
-        bytes[i] = (r & 0xfu) | ((r >> 12) & 0xf0u);
+      for (int k = 0; k < 2; ++k) {
+        uint32_t r[4];  // 0x6600 + code in each half
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t v = x[j][k * 4 + i];
+          uint32_t h;
+          asm("cvt.rn.f16x2.f32 %0, %1, %2;"
+              : "=r"(h)
+              : "f"(__uint_as_float(v & 0xffff0000u) * inv), "f"(__uint_as_float(v << 16) * inv));
+          asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r[i]) : "r"(h), "r"(0x66086608u));  // 1544
+          asm("max.f16x2 %0, %0, %1;" : "+r"(r[i]) : "r"(0x66006600u));             // 1536
+          asm("min.f16x2 %0, %0, %1;" : "+r"(r[i]) : "r"(0x660f660fu));             // 1551
+        }
+        // Codes 2 i and 2 i + 1 are the halves of r[i] and go to the nibbles of byte i.  Added up
+        // with what the 0x6600 leave (no half overflows), which is taken off at the end.
+        const uint32_t s01 = r[1] * 256u + r[0], s23 = r[3] * 256u + r[2];
+        const uint32_t even = __byte_perm(s01, s23, 0x5410u), odd = __byte_perm(s01, s23, 0x7632u);
+        word[k] = odd * 16u + even - (0x66666666u * 16u + 0x66006600u);
       }
-      word[k] = bytes[0] | bytes[1] << 8 | bytes[2] << 16 | bytes[3] << 24;
+      if (at >= 0) {
+        *reinterpret_cast<uint2*>(codes + at * (D / 2) + group * 8) = make_uint2(word[0], word[1]);
+        scales[at * (D / 16) + group] = (uint8_t)s8;
+      }
     }
-    if (at >= 0) {
-      *reinterpret_cast<uint2*>(codes + at * (D / 2) + group * 8) = make_uint2(word[0], word[1]);
-      scales[at * (D / 16) + group] = (uint8_t)s8;
-    }
+    if (++h >= w.h_end) break;
+    src += from.sh;
+    load();
   }
 }
 
-template <int D>
+template <int D, bool V8>
 __global__ void __launch_bounds__(32 * kWarps4)
-    cache4_read_kernel(const CacheParams c, const TokenView kv, const TokenView vv) {
+    cache4_read_kernel(const CacheParams c, const TokenView kv, const TokenView vv, int heads) {
   using Q = Quad<D>;
-  check_batch(c, (long long)blockIdx.x * blockDim.x + threadIdx.x,
-              (long long)gridDim.x * blockDim.x, ERR_SITE_CACHE_READ);
+  check_entries(c, ERR_SITE_CACHE_READ);
   Work w;
-  if (!find_work<D>(c, &w)) return;
+  if (!find_work<D>(c, heads, &w)) return;
   const int lane = threadIdx.x & 31, group = lane % Q::LPR;
-  const long long place = place_of(c, w.h, w.tok0, w.count, ERR_SITE_CACHE_READ);
+  const long long place = place_of(c, w.tok0, w.count, ERR_SITE_CACHE_READ);
   const uint8_t* codes = w.value ? c.v : c.k;
   const uint8_t* scales = w.value ? c.v_scale4 : c.k_scale4;
+  const TokenView& to = w.value ? vv : kv;
+  uint16_t* dst = to.p + (long long)(w.tok0 + lane / Q::LPR) * to.st + (long long)w.h * to.sh +
+                  group * 16;
+  const long long step = Q::RPI * to.st;
   long long at[kIter];
-  uint2 x[kIter];
-  uint32_t s8[kIter];
 #pragma unroll
   for (int j = 0; j < kIter; ++j) {
     at[j] = __shfl_sync(0xffffffffu, place, j * Q::RPI + lane / Q::LPR);
-    x[j] = make_uint2(0x88888888u, 0x88888888u);
-    s8[j] = 0u;  // a token without a block reads as zeros
-    if (at[j] >= 0) {
-      x[j] = __ldg(reinterpret_cast<const uint2*>(codes + at[j] * (D / 2) + group * 8));
-      s8[j] = __ldg(scales + at[j] * (D / 16) + group);
-    }
+    if (at[j] >= 0) at[j] += (long long)w.h << c.block_log2;
   }
-  const TokenView& to = w.value ? vv : kv;
-  uint16_t* dst = to.p + (long long)w.tok0 * to.st + (long long)w.h * to.sh + group * 16;
+  for (int h = w.h; h < w.h_end; ++h, dst += to.sh) {
+    uint2 x[kIter];
+    uint32_t s8[kIter];
 #pragma unroll
-  for (int j = 0; j < kIter; ++j) {
-    const int r = j * Q::RPI + lane / Q::LPR;
-    if (at[j] == -1) continue;
-    const float s = f16x2_to_f32(s8[j] << 8).x;
-    uint32_t o[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t b = (i < 4 ? x[j].x : x[j].y) >> (8 * (i & 3));
-      o[i] = pack_bf16x2((float)((int)(b & 15u) - 8) * s, (float)((int)((b >> 4) & 15u) - 8) * s);
+    for (int j = 0; j < kIter; ++j) {
+      x[j] = make_uint2(0x88888888u, 0x88888888u);
+      s8[j] = 0u;  // a token without a block reads as zeros
+      if (at[j] >= 0) {
+        x[j] = __ldg(reinterpret_cast<const uint2*>(codes + at[j] * (D / 2) + group * 8));
+        s8[j] = __ldg(scales + at[j] * (D / 16) + group);
+      }
     }
-    uint4* out = reinterpret_cast<uint4*>(dst + (long long)r * to.st);
-    out[0] = make_uint4(o[0], o[1], o[2], o[3]);
-    out[1] = make_uint4(o[4], o[5], o[6], o[7]);
+#pragma unroll
+    for (int j = 0; j < kIter; ++j) {
+      if (at[j] == -1) continue;
+      if (at[j] >= 0) at[j] += c.block_size;  // the next head's
+      uint32_t o[8];
+      const Bf16Scale s = bf16_scale(s8[j]);
+      bf16_values(x[j].x, s, o);
+      bf16_values(x[j].y, s, o + 4);
+      store32<V8>(dst + j * step, o);
+    }
   }
 }
 
 template <bool APPEND, int D>
 cudaError_t start(const CacheParams& c, const TokenView& k, const TokenView& v,
                   cudaStream_t stream) {
-  const long long warps = ((long long)c.total + Quad<D>::TOK - 1) / Quad<D>::TOK * 2 * c.H;
-  const long long ctas = (warps + kWarps4 - 1) / kWarps4;
-  if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  if constexpr (APPEND)
-    cache4_append_kernel<D><<<(unsigned)ctas, 32 * kWarps4, 0, stream>>>(c, k, v);
-  else
-    cache4_read_kernel<D><<<(unsigned)ctas, 32 * kWarps4, 0, stream>>>(c, k, v);
+  // Append: up to 4 heads a warp while there are 64 warps for every SM, which saves 43 of a
+  // group's 218 instructions (32768 tokens of 16 heads, d = 128: 66 us with one, 60 with four).
+  // Read, which waits for memory: one (57 us; 59 with four).
+  const long long groups = ((long long)c.total + Quad<D>::TOK - 1) / Quad<D>::TOK;
+  int heads = 1;
+  while (APPEND && heads < 4 && groups * 2 * c.H / (2 * heads) >= 64LL * c.n_sm) heads *= 2;
+  const int per_cta = kWarps4 * heads;
+  const dim3 grid((unsigned)groups, (unsigned)((c.H + per_cta - 1) / per_cta), 2);
+  const dim3 block(32 * kWarps4);
+  if constexpr (APPEND) {
+    cache4_append_kernel<D><<<grid, block, 0, stream>>>(c, k, v, heads);
+  } else {
+    const auto wide = [](const TokenView& x) {
+      return (reinterpret_cast<uintptr_t>(x.p) & 31u) == 0 && (x.st & 15) == 0 && (x.sh & 15) == 0;
+    };
+    if (wide(k) && wide(v))
+      cache4_read_kernel<D, true><<<grid, block, 0, stream>>>(c, k, v, heads);
+    else
+      cache4_read_kernel<D, false><<<grid, block, 0, stream>>>(c, k, v, heads);
+  }
   return cudaGetLastError();
 }
 

@@ -375,12 +375,8 @@ __global__ void __launch_bounds__(Ww<D>::THREADS, 1)
         if constexpr (I4) {
 #pragma unroll
           for (int y = 0; y < 4; ++y) {  // a word: eight codes
-            const float s = f16x2_to_f32((raw_scale[x] >> (8 * (y >> 1)) & 0xffu) << 8).x;
             uint32_t o[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              o[k] = pack_bf16x2((float)((int)(w[y] >> (8 * k) & 15u) - 8) * s,
-                                 (float)((int)(w[y] >> (8 * k + 4) & 15u) - 8) * s);
+            bf16_values(w[y], bf16_scale(raw_scale[x] >> (8 * (y >> 1)) & 0xffu), o);
             put(piece * 32 + y * 8, o);
           }
         } else {

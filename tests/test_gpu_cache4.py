@@ -356,3 +356,40 @@ def test_graph_capture_and_another_stream():
     o, lse2 = fattn.cache_forward(q, cache, batch, 0.1, True, stream=other)
     other.synchronize()
     assert torch.equal(o, out) and torch.equal(lse2, lse)
+
+
+@pytest.mark.parametrize("offset,pad", [(8, 0), (16, 8), (0, 8), (0, 16)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_read_into_rows_of_any_alignment(d, offset, pad):
+    """Outputs whose rows start on 16-byte boundaries that are none of 32 bytes, and on those."""
+    H, bs = 3, 16
+    c = Case([(40, 3), (1, 9)], H, d, bs).fill()
+    cache, batch = c.on_device()
+    ref = oc4.read(c.cache, c.batch)
+    outs = []
+    for _ in range(2):
+        flat = torch.full((offset + c.T * (H * d + pad) + 64,), 7.0, dtype=torch.bfloat16, device=DEV)
+        outs.append((flat, flat[offset:].as_strided((c.T, H, d), (H * d + pad, d, 1))))
+    got = fattn.cache_read(cache, batch, out=(outs[0][1], outs[1][1]))
+    for (flat, part), g, r in zip(outs, got, ref):
+        np.testing.assert_array_equal(g.cpu().double().numpy(), r)
+        part.fill_(7.0)
+        assert bool((flat == 7.0).all())
+
+
+def test_append_of_many_heads_and_tokens():
+    """A prompt large enough for several heads a warp, heads that do not divide among them."""
+    H, T, d, bs = 37, 16500, 64, 128
+    g = torch.Generator(device=DEV).manual_seed(9)
+    k, v = (torch.randn((T, H, d), generator=g, device=DEV).bfloat16() for _ in range(2))
+    nb = -(-T // bs)
+    i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device=DEV)
+    one, many = (fattn.new_cache(nb, H, bs, d, dtype=torch.uint8, device=DEV) for _ in range(2))
+    table = torch.randperm(nb, generator=g, device=DEV).int()[None].contiguous()
+    fattn.cache_append(k, v, one, fattn.CacheBatch(table, i32(T), i32(0, T), T, T))
+    for a in range(0, T, 500):  # in pieces too small for that
+        n = min(500, T - a)
+        fattn.cache_append(k[a:a + n], v[a:a + n], many,
+                           fattn.CacheBatch(table, i32(a + n), i32(0, n), n, n))
+    for x, y in zip(one, many):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
