@@ -34,7 +34,7 @@ template <int D, int NT_>
 struct Dec4 {
   static constexpr int NT = NT_;
   static constexpr int R = 8 * NT;
-  static constexpr int PARTS = 2;               // of 16 keys in a warp's tile
+  static constexpr int PARTS = D == 128 || NT == 2 ? 2 : 4;  // of 16 keys in a warp's tile
   static constexpr int KEYS = 16 * PARTS;
   static constexpr int CHUNK = kWarps * KEYS;
   static constexpr int ROW = D / 2;             // bytes of a key's or value's codes
@@ -42,7 +42,7 @@ struct Dec4 {
   static constexpr int PART_SCL = D;            // bytes of the scales of 16 keys
   static constexpr int TILE_SCL = PARTS * PART_SCL;
   static constexpr int STAGE = 2 * TILE + 2 * TILE_SCL;  // keys, values, their scales
-  static constexpr int ST = D == 64 ? 6 : NT == 1 ? 3 : 4;  // ring slots per warp
+  static constexpr int ST = D == 64 && NT == 2 ? 6 : NT == 1 ? 3 : 4;  // ring slots per warp
   static constexpr int CTAS = NT == 1 || D == 64 ? 3 : 2;   // per SM
   static constexpr int OFF_RED = kWarps * ST * STAGE;
   static constexpr int OFF_STAT = OFF_RED + kWarps * R * D * 4;
@@ -97,13 +97,15 @@ __global__ void __launch_bounds__(32 * kWarps, Dec4<D, NT>::CTAS)
   // Lane i holds tile i of a set of 32.  The next set's entries of the block table are on their
   // way while this one's are used.
   struct Pages {
-    int page[2];   // of each part: as the table has it; -1: no keys there
+    int page[C::PARTS];  // of each part: as the table has it; -1: no keys there
     int h, row16;  // head; place of the first key in its block, in units of 16
   };
   const int bs = p.c.block_size;
   Cursor ahead = cur;
   auto look_up = [&](int f0) {  // `ahead` being tile f0
-    Pages r{{-1, -1}, 0, 0};
+    Pages r{};
+#pragma unroll
+    for (int i = 0; i < C::PARTS; ++i) r.page[i] = -1;
     if (f0 + lane >= F) return r;
     Cursor at = ahead;
     advance<C>(p, &at, lane);
@@ -112,7 +114,7 @@ __global__ void __launch_bounds__(32 * kWarps, Dec4<D, NT>::CTAS)
     r.h = at.h;
     r.row16 = (key & (bs - 1)) >> 4;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < C::PARTS; ++i)
       if (key + 16 * i < at.seq.len) {
         const int page = table[(key + 16 * i) >> p.c.block_log2];
         // (a bad number that means "no keys" is one that may be reported here)
@@ -121,10 +123,10 @@ __global__ void __launch_bounds__(32 * kWarps, Dec4<D, NT>::CTAS)
     return r;
   };
   // Place of the part's 16 keys in the pool, in units of 16 (-1: no keys): a lane's own
-  int place[2];
+  int place[C::PARTS];
   auto settle = [&](const Pages& s) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < C::PARTS; ++i) {
       place[i] = -1;
       if (s.page[i] == -1) continue;
       if (s.page[i] < 0 || s.page[i] >= p.c.num_blocks) {
@@ -133,7 +135,7 @@ __global__ void __launch_bounds__(32 * kWarps, Dec4<D, NT>::CTAS)
       }
       // (a unit is 512 bytes of codes or more: their number stays below 2^31)
       place[i] = ((s.page[i] * p.c.H + s.h) << (p.c.block_log2 - 4)) +
-                 (bs > 16 ? s.row16 + i : 0);
+                 ((s.row16 + i) & ((bs >> 4) - 1));
     }
   };
   Pages next = look_up(0);
@@ -151,24 +153,27 @@ __global__ void __launch_bounds__(32 * kWarps, Dec4<D, NT>::CTAS)
       D == 128 ? (uint32_t)(crow * 64 + (((lane & 3) ^ ((crow >> 1) & 3)) << 4))
                : (uint32_t)(crow * 32 + (((lane & 1) ^ ((crow >> 2) & 1)) << 4));
   constexpr int LP = D / 16;  // lanes that copy a part's scales
-  const int sside = lane / (2 * LP), spart = lane / LP & 1;
+  const int sside = lane / (C::PARTS * LP), spart = lane / LP % C::PARTS;
+  static_assert(2 * C::PARTS * LP == 32 || NT == 2, "all lanes");
   const uint32_t sdst = 2 * C::TILE + sside * C::TILE_SCL + spart * C::PART_SCL + lane % LP * 16;
   const uint8_t* sfrom = (sside ? p.c.v_scale4 : p.c.k_scale4) + lane % LP * 16;
-  uint32_t live[2] = {0u, 0u};  // bit i: whether tile (issued - 1 - i) has keys in that part
+  uint32_t live[C::PARTS] = {};  // bit i: whether tile (issued - 1 - i) has keys in that part
   int fi = 0;                   // next tile to load
   uint32_t fill = ring;         // its slot
   auto issue = [&]() {
-    live[0] <<= 1, live[1] <<= 1;
+#pragma unroll
+    for (int i = 0; i < C::PARTS; ++i) live[i] <<= 1;
     if (fi < F) {
       if ((fi & 31) == 0 && fi > 0) {
         settle(next);
         advance<C>(p, &ahead, 32);
         next = look_up(fi + 32);
       }
-      int at[2];
+      int at[C::PARTS], sat = -1;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < C::PARTS; ++i) {
         at[i] = __shfl_sync(0xffffffffu, place[i], fi & 31);
+        if (spart == i) sat = at[i];
         if (at[i] >= 0) {
           live[i] |= 1u;
           const long long off = (long long)at[i] * (16 * C::ROW) + lane * 16;
@@ -182,7 +187,6 @@ __global__ void __launch_bounds__(32 * kWarps, Dec4<D, NT>::CTAS)
           }
         }
       }
-      const int sat = spart ? at[1] : at[0];
       if (sside < 2 && sat >= 0)
         copy16_async(fill + sdst, sfrom + (long long)sat * C::PART_SCL);
       ++fi;
@@ -306,11 +310,16 @@ __global__ void __launch_bounds__(32 * kWarps, Dec4<D, NT>::CTAS)
       issue();
       copies_wait<ST - 1>();
       __syncwarp();
-      const bool on[2] = {(live[0] >> (ST - 1) & 1u) != 0u, (live[1] >> (ST - 1) & 1u) != 0u};
-      if (on[0] || on[1]) {
-        float s[2][NT][4];
+      bool on[C::PARTS], any = false, all = true;
 #pragma unroll
-        for (int pt = 0; pt < 2; ++pt) {
+      for (int pt = 0; pt < C::PARTS; ++pt) {
+        on[pt] = (live[pt] >> (ST - 1) & 1u) != 0u;
+        any |= on[pt], all &= on[pt];
+      }
+      if (any) {
+        float s[C::PARTS][NT][4];
+#pragma unroll
+        for (int pt = 0; pt < C::PARTS; ++pt) {
           uint32_t a[2][W];         // keys krow and krow + 8
           Int4Scale sc[2][W / 2];   // of their groups of 16
           const uint32_t at = slot + ka0 + pt * (16 * C::ROW);
@@ -347,10 +356,10 @@ __global__ void __launch_bounds__(32 * kWarps, Dec4<D, NT>::CTAS)
           }
         }
         // some row does not see all of it, or a part has no keys (and its slot holds anything)
-        const bool masked = key0 + C::KEYS > lim_lo || !on[0] || !on[1];
+        const bool masked = key0 + C::KEYS > lim_lo || !all;
         if (masked) {
 #pragma unroll
-          for (int pt = 0; pt < 2; ++pt)
+          for (int pt = 0; pt < C::PARTS; ++pt)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -364,8 +373,10 @@ __global__ void __launch_bounds__(32 * kWarps, Dec4<D, NT>::CTAS)
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            top[nt][i] = fmaxf(fmaxf(s[0][nt][i], s[0][nt][i + 2]),
-                               fmaxf(s[1][nt][i], s[1][nt][i + 2])) * fac[nt][i];
+            float m = fmaxf(s[0][nt][i], s[0][nt][i + 2]);
+#pragma unroll
+            for (int pt = 1; pt < C::PARTS; ++pt) m = fmax3(m, s[pt][nt][i], s[pt][nt][i + 2]);
+            top[nt][i] = m * fac[nt][i];
             move |= top[nt][i] > bound[nt][i];
           }
         if (__any_sync(0xffffffffu, move)) {
@@ -396,7 +407,7 @@ __global__ void __launch_bounds__(32 * kWarps, Dec4<D, NT>::CTAS)
         }
         if (__builtin_expect(far, 0)) {
 #pragma unroll
-          for (int pt = 0; pt < 2; ++pt)
+          for (int pt = 0; pt < C::PARTS; ++pt)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -404,7 +415,7 @@ __global__ void __launch_bounds__(32 * kWarps, Dec4<D, NT>::CTAS)
                 s[pt][nt][i] = __fadd_rn(__fmul_rn(s[pt][nt][i], fac[nt][i & 1]), nref[nt][i & 1]);
         } else {
 #pragma unroll
-          for (int pt = 0; pt < 2; ++pt)
+          for (int pt = 0; pt < C::PARTS; ++pt)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -412,7 +423,7 @@ __global__ void __launch_bounds__(32 * kWarps, Dec4<D, NT>::CTAS)
                 s[pt][nt][i] = fmaf(s[pt][nt][i], fac[nt][i & 1], nref[nt][i & 1]);
         }
 #pragma unroll
-        for (int pt = 0; pt < 2; ++pt) {
+        for (int pt = 0; pt < C::PARTS; ++pt) {
           uint32_t pf[NT][2];
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
