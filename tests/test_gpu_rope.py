@@ -130,3 +130,40 @@ def test_captured_and_empty_and_refused():
         fattn.rope(x.float(), None, pos, table)
     with pytest.raises(fattn.FattnError):
         fattn.rope(x, None, pos, fattn.rope_table(24, device=DEV))
+
+
+@pytest.mark.parametrize("layout,rot", [("half", 64), ("interleaved", 32)])
+def test_training_run(layout, rot):
+    """Queries and keys of the dense layout turned (by strides), attention and its backward pass,
+    and the gradients turned back, against 64-bit differentiation of the whole.  The bars are the
+    attention's own: 2e-2 for the result and the gradients (values of size 1)."""
+    H, N, d = 2, 150, 64
+    rng = np.random.default_rng(11)
+    q, k, v, do = (_bf16(rng, (1, H, N, d)).to(DEV) for _ in range(4))
+    pos = torch.arange(N, dtype=torch.int32, device=DEV)
+    table = fattn.rope_table(rot, device=DEV)
+    rows = lambda x: x[0].transpose(0, 1)  # [N, H, d] over the dense tensor
+    qr, kr, dq, dk = (torch.empty_like(q) for _ in range(4))
+    fattn.rope(rows(q), rows(k), pos, table, layout, out=(rows(qr), rows(kr)))
+    o, lse = fattn.forward(qr, kr, v, d ** -0.5, True)
+    dqr, dkr, dv = fattn.backward(qr, kr, v, o, lse, do, d ** -0.5, True)
+    fattn.rope_backward(rows(dqr), rows(dkr), pos, table, layout, out=(rows(dq), rows(dk)))
+
+    w, _ = orope.frequencies(rot)
+    angle = pos.double()[:, None] * torch.tensor(w, device=DEV)
+    cos, sin = torch.cos(angle), torch.sin(angle)
+
+    def turn(x):
+        a, b = (x[..., :rot // 2], x[..., rot // 2:rot]) if layout == "half" else \
+            (x[..., 0:rot:2], x[..., 1:rot:2])
+        y = (a * cos - b * sin, a * sin + b * cos)
+        y = torch.cat(y, -1) if layout == "half" else torch.stack(y, -1).flatten(-2)
+        return torch.cat((y, x[..., rot:]), -1)
+
+    q64, k64, v64 = (x.double().requires_grad_() for x in (q, k, v))
+    s = turn(q64) @ turn(k64).transpose(2, 3) * d ** -0.5
+    s = s.masked_fill(torch.ones((N, N), dtype=torch.bool, device=DEV).triu(1), -np.inf)
+    ref = torch.softmax(s, dim=-1) @ v64
+    ref.backward(do.double())
+    for got, want in ((o, ref), (dq, q64.grad), (dk, k64.grad), (dv, v64.grad)):
+        assert float((got.double() - want.detach()).abs().max()) <= 2e-2 * max(1.0, float(want.detach().abs().max()))
