@@ -538,20 +538,14 @@ CacheParams cache_params(const fattn_cache* c, const fattn_cache_batch* b, unsig
   CacheParams p{};
   p.k = static_cast<uint8_t*>(c->k);
   p.v = static_cast<uint8_t*>(c->v);
-  const bool int4 = c->format == FATTN_CACHE_INT4;
-  if (int4) {
-    p.k_scale4 = static_cast<uint8_t*>(c->k_scale);
-    p.v_scale4 = static_cast<uint8_t*>(c->v_scale);
-  } else {
-    p.k_scale = static_cast<float*>(c->k_scale);
-    p.v_scale = static_cast<float*>(c->v_scale);
-  }
+  p.k_scale = static_cast<float*>(c->k_scale);
+  p.v_scale = static_cast<float*>(c->v_scale);
   p.num_blocks = c->num_blocks;
   p.H = c->H;
   p.block_size = c->block_size;
   p.block_log2 = c->block_size == 16 ? 4 : c->block_size == 32 ? 5 : c->block_size == 64 ? 6 : 7;
   p.d = c->d;
-  p.format = int4 ? FMT_INT4 : c->format == FATTN_CACHE_E5M2 ? FMT_E5M2 : FMT_E4M3;
+  p.format = c->format == FATTN_CACHE_INT4 ? FMT_INT4 : c->format == FATTN_CACHE_E5M2 ? FMT_E5M2 : FMT_E4M3;
   p.block_table = b->block_table;
   p.lens = b->lens;
   p.cu_seqlens = b->cu_seqlens;

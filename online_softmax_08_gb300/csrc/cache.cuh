@@ -42,8 +42,6 @@ struct CacheParams {
   uint8_t* v;
   float* k_scale;        // [num_blocks, H]
   float* v_scale;
-  uint8_t* k_scale4;     // 4 bits, in their place: [num_blocks, H, block_size, d / 16], e5m2
-  uint8_t* v_scale4;
   int num_blocks, H, block_size, d, format;
   int block_log2;        // block_size = 1 << block_log2
   const int* block_table;
@@ -51,8 +49,13 @@ struct CacheParams {
   const int* cu_seqlens;
   int B, table_width, total, max_seqlen;
   long long l2_bytes;    // of the device (append)
-  int n_sm;              // of the device (append and read in 4 bits)
   unsigned int* err;
+  int n_sm;              // of the device (append and read in 4 bits)
+  // 4 bits: the scales are bytes, e5m2, [num_blocks, H, block_size, d / 16]
+#ifdef __CUDACC__
+  __device__ __forceinline__ uint8_t* k_scale4() const { return reinterpret_cast<uint8_t*>(k_scale); }
+  __device__ __forceinline__ uint8_t* v_scale4() const { return reinterpret_cast<uint8_t*>(v_scale); }
+#endif
 };
 // A packed [total, heads, d] tensor by element strides.
 struct TokenView {

@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(32 * kWarps4)
   load();
   const long long place = place_of(c, w.tok0, w.count, ERR_SITE_CACHE_APPEND);
   uint8_t* codes = w.value ? c.v : c.k;
-  uint8_t* scales = w.value ? c.v_scale4 : c.k_scale4;
+  uint8_t* scales = w.value ? c.v_scale4() : c.k_scale4();
   long long places[kIter];
 #pragma unroll
   for (int j = 0; j < kIter; ++j) {
@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(32 * kWarps4)
   const int lane = threadIdx.x & 31, group = lane % Q::LPR;
   const long long place = place_of(c, w.tok0, w.count, ERR_SITE_CACHE_READ);
   const uint8_t* codes = w.value ? c.v : c.k;
-  const uint8_t* scales = w.value ? c.v_scale4 : c.k_scale4;
+  const uint8_t* scales = w.value ? c.v_scale4() : c.k_scale4();
   const TokenView& to = w.value ? vv : kv;
   uint16_t* dst = to.p + (long long)(w.tok0 + lane / Q::LPR) * to.st + (long long)w.h * to.sh +
                   group * 16;

@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(32 * kWarps, Dec4<D, NT>::CTAS)
   const int sside = lane / (C::PARTS * LP), spart = lane / LP % C::PARTS;
   static_assert(2 * C::PARTS * LP == 32 || NT == 2, "all lanes");
   const uint32_t sdst = 2 * C::TILE + sside * C::TILE_SCL + spart * C::PART_SCL + lane % LP * 16;
-  const uint8_t* sfrom = (sside ? p.c.v_scale4 : p.c.k_scale4) + lane % LP * 16;
+  const uint8_t* sfrom = (sside ? p.c.v_scale4() : p.c.k_scale4()) + lane % LP * 16;
   uint32_t live[C::PARTS] = {};  // bit i: whether tile (issued - 1 - i) has keys in that part
   int fi = 0;                   // next tile to load
   uint32_t fill = ring;         // its slot
@@ -480,7 +480,7 @@ __global__ void __launch_bounds__(32 * kWarps, Dec4<D, NT>::CTAS)
     }
     ++f;
     end_unit<C, D>(p, cur, f, share, rows, acc, ref, lsum, (float)kInt4UnitLog2, vcol, red, stat,
-                   part_lse, part_o, &rec);
+                   part_lse, part_o, h, rb, G, &rec);
     advance<C>(p, &cur, 1);
   }
   copies_wait<0>();

@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(kCopy) cache_copy_kernel(const EvictParams p, 
     for (int x = t; x < count * 2; x += kCopy) {
       const bool value = x >= count;
       const int r = value ? x - count : x;
-      uint8_t* scales = value ? c.v_scale4 : c.k_scale4;
+      uint8_t* scales = value ? c.v_scale4() : c.k_scale4();
       S s{};
       if (row_of[r] >= 0) s = *reinterpret_cast<const S*>(scales + row_of[r] * (D / 16));
       *reinterpret_cast<S*>(scales + (out0 + r) * (D / 16)) = s;

@@ -636,7 +636,8 @@ __global__ void __launch_bounds__(128, Dec<D, NT>::CTAS)
         for (int i = 0; i < 2; ++i) lsum[nt][i] = g == 0 && ref[nt][i] != -INFINITY ? 1.f : 0.f;
       lvb = 0.f;
     }
-    end_unit<C, D>(p, cur, f, share, rows, acc, ref, lsum, lvb, vcol, red, stat, part_lse, part_o, &rec);
+    end_unit<C, D>(p, cur, f, share, rows, acc, ref, lsum, lvb, vcol, red, stat, part_lse, part_o, h,
+                   rb, G, &rec);
     __syncwarp();
     if (lane == 0) mbar_arrive(red_bar);
     ++ended;

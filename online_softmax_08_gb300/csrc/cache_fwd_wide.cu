@@ -640,7 +640,7 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
           buf[value][pc][i] = at[pc] < 0 ? make_uint4(0u, 0u, 0u, 0u)
                                          : __ldg(reinterpret_cast<const uint4*>(src + i * ROWS_LD * RB));
         if constexpr (I4) {
-          const uint8_t* from = (value ? p.c.v_scale4 : p.c.k_scale4) + (long long)at[pc] * D +
+          const uint8_t* from = (value ? p.c.v_scale4() : p.c.k_scale4()) + (long long)at[pc] * D +
                                 row4 * (D / 16) + col16 * 2;
 #pragma unroll
           for (int i = 0; i < LD; ++i)

@@ -86,9 +86,10 @@ __device__ __forceinline__ int find_share(const CacheFwdParams& p, int first_row
 #pragma unroll
   for (int w = 16; w > 0; w >>= 1) total += __shfl_xor_sync(0xffffffffu, total, w);
   // (a 64-bit division takes ten times as long)
-  *chunks_each = total < 0x7fffffff ? ((unsigned)total + gridDim.x - 1) / gridDim.x
+  const long long share = total < 0x7fffffff ? ((unsigned)total + gridDim.x - 1) / gridDim.x
                                    : (total + gridDim.x - 1) / gridDim.x;
-  const long long share = *chunks_each, lo = blockIdx.x * share;
+  const long long lo = blockIdx.x * share;
+  *chunks_each = share;
   const int F = (int)max(0LL, min(share, total - lo));  // chunks of this CTA
   if (F > 0) {
     long long before = 0;
@@ -178,17 +179,19 @@ __device__ __forceinline__ uint32_t ld_shared_u8(uint32_t a) {
 // A unit (or its piece in this share) ends in front of tile f: the four warps' sums are
 // joined, and the rows go to o and lse or, of a piece, to the workspace.  Lane (g, t) holds
 // the columns vcol + 2 mt, + 1 (acc[mt][nt][i], [i + 2]) of rows 8 nt + 2 t + i.  O = 2^lvb acc /
-// l.  `red` [warps][R][D] and `stat` [warps][R] are the CTA's.
+// l.  `red` [warps][R][D] and `stat` [warps][R] are the CTA's; h, rb, G are the unit's.
 template <typename C, int D, int NT>
 __device__ __forceinline__ void end_unit(const CacheFwdParams& p, const Cursor& cur, int f,
                                          long long share, int rows,
                                          const float (&acc)[D / 16][NT][4],
                                          const float (&ref)[NT][2], float (&lsum)[NT][2],
                                          float lvb, int vcol, float* red, float* stat,
-                                         float* part_lse, float* part_o, Record* rec) {
+                                         float* part_lse, float* part_o, int h, int rb, int G,
+                                         Record* rec) {
   constexpr int R = C::R, VW = D / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int h = cur.h, rb = cur.rb, G = p.G;
+  const int ch = cur.ch;
+  const bool unit_ends = ch == cur.nch - 1;
   // this warp's rows: normalised result and log2-sum-exp
   float mine[NT][2], fac[NT][2];
 #pragma unroll
@@ -241,8 +244,6 @@ __device__ __forceinline__ void end_unit(const CacheFwdParams& p, const Cursor& 
             acc[2 * j + 1][nt][i + 2] * fac[nt][i] * up);
     }
   __syncthreads();
-  const int ch = cur.ch;
-  const bool unit_ends = ch == cur.nch - 1;
   const bool starts_here = f > ch;  // the unit's chunk 0 is in this share
   const bool whole = starts_here && unit_ends;
   const int slot = starts_here ? 1 : 0;

@@ -170,11 +170,11 @@ __global__ void __launch_bounds__(32 * kWarpsW, ctas_w(D))
         if constexpr (I4 && D == 128) {
           const uint4 x = __ldg(reinterpret_cast<const uint4*>(from + i * 8 * RB));
           w[0] = x.x, w[1] = x.y, w[RW - 2] = x.z, w[RW - 1] = x.w;
-          scales[m][i] = __ldg(reinterpret_cast<const uint16_t*>(c.k_scale4 + row * 8 + t * 2 + i * 64));
+          scales[m][i] = __ldg(reinterpret_cast<const uint16_t*>(c.k_scale4() + row * 8 + t * 2 + i * 64));
         } else if constexpr (I4) {
           const uint2 x = __ldg(reinterpret_cast<const uint2*>(from + i * 8 * RB));
           w[0] = x.x, w[1] = x.y;
-          scales[m][i] = __ldg(c.k_scale4 + row * 4 + t + i * 32);
+          scales[m][i] = __ldg(c.k_scale4() + row * 4 + t + i * 32);
         } else {
 #pragma unroll
           for (int half = 0; half < D / 64; ++half) {

@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(Ww<D>::THREADS, 1)
         raw_codes[x] = __ldg(reinterpret_cast<const uint4*>(c.k + row * RB + piece * 16));
         if constexpr (I4)
           raw_scale[x] =
-              __ldg(reinterpret_cast<const uint16_t*>(c.k_scale4 + row * (D / 16) + piece * 2));
+              __ldg(reinterpret_cast<const uint16_t*>(c.k_scale4() + row * (D / 16) + piece * 2));
       }
       const int page = page_of(key0 + t);
       ks = page < 0 ? 0.f : I4 ? 1.f : c.k_scale[(long long)page * c.H + h];
