@@ -6,23 +6,27 @@
 // Both operands are bf16 without a rounding: codes and 4-bit values have at most 7 significant
 // bits, q is what it is (a block's scale and the softmax scale make f, by key).
 //
-// A CTA (one per SM) goes through its share of the units, each 256 keys of one (sequence,
-// key/value head), in two tiles, against all rows that see some of them:
-//   warps 0-15      the keys: four warps each the columns 0-127 of tile 0, of tile 1, and the
-//                   columns 128-255.  Their codes are loaded during the unit before's last rows,
-//                   converted and stored in the 128-byte-swizzled layout that a TMA load would
-//                   leave; then S by S: tcgen05.ld, exponential, sum
+// A CTA (one per SM) goes through its share of the units, each 128 keys of one (sequence,
+// key/value head), against all rows that see some of them:
+//   warps 0-15      exponentials and sums, four warps each a quarter of the columns of every S
+//                   tile.  They also load the next unit's codes while they work on one, and
+//                   store them as bf16, in the 128-byte-swizzled layout that a TMA load would
+//                   leave, ahead of its last rows, into the other of two places
 //   warp 16         Q, 256 rows at a time, by TMA straight from the caller's tensor: a tile is
 //                   tb = 256 / G tokens of the group's G heads, which a box {64, G, tb} leaves as
 //                   rows
-//   warp 17         the MMAs, into the S of the two tiles of keys in turn
+//   warps 17, 19    the MMAs, a thread each for the tiles of one of two S buffers
 //   warp 18         the rows' log-sum-exp, in a ring of their own, as Q's slots are free again
 //                   once the MMAs have read them
 // The bound is the special-function unit: 128 x 256 exponentials take 1024 clocks at the 32 a
 // clock that were measured, the products of that tile 768 (A and B come from shared memory at
-// 128 bytes a clock).  With tiles of 128 rows, S in two buffers, the thread that issues the MMAs
-// was the bound: its waits and 16 instructions took 2250 clocks a tile of 2 x 128 keys, as it
-// shares its issue slots with the exponentials.
+// 128 bytes a clock).  One thread that issued all MMAs was the bound before: its waits, 8
+// instructions and commits take 1500 clocks a tile, as it shares its issue slots with the
+// exponentials.  (Built and measured before this, 512 queries behind 16384 tokens, 32 query and
+// 8 key heads, d = 128: mma.sync 457 us; 256 keys a unit, 8 warps, tiles of 128 rows 127 us, 16
+// warps 94 us; tiles of 256 rows, S in one buffer for each 128 keys, 88 us.)  Now 76 us: a tile
+// takes 2200 clocks, of which a warp's 64 columns take 1650, its waits and what it does between
+// tiles the rest, and a change of unit 4500.
 #define FATTN_INLINE_WAIT_SLOW_PATH
 #include <math.h>
 
@@ -37,32 +41,33 @@ constexpr float kLog2eV = 1.4426950408889634f;
 
 template <int D>
 struct Ww {
-  static constexpr int BM = 128, KEYS = 2 * BM, BN = 256;
-  static constexpr int HALF = BM * 128;      // 64 channels of 128 keys (bytes)
+  static constexpr int BM = 128, BN = 256;
+  static constexpr int HALF = BM * 128;      // 64 channels of the keys (bytes)
   static constexpr int TILE = BM * D * 2;
   static constexpr int Q_HALF = BN * 128, Q_TILE = BN * D * 2;
   static constexpr int ST = D == 128 ? 2 : 4;
-  static constexpr int OFF_K = 0;
+  static constexpr int INFO = 8;             // tiles of rows
+  static constexpr int SUMS = 4;             // units
+  static constexpr int OFF_K = 0;            // [2]
   static constexpr int OFF_Q = 2 * TILE;
-  static constexpr int OFF_INFO = OFF_Q + ST * Q_TILE;  // [INFO][BN] -lse log2(e)
-  static constexpr int INFO = 8;                          // tiles of rows
-  static constexpr int OFF_SUM = OFF_INFO + INFO * BN * 4;  // [2][BM] sums of columns 128-255
-  static constexpr int OFF_BAR = OFF_SUM + 2 * BM * 4;
+  static constexpr int OFF_INFO = OFF_Q + ST * Q_TILE;      // [INFO][BN] -lse log2(e)
+  static constexpr int OFF_SUM = OFF_INFO + INFO * BN * 4;  // [SUMS][3][BM] of the later columns
+  static constexpr int OFF_BAR = OFF_SUM + SUMS * 3 * BM * 4;
   static constexpr int SMEM = OFF_BAR + 512 + 1024;
-  static constexpr int W_LOAD = 16, W_MMA = 17, W_INFO = 18, THREADS = 608;
+  static constexpr int W_LOAD = 16, W_MMA = 17, W_INFO = 18, W_MMA2 = 19, THREADS = 640;
   static constexpr uint32_t IDESC = idesc_bf16_f32(128, BN, false, false);
   static constexpr uint32_t IDESC_128 = idesc_bf16_f32(128, 128, false, false);
   static_assert(SMEM <= 232448, "shared memory budget");
 };
 enum {
-  X_K_FULL = 0,    // [2] keys in shared memory (256 threads)
+  X_K_FULL = 0,    // [2] keys in shared memory (512 threads)
   X_S_FULL = 2,    // [2]
-  X_S_EMPTY = 4,   // [2], 8 warps
-  X_DONE = 6,
-  X_SUM = 7,       // [2] the sums of columns 128-255 (128 threads)
-  X_I_FULL = 9,    // [INFO] the rows' log-sum-exp
-  X_I_EMPTY = 17,  // [INFO], 16 warps
-  X_Q_FULL = 25,   // [ST], then q_empty [ST]
+  X_S_EMPTY = 4,   // [2], 16 warps
+  X_DONE = 6,      // [2]
+  X_SUM = 8,       // [SUMS] the sums of the later columns (384 threads)
+  X_I_FULL = 12,   // [INFO] the rows' log-sum-exp
+  X_I_EMPTY = 20,  // [INFO], 16 warps
+  X_Q_FULL = 28,   // [ST], then q_empty [ST]
 };
 
 __device__ __forceinline__ void fma_x2(float a0, float a1, float b, float c0, float c1, float& r0,
@@ -100,10 +105,10 @@ template <int KEYS>
 struct Walk {
   const WeightParams& p;
   long long before, hi;  // cost of the sequences before; end of the share
-  int b;                 // sequence
-  long long u;           // unit in it
+  int b, h, tile;        // sequence, head, tile of keys
+  long long u;           // unit in the sequence
   CacheSeq seq;
-  int tiles, row_tiles;  // 256-key tiles; tiles of rows
+  int tiles, row_tiles;  // of keys, of rows
   __device__ __forceinline__ long long cost_of(int b) {
     row_tiles = tiles = 0;
     if (!cache_seq(p.c, b, &seq) || seq.len > p.width) return 0;  // (reported by the other kernel)
@@ -123,7 +128,7 @@ struct Walk {
     }
     const long long share = (total + gridDim.x - 1) / gridDim.x, lo = blockIdx.x * share;
     hi = min(total, lo + share);
-    b = p.c.B, u = 0, before = total;
+    b = p.c.B, u = 0, h = tile = 0, before = total;
     if (lo >= hi) return;
     before = 0;
     for (int b0 = 0; b0 < p.c.B; b0 += 32) {
@@ -145,12 +150,14 @@ struct Walk {
     }
     const long long n = cost_of(b);
     u = (lo - before + row_tiles - 1) / row_tiles;
+    h = (int)(u / tiles);
+    tile = (int)(u % tiles);
     skip(n);
   }
   __device__ __forceinline__ void skip(long long n) {  // n: the cost of sequence b
     while (u * row_tiles >= n) {
       before += n;
-      u = 0;
+      u = 0, h = tile = 0;
       if (++b >= p.c.B) return;
       n = cost_of(b);
     }
@@ -160,15 +167,14 @@ struct Walk {
   }
   __device__ __forceinline__ void next() {
     ++u;
+    if (++tile == tiles) tile = 0, ++h;
     skip((long long)tiles * p.c.H * row_tiles);
   }
-  __device__ __forceinline__ int head() const { return (int)(u / tiles); }
-  __device__ __forceinline__ int key0() const { return (int)(u % tiles) * KEYS; }
+  __device__ __forceinline__ int key0() const { return tile * KEYS; }
   // the first tile of rows that see some of the unit's keys
   __device__ __forceinline__ int first_rows() const {
     return p.causal ? max(0, key0() - (seq.len - seq.n)) / p.tile_tokens : 0;
   }
-  __device__ __forceinline__ int key_tiles() const { return key0() + 128 < seq.len ? 2 : 1; }
 };
 
 template <int D, int FMT>
@@ -189,18 +195,18 @@ __global__ void __launch_bounds__(Ww<D>::THREADS, 1)
   volatile uint32_t* abort_flag = tmem_slot + 1;
   const WaitCtx wctx{abort_flag, c.err};
   static_assert(8 * (X_Q_FULL + 2 * ST) + 8 <= 512, "barrier block");
-  static_assert(X_I_EMPTY - X_I_FULL == C::INFO && X_Q_FULL - X_I_EMPTY == C::INFO, "barriers");
+  static_assert(X_I_EMPTY - X_I_FULL == C::INFO && X_Q_FULL - X_I_EMPTY == C::INFO &&
+                    X_I_FULL - X_SUM == C::SUMS,
+                "barriers");
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(X_K_FULL + i), 256);
-      mbar_init(bar(X_SUM + i), 128);
-    }
-    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(X_K_FULL + i), 512);
       mbar_init(bar(X_S_FULL + i), 1);
-      mbar_init(bar(X_S_EMPTY + i), 8);
+      mbar_init(bar(X_S_EMPTY + i), 16);
+      mbar_init(bar(X_DONE + i), 1);
     }
-    mbar_init(bar(X_DONE), 1);
+    for (int i = 0; i < C::SUMS; ++i) mbar_init(bar(X_SUM + i), 384);
     for (int i = 0; i < ST; ++i) {
       mbar_init(q_full0 + 8u * i, 1);
       mbar_init(q_empty0 + 8u * i, 1);
@@ -221,7 +227,7 @@ __global__ void __launch_bounds__(Ww<D>::THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  Walk<C::KEYS> walk(p);
+  Walk<C::BM> walk(p);
 
   if (warp == C::W_LOAD) {
     // ---------------------------------------------------------------- Q (one thread)
@@ -229,7 +235,7 @@ __global__ void __launch_bounds__(Ww<D>::THREADS, 1)
       int i = 0;  // tiles of rows so far
       bool ok = true;
       for (; ok && walk.valid(); walk.next()) {
-        const int h = walk.head(), row0 = walk.seq.row0;
+        const int h = walk.h, row0 = walk.seq.row0;
         for (int j = walk.first_rows(); j < walk.row_tiles; ++j, ++i) {
           const int stage = i % ST, use = i / ST;
           ok = use == 0 || mbar_wait(q_empty0 + 8u * stage, (use - 1) & 1, wctx,
@@ -254,7 +260,7 @@ __global__ void __launch_bounds__(Ww<D>::THREADS, 1)
     int i = 0;
     bool ok = true;
     for (; ok && walk.valid(); walk.next()) {
-      const int h = walk.head(), n = walk.seq.n, row0 = walk.seq.row0;
+      const int h = walk.h, n = walk.seq.n, row0 = walk.seq.row0;
       for (int j = walk.first_rows(); j < walk.row_tiles; ++j, ++i) {
         const int stage = i % C::INFO, use = i / C::INFO;
         const int tok0 = j * p.tile_tokens;
@@ -279,76 +285,80 @@ __global__ void __launch_bounds__(Ww<D>::THREADS, 1)
       }
     }
     __syncwarp();
-  } else if (warp == C::W_MMA) {
-    // ---------------------------------------------------------------- MMA issuer (one thread:
-    // electing one of the warp for every instruction took longer than the products)
+  } else if (warp == C::W_MMA || warp == C::W_MMA2) {
+    // ---------------------------------------------------------------- MMA issuers (a thread each:
+    // electing one of a warp for every instruction took longer)
     if (lane == 0) {
-      int i = 0, units[2] = {0, 0};  // units that have keys in each tile
-      int second = 0;  // row tiles that had a second tile of keys
+      const int buf = warp == C::W_MMA ? 0 : 1;  // this one's tiles of rows: the even, the odd ones
+      int i = 0, units = 0;
       const uint64_t ka0 = sdesc_sw128(sbase + C::OFF_K, 16, 1024);
       const uint64_t qb0 = sdesc_sw128(sbase + C::OFF_Q, 16, 1024);
       bool ok = true;
-      for (; ok && walk.valid(); walk.next()) {
-        const int tiles = walk.key_tiles();
-        for (int j = walk.first_rows(), j0 = j; ok && j < walk.row_tiles; ++j, ++i) {
-          const int stage = i % ST;
+      for (; ok && walk.valid(); walk.next(), ++units) {
+        bool keys = false;  // this unit's have been waited for
+        for (int j = walk.first_rows(); ok && j < walk.row_tiles; ++j, ++i) {
+          if ((i & 1) != buf) continue;
+          const int stage = i % ST, use = i >> 1;
           const bool half = (walk.seq.n - j * p.tile_tokens) * p.G <= 128;
-          ok = mbar_wait(q_full0 + 8u * stage, (i / ST) & 1, wctx, ERR_SITE_CACHE_WEIGHTS + 5);
+          ok = mbar_wait(q_full0 + 8u * stage, (i / ST) & 1, wctx, ERR_SITE_CACHE_WEIGHTS + 5) &&
+               (keys || mbar_wait(bar(X_K_FULL + (units & 1)), (units >> 1) & 1, wctx,
+                                  ERR_SITE_CACHE_WEIGHTS + 4)) &&
+               (use == 0 || mbar_wait(bar(X_S_EMPTY + buf), (use - 1) & 1, wctx,
+                                      ERR_SITE_CACHE_WEIGHTS + 6));
+          if (!ok) break;
+          keys = true;
+          tc_fence_after();
+          const uint64_t ka = ka0 + (uint32_t)((units & 1) * C::TILE >> 4);
+          const uint64_t qb = qb0 + (uint32_t)(stage * C::Q_TILE >> 4);
+          const uint32_t idesc = half ? C::IDESC_128 : C::IDESC;
 #pragma unroll
-          for (int a = 0; a < 2; ++a) {
-            if (!ok || a >= tiles) break;
-            if (j == j0) {
-              ok = mbar_wait(bar(X_K_FULL + a), units[a] & 1, wctx, ERR_SITE_CACHE_WEIGHTS + 4);
-              ++units[a];
-              if (!ok) break;
-            }
-            const int n = a ? second : i;
-            ok = n == 0 ||
-                 mbar_wait(bar(X_S_EMPTY + a), (n - 1) & 1, wctx, ERR_SITE_CACHE_WEIGHTS + 6);
-            if (!ok) break;
-            tc_fence_after();
-            const uint64_t ka = ka0 + (uint32_t)(a * C::TILE >> 4);
-            const uint64_t qb = qb0 + (uint32_t)(stage * C::Q_TILE >> 4);
-            const uint32_t idesc = half ? C::IDESC_128 : C::IDESC;
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-              mma_bf16_ss(tmem + a * C::BN,
-                          ka + (uint32_t)(((kk >> 2) * C::HALF + (kk & 3) * 32) >> 4),
-                          qb + (uint32_t)(((kk >> 2) * C::Q_HALF + (kk & 3) * 32) >> 4), idesc, kk > 0);
-            mma_commit(bar(X_S_FULL + a));
-            if (a) ++second;
-          }
-          if (ok) mma_commit(q_empty0 + 8u * stage);
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_bf16_ss(tmem + buf * C::BN,
+                        ka + (uint32_t)(((kk >> 2) * C::HALF + (kk & 3) * 32) >> 4),
+                        qb + (uint32_t)(((kk >> 2) * C::Q_HALF + (kk & 3) * 32) >> 4), idesc, kk > 0);
+          mma_commit(bar(X_S_FULL + buf));
+          mma_commit(q_empty0 + 8u * stage);
         }
       }
-      mma_commit(bar(X_DONE));  // drain before TMEM is freed
-      mbar_drain(bar(X_DONE), 0, wctx, ERR_SITE_CACHE_WEIGHTS + 7);
+      mma_commit(bar(X_DONE + buf));  // drain before TMEM is freed
+      mbar_drain(bar(X_DONE + buf), 0, wctx, ERR_SITE_CACHE_WEIGHTS + 7);
     }
     __syncwarp();
   } else {
     // ---------------------------------------------------------------- keys, exponentials, sums
-    const int a = warp >> 2 & 1, part = warp >> 3, t = threadIdx.x & 127;
+    const int part = warp >> 2, t = threadIdx.x & 127;
     constexpr int RB = I4 ? D / 2 : D, PPR = RB / 16;  // bytes, 16-byte pieces of a row
-    constexpr int RPI = 256 / PPR;                     // rows of a load by all threads of a tile
+    constexpr int RPI = 512 / PPR < 128 ? 512 / PPR : 128;  // rows of a load by all threads
     constexpr int LD = 128 / RPI;
-    const int prow = (part * 128 + t) / PPR, piece = t % PPR;
+    const int prow = (int)threadIdx.x / PPR, piece = threadIdx.x % PPR;
+    const bool loads = prow < RPI;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     uint4 raw_codes[LD];
     uint32_t raw_scale[LD];
     float ks = 0.f;     // of key t; 0: it has no block
-    auto page_of = [&](int key) {
-      if (key >= walk.seq.len) return -1;
-      const int page = c.block_table[(long long)walk.b * c.table_width + (key >> c.block_log2)];
-      if (page >= 0 && page < c.num_blocks) return page;
+    auto checked = [&](int page) {
+      if (page == -1 || (page >= 0 && page < c.num_blocks)) return page;
       if (c.err) atomicCAS(c.err, 0u, (unsigned)ERR_SITE_CACHE_WEIGHTS + 1);
       return -1;
     };
-    auto load = [&]() {  // the codes of the unit that `walk` is at
-      const int h = walk.head(), key0 = walk.key0() + a * C::BM;
+    // The codes of the unit that `walk` is at: block numbers first, the rest once they are there
+    int pages[LD], page_k = -1;
+    auto look_up = [&]() {
+      auto entry = [&](int key) {  // (-1: no key there)
+        if (key >= walk.seq.len) return -1;
+        const int page = c.block_table[(long long)walk.b * c.table_width + (key >> c.block_log2)];
+        return page == -1 ? -2 : page;
+      };
+#pragma unroll
+      for (int x = 0; x < LD; ++x) pages[x] = loads ? entry(walk.key0() + x * RPI + prow) : -1;
+      page_k = entry(walk.key0() + t);
+    };
+    auto load = [&]() {
+      const int h = walk.h, key0 = walk.key0();
 #pragma unroll
       for (int x = 0; x < LD; ++x) {
         const int key = key0 + x * RPI + prow;
-        const int page = page_of(key);
+        const int page = checked(pages[x]);
         raw_codes[x] = make_uint4(0u, 0u, 0u, 0u);
         raw_scale[x] = 0u;
         if (page < 0) continue;
@@ -358,13 +368,15 @@ __global__ void __launch_bounds__(Ww<D>::THREADS, 1)
           raw_scale[x] =
               __ldg(reinterpret_cast<const uint16_t*>(c.k_scale4() + row * (D / 16) + piece * 2));
       }
-      const int page = page_of(key0 + t);
+      const int page = checked(page_k);
       ks = page < 0 ? 0.f : I4 ? 1.f : c.k_scale[(long long)page * c.H + h];
     };
-    auto store = [&]() {  // as bf16, rows of 128 bytes, 16-byte columns swizzled by row & 7
-      const uint32_t tile = sbase + C::OFF_K + a * C::TILE;
+    auto store = [&](int u) {  // unit u's, as bf16, rows of 128 bytes, 16-byte columns swizzled
+      // by row & 7; the MMAs of unit u - 2, whose place it is, are done: its last S was read
+      const uint32_t tile = sbase + C::OFF_K + (u & 1) * C::TILE;
 #pragma unroll
       for (int x = 0; x < LD; ++x) {
+        if (!loads) break;
         const int row = x * RPI + prow;
         const uint32_t w[4] = {raw_codes[x].x, raw_codes[x].y, raw_codes[x].z, raw_codes[x].w};
         auto put = [&](int ch, const uint32_t (&o)[4]) {  // eight channels from ch on
@@ -394,41 +406,38 @@ __global__ void __launch_bounds__(Ww<D>::THREADS, 1)
         }
       }
       fence_proxy_async_smem();
+      mbar_arrive(bar(X_K_FULL + (u & 1)));
     };
-    int i = 0;     // tiles of rows so far, those in which this tile of keys took part
-    int mine = 0, units = 0;  // and the units in which it did
+    int i = 0;      // tiles of rows so far
+    int units = 0;
     bool ok = true;
-    if (walk.valid()) load();
+    if (walk.valid()) {
+      look_up();
+      load();
+      store(0);
+    }
     while (ok && walk.valid()) {
-      // A tile without keys has no part in the barriers of its keys and of S: its warps may run
-      // ahead of the MMAs by the ring of Q, and would lap them
-      const bool live = a < walk.key_tiles();
-      if (live) {
-        store();
-        mbar_arrive(bar(X_K_FULL + a));
-      }
       const float k_scale = ks, f = ks * p.scale_log2;
       // the unit at hand; `walk` goes on to the next one
-      const int b = walk.b, h = walk.head(), len = walk.seq.len, n = walk.seq.n;
-      const int key = walk.key0() + a * C::BM + t;
+      const int b = walk.b, h = walk.h, len = walk.seq.len, n = walk.seq.n;
+      const int key = walk.key0() + t, key_last = walk.key0() + C::BM - 1;
       const int first = walk.first_rows(), row_tiles = walk.row_tiles;
-      const int key_last = walk.key0() + a * C::BM + 127;
       walk.next();
+      const bool more = walk.valid();
+      if (more) {
+        look_up();
+        load();
+      }
+      const bool older = part == 0 && p.accumulate && key < len - n;
+      const float was = older ? p.in.p[b * p.in.sb + h * p.in.sh + key] : 0.f;
       float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
       for (int j = first; ok && j < row_tiles; ++j, ++i) {
-        if (j == row_tiles - 1 && walk.valid()) load();
-        const int stage = i % C::INFO;
-        if (!live) {  // (warp-uniform) nothing but its share of the slot's release
-          ok = __all_sync(0xffffffffu, mbar_wait(bar(X_I_FULL + stage), (i / C::INFO) & 1, wctx,
-                                                 ERR_SITE_CACHE_WEIGHTS + 8));
-          if (ok && lane == 0) mbar_arrive(bar(X_I_EMPTY + stage));
-          continue;
-        }
+        if (more && j == row_tiles - 1) store(units + 1);
+        const int stage = i % C::INFO, buf = i & 1;
         ok = __all_sync(0xffffffffu, mbar_wait(bar(X_I_FULL + stage), (i / C::INFO) & 1, wctx,
                                                ERR_SITE_CACHE_WEIGHTS + 8) &&
-                                         mbar_wait(bar(X_S_FULL + a), mine & 1, wctx,
+                                         mbar_wait(bar(X_S_FULL + buf), (i >> 1) & 1, wctx,
                                                    ERR_SITE_CACHE_WEIGHTS + 9));
-        ++mine;
         if (!ok) break;
         tc_fence_after();
         const int tok0 = j * p.tile_tokens;
@@ -437,12 +446,12 @@ __global__ void __launch_bounds__(Ww<D>::THREADS, 1)
         const int ahead = p.causal ? key - (len - n) - tok0 : 0;
         const int from = ahead >= p.tile_tokens ? C::BN : max(0, ahead) * p.G;
         const bool diagonal = p.causal && key_last - (len - n) > tok0;
-        const uint32_t info = sbase + C::OFF_INFO + (uint32_t)(stage * C::BN + part * 128) * 4u;
-        const uint32_t tS = tmem + lane_off + a * C::BN + part * 128;
+        const uint32_t info = sbase + C::OFF_INFO + (uint32_t)(stage * C::BN + part * 64) * 4u;
+        const uint32_t tS = tmem + lane_off + buf * C::BN + part * 64;
         uint32_t v[32];
 #pragma unroll 1
-        for (int x = 0; x < 4; ++x) {
-          const int col0 = part * 128 + x * 32;
+        for (int x = 0; x < 2; ++x) {
+          const int col0 = part * 64 + x * 32;
           if (col0 >= rows) break;  // uniform
           tmem_ld32(tS + x * 32, v);
           tmem_wait_ld(v);
@@ -480,27 +489,26 @@ __global__ void __launch_bounds__(Ww<D>::THREADS, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(bar(X_S_EMPTY + a));
+          mbar_arrive(bar(X_S_EMPTY + buf));
           mbar_arrive(bar(X_I_EMPTY + stage));
         }
       }
-      // The sums of columns 128-255 join the others.  (Their place is free: this unit's S came
-      // after both halves had stored its keys, hence after the last unit's sums were read.)
+      // The other columns' sums join the first quarter's.  A unit can have one tile of rows, and
+      // S has two buffers: the later quarters may be two units ahead, hence the four places.
       float w = (s0 + s1) + (s2 + s3);
-      float* sums = reinterpret_cast<float*>(smem + C::OFF_SUM) + a * C::BM + t;
-      if (!live) continue;
-      if (part == 1) {
-        *sums = w;
-        mbar_arrive(bar(X_SUM + a));
+      const int place = units % C::SUMS, turn = units / C::SUMS;
+      float* sums = reinterpret_cast<float*>(smem + C::OFF_SUM) + place * 3 * C::BM + t;
+      ++units;
+      if (part > 0) {
+        sums[(part - 1) * C::BM] = w;
+        mbar_arrive(bar(X_SUM + place));
         continue;
       }
-      ok = ok && __all_sync(0xffffffffu, mbar_wait(bar(X_SUM + a), units & 1, wctx,
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(bar(X_SUM + place), turn & 1, wctx,
                                                    ERR_SITE_CACHE_WEIGHTS + 10));
-      ++units;
       if (ok && key < len) {
-        w = k_scale == 0.f ? 0.f : w + *sums;
-        if (p.accumulate && key < len - n) w += p.in.p[b * p.in.sb + h * p.in.sh + key];
-        p.out.p[b * p.out.sb + h * p.out.sh + key] = w;
+        w = k_scale == 0.f ? 0.f : (w + sums[0]) + (sums[C::BM] + sums[2 * C::BM]);
+        p.out.p[b * p.out.sb + h * p.out.sh + key] = was + w;
       }
     }
     __syncwarp();
