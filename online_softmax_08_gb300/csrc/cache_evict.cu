@@ -49,26 +49,18 @@ __device__ __forceinline__ int length_of(const EvictParams& p, int b) {
   return len;
 }
 
-// Sum of v over the threads before this one (their order), and over all.
-__device__ __forceinline__ int sum_before(int v, int* part, int* total) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int upto = v;
+__device__ __forceinline__ float weight_of(uint32_t u) {  // any NaN, -0 as 0
+  return __uint_as_float(u == 0xffffffffu ? 0x7fffffffu : u ^ ((u >> 31) ? 0x80000000u : 0xffffffffu));
+}
+
+// Sum of v over this lane and those before it.
+__device__ __forceinline__ int sum_upto(int v) {
 #pragma unroll
   for (int w = 1; w < 32; w <<= 1) {
-    const int o = __shfl_up_sync(0xffffffffu, upto, w);
-    if (lane >= w) upto += o;
+    const int o = __shfl_up_sync(0xffffffffu, v, w);
+    if ((int)(threadIdx.x & 31) >= w) v += o;
   }
-  __syncthreads();  // part has been read
-  if (lane == 31) part[warp] = upto;
-  __syncthreads();
-  int all = part[lane], low = lane < warp ? all : 0;
-#pragma unroll
-  for (int w = 16; w > 0; w >>= 1) {
-    all += __shfl_xor_sync(0xffffffffu, all, w);
-    low += __shfl_xor_sync(0xffffffffu, low, w);
-  }
-  *total = all;
-  return upto - v + low;
+  return v;
 }
 
 // CS: CTAs of a cluster.
@@ -77,9 +69,11 @@ __global__ void __launch_bounds__(kSelect) cache_select_kernel(const EvictParams
   namespace cg = cooperative_groups;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __shared__ alignas(8) int hist[2][kBins];  // by turns: a neighbour may still read the last one
-  __shared__ int part[32];
+  __shared__ int groups[2][32];   // of 64 bins
   __shared__ int found_bin, found_above;
-  __shared__ int counts[2][2];    // larger than the smallest kept, equal to it, of a segment
+  // Of a segment's weights in a warp, in the CTA (at most 2^15): those larger than the smallest
+  // kept one, times 2^16, and those equal to it
+  __shared__ unsigned part[2][32], counts[2];
   const int unit = blockIdx.x / CS, rank = blockIdx.x % CS;
   const int b = unit / p.c.H, h = unit % p.c.H;
   const int t = threadIdx.x + rank * kSelect;  // of the cluster's threads
@@ -91,7 +85,7 @@ __global__ void __launch_bounds__(kSelect) cache_select_kernel(const EvictParams
     else
       __syncthreads();
   };
-  auto of_rank = [](int* x, int r) {
+  auto of_rank = [](auto* x, int r) {
     if constexpr (CS > 1)
       return cg::this_cluster().map_shared_rank(x, r);
     else
@@ -112,29 +106,35 @@ __global__ void __launch_bounds__(kSelect) cache_select_kernel(const EvictParams
   }
   const int old = len - p.recent;        // those that compete
   const int top = p.keep - p.recent;     // for so many places
-  for (int j = t; j < p.recent; j += T) {
+  // A warp holds a run of `steps` x 32 neighbouring weights of a segment (kRun x kSelect of them;
+  // a sequence that is no longer than that is read once), so the kept ones are numbered by
+  // ballots, and the warps' totals by one sum over those before a segment.
+  const int warp = t >> 5, lane = t & 31, cta_warp = threadIdx.x >> 5;
+  const int steps = min(kRun, (old + T - 1) / T), segment = steps * T;
+  extern __shared__ uint32_t held[];  // [kRun * kSelect], every thread its own
+  uint32_t* const own = held + cta_warp * steps * 32 + lane;
+  auto index = [&](int seg, int i) { return seg + (warp * steps + i) * 32 + lane; };
+  auto load = [&](int seg) {
+    constexpr int N = 16;  // on their way at a time
+#pragma unroll 1
+    for (int i0 = 0; i0 < steps; i0 += N) {
+      float x[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int j = index(seg, i0 + i);
+        x[i] = i0 + i < steps && j < old ? w[j] : 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (i0 + i < steps) own[(i0 + i) * 32] = order_of(x[i]);
+    }
+  };
+  if (top > 0) load(0);
+  for (int j = t; j < p.recent; j += T) {  // (behind the loads of the others)
     kept[top + j] = old + j;
     w_out[top + j] = w[old + j];
   }
   if (top == 0) return;
-
-  // A warp holds a run of `steps` x 32 neighbouring weights of a segment (kRun x kSelect of them;
-  // a sequence that is no longer than that is read once), so the kept ones are numbered by
-  // ballots, and the warps' totals by one prefix sum a segment.
-  const int warp = t >> 5, lane = t & 31;
-  const int steps = min(kRun, (old + T - 1) / T), segment = steps * T;
-  uint32_t u[kRun];
-  auto index = [&](int seg, int i) { return seg + (warp * steps + i) * 32 + lane; };
-  auto load = [&](int seg) {
-#pragma unroll
-    for (int i = 0; i < kRun; ++i) {
-      const int j = index(seg, i);
-      u[i] = i < steps && j < old ? __float_as_uint(w[j]) : 0xffffffffu;  // (NaN, see below)
-    }
-#pragma unroll
-    for (int i = 0; i < kRun; ++i) u[i] = order_of(__uint_as_float(u[i]));
-  };
-  load(0);
 
   // ---------------------------------------------------------------- the smallest kept weight
   uint32_t prefix = 0u, mask = 0u;  // the digits found
@@ -146,38 +146,52 @@ __global__ void __launch_bounds__(kSelect) cache_select_kernel(const EvictParams
     int* bins = hist[digit & 1];
     for (int i = threadIdx.x; i < kBins; i += kSelect) bins[i] = 0;
     __syncthreads();
-    int zeros = 0;  // many weights are zero, and would all add to one bin: counted by the warp
+    int zeros = 0;  // many weights are zero, and would all add to one bin: counted apart
 #pragma unroll 1
     for (int seg = 0; seg < old; seg += segment) {
       if (old > segment) load(seg);
-#pragma unroll
-      for (int i = 0; i < kRun; ++i) {
-        if (i >= steps) break;
-        const bool on = index(seg, i) < old && (u[i] & mask) == prefix, zero = u[i] == kZero;
-        zeros += __popc(__ballot_sync(0xffffffffu, on && zero));
-        if (on && !zero) atomicAdd(&bins[u[i] >> shift & low], 1);
+#pragma unroll 4
+      for (int i = 0; i < steps; ++i) {
+        const uint32_t u = own[i * 32];
+        const bool on = index(seg, i) < old && (u & mask) == prefix, zero = u == kZero;
+        zeros += on && zero;
+        if (on && !zero) atomicAdd(&bins[u >> shift & low], 1);
       }
     }
+    zeros = __reduce_add_sync(0xffffffffu, zeros);
     if (lane == 0 && zeros > 0) atomicAdd(&bins[kZero >> shift & low], zeros);
+    __syncthreads();
+    const int2 two = *reinterpret_cast<const int2*>(bins + 2 * threadIdx.x);
+    const int group_sum = __reduce_add_sync(0xffffffffu, two.x + two.y);
+    if (lane == 0) groups[digit & 1][cta_warp] = group_sum;
     cluster_sync();
-    // bins from the top: this thread's two are kBins - 1 - 2 i and the one below
-    const int top_bin = kBins - 1 - 2 * (int)threadIdx.x;
-    int h0 = 0, h1 = 0;
+    // From the top: the group of 64 bins, a lane each, then its bins, two a lane.  One warp looks
+    // (all of them at all bins of 8 CTAs took 5000 clocks a digit, this takes 1300).
+    if (cta_warp == 0) {
+      int x = 0;
 #pragma unroll
-    for (int r = 0; r < CS; ++r) {
-      const int2 x = *reinterpret_cast<const int2*>(of_rank(bins, r) + top_bin - 1);
-      h0 += x.y, h1 += x.x;
+      for (int r = 0; r < CS; ++r) x += of_rank(groups[digit & 1], r)[31 - lane];
+      int upto = sum_upto(x);
+      const unsigned enough = __ballot_sync(0xffffffffu, upto >= need);
+      const int hit = enough ? __ffs(enough) - 1 : 31;
+      const int above_group = __shfl_sync(0xffffffffu, upto - x, hit);
+      const int top_bin = (31 - hit) * 64 + 63 - 2 * lane;
+      int h0 = 0, h1 = 0;
+#pragma unroll
+      for (int r = 0; r < CS; ++r) {
+        const int2 y = *reinterpret_cast<const int2*>(of_rank(bins, r) + top_bin - 1);
+        h0 += y.y, h1 += y.x;
+      }
+      upto = sum_upto(h0 + h1);
+      const int above = above_group + upto - h0 - h1;
+      if (above < need && above + h0 >= need) found_bin = top_bin, found_above = above;
+      if (above + h0 < need && above + h0 + h1 >= need)
+        found_bin = top_bin - 1, found_above = above + h0;
     }
-    int total;
-    const int above = sum_before(h0 + h1, part, &total);
-    if (above < need && above + h0 >= need) found_bin = top_bin, found_above = above;
-    if (above + h0 < need && above + h0 + h1 >= need)
-      found_bin = top_bin - 1, found_above = above + h0;
     __syncthreads();
     prefix |= (uint32_t)found_bin << shift;
     mask |= low << shift;
     need -= found_above;
-    __syncthreads();
   }
 
   // ---------------------------------------------------------------- the kept ones, in order
@@ -185,46 +199,68 @@ __global__ void __launch_bounds__(kSelect) cache_select_kernel(const EvictParams
 #pragma unroll 1
   for (int seg = 0, turn = 0; seg < old; seg += segment, turn ^= 1) {
     if (old > segment) load(seg);
-    int more = 0, ties = 0;  // of the warp
-#pragma unroll
-    for (int i = 0; i < kRun; ++i) {
-      if (i >= steps) break;
+    int more = 0, ties = 0;  // of the lane, then of the warp
+#pragma unroll 4
+    for (int i = 0; i < steps; ++i) {
+      const uint32_t u = own[i * 32];
       const bool in = index(seg, i) < old;
-      more += __popc(__ballot_sync(0xffffffffu, in && u[i] > prefix));
-      ties += __popc(__ballot_sync(0xffffffffu, in && u[i] == prefix));
+      more += in && u > prefix;
+      ties += in && u == prefix;
     }
-    int all_more, all_ties;
-    more = more0 + sum_before(lane == 0 ? more : 0, part, &all_more);
-    ties = ties0 + sum_before(lane == 0 ? ties : 0, part, &all_ties);
-    more = __shfl_sync(0xffffffffu, more, 0);
-    ties = __shfl_sync(0xffffffffu, ties, 0);
+    more = __reduce_add_sync(0xffffffffu, more);
+    ties = __reduce_add_sync(0xffffffffu, ties);
+    const bool any_ties = ties > 0;
+    if (lane == 0) part[turn][cta_warp] = (unsigned)more << 16 | (unsigned)ties;
+    __syncthreads();
+    const unsigned of_warp = part[turn][lane];
+    const unsigned all = __reduce_add_sync(0xffffffffu, of_warp);
+    const unsigned front = __reduce_add_sync(0xffffffffu, lane < cta_warp ? of_warp : 0u);
+    more = more0 + (int)(front >> 16), ties = ties0 + (int)(front & 0xffffu);
+    int all_more = (int)(all >> 16), all_ties = (int)(all & 0xffffu);
     if constexpr (CS > 1) {  // and of the CTAs in front
-      if (threadIdx.x == 0) counts[turn][0] = all_more, counts[turn][1] = all_ties;
+      if (threadIdx.x == 0) counts[turn] = all;
       cluster_sync();
       all_more = all_ties = 0;
 #pragma unroll
       for (int r = 0; r < CS; ++r) {
-        const int* x = of_rank(counts[turn], r);
-        const int m = x[0], e = x[1];
+        const unsigned x = *of_rank(&counts[turn], r);
+        const int m = (int)(x >> 16), e = (int)(x & 0xffffu);
         if (r < rank) more += m, ties += e;
         all_more += m, all_ties += e;
       }
     }
+    // (places are below `top` unless the weights change meanwhile, which must not harm others)
     const unsigned before = (1u << lane) - 1u;
-#pragma unroll
-    for (int i = 0; i < kRun; ++i) {
-      if (i >= steps) break;
-      const int j = index(seg, i);
-      const bool in = j < old;
-      const unsigned m = __ballot_sync(0xffffffffu, in && u[i] > prefix);
-      const unsigned e = __ballot_sync(0xffffffffu, in && u[i] == prefix);
-      const int ties_here = ties + __popc(e & before);
-      if ((m >> lane & 1u) || ((e >> lane & 1u) && ties_here < need)) {
-        const int at = more + __popc(m & before) + min(ties_here, need);
-        kept[at] = j;
-        w_out[at] = w[j];
+    if (!any_ties) {  // nearly always
+      int at = more + min(ties, need);
+#pragma unroll 4
+      for (int i = 0; i < steps; ++i) {
+        const uint32_t u = own[i * 32];
+        const bool mine = index(seg, i) < old && u > prefix;
+        const unsigned m = __ballot_sync(0xffffffffu, mine);
+        const int place = at + __popc(m & before);
+        if (mine && (unsigned)place < (unsigned)top) {
+          kept[place] = index(seg, i);
+          w_out[place] = weight_of(u);
+        }
+        at += __popc(m);
       }
-      more += __popc(m), ties += __popc(e);
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < steps; ++i) {
+        const uint32_t u = own[i * 32];
+        const bool in = index(seg, i) < old;
+        const unsigned m = __ballot_sync(0xffffffffu, in && u > prefix);
+        const unsigned e = __ballot_sync(0xffffffffu, in && u == prefix);
+        const int ties_here = ties + __popc(e & before);
+        const int place = more + __popc(m & before) + min(ties_here, need);
+        if (((m >> lane & 1u) || ((e >> lane & 1u) && ties_here < need)) &&
+            (unsigned)place < (unsigned)top) {
+          kept[place] = index(seg, i);
+          w_out[place] = weight_of(u);
+        }
+        more += __popc(m), ties += __popc(e);
+      }
     }
     more0 += all_more, ties0 += all_ties;
   }
@@ -334,6 +370,13 @@ __global__ void __launch_bounds__(kCopy) cache_copy_kernel(const EvictParams p, 
 
 template <int CS>
 cudaError_t launch_select(const EvictParams& p, long long units, cudaStream_t stream) {
+  constexpr int SMEM = kRun * kSelect * 4;
+  static unsigned long long prepared[64];
+  const cudaError_t e = prepare_once(prepared, [] {
+    return cudaFuncSetAttribute(cache_select_kernel<CS>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+  });
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeClusterDimension;
@@ -341,6 +384,7 @@ cudaError_t launch_select(const EvictParams& p, long long units, cudaStream_t st
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.gridDim = dim3((unsigned)(units * CS));
   cfg.blockDim = dim3(kSelect);
+  cfg.dynamicSmemBytes = SMEM;
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;

@@ -31,6 +31,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "evict.cuh"
 
@@ -89,6 +90,21 @@ __device__ __forceinline__ void add_x2(float& s0, float& s1, float a0, float a1)
       "mov.b64 {%0, %1}, s;\n\t}"
       : "+f"(s0), "+f"(s1)
       : "f"(a0), "f"(a1));
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t at, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+        "=r"(r[15])
+      : "r"(at));
+}
+__device__ __forceinline__ void tmem_wait_ld16(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
+                 "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
 }
 __device__ __forceinline__ float4 ld_shared_f4(uint32_t a) {
   float4 v;
@@ -448,43 +464,37 @@ __global__ void __launch_bounds__(Ww<D>::THREADS, 1)
         const bool diagonal = p.causal && key_last - (len - n) > tok0;
         const uint32_t info = sbase + C::OFF_INFO + (uint32_t)(stage * C::BN + part * 64) * 4u;
         const uint32_t tS = tmem + lane_off + buf * C::BN + part * 64;
-        uint32_t v[32];
-#pragma unroll 1
-        for (int x = 0; x < 2; ++x) {
-          const int col0 = part * 64 + x * 32;
-          if (col0 >= rows) break;  // uniform
-          tmem_ld32(tS + x * 32, v);
-          tmem_wait_ld(v);
-          // exponents of columns k, k + 1 at a time
-          auto term = [&](int k, float l0, float l1, float& e0, float& e1) {
-            fma_x2(__uint_as_float(v[k]), __uint_as_float(v[k + 1]), f, l0, l1, e0, e1);
-            e0 = ex2(e0), e1 = ex2(e1);
-          };
-          const uint32_t li = info + (uint32_t)(x * 32) * 4u;
-          if (diagonal || col0 + 32 > rows) {
+        // 16 columns at a time, the next ones on their way; the exponents of two at a time
+        uint32_t v[2][16];
+        auto columns = [&](auto masked) {
+          tmem_ld16(tS, v[0]);
 #pragma unroll
-            for (int k = 0; k < 32; k += 4) {
-              const float4 l = ld_shared_f4(li + k * 4u);
+          for (int x = 0; x < 4; ++x) {
+            uint32_t(&y)[16] = v[x & 1];
+            tmem_wait_ld16(y);
+            if (x < 3) tmem_ld16(tS + (x + 1) * 16, v[(x + 1) & 1]);
+#pragma unroll
+            for (int k = 0; k < 16; k += 4) {
+              const float4 l = ld_shared_f4(info + (x * 16 + k) * 4u);
               float e[4];
-              term(k, l.x, l.y, e[0], e[1]);
-              term(k + 2, l.z, l.w, e[2], e[3]);
+              fma_x2(__uint_as_float(y[k]), __uint_as_float(y[k + 1]), f, l.x, l.y, e[0], e[1]);
+              fma_x2(__uint_as_float(y[k + 2]), __uint_as_float(y[k + 3]), f, l.z, l.w, e[2], e[3]);
 #pragma unroll
-              for (int y = 0; y < 4; ++y)
-                if (col0 + k + y < from || col0 + k + y >= rows) e[y] = 0.f;
+              for (int z = 0; z < 4; ++z) {
+                e[z] = ex2(e[z]);
+                const int col = part * 64 + x * 16 + k + z;
+                if (masked && (col < from || col >= rows)) e[z] = 0.f;
+              }
               add_x2(s0, s1, e[0], e[1]);
               add_x2(s2, s3, e[2], e[3]);
             }
-          } else {
-#pragma unroll
-            for (int k = 0; k < 32; k += 4) {
-              const float4 l = ld_shared_f4(li + k * 4u);
-              float e0, e1, e2, e3;
-              term(k, l.x, l.y, e0, e1);
-              term(k + 2, l.z, l.w, e2, e3);
-              add_x2(s0, s1, e0, e1);
-              add_x2(s2, s3, e2, e3);
-            }
           }
+        };
+        if (part * 64 < rows) {
+          if (diagonal || part * 64 + 64 > rows)
+            columns(std::true_type());
+          else
+            columns(std::false_type());
         }
         tc_fence_before();
         __syncwarp();

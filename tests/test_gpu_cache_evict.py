@@ -334,6 +334,99 @@ def test_bad_entries_are_reported():
     assert fattn.fattn_device_error() == 0x481
 
 
+@pytest.mark.parametrize("n", [1, 70])
+def test_captured_and_on_another_stream(n):
+    """Weights and eviction captured once and replayed with other lengths, queries and weights;
+    on a stream of their own; and two at a time."""
+    H, G, d, bs, keep = 2, 4, 128, 32, 40
+    c = _case([(n, 130), (n, 20), (n, 300)], H, d, bs, "e4m3", seed=n).fill()
+    table_out = _scatter(c, [keep] * 3, bs)
+    cache, batch = c.on_device()
+    table_out = torch.tensor(table_out, device=DEV)
+    lens = batch.lens.clone()
+    q = _bf16(c.rng, (c.T, H * G, d)).to(DEV)
+    w = torch.zeros((3, H, 384), device=DEV)
+    ws = torch.empty(1 << 26, dtype=torch.uint8, device=DEV)
+    w_out = torch.zeros((3, H, keep), device=DEV)
+
+    def step():
+        o, lse = fattn.cache_forward(q, cache, batch, 0.1, True, workspace=ws)
+        fattn.cache_weights(q, lse, cache, batch, 0.1, True, None, out=w)
+        new, kept, _ = fattn.cache_evict(cache, w, batch.block_table, batch.lens, table_out, keep,
+                                         7, out=w_out)
+        return lse, new, kept
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        step()
+        with torch.cuda.graph(graph, stream=side):
+            lse, new, kept = step()
+    torch.cuda.synchronize()
+    for i in range(2):
+        batch.lens.copy_(lens - 11 * i)
+        c.lens = (lens - 11 * i).cpu().numpy()
+        q.copy_(_bf16(c.rng, tuple(q.shape)))
+        w.zero_()
+        w_out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        _check_weights(c, "e4m3", q, lse, 0.1, True, None, np.zeros(w.shape), w)
+        host = {name: getattr(cache, name).cpu() for name in cache._fields}
+        want, chosen, count = oe.evict(
+            {name: (a.view(torch.uint8) if a.element_size() == 1 else a).numpy()
+             for name, a in host.items()}, "e4m3", c.table, c.lens, w.cpu().numpy(),
+            table_out.cpu().numpy(), keep, 7)
+        np.testing.assert_array_equal(new.cpu().numpy(), count)
+        for b in range(3):
+            for h in range(H):
+                np.testing.assert_array_equal(kept[b, h, :count[b]].cpu().numpy(), chosen[b][h])
+        base8._assert_cache(cache, want, "e4m3")
+    # two streams at once, each its own outputs
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [torch.zeros_like(w) for _ in streams]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for st, x in zip(streams, outs):
+            fattn.cache_weights(q, lse, cache, batch, 0.1, True, None, out=x, stream=st)
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], w) and torch.equal(outs[1], w)
+    other = fattn.cache_evict(cache, w, batch.block_table, batch.lens, table_out, keep, 7,
+                              stream=streams[0])
+    streams[0].synchronize()
+    assert torch.equal(other[0], new) and torch.equal(other[1], kept) and torch.equal(other[2], w_out)
+
+
+def test_weights_and_eviction_past_32_bits():
+    """A pool of more than 2^32 bytes of codes, whose last blocks are used."""
+    H, d, bs, keep = 8, 128, 128, 100
+    nb = (1 << 32) // (H * bs * d // 2) + 8
+    c = _case([(1, 200), (140, 30)], H, d, bs, "int4", spare=0).fill()
+    table_out = _scatter(c, [keep, keep], bs)
+    small, batch = c.on_device()
+    cache = fattn.new_cache(nb, H, bs, d, dtype=torch.uint8, device=DEV)
+    used = small.k.shape[0]
+    for name in cache._fields:
+        getattr(cache, name).view(torch.uint8)[-used:] = getattr(small, name).view(torch.uint8)
+    move = lambda t: torch.where((t >= 0) & (t < used), t + (nb - used), t).contiguous()
+    moved = batch._replace(block_table=move(batch.block_table))
+    table_out = torch.tensor(table_out, device=DEV)
+    q = _bf16(c.rng, (c.T, H * 2, d)).to(DEV)
+    _, lse = fattn.cache_forward(q, small, batch, 0.1, True)
+    got = []
+    for pool, b, to in ((small, batch, table_out), (cache, moved, move(table_out))):
+        w = fattn.cache_weights(q, lse, pool, b, 0.1, True)
+        got.append((w,) + fattn.cache_evict(pool, w, b.block_table, b.lens, to, keep, 9))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    for name in cache._fields:
+        assert torch.equal(getattr(cache, name).view(torch.uint8)[-used:],
+                           getattr(small, name).view(torch.uint8))
+    del cache
+    torch.cuda.empty_cache()
+
+
 def test_serving_run():
     """What they are for, together: queries and keys are turned, the keys and values go into the
     4-bit cache, the queries attend and weigh the keys, the cache is cut to its most attended
