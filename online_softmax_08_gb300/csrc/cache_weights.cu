@@ -82,8 +82,9 @@ __global__ void __launch_bounds__(32 * kWarpsW, ctas_w(D))
   };
   long long total = 0;
   CacheSeq seq;
+  const long long n_first = lane < c.B ? units_of(lane, &seq) : 0;
   for (int b0 = 0; b0 < c.B; b0 += 32) {
-    long long n = b0 + lane < c.B ? units_of(b0 + lane, &seq) : 0;
+    long long n = b0 == 0 ? n_first : b0 + lane < c.B ? units_of(b0 + lane, &seq) : 0;
 #pragma unroll
     for (int w = 16; w > 0; w >>= 1) n += __shfl_xor_sync(0xffffffffu, n, w);
     total += n;
@@ -94,7 +95,7 @@ __global__ void __launch_bounds__(32 * kWarpsW, ctas_w(D))
   long long before = 0;  // units of the sequences before b
   int b = 0;
   for (int b0 = 0; b0 < c.B; b0 += 32) {
-    const long long n = b0 + lane < c.B ? units_of(b0 + lane, &seq) : 0;
+    const long long n = b0 == 0 ? n_first : b0 + lane < c.B ? units_of(b0 + lane, &seq) : 0;
     long long upto = n;
 #pragma unroll
     for (int w = 1; w < 32; w <<= 1) {
@@ -134,9 +135,11 @@ __global__ void __launch_bounds__(32 * kWarpsW, ctas_w(D))
   uint32_t codes[2][2][RW], scales[2][2];
   float ks_next[2] = {1.f, 1.f};
   bool live[2];
+  const bool one_block = c.block_size >= 32;  // holds all of a warp's keys
   auto look_up = [&](const At& at) {
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
+      if (m == 1 && one_block) break;
       pages[m] = -1;
       if (at.left <= 0) continue;
       const int key = at.key + warp * 32 + 16 * m;
@@ -146,27 +149,30 @@ __global__ void __launch_bounds__(32 * kWarpsW, ctas_w(D))
     }
   };
   auto load = [&](const At& at) {  // from the pages looked up for it
+    long long row = 0;
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
-      const int key = at.key + warp * 32 + 16 * m;
-      int page = pages[m];
-      if (page != -1 && (page < 0 || page >= c.num_blocks)) {
-        if (c.err) atomicCAS(c.err, 0u, (unsigned)ERR_SITE_CACHE_WEIGHTS + 1);
-        page = -1;
+      if (m == 1 && one_block) {
+        row += 16;
+        live[1] = live[0];
+        ks_next[1] = ks_next[0];
+      } else {
+        const int key = at.key + warp * 32 + 16 * m;
+        int page = pages[m];
+        live[m] = page >= 0 && page < c.num_blocks;
+        if (!live[m]) {  // (block 0 is read instead, and what comes of it is not used)
+          if (page != -1 && c.err) atomicCAS(c.err, 0u, (unsigned)ERR_SITE_CACHE_WEIGHTS + 1);
+          page = 0;
+        }
+        const long long block = (long long)page * c.H + at.h;
+        if constexpr (!I4) ks_next[m] = c.k_scale[block];
+        // (rows behind the sequence's end are read as well: they lie in its block)
+        row = (block << c.block_log2) + (key & (c.block_size - 1)) + g;
       }
-      live[m] = page >= 0;
-      if constexpr (!I4) ks_next[m] = page < 0 ? 1.f : c.k_scale[(long long)page * c.H + at.h];
-      // (rows behind the sequence's end are read as well: they lie in its block)
-      const long long row =
-          ((((long long)page * c.H + at.h) << c.block_log2) + (key & (c.block_size - 1))) + g;
       const uint8_t* from = c.k + row * RB + t * (I4 ? D / 8 : 16);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         uint32_t(&w)[RW] = codes[m][i];
-#pragma unroll
-        for (int x = 0; x < RW; ++x) w[x] = 0u;
-        scales[m][i] = 0u;
-        if (page < 0) continue;
         if constexpr (I4 && D == 128) {
           const uint4 x = __ldg(reinterpret_cast<const uint4*>(from + i * 8 * RB));
           w[0] = x.x, w[1] = x.y, w[RW - 2] = x.z, w[RW - 1] = x.w;
@@ -231,19 +237,11 @@ __global__ void __launch_bounds__(32 * kWarpsW, ctas_w(D))
         }
       }
     }
-    const long long first = key0 + g;
-    float* const out = p.out.p + (b * p.out.sb + h * p.out.sh + first);
-    const float* const in = p.in.p + (b * p.in.sb + h * p.in.sh + first);
-    const int ends = seq.len - (int)first;                // keys of this lane behind it
-    const int older = p.accumulate ? ends - seq.n : 0;    // those that had a weight before
-    float was[2][2];  // of the lanes that write
-#pragma unroll
-    for (int m = 0; m < 2; ++m)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int x = 16 * m + 8 * i;
-        was[m][i] = t == 0 && x < older ? in[x] : 0.f;
-      }
+    // A lane ends with the sum of one key, key0 + 8 t + g, and stores it
+    const int mine = key0 + 8 * t + g;
+    const bool kept = mine < seq.len;
+    const float was = p.accumulate && mine < seq.len - seq.n
+                          ? p.in.p[b * p.in.sb + h * p.in.sh + mine] : 0.f;
     load(next);
     now = next;
     advance(&next);
@@ -348,16 +346,16 @@ __global__ void __launch_bounds__(32 * kWarpsW, ctas_w(D))
           for (int i = 0; i < 2; ++i) sum[m][i] += s[m][2 * i] + s[m][2 * i + 1];
       }
     }
+    // over the four lanes of a key; lane t goes on with keys 8 t + g alone
+    float half[2];
 #pragma unroll
     for (int m = 0; m < 2; ++m)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float x = sum[m][i];
-        x += __shfl_xor_sync(0xffffffffu, x, 1);
-        x += __shfl_xor_sync(0xffffffffu, x, 2);
-        // (no block there: nothing from the queries)
-        if (t == 0 && 16 * m + 8 * i < ends) out[16 * m + 8 * i] = was[m][i] + (there[m] ? x : 0.f);
-      }
+      half[m] = (t & 1 ? sum[m][1] : sum[m][0]) +
+                __shfl_xor_sync(0xffffffffu, t & 1 ? sum[m][0] : sum[m][1], 1);
+    const float x = (t & 2 ? half[1] : half[0]) +
+                    __shfl_xor_sync(0xffffffffu, t & 2 ? half[0] : half[1], 2);
+    // (no block there: nothing from the queries)
+    if (kept) p.out.p[b * p.out.sb + h * p.out.sh + mine] = was + ((t & 2 ? there[1] : there[0]) ? x : 0.f);
   }
 }
 
