@@ -32,6 +32,7 @@ constexpr int kBins = 2048;
 constexpr int kRun = 32;       // weights that a thread of it holds at a time
 constexpr uint32_t kZero = 0x80000000u;  // a weight of zero, as an ordered number
 constexpr int kCopy = 128;     // threads of a copy
+constexpr int kAhead = 4;      // 16-byte pieces that each has on their way
 
 __device__ __forceinline__ uint32_t order_of(float w) {
   const uint32_t u = __float_as_uint(w + 0.f);  // -0 as 0
@@ -330,30 +331,43 @@ __global__ void __launch_bounds__(kCopy) cache_copy_kernel(const EvictParams p, 
   }
   constexpr int RB = I4 ? D / 2 : D, PIECES = RB / 16;  // 16-byte pieces of a row
   const long long out0 = block_out << c.block_log2;
-  for (int x = t; x < count * PIECES * 2; x += kCopy) {
-    const bool value = x >= count * PIECES;
-    const int y = value ? x - count * PIECES : x;
-    const int r = y / PIECES, piece = y % PIECES;
-    const long long row = row_of[r];
-    uint8_t* codes = value ? c.v : c.k;
-    uint4 v = I4 ? make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u)
-                 : make_uint4(0u, 0u, 0u, 0u);
-    if (row >= 0) v = *reinterpret_cast<const uint4*>(codes + row * RB + piece * 16);
-    if constexpr (!I4) {
-      const float from = value ? vs_of[r] : ks_of[r], to = value ? vs_max : ks_max;
-      if (from != to && row >= 0) {  // rounded for the larger scale
-        const float f = from / to;
-        uint32_t* w = &v.x;
+  const int pieces = count * PIECES;  // of the keys, and as many of the values
+  for (int x0 = t; x0 < 2 * pieces; x0 += kAhead * kCopy) {
+    uint4 v[kAhead];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 lo = f16x2_to_f32(codes_to_f16x2<E5M2>((uint16_t)(w[k] & 0xffffu)));
-          const float2 hi = f16x2_to_f32(codes_to_f16x2<E5M2>((uint16_t)(w[k] >> 16)));
-          w[k] = (uint32_t)f32_to_codes<E5M2>(lo.x * f, lo.y * f) |
-                 (uint32_t)f32_to_codes<E5M2>(hi.x * f, hi.y * f) << 16;
+    for (int n = 0; n < kAhead; ++n) {
+      const int x = x0 + n * kCopy;
+      const bool value = x >= pieces;
+      const int y = value ? x - pieces : x;
+      v[n] = I4 ? make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u)
+                : make_uint4(0u, 0u, 0u, 0u);
+      if (x >= 2 * pieces) continue;
+      const long long row = row_of[y / PIECES];
+      if (row >= 0)
+        v[n] = *reinterpret_cast<const uint4*>((value ? c.v : c.k) + row * RB + y % PIECES * 16);
+    }
+#pragma unroll
+    for (int n = 0; n < kAhead; ++n) {
+      const int x = x0 + n * kCopy;
+      if (x >= 2 * pieces) break;
+      const bool value = x >= pieces;
+      const int y = value ? x - pieces : x, r = y / PIECES;
+      if constexpr (!I4) {
+        const float from = value ? vs_of[r] : ks_of[r], to = value ? vs_max : ks_max;
+        if (from != to && row_of[r] >= 0) {  // rounded for the larger scale
+          const float f = from / to;
+          uint32_t* w = &v[n].x;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 lo = f16x2_to_f32(codes_to_f16x2<E5M2>((uint16_t)(w[k] & 0xffffu)));
+            const float2 hi = f16x2_to_f32(codes_to_f16x2<E5M2>((uint16_t)(w[k] >> 16)));
+            w[k] = (uint32_t)f32_to_codes<E5M2>(lo.x * f, lo.y * f) |
+                   (uint32_t)f32_to_codes<E5M2>(hi.x * f, hi.y * f) << 16;
+          }
         }
       }
+      *reinterpret_cast<uint4*>((value ? c.v : c.k) + (out0 + r) * RB + y % PIECES * 16) = v[n];
     }
-    *reinterpret_cast<uint4*>(codes + (out0 + r) * RB + piece * 16) = v;
   }
   if constexpr (I4) {
     using S = typename std::conditional<D == 128, uint2, uint32_t>::type;  // a token's scales
