@@ -16,8 +16,8 @@
 // even, and leaves the code in the low four bits.
 //
 // The bound is memory, and next to it the logic pipe, which the quantising of a group takes
-// 70 % of while it is written (measured: 32768 tokens of 16 heads, d = 128, 60 us written, 57
-// read back, 84 and 89 % of the measured copy bandwidth).
+// 68 % of while it is written (measured: 32768 tokens of 16 heads, d = 128, 58.5 us written, 54.5
+// read back, 87 and 93 % of the measured copy bandwidth).
 // A thread holds one group: 32 bytes of bf16 and 8 + 1 of the cache.
 // A warp takes kIter x 32 groups of one head: the rows of 16 (d = 64: 32) packed tokens one
 // behind another, so a prompt's codes and scales are written as whole lines, then the same of

@@ -16,6 +16,13 @@
 // Work split.  A unit is (sequence, head, 128 keys); the units in that order are cut into equal
 // contiguous shares, one per CTA, so a CTA goes through neighbouring keys of one sequence and,
 // where the rows are at most 32, loads them once for all of them.
+//
+// Measured, one token of each of 32 sequences of 512 to 8192 tokens, 32 query and 8 key heads, 4 bits,
+// d = 128: 20.5 us, 42 % of the measured copy bandwidth.  It is bound by issue, 520 instructions
+// for 32 keys a warp at 2.0 a clock (168 registers: 12 warps an SM), and by the start of a
+// share, 5000 of 39,000 clocks.  (With the next keys' codes loaded where they are needed 32 us, a block
+// number for every 16 keys, zeroed registers for keys without a block and a key's sum
+// stored by one lane of four 23.4; the rows staged ahead of the keys' conversion 21.8.)
 #include <math.h>
 
 #include "evict.cuh"

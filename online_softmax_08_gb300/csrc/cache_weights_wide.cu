@@ -24,9 +24,10 @@
 // instructions and commits take 1500 clocks a tile, as it shares its issue slots with the
 // exponentials.  (Built and measured before this, 512 queries behind 16384 tokens, 32 query and
 // 8 key heads, d = 128: mma.sync 457 us; 256 keys a unit, 8 warps, tiles of 128 rows 127 us, 16
-// warps 94 us; tiles of 256 rows, S in one buffer for each 128 keys, 88 us.)  Now 76 us: a tile
-// takes 2200 clocks, of which a warp's 64 columns take 1650, its waits and what it does between
-// tiles the rest, and a change of unit 4500.
+// warps 94 us; tiles of 256 rows, S in one buffer for each 128 keys, 88 us; S in two, 32
+// columns loaded at a time, 76 us: a tile took 2200 clocks, of which a warp's 64 columns took 1650,
+// its waits and what it does between tiles the rest, and a change of unit 4500.)  Now, the next 16
+// columns on their way while 16 are worked on, 75 us, 931 TFLOP/s.
 #define FATTN_INLINE_WAIT_SLOW_PATH
 #include <math.h>
 

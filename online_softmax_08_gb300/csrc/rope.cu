@@ -13,6 +13,8 @@
 // The bound is memory: every value is read and written once.  A thread holds 8 pairs, so
 // eight sines and cosines, and takes them through the heads of its token, queries and keys:
 // 32 bytes of a row, as two 16-byte pieces.  kUnroll heads' loads are in flight at a time.
+// Measured: 16384 tokens of 32 + 8 heads, d = 128, 53 us, 6340 GB/s, 93 % of the measured copy
+// bandwidth; 64 tokens 2.9 us.
 #include "rope.cuh"
 
 namespace fattn {
