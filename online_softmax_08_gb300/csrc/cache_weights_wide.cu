@@ -16,8 +16,7 @@
 //                   tb = 256 / G tokens of the group's G heads, which a box {64, G, tb} leaves as
 //                   rows
 //   warps 17, 19    the MMAs, a thread each for the tiles of one of two S buffers
-//   warp 18         the rows' log-sum-exp, in a ring of their own, as Q's slots are free again
-//                   once the MMAs have read them
+//   warp 18         the rows' log-sum-exp, a place for each S buffer
 // The bound is the special-function unit: 128 x 256 exponentials take 1024 clocks at the 32 a
 // clock that were measured, the products of that tile 768 (A and B come from shared memory at
 // 128 bytes a clock).  One thread that issued all MMAs was the bound before: its waits, 8
@@ -48,12 +47,11 @@ struct Ww {
   static constexpr int TILE = BM * D * 2;
   static constexpr int Q_HALF = BN * 128, Q_TILE = BN * D * 2;
   static constexpr int ST = D == 128 ? 2 : 4;
-  static constexpr int INFO = 8;             // tiles of rows
   static constexpr int SUMS = 4;             // units
   static constexpr int OFF_K = 0;            // [2]
   static constexpr int OFF_Q = 2 * TILE;
-  static constexpr int OFF_INFO = OFF_Q + ST * Q_TILE;      // [INFO][BN] -lse log2(e)
-  static constexpr int OFF_SUM = OFF_INFO + INFO * BN * 4;  // [SUMS][3][BM] of the later columns
+  static constexpr int OFF_INFO = OFF_Q + ST * Q_TILE;      // [2][BN] -lse log2(e)
+  static constexpr int OFF_SUM = OFF_INFO + 2 * BN * 4;  // [SUMS][3][BM] of the later columns
   static constexpr int OFF_BAR = OFF_SUM + SUMS * 3 * BM * 4;
   static constexpr int SMEM = OFF_BAR + 512 + 1024;
   static constexpr int W_LOAD = 16, W_MMA = 17, W_INFO = 18, W_MMA2 = 19, THREADS = 640;
@@ -63,13 +61,12 @@ struct Ww {
 };
 enum {
   X_K_FULL = 0,    // [2] keys in shared memory (512 threads)
-  X_S_FULL = 2,    // [2]
+  X_S_FULL = 2,    // [2] S, and the log-sum-exp of its rows
   X_S_EMPTY = 4,   // [2], 16 warps
   X_DONE = 6,      // [2]
   X_SUM = 8,       // [SUMS] the sums of the later columns (384 threads)
-  X_I_FULL = 12,   // [INFO] the rows' log-sum-exp
-  X_I_EMPTY = 20,  // [INFO], 16 warps
-  X_Q_FULL = 28,   // [ST], then q_empty [ST]
+  X_I_FULL = 12,   // [2] the rows' log-sum-exp
+  X_Q_FULL = 14,   // [ST], then q_empty [ST]
 };
 
 __device__ __forceinline__ void fma_x2(float a0, float a1, float b, float c0, float c1, float& r0,
@@ -212,25 +209,20 @@ __global__ void __launch_bounds__(Ww<D>::THREADS, 1)
   volatile uint32_t* abort_flag = tmem_slot + 1;
   const WaitCtx wctx{abort_flag, c.err};
   static_assert(8 * (X_Q_FULL + 2 * ST) + 8 <= 512, "barrier block");
-  static_assert(X_I_EMPTY - X_I_FULL == C::INFO && X_Q_FULL - X_I_EMPTY == C::INFO &&
-                    X_I_FULL - X_SUM == C::SUMS,
-                "barriers");
+  static_assert(X_I_FULL - X_SUM == C::SUMS, "barriers");
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(X_K_FULL + i), 512);
-      mbar_init(bar(X_S_FULL + i), 1);
+      mbar_init(bar(X_S_FULL + i), 2);
       mbar_init(bar(X_S_EMPTY + i), 16);
       mbar_init(bar(X_DONE + i), 1);
+      mbar_init(bar(X_I_FULL + i), 1);
     }
     for (int i = 0; i < C::SUMS; ++i) mbar_init(bar(X_SUM + i), 384);
     for (int i = 0; i < ST; ++i) {
       mbar_init(q_full0 + 8u * i, 1);
       mbar_init(q_empty0 + 8u * i, 1);
-    }
-    for (int i = 0; i < C::INFO; ++i) {
-      mbar_init(bar(X_I_FULL + i), 1);
-      mbar_init(bar(X_I_EMPTY + i), 16);
     }
     *abort_flag = 0u;
     fence_mbar_init();
@@ -279,7 +271,7 @@ __global__ void __launch_bounds__(Ww<D>::THREADS, 1)
     for (; ok && walk.valid(); walk.next()) {
       const int h = walk.h, n = walk.seq.n, row0 = walk.seq.row0;
       for (int j = walk.first_rows(); j < walk.row_tiles; ++j, ++i) {
-        const int stage = i % C::INFO, use = i / C::INFO;
+        const int buf = i & 1, use = i >> 1;
         const int tok0 = j * p.tile_tokens;
         const int rows = min(p.tile_tokens, n - tok0) * p.G;
         float l[C::BN / 32];
@@ -290,15 +282,15 @@ __global__ void __launch_bounds__(Ww<D>::THREADS, 1)
           if (r < rows)
             l[k] = p.lse[(long long)(h * p.G + p.by_G.mod(r)) * c.total + row0 + tok0 + p.by_G.div(r)];
         }
-        ok = use == 0 || __all_sync(0xffffffffu, mbar_wait(bar(X_I_EMPTY + stage), (use - 1) & 1, wctx,
+        ok = use == 0 || __all_sync(0xffffffffu, mbar_wait(bar(X_S_EMPTY + buf), (use - 1) & 1, wctx,
                                                            ERR_SITE_CACHE_WEIGHTS + 11));
         if (!ok) break;
 #pragma unroll
         for (int k = 0; k < C::BN / 32; ++k)  // a row that saw nothing adds nothing
-          reinterpret_cast<float*>(smem + C::OFF_INFO)[stage * C::BN + k * 32 + lane] =
+          reinterpret_cast<float*>(smem + C::OFF_INFO)[buf * C::BN + k * 32 + lane] =
               l[k] == -INFINITY ? -INFINITY : -l[k] * kLog2eV;
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(X_I_FULL + stage));
+        if (lane == 0) mbar_arrive(bar(X_I_FULL + buf));
       }
     }
     __syncwarp();
@@ -335,6 +327,9 @@ __global__ void __launch_bounds__(Ww<D>::THREADS, 1)
                         qb + (uint32_t)(((kk >> 2) * C::Q_HALF + (kk & 3) * 32) >> 4), idesc, kk > 0);
           mma_commit(bar(X_S_FULL + buf));
           mma_commit(q_empty0 + 8u * stage);
+          // on behalf of the log-sum-exp: one wait less for 16 warps
+          ok = mbar_wait(bar(X_I_FULL + buf), use & 1, wctx, ERR_SITE_CACHE_WEIGHTS + 8);
+          if (ok) mbar_arrive(bar(X_S_FULL + buf));
         }
       }
       mma_commit(bar(X_DONE + buf));  // drain before TMEM is freed
@@ -450,11 +445,9 @@ __global__ void __launch_bounds__(Ww<D>::THREADS, 1)
       float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
       for (int j = first; ok && j < row_tiles; ++j, ++i) {
         if (more && j == row_tiles - 1) store(units + 1);
-        const int stage = i % C::INFO, buf = i & 1;
-        ok = __all_sync(0xffffffffu, mbar_wait(bar(X_I_FULL + stage), (i / C::INFO) & 1, wctx,
-                                               ERR_SITE_CACHE_WEIGHTS + 8) &&
-                                         mbar_wait(bar(X_S_FULL + buf), (i >> 1) & 1, wctx,
-                                                   ERR_SITE_CACHE_WEIGHTS + 9));
+        const int buf = i & 1;
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(X_S_FULL + buf), (i >> 1) & 1, wctx,
+                                               ERR_SITE_CACHE_WEIGHTS + 9));
         if (!ok) break;
         tc_fence_after();
         const int tok0 = j * p.tile_tokens;
@@ -463,7 +456,7 @@ __global__ void __launch_bounds__(Ww<D>::THREADS, 1)
         const int ahead = p.causal ? key - (len - n) - tok0 : 0;
         const int from = ahead >= p.tile_tokens ? C::BN : max(0, ahead) * p.G;
         const bool diagonal = p.causal && key_last - (len - n) > tok0;
-        const uint32_t info = sbase + C::OFF_INFO + (uint32_t)(stage * C::BN + part * 64) * 4u;
+        const uint32_t info = sbase + C::OFF_INFO + (uint32_t)(buf * C::BN + part * 64) * 4u;
         const uint32_t tS = tmem + lane_off + buf * C::BN + part * 64;
         // 16 columns at a time, the next ones on their way; the exponents of two at a time
         uint32_t v[2][16];
@@ -499,10 +492,7 @@ __global__ void __launch_bounds__(Ww<D>::THREADS, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(bar(X_S_EMPTY + buf));
-          mbar_arrive(bar(X_I_EMPTY + stage));
-        }
+        if (lane == 0) mbar_arrive(bar(X_S_EMPTY + buf));
       }
       // The other columns' sums join the first quarter's.  A unit can have one tile of rows, and
       // S has two buffers: the later quarters may be two units ahead, hence the four places.
