@@ -420,6 +420,7 @@ __global__ void __launch_bounds__(Ww<D>::THREADS, 1)
       fence_proxy_async_smem();
       mbar_arrive(bar(X_K_FULL + (u & 1)));
     };
+    const bool whole = part * 64 + 64 <= p.tile_tokens * p.G;  // of a tile without its last rows
     int i = 0;      // tiles of rows so far
     int units = 0;
     bool ok = true;
@@ -443,24 +444,31 @@ __global__ void __launch_bounds__(Ww<D>::THREADS, 1)
       const bool older = part == 0 && p.accumulate && key < len - n;
       const float was = older ? p.in.p[b * p.in.sb + h * p.in.sh + key] : 0.f;
       float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
-      for (int j = first; ok && j < row_tiles; ++j, ++i) {
+      // rows of tokens from here on see all of the unit's keys
+      const int all_seen = p.causal ? key_last - (len - n) : 0;
+      int tok0 = first * p.tile_tokens;
+      for (int j = first; ok && j < row_tiles; ++j, ++i, tok0 += p.tile_tokens) {
         if (more && j == row_tiles - 1) store(units + 1);
         const int buf = i & 1;
         ok = __all_sync(0xffffffffu, mbar_wait(bar(X_S_FULL + buf), (i >> 1) & 1, wctx,
                                                ERR_SITE_CACHE_WEIGHTS + 9));
         if (!ok) break;
         tc_fence_after();
-        const int tok0 = j * p.tile_tokens;
-        const int rows = min(p.tile_tokens, n - tok0) * p.G;
-        // this key is seen by rows from `from` on
-        const int ahead = p.causal ? key - (len - n) - tok0 : 0;
-        const int from = ahead >= p.tile_tokens ? C::BN : max(0, ahead) * p.G;
-        const bool diagonal = p.causal && key_last - (len - n) > tok0;
+        int rows = 0, from = 0;
+        bool masked = false, some = true;
+        if (tok0 < all_seen || tok0 + p.tile_tokens > n || !whole) {
+          rows = min(p.tile_tokens, n - tok0) * p.G;
+          // this key is seen by rows from `from` on
+          const int ahead = p.causal ? key - (len - n) - tok0 : 0;
+          from = ahead >= p.tile_tokens ? C::BN : max(0, ahead) * p.G;
+          masked = tok0 < all_seen || part * 64 + 64 > rows;
+          some = part * 64 < rows;
+        }
         const uint32_t info = sbase + C::OFF_INFO + (uint32_t)(buf * C::BN + part * 64) * 4u;
         const uint32_t tS = tmem + lane_off + buf * C::BN + part * 64;
         // 16 columns at a time, the next ones on their way; the exponents of two at a time
         uint32_t v[2][16];
-        auto columns = [&](auto masked) {
+        auto columns = [&](auto with_mask) {
           tmem_ld16(tS, v[0]);
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
@@ -477,19 +485,17 @@ __global__ void __launch_bounds__(Ww<D>::THREADS, 1)
               for (int z = 0; z < 4; ++z) {
                 e[z] = ex2(e[z]);
                 const int col = part * 64 + x * 16 + k + z;
-                if (masked && (col < from || col >= rows)) e[z] = 0.f;
+                if (with_mask && (col < from || col >= rows)) e[z] = 0.f;
               }
               add_x2(s0, s1, e[0], e[1]);
               add_x2(s2, s3, e[2], e[3]);
             }
           }
         };
-        if (part * 64 < rows) {
-          if (diagonal || part * 64 + 64 > rows)
-            columns(std::true_type());
-          else
-            columns(std::false_type());
-        }
+        if (!masked && some)
+          columns(std::false_type());
+        else if (some)
+          columns(std::true_type());
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(X_S_EMPTY + buf));
