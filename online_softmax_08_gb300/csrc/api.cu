@@ -752,6 +752,7 @@ extern "C" int fattn_cache_weights(const fattn_cache* cache, const fattn_cache_b
   if ((long long)batch->max_seqlen * p.G > 32 && p.G <= 256 && mapped) {
     p.narrow_rows = 32;
     p.tile_tokens = 256 / p.G;
+    p.by_tile = FastDiv((unsigned)p.tile_tokens);
     CUtensorMap tq;
     const cuuint64_t dims[3] = {(cuuint64_t)cache->d, (cuuint64_t)Hq, (cuuint64_t)T};
     const cuuint64_t strides[2] = {(cuuint64_t)(Hq > 1 ? v.sh : cache->d) * 2,

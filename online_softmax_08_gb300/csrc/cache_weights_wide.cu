@@ -119,8 +119,8 @@ template <int KEYS>
 struct Walk {
   const WeightParams& p;
   long long before, hi;  // cost of the sequences before; end of the share
+  long long rest;        // units of the sequence that are the share's, from this one on
   int b, h, tile;        // sequence, head, tile of keys
-  long long u;           // unit in the sequence
   CacheSeq seq;
   int tiles, row_tiles;  // of keys, of rows
   __device__ __forceinline__ long long cost_of(int b) {
@@ -142,7 +142,7 @@ struct Walk {
     }
     const long long share = (total + gridDim.x - 1) / gridDim.x, lo = blockIdx.x * share;
     hi = min(total, lo + share);
-    b = p.c.B, u = 0, h = tile = 0, before = total;
+    b = p.c.B, rest = 0, h = tile = 0, before = total;
     if (lo >= hi) return;
     before = 0;
     for (int b0 = 0; b0 < p.c.B; b0 += 32) {
@@ -162,32 +162,39 @@ struct Walk {
       }
       before += __shfl_sync(0xffffffffu, upto, 31);
     }
-    const long long n = cost_of(b);
-    u = (lo - before + row_tiles - 1) / row_tiles;
+    const long long n = cost_of(b), u = (lo - before + row_tiles - 1) / row_tiles;
     h = (int)(u / tiles);
     tile = (int)(u % tiles);
-    skip(n);
+    rest = of_share() - u;
+    if (u * row_tiles >= n)
+      enter(n);
+    else if (rest <= 0)
+      b = p.c.B;
   }
-  __device__ __forceinline__ void skip(long long n) {  // n: the cost of sequence b
-    while (u * row_tiles >= n) {
+  __device__ __forceinline__ long long of_share() const {  // units that begin before its end
+    return min((long long)tiles * p.c.H, (hi - before + row_tiles - 1) / row_tiles);
+  }
+  __device__ __forceinline__ void enter(long long n) {  // the sequence after b, whose cost is n
+    h = tile = 0;
+    do {
       before += n;
-      u = 0, h = tile = 0;
-      if (++b >= p.c.B) return;
+      if (before >= hi || ++b >= p.c.B) {
+        b = p.c.B;
+        return;
+      }
       n = cost_of(b);
-    }
+    } while (n == 0);
+    rest = of_share();
   }
-  __device__ __forceinline__ bool valid() const {
-    return b < p.c.B && before + u * row_tiles < hi;
-  }
+  __device__ __forceinline__ bool valid() const { return b < p.c.B; }
   __device__ __forceinline__ void next() {
-    ++u;
+    if (--rest <= 0) return enter((long long)tiles * p.c.H * row_tiles);
     if (++tile == tiles) tile = 0, ++h;
-    skip((long long)tiles * p.c.H * row_tiles);
   }
   __device__ __forceinline__ int key0() const { return tile * KEYS; }
   // the first tile of rows that see some of the unit's keys
   __device__ __forceinline__ int first_rows() const {
-    return p.causal ? max(0, key0() - (seq.len - seq.n)) / p.tile_tokens : 0;
+    return p.causal ? p.by_tile.div(max(0, key0() - (seq.len - seq.n))) : 0;
   }
 };
 

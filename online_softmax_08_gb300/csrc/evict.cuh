@@ -27,6 +27,7 @@ struct WeightParams {
   float scale_log2;
   int narrow_rows;   // sequences with more query rows per key/value head go to the tcgen05 kernel
   int tile_tokens;   // of its tiles of rows: 256 / G
+  FastDiv by_tile;
 };
 cudaError_t launch_cache_weights(const WeightParams& p, int n_sm, cudaStream_t stream);
 // tq: map of q, {d, Hq, total}, boxes {64, G, tile_tokens}
