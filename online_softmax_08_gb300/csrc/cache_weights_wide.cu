@@ -24,9 +24,14 @@
 // exponentials.  (Built and measured before this, 512 queries behind 16384 tokens, 32 query and
 // 8 key heads, d = 128: mma.sync 457 us; 256 keys a unit, 8 warps, tiles of 128 rows 127 us, 16
 // warps 94 us; tiles of 256 rows, S in one buffer for each 128 keys, 88 us; S in two, 32
-// columns loaded at a time, 76 us: a tile took 2200 clocks, of which a warp's 64 columns took 1650,
-// its waits and what it does between tiles the rest, and a change of unit 4500.)  Now, the next 16
-// columns on their way while 16 are worked on, 75 us, 931 TFLOP/s.
+// columns loaded at a time, 76 us; the next 16 on their way while 16 are worked on 74; one
+// barrier for S and the log-sum-exp instead of two 70; whole tiles without the mask's arithmetic
+// and units found by counting 68.5.)  Now 68.5 us, 1018 TFLOP/s.  The warps of exponentials are the
+// bound: a warp's 64 columns take 1500 clocks, the four warps of a scheduler at once, its arrival
+// and the next wait 300, a change of unit 2000.  (Work for the next unit moved into a tile, another
+// for every quarter of the columns: 73.  With half of Q loaded, to see what its way from L2
+// costs, 73 where the whole took 74; without the loads of the log-sum-exp 70; without the
+// exponentials 64.)
 #define FATTN_INLINE_WAIT_SLOW_PATH
 #include <math.h>
 
