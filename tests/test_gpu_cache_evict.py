@@ -282,6 +282,34 @@ def test_evict_of_a_long_sequence():
         assert torch.equal(dst, src.gather(1, at))
 
 
+@pytest.mark.parametrize("B,L,keep,recent", [(80, 40000, 999, 10), (40, 70001, 40000, 1),
+                                             (1, 300001, 150000, 0), (200, 33333, 5, 5)])
+def test_evict_of_rows_read_in_parts(B, L, keep, recent):
+    """More weights than the CTAs of a row hold, many of them equal, in one to eight CTAs a row."""
+    d, bs = 64, 128
+    g = torch.Generator(device=DEV).manual_seed(B)
+    w = torch.floor(torch.rand((B, 1, L), generator=g, device=DEV) * 500) / 256
+    w[:, :, ::7] = 0.0
+    nb, nk = -(-L // bs), -(-keep // bs)
+    cache = fattn.new_cache(nb + B * nk, 1, bs, d, dtype=torch.uint8, device=DEV)
+    cache.k.copy_(torch.randint(0, 256, cache.k.shape, generator=g, device=DEV))
+    i32 = dict(dtype=torch.int32, device=DEV)
+    table = torch.arange(nb, **i32).expand(B, nb).contiguous()  # all of them share their blocks
+    out_table = torch.arange(nb, nb + B * nk, **i32).reshape(B, nk)
+    lens = torch.full((B,), L, **i32)
+    lens[0] = L - 3
+    new, kept, moved = fattn.cache_evict(cache, w, table, lens, out_table, keep, recent)
+    assert new.tolist() == [keep] * B
+    for b in (0, B // 2, B - 1):
+        n = int(lens[b]) - recent
+        order = torch.sort(w[b, 0, :n].double(), descending=True, stable=True).indices
+        want = torch.cat((order[:keep - recent].sort().values, torch.arange(n, n + recent, device=DEV)))
+        assert torch.equal(kept[b, 0].long(), want)
+        assert torch.equal(moved[b, 0], w[b, 0][want])
+        src = cache.k[:nb, 0].reshape(-1, d // 2)
+        assert torch.equal(cache.k[out_table[b].long(), 0].reshape(-1, d // 2)[:keep], src[want])
+
+
 def test_evict_to_its_own_blocks():
     """A sequence that is short enough may be given its own blocks: it stays as it is."""
     c = _case([(0, 30), (0, 100)], 2, 64, 16, "e4m3").fill()
@@ -425,6 +453,31 @@ def test_weights_and_eviction_past_32_bits():
                            getattr(small, name).view(torch.uint8))
     del cache
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("fmt,n", [("int4", 1), ("e4m3", 1), ("int4", 70), ("e5m2", 70)])
+def test_missing_large_block(fmt, n):
+    """A bad number of a block that holds several warps' keys: they get 0, the others what they
+    get without it, whatever lies in the pool's first block."""
+    H, G, d, bs = 2, 2, 128, 64
+    c = _case([(n, 300), (1, 90)], H, d, bs, fmt, seed=3, spare=40).fill()
+    assert 0 not in c.table
+    for name in ("k", "k_scale"):
+        a = c.cache[name]
+        a[0] = np.nan if a.dtype.kind == "f" else 0xff if name == "k" else 0x7f
+    q = _bf16(c.rng, (c.T, H * G, d)).to(DEV)
+    cache, batch = c.on_device()
+    _, lse = fattn.cache_forward(q, cache, batch, 0.1, True)
+    ref = fattn.cache_weights(q, lse, cache, batch, 0.1, True)
+    for bad in (-1, 10 ** 6):
+        table = batch.block_table.clone()
+        table[0, 2] = bad
+        got = fattn.cache_weights(q, lse, cache, batch._replace(block_table=table), 0.1, True)
+        assert fattn.fattn_device_error() == 0x471
+        assert bool((got[0, :, 128:192] == 0).all())
+        for part in (slice(0, 128), slice(192, None)):
+            assert torch.equal(got[0, :, part], ref[0, :, part])
+        assert torch.equal(got[1], ref[1])
 
 
 def test_serving_run():
