@@ -232,7 +232,7 @@ __device__ __forceinline__ void int4_values(uint32_t w, const Int4Scale& s, cons
   o[3] = fma_f16x2(nibbles<1>(u, m.m64), s.s, s.hi);
 }
 // The same in bf16, eight codes of one scale in their order: a code in the mantissa of 128
-// (0x4300) is 128 + c, and (128 + c) s - 136 s = (c - 8) s, every term exact for any scale.
+// (0x4300) is 128 + c, and (128 + c) s - 136 s = (c - 8) s, every term exact for any finite scale.
 struct Bf16Scale {
   uint32_t s, off;  // pairs: s, -136 s
 };

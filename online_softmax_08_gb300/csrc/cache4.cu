@@ -16,8 +16,8 @@
 // even, and leaves the code in the low four bits.
 //
 // The bound is memory, and next to it the logic pipe, which the quantising of a group takes
-// 68 % of while it is written (measured: 32768 tokens of 16 heads, d = 128, 58.5 us written, 54.5
-// read back, 87 and 93 % of the measured copy bandwidth).
+// 68 % of while it is written (measured: 32768 tokens of 16 heads, d = 128, 58.3 us written, 55.1
+// read back, 87 and 92 % of the measured copy bandwidth).
 // A thread holds one group: 32 bytes of bf16 and 8 + 1 of the cache.
 // A warp takes kIter x 32 groups of one head: the rows of 16 (d = 64: 32) packed tokens one
 // behind another, so a prompt's codes and scales are written as whole lines, then the same of
@@ -263,9 +263,15 @@ __global__ void __launch_bounds__(32 * kWarps4)
       if (at[j] == -1) continue;
       if (at[j] >= 0) at[j] += c.block_size;  // the next head's
       uint32_t o[8];
-      const Bf16Scale s = bf16_scale(s8[j]);
+      const bool infinite = (s8[j] & 0x7fu) == 0x7cu;  // (which the multiply-add makes NaN of)
+      const Bf16Scale s = bf16_scale(infinite ? 0x3cu : s8[j]);  // 1
       bf16_values(x[j].x, s, o);
       bf16_values(x[j].y, s, o + 4);
+      if (__builtin_expect(infinite, 0)) {
+        const uint32_t inf = (s8[j] & 0x80u) ? 0xff80ff80u : 0x7f807f80u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(o[i]) : "r"(inf));
+      }
       store32<V8>(dst + j * step, o);
     }
   }

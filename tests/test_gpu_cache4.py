@@ -393,3 +393,22 @@ def test_append_of_many_heads_and_tokens():
                            fattn.CacheBatch(table, i32(a + n), i32(0, n), n, n))
     for x, y in zip(one, many):
         assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("layout", ["own", "slice"])
+def test_read_of_any_scale(d, layout):
+    """Every scale there is, infinities and NaN among them: (c - 8) inf is an infinity, 0 inf NaN."""
+    H, bs = 3, 32
+    c = Case([(70, 0), (200, 30)], H, d, bs, seed=d)
+    assert len(np.unique(c.cache["k_scale"])) == 256
+    cache, batch = c.on_device()
+    whole = torch.full((2, c.T, H + 1, d + 8), 7.0, dtype=torch.bfloat16, device=DEV)
+    out = whole[:, :, :H, 8:] if layout == "slice" else torch.empty((2, c.T, H, d), dtype=torch.bfloat16,
+                                                                    device=DEV)
+    got = fattn.cache_read(cache, batch, out=(out[0], out[1]))
+    with np.errstate(invalid="ignore"):
+        want = oc4.read(c.cache, c.batch)
+    for g, ref in zip(got, want):
+        assert np.isinf(ref).any() and np.isnan(ref).any()
+        np.testing.assert_array_equal(g.cpu().double().numpy(), ref)
