@@ -368,8 +368,11 @@ __global__ void __launch_bounds__(kCopy) cache_copy_kernel(const EvictParams p, 
           for (int k = 0; k < 4; ++k) {
             const float2 lo = f16x2_to_f32(codes_to_f16x2<E5M2>((uint16_t)(w[k] & 0xffffu)));
             const float2 hi = f16x2_to_f32(codes_to_f16x2<E5M2>((uint16_t)(w[k] >> 16)));
-            w[k] = (uint32_t)f32_to_codes<E5M2>(lo.x * f, lo.y * f) |
-                   (uint32_t)f32_to_codes<E5M2>(hi.x * f, hi.y * f) << 16;
+            // (infinities, which the conversion would bring to the largest value, stay)
+            const uint32_t inf = E5M2 ? __vcmpeq4(w[k] & 0x7f7f7f7fu, 0x7c7c7c7cu) : 0u;
+            const uint32_t r = (uint32_t)f32_to_codes<E5M2>(lo.x * f, lo.y * f) |
+                               (uint32_t)f32_to_codes<E5M2>(hi.x * f, hi.y * f) << 16;
+            w[k] = (w[k] & inf) | (r & ~inf);
           }
         }
       }

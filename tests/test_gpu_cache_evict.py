@@ -552,3 +552,30 @@ def test_serving_run():
             want += p.sum(dim=1)
             assert float((w2[s, :, :L].double() - want).abs().max()) <= 1e-4
             assert torch.equal(w2[s, :, L:], old[s, :, L:])
+
+
+def test_evict_keeps_infinities():
+    """e5m2: an infinite code stays one, whatever scale its block gets; NaN stays NaN."""
+    d, bs, keep = 64, 16, 16
+    cache = fattn.new_cache(4, 1, bs, d, dtype=torch.float8_e5m2, device=DEV)
+    for side, scale in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)):
+        side.view(torch.uint8)[:2] = 0x3c  # 1.0
+        side.view(torch.uint8)[0, 0, :, 5] = 0x7c
+        side.view(torch.uint8)[0, 0, :, 6] = 0xfc
+        side.view(torch.uint8)[0, 0, :, 7] = 0x7e
+        side.view(torch.uint8)[0, 0, :, 8] = 0x7b  # the largest finite one
+        scale[0], scale[1] = 2.0, 8.0
+    i32 = dict(dtype=torch.int32, device=DEV)
+    w = torch.ones((1, 1, 32), device=DEV)
+    w[..., 8:24] = 2.0  # half of either block
+    table, table_out = torch.tensor([[0, 1]], **i32), torch.tensor([[3]], **i32)
+    _, kept, _ = fattn.cache_evict(cache, w, table, torch.tensor([32], **i32), table_out, keep)
+    assert kept[0, 0].tolist() == list(range(8, 24))
+    for side, scale in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)):
+        assert float(scale[3]) == 8.0
+        got = side.view(torch.uint8)[3, 0]
+        assert bool((got[:8, 5] == 0x7c).all()) and bool((got[:8, 6] == 0xfc).all())
+        assert bool(torch.isnan(side[3, 0, :8, 7].float()).all())
+        assert bool((got[:8, 8] == 0x73).all())  # a quarter of 57344
+        assert bool((got[:8, 9:] == 0x34).all()) and bool((got[:8, :5] == 0x34).all())
+        assert bool((got[8:] == 0x3c).all())
