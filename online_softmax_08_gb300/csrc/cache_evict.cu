@@ -121,16 +121,19 @@ __global__ void __launch_bounds__(kSelect) cache_select_kernel(const EvictParams
   const int steps = min(kRun, (old + T - 1) / T), segment = steps * T;
   extern __shared__ uint32_t held[];  // [kRun * kSelect], every thread its own
   uint32_t* const own = held + cta_warp * steps * 32 + lane;
-  auto index = [&](int seg, int i) { return seg + (warp * steps + i) * 32 + lane; };
+  // (a place in a segment is compared with what is left from its start on: the number of the
+  // weight behind a segment may pass 32 bits)
+  auto index = [&](int i) { return (warp * steps + i) * 32 + lane; };
   auto load = [&](int seg) {
+    const int left = old - seg;
     constexpr int N = 16;  // on their way at a time
 #pragma unroll 1
     for (int i0 = 0; i0 < steps; i0 += N) {
       float x[N];
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const int j = index(seg, i0 + i);
-        x[i] = i0 + i < steps && j < old ? w[j] : 0.f;
+        const int j = index(i0 + i);
+        x[i] = i0 + i < steps && j < left ? w[seg + j] : 0.f;
       }
 #pragma unroll
       for (int i = 0; i < N; ++i)
@@ -156,15 +159,17 @@ __global__ void __launch_bounds__(kSelect) cache_select_kernel(const EvictParams
     __syncthreads();
     int zeros = 0;  // many weights are zero, and would all add to one bin: counted apart
 #pragma unroll 1
-    for (int seg = 0; seg < old; seg += segment) {
+    for (int seg = 0;; seg += segment) {
+      const int left = old - seg;
       if (old > segment) load(seg);
 #pragma unroll 4
       for (int i = 0; i < steps; ++i) {
         const uint32_t u = own[i * 32];
-        const bool on = index(seg, i) < old && (u & mask) == prefix, zero = u == kZero;
+        const bool on = index(i) < left && (u & mask) == prefix, zero = u == kZero;
         zeros += on && zero;
         if (on && !zero) atomicAdd(&bins[u >> shift & low], 1);
       }
+      if (left <= segment) break;
     }
     zeros = __reduce_add_sync(0xffffffffu, zeros);
     if (lane == 0 && zeros > 0) atomicAdd(&bins[kZero >> shift & low], zeros);
@@ -205,13 +210,14 @@ __global__ void __launch_bounds__(kSelect) cache_select_kernel(const EvictParams
   // ---------------------------------------------------------------- the kept ones, in order
   int more0 = 0, ties0 = 0;  // in the segments before: larger than the smallest kept, equal to it
 #pragma unroll 1
-  for (int seg = 0, turn = 0; seg < old; seg += segment, turn ^= 1) {
+  for (int seg = 0, turn = 0;; seg += segment, turn ^= 1) {
+    const int left = old - seg;
     if (old > segment) load(seg);
     int more = 0, ties = 0;  // of the lane, then of the warp
 #pragma unroll 4
     for (int i = 0; i < steps; ++i) {
       const uint32_t u = own[i * 32];
-      const bool in = index(seg, i) < old;
+      const bool in = index(i) < left;
       more += in && u > prefix;
       ties += in && u == prefix;
     }
@@ -244,11 +250,11 @@ __global__ void __launch_bounds__(kSelect) cache_select_kernel(const EvictParams
 #pragma unroll 4
       for (int i = 0; i < steps; ++i) {
         const uint32_t u = own[i * 32];
-        const bool mine = index(seg, i) < old && u > prefix;
+        const bool mine = index(i) < left && u > prefix;
         const unsigned m = __ballot_sync(0xffffffffu, mine);
         const int place = at + __popc(m & before);
         if (mine && (unsigned)place < (unsigned)top) {
-          kept[place] = index(seg, i);
+          kept[place] = seg + index(i);
           w_out[place] = weight_of(u);
         }
         at += __popc(m);
@@ -257,20 +263,21 @@ __global__ void __launch_bounds__(kSelect) cache_select_kernel(const EvictParams
 #pragma unroll 1
       for (int i = 0; i < steps; ++i) {
         const uint32_t u = own[i * 32];
-        const bool in = index(seg, i) < old;
+        const bool in = index(i) < left;
         const unsigned m = __ballot_sync(0xffffffffu, in && u > prefix);
         const unsigned e = __ballot_sync(0xffffffffu, in && u == prefix);
         const int ties_here = ties + __popc(e & before);
         const int place = more + __popc(m & before) + min(ties_here, need);
         if (((m >> lane & 1u) || ((e >> lane & 1u) && ties_here < need)) &&
             (unsigned)place < (unsigned)top) {
-          kept[place] = index(seg, i);
+          kept[place] = seg + index(i);
           w_out[place] = weight_of(u);
         }
         more += __popc(m), ties += __popc(e);
       }
     }
     more0 += all_more, ties0 += all_ties;
+    if (left <= segment) break;
   }
   if constexpr (CS > 1) cluster_sync();  // nobody's shared memory goes while it is read
 }

@@ -579,3 +579,34 @@ def test_evict_keeps_infinities():
         assert bool((got[:8, 8] == 0x73).all())  # a quarter of 57344
         assert bool((got[:8, 9:] == 0x34).all()) and bool((got[:8, :5] == 0x34).all())
         assert bool((got[8:] == 0x3c).all())
+
+
+@pytest.mark.parametrize("B", [1, 20])
+def test_evict_of_the_longest_rows(B):
+    """As many tokens as a table row may name, in eight and in four CTAs a row: the number of the
+    weight behind the last segment does not fit 32 bits."""
+    d, bs, keep, recent = 64, 128, 1000, 9
+    L = (1 << 31) - 65536
+    i32 = dict(dtype=torch.int32, device=DEV)
+    nb, nk = 50, -(-keep // bs)
+    cache = fattn.new_cache(nb + B * nk, 1, bs, d, dtype=torch.uint8, device=DEV)
+    g = torch.Generator(device=DEV).manual_seed(3)
+    cache.k.copy_(torch.randint(0, 256, cache.k.shape, generator=g, device=DEV))
+    # weights of zero but for some, the last ones among them; zeros fill up from the front
+    some = torch.cat((torch.arange(300, device=DEV) * 7000001 + 5,
+                      L - recent - 1 - torch.arange(200, device=DEV)))
+    w = torch.zeros((1, 1, L), device=DEV)
+    w[0, 0, some] = 1.0 + torch.rand((500,), generator=g, device=DEV)
+    table = (torch.arange(L // bs, **i32) % nb).expand(B, -1).contiguous()
+    table_out = torch.arange(nb, nb + B * nk, **i32).reshape(B, nk)
+    lens = torch.full((B,), L, **i32)
+    new, kept, moved = fattn.cache_evict(cache, w.expand(B, 1, L), table, lens, table_out, keep, recent)
+    assert new.tolist() == [keep] * B
+    chosen = some.tolist()
+    first = [j for j in range(keep) if j not in chosen][:keep - recent - 500]
+    want = torch.tensor(sorted(chosen + first) + list(range(L - recent, L)), device=DEV)
+    src = cache.k[:nb, 0].reshape(-1, d // 2)
+    for b in range(B):
+        assert torch.equal(kept[b, 0].long(), want) and torch.equal(moved[b, 0], w[0, 0, want])
+        assert torch.equal(cache.k[table_out[b].long(), 0].reshape(-1, d // 2)[:keep],
+                           src[want % (nb * bs)])
