@@ -104,7 +104,8 @@ __global__ void __launch_bounds__(kSelect) cache_select_kernel(const EvictParams
   if (h == 0 && t == 0) p.lens_out[b] = n;
   const float* w = p.in.p + b * p.in.sb + h * p.in.sh;
   float* w_out = p.out.p + b * p.out.sb + h * p.out.sh;
-  for (int j = n + t; j < p.keep; j += T) kept[j] = -1;
+  // (unsigned: keep may be 2^31 - 1, and the last step goes past it)
+  for (unsigned j = (unsigned)(n + t); j < (unsigned)p.keep; j += T) kept[j] = -1;
   if (len <= p.keep) {
     for (int j = t; j < n; j += T) {
       kept[j] = j;

@@ -610,3 +610,28 @@ def test_evict_of_the_longest_rows(B):
         assert torch.equal(kept[b, 0].long(), want) and torch.equal(moved[b, 0], w[0, 0, want])
         assert torch.equal(cache.k[table_out[b].long(), 0].reshape(-1, d // 2)[:keep],
                            src[want % (nb * bs)])
+
+
+@pytest.mark.parametrize("keep", [(1 << 31) - 1, (1 << 31) - 1024])
+def test_evict_that_keeps_all(keep):
+    """The largest `keep`, whose places behind the last token are filled, and nothing behind them."""
+    c = _case([(0, 21)], 1, 64, 16, "int4").fill()
+    table_out = torch.tensor(_scatter(c, [21], 16), device=DEV)
+    cache, batch = c.on_device()
+    w = torch.rand((1, 1, 21), device=DEV)
+    out = torch.full((1, 1, 25), 7.0, device=DEV)
+    lens_out = torch.empty((1,), dtype=torch.int32, device=DEV)
+    whole = torch.full((keep + 4096,), 7, dtype=torch.int32, device=DEV)
+    pool, dev, _, _ = fattn._pool_args(cache)
+    b = fattn._pack_batch(batch.block_table.data_ptr(), batch.lens.data_ptr(), batch.lens.data_ptr(), 1,
+                          batch.block_table.shape[1], 0, 0)
+    st = fattn.load().fattn_cache_evict(pool, b, w.data_ptr(), 0, 0, 21, table_out.data_ptr(),
+                                        table_out.shape[1], keep, 3, lens_out.data_ptr(),
+                                        whole[1024:].data_ptr(), out.data_ptr(), 0, 0, 25,
+                                        torch.cuda.current_stream().cuda_stream)
+    assert st == 0 and lens_out.tolist() == [21]
+    assert whole[1024:1045].tolist() == list(range(21)) and torch.equal(out[..., :21], w)
+    assert bool((out[..., 21:] == 7.0).all())
+    low, high = torch.aminmax(whole[1045:1024 + keep])
+    assert int(low) == -1 and int(high) == -1
+    assert bool((whole[:1024] == 7).all()) and bool((whole[1024 + keep:] == 7).all())
