@@ -311,7 +311,10 @@ __global__ void __launch_bounds__(kCopy) cache_copy_kernel(const EvictParams p, 
   float ks_max = 0.f, vs_max = 0.f;
   if (t < count) {  // (a block has at most 128 tokens)
     const int pos = p.kept[(long long)bh * p.keep + blk * bs + t];
-    const int page = c.block_table[(long long)b * c.table_width + (pos >> c.block_log2)];
+    // (no such token: its place was not written, as the weights changed under the selection)
+    const bool there = (unsigned)pos < (unsigned)(c.table_width * bs);
+    const int page =
+        there ? c.block_table[(long long)b * c.table_width + (pos >> c.block_log2)] : -1;
     Source s{-1, 0.f, 0.f};
     if (page < 0 || page >= c.num_blocks) {
       if (c.err) atomicCAS(c.err, 0u, (unsigned)ERR_SITE_CACHE_EVICT + 1);

@@ -635,3 +635,46 @@ def test_evict_that_keeps_all(keep):
     low, high = torch.aminmax(whole[1045:1024 + keep])
     assert int(low) == -1 and int(high) == -1
     assert bool((whole[:1024] == 7).all()) and bool((whole[1024 + keep:] == 7).all())
+
+
+def test_evict_of_weights_that_change():
+    """Weights that change while a row is read (here: its own results, written over weights that are
+    still to be read, which the call does not allow) may leave places without a token.  What lies
+    there is no block's number: such a token becomes zeros and is reported, nothing else changes."""
+    L, keep, many, d, bs, nb = 600000, 76712, 75712, 64, 128, 50
+    i32 = dict(dtype=torch.int32, device=DEV)
+    g = torch.Generator(device=DEV).manual_seed(5)
+    nk = -(-keep // bs)
+    cache = fattn.new_cache(nb + nk + 7, 1, bs, d, dtype=torch.uint8, device=DEV)
+    for x in (cache.k, cache.v, cache.k_scale.view(torch.uint8), cache.v_scale.view(torch.uint8)):
+        x.copy_(torch.randint(0, 112, x.shape, generator=g, device=DEV))
+    old = [x.view(torch.uint8).clone() for x in cache]
+    # the first 1000 tokens are kept, of many that are equal, and the last 75712; the first ones'
+    # weights then take the places of some of the last ones'
+    buf = torch.zeros((1, 1, 700000), device=DEV)
+    buf[..., :262144] = 1.0
+    buf[..., L - many:L] = 2.0
+    table = (torch.arange(-(-L // bs), **i32) % nb)[None].contiguous()
+    table_out = torch.arange(nb, nb + nk, **i32)[None].contiguous()
+    lens, lens_out = torch.tensor([L], **i32), torch.empty((1,), **i32)
+    kept = torch.full((keep,), 1 << 30, **i32)
+    kept[1::2] = -5
+    blank = kept.clone()
+    pool = fattn._pool_args(cache)[0]
+    b = fattn._pack_batch(table.data_ptr(), lens.data_ptr(), lens.data_ptr(), 1, table.shape[1], 0, 0)
+    st = fattn.load().fattn_cache_evict(pool, b, buf.data_ptr(), 0, 0, L, table_out.data_ptr(), nk, keep,
+                                        0, lens_out.data_ptr(), kept.data_ptr(),
+                                        buf[..., 550000:].data_ptr(), 0, 0, keep,
+                                        torch.cuda.current_stream().cuda_stream)
+    assert st == 0
+    torch.cuda.synchronize()
+    none = kept == blank
+    assert bool(none.any()) and not bool(none[:1000].any())
+    assert fattn.fattn_device_error() == 0x481
+    at = torch.where(none, 0, kept).long()
+    for x, was, empty in zip(cache, old, (0x88, 0x88, 0, 0)):
+        x = x.view(torch.uint8)
+        assert torch.equal(x[:nb], was[:nb]) and torch.equal(x[nb + nk:], was[nb + nk:])
+        src = was[:nb].reshape(nb * bs, -1)
+        want = torch.where(none[:, None], torch.full_like(src[:1], empty), src[at % (nb * bs)])
+        assert torch.equal(x[nb:nb + nk].reshape(nk * bs, -1)[:keep], want)
