@@ -412,10 +412,11 @@ size_t fattn_cache_fwd_workspace_bytes(const fattn_cache* cache, const fattn_cac
  * of group h; the batch's own tokens (positions from lens[b] - n_b on) start at 0.  Weights are
  * kept by sequence, not by block, as a shared block's keys have others in every sequence.
  * q as for fattn_cache_fwd, lse DEVICE fp32 [Hq, total] as it wrote it (a row with -inf adds
- * nothing).  weights (NULL: zeros) and weights_out: DEVICE fp32, 4-byte aligned, element
- * (b, h, j) at b * sequence stride + h * head stride + j, strides in elements and not negative,
- * rows of `width` elements, those of weights_out not overlapping; they may be the same, with the
- * same strides, and must not overlap otherwise.  Elements at and behind lens[b], and sequences with n_b = 0, are not touched.
+ * nothing), Hq / H x max_seqlen at most 2^31 - 65536.  weights (NULL: zeros) and weights_out: DEVICE
+ * fp32, 4-byte aligned, element (b, h, j) at b * sequence stride + h * head stride + j, strides in
+ * elements and not negative, rows of `width` elements, those of weights_out not overlapping; they
+ * may be the same, with the same strides, and must not overlap otherwise.  Elements at and behind
+ * lens[b], and sequences with n_b = 0, are not touched.
  * A sequence whose entries are bad (as above) or whose length exceeds width is skipped (code
  * 0x470), keys of a bad block number get 0 from the queries (0x471).  Every sum is formed in
  * one order: repeated calls agree bit for bit.  Scores, exponentials and sums are fp32.

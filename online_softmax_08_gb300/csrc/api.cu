@@ -712,6 +712,9 @@ extern "C" int fattn_cache_weights(const fattn_cache* cache, const fattn_cache_b
   if (st != FATTN_OK) return st;
   st = check_cache_heads(cache, batch, Hq);
   if (st != FATTN_OK) return st;
+  // (65536: the kernels count rows some tiles ahead, in 32 bits)
+  if ((long long)(Hq / cache->H) * batch->max_seqlen > (1LL << 31) - 65536)
+    return FATTN_ERR_INVALID_ARG;
   if (!(scale > 0.f) || !isfinite(scale) || width < 0) return FATTN_ERR_INVALID_ARG;
   st = check_cache_pointers(cache, batch);
   if (st != FATTN_OK) return st;

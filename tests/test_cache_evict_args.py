@@ -98,3 +98,16 @@ def test_oracle_weights_sum_to_the_queries():
     w, _ = oe.weights(cache, "e4m3", batch, q, lse, 0.1, True, before, np.full((1, 1, 44), 7.0))
     np.testing.assert_allclose(w[0, 0, :40].sum() - before[0, 0, :33].sum(), 14.0, rtol=1e-12)
     assert np.all(w[0, 0, 40:] == 7.0)
+
+
+def test_weights_refuse_more_rows_than_are_counted(lib):
+    """The kernels step through a sequence's query rows 32 or 256 at a time, in 32 bits."""
+    c = _cache(H=1)
+    call = lambda n, total=(1 << 31) - 1: _weights(lib, c, _batch(total=total, max_seqlen=n), qst=0,
+                                                   qsh=0, Hq=1)
+    for n in ((1 << 31) - 1, (1 << 31) - 65535):
+        assert call(n) == INVALID, n
+    assert _weights(lib, c, _batch(total=(1 << 28) - 1, max_seqlen=(1 << 28) - 1), qst=0,
+                    qsh=0, Hq=8) == INVALID
+    if not torch.cuda.is_available():
+        assert call((1 << 31) - 65536) == CUDA
