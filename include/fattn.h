@@ -491,10 +491,10 @@ int fattn_rope_turns(unsigned long long* turns, float* magnitude, int rot, doubl
  * DEVICE, 16-byte aligned, strides in elements as for fattn_cache_append, those of the outputs
  * as for fattn_cache_read) and writes rows of d channels to q_out and k_out; the channels from
  * rot on are copied.  An output may be its input, with the same strides; otherwise they must not
- * overlap.  Hq and Hk are at most 65535; one may be 0 (its pointers are not looked at).  positions: DEVICE int32
- * [total], of either sign; turns: DEVICE [rot / 2] of 64 bits, 8-byte aligned, as
- * fattn_rope_turns gives them; magnitude m finite and > 0.  d is 64 or 128, rot a multiple of
- * 16 up to d.  The angle is exact in turns (64-bit arithmetic modulo one turn) up to the
+ * overlap.  Hq and Hk are at most 65535; one may be 0 (its pointers are not looked at).  total x
+ * (Hq + Hk) is at most 2^31 - 4.  positions: DEVICE int32 [total], of either sign; turns: DEVICE
+ * [rot / 2] of 64 bits, 8-byte aligned, as fattn_rope_turns gives them; magnitude m finite and
+ * > 0.  d is 64 or 128, rot a multiple of 16 up to d.  The angle is exact in turns (64-bit arithmetic modulo one turn) up to the
  * fractions given; sines, products and sums are fp32, rounded once to bf16.
  * backward != 0: the gradient, i.e. the transposed map (q and k are dL/dq_out and dL/dk_out).
  * Returns FATTN_OK, FATTN_ERR_INVALID_ARG, FATTN_ERR_UNSUPPORTED or FATTN_ERR_CUDA; launches

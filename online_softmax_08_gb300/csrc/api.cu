@@ -869,7 +869,7 @@ extern "C" int fattn_rope(const void* q, long long q_token_stride, long long q_h
                           float magnitude, int total, int d, int rot, int layout, int backward,
                           void* stream) {
   if (total < 0 || Hq < 0 || Hk < 0 || Hq > 65535 || Hk > 65535 || Hq + Hk < 1 ||
-      (long long)(Hq + Hk) * total >= (1LL << 31))
+      (long long)(Hq + Hk) * total > (1LL << 31) - 4)  // (four tokens a CTA, counted in 32 bits)
     return FATTN_ERR_INVALID_ARG;
   if (d != 64 && d != 128) return FATTN_ERR_UNSUPPORTED;
   if (layout != FATTN_ROPE_HALF && layout != FATTN_ROPE_INTERLEAVED) return FATTN_ERR_UNSUPPORTED;

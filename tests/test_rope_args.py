@@ -103,3 +103,11 @@ def test_bad_tables(lib):
         fattn.rope(x, x, torch.zeros(3, dtype=torch.int32), table)  # (on no CUDA device)
     with pytest.raises(ValueError):
         fattn.rope(x, x, torch.zeros(3, dtype=torch.int32), table, layout="quarter")
+
+
+def test_most_rows(lib):
+    one = dict(k=None, ko=None, Hk=0, Hq=1, qst=0, qsh=0, d=64)
+    for T in ((1 << 31) - 1, (1 << 31) - 3):
+        assert _rope(lib, T=T, **one) == INVALID, T
+    if not torch.cuda.is_available():  # accepted
+        assert _rope(lib, T=(1 << 31) - 4, **one) == CUDA
