@@ -475,15 +475,17 @@ typedef enum {
                             factor and the fastest is kept */
   FATTN_ROPE_YARN = 3,   /* w_i where the pair makes more than about `fast` turns over `length`,
                             w_i / factor where fewer than `slow`, a ramp over the pairs between
-                            (floor and ceiling of the two pairs); m = 0.1 ln(factor) + 1 */
+                            (floor and ceiling of the two pairs; pair 0 always has w_0);
+                            m = 0.1 ln(factor) + 1 */
   FATTN_ROPE_BANDS = 4   /* the same by turns n_i = length w_i / 2 pi: the share of w_i is
                             (n_i - slow) / (fast - slow), cut to [0, 1]; m = 1 */
 } fattn_rope_scaling;
 
 /* The frequencies as fractions of a turn, on the HOST (no device is touched): turns[i] =
- * 2^64 frac(w_i / 2 pi) for i < rot / 2, and *magnitude = m.  rot even, base > 1; factor is
- * read unless kind is NONE, length, fast and slow (fast > slow > 0) by YARN and BANDS.
- * Formed in double precision: an angle at position p is off by about 2^-52 p turns at most. */
+ * 2^64 frac(w_i / 2 pi) for i < rot / 2, and *magnitude = m.  rot even, base > 1; factor
+ * (finite, > 0, as its inverse) is read unless kind is NONE, length, fast and slow (fast > slow >
+ * 0) by YARN and BANDS.  Formed in double precision: an angle at position p is off by about
+ * 2^-52 p turns at most (2^-52 p w_i where a factor below 1 makes w_i larger than 1). */
 int fattn_rope_turns(unsigned long long* turns, float* magnitude, int rot, double base, int kind,
                      double factor, int length, double fast, double slow);
 

@@ -829,7 +829,8 @@ extern "C" int fattn_rope_turns(unsigned long long* turns, float* magnitude, int
   if (!turns || !magnitude || rot < 2 || (rot & 1) || rot > 65536) return FATTN_ERR_INVALID_ARG;
   if (!(base > 1.0) || !isfinite(base)) return FATTN_ERR_INVALID_ARG;
   if (kind < FATTN_ROPE_NONE || kind > FATTN_ROPE_BANDS) return FATTN_ERR_UNSUPPORTED;
-  if (kind != FATTN_ROPE_NONE && (!(factor > 0.0) || !isfinite(factor))) return FATTN_ERR_INVALID_ARG;
+  if (kind != FATTN_ROPE_NONE && (!(factor > 0.0) || !isfinite(factor) || !isfinite(1.0 / factor)))
+    return FATTN_ERR_INVALID_ARG;  // (w_0 / factor is 1 / factor)
   const bool by_length = kind == FATTN_ROPE_YARN || kind == FATTN_ROPE_BANDS;
   if (by_length && (length < 1 || !(slow > 0.0) || !(fast > slow) || !isfinite(fast)))
     return FATTN_ERR_INVALID_ARG;

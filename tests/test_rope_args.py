@@ -111,3 +111,12 @@ def test_most_rows(lib):
         assert _rope(lib, T=T, **one) == INVALID, T
     if not torch.cuda.is_available():  # accepted
         assert _rope(lib, T=(1 << 31) - 4, **one) == CUDA
+
+
+def test_frequencies_that_overflow(lib):
+    """A factor whose inverse is no finite number: the first pair's frequency would be none."""
+    buf, m = (ctypes.c_uint64 * 32)(*([7] * 32)), ctypes.c_float(-1.0)
+    for kind in (1, 4):
+        assert lib.fattn_rope_turns(buf, ctypes.byref(m), 64, 1e4, kind, 1e-310, 64, 4.0, 1.0) == INVALID
+        assert list(buf) == [7] * 32 and m.value == -1.0
+    assert lib.fattn_rope_turns(buf, ctypes.byref(m), 64, 1e4, 1, 1e-300, 64, 4.0, 1.0) == 0
