@@ -627,7 +627,10 @@ def cache_weights(q, lse, cache, batch, scale, causal, weights=None, out=None, s
     [B, H, width], summed over the queries and the heads of a group.  weights: what the keys
     had before, which is added to (None: nothing); the batch's own tokens start anew.  out: a
     tensor to write to (None: `weights`, in place, or a new one with room for the table).
-    Entries behind a sequence's length stay as they are (new: zero)."""
+    Entries behind a sequence's length stay as they are (new: zero), and so do all of a sequence
+    without queries: in an `out` apart from `weights`, that is what `out` had, not its weights.
+    The rows need room for a sequence's whole length: one that is longer than `width` is left out,
+    which only the device error word tells (0x470)."""
     c, b, dev, H, d = _cache_args(cache, batch)
     if _elsewhere(dev, stream):
         with _on(dev, stream):
@@ -663,7 +666,8 @@ def cache_evict(cache, weights, block_table, lens, table_out, keep, recent=0, ou
     table_out (int32 [B, width]); a sequence of at most `keep` tokens is copied whole.  Returns
     the new lengths (int32 [B]), the positions of the kept tokens (int32 [B, H, keep], -1 behind
     the last) and their weights (fp32 [B, H, keep], or `out`).  The source blocks stay as they
-    are."""
+    are.  Weights that cache_weights is to go on with need rows with room for the tokens to come:
+    an `out` that is wider than `keep`."""
     c, dev, H, d = _pool_args(cache)
     if _elsewhere(dev, stream):
         with _on(dev, stream):
