@@ -678,3 +678,53 @@ def test_evict_of_weights_that_change():
         src = was[:nb].reshape(nb * bs, -1)
         want = torch.where(none[:, None], torch.full_like(src[:1], empty), src[at % (nb * bs)])
         assert torch.equal(x[nb:nb + nk].reshape(nk * bs, -1)[:keep], want)
+
+
+@pytest.mark.parametrize("bad", [-1, 1000, 2 ** 30])
+@pytest.mark.parametrize("fmt", ["int4", "e4m3", "e5m2"])
+def test_evict_of_missing_blocks(fmt, bad):
+    """Kept tokens whose block number is bad become zeros (8 bits: of the scale that the others
+    give, 2^-100 where there are none); a bad number to write to drops its tokens alone."""
+    H, d, bs, keep = 2, 64, 16, 48
+    lens = [160, 100]
+    c = _case([(0, x) for x in lens], H, d, bs, fmt).fill()
+    table_out = _scatter(c, [keep, keep], bs)
+    w = np.zeros((2, H, 160), dtype=np.float32)
+    # head 0: a part of two destination blocks is missing; head 1: the whole second one
+    first = [list(range(8)) + list(range(16, 32)) + list(range(40, 64)),
+             list(range(32)) + list(range(64, 80))]
+    for h in range(H):
+        w[0, h, first[h]] = 1.0
+        w[1, h, 30 + h:30 + h + keep] = 1.0
+    # the oracle's: a block of nothing in the place of the missing one
+    missing = int(c.table[0, 1])
+    nothing = {n: a.copy() for n, a in c.cache.items()}
+    for side in ("k", "v"):
+        nothing[side][missing] = 0x88 if fmt == "int4" else 0
+        nothing[side + "_scale"][missing] = 0 if fmt == "int4" else 2.0 ** -100
+    want, kept, new = oe.evict(nothing, fmt, c.table, c.lens, w, table_out, keep, 0)
+    assert kept[0][0].tolist() == first[0] and kept[0][1].tolist() == first[1]
+    for n in want:
+        want[n][missing] = c.cache[n][missing]
+    check = lambda cache: base4._assert_cache(cache, want) if fmt == "int4" else \
+        base8._assert_cache(cache, want, fmt)
+    dev = lambda a: torch.tensor(a, device=DEV)
+    table = c.table.copy()
+    table[0, 1] = bad
+    cache, batch = c.on_device()
+    got = fattn.cache_evict(cache, dev(w), dev(table), batch.lens, dev(table_out), keep)
+    assert fattn.fattn_device_error() == 0x481
+    assert got[0].tolist() == [keep, keep]
+    np.testing.assert_array_equal(got[1].cpu().numpy(), np.array(kept))
+    np.testing.assert_array_equal(got[2].cpu().numpy(), np.take_along_axis(w, np.array(kept), axis=2))
+    check(cache)
+    # a bad number to write to: as if nothing had been written there
+    want, _, _ = oe.evict(c.cache, fmt, c.table, c.lens, w, table_out, keep, 0)
+    for n in want:
+        want[n][table_out[1, 1]] = c.cache[n][table_out[1, 1]]
+    wrong = table_out.copy()
+    wrong[1, 1] = bad
+    cache, batch = c.on_device()
+    fattn.cache_evict(cache, dev(w), batch.block_table, batch.lens, dev(wrong), keep)
+    assert fattn.fattn_device_error() == 0x481
+    check(cache)
