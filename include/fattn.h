@@ -286,9 +286,10 @@ int fattn_fwd_bwd_host(const void* q, const void* k, const void* v, const void* 
  * for every 16 neighbouring channels of a token, bytes [num_blocks, H, block_size,
  * d / 16].  The value that code c (0 to 15) stands for is (c - 8) * scale.  All four
  * are 16-byte aligned.  Every token has its own scales, so nothing that is written
- * later changes what is there.  The reader takes any scale; for the attention its
- * magnitude is at most 7168, the largest that append writes (a row that sees a
- * larger one, an infinity or a NaN gets values of no meaning; others do not). */
+ * later changes what is there.  The reader takes any scale; for the attention and
+ * the keys' weights its magnitude is at most 7168, the largest that append writes (a
+ * row that sees a larger one, an infinity or a NaN gets values of no meaning, and so
+ * do the weights that come of it; other heads' and sequences' do not). */
 typedef enum {
   FATTN_CACHE_E4M3 = 0, /* 4 exponent, 3 mantissa bits, largest value 448, no infinities */
   FATTN_CACHE_E5M2 = 1, /* 5 exponent, 2 mantissa bits, largest value 57344 */

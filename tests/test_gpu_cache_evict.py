@@ -728,3 +728,21 @@ def test_evict_of_missing_blocks(fmt, bad):
     fattn.cache_evict(cache, dev(w), batch.block_table, batch.lens, dev(wrong), keep)
     assert fattn.fattn_device_error() == 0x481
     check(cache)
+
+
+@pytest.mark.parametrize("n", [1, 70])
+@pytest.mark.parametrize("byte", [0x70, 0x78, 0x7c, 0xfc, 0x7f])
+def test_weights_beside_scales_out_of_range(n, byte):
+    """A scale of 4 bits beyond what the attention takes (8192, 32768, infinities, NaN): the weights
+    of other heads and other sequences are what they are without it."""
+    H, G, d, bs = 2, 2, 128, 16
+    c = _case([(n, 50), (n, 33)], H, d, bs, "int4", seed=9).fill()
+    q = _bf16(c.rng, (c.T, H * G, d)).to(DEV)
+    got = []
+    for scale in (None, byte):
+        if scale is not None:
+            c.cache["k_scale"][c.table[0, 1], 0, 3, 2] = scale
+        cache, batch = c.on_device()
+        _, lse = fattn.cache_forward(q, cache, batch, 0.1, True)
+        got.append(fattn.cache_weights(q, lse, cache, batch, 0.1, True))
+    assert torch.equal(got[0][0, 1], got[1][0, 1]) and torch.equal(got[0][1], got[1][1])
