@@ -42,7 +42,7 @@ namespace {
 template <int D, int NT_>
 struct Dec4 {
   static constexpr int NT = NT_;
-  static constexpr int R = 8 * NT;
+  static constexpr int R = split_rows(NT);
   static constexpr int PARTS = D == 128 || NT == 2 ? 2 : 4;  // of 16 keys in a warp's tile
   static constexpr int KEYS = 16 * PARTS;
   static constexpr int CHUNK = kWarps * KEYS;
@@ -52,7 +52,7 @@ struct Dec4 {
   static constexpr int TILE_SCL = PARTS * PART_SCL;
   static constexpr int STAGE = 2 * TILE + 2 * TILE_SCL;  // keys, values, their scales
   static constexpr int ST = D == 64 && NT == 2 ? 6 : NT == 1 ? 3 : 4;  // ring slots per warp
-  static constexpr int CTAS = NT == 1 || D == 64 ? 3 : 2;   // per SM
+  static constexpr int CTAS = split_ctas(D, NT);  // per SM
   static constexpr int OFF_RED = kWarps * ST * STAGE;
   static constexpr int OFF_STAT = OFF_RED + kWarps * R * D * 4;
   static constexpr int SMEM = OFF_STAT + kWarps * R * 4 + 128;

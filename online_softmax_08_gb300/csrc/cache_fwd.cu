@@ -67,7 +67,7 @@ constexpr float kNothing = -60.f;  // what lies below it is taken as it
 template <int D, int NT_>
 struct Dec {
   static constexpr int NT = NT_;
-  static constexpr int R = 8 * NT;                // query rows per unit
+  static constexpr int R = split_rows(NT);        // query rows per unit
   static constexpr int PARTS = D == 128 ? 1 : 2;  // of 16 keys in a warp's tile (4 KB with values)
   static constexpr int KEYS = 16 * PARTS;
   static constexpr int CHUNK = kWarps * KEYS;     // keys per CTA step
@@ -81,7 +81,7 @@ struct Dec {
   static constexpr int OFF_STAT = OFF_SCL + kWarps * ST * 16;
   static constexpr int OFF_BAR = OFF_STAT + kWarps * R * 4;
   static constexpr int SMEM = OFF_BAR + kWarps * ST * 8 + 16 + 1024;
-  static constexpr int CTAS = NT == 1 || D == 64 ? 3 : 2;    // per SM
+  static constexpr int CTAS = split_ctas(D, NT);  // per SM
 };
 
 constexpr int kWideMerge = 8;  // merge blocks per CTA of the 256-row kernel
@@ -779,9 +779,9 @@ size_t pieces_bytes(size_t ctas, int R, int d) {
   return ((ctas * sizeof(Record) + 255) & ~(size_t)255) +
          ((ctas * 2 * R + 63) & ~(size_t)63) * 4 + ctas * 2 * R * d * 4;
 }
-size_t narrow_bytes(int d, int n_sm) {  // the larger of the two variants (4 bits: the same)
-  return std::max(pieces_bytes((size_t)n_sm * Dec<128, 1>::CTAS, Dec<128, 1>::R, d),
-                  pieces_bytes((size_t)n_sm * Dec<64, 2>::CTAS, Dec<64, 2>::R, d));
+size_t narrow_bytes(int d, int n_sm) {  // the largest variant's, in 8 and in 4 bits
+  return std::max(pieces_bytes((size_t)n_sm * split_ctas(128, 1), split_rows(1), d),
+                  pieces_bytes((size_t)n_sm * split_ctas(64, 2), split_rows(2), d));
 }
 // The most query rows per key/value head (tokens x grouped heads) of a sequence that
 // stays with the kernel above.  From 33 rows on it reads the keys three times and

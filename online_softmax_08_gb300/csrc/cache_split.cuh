@@ -15,6 +15,10 @@ constexpr float kOff = 8.f;    // the reference lies this far below the running 
 constexpr float kRoom = 15.f;  // and moves when a y exceeds it by more
 constexpr float kFar = 4194304.f;
 constexpr int kWarps = 4;
+// Of the kernels, for 8 nt query rows a unit: rows of a unit and CTAs per SM, by which the
+// workspace is sized.
+constexpr int split_rows(int nt) { return 8 * nt; }
+constexpr int split_ctas(int d, int nt) { return nt == 1 || d == 64 ? 3 : 2; }
 
 // A position in the list of all chunks: chunk ch of unit (sequence b, head h, row
 // block rb).  Sequence b has H x nrb units of nch chunks (none: nch = 0).
