@@ -812,7 +812,6 @@ extern "C" int fattn_cache_evict(const fattn_cache* cache, const fattn_cache_bat
   p.in = WeightView{const_cast<float*>(weights), weights_seq_stride, weights_head_stride};
   p.out = WeightView{weights_out, out_seq_stride, out_head_stride};
   p.width = width;
-  p.out_width = out_width;
   p.table_out = table_out;
   p.table_out_width = table_out_width;
   p.keep = keep;

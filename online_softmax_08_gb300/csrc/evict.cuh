@@ -37,7 +37,7 @@ cudaError_t launch_cache_weights_wide(const CUtensorMap& tq, const WeightParams&
 struct EvictParams {
   CacheParams c;       // cu_seqlens, total and max_seqlen are not used
   WeightView in, out;
-  int width, out_width;
+  int width;
   const int* table_out;
   int table_out_width;
   int keep, recent;
