@@ -419,8 +419,9 @@ size_t fattn_cache_fwd_workspace_bytes(const fattn_cache* cache, const fattn_cac
  * may be the same, with the same strides, and must not overlap otherwise.  Elements at and behind
  * lens[b], and sequences with n_b = 0, are not touched.
  * A sequence whose entries are bad (as above) or whose length exceeds width is skipped (code
- * 0x470), keys of a bad block number get 0 from the queries (0x471).  Every sum is formed in
- * one order: repeated calls agree bit for bit.  Scores, exponentials and sums are fp32.
+ * 0x470), keys of a bad block number get 0 from the queries (0x471); 0x472 to 0x47b say that a
+ * wait inside the kernel ran out.  Every sum is formed in one order: repeated calls agree bit for
+ * bit.  Scores, exponentials and sums are fp32.
  * A NaN key makes its weight NaN and, by way of lse, those of the keys whose queries see it. */
 int fattn_cache_weights(const fattn_cache* cache, const fattn_cache_batch* batch, const void* q,
                         long long q_token_stride, long long q_head_stride, const float* lse,

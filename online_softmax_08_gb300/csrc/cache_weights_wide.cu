@@ -17,9 +17,10 @@
 //                   rows
 //   warps 17, 19    the MMAs, a thread each for the tiles of one of two S buffers
 //   warp 18         the rows' log-sum-exp, a place for each S buffer
-// The bound is the special-function unit: 128 x 256 exponentials take 1024 clocks at the 32 a
-// clock that were measured, the products of that tile 768 (A and B come from shared memory at
-// 128 bytes a clock).  One thread that issued all MMAs was the bound before: its waits, 8
+// Two units are needed about equally: 128 x 256 exponentials take 1024 clocks of the
+// special-function unit at the 32 a clock that were measured, and the products of that tile keep
+// the tensor pipe busy for 1015 (its counter; A and B alone, read from shared memory at 128 bytes a
+// clock, would take 768).  One thread that issued all MMAs was the bound before: its waits, 8
 // instructions and commits take 1500 clocks a tile, as it shares its issue slots with the
 // exponentials.  (Built and measured before this, 512 queries behind 16384 tokens, 32 query and
 // 8 key heads, d = 128: mma.sync 457 us; 256 keys a unit, 8 warps, tiles of 128 rows 127 us, 16
@@ -117,9 +118,11 @@ __device__ __forceinline__ float4 ld_shared_f4(uint32_t a) {
   return v;
 }
 
-// A unit of this CTA's share, found alike by every warp.  The units of a sequence cost as many
-// row tiles as it has; a share is an equal part of all cost, to which the units belong that
-// begin in it.
+// A unit of this CTA's share, found alike by every warp.  The units of a sequence count as many
+// row tiles as it has; a share is an equal part of all, to which the units belong that begin in it.
+// (The causal mask is not counted: of a prompt without tokens before it, the shares with a head's
+// first keys have up to twice the mean to do; and a unit is one CTA's, however many rows it has.
+// 8192 such tokens, 32 query and 8 key heads, d = 128, take 468 us, 587 TFLOP/s.)
 template <int KEYS>
 struct Walk {
   const WeightParams& p;
